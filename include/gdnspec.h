@@ -83,7 +83,8 @@ enum {
     GDN_DEV_TOKEN_OOR = 4u,       /* draft id outside [0, vocab): counted as a miss */
     GDN_DEV_CKPT_UNWRITTEN = 8u,  /* commit asked for a checkpoint not written in this transaction */
     GDN_DEV_ACCEPT_BAD = 16u,     /* accept length outside [0, rows written) */
-    GDN_DEV_TIMEOUT = 32u         /* a bounded wait on an asynchronous copy ran out */
+    GDN_DEV_TIMEOUT = 32u,        /* a bounded wait on an asynchronous copy ran out */
+    GDN_DEV_PAGE_OOR = 64u        /* page id outside [0, num_pages) in a page table or move list */
 };
 
 typedef struct gdn_dims {
@@ -544,6 +545,137 @@ int gdn_decode_transaction_at(const gdn_dims *dims, int32_t num_layers, int32_t 
                               gdn_pool *pool, gdn_plan *plan, uint32_t *txn,
                               const gdn_decode_io *io, const gdn_arena_io *arena,
                               float *kernel_ms, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache: the softmax-attention layers that a hybrid
+ * model interleaves with its GatedDeltaNet layers ([ENGINE] H200 RC4
+ * evidence: paged Engine with a composite cache).  A transaction treats it as
+ * it treats the recurrent state: kv8_attend reads the committed cache and the
+ * transaction's own rows and writes nothing but outputs; kv8_append commits
+ * the accepted rows; not calling it is the rollback.
+ *
+ * Page p of layer l (kv + p*page_stride + l*layer_stride, bytes) holds e4m3
+ * codes [2 (K, V)][h_kv][page_tokens][d]; its scales (scale +
+ * p*scale_page_stride + l*scale_layer_stride, floats) are fp32
+ * [h_kv][2 (K, V)], each a power of two.  A stored element is code * scale.
+ * Token t of request r lives in page table[r*table_stride + t/page_tokens].
+ * Supported: d in {64, 128, 256}; page_tokens in {16, 32, 64, 128}; h_q a
+ * multiple of h_kv, h_q/h_kv <= 64.  kv 16-byte aligned with strides
+ * multiples of 16; scale 8-byte aligned with even strides.
+ * ------------------------------------------------------------------------ */
+typedef struct kv8_cache {
+    int32_t h_q, h_kv, d, page_tokens;
+    int32_t window;               /* a row at position p sees positions > p - window; 0 = all */
+    int32_t num_pages, num_layers;
+    float sm_scale;               /* multiplies q.k */
+    uint8_t *kv;                  /* device */
+    int64_t page_stride, layer_stride;
+    float *scale;                 /* device */
+    int64_t scale_page_stride, scale_layer_stride;
+} kv8_cache;
+
+/*
+ * kv8_attend -- one layer's attention for a transaction's packed rows.
+ *   Request r has cache_len[r] committed positions (0 .. max_len) and n =
+ *   cu_rows[r+1]-cu_rows[r] rows (0 .. max_rows <= GDN_MAX_ROWS; 0 rows: no
+ *   work).  Row i sits at position cache_len[r] + i and sees the committed
+ *   positions and the new rows j <= i, all inside the window; k_new and v_new
+ *   are used as given (bf16), the cache as stored.  With k_new = v_new = NULL
+ *   every row sees the committed positions only (the last `window` of them).
+ *     o[row][h]   = sum_t softmax_t(sm_scale q.k_t) v_t          (bf16)
+ *     lse[row][h] = log sum_t exp(sm_scale q.k_t)                (fp32, may be NULL)
+ *   A row that sees nothing gets o = 0 and lse = -inf.  Query head h reads
+ *   kv head h / (h_q/h_kv).  q [row][h_q][d], k_new and v_new [row][h_kv][d],
+ *   o [row][h_q][d]: rows q_stride, k_stride, v_stride, o_stride elements
+ *   apart (multiples of 8), bases 16-byte aligned; lse rows are h_q apart.
+ *   split_tokens: cached positions per independently summed piece.  0 picks
+ *   it from B, max_len, max_rows and the head layout; a given value (rounded
+ *   up to 128) makes a request's bits independent of what else is in the
+ *   batch.  Bytes of cache past cache_len, whatever they hold, reach no
+ *   output.  Requests past max_len, max_rows or row_capacity set
+ *   GDN_DEV_ROWS_BAD, page ids out of range GDN_DEV_PAGE_OOR; either skips
+ *   the request (its o and lse are not written).
+ *   workspace: kv8_attend_workspace_bytes(...) device bytes (16-byte aligned,
+ *   no initialisation), 0 when no request can need more than one piece.
+ */
+size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t max_len, int32_t max_rows,
+                                  int32_t split_tokens);
+int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+               const int32_t *cu_rows, const int32_t *cache_len,
+               const int32_t *table, int32_t table_stride,
+               const gdn_bf16 *q, int64_t q_stride,
+               const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
+               gdn_bf16 *o, int64_t o_stride, float *lse,
+               int32_t max_len, int32_t max_rows, int32_t split_tokens,
+               void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/*
+ * kv8_append -- commit rows into one layer's cache.  Of request r the first
+ *   n = accept_len[r] + 1 rows (every row when accept_len is NULL; none when
+ *   accept_len[r] < 0, a refused request) go to positions cache_len[r] ..
+ *   cache_len[r] + n - 1.  Per page, kv head and K or V:
+ *     scale' = max(scale, 2^ceil(log2(amax / 448)), 2^-100),
+ *   amax over the finite new elements, scale only if the page already held
+ *   tokens of this request (a page whose token 0 is written now starts over);
+ *   when the scale grows the page's earlier codes are rounded to it; new
+ *   codes are code = e4m3(x / scale') to nearest even, infinities to +-448,
+ *   NaN to NaN.  Rows may be any number up to max_rows (a decode's accepted
+ *   rows, a whole prompt).  cache_len is not changed: the caller advances it
+ *   once every layer is appended.  No page may be written for two requests,
+ *   or read by another request, in the same call (kv8_pages_reserve sees to
+ *   that).  accept_len[r] >= rows sets GDN_DEV_ACCEPT_BAD; bad rows or
+ *   lengths GDN_DEV_ROWS_BAD, pages GDN_DEV_PAGE_OOR: the request (for a bad
+ *   page: that page) is skipped.  If *dev_status already holds
+ *   GDN_DEV_TIMEOUT nothing is appended.
+ */
+int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+               const int32_t *cu_rows, const int32_t *cache_len,
+               const int32_t *table, int32_t table_stride,
+               const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
+               const int32_t *accept_len, int32_t max_rows, uint32_t *dev_status, void *stream);
+
+/*
+ * kv8_copy_pages -- page dst[i] <- page src[i], every layer, codes and scales
+ *   (src, dst: device int32 [n]).  The destinations are distinct and none is
+ *   a source of another pair (kv8_pages_* lists satisfy this); src[i] ==
+ *   dst[i] is skipped, an id out of range sets GDN_DEV_PAGE_OOR and skips the
+ *   pair.
+ */
+int kv8_copy_pages(const kv8_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,
+                   uint32_t *dev_status, void *stream);
+
+/*
+ * Page tables (HOST memory, synchronous), over a gdn_pool whose slots are the
+ * pages.  A table is a host int32 row of table_cap entries of which the first
+ * *n_pages name pages.  Every call is all or nothing: an error leaves the
+ * pool and the tables unchanged.
+ *
+ * kv8_pages_reserve -- make positions len .. len + n_new - 1 writable:
+ *   allocates the pages they still lack, and replaces a shared page that
+ *   position len would write into by a fresh one (copy-on-write: *n_copy = 1
+ *   and copy_src/copy_dst name the page to copy before the append).  Pages of
+ *   whole tokens past the end (after a rollback of len) are kept.
+ * kv8_pages_fork -- dst becomes a second holder of the first len positions:
+ *   whole pages are shared, an unfinished last page gets a fresh page
+ *   (*n_copy = 1, copy_src/copy_dst as above).
+ * kv8_pages_free -- releases the *n_pages pages and empties the table.
+ * kv8_pages_compact -- renumbers the live pages to 0 .. live-1: each live page
+ *   past that moves to the lowest free id, in increasing order.  tables holds
+ *   n_tables rows, table_stride apart, n_pages[i] entries used; every live
+ *   page must be named as often as its reference count says (otherwise
+ *   GDN_ERR_ARG: somebody else holds it).  Writes the moves (up to num_slots
+ *   pairs) for kv8_copy_pages, renames the tables and counts, and leaves the
+ *   free list in increasing order.
+ */
+int kv8_pages_reserve(gdn_pool *pool, int32_t *table, int32_t table_cap, int32_t *n_pages,
+                      int32_t len, int32_t n_new, int32_t page_tokens,
+                      int32_t *copy_src, int32_t *copy_dst, int32_t *n_copy);
+int kv8_pages_fork(gdn_pool *pool, const int32_t *src_table, int32_t src_pages, int32_t len,
+                   int32_t page_tokens, int32_t *dst_table, int32_t table_cap, int32_t *dst_pages,
+                   int32_t *copy_src, int32_t *copy_dst, int32_t *n_copy);
+int kv8_pages_free(gdn_pool *pool, int32_t *table, int32_t *n_pages);
+int kv8_pages_compact(gdn_pool *pool, int32_t n_tables, int32_t *tables, int32_t table_stride,
+                      const int32_t *n_pages, int32_t *move_src, int32_t *move_dst, int32_t *n_moves);
 
 const char *gdn_status_string(int status);
 

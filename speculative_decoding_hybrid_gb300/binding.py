@@ -23,6 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libgdnspec.so")
 GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_ARG = 0, -1, -2, -3
 GDN_ERR_DUP_SLOT, GDN_ERR_NO_SLOT, GDN_ERR_CUDA, GDN_ERR_WORKSPACE, GDN_ERR_REFUSED = -4, -5, -6, -7, -8
 DEV_SLOT_OOR, DEV_ROWS_BAD, DEV_TOKEN_OOR, DEV_CKPT_UNWRITTEN, DEV_ACCEPT_BAD, DEV_TIMEOUT = 1, 2, 4, 8, 16, 32
+DEV_PAGE_OOR = 64
 K_MAX = 15
 MAX_ROWS = K_MAX + 1
 REQ_DECODE, REQ_PREFILL = 0, 1
@@ -35,7 +36,8 @@ EXPORTS = ["gdn_decode_step", "gdn_verify", "mtp_accept_workspace_bytes", "mtp_g
            "gdn_prefill_workspace_bytes", "gdn_chunked_prefill", "gdn_pool_init", "gdn_pool_alloc",
            "gdn_pool_share", "gdn_pool_release", "plan_transaction", "gdn_pool_apply", "gdn_pool_abort",
            "gdn_decode_transaction", "gdn_decode_transaction_at", "gdn_status_string",
-           "gdn_selftest_prefill_timeout"]
+           "gdn_selftest_prefill_timeout", "kv8_attend_workspace_bytes", "kv8_attend", "kv8_append",
+           "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free", "kv8_pages_compact"]
 
 
 class GdnError(RuntimeError):
@@ -105,6 +107,14 @@ class gdn_arena_io(ctypes.Structure):
                 ("area_off", ctypes.c_int64 * 2)]
 
 
+class kv8_cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("h_q", "h_kv", "d", "page_tokens", "window", "num_pages",
+                                                "num_layers")] +
+                [("sm_scale", ctypes.c_float), ("kv", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                 ("layer_stride", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                 ("scale_page_stride", ctypes.c_int64), ("scale_layer_stride", ctypes.c_int64)])
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libgdnspec.so is not built (expected at %s); run "
@@ -112,6 +122,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, U32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
     DP = ctypes.POINTER(gdn_dims)
+    CP, PP = ctypes.POINTER(kv8_cache), ctypes.POINTER(gdn_pool)
     sig = {
         "gdn_decode_step": [DP, I32, P, P, P, P, P, P, I64, I32, P, P, P, P, P],
         "gdn_verify": [DP, I32, I32, P, P, P, P, P, P, P, I64, I32, P, P, P, U32, P, P, P],
@@ -137,6 +148,14 @@ def _load():
         "gdn_verify_layers": [DP, I32, I32, I32, P, P, P, I64, I64, I32, P, P, I64, P, U32, P, I64, P, P],
         "gdn_verify_at_layers": [DP, I32, I32, I32, P, P, P, I64, P, P, I64, P, U32, P, I64, P, P],
         "gdn_verify_replay_layers": [DP, I32, I32, I32, P, P, I32, P, P, P, P, I64, I64, I32, P, P, P, I64, P, P],
+        "kv8_attend_workspace_bytes": [CP, I32, I32, I32, I32],
+        "kv8_attend": [CP, I32, I32, I32, P, P, P, I32, P, I64, P, I64, P, I64, P, I64, P, I32, I32, I32, P, SZ, P, P],
+        "kv8_append": [CP, I32, I32, I32, P, P, P, I32, P, I64, P, I64, P, I32, P, P],
+        "kv8_copy_pages": [CP, I32, P, P, P, P],
+        "kv8_pages_reserve": [PP, P, I32, P, I32, I32, I32, P, P, P],
+        "kv8_pages_fork": [PP, P, I32, I32, I32, P, I32, P, P, P, P],
+        "kv8_pages_free": [PP, P, P],
+        "kv8_pages_compact": [PP, I32, P, I32, P, P, P, P],
         "gdn_selftest_wait_timeout": [P, ctypes.c_uint64, P],
         "gdn_selftest_prefill_timeout": [DP, I32, I32, P, P, P, P, P, P, P, I64, I32, P, P, P, P, SZ, P,
                                          ctypes.c_uint64, P],
@@ -154,6 +173,7 @@ def _load():
         f.restype = ctypes.c_int
     L.mtp_accept_workspace_bytes.restype = SZ
     L.gdn_prefill_workspace_bytes.restype = SZ
+    L.kv8_attend_workspace_bytes.restype = SZ
     L.gdn_status_string.restype = ctypes.c_char_p
     return L
 
@@ -351,6 +371,31 @@ def gdn_selftest_prefill_timeout(d: gdn_dims, nseq, row_capacity, cu_seqlens, q,
         workspace_bytes, _ptr(dev_status), int(limit_ns), _stream(stream)))
 
 
+def kv8_attend_workspace_bytes(c: kv8_cache, B, max_len, max_rows, split_tokens=0) -> int:
+    return int(lib.kv8_attend_workspace_bytes(ctypes.byref(c), B, max_len, max_rows, split_tokens))
+
+
+def kv8_attend(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_stride, q, q_stride, k_new,
+               k_stride, v_new, v_stride, o, o_stride, lse, max_len, max_rows, split_tokens, workspace,
+               workspace_bytes, dev_status, stream=None):
+    return _check("kv8_attend", lib.kv8_attend(
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_stride, _ptr(q),
+        q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse), max_len, max_rows,
+        split_tokens, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
+
+
+def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_stride, k_new, k_stride, v_new,
+               v_stride, accept_len, max_rows, dev_status, stream=None):
+    return _check("kv8_append", lib.kv8_append(
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_stride,
+        _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(accept_len), max_rows, _ptr(dev_status), _stream(stream)))
+
+
+def kv8_copy_pages(c: kv8_cache, n, src, dst, dev_status, stream=None):
+    return _check("kv8_copy_pages", lib.kv8_copy_pages(ctypes.byref(c), n, _ptr(src), _ptr(dst), _ptr(dev_status),
+                                                       _stream(stream)))
+
+
 # ---------------------------------------------------------------------------
 # Host planner and slot pool (host memory)
 # ---------------------------------------------------------------------------
@@ -432,3 +477,41 @@ def gdn_pool_apply(pool: Pool, plan: Plan, n: int) -> int:
 
 def gdn_pool_abort(pool: Pool, plan: Plan, n: int) -> int:
     return int(lib.gdn_pool_abort(ctypes.byref(pool.c), ctypes.byref(plan.c), n))
+
+
+def _i32(n=0):
+    return ctypes.c_int32(n)
+
+
+def kv8_pages_reserve(pool: Pool, table: np.ndarray, n_pages: int, length: int, n_new: int, page_tokens: int):
+    """-> (n_pages, (src, dst) to copy before the append, or None).  table: int32 row, changed in place."""
+    have, src, dst, n = _i32(n_pages), _i32(-1), _i32(-1), _i32()
+    _check("kv8_pages_reserve", lib.kv8_pages_reserve(
+        ctypes.byref(pool.c), table.ctypes.data, len(table), ctypes.byref(have), length, n_new, page_tokens,
+        ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)))
+    return have.value, ((src.value, dst.value) if n.value else None)
+
+
+def kv8_pages_fork(pool: Pool, src_table: np.ndarray, src_pages: int, length: int, page_tokens: int,
+                   dst_table: np.ndarray):
+    """-> (pages of dst, (src, dst) to copy, or None).  dst_table: an empty table's int32 row, changed in place."""
+    have, src, dst, n = _i32(), _i32(-1), _i32(-1), _i32()
+    _check("kv8_pages_fork", lib.kv8_pages_fork(
+        ctypes.byref(pool.c), src_table.ctypes.data, src_pages, length, page_tokens, dst_table.ctypes.data,
+        len(dst_table), ctypes.byref(have), ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)))
+    return have.value, ((src.value, dst.value) if n.value else None)
+
+
+def kv8_pages_free(pool: Pool, table: np.ndarray, n_pages: int):
+    have = _i32(n_pages)
+    _check("kv8_pages_free", lib.kv8_pages_free(ctypes.byref(pool.c), table.ctypes.data, ctypes.byref(have)))
+
+
+def kv8_pages_compact(pool: Pool, tables: np.ndarray, n_pages: np.ndarray):
+    """-> (move_src, move_dst) int32 arrays.  tables: C-contiguous int32 [n][cap], renamed in place."""
+    assert tables.dtype == np.int32 and tables.flags.c_contiguous and n_pages.dtype == np.int32
+    src, dst, n = np.empty(pool.c.num_slots, np.int32), np.empty(pool.c.num_slots, np.int32), _i32()
+    _check("kv8_pages_compact", lib.kv8_pages_compact(
+        ctypes.byref(pool.c), tables.shape[0], tables.ctypes.data, tables.shape[1], n_pages.ctypes.data,
+        src.ctypes.data, dst.ctypes.data, ctypes.byref(n)))
+    return src[:n.value], dst[:n.value]

@@ -1,0 +1,253 @@
+// Commit of rows into the paged 8-bit key/value cache, and page copies
+// (sm_103a).
+//
+// kv8_append: one CTA per (page touched, kv head and K or V, request).  A
+// thread holds its pieces of 16 new elements (32 bytes of bf16) in registers
+// between the two things done with them: the page's largest magnitude, which
+// fixes the scale 2^e with amax <= 448 * 2^e, and the rounding to codes.  A
+// power of two makes x / scale exact, so codes do not depend on the order of
+// appends, and a scale that grows moves earlier codes exactly unless they
+// fall into e4m3's subnormals.
+#include "kv8.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct AppendArgs {
+    kv8_cache c;
+    int32_t layer, B, row_capacity, table_stride, max_rows;
+    const int32_t *cu_rows, *cache_len, *table, *accept_len;
+    const uint16_t *k, *v;
+    int64_t k_stride, v_stride;
+    uint32_t *status;
+};
+
+__device__ __forceinline__ float amax_finite(uint32_t w, float m) {
+    const float a = __uint_as_float((w << 16) & 0x7fffffffu), b = __uint_as_float(w & 0x7fff0000u);
+    m = a < INFINITY && a > m ? a : m;  // false for NaN and infinity
+    return b < INFINITY && b > m ? b : m;
+}
+
+// 16 bf16 values -> 16 codes.
+__device__ __forceinline__ uint4 encode16(const uint4 &a, const uint4 &b, float inv) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = kv8::e4m3x2(__uint_as_float(w[2 * i] << 16) * inv,
+                                        __uint_as_float(w[2 * i] & 0xffff0000u) * inv);
+        const uint32_t hi = kv8::e4m3x2(__uint_as_float(w[2 * i + 1] << 16) * inv,
+                                        __uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv);
+        o[i] = lo | (hi << 16);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// PIECES: the most 16-element pieces of a page a thread may hold.
+template <int PIECES>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
+    gdn::pdl_enter();
+    const int r = blockIdx.z, h = blockIdx.y >> 1, is_v = blockIdx.y & 1;
+    const int T = a.c.page_tokens, d = a.c.d;
+    const int t0 = a.cu_rows[r], rows = a.cu_rows[r + 1] - t0, len = a.cache_len[r];
+    if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
+    const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    if (t0 < 0 || rows < 0 || rows > a.max_rows || int64_t(t0) + rows > a.row_capacity || len < 0 ||
+        int64_t(len) + rows > int64_t(a.table_stride) * T) {
+        if (first_cta) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
+        return;
+    }
+    int n = rows;
+    if (a.accept_len) {
+        const int j = a.accept_len[r];
+        if (j >= rows) {
+            if (first_cta) gdn::set_status(a.status, GDN_DEV_ACCEPT_BAD);
+            return;
+        }
+        n = j < 0 ? 0 : j + 1;
+    }
+    const int pj = len / T + blockIdx.x;           // page of the request's table
+    const int p0 = pj * T;                         // its first position
+    const int from = max(len, p0), to = min(len + n, p0 + T);
+    if (from >= to) return;
+    const int page = a.table[int64_t(r) * a.table_stride + pj];
+    if (page < 0 || page >= a.c.num_pages) {
+        if (threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        return;
+    }
+    const uint16_t *x = is_v ? a.v : a.k;
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    uint8_t *codes = a.c.kv + int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                     (int64_t(is_v) * a.c.h_kv + h) * T * d;
+    float *scale = a.c.scale + int64_t(page) * a.c.scale_page_stride + int64_t(a.layer) * a.c.scale_layer_stride +
+                   2 * h + is_v;
+    const int per = d / 16;                        // pieces a token
+    const int held = from - p0;                    // tokens the page already holds
+    const int total = (to - from) * per;
+    const uint16_t *src = x + (int64_t(t0) + (from - len)) * stride + int64_t(h) * d;
+
+    uint4 w[PIECES][2];
+    float m = 0.f;
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
+        if (i < total) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(src + int64_t(i / per) * stride + (i % per) * 16);
+            w[u][0] = __ldcs(p);
+            w[u][1] = __ldcs(p + 1);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            m = amax_finite(w[u][k].x, m);
+            m = amax_finite(w[u][k].y, m);
+            m = amax_finite(w[u][k].z, m);
+            m = amax_finite(w[u][k].w, m);
+        }
+    // magnitudes order like their bit patterns
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    __shared__ uint32_t red[kThreads / 32];
+    const float was = held ? *scale : 0.f;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wm;
+    __syncthreads();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, red[i]);
+    const int e = kv8::scale_exp(__uint_as_float(top));
+    const float fit = kv8::pow2i(e);
+    const float now = fmaxf(was, fit);
+    const float inv = 1.f / now;                   // exact: a power of two
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        if (i < total) *reinterpret_cast<uint4 *>(codes + int64_t(held) * d + int64_t(i) * 16) = encode16(w[u][0], w[u][1], inv);
+    }
+    if (held && now > was) {
+        const float f = was * inv;
+        for (int i = threadIdx.x; i < held * per; i += kThreads) {
+            uint4 *p = reinterpret_cast<uint4 *>(codes + int64_t(i) * 16);
+            const uint4 old = *p;
+            uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 lo = kv8::f32x2_of(uint16_t(o[k])), hi = kv8::f32x2_of(uint16_t(o[k] >> 16));
+                o[k] = kv8::e4m3x2(lo.x * f, lo.y * f) | (kv8::e4m3x2(hi.x * f, hi.y * f) << 16);
+            }
+            *p = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    // every thread has read *scale before the barrier above
+    if (threadIdx.x == 0) *scale = now;
+}
+
+struct CopyArgs {
+    kv8_cache c;
+    int32_t n, pieces;  // 16 KB pieces of a page and layer
+    const int32_t *src, *dst;
+    uint32_t *status;
+};
+
+constexpr int kPiece = 16384;
+
+// One CTA per (16 KB piece of a page of a layer, layer, pair).
+__global__ void __launch_bounds__(kThreads) kv8_copy_kernel(const CopyArgs a) {
+    gdn::pdl_enter();
+    const int64_t id = blockIdx.x;
+    const int piece = int(id % a.pieces);
+    const int64_t rest = id / a.pieces;
+    const int l = int(rest % a.c.num_layers), i = int(rest / a.c.num_layers);
+    const int s = a.src[i], t = a.dst[i];
+    if (s < 0 || s >= a.c.num_pages || t < 0 || t >= a.c.num_pages) {
+        if (piece == 0 && l == 0 && threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        return;
+    }
+    if (s == t) return;
+    const int bytes = 2 * a.c.h_kv * a.c.page_tokens * a.c.d;
+    const int at = piece * kPiece, n16 = min(kPiece, bytes - at) / 16;
+    const int64_t lo = int64_t(l) * a.c.layer_stride + at;
+    const uint4 *from = reinterpret_cast<const uint4 *>(a.c.kv + int64_t(s) * a.c.page_stride + lo);
+    uint4 *to = reinterpret_cast<uint4 *>(a.c.kv + int64_t(t) * a.c.page_stride + lo);
+    uint4 w[kPiece / 16 / kThreads];
+#pragma unroll
+    for (int u = 0; u < kPiece / 16 / kThreads; ++u)
+        if (threadIdx.x + u * kThreads < n16) w[u] = __ldcs(from + threadIdx.x + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < kPiece / 16 / kThreads; ++u)
+        if (threadIdx.x + u * kThreads < n16) __stcs(to + threadIdx.x + u * kThreads, w[u]);
+    if (piece == 0) {
+        const int64_t ls = int64_t(l) * a.c.scale_layer_stride;
+        for (int k = threadIdx.x; k < 2 * a.c.h_kv; k += kThreads)
+            a.c.scale[int64_t(t) * a.c.scale_page_stride + ls + k] =
+                a.c.scale[int64_t(s) * a.c.scale_page_stride + ls + k];
+    }
+}
+
+}  // namespace
+
+extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+                          const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
+                          int32_t table_stride, const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new,
+                          int64_t v_stride, const int32_t *accept_len, int32_t max_rows, uint32_t *dev_status,
+                          void *stream) {
+    const int bad = gdn_host::kv8_check(cache);
+    if (bad != GDN_OK) return bad;
+    if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_stride < 0 ||
+        max_rows < 0 || max_rows > gdn_host::kKv8MaxLen)
+        return GDN_ERR_ARG;
+    if (int64_t(table_stride) * cache->page_tokens > gdn_host::kKv8MaxLen) return GDN_ERR_ARG;
+    if (B == 0 || max_rows == 0) return GDN_OK;
+    if (!cu_rows || !cache_len || !table || !k_new || !v_new) return GDN_ERR_NULL;
+    if (!gdn_host::kv8_rows_ok(k_new, k_stride, cache->h_kv, cache->d) ||
+        !gdn_host::kv8_rows_ok(v_new, v_stride, cache->h_kv, cache->d))
+        return GDN_ERR_ARG;
+    AppendArgs a{};
+    a.c = *cache;
+    a.layer = layer;
+    a.B = B;
+    a.row_capacity = row_capacity;
+    a.table_stride = table_stride;
+    a.max_rows = max_rows;
+    a.cu_rows = cu_rows;
+    a.cache_len = cache_len;
+    a.table = table;
+    a.accept_len = accept_len;
+    a.k = k_new;
+    a.v = v_new;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.status = dev_status;
+    const int T = cache->page_tokens;
+    // n rows starting anywhere touch at most (T - 1 + n - 1) / T + 1 pages
+    const dim3 grid(unsigned((max_rows + T - 2) / T + 1), unsigned(2 * cache->h_kv), unsigned(B));
+    const int most = max_rows < T ? max_rows : T;
+    const int pieces = (most * cache->d / 16 + kThreads - 1) / kThreads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1>, grid, dim3(kThreads), 0, st, a);
+    if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2>, grid, dim3(kThreads), 0, st, a);
+    if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4>, grid, dim3(kThreads), 0, st, a);
+    return gdn_host::launch_pdl(kv8_append_kernel<8>, grid, dim3(kThreads), 0, st, a);
+}
+
+extern "C" int kv8_copy_pages(const kv8_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,
+                              uint32_t *dev_status, void *stream) {
+    const int bad = gdn_host::kv8_check(cache);
+    if (bad != GDN_OK) return bad;
+    if (n < 0) return GDN_ERR_ARG;
+    if (n == 0) return GDN_OK;
+    if (!src || !dst) return GDN_ERR_NULL;
+    CopyArgs a{};
+    a.c = *cache;
+    a.n = n;
+    a.src = src;
+    a.dst = dst;
+    a.status = dev_status;
+    a.pieces = int((int64_t(2) * cache->h_kv * cache->page_tokens * cache->d + kPiece - 1) / kPiece);
+    const int64_t grid = int64_t(n) * cache->num_layers * a.pieces;
+    if (grid > 0x7fffffffLL) return GDN_ERR_ARG;
+    return gdn_host::launch_pdl(kv8_copy_kernel, dim3(unsigned(grid)), dim3(kThreads), 0,
+                                static_cast<cudaStream_t>(stream), a);
+}
