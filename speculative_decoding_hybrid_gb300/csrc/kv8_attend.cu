@@ -1,122 +1,893 @@
 // Attention of a transaction's rows over the paged 8-bit cache (sm_103a).
 //
-// One CTA per (row, query head); its warps take every eighth position, each
-// keeping a running maximum, sum and weighted value, joined at the end.
+// With R = rows * (h_q / h_kv) query vectors on one kv head a position costs
+// 2 d bytes and 4 d R flops: from R of about 8 on only the tensor cores keep
+// up with the memory.  Keys and values go to them as they lie in the cache,
+// without a conversion: the products are e4m3 x e4m3 with the cache's side
+// exact by construction and the other side split into exact or nearly exact
+// e4m3 parts, side by side in the N extent, which the few rows leave free:
+//   scores   S^T[128 positions][2 RB] = K [q_hi | q_lo]     q = (q_hi + q_lo/32) 2^-k  (bf16's 8 bits, exactly)
+//   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 32^-j
+// A part is its predecessor's remainder times 32, so three carry 14 bits of a
+// weight; the fourth keeps that precision for weights 2^-12 times smaller.
+// A position is a tensor-memory lane, so its page's scales are one register
+// of the thread that owns the lane: K's multiplies the score, V's the weight.
+//
+// The softmax keeps a reference m per column, not the running maximum: a
+// column's weights are 2^(z - m), and only when some z passes m + kSlack (or a
+// page's V scale the reference one) is m moved and the sums rescaled; usually
+// that is once, at a piece's first tile.  One vote a tile decides.
+//
+// One CTA per (piece of a request's positions, kv head and block of RB
+// columns, request): warps 0-3 softmax (thread = position = lane), warp 4
+// copies pages (tiled TMA, 128- or 64-byte swizzle, K and V tiles through one
+// ring), warp 5 issues the products.  The transaction's own rows, bf16, come
+// last: their keys as one more tile, each a hi and a lo position (16 + 16
+// lanes) split like q, their values in fp32 in the epilogue.
+// Pieces leave (m, l, O) in the workspace for kv8_join_kernel; a request with
+// one piece is written directly.
+#include <cuda.h>
+
 #include "kv8.cuh"
+#include "tc.cuh"
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTile = 128;      // positions a tile
+constexpr int kSoft = 128;      // softmax threads
+constexpr int kThreads = kSoft + 64;
+// Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
+// is 2^-25, so 2^-27 of a weight at the reference.  More slack moves the
+// reference less often and costs that many bits at the low end.
+constexpr float kBase = 4.f, kSlack = 6.f;
+constexpr float kUnset = -1e30f;
 
 struct AttendArgs {
+    CUtensorMap map;
     kv8_cache c;
     int32_t layer, B, row_capacity, table_stride, max_len, max_rows;
+    int32_t group, blocks, piece_tiles, max_pieces;
     const int32_t *cu_rows, *cache_len, *table;
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride, o_stride;
     uint16_t *o;
     float *lse;
+    float *ws_o;       // [unit][RB][d]
+    float2 *ws_ml;     // [unit][RB]
     uint32_t *status;
+    uint64_t wait_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv8_attend_kernel(const AttendArgs a) {
+// What a request asks for; the same test in both kernels.
+struct Request {
+    int t0, n, len, lo, tiles, pieces;  // lo: first position any row sees; tiles from lo / 128 on
+    bool bad;
+};
+__device__ __forceinline__ Request request_of(const AttendArgs &a, int r) {
+    Request q;
+    q.t0 = a.cu_rows[r];
+    q.n = a.cu_rows[r + 1] - q.t0;
+    q.len = a.cache_len[r];
+    q.bad = q.t0 < 0 || q.n < 0 || q.n > a.max_rows || int64_t(q.t0) + q.n > a.row_capacity || q.len < 0 ||
+            q.len > a.max_len || int64_t(q.len) > int64_t(a.table_stride) * a.c.page_tokens;
+    const int w = a.c.window;
+    q.lo = w ? max(0, q.len + (a.k ? 1 : 0) - w) : 0;
+    if (q.lo > q.len) q.lo = q.len;
+    const int first = q.lo / kTile;
+    q.tiles = q.lo < q.len ? (q.len + kTile - 1) / kTile - first : 0;
+    q.pieces = max(1, (q.tiles + a.piece_tiles - 1) / a.piece_tiles);
+    return q;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Barrier of the softmax warps with an OR over a predicate.
+__device__ __forceinline__ bool soft_or(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, "
+        "q;\n}\n"
+        : "=r"(r)
+        : "r"(uint32_t(p))
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// fp16 pair arithmetic of the splits.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint16_t e4m3x2_of(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+// (h - back) * 32 of two fp16 values: exact, `back` being h to 4 bits.
+__device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t back) {
+    uint32_t t, r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(h), "r"(0x50005000u));              // 32, 32
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(back), "r"(0xd000d000u), "r"(t));  // -32, -32
+    return r;
+}
+
+template <int D, int RB>
+struct Cfg {
+    static constexpr int kRow = D < 128 ? D : 128;       // bytes of an operand tile's row
+    static constexpr int kAtoms = D / kRow;              // such tiles side by side
+    static constexpr int kNs = 2 * RB;                   // score columns
+    static constexpr int kNp = 4 * RB;                   // weight columns
+    static constexpr int kPRow = RB == 8 ? 64 : RB == 64 ? 128 : kNp;  // bytes of a weight tile's row (64 or 128)
+    static constexpr int kFresh = 32 * D;                // bytes of the fresh keys
+    static constexpr int kQ = kNs * D;
+    static constexpr int kP = kTile * (RB == 8 ? 64 : kNp);
+    static constexpr int kSlot = kTile * D;
+    // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule it out
+    static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
+    static constexpr int kFixed = kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024 + 4096;
+    static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kFixed;
+    static constexpr int kSlots = kRoom / kSlot > 10 ? 10 : kRoom / kSlot;
+    static constexpr int kSmem = kFixed + kSlots * kSlot;
+    static constexpr int kTmemUse = 2 * kNs + kNp * (D == 256 ? 2 : 1);
+    static constexpr int kTmem = kTmemUse <= 64 ? 64 : kTmemUse <= 128 ? 128 : kTmemUse <= 256 ? 256 : 512;
+    static_assert(kTmemUse <= 512 && kSlots >= 3, "does not fit an SM");
+};
+
+// Ring positions of the tiles' loads, in the order the products use them:
+// K0 K1 V0 K2 V1 ... V(n-1).
+__device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+
+template <int D, int RB>
+__global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
+    using C = Cfg<D, RB>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
+    __shared__ uint32_t tmem_ptr;
+    __shared__ float col_m[RB], col_coef[RB], col_fac[RB], col_max[4][RB], v_max[4];
+    __shared__ int col_lo[RB], col_row[RB];
+    __shared__ float fresh_k[16], fresh_p[RB][16];
+    __shared__ float col_l[RB];
+
     gdn::pdl_enter();
-    constexpr int E = D / 32;
-    const int i = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int piece = blockIdx.x, hk = blockIdx.y / a.blocks, blk = blockIdx.y % a.blocks, r = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Request rq = request_of(a, r);
+    if (rq.bad) {
+        if (piece == 0 && blockIdx.y == 0 && tid == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
+        return;
+    }
+    const int cols = min(RB, rq.n * a.group - blk * RB);  // columns of this block in use
+    if (piece >= rq.pieces || cols <= 0) return;
+
     const int T = a.c.page_tokens;
-    const int t0 = a.cu_rows[r], n = a.cu_rows[r + 1] - t0, len = a.cache_len[r];
-    if (t0 < 0 || n < 0 || n > a.max_rows || int64_t(t0) + n > a.row_capacity || len < 0 || len > a.max_len ||
-        int64_t(len) > int64_t(a.table_stride) * T) {
-        if (i == 0 && h == 0 && threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
-        return;
+    const int tile0 = rq.lo / kTile + piece * a.piece_tiles;
+    const int nc = max(0, min(a.piece_tiles, rq.tiles - piece * a.piece_tiles));  // cached tiles
+    const bool fresh = a.k != nullptr && piece == rq.pieces - 1;
+    const int nt = nc + (fresh ? 1 : 0);
+
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *s_fk = sm, *s_q = s_fk + C::kFresh;
+    uint8_t *s_p = s_q + ((C::kQ + 1023) & ~1023), *s_ring = s_p + 2 * C::kP;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            gdn::mbar_init(&full[i], 1);
+            gdn::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            gdn::mbar_init(&s_full[i], 1);
+            gdn::mbar_init(&s_free[i], 4);
+            gdn::mbar_init(&p_full[i], 4);
+            gdn::mbar_init(&pv_done[i], 1);
+        }
+        gdn::mbar_init(&q_ready, 4);
+        gdn::mbar_init(&drain, 1);
     }
-    if (i >= n) return;
-    const int hk = h / (a.c.h_q / a.c.h_kv), w = a.c.window;
-    const int lo = w ? max(0, (a.k ? len + i + 1 : len) - w) : 0;
-    bool bad = false;
-    for (int t = lo / T + threadIdx.x; t * T < len; t += kThreads) {
-        const int p = a.table[int64_t(r) * a.table_stride + t];
-        bad |= p < 0 || p >= a.c.num_pages;
-    }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
-        return;
-    }
-    float q[E], acc[E], m = -INFINITY, l = 0.f;
-    const float c = a.c.sm_scale;
+    if (warp == 5) tc::tmem_alloc(&tmem_ptr, C::kTmem);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_ptr, tm_o = tm + 2 * C::kNs;
+
+    if (warp == 4) {
+        // ---- copies: page ids 32 at a time, the next 32 loaded ahead
+        const int per = kTile / T;  // pages a tile
+        const int page0 = tile0 * per, first = rq.lo / T, last = (rq.len + T - 1) / T;
+        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
+        auto ids = [&](int batch) {
+            const int j = page0 + batch * 32 + lane;
+            const int p = j >= first && j < last && batch * 32 + lane < nc * per ? tab[j] : -1;
+            return p >= 0 && p < a.c.num_pages ? p : -1;
+        };
+        int cur = ids(0), nxt = ids(1), batch = 0;
+        bool ok = true;
+        int issued = 0;
+        auto issue = [&](int pos, int page, int is_v) {
+            const int slot = pos % C::kSlots;
+            if (pos >= C::kSlots)
+                ok = ok && gdn::mbar_wait_bounded(&empty[slot], ((pos / C::kSlots) - 1) & 1, a.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            const uint32_t have = __ballot_sync(0xffffffffu, lane < per && page >= 0);
+            if (lane == 0) gdn::mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(have)) * uint32_t(T * D));
+            __syncwarp();
+            issued = pos + 1;
+            if (lane < per && page >= 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = gdn::bf16_to_f32(a.q[(int64_t(t0) + i) * a.q_stride + int64_t(h) * D + e * 32 + lane]);
-        acc[e] = 0.f;
-    }
-    const int news = a.k ? i + 1 : 0, skip = w ? max(0, i - w + 1) : 0;
-    const int total = len - min(lo, len) + max(0, news - skip);
-    for (int x = warp; x < total; x += kWarps) {
-        float kk[E], vv[E];
-        const int t = lo + x;
-        if (t < len) {
-            const int p = a.table[int64_t(r) * a.table_stride + t / T];
-            const uint8_t *base = a.c.kv + int64_t(p) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
-                                  (int64_t(hk) * T + t % T) * D;
-            const float *s = a.c.scale + int64_t(p) * a.c.scale_page_stride +
-                             int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                kk[e] = kv8::f32x2_of(base[e * 32 + lane]).x * s[0];
-                vv[e] = kv8::f32x2_of(base[int64_t(a.c.h_kv) * T * D + e * 32 + lane]).x * s[1];
+                for (int x = 0; x < C::kAtoms; ++x)
+                    gdn::tma_load_3d(s_ring + slot * C::kSlot + x * kTile * C::kRow + lane * T * C::kRow, &a.map,
+                                     x * C::kRow, (is_v * a.c.h_kv + hk) * T, page, &full[slot]);
             }
-        } else {
-            const int64_t j = int64_t(t0) + skip + (x - (len - min(lo, len)));
+        };
+        int prev = -1;
+        for (int i = 0; i <= nc && ok; ++i) {
+            int page = -1;
+            if (i < nc) {
+                const int at = i * per;
+                if (at / 32 != batch) {
+                    batch = at / 32;
+                    cur = nxt;
+                    nxt = ids(batch + 1);
+                }
+                page = __shfl_sync(0xffffffffu, cur, (at % 32) + (lane & (per - 1)));
+                issue(k_pos(i), page, 0);
+            }
+            if (i > 0 && ok) issue(v_pos(i - 1, nc), prev, 1);
+            prev = page;
+        }
+        if (!ok) {
+            // wait, again bounded, for the copies in flight into this CTA's shared memory
+            gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+            for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
+                (void)gdn::mbar_wait_bounded(&full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
+        }
+    } else if (warp == 5) {
+        // ---- products
+        if (lane == 0 && nt > 0) {
+            constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
+            constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kAMnMajor | tc::kBMnMajor;
+            const uint64_t dq = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_q), 16);
+            // weights: rows are positions; RB = 64 has two tiles of 128 columns
+            const uint64_t dp = tc::smem_desc8<C::kPRow>(gdn::smem_u32(s_p), kTile * C::kPRow);
+            // V has 128 rows of M at d >= 128; at d = 64 rows 64.. read the next slot and are not used
+            constexpr uint32_t lbo = C::kRow == 64 ? C::kSlot : 16;
+            bool ok = gdn::mbar_wait_bounded(&q_ready, 0, a.wait_ns);
+            tc::fence_after();
+            for (int i = 0; i <= nt && ok; ++i) {
+                if (i < nt) {
+                    const bool cached = i < nc;
+                    const int pos = k_pos(i), slot = pos % C::kSlots;
+                    if (cached) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                    if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&s_free[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t base = gdn::smem_u32(cached ? s_ring + slot * C::kSlot : s_fk);
+                    const uint32_t atom = cached ? kTile * C::kRow : 32 * C::kRow;
+                    const uint64_t dk = tc::smem_desc8<C::kRow>(base, 16);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                kk[e] = gdn::bf16_to_f32(a.k[j * a.k_stride + int64_t(hk) * D + e * 32 + lane]);
-                vv[e] = gdn::bf16_to_f32(a.v[j * a.v_stride + int64_t(hk) * D + e * 32 + lane]);
+                    for (int s = 0; s < D / 32; ++s) {
+                        const uint32_t x = s * 32 / C::kRow, in = s * 32 % C::kRow;
+                        tc::mma_e4m3(tm + (i & 1) * C::kNs, tc::desc_at(dk, x * atom + in),
+                                     tc::desc_at(dq, x * C::kNs * C::kRow + in), id_s, s > 0);
+                    }
+                    tc::commit(&s_full[i & 1]);
+                    if (cached) tc::commit(&empty[slot]);
+                }
+                if (i > 0 && i <= nc) {
+                    const int j = i - 1, pos = v_pos(j, nc), slot = pos % C::kSlots;
+                    ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                    if (ok) ok = gdn::mbar_wait_bounded(&p_full[j & 1], (j >> 1) & 1, a.wait_ns);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t base = gdn::smem_u32(s_ring + slot * C::kSlot);
+#pragma unroll
+                    for (int x = 0; x < C::kAtoms; ++x) {
+                        const uint64_t dv = tc::smem_desc8<C::kRow>(base + x * kTile * C::kRow, lbo);
+#pragma unroll
+                        for (int s = 0; s < kTile / 32; ++s)
+                            tc::mma_e4m3(tm_o + x * C::kNp, tc::desc_at(dv, s * 32 * C::kRow),
+                                         tc::desc_at(dp, (j & 1) * C::kP + s * 32 * C::kPRow), id_p, j > 0 || s > 0);
+                    }
+                    tc::commit(&pv_done[j & 1]);
+                    tc::commit(&empty[slot]);
+                }
+            }
+            if (!ok) {
+                gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+                tc::commit(&drain);  // products in flight read shared and write tensor memory
+                (void)gdn::mbar_wait_bounded(&drain, 0, a.wait_ns);
             }
         }
-        float s = 0.f;
+        __syncwarp();
+    } else {
+        // ---- softmax warps.  First the operands that come as bf16.
+        {
+            const int sub = tid & 7;
+            constexpr int E = D / 8;  // elements a thread takes of a row
+            auto load = [&](const uint16_t *p, float (&x)[E]) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], kk[e], s);
+                for (int e = 0; e < E / 8; ++e) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(p + sub * E + e * 8);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= c;
-        const float top = fmaxf(m, s), f = m == top ? 1.f : expf(m - top), p = expf(s - top);
-        m = top;
-        l = l * f + p;
+                    for (int i = 0; i < 4; ++i) {
+                        x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
+                        x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+                    }
+                }
+            };
+            // Splits a row x = (hi + lo/32) 2^-k into rows rh and rl of a tile of `rows`
+            // rows; -> 2^-k, or NaN for a row that is not finite.
+            auto split = [&](float (&x)[E], uint8_t *tile, int rows, int rh, int rl) {
+                float m = 0.f;
+                bool finite = true;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + p * vv[e];
+                for (int e = 0; e < E; ++e) {
+                    const bool f = fabsf(x[e]) < INFINITY;
+                    finite &= f;
+                    x[e] = f ? x[e] : 0.f;
+                    m = fmaxf(m, fabsf(x[e]));
+                }
+                uint32_t w = __float_as_uint(m);
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+                const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (lane & 24)) & 0xffu;
+                const int k = max(-110, min(110, 7 - (int(w >> 23) - 127)));  // largest in [128, 256)
+                const float up = kv8::pow2i(k), down = kv8::pow2i(-k);
+#pragma unroll
+                for (int b = 0; b < E / 8; ++b) {
+                    uint32_t h[2], l[2];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t hh[2], ll[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x0 = x[b * 8 + g * 4 + 2 * i] * up, x1 = x[b * 8 + g * 4 + 2 * i + 1] * up;
+                            hh[i] = kv8::e4m3x2(x0, x1);
+                            const float2 back = kv8::f32x2_of(uint16_t(hh[i]));
+                            ll[i] = kv8::e4m3x2((x0 - back.x) * 32.f, (x1 - back.y) * 32.f);
+                        }
+                        h[g] = hh[0] | (hh[1] << 16);
+                        l[g] = ll[0] | (ll[1] << 16);
+                    }
+                    const int e0 = sub * E + b * 8, x0 = e0 / C::kRow, in = e0 % C::kRow;
+                    uint8_t *t = tile + x0 * rows * C::kRow + (in & 8);
+                    *reinterpret_cast<uint2 *>(t + tc::swz8_off<C::kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
+                    *reinterpret_cast<uint2 *>(t + tc::swz8_off<C::kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
+                }
+                return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
+            };
+            const float coef = a.c.sm_scale * 1.4426950408889634f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < RB; c0 += 16) {
+                const int c = c0 + (tid >> 3);
+                const bool in = c < RB;  // RB = 8 leaves half of the threads without a column
+                const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
+                float e[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) e[i] = 0.f;
+                if (in && c < cols) load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, e);
+                // a thread without a column repeats the last one's zeros' work on that column's values
+                const int cc = in ? c : RB - 1;
+                if (RB >= 16 || warp < 2) {
+                    const float down = split(e, s_q, C::kNs, cc, RB + cc);
+                    if (sub == 0 && in) {
+                        col_m[c] = kUnset;
+                        col_coef[c] = coef * down;
+                        col_row[c] = row;
+                        // positions the row sees start here
+                        const int w = a.c.window;
+                        col_lo[c] = w ? max(0, rq.len + (a.k ? row + 1 : 0) - w) : 0;
+                    }
+                }
+            }
+            if (fresh) {
+                const int j = tid >> 3;
+                float e[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) e[i] = 0.f;
+                if (j < rq.n) load(a.k + (int64_t(rq.t0) + j) * a.k_stride + int64_t(hk) * D, e);
+                const float dk = split(e, s_fk, 32, j, 16 + j);
+                if (sub == 0) fresh_k[j] = dk;
+            }
+            gdn::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&q_ready);
+            soft_sync();
+        }
+        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
+        const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
+        bool bad = false, ok = true;
+        auto page_of = [&](int i) {  // page of this thread's position in tile i, -1 if no row sees it
+            const int t = (tile0 + i) * kTile + tid;
+            if (i >= nc || t < rq.lo || t >= rq.len) return -1;
+            const int p = tab[t / T];
+            if (p < 0 || p >= a.c.num_pages) {
+                bad = true;
+                return -1;
+            }
+            return p;
+        };
+        auto scales_of = [&](int p) {
+            return p >= 0 ? *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride)
+                          : make_float2(0.f, 0.f);
+        };
+        // ids two tiles ahead, scales one
+        int page1 = page_of(1);
+        float2 sc_next = scales_of(page_of(0));
+        float l[RB], z[RB];
+#pragma unroll
+        for (int c = 0; c < RB; ++c) l[c] = 0.f;
+        float vref = kv8::pow2i(kv8::kMinScaleExp);
+        const uint32_t lane_base = uint32_t(warp * 32) << 16;
+
+        for (int i = 0; i < nt; ++i) {
+            const bool is_fresh = i >= nc;
+            const int t = (tile0 + i) * kTile + tid;
+            float2 sc = sc_next;
+            sc_next = scales_of(page1);
+            page1 = page_of(i + 2);
+            if (is_fresh) sc = make_float2(tid < 32 && (tid & 15) < rq.n ? fresh_k[tid & 15] : 0.f, 0.f);
+            // whole: every row sees every position of the tile
+            const bool whole = !is_fresh && (tile0 + i + 1) * kTile <= rq.len && (tile0 + i) * kTile >= col_lo[cols - 1];
+            if (ok) ok = gdn::mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, a.wait_ns);
+            tc::fence_after();
+
+            // z - m of every column (m = 0 where the reference is to move)
+            auto load_z = [&](bool plain) {
+#pragma unroll
+                for (int c0 = 0; c0 < RB; c0 += 16) {
+                    uint32_t hi[16], lo[16];
+                    tc::ld16_async(tm + lane_base + (i & 1) * C::kNs + c0, hi);
+                    if (RB > 8) tc::ld16_async(tm + lane_base + (i & 1) * C::kNs + RB + c0, lo);
+                    tc::ld_wait();
+                    tc::ld_fence_regs(hi);
+                    if (RB > 8) tc::ld_fence_regs(lo);
+#pragma unroll
+                    for (int c = 0; c < (RB > 8 ? 16 : 8); ++c) {
+                        float s = fmaf(__uint_as_float(RB > 8 ? lo[c] : hi[8 + c]), 1.f / 32.f, __uint_as_float(hi[c]));
+                        if (is_fresh) {  // the other part of the position
+                            const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+                            s = tid & 16 ? fmaf(s, 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, s);
+                        }
+                        z[c0 + c] = fmaf(s, sc.x * col_coef[c0 + c], plain ? 0.f : -col_m[c0 + c]);
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < RB; ++c) {
+                        bool see;
+                        if (is_fresh) {
+                            const int j = tid & 15, row = col_row[c], w = a.c.window;
+                            see = tid < 32 && j < rq.n && j <= row && (!w || j > row - w);
+                        } else {
+                            see = t < rq.len && t >= col_lo[c];
+                        }
+                        if (!see) z[c] = -INFINITY;
+                    }
+                }
+            };
+            load_z(false);
+            float over = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < RB; ++c) over = fmaxf(over, z[c]);
+            if (soft_or(over > kSlack || sc.y > vref || !ok)) {
+                // ---- the reference moves (or a wait ran out)
+                if (soft_or(!ok)) {
+                    ok = false;
+                    break;
+                }
+                load_z(true);
+#pragma unroll
+                for (int c = 0; c < RB; ++c) {
+                    const float x = warp_max(z[c]);
+                    if (lane == 0) col_max[warp][c] = x;
+                }
+                const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
+                if (lane == 0) v_max[warp] = __uint_as_float(vm);
+                soft_sync();
+                for (int c = tid; c < RB; c += kSoft) {
+                    const float was = col_m[c];
+                    const float now =
+                        fmaxf(fmaxf(fmaxf(col_max[0][c], col_max[1][c]), fmaxf(col_max[2][c], col_max[3][c])), was);
+                    col_fac[c] = ex2(was - now);
+                    col_m[c] = now;
+                }
+                const float vnow = fmaxf(fmaxf(fmaxf(v_max[0], v_max[1]), fmaxf(v_max[2], v_max[3])), vref);
+                const float vfac = vref / vnow;
+                vref = vnow;
+                soft_sync();
+#pragma unroll
+                for (int c = 0; c < RB; ++c) {
+                    l[c] *= col_fac[c];
+                    z[c] -= col_m[c];
+                }
+                if (i > 0) {
+                    ok = gdn::mbar_wait_bounded(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, a.wait_ns);
+                    if (soft_or(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < C::kAtoms * C::kNp; x += 16) {
+                        uint32_t w[16];
+                        tc::ld16_async(tm_o + lane_base + x, w);
+                        tc::ld_wait();
+                        tc::ld_fence_regs(w);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            w[c] = __float_as_uint(__uint_as_float(w[c]) * (col_fac[(x + c) % RB] * vfac));
+                        st16(tm_o + lane_base + x, w);
+                    }
+                    tc::st_wait();
+                }
+            }
+            // scores are read: their buffer is free
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&s_free[i & 1]);
+
+            if (is_fresh) {
+                if (tid < 16) {
+#pragma unroll
+                    for (int c = 0; c < RB; ++c) {
+                        const float p = ex2(z[c]);
+                        l[c] += p;
+                        fresh_p[c][tid] = p;
+                    }
+                }
+                break;  // the last tile
+            }
+            const float xw = sc.y / vref * kBase;
+            if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&pv_done[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
+            uint8_t *pb = s_p + (i & 1) * C::kP;
+            // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
+            constexpr int W = RB < 16 ? 8 : 16;
+#pragma unroll
+            for (int c0 = 0; c0 < RB; c0 += W) {
+                uint32_t part[4][W / 4];
+#pragma unroll
+                for (int c = 0; c < W; c += 2) {
+                    const float p0 = ex2(z[c0 + c]), p1 = ex2(z[c0 + c + 1]);
+                    l[c0 + c] += p0;
+                    l[c0 + c + 1] += p1;
+                    const float x0 = p0 * xw, x1 = p1 * xw;
+                    uint16_t e[4];
+                    e[0] = uint16_t(kv8::e4m3x2(x0, x1));
+                    const float2 b0 = kv8::f32x2_of(e[0]);
+                    uint32_t rest = f16x2((x0 - b0.x) * 32.f, (x1 - b0.y) * 32.f);
+                    e[1] = e4m3x2_of(rest);
+                    rest = rest32(rest, kv8::f16x2_of(e[1]));
+                    e[2] = e4m3x2_of(rest);
+                    e[3] = e4m3x2_of(rest32(rest, kv8::f16x2_of(e[2])));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        part[k][c / 4] = c % 4 ? part[k][c / 4] | (uint32_t(e[k]) << 16) : uint32_t(e[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int b = k * RB + c0;  // byte of the row
+                    uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
+                                   tc::swz8_off<C::kPRow>(tid, (b % C::kPRow) >> 4) + (b & 8);
+                    if constexpr (W == 16)
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+                    else
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(part[k][0], part[k][1]);
+                }
+            }
+            if (!whole) {
+                // What no row sees may hold anything, NaN codes too, and 0 * NaN is
+                // NaN: its values become zero.  Positions only some rows see keep
+                // their values but for NaN, which the epilogue gives to those rows.
+                const int pos = v_pos(i, nc), slot = pos % C::kSlots;
+                if (ok) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                const bool none = t < rq.lo || t >= rq.len, some = !none && t < col_lo[cols - 1];
+                if (ok && (none || some)) {
+#pragma unroll
+                    for (int x = 0; x < C::kAtoms; ++x)
+#pragma unroll
+                        for (int k = 0; k < C::kRow / 16; ++k) {
+                            uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot + x * kTile * C::kRow +
+                                                                 tc::swz8_off<C::kRow>(tid, k));
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (some) {
+                                w = *p;
+                                uint32_t *u = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                                for (int b = 0; b < 4; ++b)
+                                    u[b] &= ~__vcmpeq4(u[b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            }
+                            *p = w;
+                        }
+                }
+            }
+            gdn::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&p_full[i & 1]);
+        }
+        // ---- the piece's end
+        if (ok && nc > 0) ok = gdn::mbar_wait_bounded(&pv_done[(nc - 1) & 1], ((nc - 1) >> 1) & 1, a.wait_ns);
+        const bool skip = soft_or(!ok || bad);
+        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+        if (bad) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        tc::fence_after();
+        // sums of the 128 positions' parts, through the weights' buffers
+        float *red = reinterpret_cast<float *>(s_p);
+        if (!skip) {
+#pragma unroll
+            for (int c = 0; c < RB; ++c) red[c * 129 + tid] = l[c];
+        }
+        soft_sync();
+        {
+            constexpr int per = kSoft / RB;  // threads a column
+            const int c = tid / per, s = tid % per;
+            float x = 0.f;
+            if (!skip)
+                for (int k = s; k < kSoft; k += per) x += red[c * 129 + k];
+#pragma unroll
+            for (int o = 1; o < per; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (s == 0) col_l[c] = x;
+        }
+        soft_sync();
+        const bool direct = rq.pieces == 1;
+        const int64_t unit = (int64_t(r) * a.max_pieces + piece) * gridDim.y + blockIdx.y;
+        if (!direct && tid < RB) a.ws_ml[unit * RB + tid] = make_float2(col_m[tid], skip ? -1.f : col_l[tid]);
+        if (direct && a.lse && tid < cols && !skip)
+            a.lse[(int64_t(rq.t0) + col_row[tid]) * a.c.h_q + hk * a.group + (blk * RB + tid) % a.group] =
+                col_l[tid] == 0.f ? -INFINITY : (col_m[tid] + log2f(col_l[tid])) * 0.6931471805599453f;
+        if (!skip) {
+            const float back = vref / kBase;
+#pragma unroll 1
+            for (int x = 0; x < C::kAtoms; ++x) {
+                const int e = x * C::kRow + tid;  // this thread's element (d = 64: lanes past 63 hold none)
+                const bool mine = e < D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 8) {
+                    uint32_t w0[8], w1[8], w2[8], w3[8];
+                    float o[8];
+                    if (nc > 0) {
+                        tc::ld8_async(tm_o + lane_base + x * C::kNp + c0, w0);
+                        tc::ld8_async(tm_o + lane_base + x * C::kNp + RB + c0, w1);
+                        tc::ld8_async(tm_o + lane_base + x * C::kNp + 2 * RB + c0, w2);
+                        tc::ld8_async(tm_o + lane_base + x * C::kNp + 3 * RB + c0, w3);
+                        tc::ld_wait();
+                        tc::ld_fence_regs(w0);
+                        tc::ld_fence_regs(w1);
+                        tc::ld_fence_regs(w2);
+                        tc::ld_fence_regs(w3);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float s = fmaf(__uint_as_float(w3[c]), 1.f / 32.f, __uint_as_float(w2[c]));
+                            o[c] = back * fmaf(fmaf(s, 1.f / 32.f, __uint_as_float(w1[c])), 1.f / 32.f,
+                                               __uint_as_float(w0[c]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) o[c] = 0.f;
+                    }
+                    if (!mine) continue;
+                    if (fresh)
+                        for (int j = 0; j < rq.n; ++j) {
+                            const float v = gdn::bf16_to_f32(a.v[(int64_t(rq.t0) + j) * a.v_stride + int64_t(hk) * D + e]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const int row = col_row[c0 + c], win = a.c.window;
+                                if (j <= row && (!win || j > row - win)) o[c] = fmaf(fresh_p[c0 + c][j], v, o[c]);
+                            }
+                        }
+                    // NaN of positions that only some rows see
+                    const int edge = min(min(col_lo[cols - 1], rq.len), (tile0 + nc) * kTile);
+                    for (int t = max(rq.lo, tile0 * kTile); t < edge; ++t) {
+                        const uint8_t code = a.c.kv[int64_t(tab[t / T]) * a.c.page_stride +
+                                                    int64_t(a.layer) * a.c.layer_stride +
+                                                    (int64_t(a.c.h_kv + hk) * T + t % T) * D + e];
+                        if ((code & 0x7f) == 0x7f) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (c0 + c < cols && t >= col_lo[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c0 + c >= cols) break;
+                        if (direct) {
+                            const float s = col_l[c0 + c];
+                            a.o[(int64_t(rq.t0) + col_row[c0 + c]) * a.o_stride +
+                                int64_t(hk * a.group + (blk * RB + c0 + c) % a.group) * D + e] =
+                                gdn::f32_to_bf16(s == 0.f ? 0.f : o[c] / s);
+                        } else {
+                            a.ws_o[(unit * RB + c0 + c) * D + e] = o[c];
+                        }
+                    }
+                }
+            }
+        }
+        tc::fence_before();
     }
-    __shared__ float sm[kWarps], sl[kWarps], sa[kWarps][D];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sa[warp][e * 32 + lane] = acc[e];
     __syncthreads();
-    float top = -INFINITY;
-    for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sm[k]);
-    float sum = 0.f, f[kWarps];
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        f[k] = sm[k] == -INFINITY ? 0.f : expf(sm[k] - top);
-        sum += f[k] * sl[k];
+    if (warp == 5) {
+        tc::fence_after();
+        tc::tmem_dealloc(tm, C::kTmem);
     }
-    for (int e = threadIdx.x; e < D; e += kThreads) {
-        float x = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) x += f[k] * sa[k][e];
-        a.o[(int64_t(t0) + i) * a.o_stride + int64_t(h) * D + e] = gdn::f32_to_bf16(total ? x / sum : 0.f);
+}
+
+// Joins the pieces of one (row, query head): o = sum 2^(m_s - M) O_s / sum
+// 2^(m_s - M) l_s in piece order.  Groups of d/4 threads take every G-th
+// piece, so that the pieces' loads are in flight together.
+constexpr int kJoin = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__ AttendArgs a, const int RB) {
+    gdn::pdl_enter();
+    constexpr int W = D / 4, G = kJoin / W;
+    const int i = blockIdx.x, h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
+    const Request rq = request_of(a, r);
+    if (rq.bad || i >= rq.n || rq.pieces <= 1) return;
+    const int hk = h / a.group, x = i * a.group + h % a.group, blk = x / RB, c = x % RB;
+    const int gy = a.c.h_kv * a.blocks;
+    const int64_t unit0 = int64_t(r) * a.max_pieces * gy + hk * a.blocks + blk;
+    __shared__ float s_m[kJoin / 32], s_l[G];
+    __shared__ float4 s_o[G][W];
+    float m = -INFINITY;
+    bool skip = false;
+    for (int s = tid; s < rq.pieces; s += kJoin) {
+        const float2 ml = a.ws_ml[(unit0 + int64_t(s) * gy) * RB + c];
+        m = fmaxf(m, ml.x);
+        skip |= ml.y < 0.f;
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[(int64_t(t0) + i) * a.c.h_q + h] = total ? top + logf(sum) : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) s_m[tid >> 5] = m;
+    if (__syncthreads_or(skip)) return;
+#pragma unroll
+    for (int k = 0; k < kJoin / 32; ++k) m = fmaxf(m, s_m[k]);
+    const int g = tid / W, e = tid % W;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = g; s < rq.pieces; s += G) {
+        const int64_t u = (unit0 + int64_t(s) * gy) * RB + c;
+        const float2 ml = a.ws_ml[u];
+        const float4 o = __ldcs(reinterpret_cast<const float4 *>(a.ws_o + u * D) + e);
+        const float f = ex2(ml.x - m);
+        if (ml.y != 0.f) {  // a piece of which the row sees nothing has no sums (and its outputs no meaning)
+            l = fmaf(f, ml.y, l);
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+            acc.z = fmaf(f, o.z, acc.z);
+            acc.w = fmaf(f, o.w, acc.w);
+        }
+    }
+    s_o[g][e] = acc;
+    if (e == 0) s_l[g] = l;
+    __syncthreads();
+    if (tid >= W) return;
+    acc = s_o[0][e];
+    l = s_l[0];
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+        const float4 o = s_o[k][e];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+        l += s_l[k];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2 w;
+    w.x = gdn::f32_to_bf16(acc.x * inv) | (uint32_t(gdn::f32_to_bf16(acc.y * inv)) << 16);
+    w.y = gdn::f32_to_bf16(acc.z * inv) | (uint32_t(gdn::f32_to_bf16(acc.w * inv)) << 16);
+    *reinterpret_cast<uint2 *>(a.o + (int64_t(rq.t0) + i) * a.o_stride + int64_t(h) * D + e * 4) = w;
+    if (e == 0 && a.lse)
+        a.lse[(int64_t(rq.t0) + i) * a.c.h_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// A layer's pages as [page][2 h_kv page_tokens rows][d] bytes; boxes of one
+// page and head, rows of at most 128 bytes, swizzled to that width.
+bool encode_pages(CUtensorMap *m, const kv8_cache *c, int layer) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(c->d), cuuint64_t(2) * c->h_kv * c->page_tokens, cuuint64_t(c->num_pages)};
+    const cuuint64_t strides[2] = {cuuint64_t(c->d), cuuint64_t(c->page_stride)};
+    const cuuint32_t box[3] = {cuuint32_t(c->d < 128 ? c->d : 128), cuuint32_t(c->page_tokens), 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c->kv + int64_t(layer) * c->layer_stride, dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, c->d < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int rb, blocks, piece_tiles, max_pieces;
+};
+
+Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, int32_t split_tokens) {
+    Plan p;
+    const int64_t cols = int64_t(max_rows) * (c->h_q / c->h_kv);
+    const int most = c->d == 256 ? 32 : 64;
+    p.rb = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || most == 32 ? 32 : 64;
+    p.blocks = int((cols + p.rb - 1) / p.rb);
+    // positions a request's rows can see, and the tiles they may lie in
+    int64_t seen = max_len;
+    if (c->window && c->window < seen) seen = int64_t(c->window) + kTile;
+    const int64_t tiles = (seen + kTile - 1) / kTile;
+    const int64_t units = int64_t(B) * c->h_kv * p.blocks;
+    const int64_t slots = 152 * (c->d == 256 || p.rb == 64 ? 1 : 2);
+    int64_t t;
+    if (split_tokens > 0)
+        t = (int64_t(split_tokens) + kTile - 1) / kTile;
+    else
+        t = (tiles * units + slots - 1) / slots;  // one wave
+    if (split_tokens <= 0 && t > 32) t = 32;
+    if (t > tiles) t = tiles;
+    if (t < 1) t = 1;
+    p.piece_tiles = int(t);
+    p.max_pieces = int(tiles > 0 ? (tiles + t - 1) / t : 1);
+    return p;
+}
+
+template <int D, int RB>
+int launch(const AttendArgs &a, dim3 grid, cudaStream_t st) {
+    using C = Cfg<D, RB>;
+    static const cudaError_t set = cudaFuncSetAttribute(kv8_attend_kernel<D, RB>,
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (set != cudaSuccess) return GDN_ERR_CUDA;
+    return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, grid, dim3(kThreads), C::kSmem, st, a);
 }
 
 }  // namespace
 
+static size_t ws_bytes(const kv8_cache *c, int32_t B, const Plan &p) {
+    if (p.max_pieces <= 1) return 0;
+    const size_t cols = size_t(B) * p.max_pieces * c->h_kv * p.blocks * p.rb;
+    return cols * (size_t(c->d) * 4 + 8);
+}
+
 extern "C" size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t max_len, int32_t max_rows,
                                              int32_t split_tokens) {
-    return 0;
+    if (gdn_host::kv8_check(cache) != GDN_OK || B <= 0 || max_len < 0 || max_len > gdn_host::kKv8MaxLen ||
+        max_rows <= 0 || max_rows > GDN_MAX_ROWS || split_tokens < 0)
+        return 0;
+    return ws_bytes(cache, B, plan_of(cache, B, max_len, max_rows, split_tokens));
 }
 
 extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
@@ -138,7 +909,13 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     if (k_new && (!gdn_host::kv8_rows_ok(k_new, k_stride, cache->h_kv, cache->d) ||
                   !gdn_host::kv8_rows_ok(v_new, v_stride, cache->h_kv, cache->d)))
         return GDN_ERR_ARG;
+    const Plan p = plan_of(cache, B, max_len, max_rows, split_tokens);
+    const size_t need = ws_bytes(cache, B, p);
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (need && !gdn_host::aligned16(workspace)) return GDN_ERR_ARG;
+    if (int64_t(cache->h_kv) * p.blocks > 65535) return GDN_ERR_ARG;
     AttendArgs a{};
+    if (!encode_pages(&a.map, cache, layer)) return GDN_ERR_CUDA;
     a.c = *cache;
     a.layer = layer;
     a.B = B;
@@ -146,6 +923,10 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.table_stride = table_stride;
     a.max_len = max_len;
     a.max_rows = max_rows;
+    a.group = cache->h_q / cache->h_kv;
+    a.blocks = p.blocks;
+    a.piece_tiles = p.piece_tiles;
+    a.max_pieces = p.max_pieces;
     a.cu_rows = cu_rows;
     a.cache_len = cache_len;
     a.table = table;
@@ -158,10 +939,33 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.o_stride = o_stride;
     a.o = o;
     a.lse = lse;
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_ml = need ? reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                                need / (size_t(cache->d) * 4 + 8) * (size_t(cache->d) * 4))
+                   : nullptr;
     a.status = dev_status;
-    const dim3 grid(unsigned(max_rows), unsigned(cache->h_q), unsigned(B));
+    a.wait_ns = gdn::kWaitLimitNs;
+    const dim3 grid(unsigned(p.max_pieces), unsigned(cache->h_kv * p.blocks), unsigned(B));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache->d == 64) return gdn_host::launch_pdl(kv8_attend_kernel<64>, grid, dim3(kThreads), 0, st, a);
-    if (cache->d == 128) return gdn_host::launch_pdl(kv8_attend_kernel<128>, grid, dim3(kThreads), 0, st, a);
-    return gdn_host::launch_pdl(kv8_attend_kernel<256>, grid, dim3(kThreads), 0, st, a);
+    int rc = GDN_ERR_SHAPE;
+    const int key = cache->d * 100 + p.rb;
+    switch (key) {
+        case 6408: rc = launch<64, 8>(a, grid, st); break;
+        case 6416: rc = launch<64, 16>(a, grid, st); break;
+        case 6432: rc = launch<64, 32>(a, grid, st); break;
+        case 6464: rc = launch<64, 64>(a, grid, st); break;
+        case 12808: rc = launch<128, 8>(a, grid, st); break;
+        case 12816: rc = launch<128, 16>(a, grid, st); break;
+        case 12832: rc = launch<128, 32>(a, grid, st); break;
+        case 12864: rc = launch<128, 64>(a, grid, st); break;
+        case 25608: rc = launch<256, 8>(a, grid, st); break;
+        case 25616: rc = launch<256, 16>(a, grid, st); break;
+        case 25632: rc = launch<256, 32>(a, grid, st); break;
+        default: break;
+    }
+    if (rc != GDN_OK || p.max_pieces <= 1) return rc;
+    const dim3 jgrid{unsigned(max_rows), unsigned(cache->h_q), unsigned(B)};
+    if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, jgrid, dim3(kJoin), 0, st, a, p.rb);
+    if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, jgrid, dim3(kJoin), 0, st, a, p.rb);
+    return gdn_host::launch_pdl(kv8_join_kernel<256>, jgrid, dim3(kJoin), 0, st, a, p.rb);
 }

@@ -130,6 +130,47 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// ---- kind::f8f6f4: e4m3 x e4m3, fp32 accumulation, K = 32 a step -----------
+
+// Instruction descriptor; A or B MN-major with the bits above.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4)                       // D format: f32 (A, B formats 0: e4m3)
+           | (uint32_t(N >> 3) << 17)      // N / 8
+           | (uint32_t(M >> 4) << 24);     // M / 16
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an 8-bit tile whose rows are ROW bytes (64 or 128) in the
+// swizzle of that width: 8-row groups 8 * ROW bytes apart.  K-major tiles
+// leave lbo unused; an MN-major tile (rows are K, the ROW elements of a row
+// are MN) finds MN element ROW and up lbo bytes further on.  K steps of 32
+// advance a K-major start by 32 bytes and an MN-major one by 32 rows.
+template <int ROW>
+__device__ __forceinline__ uint64_t smem_desc8(uint32_t saddr, uint32_t lbo) {
+    static_assert(ROW == 64 || ROW == 128, "swizzles of 64 and 128 bytes");
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3fffu);
+    d |= uint64_t((lbo >> 4) & 0x3fffu) << 16;
+    d |= uint64_t((8u * ROW) >> 4) << 32;
+    d |= uint64_t(1u) << 46;
+    d |= uint64_t(ROW == 128 ? 2u : 4u) << 61;
+    return d;
+}
+
+// Byte offset of 16-byte chunk `chunk` of row r in such a tile.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz8_off(int r, int chunk) {
+    return uint32_t(r) * ROW + (uint32_t(ROW == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) << 4);
+}
+
 // Arrive on the mbarrier once every MMA issued so far by this thread is done.
 __device__ __forceinline__ void commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -163,6 +204,17 @@ __device__ __forceinline__ void ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 lanes x 32 bits, 8 consecutive columns, without waiting.
+__device__ __forceinline__ void ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void ld_fence_regs(uint32_t (&r)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[i]));
+}
 // After ld_wait(): ties the loaded registers to a point after the wait, so
 // that no use of them is scheduled before it.
 __device__ __forceinline__ void ld_fence_regs(uint32_t (&r)[16]) {

@@ -1,6 +1,8 @@
 """Attention over the paged 8-bit cache against the fp64 form: head layouts,
 page sizes, ragged rows and lengths, windows, empty rows, pieces of any size,
 what lies past a request's end, strides, streams and refusals."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -367,3 +369,11 @@ def test_host_refusals(cuda_dev):
     for kw in (dict(q=qt.float()), dict(q=qt[:, :2]), dict(k_new=kt[:1]), dict(table=table.long())):
         with pytest.raises(ValueError):
             call(**kw)
+
+    big = ctypes.byref(c.c)
+    need = gs.lib.kv8_attend_workspace_bytes(big, 1, 100000, 2, 128)
+    assert need > 0
+    st = gs.lib.kv8_attend(big, 0, 1, 2, cu.data_ptr(), length.data_ptr(), table.data_ptr(), 4, qt.data_ptr(),
+                           qt.stride(0), kt.data_ptr(), kt.stride(0), vt.data_ptr(), vt.stride(0), o.data_ptr(), 512,
+                           None, 100000, 2, 128, None, 0, c.status.data_ptr(), None)
+    assert st == gs.GDN_ERR_WORKSPACE
