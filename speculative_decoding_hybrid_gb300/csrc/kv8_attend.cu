@@ -19,9 +19,10 @@
 // that is once, at a piece's first tile.  One vote a tile decides.
 //
 // One CTA per (piece of a request's positions, kv head and block of RB
-// columns, request): warps 0-3 softmax (thread = position = lane), warp 4
-// copies pages (tiled TMA, 128- or 64-byte swizzle, K and V tiles through one
-// ring), warp 5 issues the products.  The transaction's own rows, bf16, come
+// columns, request): groups of four softmax warps (thread = position = lane,
+// a group's share of the columns each), one warp that copies pages (tiled TMA,
+// 128- or 64-byte swizzle, K and V tiles through one ring), one that issues
+// the products.  The transaction's own rows, bf16, come
 // last: their keys as one more tile, each a hi and a lo position (16 + 16
 // lanes) split like q, their values in fp32 in the epilogue.
 // Pieces leave (m, l, O) in the workspace for kv8_join_kernel; a request with
@@ -34,8 +35,6 @@
 namespace {
 
 constexpr int kTile = 128;      // positions a tile
-constexpr int kSoft = 128;      // softmax threads
-constexpr int kThreads = kSoft + 64;
 // Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
 // is 2^-25, so 2^-27 of a weight at the reference.  More slack moves the
 // reference less often and costs that many bits at the low end.
@@ -89,18 +88,24 @@ __device__ __forceinline__ float warp_max(float x) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
-// Barrier of the softmax warps with an OR over a predicate.
-__device__ __forceinline__ bool soft_or(bool p) {
+// Barrier of a group's four softmax warps with an OR over a predicate.
+__device__ __forceinline__ bool group_or(int group, bool p) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, "
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, "
         "q;\n}\n"
         : "=r"(r)
-        : "r"(uint32_t(p))
+        : "r"(uint32_t(p)), "r"(group + 1)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("barrier.cta.sync 5, %0;" ::"n"(THREADS) : "memory");
+}
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_u32(bar)) : "memory");
 }
@@ -143,6 +148,13 @@ struct Cfg {
     static constexpr int kQ = kNs * D;
     static constexpr int kP = kTile * (RB == 8 ? 64 : kNp);
     static constexpr int kSlot = kTile * D;
+    // groups of four softmax warps, each with its share of the columns: a warp
+    // waits on its own chain of loads, exponentials and conversions most of the
+    // time, so an SM wants at least eight of them
+    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : RB / 16;
+    static constexpr int kCols = RB / kGroups;           // columns a thread
+    static constexpr int kSoft = 128 * kGroups;          // softmax threads
+    static constexpr int kThreads = kSoft + 64;
     // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule it out
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
     static constexpr int kFixed = kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024 + 4096;
@@ -160,12 +172,13 @@ __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
 template <int D, int RB>
-__global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
+    kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
     using C = Cfg<D, RB>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
     __shared__ uint32_t tmem_ptr;
-    __shared__ float col_m[RB], col_coef[RB], col_fac[RB], col_max[4][RB], v_max[4];
+    __shared__ float col_m[RB], col_coef[RB], col_fac[RB], col_max[4][RB], v_max[C::kGroups][4];
     __shared__ int col_lo[RB], col_row[RB];
     __shared__ float fresh_k[16], fresh_p[RB][16];
     __shared__ float col_l[RB];
@@ -198,20 +211,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
         }
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(&s_full[i], 1);
-            gdn::mbar_init(&s_free[i], 4);
-            gdn::mbar_init(&p_full[i], 4);
+            gdn::mbar_init(&s_free[i], C::kSoft / 32);
+            gdn::mbar_init(&p_full[i], C::kSoft / 32);
             gdn::mbar_init(&pv_done[i], 1);
         }
-        gdn::mbar_init(&q_ready, 4);
+        gdn::mbar_init(&q_ready, C::kSoft / 32);
         gdn::mbar_init(&drain, 1);
     }
-    if (warp == 5) tc::tmem_alloc(&tmem_ptr, C::kTmem);
+    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
+    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_ptr, C::kTmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_ptr, tm_o = tm + 2 * C::kNs;
 
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         // ---- copies: page ids 32 at a time, the next 32 loaded ahead
         const int per = kTile / T;  // pages a tile
         const int page0 = tile0 * per, first = rq.lo / T, last = (rq.len + T - 1) / T;
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
                 (void)gdn::mbar_wait_bounded(&full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
         }
-    } else if (warp == 5) {
+    } else if (warp == kMmaWarp) {
         // ---- products
         if (lane == 0 && nt > 0) {
             constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
@@ -380,20 +394,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
                 return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
             };
             const float coef = a.c.sm_scale * 1.4426950408889634f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < RB; c0 += 16) {
-                const int c = c0 + (tid >> 3);
-                const bool in = c < RB;  // RB = 8 leaves half of the threads without a column
+            // eight threads a column; the columns fill whole warps
+            for (int c = tid >> 3; c < RB; c += C::kSoft / 8) {
                 const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
                 float e[E];
 #pragma unroll
                 for (int i = 0; i < E; ++i) e[i] = 0.f;
-                if (in && c < cols) load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, e);
-                // a thread without a column repeats the last one's zeros' work on that column's values
-                const int cc = in ? c : RB - 1;
-                if (RB >= 16 || warp < 2) {
-                    const float down = split(e, s_q, C::kNs, cc, RB + cc);
-                    if (sub == 0 && in) {
+                if (c < cols) load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, e);
+                {
+                    const float down = split(e, s_q, C::kNs, c, RB + c);
+                    if (sub == 0) {
                         col_m[c] = kUnset;
                         col_coef[c] = coef * down;
                         col_row[c] = row;
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
                     }
                 }
             }
-            if (fresh) {
+            if (fresh && tid < 128) {
                 const int j = tid >> 3;
                 float e[E];
 #pragma unroll
@@ -415,13 +425,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             gdn::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&q_ready);
-            soft_sync();
+            soft_sync<C::kSoft>();
         }
+        // this thread's position in a tile and its columns col0 .. col0 + N - 1
+        constexpr int N = C::kCols;
+        const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N;
         const int32_t *tab = a.table + int64_t(r) * a.table_stride;
         const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
         bool bad = false, ok = true;
         auto page_of = [&](int i) {  // page of this thread's position in tile i, -1 if no row sees it
-            const int t = (tile0 + i) * kTile + tid;
+            const int t = (tile0 + i) * kTile + pos_in;
             if (i >= nc || t < rq.lo || t >= rq.len) return -1;
             const int p = tab[t / T];
             if (p < 0 || p >= a.c.num_pages) {
@@ -437,19 +450,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
         // ids two tiles ahead, scales one
         int page1 = page_of(1);
         float2 sc_next = scales_of(page_of(0));
-        float l[RB], z[RB];
+        float l[N], z[N];
 #pragma unroll
-        for (int c = 0; c < RB; ++c) l[c] = 0.f;
+        for (int c = 0; c < N; ++c) l[c] = 0.f;
         float vref = kv8::pow2i(kv8::kMinScaleExp);
-        const uint32_t lane_base = uint32_t(warp * 32) << 16;
+        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
 
         for (int i = 0; i < nt; ++i) {
             const bool is_fresh = i >= nc;
-            const int t = (tile0 + i) * kTile + tid;
+            const int t = (tile0 + i) * kTile + pos_in;
             float2 sc = sc_next;
             sc_next = scales_of(page1);
             page1 = page_of(i + 2);
-            if (is_fresh) sc = make_float2(tid < 32 && (tid & 15) < rq.n ? fresh_k[tid & 15] : 0.f, 0.f);
+            if (is_fresh) sc = make_float2(pos_in < 32 && (pos_in & 15) < rq.n ? fresh_k[pos_in & 15] : 0.f, 0.f);
             // whole: every row sees every position of the tile
             const bool whole = !is_fresh && (tile0 + i + 1) * kTile <= rq.len && (tile0 + i) * kTile >= col_lo[cols - 1];
             if (ok) ok = gdn::mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, a.wait_ns);
@@ -458,32 +471,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             // z - m of every column (m = 0 where the reference is to move)
             auto load_z = [&](bool plain) {
 #pragma unroll
-                for (int c0 = 0; c0 < RB; c0 += 16) {
-                    uint32_t hi[16], lo[16];
-                    tc::ld16_async(tm + lane_base + (i & 1) * C::kNs + c0, hi);
-                    if (RB > 8) tc::ld16_async(tm + lane_base + (i & 1) * C::kNs + RB + c0, lo);
+                for (int c0 = 0; c0 < N; c0 += 8) {
+                    uint32_t hi[8], lo[8];
+                    tc::ld8_async(tm + lane_base + (i & 1) * C::kNs + col0 + c0, hi);
+                    tc::ld8_async(tm + lane_base + (i & 1) * C::kNs + RB + col0 + c0, lo);
                     tc::ld_wait();
                     tc::ld_fence_regs(hi);
-                    if (RB > 8) tc::ld_fence_regs(lo);
+                    tc::ld_fence_regs(lo);
 #pragma unroll
-                    for (int c = 0; c < (RB > 8 ? 16 : 8); ++c) {
-                        float s = fmaf(__uint_as_float(RB > 8 ? lo[c] : hi[8 + c]), 1.f / 32.f, __uint_as_float(hi[c]));
+                    for (int c = 0; c < 8; ++c) {
+                        float s = fmaf(__uint_as_float(lo[c]), 1.f / 32.f, __uint_as_float(hi[c]));
                         if (is_fresh) {  // the other part of the position
                             const float other = __shfl_xor_sync(0xffffffffu, s, 16);
-                            s = tid & 16 ? fmaf(s, 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, s);
+                            s = pos_in & 16 ? fmaf(s, 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, s);
                         }
-                        z[c0 + c] = fmaf(s, sc.x * col_coef[c0 + c], plain ? 0.f : -col_m[c0 + c]);
+                        z[c0 + c] = fmaf(s, sc.x * col_coef[col0 + c0 + c], plain ? 0.f : -col_m[col0 + c0 + c]);
                     }
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int c = 0; c < RB; ++c) {
+                    for (int c = 0; c < N; ++c) {
                         bool see;
                         if (is_fresh) {
-                            const int j = tid & 15, row = col_row[c], w = a.c.window;
-                            see = tid < 32 && j < rq.n && j <= row && (!w || j > row - w);
+                            const int j = pos_in & 15, row = col_row[col0 + c], w = a.c.window;
+                            see = pos_in < 32 && j < rq.n && j <= row && (!w || j > row - w);
                         } else {
-                            see = t < rq.len && t >= col_lo[c];
+                            see = t < rq.len && t >= col_lo[col0 + c];
                         }
                         if (!see) z[c] = -INFINITY;
                     }
@@ -492,55 +505,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             load_z(false);
             float over = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < RB; ++c) over = fmaxf(over, z[c]);
-            if (soft_or(over > kSlack || sc.y > vref || !ok)) {
+            for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
+            if (group_or(grp, over > kSlack || sc.y > vref || !ok)) {
                 // ---- the reference moves (or a wait ran out)
-                if (soft_or(!ok)) {
+                if (group_or(grp, !ok)) {
                     ok = false;
                     break;
                 }
                 load_z(true);
 #pragma unroll
-                for (int c = 0; c < RB; ++c) {
+                for (int c = 0; c < N; ++c) {
                     const float x = warp_max(z[c]);
-                    if (lane == 0) col_max[warp][c] = x;
+                    if (lane == 0) col_max[warp & 3][col0 + c] = x;
                 }
                 const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
-                if (lane == 0) v_max[warp] = __uint_as_float(vm);
-                soft_sync();
-                for (int c = tid; c < RB; c += kSoft) {
+                if (lane == 0) v_max[grp][warp & 3] = __uint_as_float(vm);
+                group_sync(grp);
+                if (pos_in < N) {
+                    const int c = col0 + pos_in;
                     const float was = col_m[c];
                     const float now =
                         fmaxf(fmaxf(fmaxf(col_max[0][c], col_max[1][c]), fmaxf(col_max[2][c], col_max[3][c])), was);
                     col_fac[c] = ex2(was - now);
                     col_m[c] = now;
                 }
-                const float vnow = fmaxf(fmaxf(fmaxf(v_max[0], v_max[1]), fmaxf(v_max[2], v_max[3])), vref);
+                const float vnow = fmaxf(fmaxf(fmaxf(v_max[grp][0], v_max[grp][1]), fmaxf(v_max[grp][2], v_max[grp][3])), vref);
                 const float vfac = vref / vnow;
                 vref = vnow;
-                soft_sync();
+                group_sync(grp);
 #pragma unroll
-                for (int c = 0; c < RB; ++c) {
-                    l[c] *= col_fac[c];
-                    z[c] -= col_m[c];
+                for (int c = 0; c < N; ++c) {
+                    l[c] *= col_fac[col0 + c];
+                    z[c] -= col_m[col0 + c];
                 }
                 if (i > 0) {
                     ok = gdn::mbar_wait_bounded(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, a.wait_ns);
-                    if (soft_or(!ok)) {
+                    if (group_or(grp, !ok)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < C::kAtoms * C::kNp; x += 16) {
-                        uint32_t w[16];
-                        tc::ld16_async(tm_o + lane_base + x, w);
+                    for (int x = 0; x < C::kAtoms * 4 * N; x += 8) {  // this group's columns of every part
+                        const int at = x / N * RB + col0 + x % N;
+                        uint32_t w[8];
+                        tc::ld8_async(tm_o + lane_base + at, w);
                         tc::ld_wait();
                         tc::ld_fence_regs(w);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            w[c] = __float_as_uint(__uint_as_float(w[c]) * (col_fac[(x + c) % RB] * vfac));
-                        st16(tm_o + lane_base + x, w);
+                        for (int c = 0; c < 8; ++c)
+                            w[c] = __float_as_uint(__uint_as_float(w[c]) * (col_fac[at % RB + c] * vfac));
+                        tc::st8(tm_o + lane_base + at, w);
                     }
                     tc::st_wait();
                 }
@@ -551,12 +566,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             if (lane == 0) arrive(&s_free[i & 1]);
 
             if (is_fresh) {
-                if (tid < 16) {
+                if (pos_in < 16) {
 #pragma unroll
-                    for (int c = 0; c < RB; ++c) {
+                    for (int c = 0; c < N; ++c) {
                         const float p = ex2(z[c]);
                         l[c] += p;
-                        fresh_p[c][tid] = p;
+                        fresh_p[col0 + c][pos_in] = p;
                     }
                 }
                 break;  // the last tile
@@ -565,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
             if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&pv_done[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
             uint8_t *pb = s_p + (i & 1) * C::kP;
             // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
-            constexpr int W = RB < 16 ? 8 : 16;
+            constexpr int W = N < 16 ? 8 : 16;
 #pragma unroll
-            for (int c0 = 0; c0 < RB; c0 += W) {
+            for (int c0 = 0; c0 < N; c0 += W) {
                 uint32_t part[4][W / 4];
 #pragma unroll
                 for (int c = 0; c < W; c += 2) {
@@ -589,16 +604,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int b = k * RB + c0;  // byte of the row
+                    const int b = k * RB + col0 + c0;  // byte of the row
                     uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
-                                   tc::swz8_off<C::kPRow>(tid, (b % C::kPRow) >> 4) + (b & 8);
+                                   tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
                     if constexpr (W == 16)
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
                     else
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(part[k][0], part[k][1]);
                 }
             }
-            if (!whole) {
+            if (!whole && grp == 0) {
                 // What no row sees may hold anything, NaN codes too, and 0 * NaN is
                 // NaN: its values become zero.  Positions only some rows see keep
                 // their values but for NaN, which the epilogue gives to those rows.
@@ -611,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
 #pragma unroll
                         for (int k = 0; k < C::kRow / 16; ++k) {
                             uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot + x * kTile * C::kRow +
-                                                                 tc::swz8_off<C::kRow>(tid, k));
+                                                                 tc::swz8_off<C::kRow>(pos_in, k));
                             uint4 w = make_uint4(0, 0, 0, 0);
                             if (some) {
                                 w = *p;
@@ -630,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
         }
         // ---- the piece's end
         if (ok && nc > 0) ok = gdn::mbar_wait_bounded(&pv_done[(nc - 1) & 1], ((nc - 1) >> 1) & 1, a.wait_ns);
-        const bool skip = soft_or(!ok || bad);
+        const bool skip = group_or(grp, !ok || bad);
         if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
         if (bad) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
         tc::fence_after();
@@ -638,34 +653,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
         float *red = reinterpret_cast<float *>(s_p);
         if (!skip) {
 #pragma unroll
-            for (int c = 0; c < RB; ++c) red[c * 129 + tid] = l[c];
+            for (int c = 0; c < N; ++c) red[(col0 + c) * 129 + pos_in] = l[c];
         }
-        soft_sync();
+        group_sync(grp);
         {
-            constexpr int per = kSoft / RB;  // threads a column
-            const int c = tid / per, s = tid % per;
+            constexpr int per = 128 / N;  // threads a column
+            const int c = col0 + pos_in / per, s = pos_in % per;
             float x = 0.f;
             if (!skip)
-                for (int k = s; k < kSoft; k += per) x += red[c * 129 + k];
+                for (int k = s; k < 128; k += per) x += red[c * 129 + k];
 #pragma unroll
             for (int o = 1; o < per; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (s == 0) col_l[c] = x;
         }
-        soft_sync();
+        group_sync(grp);
+        const int col = col0 + pos_in;  // of the threads that finish one
         const bool direct = rq.pieces == 1;
         const int64_t unit = (int64_t(r) * a.max_pieces + piece) * gridDim.y + blockIdx.y;
-        if (!direct && tid < RB) a.ws_ml[unit * RB + tid] = make_float2(col_m[tid], skip ? -1.f : col_l[tid]);
-        if (direct && a.lse && tid < cols && !skip)
-            a.lse[(int64_t(rq.t0) + col_row[tid]) * a.c.h_q + hk * a.group + (blk * RB + tid) % a.group] =
-                col_l[tid] == 0.f ? -INFINITY : (col_m[tid] + log2f(col_l[tid])) * 0.6931471805599453f;
+        if (!direct && pos_in < N) a.ws_ml[unit * RB + col] = make_float2(col_m[col], skip ? -1.f : col_l[col]);
+        if (direct && a.lse && pos_in < N && col < cols && !skip)
+            a.lse[(int64_t(rq.t0) + col_row[col]) * a.c.h_q + hk * a.group + (blk * RB + col) % a.group] =
+                col_l[col] == 0.f ? -INFINITY : (col_m[col] + log2f(col_l[col])) * 0.6931471805599453f;
         if (!skip) {
             const float back = vref / kBase;
 #pragma unroll 1
             for (int x = 0; x < C::kAtoms; ++x) {
-                const int e = x * C::kRow + tid;  // this thread's element (d = 64: lanes past 63 hold none)
+                const int e = x * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
                 const bool mine = e < D;
 #pragma unroll 1
-                for (int c0 = 0; c0 < cols; c0 += 8) {
+                for (int c0 = col0; c0 < min(cols, col0 + N); c0 += 8) {
                     uint32_t w0[8], w1[8], w2[8], w3[8];
                     float o[8];
                     if (nc > 0) {
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, RB>::kCtas) kv8_attend_kernel
         tc::fence_before();
     }
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         tc::fence_after();
         tc::tmem_dealloc(tm, C::kTmem);
     }
@@ -871,7 +887,7 @@ int launch(const AttendArgs &a, dim3 grid, cudaStream_t st) {
     static const cudaError_t set = cudaFuncSetAttribute(kv8_attend_kernel<D, RB>,
                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (set != cudaSuccess) return GDN_ERR_CUDA;
-    return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, grid, dim3(kThreads), C::kSmem, st, a);
+    return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, grid, dim3(C::kThreads), C::kSmem, st, a);
 }
 
 }  // namespace
