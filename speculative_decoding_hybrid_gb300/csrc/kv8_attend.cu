@@ -45,7 +45,7 @@ struct AttendArgs {
     CUtensorMap map;
     kv8_cache c;
     int32_t layer, B, row_capacity, table_stride, max_len, max_rows;
-    int32_t group, blocks, piece_tiles, max_pieces;
+    int32_t group, blocks, piece_tiles, max_pieces, page_shift;  // page_tokens = 1 << page_shift
     const int32_t *cu_rows, *cache_len, *table;
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride, o_stride;
@@ -109,13 +109,10 @@ __device__ __forceinline__ void soft_sync() {
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 
 // fp16 pair arithmetic of the splits.
@@ -144,7 +141,7 @@ struct Cfg {
     static constexpr int kNs = 2 * RB;                   // score columns
     static constexpr int kNp = 4 * RB;                   // weight columns
     static constexpr int kPRow = RB == 8 ? 64 : RB == 64 ? 128 : kNp;  // bytes of a weight tile's row (64 or 128)
-    static constexpr int kFresh = 32 * D;                // bytes of the fresh keys
+    static constexpr int kFresh = 32 * D > 64 * RB ? 32 * D : 64 * RB;  // bytes of the fresh keys, and of the values
     static constexpr int kQ = kNs * D;
     static constexpr int kP = kTile * (RB == 8 ? 64 : kNp);
     static constexpr int kSlot = kTile * D;
@@ -157,8 +154,9 @@ struct Cfg {
     static constexpr int kThreads = kSoft + 64;
     // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule it out
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
-    static constexpr int kFixed = kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024 + 4096;
-    static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kFixed;
+    static constexpr int kFixed = 2 * kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024;
+    static constexpr int kStatic = RB == 64 ? 4096 : 2048;  // at least what __shared__ takes below
+    static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kStatic - kFixed;
     static constexpr int kSlots = kRoom / kSlot > 10 ? 10 : kRoom / kSlot;
     static constexpr int kSmem = kFixed + kSlots * kSlot;
     static constexpr int kTmemUse = 2 * kNs + kNp * (D == 256 ? 2 : 1);
@@ -178,9 +176,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
     __shared__ uint32_t tmem_ptr;
-    __shared__ float col_m[RB], col_coef[RB], col_fac[RB], col_max[4][RB], v_max[C::kGroups][4];
+    __shared__ alignas(16) float col_m[RB], col_coef[RB], col_fac[RB];
+    __shared__ float col_max[4][RB], v_max[C::kGroups][4];
     __shared__ int col_lo[RB], col_row[RB];
-    __shared__ float fresh_k[16], fresh_p[RB][16];
+    __shared__ float fresh_k[16];
     __shared__ float col_l[RB];
 
     gdn::pdl_enter();
@@ -194,14 +193,14 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     const int cols = min(RB, rq.n * a.group - blk * RB);  // columns of this block in use
     if (piece >= rq.pieces || cols <= 0) return;
 
-    const int T = a.c.page_tokens;
+    const int T = a.c.page_tokens, shift = a.page_shift;
     const int tile0 = rq.lo / kTile + piece * a.piece_tiles;
     const int nc = max(0, min(a.piece_tiles, rq.tiles - piece * a.piece_tiles));  // cached tiles
     const bool fresh = a.k != nullptr && piece == rq.pieces - 1;
     const int nt = nc + (fresh ? 1 : 0);
 
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *s_fk = sm, *s_q = s_fk + C::kFresh;
+    uint8_t *s_fk = sm, *s_fv = s_fk + C::kFresh, *s_q = s_fv + C::kFresh;
     uint8_t *s_p = s_q + ((C::kQ + 1023) & ~1023), *s_ring = s_p + 2 * C::kP;
 
     if (tid == 0) {
@@ -223,12 +222,14 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    float *fresh_p = reinterpret_cast<float *>(s_fk);  // [RB][16], once the fresh keys' product is done
+    static_assert(RB * 16 * 4 <= C::kFresh, "weights of the fresh rows");
     const uint32_t tm = tmem_ptr, tm_o = tm + 2 * C::kNs;
 
     if (warp == kCopyWarp) {
         // ---- copies: page ids 32 at a time, the next 32 loaded ahead
-        const int per = kTile / T;  // pages a tile
-        const int page0 = tile0 * per, first = rq.lo / T, last = (rq.len + T - 1) / T;
+        const int per = kTile >> shift;  // pages a tile
+        const int page0 = tile0 * per, first = rq.lo >> shift, last = (rq.len + T - 1) >> shift;
         const int32_t *tab = a.table + int64_t(r) * a.table_stride;
         auto ids = [&](int batch) {
             const int j = page0 + batch * 32 + lane;
@@ -278,8 +279,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 (void)gdn::mbar_wait_bounded(&full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
         }
     } else if (warp == kMmaWarp) {
-        // ---- products
-        if (lane == 0 && nt > 0) {
+        // ---- products: the warp runs the loop, one elected lane issues
+        if (nt > 0) {
             constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
             constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kAMnMajor | tc::kBMnMajor;
             const uint64_t dq = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_q), 16);
@@ -287,76 +288,96 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const uint64_t dp = tc::smem_desc8<C::kPRow>(gdn::smem_u32(s_p), kTile * C::kPRow);
             // V has 128 rows of M at d >= 128; at d = 64 rows 64.. read the next slot and are not used
             constexpr uint32_t lbo = C::kRow == 64 ? C::kSlot : 16;
+            const uint64_t dk0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), 16);
+            const uint64_t dv0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), lbo);
+            const uint64_t dfk = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_fk), 16);
+            const bool leader = elect_one();
             bool ok = gdn::mbar_wait_bounded(&q_ready, 0, a.wait_ns);
-            tc::fence_after();
             for (int i = 0; i <= nt && ok; ++i) {
                 if (i < nt) {
                     const bool cached = i < nc;
                     const int pos = k_pos(i), slot = pos % C::kSlots;
                     if (cached) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
                     if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&s_free[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t base = gdn::smem_u32(cached ? s_ring + slot * C::kSlot : s_fk);
-                    const uint32_t atom = cached ? kTile * C::kRow : 32 * C::kRow;
-                    const uint64_t dk = tc::smem_desc8<C::kRow>(base, 16);
+                    if (leader) {
+                        const uint64_t dk = cached ? tc::desc_at(dk0, slot * C::kSlot) : dfk;
+                        const uint32_t atom = cached ? kTile * C::kRow : 32 * C::kRow;
 #pragma unroll
-                    for (int s = 0; s < D / 32; ++s) {
-                        const uint32_t x = s * 32 / C::kRow, in = s * 32 % C::kRow;
-                        tc::mma_e4m3(tm + (i & 1) * C::kNs, tc::desc_at(dk, x * atom + in),
-                                     tc::desc_at(dq, x * C::kNs * C::kRow + in), id_s, s > 0);
+                        for (int s = 0; s < D / 32; ++s) {
+                            const uint32_t x = s * 32 / C::kRow, in = s * 32 % C::kRow;
+                            tc::mma_e4m3(tm + (i & 1) * C::kNs, tc::desc_at(dk, x * atom + in),
+                                         tc::desc_at(dq, x * C::kNs * C::kRow + in), id_s, s > 0);
+                        }
+                        tc::commit(&s_full[i & 1]);
+                        if (cached) tc::commit(&empty[slot]);
                     }
-                    tc::commit(&s_full[i & 1]);
-                    if (cached) tc::commit(&empty[slot]);
+                    __syncwarp();
                 }
                 if (i > 0 && i <= nc) {
                     const int j = i - 1, pos = v_pos(j, nc), slot = pos % C::kSlots;
                     ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
                     if (ok) ok = gdn::mbar_wait_bounded(&p_full[j & 1], (j >> 1) & 1, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint32_t base = gdn::smem_u32(s_ring + slot * C::kSlot);
+                    if (leader) {
+                        const uint64_t dv = tc::desc_at(dv0, slot * C::kSlot), dpj = tc::desc_at(dp, (j & 1) * C::kP);
 #pragma unroll
-                    for (int x = 0; x < C::kAtoms; ++x) {
-                        const uint64_t dv = tc::smem_desc8<C::kRow>(base + x * kTile * C::kRow, lbo);
+                        for (int x = 0; x < C::kAtoms; ++x)
 #pragma unroll
-                        for (int s = 0; s < kTile / 32; ++s)
-                            tc::mma_e4m3(tm_o + x * C::kNp, tc::desc_at(dv, s * 32 * C::kRow),
-                                         tc::desc_at(dp, (j & 1) * C::kP + s * 32 * C::kPRow), id_p, j > 0 || s > 0);
+                            for (int s = 0; s < kTile / 32; ++s)
+                                tc::mma_e4m3(tm_o + x * C::kNp,
+                                             tc::desc_at(dv, x * kTile * C::kRow + s * 32 * C::kRow),
+                                             tc::desc_at(dpj, s * 32 * C::kPRow), id_p, j > 0 || s > 0);
+                        tc::commit(&pv_done[j & 1]);
+                        tc::commit(&empty[slot]);
                     }
-                    tc::commit(&pv_done[j & 1]);
-                    tc::commit(&empty[slot]);
+                    __syncwarp();
                 }
             }
             if (!ok) {
                 gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-                tc::commit(&drain);  // products in flight read shared and write tensor memory
+                if (leader) tc::commit(&drain);  // products in flight read shared and write tensor memory
                 (void)gdn::mbar_wait_bounded(&drain, 0, a.wait_ns);
             }
         }
         __syncwarp();
     } else {
         // ---- softmax warps.  First the operands that come as bf16.
+        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
+        // page of this thread's position in tile i, if a row sees it; the id is looked
+        // at only where it is used, a tile later
+        auto wanted = [&](int i) {
+            const int t = (tile0 + i) * kTile + (tid & 127);
+            return i < nc && t >= rq.lo && t < rq.len;
+        };
+        auto page_of = [&](int i) { return wanted(i) ? tab[((tile0 + i) * kTile + (tid & 127)) >> shift] : -1; };
+        int page1 = page_of(0);
         {
             const int sub = tid & 7;
             constexpr int E = D / 8;  // elements a thread takes of a row
-            auto load = [&](const uint16_t *p, float (&x)[E]) {
+            auto load = [&](const uint16_t *p, uint4 (&w)[E / 8], bool have) {
+#pragma unroll
+                for (int e = 0; e < E / 8; ++e)
+                    w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * E + e * 8) : make_uint4(0, 0, 0, 0);
+            };
+            // Splits a row x = (hi + lo/32) 2^-k into rows rh and rl of a tile of `rows`
+            // rows; -> 2^-k, or NaN for a row that is not finite.
+            auto split = [&](const uint4 (&raw4)[E / 8], uint8_t *tile, int rows, int rh, int rl) {
+                float m = 0.f, x[E];
+                bool finite = true;
 #pragma unroll
                 for (int e = 0; e < E / 8; ++e) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(p + sub * E + e * 8);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    const uint32_t u[4] = {raw4[e].x, raw4[e].y, raw4[e].z, raw4[e].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
                         x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
                     }
                 }
-            };
-            // Splits a row x = (hi + lo/32) 2^-k into rows rh and rl of a tile of `rows`
-            // rows; -> 2^-k, or NaN for a row that is not finite.
-            auto split = [&](float (&x)[E], uint8_t *tile, int rows, int rh, int rl) {
-                float m = 0.f;
-                bool finite = true;
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const bool f = fabsf(x[e]) < INFINITY;
@@ -394,33 +415,31 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
             };
             const float coef = a.c.sm_scale * 1.4426950408889634f;
-            // eight threads a column; the columns fill whole warps
-            for (int c = tid >> 3; c < RB; c += C::kSoft / 8) {
-                const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
-                float e[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) e[i] = 0.f;
-                if (c < cols) load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, e);
-                {
-                    const float down = split(e, s_q, C::kNs, c, RB + c);
-                    if (sub == 0) {
-                        col_m[c] = kUnset;
-                        col_coef[c] = coef * down;
-                        col_row[c] = row;
-                        // positions the row sees start here
-                        const int w = a.c.window;
-                        col_lo[c] = w ? max(0, rq.len + (a.k ? row + 1 : 0) - w) : 0;
-                    }
+            // eight threads a row; q's columns fill whole warps, one pass takes them all
+            static_assert(RB <= C::kSoft / 8, "a thread has one column");
+            const int c = tid >> 3, x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
+            uint4 wq[E / 8], wk[E / 8], wv[E / 8];
+            load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, wq, c < cols);
+            const bool mine = fresh && c < rq.n;  // c: the row of k and v here
+            load(a.k + (int64_t(rq.t0) + c) * a.k_stride + int64_t(hk) * D, wk, mine);
+            load(a.v + (int64_t(rq.t0) + c) * a.v_stride + int64_t(hk) * D, wv, mine);
+            if (c < RB) {
+                const float down = split(wq, s_q, C::kNs, c, RB + c);
+                if (sub == 0) {
+                    col_m[c] = kUnset;
+                    col_coef[c] = coef * down;
+                    col_row[c] = row;
+                    // positions the row sees start here
+                    const int w = a.c.window;
+                    col_lo[c] = w ? max(0, rq.len + (a.k ? row + 1 : 0) - w) : 0;
                 }
             }
             if (fresh && tid < 128) {
-                const int j = tid >> 3;
-                float e[E];
+                const float dk = split(wk, s_fk, 32, c, 16 + c);
+                if (sub == 0) fresh_k[c] = dk;
 #pragma unroll
-                for (int i = 0; i < E; ++i) e[i] = 0.f;
-                if (j < rq.n) load(a.k + (int64_t(rq.t0) + j) * a.k_stride + int64_t(hk) * D, e);
-                const float dk = split(e, s_fk, 32, j, 16 + j);
-                if (sub == 0) fresh_k[j] = dk;
+                for (int e = 0; e < E / 8; ++e)
+                    *reinterpret_cast<uint4 *>(s_fv + (c * D + sub * E + e * 8) * 2) = wv[e];
             }
             gdn::fence_proxy_async_smem();
             __syncwarp();
@@ -430,37 +449,29 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         // this thread's position in a tile and its columns col0 .. col0 + N - 1
         constexpr int N = C::kCols;
         const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N;
-        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
         const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
         bool bad = false, ok = true;
-        auto page_of = [&](int i) {  // page of this thread's position in tile i, -1 if no row sees it
-            const int t = (tile0 + i) * kTile + pos_in;
-            if (i >= nc || t < rq.lo || t >= rq.len) return -1;
-            const int p = tab[t / T];
+        auto scales_of = [&](int p, int i) {
             if (p < 0 || p >= a.c.num_pages) {
-                bad = true;
-                return -1;
+                bad |= wanted(i);
+                return make_float2(0.f, 0.f);
             }
-            return p;
-        };
-        auto scales_of = [&](int p) {
-            return p >= 0 ? *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride)
-                          : make_float2(0.f, 0.f);
+            return *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride);
         };
         // ids two tiles ahead, scales one
-        int page1 = page_of(1);
-        float2 sc_next = scales_of(page_of(0));
+        float2 sc_next = scales_of(page1, 0);
+        page1 = page_of(1);
         float l[N], z[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) l[c] = 0.f;
-        float vref = kv8::pow2i(kv8::kMinScaleExp);
+        float vref = kv8::pow2i(kv8::kMinScaleExp), vinv = kBase / vref;
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
 
         for (int i = 0; i < nt; ++i) {
             const bool is_fresh = i >= nc;
             const int t = (tile0 + i) * kTile + pos_in;
             float2 sc = sc_next;
-            sc_next = scales_of(page1);
+            sc_next = scales_of(page1, i + 1);
             page1 = page_of(i + 2);
             if (is_fresh) sc = make_float2(pos_in < 32 && (pos_in & 15) < rq.n ? fresh_k[pos_in & 15] : 0.f, 0.f);
             // whole: every row sees every position of the tile
@@ -470,36 +481,48 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 
             // z - m of every column (m = 0 where the reference is to move)
             auto load_z = [&](bool plain) {
-#pragma unroll
-                for (int c0 = 0; c0 < N; c0 += 8) {
-                    uint32_t hi[8], lo[8];
-                    tc::ld8_async(tm + lane_base + (i & 1) * C::kNs + col0 + c0, hi);
-                    tc::ld8_async(tm + lane_base + (i & 1) * C::kNs + RB + col0 + c0, lo);
-                    tc::ld_wait();
-                    tc::ld_fence_regs(hi);
-                    tc::ld_fence_regs(lo);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float s = fmaf(__uint_as_float(lo[c]), 1.f / 32.f, __uint_as_float(hi[c]));
-                        if (is_fresh) {  // the other part of the position
-                            const float other = __shfl_xor_sync(0xffffffffu, s, 16);
-                            s = pos_in & 16 ? fmaf(s, 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, s);
-                        }
-                        z[c0 + c] = fmaf(s, sc.x * col_coef[col0 + c0 + c], plain ? 0.f : -col_m[col0 + c0 + c]);
-                    }
+                uint32_t hi[N], lo[N];
+                const uint32_t at = tm + lane_base + (i & 1) * C::kNs + col0;
+                if constexpr (N == 16) {
+                    tc::ld16_async(at, hi);
+                    tc::ld16_async(at + RB, lo);
+                } else {
+                    tc::ld8_async(at, hi);
+                    tc::ld8_async(at + RB, lo);
                 }
-                if (!whole) {
+                tc::ld_wait();
+                tc::ld_fence_regs(hi);
+                tc::ld_fence_regs(lo);
+#pragma unroll
+                for (int c = 0; c < N; ++c) z[c] = fmaf(__uint_as_float(lo[c]), 1.f / 32.f, __uint_as_float(hi[c]));
+                if (is_fresh) {  // the other part of the position
 #pragma unroll
                     for (int c = 0; c < N; ++c) {
-                        bool see;
-                        if (is_fresh) {
-                            const int j = pos_in & 15, row = col_row[col0 + c], w = a.c.window;
-                            see = pos_in < 32 && j < rq.n && j <= row && (!w || j > row - w);
-                        } else {
-                            see = t < rq.len && t >= col_lo[col0 + c];
-                        }
-                        if (!see) z[c] = -INFINITY;
+                        const float other = __shfl_xor_sync(0xffffffffu, z[c], 16);
+                        z[c] = pos_in & 16 ? fmaf(z[c], 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, z[c]);
                     }
+                }
+#pragma unroll
+                for (int c = 0; c < N; c += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(col_coef + col0 + c);
+                    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!plain) m = *reinterpret_cast<const float4 *>(col_m + col0 + c);
+                    z[c] = fmaf(z[c], sc.x * k.x, -m.x);
+                    z[c + 1] = fmaf(z[c + 1], sc.x * k.y, -m.y);
+                    z[c + 2] = fmaf(z[c + 2], sc.x * k.z, -m.z);
+                    z[c + 3] = fmaf(z[c + 3], sc.x * k.w, -m.w);
+                }
+                if (is_fresh) {
+                    const int j = pos_in & 15, w = a.c.window;
+#pragma unroll
+                    for (int c = 0; c < N; ++c) {
+                        const int row = col_row[col0 + c];
+                        const bool see = pos_in < 32 && j < rq.n && j <= row && (!w || j > row - w);
+                        z[c] = see ? z[c] : -INFINITY;
+                    }
+                } else if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < N; ++c) z[c] = t < rq.len && t >= col_lo[col0 + c] ? z[c] : -INFINITY;
                 }
             };
             load_z(false);
@@ -532,6 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 const float vnow = fmaxf(fmaxf(fmaxf(v_max[grp][0], v_max[grp][1]), fmaxf(v_max[grp][2], v_max[grp][3])), vref);
                 const float vfac = vref / vnow;
                 vref = vnow;
+                vinv = kBase / vnow;
                 group_sync(grp);
 #pragma unroll
                 for (int c = 0; c < N; ++c) {
@@ -571,12 +595,12 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     for (int c = 0; c < N; ++c) {
                         const float p = ex2(z[c]);
                         l[c] += p;
-                        fresh_p[col0 + c][pos_in] = p;
+                        fresh_p[(col0 + c) * 16 + pos_in] = p;
                     }
                 }
                 break;  // the last tile
             }
-            const float xw = sc.y / vref * kBase;
+            const float xw = sc.y * vinv;
             if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&pv_done[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
             uint8_t *pb = s_p + (i & 1) * C::kP;
             // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
@@ -707,19 +731,19 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (!mine) continue;
                     if (fresh)
                         for (int j = 0; j < rq.n; ++j) {
-                            const float v = gdn::bf16_to_f32(a.v[(int64_t(rq.t0) + j) * a.v_stride + int64_t(hk) * D + e]);
+                            const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int row = col_row[c0 + c], win = a.c.window;
-                                if (j <= row && (!win || j > row - win)) o[c] = fmaf(fresh_p[c0 + c][j], v, o[c]);
+                                if (j <= row && (!win || j > row - win)) o[c] = fmaf(fresh_p[(c0 + c) * 16 + j], v, o[c]);
                             }
                         }
                     // NaN of positions that only some rows see
                     const int edge = min(min(col_lo[cols - 1], rq.len), (tile0 + nc) * kTile);
                     for (int t = max(rq.lo, tile0 * kTile); t < edge; ++t) {
-                        const uint8_t code = a.c.kv[int64_t(tab[t / T]) * a.c.page_stride +
+                        const uint8_t code = a.c.kv[int64_t(tab[t >> shift]) * a.c.page_stride +
                                                     int64_t(a.layer) * a.c.layer_stride +
-                                                    (int64_t(a.c.h_kv + hk) * T + t % T) * D + e];
+                                                    (int64_t(a.c.h_kv + hk) * T + (t & (T - 1))) * D + e];
                         if ((code & 0x7f) == 0x7f) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
@@ -943,6 +967,7 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.blocks = p.blocks;
     a.piece_tiles = p.piece_tiles;
     a.max_pieces = p.max_pieces;
+    a.page_shift = 31 - __builtin_clz(unsigned(cache->page_tokens));
     a.cu_rows = cu_rows;
     a.cache_len = cache_len;
     a.table = table;
