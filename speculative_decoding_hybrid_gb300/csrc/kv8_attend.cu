@@ -40,6 +40,7 @@ constexpr int kTile = 128;      // positions a tile
 // reference less often and costs that many bits at the low end.
 constexpr float kBase = 4.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
+constexpr int kScales = 8;      // tiles whose scales may wait to be read; the ring of 10 slots holds back the copies before that
 
 struct AttendArgs {
     CUtensorMap map;
@@ -164,6 +165,86 @@ struct Cfg {
     static_assert(kTmemUse <= 512 && kSlots >= 3, "does not fit an SM");
 };
 
+// A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
+// into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a
+// row that is not finite.
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, uint4 (&w)[D / 64]) {
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+        w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * (D / 8) + e * 8) : make_uint4(0, 0, 0, 0);
+}
+template <int D>
+__device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl) {
+    constexpr int E = D / 8, kRow = D < 128 ? D : 128;
+    float m = 0.f, x[E];
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
+            x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const bool f = fabsf(x[e]) < INFINITY;
+        finite &= f;
+        x[e] = f ? x[e] : 0.f;
+        m = fmaxf(m, fabsf(x[e]));
+    }
+    uint32_t top = __float_as_uint(m);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (threadIdx.x & 24)) & 0xffu;
+    const int k = max(-110, min(110, 7 - (int(top >> 23) - 127)));  // largest in [128, 256)
+    const float up = kv8::pow2i(k), up32 = up * 32.f, down = kv8::pow2i(-k);
+#pragma unroll
+    for (int b = 0; b < E / 8; ++b) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t hh[2], ll[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x0 = x[b * 8 + g * 4 + 2 * i], x1 = x[b * 8 + g * 4 + 2 * i + 1];
+                hh[i] = kv8::e4m3x2(x0 * up, x1 * up);
+                const float2 back = kv8::f32x2_of(uint16_t(hh[i]));
+                ll[i] = kv8::e4m3x2(fmaf(back.x, -32.f, x0 * up32), fmaf(back.y, -32.f, x1 * up32));
+            }
+            h[g] = hh[0] | (hh[1] << 16);
+            l[g] = ll[0] | (ll[1] << 16);
+        }
+        const int e0 = sub * E + b * 8, atom = e0 / kRow, in = e0 % kRow;
+        uint8_t *t = tile + atom * rows * kRow + (in & 8);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
+    }
+    return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
+}
+
+// Sums of N values over a warp's lanes: value k's sum lands in v[0] of the
+// lanes whose top log2(N) bits are k.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
+    constexpr int kSteps = N == 16 ? 4 : 3;
+    static_assert(N == 16 || N == 8, "columns a thread");
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int off = 16 >> s, half = N >> (s + 1);
+        const bool up = lane & off;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+#pragma unroll
+    for (int off = 16 >> kSteps; off; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+}
+
 // Ring positions of the tiles' loads, in the order the products use them:
 // K0 K1 V0 K2 V1 ... V(n-1).
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
@@ -175,10 +256,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     using C = Cfg<D, RB>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
+    __shared__ uint64_t sc_full[kScales], fk_ready, fv_full;
+    __shared__ float2 sc_ring[kScales][8];
+    __shared__ int bad_page;
     __shared__ uint32_t tmem_ptr;
     __shared__ alignas(16) float col_m[RB], col_coef[RB], col_fac[RB];
     __shared__ float col_max[4][RB], v_max[C::kGroups][4];
-    __shared__ int col_lo[RB], col_row[RB];
+    __shared__ uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
     __shared__ float fresh_k[16];
     __shared__ float col_l[RB];
 
@@ -214,29 +298,47 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             gdn::mbar_init(&p_full[i], C::kSoft / 32);
             gdn::mbar_init(&pv_done[i], 1);
         }
+        for (int i = 0; i < kScales; ++i) gdn::mbar_init(&sc_full[i], 1);
         gdn::mbar_init(&q_ready, C::kSoft / 32);
+        gdn::mbar_init(&fk_ready, 1);
+        gdn::mbar_init(&fv_full, 1);
         gdn::mbar_init(&drain, 1);
+        bad_page = 0;
     }
     constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_ptr, C::kTmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    float *fresh_p = reinterpret_cast<float *>(s_fk);  // [RB][16], once the fresh keys' product is done
+    float *fresh_p = reinterpret_cast<float *>(s_fk);  // [16][RB], once the fresh keys' product is done
     static_assert(RB * 16 * 4 <= C::kFresh, "weights of the fresh rows");
     const uint32_t tm = tmem_ptr, tm_o = tm + 2 * C::kNs;
 
     if (warp == kCopyWarp) {
-        // ---- copies: page ids 32 at a time, the next 32 loaded ahead
+        // ---- copies.  Page ids and scales come 32 pages at a time, ids two and scales
+        // one such batch ahead.
+        if (fresh && rq.n > 0) {
+            if (lane == 0) gdn::mbar_arrive_expect_tx(&fv_full, uint32_t(rq.n) * (2 * D));
+            __syncwarp();
+            if (lane < rq.n)
+                gdn::bulk_g2s(s_fv + lane * 2 * D, a.v + (int64_t(rq.t0) + lane) * a.v_stride + int64_t(hk) * D, 2 * D,
+                              &fv_full);
+        }
         const int per = kTile >> shift;  // pages a tile
         const int page0 = tile0 * per, first = rq.lo >> shift, last = (rq.len + T - 1) >> shift;
         const int32_t *tab = a.table + int64_t(r) * a.table_stride;
-        auto ids = [&](int batch) {
+        const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
+        constexpr int kNone = -1;  // a page no row sees
+        auto wanted = [&](int batch) {
             const int j = page0 + batch * 32 + lane;
-            const int p = j >= first && j < last && batch * 32 + lane < nc * per ? tab[j] : -1;
-            return p >= 0 && p < a.c.num_pages ? p : -1;
+            return j >= first && j < last && batch * 32 + lane < nc * per;
         };
-        int cur = ids(0), nxt = ids(1), batch = 0;
+        auto ids = [&](int batch) { return wanted(batch) ? tab[page0 + batch * 32 + lane] : kNone; };
+        auto scales = [&](int p) {
+            return p >= 0 && p < a.c.num_pages
+                       ? *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride)
+                       : make_float2(0.f, 0.f);
+        };
         bool ok = true;
         int issued = 0;
         auto issue = [&](int pos, int page, int is_v) {
@@ -256,20 +358,40 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                                      x * C::kRow, (is_v * a.c.h_kv + hk) * T, page, &full[slot]);
             }
         };
-        int prev = -1;
+        int cur = ids(0), nxt = ids(1), far = ids(2), batch = 0, prev = -1;
+        float2 sc = scales(cur), sc_nxt = scales(nxt);
         for (int i = 0; i <= nc && ok; ++i) {
             int page = -1;
+            float2 s = make_float2(0.f, 0.f);
             if (i < nc) {
                 const int at = i * per;
                 if (at / 32 != batch) {
                     batch = at / 32;
                     cur = nxt;
-                    nxt = ids(batch + 1);
+                    sc = sc_nxt;
+                    nxt = far;
+                    sc_nxt = scales(nxt);
+                    far = ids(batch + 2);
                 }
-                page = __shfl_sync(0xffffffffu, cur, (at % 32) + (lane & (per - 1)));
+                // an id out of range is not loaded; the piece's outputs are dropped
+                const int src = (at % 32) + (lane & (per - 1));
+                page = __shfl_sync(0xffffffffu, cur, src);
+                const bool want = page0 + at + (lane & (per - 1)) >= first && page0 + at + (lane & (per - 1)) < last;
+                if (page < 0 || page >= a.c.num_pages) {
+                    if (want) *reinterpret_cast<volatile int *>(&bad_page) = 1;
+                    page = -1;
+                }
                 issue(k_pos(i), page, 0);
             }
             if (i > 0 && ok) issue(v_pos(i - 1, nc), prev, 1);
+            if (i < nc && ok) {
+                const int src = (i * per % 32) + (lane & (per - 1));
+                s.x = __shfl_sync(0xffffffffu, sc.x, src);
+                s.y = __shfl_sync(0xffffffffu, sc.y, src);
+                if (lane < per) sc_ring[i % kScales][lane] = s;
+                __syncwarp();
+                if (lane == 0) arrive(&sc_full[i % kScales]);
+            }
             prev = page;
         }
         if (!ok) {
@@ -278,6 +400,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
                 (void)gdn::mbar_wait_bounded(&full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
         }
+        if (fresh && rq.n > 0) (void)gdn::mbar_wait_bounded(&fv_full, 0, a.wait_ns);
     } else if (warp == kMmaWarp) {
         // ---- products: the warp runs the loop, one elected lane issues
         if (nt > 0) {
@@ -292,6 +415,18 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const uint64_t dv0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), lbo);
             const uint64_t dfk = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_fk), 16);
             const bool leader = elect_one();
+            if (fresh) {
+                for (int j0 = 0; j0 < rq.n; j0 += 4) {
+                    const int j = j0 + (lane >> 3);
+                    uint4 w[D / 64];
+                    load_row<D>(a.k + (int64_t(rq.t0) + j) * a.k_stride + int64_t(hk) * D, lane & 7, j < rq.n, w);
+                    const float down = split_row<D>(w, lane & 7, s_fk, 32, j, 16 + j);
+                    if ((lane & 7) == 0) fresh_k[j] = down;
+                }
+                gdn::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&fk_ready);
+            }
             bool ok = gdn::mbar_wait_bounded(&q_ready, 0, a.wait_ns);
             for (int i = 0; i <= nt && ok; ++i) {
                 if (i < nt) {
@@ -347,99 +482,21 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         __syncwarp();
     } else {
         // ---- softmax warps.  First the operands that come as bf16.
-        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
-        // page of this thread's position in tile i, if a row sees it; the id is looked
-        // at only where it is used, a tile later
-        auto wanted = [&](int i) {
-            const int t = (tile0 + i) * kTile + (tid & 127);
-            return i < nc && t >= rq.lo && t < rq.len;
-        };
-        auto page_of = [&](int i) { return wanted(i) ? tab[((tile0 + i) * kTile + (tid & 127)) >> shift] : -1; };
-        int page1 = page_of(0);
         {
-            const int sub = tid & 7;
-            constexpr int E = D / 8;  // elements a thread takes of a row
-            auto load = [&](const uint16_t *p, uint4 (&w)[E / 8], bool have) {
-#pragma unroll
-                for (int e = 0; e < E / 8; ++e)
-                    w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * E + e * 8) : make_uint4(0, 0, 0, 0);
-            };
-            // Splits a row x = (hi + lo/32) 2^-k into rows rh and rl of a tile of `rows`
-            // rows; -> 2^-k, or NaN for a row that is not finite.
-            auto split = [&](const uint4 (&raw4)[E / 8], uint8_t *tile, int rows, int rh, int rl) {
-                float m = 0.f, x[E];
-                bool finite = true;
-#pragma unroll
-                for (int e = 0; e < E / 8; ++e) {
-                    const uint32_t u[4] = {raw4[e].x, raw4[e].y, raw4[e].z, raw4[e].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
-                        x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const bool f = fabsf(x[e]) < INFINITY;
-                    finite &= f;
-                    x[e] = f ? x[e] : 0.f;
-                    m = fmaxf(m, fabsf(x[e]));
-                }
-                uint32_t w = __float_as_uint(m);
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
-                const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (lane & 24)) & 0xffu;
-                const int k = max(-110, min(110, 7 - (int(w >> 23) - 127)));  // largest in [128, 256)
-                const float up = kv8::pow2i(k), down = kv8::pow2i(-k);
-#pragma unroll
-                for (int b = 0; b < E / 8; ++b) {
-                    uint32_t h[2], l[2];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t hh[2], ll[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float x0 = x[b * 8 + g * 4 + 2 * i] * up, x1 = x[b * 8 + g * 4 + 2 * i + 1] * up;
-                            hh[i] = kv8::e4m3x2(x0, x1);
-                            const float2 back = kv8::f32x2_of(uint16_t(hh[i]));
-                            ll[i] = kv8::e4m3x2((x0 - back.x) * 32.f, (x1 - back.y) * 32.f);
-                        }
-                        h[g] = hh[0] | (hh[1] << 16);
-                        l[g] = ll[0] | (ll[1] << 16);
-                    }
-                    const int e0 = sub * E + b * 8, x0 = e0 / C::kRow, in = e0 % C::kRow;
-                    uint8_t *t = tile + x0 * rows * C::kRow + (in & 8);
-                    *reinterpret_cast<uint2 *>(t + tc::swz8_off<C::kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
-                    *reinterpret_cast<uint2 *>(t + tc::swz8_off<C::kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
-                }
-                return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
-            };
-            const float coef = a.c.sm_scale * 1.4426950408889634f;
-            // eight threads a row; q's columns fill whole warps, one pass takes them all
+            // eight threads a column; the columns fill whole warps, one pass takes them all
             static_assert(RB <= C::kSoft / 8, "a thread has one column");
-            const int c = tid >> 3, x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
-            uint4 wq[E / 8], wk[E / 8], wv[E / 8];
-            load(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, wq, c < cols);
-            const bool mine = fresh && c < rq.n;  // c: the row of k and v here
-            load(a.k + (int64_t(rq.t0) + c) * a.k_stride + int64_t(hk) * D, wk, mine);
-            load(a.v + (int64_t(rq.t0) + c) * a.v_stride + int64_t(hk) * D, wv, mine);
+            const int c = tid >> 3, sub = tid & 7;
             if (c < RB) {
-                const float down = split(wq, s_q, C::kNs, c, RB + c);
+                const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
+                uint4 w[D / 64];
+                load_row<D>(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, sub, c < cols, w);
+                const float down = split_row<D>(w, sub, s_q, C::kNs, c, RB + c);
                 if (sub == 0) {
                     col_m[c] = kUnset;
-                    col_coef[c] = coef * down;
-                    col_row[c] = row;
-                    // positions the row sees start here
-                    const int w = a.c.window;
-                    col_lo[c] = w ? max(0, rq.len + (a.k ? row + 1 : 0) - w) : 0;
+                    col_coef[c] = a.c.sm_scale * 1.4426950408889634f * down;
+                    col_row[c] = uint8_t(row);
+                    col_head[c] = uint8_t(x % a.group);
                 }
-            }
-            if (fresh && tid < 128) {
-                const float dk = split(wk, s_fk, 32, c, 16 + c);
-                if (sub == 0) fresh_k[c] = dk;
-#pragma unroll
-                for (int e = 0; e < E / 8; ++e)
-                    *reinterpret_cast<uint4 *>(s_fv + (c * D + sub * E + e * 8) * 2) = wv[e];
             }
             gdn::fence_proxy_async_smem();
             __syncwarp();
@@ -449,18 +506,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         // this thread's position in a tile and its columns col0 .. col0 + N - 1
         constexpr int N = C::kCols;
         const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N;
-        const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
-        bool bad = false, ok = true;
-        auto scales_of = [&](int p, int i) {
-            if (p < 0 || p >= a.c.num_pages) {
-                bad |= wanted(i);
-                return make_float2(0.f, 0.f);
-            }
-            return *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride);
-        };
-        // ids two tiles ahead, scales one
-        float2 sc_next = scales_of(page1, 0);
-        page1 = page_of(1);
+        // a row sees positions from lo0 + row * lo1 on (rq.lo is row 0's, and not negative)
+        const int lo0 = a.c.window ? rq.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
+        const int lo_last = lo0 + lo1 * col_row[cols - 1];
+        bool ok = true;
         float l[N], z[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) l[c] = 0.f;
@@ -470,12 +519,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         for (int i = 0; i < nt; ++i) {
             const bool is_fresh = i >= nc;
             const int t = (tile0 + i) * kTile + pos_in;
-            float2 sc = sc_next;
-            sc_next = scales_of(page1, i + 1);
-            page1 = page_of(i + 2);
-            if (is_fresh) sc = make_float2(pos_in < 32 && (pos_in & 15) < rq.n ? fresh_k[pos_in & 15] : 0.f, 0.f);
+            if (ok)
+                ok = is_fresh ? gdn::mbar_wait_bounded(&fk_ready, 0, a.wait_ns)
+                              : gdn::mbar_wait_bounded(&sc_full[i % kScales], (i / kScales) & 1, a.wait_ns);
+            const float2 sc = is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < rq.n ? fresh_k[pos_in & 15] : 0.f, 0.f)
+                                       : sc_ring[i % kScales][pos_in >> shift];
             // whole: every row sees every position of the tile
-            const bool whole = !is_fresh && (tile0 + i + 1) * kTile <= rq.len && (tile0 + i) * kTile >= col_lo[cols - 1];
+            const bool whole = !is_fresh && (tile0 + i + 1) * kTile <= rq.len && (tile0 + i) * kTile >= lo_last;
             if (ok) ok = gdn::mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, a.wait_ns);
             tc::fence_after();
 
@@ -522,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     }
                 } else if (!whole) {
 #pragma unroll
-                    for (int c = 0; c < N; ++c) z[c] = t < rq.len && t >= col_lo[col0 + c] ? z[c] : -INFINITY;
+                    for (int c = 0; c < N; ++c) z[c] = t < rq.len && t >= lo0 + lo1 * col_row[col0 + c] ? z[c] : -INFINITY;
                 }
             };
             load_z(false);
@@ -595,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     for (int c = 0; c < N; ++c) {
                         const float p = ex2(z[c]);
                         l[c] += p;
-                        fresh_p[(col0 + c) * 16 + pos_in] = p;
+                        fresh_p[pos_in * RB + col0 + c] = p;
                     }
                 }
                 break;  // the last tile
@@ -643,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 // their values but for NaN, which the epilogue gives to those rows.
                 const int pos = v_pos(i, nc), slot = pos % C::kSlots;
                 if (ok) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                const bool none = t < rq.lo || t >= rq.len, some = !none && t < col_lo[cols - 1];
+                const bool none = t < rq.lo || t >= rq.len, some = !none && t < lo_last;
                 if (ok && (none || some)) {
 #pragma unroll
                     for (int x = 0; x < C::kAtoms; ++x)
@@ -669,37 +719,33 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         }
         // ---- the piece's end
         if (ok && nc > 0) ok = gdn::mbar_wait_bounded(&pv_done[(nc - 1) & 1], ((nc - 1) >> 1) & 1, a.wait_ns);
+        if (ok && fresh && rq.n > 0) ok = gdn::mbar_wait_bounded(&fv_full, 0, a.wait_ns);
+        const bool bad = *reinterpret_cast<volatile int *>(&bad_page) != 0;  // set before the last tile's scales
         const bool skip = group_or(grp, !ok || bad);
         if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-        if (bad) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        if (bad && pos_in == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
         tc::fence_after();
-        // sums of the 128 positions' parts, through the weights' buffers
-        float *red = reinterpret_cast<float *>(s_p);
-        if (!skip) {
-#pragma unroll
-            for (int c = 0; c < N; ++c) red[(col0 + c) * 129 + pos_in] = l[c];
-        }
+        // sums over the 128 positions
+        warp_sums<N>(l, lane);
+        if ((lane & (32 / N - 1)) == 0) col_max[warp & 3][col0 + lane / (32 / N)] = l[0];
         group_sync(grp);
-        {
-            constexpr int per = 128 / N;  // threads a column
-            const int c = col0 + pos_in / per, s = pos_in % per;
-            float x = 0.f;
-            if (!skip)
-                for (int k = s; k < 128; k += per) x += red[c * 129 + k];
-#pragma unroll
-            for (int o = 1; o < per; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (s == 0) col_l[c] = x;
-        }
-        group_sync(grp);
-        const int col = col0 + pos_in;  // of the threads that finish one
         const bool direct = rq.pieces == 1;
         const int64_t unit = (int64_t(r) * a.max_pieces + piece) * gridDim.y + blockIdx.y;
-        if (!direct && pos_in < N) a.ws_ml[unit * RB + col] = make_float2(col_m[col], skip ? -1.f : col_l[col]);
-        if (direct && a.lse && pos_in < N && col < cols && !skip)
-            a.lse[(int64_t(rq.t0) + col_row[col]) * a.c.h_q + hk * a.group + (blk * RB + col) % a.group] =
-                col_l[col] == 0.f ? -INFINITY : (col_m[col] + log2f(col_l[col])) * 0.6931471805599453f;
+        if (pos_in < N) {
+            const int c = col0 + pos_in;
+            const float sum = (col_max[0][c] + col_max[1][c]) + (col_max[2][c] + col_max[3][c]);
+            if (!direct) {
+                a.ws_ml[unit * RB + c] = make_float2(col_m[c], skip ? -1.f : sum);
+            } else if (a.lse && c < cols && !skip) {
+                a.lse[(int64_t(rq.t0) + col_row[c]) * a.c.h_q + hk * a.group + col_head[c]] =
+                    sum == 0.f ? -INFINITY : (col_m[c] + log2f(sum)) * 0.6931471805599453f;
+            }
+            col_l[c] = sum == 0.f ? 0.f : 1.f / sum;
+        }
+        group_sync(grp);
         if (!skip) {
             const float back = vref / kBase;
+            const int edge = min(min(lo_last, rq.len), (tile0 + nc) * kTile);
 #pragma unroll 1
             for (int x = 0; x < C::kAtoms; ++x) {
                 const int e = x * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
@@ -729,38 +775,40 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         for (int c = 0; c < 8; ++c) o[c] = 0.f;
                     }
                     if (!mine) continue;
-                    if (fresh)
+                    if (fresh) {
+                        int row[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) row[c] = col_row[c0 + c];
+                        const int wdw = a.c.window ? a.c.window : GDN_MAX_ROWS;
                         for (int j = 0; j < rq.n; ++j) {
                             const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
+                            const float4 p0 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0),
+                                         p1 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0 + 4);
+                            const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const int row = col_row[c0 + c], win = a.c.window;
-                                if (j <= row && (!win || j > row - win)) o[c] = fmaf(fresh_p[(c0 + c) * 16 + j], v, o[c]);
-                            }
+                            for (int c = 0; c < 8; ++c)
+                                o[c] = uint32_t(row[c] - j) < uint32_t(wdw) ? fmaf(p[c], v, o[c]) : o[c];
                         }
+                    }
                     // NaN of positions that only some rows see
-                    const int edge = min(min(col_lo[cols - 1], rq.len), (tile0 + nc) * kTile);
                     for (int t = max(rq.lo, tile0 * kTile); t < edge; ++t) {
-                        const uint8_t code = a.c.kv[int64_t(tab[t >> shift]) * a.c.page_stride +
-                                                    int64_t(a.layer) * a.c.layer_stride +
+                        const int page = a.table[int64_t(r) * a.table_stride + (t >> shift)];
+                        const uint8_t code = a.c.kv[int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
                                                     (int64_t(a.c.h_kv + hk) * T + (t & (T - 1))) * D + e];
                         if ((code & 0x7f) == 0x7f) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                if (c0 + c < cols && t >= col_lo[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
+                                if (c0 + c < cols && t >= lo0 + lo1 * col_row[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
                         }
                     }
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         if (c0 + c >= cols) break;
-                        if (direct) {
-                            const float s = col_l[c0 + c];
+                        if (direct)
                             a.o[(int64_t(rq.t0) + col_row[c0 + c]) * a.o_stride +
-                                int64_t(hk * a.group + (blk * RB + c0 + c) % a.group) * D + e] =
-                                gdn::f32_to_bf16(s == 0.f ? 0.f : o[c] / s);
-                        } else {
+                                int64_t(hk * a.group + col_head[c0 + c]) * D + e] = gdn::f32_to_bf16(o[c] * col_l[c0 + c]);
+                        else
                             a.ws_o[(unit * RB + c0 + c) * D + e] = o[c];
-                        }
                     }
                 }
             }
@@ -774,75 +822,80 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     }
 }
 
-// Joins the pieces of one (row, query head): o = sum 2^(m_s - M) O_s / sum
-// 2^(m_s - M) l_s in piece order.  Groups of d/4 threads take every G-th
-// piece, so that the pieces' loads are in flight together.
+// Joins a request's pieces: o = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
+// Groups of d/4 threads; a CTA takes `per_cta` columns of a (request, kv head,
+// block).  With few pieces a group joins a column by itself; with many the
+// groups share one column's pieces, so that their loads are in flight together.
+// Which of the two, and so the order of the sums, goes by the pieces alone.
 constexpr int kJoin = 512;
 
 template <int D>
-__global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__ AttendArgs a, const int RB) {
+__global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__ AttendArgs a, const int RB,
+                                                         const int per_cta) {
     gdn::pdl_enter();
     constexpr int W = D / 4, G = kJoin / W;
-    const int i = blockIdx.x, h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
+    const int hk = blockIdx.y / a.blocks, blk = blockIdx.y % a.blocks, r = blockIdx.z, tid = threadIdx.x;
     const Request rq = request_of(a, r);
-    if (rq.bad || i >= rq.n || rq.pieces <= 1) return;
-    const int hk = h / a.group, x = i * a.group + h % a.group, blk = x / RB, c = x % RB;
-    const int gy = a.c.h_kv * a.blocks;
-    const int64_t unit0 = int64_t(r) * a.max_pieces * gy + hk * a.blocks + blk;
-    __shared__ float s_m[kJoin / 32], s_l[G];
+    if (rq.bad || rq.pieces <= 1) return;
+    const int begin = blockIdx.x * per_cta, end = min(min(RB, rq.n * a.group - blk * RB), begin + per_cta);
+    const int64_t unit0 = int64_t(r) * a.max_pieces * gridDim.y + blockIdx.y;
+    __shared__ float s_l[G];
     __shared__ float4 s_o[G][W];
-    float m = -INFINITY;
-    bool skip = false;
-    for (int s = tid; s < rq.pieces; s += kJoin) {
-        const float2 ml = a.ws_ml[(unit0 + int64_t(s) * gy) * RB + c];
-        m = fmaxf(m, ml.x);
-        skip |= ml.y < 0.f;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) s_m[tid >> 5] = m;
-    if (__syncthreads_or(skip)) return;
-#pragma unroll
-    for (int k = 0; k < kJoin / 32; ++k) m = fmaxf(m, s_m[k]);
     const int g = tid / W, e = tid % W;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int s = g; s < rq.pieces; s += G) {
-        const int64_t u = (unit0 + int64_t(s) * gy) * RB + c;
-        const float2 ml = a.ws_ml[u];
-        const float4 o = __ldcs(reinterpret_cast<const float4 *>(a.ws_o + u * D) + e);
-        const float f = ex2(ml.x - m);
-        if (ml.y != 0.f) {  // a piece of which the row sees nothing has no sums (and its outputs no meaning)
-            l = fmaf(f, ml.y, l);
-            acc.x = fmaf(f, o.x, acc.x);
-            acc.y = fmaf(f, o.y, acc.y);
-            acc.z = fmaf(f, o.z, acc.z);
-            acc.w = fmaf(f, o.w, acc.w);
+    const bool few = rq.pieces <= 8;
+    const int step = few ? G : 1, ps = few ? 1 : G, p0 = few ? 0 : g;
+    for (int c = begin + (few ? g : 0); c < end; c += step) {
+        const float2 *ml0 = a.ws_ml + unit0 * RB + c;
+        const int64_t ml_step = int64_t(gridDim.y) * RB;
+        float m = -INFINITY;
+        bool skip = false;
+#pragma unroll 8
+        for (int s = 0; s < rq.pieces; ++s) {
+            const float2 ml = ml0[s * ml_step];
+            m = fmaxf(m, ml.x);
+            skip |= ml.y < 0.f;
         }
+        if (skip) return;  // a piece was refused: so for every thread of the request
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 4
+        for (int s = p0; s < rq.pieces; s += ps) {
+            const float2 ml = ml0[s * ml_step];
+            const float4 o =
+                __ldcs(reinterpret_cast<const float4 *>(a.ws_o + ((unit0 + int64_t(s) * gridDim.y) * RB + c) * D) + e);
+            const float f = ex2(ml.x - m);
+            if (ml.y != 0.f) {  // else the row sees nothing of the piece
+                l = fmaf(f, ml.y, l);
+                acc.x = fmaf(f, o.x, acc.x);
+                acc.y = fmaf(f, o.y, acc.y);
+                acc.z = fmaf(f, o.z, acc.z);
+                acc.w = fmaf(f, o.w, acc.w);
+            }
+        }
+        if (!few) {
+            __syncthreads();  // the last column's sums are read
+            s_o[g][e] = acc;
+            if (e == 0) s_l[g] = l;
+            __syncthreads();
+            if (g > 0) continue;
+            for (int k = 1; k < G; ++k) {
+                const float4 o = s_o[k][e];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
+                l += s_l[k];
+            }
+        }
+        const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint2 w;
+        w.x = gdn::f32_to_bf16(acc.x * inv) | (uint32_t(gdn::f32_to_bf16(acc.y * inv)) << 16);
+        w.y = gdn::f32_to_bf16(acc.z * inv) | (uint32_t(gdn::f32_to_bf16(acc.w * inv)) << 16);
+        *reinterpret_cast<uint2 *>(a.o + (int64_t(rq.t0) + row) * a.o_stride + int64_t(h) * D + e * 4) = w;
+        if (e == 0 && a.lse)
+            a.lse[(int64_t(rq.t0) + row) * a.c.h_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    s_o[g][e] = acc;
-    if (e == 0) s_l[g] = l;
-    __syncthreads();
-    if (tid >= W) return;
-    acc = s_o[0][e];
-    l = s_l[0];
-#pragma unroll
-    for (int k = 1; k < G; ++k) {
-        const float4 o = s_o[k][e];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-        l += s_l[k];
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2 w;
-    w.x = gdn::f32_to_bf16(acc.x * inv) | (uint32_t(gdn::f32_to_bf16(acc.y * inv)) << 16);
-    w.y = gdn::f32_to_bf16(acc.z * inv) | (uint32_t(gdn::f32_to_bf16(acc.w * inv)) << 16);
-    *reinterpret_cast<uint2 *>(a.o + (int64_t(rq.t0) + i) * a.o_stride + int64_t(h) * D + e * 4) = w;
-    if (e == 0 && a.lse)
-        a.lse[(int64_t(rq.t0) + i) * a.c.h_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1005,8 +1058,11 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
         default: break;
     }
     if (rc != GDN_OK || p.max_pieces <= 1) return rc;
-    const dim3 jgrid{unsigned(max_rows), unsigned(cache->h_q), unsigned(B)};
-    if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, jgrid, dim3(kJoin), 0, st, a, p.rb);
-    if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, jgrid, dim3(kJoin), 0, st, a, p.rb);
-    return gdn_host::launch_pdl(kv8_join_kernel<256>, jgrid, dim3(kJoin), 0, st, a, p.rb);
+    // as many columns a CTA as still leave four CTAs for each SM
+    const int64_t columns = int64_t(B) * grid.y * p.rb;
+    const int per = int(columns / (4 * 152) < 1 ? 1 : columns / (4 * 152) > p.rb ? p.rb : columns / (4 * 152));
+    const dim3 jgrid{unsigned((p.rb + per - 1) / per), grid.y, unsigned(B)};
+    if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
+    if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
+    return gdn_host::launch_pdl(kv8_join_kernel<256>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
 }
