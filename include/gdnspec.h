@@ -558,7 +558,8 @@ int gdn_decode_transaction_at(const gdn_dims *dims, int32_t num_layers, int32_t 
  * codes [2 (K, V)][h_kv][page_tokens][d]; its scales (scale +
  * p*scale_page_stride + l*scale_layer_stride, floats) are fp32
  * [h_kv][2 (K, V)], each a power of two.  A stored element is code * scale.
- * Token t of request r lives in page table[r*table_stride + t/page_tokens].
+ * Token t of request r lives in page table[r*table_stride + t/page_tokens];
+ * a row of the table has table_pages entries (unused ones may hold anything).
  * Supported: d in {64, 128, 256}; page_tokens in {16, 32, 64, 128}; h_q a
  * multiple of h_kv, h_q/h_kv <= 64.  kv 16-byte aligned with strides
  * multiples of 16; scale 8-byte aligned with even strides.
@@ -602,7 +603,7 @@ size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t max
                                   int32_t split_tokens);
 int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
                const int32_t *cu_rows, const int32_t *cache_len,
-               const int32_t *table, int32_t table_stride,
+               const int32_t *table, int32_t table_pages, int64_t table_stride,
                const gdn_bf16 *q, int64_t q_stride,
                const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
                gdn_bf16 *o, int64_t o_stride, float *lse,
@@ -630,7 +631,7 @@ int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_cap
  */
 int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
                const int32_t *cu_rows, const int32_t *cache_len,
-               const int32_t *table, int32_t table_stride,
+               const int32_t *table, int32_t table_pages, int64_t table_stride,
                const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
                const int32_t *accept_len, int32_t max_rows, uint32_t *dev_status, void *stream);
 

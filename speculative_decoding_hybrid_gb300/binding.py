@@ -149,8 +149,9 @@ def _load():
         "gdn_verify_at_layers": [DP, I32, I32, I32, P, P, P, I64, P, P, I64, P, U32, P, I64, P, P],
         "gdn_verify_replay_layers": [DP, I32, I32, I32, P, P, I32, P, P, P, P, I64, I64, I32, P, P, P, I64, P, P],
         "kv8_attend_workspace_bytes": [CP, I32, I32, I32, I32],
-        "kv8_attend": [CP, I32, I32, I32, P, P, P, I32, P, I64, P, I64, P, I64, P, I64, P, I32, I32, I32, P, SZ, P, P],
-        "kv8_append": [CP, I32, I32, I32, P, P, P, I32, P, I64, P, I64, P, I32, P, P],
+        "kv8_attend": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, P, I64, P, I64, P, I32, I32, I32, P, SZ, P,
+                       P],
+        "kv8_append": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, P, I32, P, P],
         "kv8_copy_pages": [CP, I32, P, P, P, P],
         "kv8_pages_reserve": [PP, P, I32, P, I32, I32, I32, P, P, P],
         "kv8_pages_fork": [PP, P, I32, I32, I32, P, I32, P, P, P, P],
@@ -375,20 +376,20 @@ def kv8_attend_workspace_bytes(c: kv8_cache, B, max_len, max_rows, split_tokens=
     return int(lib.kv8_attend_workspace_bytes(ctypes.byref(c), B, max_len, max_rows, split_tokens))
 
 
-def kv8_attend(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_stride, q, q_stride, k_new,
-               k_stride, v_new, v_stride, o, o_stride, lse, max_len, max_rows, split_tokens, workspace,
+def kv8_attend(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, q,
+               q_stride, k_new, k_stride, v_new, v_stride, o, o_stride, lse, max_len, max_rows, split_tokens, workspace,
                workspace_bytes, dev_status, stream=None):
     return _check("kv8_attend", lib.kv8_attend(
-        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_stride, _ptr(q),
-        q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse), max_len, max_rows,
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
+        table_stride, _ptr(q), q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse), max_len, max_rows,
         split_tokens, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
 
 
-def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_stride, k_new, k_stride, v_new,
-               v_stride, accept_len, max_rows, dev_status, stream=None):
+def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, k_new,
+               k_stride, v_new, v_stride, accept_len, max_rows, dev_status, stream=None):
     return _check("kv8_append", lib.kv8_append(
-        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_stride,
-        _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(accept_len), max_rows, _ptr(dev_status), _stream(stream)))
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
+        table_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(accept_len), max_rows, _ptr(dev_status), _stream(stream)))
 
 
 def kv8_copy_pages(c: kv8_cache, n, src, dst, dev_status, stream=None):

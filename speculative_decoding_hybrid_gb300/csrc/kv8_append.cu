@@ -16,7 +16,8 @@ constexpr int kThreads = 256;
 
 struct AppendArgs {
     kv8_cache c;
-    int32_t layer, B, row_capacity, table_stride, max_rows;
+    int32_t layer, B, row_capacity, table_pages, max_rows;
+    int64_t table_stride;
     const int32_t *cu_rows, *cache_len, *table, *accept_len;
     const uint16_t *k, *v;
     int64_t k_stride, v_stride;
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a
     if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
     if (t0 < 0 || rows < 0 || rows > a.max_rows || int64_t(t0) + rows > a.row_capacity || len < 0 ||
-        int64_t(len) + rows > int64_t(a.table_stride) * T) {
+        int64_t(len) + rows > int64_t(a.table_pages) * T) {
         if (first_cta) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
         return;
     }
@@ -190,15 +191,16 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(const CopyArgs a) {
 
 extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
                           const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
-                          int32_t table_stride, const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new,
+                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new,
                           int64_t v_stride, const int32_t *accept_len, int32_t max_rows, uint32_t *dev_status,
                           void *stream) {
     const int bad = gdn_host::kv8_check(cache);
     if (bad != GDN_OK) return bad;
-    if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_stride < 0 ||
+    if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_pages < 0 ||
+        (B > 1 && table_stride < table_pages) ||
         max_rows < 0 || max_rows > gdn_host::kKv8MaxLen)
         return GDN_ERR_ARG;
-    if (int64_t(table_stride) * cache->page_tokens > gdn_host::kKv8MaxLen) return GDN_ERR_ARG;
+    if (int64_t(table_pages) * cache->page_tokens > gdn_host::kKv8MaxLen) return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0) return GDN_OK;
     if (!cu_rows || !cache_len || !table || !k_new || !v_new) return GDN_ERR_NULL;
     if (!gdn_host::kv8_rows_ok(k_new, k_stride, cache->h_kv, cache->d) ||
@@ -209,6 +211,7 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.layer = layer;
     a.B = B;
     a.row_capacity = row_capacity;
+    a.table_pages = table_pages;
     a.table_stride = table_stride;
     a.max_rows = max_rows;
     a.cu_rows = cu_rows;

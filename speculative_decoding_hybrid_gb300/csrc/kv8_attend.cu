@@ -45,8 +45,9 @@ constexpr int kScales = 8;      // tiles whose scales may wait to be read; the r
 struct AttendArgs {
     CUtensorMap map;
     kv8_cache c;
-    int32_t layer, B, row_capacity, table_stride, max_len, max_rows;
+    int32_t layer, B, row_capacity, table_pages, max_len, max_rows;
     int32_t group, blocks, piece_tiles, max_pieces, page_shift;  // page_tokens = 1 << page_shift
+    int64_t table_stride;
     const int32_t *cu_rows, *cache_len, *table;
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride, o_stride;
@@ -69,7 +70,7 @@ __device__ __forceinline__ Request request_of(const AttendArgs &a, int r) {
     q.n = a.cu_rows[r + 1] - q.t0;
     q.len = a.cache_len[r];
     q.bad = q.t0 < 0 || q.n < 0 || q.n > a.max_rows || int64_t(q.t0) + q.n > a.row_capacity || q.len < 0 ||
-            q.len > a.max_len || int64_t(q.len) > int64_t(a.table_stride) * a.c.page_tokens;
+            q.len > a.max_len || int64_t(q.len) > int64_t(a.table_pages) * a.c.page_tokens;
     const int w = a.c.window;
     q.lo = w ? max(0, q.len + (a.k ? 1 : 0) - w) : 0;
     if (q.lo > q.len) q.lo = q.len;
@@ -114,6 +115,53 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
+}
+
+// Pairs of fp32 values: one instruction an operation.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pair(uint32_t a, uint32_t b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// c - 32 h of two fp32 values c and two fp16 values h.
+__device__ __forceinline__ float2 minus32(float2 c, uint32_t h) {
+    float2 r;
+    asm("{\n .reg .b16 a, b, k;\n mov.b32 {a, b}, %2;\n mov.b16 k, 0xd000;\n fma.rn.f32.f16 %0, a, k, %3;\n"
+        " fma.rn.f32.f16 %1, b, k, %4;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(h), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) {
+    uint32_t r;
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
+    return r;
 }
 
 // fp16 pair arithmetic of the splits.
@@ -260,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     __shared__ float2 sc_ring[kScales][8];
     __shared__ int bad_page;
     __shared__ uint32_t tmem_ptr;
-    __shared__ alignas(16) float col_m[RB], col_coef[RB], col_fac[RB];
+    __shared__ alignas(16) float col_nm[RB], col_coef[RB], col_fac[RB];  // -m
     __shared__ float col_max[4][RB], v_max[C::kGroups][4];
     __shared__ uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
     __shared__ float fresh_k[16];
@@ -492,7 +540,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 load_row<D>(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, sub, c < cols, w);
                 const float down = split_row<D>(w, sub, s_q, C::kNs, c, RB + c);
                 if (sub == 0) {
-                    col_m[c] = kUnset;
+                    col_nm[c] = -kUnset;
                     col_coef[c] = a.c.sm_scale * 1.4426950408889634f * down;
                     col_row[c] = uint8_t(row);
                     col_head[c] = uint8_t(x % a.group);
@@ -510,9 +558,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         const int lo0 = a.c.window ? rq.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
         const int lo_last = lo0 + lo1 * col_row[cols - 1];
         bool ok = true;
-        float l[N], z[N];
+        f2 l[N / 2];
+        float z[N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) l[c] = 0.f;
+        for (int c = 0; c < N / 2; ++c) l[c] = 0;
         float vref = kv8::pow2i(kv8::kMinScaleExp), vinv = kBase / vref;
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
 
@@ -543,24 +592,32 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 tc::ld_wait();
                 tc::ld_fence_regs(hi);
                 tc::ld_fence_regs(lo);
+                f2 s[N / 2];
 #pragma unroll
-                for (int c = 0; c < N; ++c) z[c] = fmaf(__uint_as_float(lo[c]), 1.f / 32.f, __uint_as_float(hi[c]));
+                for (int c = 0; c < N / 2; ++c)
+                    s[c] = fma2(pair(lo[2 * c], lo[2 * c + 1]), pair(1.f / 32.f, 1.f / 32.f),
+                                pair(hi[2 * c], hi[2 * c + 1]));
                 if (is_fresh) {  // the other part of the position
 #pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        const float other = __shfl_xor_sync(0xffffffffu, z[c], 16);
-                        z[c] = pos_in & 16 ? fmaf(z[c], 1.f / 32.f, other) : fmaf(other, 1.f / 32.f, z[c]);
+                    for (int c = 0; c < N / 2; ++c) {
+                        const float2 x = both(s[c]);
+                        const f2 other = pair(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16));
+                        s[c] = pos_in & 16 ? fma2(s[c], pair(1.f / 32.f, 1.f / 32.f), other)
+                                           : fma2(other, pair(1.f / 32.f, 1.f / 32.f), s[c]);
                     }
                 }
+                const f2 sx = pair(sc.x, sc.x);
 #pragma unroll
                 for (int c = 0; c < N; c += 4) {
-                    const float4 k = *reinterpret_cast<const float4 *>(col_coef + col0 + c);
-                    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (!plain) m = *reinterpret_cast<const float4 *>(col_m + col0 + c);
-                    z[c] = fmaf(z[c], sc.x * k.x, -m.x);
-                    z[c + 1] = fmaf(z[c + 1], sc.x * k.y, -m.y);
-                    z[c + 2] = fmaf(z[c + 2], sc.x * k.z, -m.z);
-                    z[c + 3] = fmaf(z[c + 3], sc.x * k.w, -m.w);
+                    const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(col_coef + col0 + c);
+                    ulonglong2 nm = make_ulonglong2(0, 0);
+                    if (!plain) nm = *reinterpret_cast<const ulonglong2 *>(col_nm + col0 + c);
+                    const float2 x = both(fma2(s[c / 2], mul2(sx, k.x), nm.x)),
+                                 y = both(fma2(s[c / 2 + 1], mul2(sx, k.y), nm.y));
+                    z[c] = x.x;
+                    z[c + 1] = x.y;
+                    z[c + 2] = y.x;
+                    z[c + 3] = y.y;
                 }
                 if (is_fresh) {
                     const int j = pos_in & 15, w = a.c.window;
@@ -596,11 +653,11 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 group_sync(grp);
                 if (pos_in < N) {
                     const int c = col0 + pos_in;
-                    const float was = col_m[c];
+                    const float was = -col_nm[c];
                     const float now =
                         fmaxf(fmaxf(fmaxf(col_max[0][c], col_max[1][c]), fmaxf(col_max[2][c], col_max[3][c])), was);
                     col_fac[c] = ex2(was - now);
-                    col_m[c] = now;
+                    col_nm[c] = -now;
                 }
                 const float vnow = fmaxf(fmaxf(fmaxf(v_max[grp][0], v_max[grp][1]), fmaxf(v_max[grp][2], v_max[grp][3])), vref);
                 const float vfac = vref / vnow;
@@ -608,9 +665,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 vinv = kBase / vnow;
                 group_sync(grp);
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    l[c] *= col_fac[col0 + c];
-                    z[c] -= col_m[col0 + c];
+                for (int c = 0; c < N; c += 2) {
+                    l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(col_fac + col0 + c));
+                    z[c] += col_nm[col0 + c];
+                    z[c + 1] += col_nm[col0 + c + 1];
                 }
                 if (i > 0) {
                     ok = gdn::mbar_wait_bounded(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, a.wait_ns);
@@ -642,39 +700,35 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             if (is_fresh) {
                 if (pos_in < 16) {
 #pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        const float p = ex2(z[c]);
-                        l[c] += p;
-                        fresh_p[pos_in * RB + col0 + c] = p;
+                    for (int c = 0; c < N; c += 2) {
+                        const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
+                        l[c / 2] = add2(l[c / 2], p);
+                        *reinterpret_cast<f2 *>(fresh_p + pos_in * RB + col0 + c) = p;
                     }
                 }
                 break;  // the last tile
             }
             const float xw = sc.y * vinv;
+            const f2 xw2 = pair(xw, xw), xw32 = pair(32.f * xw, 32.f * xw);
             if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&pv_done[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
             uint8_t *pb = s_p + (i & 1) * C::kP;
             // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
             constexpr int W = N < 16 ? 8 : 16;
 #pragma unroll
             for (int c0 = 0; c0 < N; c0 += W) {
-                uint32_t part[4][W / 4];
+                uint16_t e[4][W / 2];
 #pragma unroll
-                for (int c = 0; c < W; c += 2) {
-                    const float p0 = ex2(z[c0 + c]), p1 = ex2(z[c0 + c + 1]);
-                    l[c0 + c] += p0;
-                    l[c0 + c + 1] += p1;
-                    const float x0 = p0 * xw, x1 = p1 * xw;
-                    uint16_t e[4];
-                    e[0] = uint16_t(kv8::e4m3x2(x0, x1));
-                    const float2 b0 = kv8::f32x2_of(e[0]);
-                    uint32_t rest = f16x2((x0 - b0.x) * 32.f, (x1 - b0.y) * 32.f);
-                    e[1] = e4m3x2_of(rest);
-                    rest = rest32(rest, kv8::f16x2_of(e[1]));
-                    e[2] = e4m3x2_of(rest);
-                    e[3] = e4m3x2_of(rest32(rest, kv8::f16x2_of(e[2])));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        part[k][c / 4] = c % 4 ? part[k][c / 4] | (uint32_t(e[k]) << 16) : uint32_t(e[k]);
+                for (int c = 0; c < W / 2; ++c) {
+                    const f2 p = pair(ex2(z[c0 + 2 * c]), ex2(z[c0 + 2 * c + 1]));
+                    l[c0 / 2 + c] = add2(l[c0 / 2 + c], p);
+                    const float2 x = both(mul2(p, xw2));
+                    e[0][c] = uint16_t(kv8::e4m3x2(x.x, x.y));
+                    const float2 r = minus32(both(mul2(p, xw32)), kv8::f16x2_of(e[0][c]));  // exact
+                    uint32_t rest = f16x2(r.x, r.y);
+                    e[1][c] = e4m3x2_of(rest);
+                    rest = rest32(rest, kv8::f16x2_of(e[1][c]));
+                    e[2][c] = e4m3x2_of(rest);
+                    e[3][c] = e4m3x2_of(rest32(rest, kv8::f16x2_of(e[2][c])));
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -682,9 +736,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
                                    tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
                     if constexpr (W == 16)
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(join16(e[k][0], e[k][1]), join16(e[k][2], e[k][3]),
+                                                                     join16(e[k][4], e[k][5]), join16(e[k][6], e[k][7]));
                     else
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(part[k][0], part[k][1]);
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(join16(e[k][0], e[k][1]), join16(e[k][2], e[k][3]));
                 }
             }
             if (!whole && grp == 0) {
@@ -726,8 +781,14 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         if (bad && pos_in == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
         tc::fence_after();
         // sums over the 128 positions
-        warp_sums<N>(l, lane);
-        if ((lane & (32 / N - 1)) == 0) col_max[warp & 3][col0 + lane / (32 / N)] = l[0];
+        float sums[N];
+#pragma unroll
+        for (int c = 0; c < N / 2; ++c) {
+            sums[2 * c] = both(l[c]).x;
+            sums[2 * c + 1] = both(l[c]).y;
+        }
+        warp_sums<N>(sums, lane);
+        if ((lane & (32 / N - 1)) == 0) col_max[warp & 3][col0 + lane / (32 / N)] = sums[0];
         group_sync(grp);
         const bool direct = rq.pieces == 1;
         const int64_t unit = (int64_t(r) * a.max_pieces + piece) * gridDim.y + blockIdx.y;
@@ -735,10 +796,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int c = col0 + pos_in;
             const float sum = (col_max[0][c] + col_max[1][c]) + (col_max[2][c] + col_max[3][c]);
             if (!direct) {
-                a.ws_ml[unit * RB + c] = make_float2(col_m[c], skip ? -1.f : sum);
+                a.ws_ml[unit * RB + c] = make_float2(-col_nm[c], skip ? -1.f : sum);
             } else if (a.lse && c < cols && !skip) {
                 a.lse[(int64_t(rq.t0) + col_row[c]) * a.c.h_q + hk * a.group + col_head[c]] =
-                    sum == 0.f ? -INFINITY : (col_m[c] + log2f(sum)) * 0.6931471805599453f;
+                    sum == 0.f ? -INFINITY : (log2f(sum) - col_nm[c]) * 0.6931471805599453f;
             }
             col_l[c] = sum == 0.f ? 0.f : 1.f / sum;
         }
@@ -985,17 +1046,18 @@ extern "C" size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, 
 
 extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
                           const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
-                          int32_t table_stride, const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k_new,
+                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k_new,
                           int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride, gdn_bf16 *o, int64_t o_stride,
                           float *lse, int32_t max_len, int32_t max_rows, int32_t split_tokens, void *workspace,
                           size_t workspace_bytes, uint32_t *dev_status, void *stream) {
     const int bad = gdn_host::kv8_check(cache);
     if (bad != GDN_OK) return bad;
-    if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_stride < 0 ||
+    if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_pages < 0 ||
+        table_stride < 0 ||
         max_len < 0 || max_len > gdn_host::kKv8MaxLen || max_rows < 0 || max_rows > GDN_MAX_ROWS || split_tokens < 0)
         return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0) return GDN_OK;
-    if (!cu_rows || !cache_len || (!table && table_stride > 0) || !q || !o || !k_new != !v_new) return GDN_ERR_NULL;
+    if (!cu_rows || !cache_len || (!table && table_pages > 0) || !q || !o || !k_new != !v_new) return GDN_ERR_NULL;
     if (!gdn_host::kv8_rows_ok(q, q_stride, cache->h_q, cache->d) ||
         !gdn_host::kv8_rows_ok(o, o_stride, cache->h_q, cache->d))
         return GDN_ERR_ARG;
@@ -1013,6 +1075,7 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.layer = layer;
     a.B = B;
     a.row_capacity = row_capacity;
+    a.table_pages = table_pages;
     a.table_stride = table_stride;
     a.max_len = max_len;
     a.max_rows = max_rows;

@@ -26,13 +26,13 @@ PAGE_TOKENS = (16, 32, 64, 128)
 HEAD_SIZES = (64, 128, 256)
 
 
-def _on(stream):
-    """(context in which to allocate, raw handle) of a stream argument."""
-    if stream is None:
-        return nullcontext(), torch.cuda.current_stream().cuda_stream
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream), stream.cuda_stream
+# The current stream's handle without building a Stream object (a few microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _stream_object(stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
 
 
 class Kv8Cache:
@@ -62,25 +62,34 @@ class Kv8Cache:
                               1.0 / math.sqrt(d) if sm_scale is None else sm_scale, kv.data_ptr(), kv.stride(0),
                               kv.stride(1), scale.data_ptr(), scale.stride(0), scale.stride(1))
         self._c = ctypes.byref(self.c)
-        self._q, self._kv = ((h_q, d), (d, 1)), ((h_kv, d), (d, 1))
+        self._device = kv.device
+        self._index = kv.get_device()
+        self._status = status.data_ptr()
+        self._workspace = {}  # (B, max_len, max_rows, split_tokens) -> bytes
 
-    @staticmethod
-    def _rows(x: torch.Tensor, want, name: str):
-        if x.dtype != torch.bfloat16 or x.shape[1:] != want[0] or x.stride()[1:] != want[1]:
-            raise ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads" % (name, *want[0]))
-        return x.data_ptr(), x.stride(0)
+    def _rows(self, x: torch.Tensor, heads: int, name: str):
+        """-> (address, row stride) of packed rows of heads."""
+        shape, stride = x.shape, x.stride()
+        if (x.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != self.d
+                or stride[1] != self.d or stride[2] != 1 or x.get_device() != self._index):
+            raise ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads, on the cache's device"
+                             % (name, heads, self.d))
+        return x.data_ptr(), stride[0]
 
-    @staticmethod
-    def _tables(table, cache_len, cu_rows):
-        if table.dim() != 2 or table.stride(1) != 1:
-            raise ValueError("table must be int32 [requests, pages] with contiguous rows")
-        if not (table.dtype == cache_len.dtype == cu_rows.dtype == torch.int32):
-            raise ValueError("table, cache_len and cu_rows must be int32")
-        B = cache_len.shape[0]
-        if table.shape[0] < B or cu_rows.shape[0] < B + 1 or not (cache_len.is_contiguous()
-                                                                  and cu_rows.is_contiguous()):
-            raise ValueError("cache_len [B], cu_rows [B + 1] and table [B, pages] do not fit together")
-        return B
+    def _ints(self, x: torch.Tensor, n: int, name: str):
+        """-> address of a contiguous int32 list of at least n."""
+        if (x.dtype is not torch.int32 or x.dim() != 1 or x.numel() < n or not x.is_contiguous()
+                or x.get_device() != self._index):
+            raise ValueError("%s must be a contiguous int32 list of at least %d, on the cache's device" % (name, n))
+        return x.data_ptr()
+
+    def _table(self, table: torch.Tensor, B: int):
+        """-> (address, entries a row, row stride) of the page table."""
+        shape, stride = table.shape, table.stride()
+        if (table.dtype is not torch.int32 or len(shape) != 2 or shape[0] < B or (stride[1] != 1 and shape[1] > 1)
+                or table.get_device() != self._index):
+            raise ValueError("table must be int32 [requests, pages] with contiguous rows, on the cache's device")
+        return table.data_ptr(), shape[1], stride[0]
 
     def attend(self, layer: int, table: torch.Tensor, cache_len: torch.Tensor, cu_rows: torch.Tensor,
                q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor], max_len: int,
@@ -90,29 +99,44 @@ class Kv8Cache:
         """-> (o bf16 [rows, h_q, d], lse fp32 [rows, h_q] or None); ``kv8_attend`` in the header.
 
         max_len and max_rows are host bounds on cache_len and on a request's rows."""
-        B = self._tables(table, cache_len, cu_rows)
-        qp, qs = self._rows(q, self._q, "q")
-        kp = ks = vp = vs = 0
-        R = q.shape[0]
-        if k_new is not None:
-            kp, ks = self._rows(k_new, self._kv, "k_new")
-            vp, vs = self._rows(v_new, self._kv, "v_new")
-            if k_new.shape[0] < R or v_new.shape[0] < R:
-                raise ValueError("k_new and v_new need a row for each of q's")
-        ctx, raw = _on(stream)
-        need = gs.lib.kv8_attend_workspace_bytes(self._c, B, max_len, max_rows, split_tokens)
-        with ctx:
+        B, R = cache_len.shape[0], q.shape[0]
+        len_p, cu_p = self._ints(cache_len, B, "cache_len"), self._ints(cu_rows, B + 1, "cu_rows")
+        table_p, table_n, table_s = self._table(table, B)
+        q_p, q_s = self._rows(q, self.h_q, "q")
+        k_p = k_s = v_p = v_s = 0
+        if k_new is not None or v_new is not None:
+            if k_new is None or v_new is None or k_new.shape[0] < R or v_new.shape[0] < R:
+                raise ValueError("k_new and v_new come together and need a row for each of q's")
+            k_p, k_s = self._rows(k_new, self.h_kv, "k_new")
+            v_p, v_s = self._rows(v_new, self.h_kv, "v_new")
+        key = (B, max_len, max_rows, split_tokens)
+        need = self._workspace.get(key)
+        if need is None:
+            if len(self._workspace) > 4096:
+                self._workspace.clear()
+            need = self._workspace[key] = gs.lib.kv8_attend_workspace_bytes(self._c, *key)
+        if stream is not None:
+            # what the call allocates belongs to the stream it runs on
+            stream = _stream_object(stream)
+            before = torch.cuda.current_stream(self._device)
+            torch.cuda.set_stream(stream)
+        try:
+            raw = _raw_stream(self._index)
             if out is None:
-                out = torch.empty((R, self.h_q, self.d), dtype=torch.bfloat16, device=q.device)
-            lse = torch.empty((R, self.h_q), dtype=torch.float32, device=q.device) if want_lse else None
-            ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
-        op, os_ = self._rows(out, self._q, "out")
-        if out.shape[0] < R:
-            raise ValueError("out needs a row for each of q's")
-        st = gs.lib.kv8_attend(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(),
-                               table.shape[1] if B == 1 else table.stride(0), qp, qs, kp or None, ks, vp or None, vs,
-                               op, os_, lse.data_ptr() if want_lse else None, max_len, max_rows, split_tokens,
-                               ws.data_ptr() if need else None, need, self.status.data_ptr(), raw)
+                out = torch.empty((R, self.h_q, self.d), dtype=torch.bfloat16, device=self._device)
+                o_p, o_s = out.data_ptr(), self.h_q * self.d
+            elif out.shape[0] < R:
+                raise ValueError("out needs a row for each of q's")
+            else:
+                o_p, o_s = self._rows(out, self.h_q, "out")
+            lse = torch.empty((R, self.h_q), dtype=torch.float32, device=self._device) if want_lse else None
+            ws = torch.empty((need,), dtype=torch.uint8, device=self._device) if need else None
+        finally:
+            if stream is not None:
+                torch.cuda.set_stream(before)
+        st = gs.lib.kv8_attend(self._c, layer, B, R, cu_p, len_p, table_p, table_n, table_s, q_p, q_s, k_p or None, k_s,
+                               v_p or None, v_s, o_p, o_s, lse.data_ptr() if want_lse else None, max_len, max_rows,
+                               split_tokens, ws.data_ptr() if need else None, need, self._status, raw)
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_attend", st)
         return out, lse
@@ -122,28 +146,25 @@ class Kv8Cache:
                max_rows: int = gs.MAX_ROWS, stream=None):
         """Commits the first accept_len[r] + 1 rows of each request (all rows without accept_len);
         ``kv8_append`` in the header."""
-        B = self._tables(table, cache_len, cu_rows)
-        kp, ks = self._rows(k_new, self._kv, "k_new")
-        vp, vs = self._rows(v_new, self._kv, "v_new")
-        if accept_len is not None and (accept_len.dtype != torch.int32 or accept_len.shape[0] < B
-                                       or not accept_len.is_contiguous()):
-            raise ValueError("accept_len must be int32 [requests]")
-        raw = torch.cuda.current_stream().cuda_stream if stream is None else gs._stream(stream)
-        st = gs.lib.kv8_append(self._c, layer, B, min(k_new.shape[0], v_new.shape[0]), cu_rows.data_ptr(),
-                               cache_len.data_ptr(), table.data_ptr(),
-                               table.shape[1] if B == 1 else table.stride(0), kp, ks, vp, vs,
-                               None if accept_len is None else accept_len.data_ptr(), max_rows,
-                               self.status.data_ptr(), raw)
+        B = cache_len.shape[0]
+        len_p, cu_p = self._ints(cache_len, B, "cache_len"), self._ints(cu_rows, B + 1, "cu_rows")
+        table_p, table_n, table_s = self._table(table, B)
+        k_p, k_s = self._rows(k_new, self.h_kv, "k_new")
+        v_p, v_s = self._rows(v_new, self.h_kv, "v_new")
+        acc_p = None if accept_len is None else self._ints(accept_len, B, "accept_len")
+        st = gs.lib.kv8_append(self._c, layer, B, min(k_new.shape[0], v_new.shape[0]), cu_p, len_p, table_p, table_s,
+                               k_p, k_s, v_p, v_s, acc_p, max_rows, self._status,
+                               _raw_stream(self._index) if stream is None else gs._stream(stream))
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_append", st)
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Page dst[i] <- page src[i], every layer; ``kv8_copy_pages`` in the header."""
-        if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.shape != dst.shape or src.dim() != 1 \
-                or not (src.is_contiguous() and dst.is_contiguous()):
-            raise ValueError("src and dst must be int32 lists of one length")
-        raw = torch.cuda.current_stream().cuda_stream if stream is None else gs._stream(stream)
-        st = gs.lib.kv8_copy_pages(self._c, src.shape[0], src.data_ptr(), dst.data_ptr(), self.status.data_ptr(), raw)
+        n = src.shape[0]
+        if dst.shape != src.shape:
+            raise ValueError("src and dst must be lists of one length")
+        st = gs.lib.kv8_copy_pages(self._c, n, self._ints(src, n, "src"), self._ints(dst, n, "dst"), self._status,
+                                   _raw_stream(self._index) if stream is None else gs._stream(stream))
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_copy_pages", st)
 
@@ -244,7 +265,6 @@ class PagedKv(Kv8Cache):
     def _copy(self, pairs, stream):
         if not pairs:
             return
-        ctx, _ = _on(stream)
-        with ctx:
+        with nullcontext() if stream is None else torch.cuda.stream(_stream_object(stream)):
             ids = torch.tensor(pairs, dtype=torch.int32).t().contiguous().to(self.kv.device)
             self.copy_pages(ids[0], ids[1])

@@ -373,7 +373,7 @@ def test_host_refusals(cuda_dev):
     big = ctypes.byref(c.c)
     need = gs.lib.kv8_attend_workspace_bytes(big, 1, 100000, 2, 128)
     assert need > 0
-    st = gs.lib.kv8_attend(big, 0, 1, 2, cu.data_ptr(), length.data_ptr(), table.data_ptr(), 4, qt.data_ptr(),
+    st = gs.lib.kv8_attend(big, 0, 1, 2, cu.data_ptr(), length.data_ptr(), table.data_ptr(), 4, 4, qt.data_ptr(),
                            qt.stride(0), kt.data_ptr(), kt.stride(0), vt.data_ptr(), vt.stride(0), o.data_ptr(), 512,
                            None, 100000, 2, 128, None, 0, c.status.data_ptr(), None)
     assert st == gs.GDN_ERR_WORKSPACE
