@@ -10,29 +10,36 @@
 //   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 32^-j
 // A part is its predecessor's remainder times 32, so three carry 14 bits of a
 // weight; the fourth keeps that precision for weights 2^-12 times smaller.
-// A position is a tensor-memory lane, so its page's scales are one register
-// of the thread that owns the lane: K's multiplies the score, V's the weight.
+// A position is a tensor-memory lane, so its page's scales are two numbers of
+// the thread that owns the lane: K's multiplies the score, V's the weight.
 //
 // The softmax keeps a reference m per column, not the running maximum: a
 // column's weights are 2^(z - m), and only when some z passes m + kSlack (or a
 // page's V scale the reference one) is m moved and the sums rescaled; usually
-// that is once, at a piece's first tile.  One vote a tile decides.
+// that is once, at a segment's first tile.  One vote a tile decides.
 //
-// One CTA per (piece of a request's positions, kv head and block of RB
-// columns, request): groups of four softmax warps (thread = position = lane,
-// a group's share of the columns each), one warp that copies pages (tiled TMA,
-// 128- or 64-byte swizzle, K and V tiles through one ring), one that issues
-// the products.  The transaction's own rows, bf16, come
-// last: their keys as one more tile, each a hi and a lo position (16 + 16
-// lanes) split like q, their values in fp32 in the epilogue.
-// Pieces leave (m, l, O) in the workspace for kv8_join_kernel; a request with
-// one piece is written directly.
+// Work is measured in tiles of 128 positions: a unit (request, kv head, block of
+// RB columns) costs its tiles plus one, and the units laid end to end are cut
+// into equal ranges, one for each of the persistent CTAs.  A CTA runs the units
+// and parts of units of its range as segments.  Its warps:
+//   copy     finds the segments, queues them, and moves pages (tiled TMA, K and V
+//            tiles through one ring) and their scales, into the next segment while
+//            the last one is still being summed
+//   product  issues the tensor-core products, and splits the segment's new keys
+//   softmax  groups of four warps (thread = position = lane), a share of the
+//            columns each: queries in, weights, outputs out
+// The transaction's own rows, bf16, come last in a unit: their keys as one more
+// tile, each a hi and a lo position (16 + 16 lanes) split like q, their values in
+// fp32 in the epilogue.  A unit inside one range is written directly; the parts
+// of a cut one leave (m, l, O) in the workspace for kv8_join_kernel.  With a
+// given split the cuts are at its multiples instead, whatever the ranges.
 #include <cuda.h>
 
-#include "kv8.cuh"
-#include "tc.cuh"
+#include "kv8_math.cuh"
 
 namespace {
+
+using namespace kv8;
 
 constexpr int kTile = 128;      // positions a tile
 // Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
@@ -40,28 +47,38 @@ constexpr int kTile = 128;      // positions a tile
 // reference less often and costs that many bits at the low end.
 constexpr float kBase = 4.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
-constexpr int kScales = 8;      // tiles whose scales may wait to be read; the ring of 10 slots holds back the copies before that
+constexpr int kQueue = 4;       // segments queued
+constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
+constexpr int kWhole = 8;       // units of so few tiles are not cut
+
+// A part of a unit cut by the ranges: which unit, and the CTAs owner .. owner +
+// count - 1 that have its parts (count 0: none).
+struct Part {
+    int r, y, owner, count;
+};
 
 struct AttendArgs {
     CUtensorMap map;
     kv8_cache c;
     int32_t layer, B, row_capacity, table_pages, max_len, max_rows;
-    int32_t group, blocks, piece_tiles, max_pieces, page_shift;  // page_tokens = 1 << page_shift
+    int32_t group, blocks, page_shift;  // page_tokens = 1 << page_shift
+    int32_t pinned, piece_tiles, max_pieces;
     int64_t table_stride;
     const int32_t *cu_rows, *cache_len, *table;
     const uint16_t *q, *k, *v;
     int64_t q_stride, k_stride, v_stride, o_stride;
     uint16_t *o;
     float *lse;
-    float *ws_o;       // [unit][RB][d]
-    float2 *ws_ml;     // [unit][RB]
+    float *ws_o;       // [part][RB][d]
+    float2 *ws_ml;     // [part][RB]
+    Part *parts;       // [CTA][2]: of a unit begun before the range, of one that goes on after it
     uint32_t *status;
     uint64_t wait_ns;
 };
 
 // What a request asks for; the same test in both kernels.
 struct Request {
-    int t0, n, len, lo, tiles, pieces;  // lo: first position any row sees; tiles from lo / 128 on
+    int t0, n, len, lo, tiles;  // lo: first position any row sees; tiles from lo / 128 on
     bool bad;
 };
 __device__ __forceinline__ Request request_of(const AttendArgs &a, int r) {
@@ -76,112 +93,21 @@ __device__ __forceinline__ Request request_of(const AttendArgs &a, int r) {
     if (q.lo > q.len) q.lo = q.len;
     const int first = q.lo / kTile;
     q.tiles = q.lo < q.len ? (q.len + kTile - 1) / kTile - first : 0;
-    q.pieces = max(1, (q.tiles + a.piece_tiles - 1) / a.piece_tiles);
     return q;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Barrier of a group's four softmax warps with an OR over a predicate.
-__device__ __forceinline__ bool group_or(int group, bool p) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, "
-        "q;\n}\n"
-        : "=r"(r)
-        : "r"(uint32_t(p)), "r"(group + 1)
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void group_sync(int group) {
-    asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
-}
-template <int THREADS>
-__device__ __forceinline__ void soft_sync() {
-    asm volatile("barrier.cta.sync 5, %0;" ::"n"(THREADS) : "memory");
-}
-__device__ __forceinline__ void arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
+// The pieces of one unit in the workspace, in order.
+struct Pieces {
+    int count;
+    int64_t first, base, step;
+    __device__ __forceinline__ int64_t at(int s) const { return s == 0 ? first : base + s * step; }
+};
 
-// Pairs of fp32 values: one instruction an operation.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pair(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f2 pair(uint32_t a, uint32_t b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ float2 both(f2 x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// c - 32 h of two fp32 values c and two fp16 values h.
-__device__ __forceinline__ float2 minus32(float2 c, uint32_t h) {
-    float2 r;
-    asm("{\n .reg .b16 a, b, k;\n mov.b32 {a, b}, %2;\n mov.b16 k, 0xd000;\n fma.rn.f32.f16 %0, a, k, %3;\n"
-        " fma.rn.f32.f16 %1, b, k, %4;\n}\n"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(h), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) {
-    uint32_t r;
-    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
-    return r;
-}
-
-// fp16 pair arithmetic of the splits.
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint16_t e4m3x2_of(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
-// (h - back) * 32 of two fp16 values: exact, `back` being h to 4 bits.
-__device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t back) {
-    uint32_t t, r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(h), "r"(0x50005000u));              // 32, 32
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(back), "r"(0xd000d000u), "r"(t));  // -32, -32
-    return r;
-}
+struct Segment {
+    int r, t0, len, lo, tile0, nc, out;  // cached tiles tile0 .. + nc; out: part of the workspace, -1: direct
+    uint16_t hk, blk;
+    uint8_t n, cols, fresh;              // cols 0: no more segments
+};
 
 template <int D, int RB>
 struct Cfg {
@@ -204,284 +130,376 @@ struct Cfg {
     // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule it out
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
     static constexpr int kFixed = 2 * kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024;
-    static constexpr int kStatic = RB == 64 ? 4096 : 2048;  // at least what __shared__ takes below
+    static constexpr int kStatic = RB == 64 ? 4096 : D == 64 ? 2560 : 2048;  // bound on sizeof(Shared)
     static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kStatic - kFixed;
     static constexpr int kSlots = kRoom / kSlot > 10 ? 10 : kRoom / kSlot;
     static constexpr int kSmem = kFixed + kSlots * kSlot;
+    // Tiles whose scales may wait to be read: the copy of tile i + kScales' keys
+    // needs a slot that tile i + 2's keys (or tile i's values) have left, and the
+    // scales of tile i are read before either
+    static constexpr int kScales = kSlots <= 5 ? 4 : 8;
     static constexpr int kTmemUse = 2 * kNs + kNp * (D == 256 ? 2 : 1);
     static constexpr int kTmem = kTmemUse <= 64 ? 64 : kTmemUse <= 128 ? 128 : kTmemUse <= 256 ? 256 : 512;
     static_assert(kTmemUse <= 512 && kSlots >= 3, "does not fit an SM");
 };
 
-// A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
-// into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a
-// row that is not finite.
-template <int D>
-__device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, uint4 (&w)[D / 64]) {
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-        w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * (D / 8) + e * 8) : make_uint4(0, 0, 0, 0);
-}
-template <int D>
-__device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl) {
-    constexpr int E = D / 8, kRow = D < 128 ? D : 128;
-    float m = 0.f, x[E];
-    bool finite = true;
-#pragma unroll
-    for (int e = 0; e < E / 8; ++e) {
-        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
-            x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const bool f = fabsf(x[e]) < INFINITY;
-        finite &= f;
-        x[e] = f ? x[e] : 0.f;
-        m = fmaxf(m, fabsf(x[e]));
-    }
-    uint32_t top = __float_as_uint(m);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (threadIdx.x & 24)) & 0xffu;
-    const int k = max(-110, min(110, 7 - (int(top >> 23) - 127)));  // largest in [128, 256)
-    const float up = kv8::pow2i(k), up32 = up * 32.f, down = kv8::pow2i(-k);
-#pragma unroll
-    for (int b = 0; b < E / 8; ++b) {
-        uint32_t h[2], l[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t hh[2], ll[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x0 = x[b * 8 + g * 4 + 2 * i], x1 = x[b * 8 + g * 4 + 2 * i + 1];
-                hh[i] = kv8::e4m3x2(x0 * up, x1 * up);
-                const float2 back = kv8::f32x2_of(uint16_t(hh[i]));
-                ll[i] = kv8::e4m3x2(fmaf(back.x, -32.f, x0 * up32), fmaf(back.y, -32.f, x1 * up32));
-            }
-            h[g] = hh[0] | (hh[1] << 16);
-            l[g] = ll[0] | (ll[1] << 16);
-        }
-        const int e0 = sub * E + b * 8, atom = e0 / kRow, in = e0 % kRow;
-        uint8_t *t = tile + atom * rows * kRow + (in & 8);
-        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
-        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
-    }
-    return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
-}
+template <int D, int RB>
+struct Shared {
+    using C = Cfg<D, RB>;
+    uint64_t full[C::kSlots], empty[C::kSlots], sc_full[C::kScales], s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t seg_full[kQueue], seg_empty[kQueue], q_ready, epi_done, fk_ready, fv_full, drain;
+    float2 scales[C::kScales][8];
+    alignas(16) float col_nm[RB], col_coef[RB], col_fac[RB];  // -m, score factor, rescaling
+    float col_l[RB];
+    union {
+        float col_max[4][RB];
+        long long scan[C::kThreads / 32];
+    };
+    float v_max[C::kGroups][4], fresh_k[16];
+    Segment seg[kQueue];
+    int bad[kQueue];
+    long long start_at;
+    int start_r;
+    uint32_t tmem;
+    uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
+};
 
-// Sums of N values over a warp's lanes: value k's sum lands in v[0] of the
-// lanes whose top log2(N) bits are k.
-template <int N>
-__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
-    constexpr int kSteps = N == 16 ? 4 : 3;
-    static_assert(N == 16 || N == 8, "columns a thread");
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int off = 16 >> s, half = N >> (s + 1);
-        const bool up = lane & off;
-#pragma unroll
-        for (int k = 0; k < half; ++k) {
-            const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
-            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-        }
-    }
-#pragma unroll
-    for (int off = 16 >> kSteps; off; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-}
-
-// Ring positions of the tiles' loads, in the order the products use them:
+// Ring positions of a segment's loads, in the order the products use them:
 // K0 K1 V0 K2 V1 ... V(n-1).
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+
+__device__ __forceinline__ long long weight_of(const AttendArgs &a, const Request &q, int rb) {
+    if (q.bad || q.n == 0) return 0;
+    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + 1);
+}
+
+// Where a range's end at x falls in a unit of `tiles` tiles: 0 its start, tiles
+// + 1 its end.  Free cuts leave no part of fewer than kLeast tiles.
+__device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles) {
+    if (x <= 0) return 0;
+    if (x > tiles) return tiles + 1;
+    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + 1 : int(x);
+    const long long y = (x + a.piece_tiles - 1) / a.piece_tiles * a.piece_tiles;
+    return y >= tiles ? tiles + 1 : int(y);
+}
 
 template <int D, int RB>
 __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     kv8_attend_kernel(const __grid_constant__ AttendArgs a) {
     using C = Cfg<D, RB>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
-    __shared__ uint64_t sc_full[kScales], fk_ready, fv_full;
-    __shared__ float2 sc_ring[kScales][8];
-    __shared__ int bad_page;
-    __shared__ uint32_t tmem_ptr;
-    __shared__ alignas(16) float col_nm[RB], col_coef[RB], col_fac[RB];  // -m
-    __shared__ float col_max[4][RB], v_max[C::kGroups][4];
-    __shared__ uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
-    __shared__ float fresh_k[16];
-    __shared__ float col_l[RB];
+    __shared__ Shared<D, RB> s;
+    static_assert(sizeof(Shared<D, RB>) <= C::kStatic, "static shared memory");
 
     gdn::pdl_enter();
-    const int piece = blockIdx.x, hk = blockIdx.y / a.blocks, blk = blockIdx.y % a.blocks, r = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Request rq = request_of(a, r);
-    if (rq.bad) {
-        if (piece == 0 && blockIdx.y == 0 && tid == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
-        return;
+    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
+
+    // ---- this CTA's range of the units laid end to end
+    long long total, begin, end;
+    int ctas;
+    {
+        const int chunk = (a.B + C::kThreads - 1) / C::kThreads, r0 = tid * chunk, r1 = min(a.B, r0 + chunk);
+        long long mine = 0;
+        for (int r = r0; r < r1; ++r) {
+            const Request q = request_of(a, r);
+            mine += weight_of(a, q, RB);
+            if (q.bad && blockIdx.x == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) s.scan[warp] = incl;
+        __syncthreads();
+        total = 0;
+        long long before = 0;
+#pragma unroll
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            if (w < warp) before += s.scan[w];
+            total += s.scan[w];
+        }
+        // free cuts: at least four tiles a range, so that none is empty inside a unit
+        const long long most = a.pinned ? total : total / 4;
+        ctas = int(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
+        const int cta = blockIdx.x;
+        if (tid == 0 && a.parts) a.parts[2 * cta].count = a.parts[2 * cta + 1].count = 0;
+        if (cta >= ctas || total == 0) return;
+        begin = total * cta / ctas;
+        end = total * (cta + 1) / ctas;
+        incl += before;
+        if (incl - mine <= begin && begin < incl) {
+            long long at = incl - mine;
+            for (int r = r0; r < r1; ++r) {
+                const long long w = weight_of(a, request_of(a, r), RB);
+                if (at + w > begin) {
+                    s.start_r = r;
+                    s.start_at = at;
+                    break;
+                }
+                at += w;
+            }
+        }
     }
-    const int cols = min(RB, rq.n * a.group - blk * RB);  // columns of this block in use
-    if (piece >= rq.pieces || cols <= 0) return;
 
     const int T = a.c.page_tokens, shift = a.page_shift;
-    const int tile0 = rq.lo / kTile + piece * a.piece_tiles;
-    const int nc = max(0, min(a.piece_tiles, rq.tiles - piece * a.piece_tiles));  // cached tiles
-    const bool fresh = a.k != nullptr && piece == rq.pieces - 1;
-    const int nt = nc + (fresh ? 1 : 0);
-
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *s_fk = sm, *s_fv = s_fk + C::kFresh, *s_q = s_fv + C::kFresh;
     uint8_t *s_p = s_q + ((C::kQ + 1023) & ~1023), *s_ring = s_p + 2 * C::kP;
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            gdn::mbar_init(&full[i], 1);
-            gdn::mbar_init(&empty[i], 1);
+            gdn::mbar_init(&s.full[i], 1);
+            gdn::mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            gdn::mbar_init(&s_full[i], 1);
-            gdn::mbar_init(&s_free[i], C::kSoft / 32);
-            gdn::mbar_init(&p_full[i], C::kSoft / 32);
-            gdn::mbar_init(&pv_done[i], 1);
+            gdn::mbar_init(&s.s_full[i], 1);
+            gdn::mbar_init(&s.s_free[i], C::kSoft / 32);
+            gdn::mbar_init(&s.p_full[i], C::kSoft / 32);
+            gdn::mbar_init(&s.pv_done[i], 1);
         }
-        for (int i = 0; i < kScales; ++i) gdn::mbar_init(&sc_full[i], 1);
-        gdn::mbar_init(&q_ready, C::kSoft / 32);
-        gdn::mbar_init(&fk_ready, 1);
-        gdn::mbar_init(&fv_full, 1);
-        gdn::mbar_init(&drain, 1);
-        bad_page = 0;
+        for (int i = 0; i < C::kScales; ++i) gdn::mbar_init(&s.sc_full[i], 1);
+        for (int i = 0; i < kQueue; ++i) {
+            gdn::mbar_init(&s.seg_full[i], 1);
+            gdn::mbar_init(&s.seg_empty[i], C::kSoft / 32 + 1);
+        }
+        gdn::mbar_init(&s.q_ready, C::kSoft / 32);
+        gdn::mbar_init(&s.epi_done, C::kSoft / 32);
+        gdn::mbar_init(&s.fk_ready, 1);
+        gdn::mbar_init(&s.fv_full, 1);
+        gdn::mbar_init(&s.drain, 1);
     }
-    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
-    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_ptr, C::kTmem);
+    if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, C::kTmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     float *fresh_p = reinterpret_cast<float *>(s_fk);  // [16][RB], once the fresh keys' product is done
     static_assert(RB * 16 * 4 <= C::kFresh, "weights of the fresh rows");
-    const uint32_t tm = tmem_ptr, tm_o = tm + 2 * C::kNs;
+    const uint32_t tm = s.tmem, tm_o = tm + 2 * C::kNs;
 
     if (warp == kCopyWarp) {
-        // ---- copies.  Page ids and scales come 32 pages at a time, ids two and scales
-        // one such batch ahead.
-        if (fresh && rq.n > 0) {
-            if (lane == 0) gdn::mbar_arrive_expect_tx(&fv_full, uint32_t(rq.n) * (2 * D));
-            __syncwarp();
-            if (lane < rq.n)
-                gdn::bulk_g2s(s_fv + lane * 2 * D, a.v + (int64_t(rq.t0) + lane) * a.v_stride + int64_t(hk) * D, 2 * D,
-                              &fv_full);
-        }
+        // ---- copies
         const int per = kTile >> shift;  // pages a tile
-        const int page0 = tile0 * per, first = rq.lo >> shift, last = (rq.len + T - 1) >> shift;
-        const int32_t *tab = a.table + int64_t(r) * a.table_stride;
-        const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride + 2 * hk;
-        constexpr int kNone = -1;  // a page no row sees
-        auto wanted = [&](int batch) {
-            const int j = page0 + batch * 32 + lane;
-            return j >= first && j < last && batch * 32 + lane < nc * per;
-        };
-        auto ids = [&](int batch) { return wanted(batch) ? tab[page0 + batch * 32 + lane] : kNone; };
-        auto scales = [&](int p) {
-            return p >= 0 && p < a.c.num_pages
-                       ? *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride)
-                       : make_float2(0.f, 0.f);
-        };
+        const float *sc0 = a.c.scale + int64_t(a.layer) * a.c.scale_layer_stride;
+        const int cta = blockIdx.x;
         bool ok = true;
-        int issued = 0;
-        auto issue = [&](int pos, int page, int is_v) {
-            const int slot = pos % C::kSlots;
-            if (pos >= C::kSlots)
-                ok = ok && gdn::mbar_wait_bounded(&empty[slot], ((pos / C::kSlots) - 1) & 1, a.wait_ns);
+        int k = 0, ring = 0, issued = 0;       // segments and ring positions so far; copies issued
+        int tiles_done = 0, fresh_done = 0;
+        auto push = [&](const Segment &g) {
+            if (k >= kQueue)
+                ok = ok && gdn::mbar_wait_bounded(&s.seg_empty[k % kQueue], (k / kQueue - 1) & 1, a.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            const uint32_t have = __ballot_sync(0xffffffffu, lane < per && page >= 0);
-            if (lane == 0) gdn::mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(have)) * uint32_t(T * D));
+            if (lane == 0) {
+                s.seg[k % kQueue] = g;
+                s.bad[k % kQueue] = 0;
+                arrive(&s.seg_full[k % kQueue]);
+            }
             __syncwarp();
-            issued = pos + 1;
-            if (lane < per && page >= 0) {
-#pragma unroll
-                for (int x = 0; x < C::kAtoms; ++x)
-                    gdn::tma_load_3d(s_ring + slot * C::kSlot + x * kTile * C::kRow + lane * T * C::kRow, &a.map,
-                                     x * C::kRow, (is_v * a.c.h_kv + hk) * T, page, &full[slot]);
-            }
         };
-        int cur = ids(0), nxt = ids(1), far = ids(2), batch = 0, prev = -1;
-        float2 sc = scales(cur), sc_nxt = scales(nxt);
-        for (int i = 0; i <= nc && ok; ++i) {
-            int page = -1;
-            float2 s = make_float2(0.f, 0.f);
-            if (i < nc) {
-                const int at = i * per;
-                if (at / 32 != batch) {
-                    batch = at / 32;
-                    cur = nxt;
-                    sc = sc_nxt;
-                    nxt = far;
-                    sc_nxt = scales(nxt);
-                    far = ids(batch + 2);
-                }
-                // an id out of range is not loaded; the piece's outputs are dropped
-                const int src = (at % 32) + (lane & (per - 1));
-                page = __shfl_sync(0xffffffffu, cur, src);
-                const bool want = page0 + at + (lane & (per - 1)) >= first && page0 + at + (lane & (per - 1)) < last;
-                if (page < 0 || page >= a.c.num_pages) {
-                    if (want) *reinterpret_cast<volatile int *>(&bad_page) = 1;
-                    page = -1;
-                }
-                issue(k_pos(i), page, 0);
-            }
-            if (i > 0 && ok) issue(v_pos(i - 1, nc), prev, 1);
-            if (i < nc && ok) {
-                const int src = (i * per % 32) + (lane & (per - 1));
-                s.x = __shfl_sync(0xffffffffu, sc.x, src);
-                s.y = __shfl_sync(0xffffffffu, sc.y, src);
-                if (lane < per) sc_ring[i % kScales][lane] = s;
+        // A segment: queue it, then its tiles.  Page ids and scales come 32 pages at a
+        // time, ids two and scales one such batch ahead.
+        auto run = [&](const Segment &g) {
+            push(g);
+            if (!ok) return;
+            const int nc = g.nc, page0 = g.tile0 * per, first = g.lo >> shift, last = (g.len + T - 1) >> shift;
+            const int32_t *tab = a.table + int64_t(g.r) * a.table_stride;
+            auto ids = [&](int batch) {
+                const int x = batch * 32 + lane, j = page0 + x;
+                return j >= first && j < last && x < nc * per ? tab[j] : -1;
+            };
+            auto scales = [&](int p) {
+                return p >= 0 && p < a.c.num_pages
+                           ? *reinterpret_cast<const float2 *>(sc0 + int64_t(p) * a.c.scale_page_stride + 2 * g.hk)
+                           : make_float2(0.f, 0.f);
+            };
+            auto issue = [&](int pos, int page, int is_v) {
+                const int slot = pos % C::kSlots;
+                if (pos >= C::kSlots)
+                    ok = ok && gdn::mbar_wait_bounded(&s.empty[slot], (pos / C::kSlots - 1) & 1, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                const uint32_t have = __ballot_sync(0xffffffffu, lane < per && page >= 0);
+                if (lane == 0) gdn::mbar_arrive_expect_tx(&s.full[slot], uint32_t(__popc(have)) * uint32_t(T * D));
                 __syncwarp();
-                if (lane == 0) arrive(&sc_full[i % kScales]);
+                issued = pos + 1;
+                if (lane < per && page >= 0) {
+#pragma unroll
+                    for (int x = 0; x < C::kAtoms; ++x)
+                        gdn::tma_load_3d(s_ring + slot * C::kSlot + x * kTile * C::kRow + lane * T * C::kRow, &a.map,
+                                         x * C::kRow, (is_v * a.c.h_kv + g.hk) * T, page, &s.full[slot]);
+                }
+            };
+            int cur = ids(0), nxt = ids(1), far = ids(2), batch = 0, prev = -1;
+            float2 sc = scales(cur), sc_nxt = scales(nxt);
+            for (int i = 0; i <= nc && ok; ++i) {
+                int page = -1;
+                const int at = i * per, src = (at % 32) + (lane & (per - 1));
+                if (i < nc) {
+                    if (at / 32 != batch) {
+                        batch = at / 32;
+                        cur = nxt;
+                        sc = sc_nxt;
+                        nxt = far;
+                        sc_nxt = scales(nxt);
+                        far = ids(batch + 2);
+                    }
+                    page = __shfl_sync(0xffffffffu, cur, src);
+                    if (page < 0 || page >= a.c.num_pages) {
+                        // a bad id is not loaded, and the segment's outputs are dropped
+                        const int j = page0 + at + (lane & (per - 1));
+                        if (j >= first && j < last) *reinterpret_cast<volatile int *>(&s.bad[k % kQueue]) = 1;
+                        page = -1;
+                    }
+                    issue(ring + k_pos(i), page, 0);
+                }
+                if (i > 0 && ok) issue(ring + v_pos(i - 1, nc), prev, 1);
+                if (i < nc && ok) {
+                    float2 x;
+                    x.x = __shfl_sync(0xffffffffu, sc.x, src);
+                    x.y = __shfl_sync(0xffffffffu, sc.y, src);
+                    const int e = (tiles_done + i) % C::kScales;
+                    if (lane < per) s.scales[e][lane] = x;
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.sc_full[e]);
+                }
+                prev = page;
             }
-            prev = page;
+            if (ok) {
+                ring += 2 * nc;
+                tiles_done += nc;
+            }
+            if (ok && g.fresh) {
+                // the new rows' values, once the segment before is done with their place
+                if (k > 0)
+                    ok = gdn::mbar_wait_bounded(&s.seg_empty[(k - 1) % kQueue], ((k - 1) / kQueue) & 1, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    if (lane == 0) gdn::mbar_arrive_expect_tx(&s.fv_full, uint32_t(g.n) * (2 * D));
+                    __syncwarp();
+                    if (lane < g.n)
+                        gdn::bulk_g2s(s_fv + lane * 2 * D, a.v + (int64_t(g.t0) + lane) * a.v_stride + int64_t(g.hk) * D,
+                                      2 * D, &s.fv_full);
+                    ++fresh_done;
+                }
+            }
+            ++k;
+        };
+        int r = s.start_r;
+        long long at = s.start_at;
+        Request q = request_of(a, r);
+        while (at < end && ok) {
+            const Request next = request_of(a, min(r + 1, a.B - 1));
+            const long long w = weight_of(a, q, RB);
+            if (w > 0) {
+                const int cost = q.tiles + 1, nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
+                for (int u = begin > at ? int((begin - at) / cost) : 0; u < units && at + (long long)u * cost < end && ok;
+                     ++u) {
+                    const long long su = at + (long long)u * cost;
+                    const int x0 = cut_at(a, begin - su, q.tiles), x1 = cut_at(a, end - su, q.tiles);
+                    Segment g;
+                    g.r = r;
+                    g.t0 = q.t0;
+                    g.n = uint8_t(q.n);
+                    g.len = q.len;
+                    g.lo = q.lo;
+                    g.hk = uint16_t(u / nb);
+                    g.blk = uint16_t(u % nb);
+                    g.cols = uint8_t(min(RB, q.n * a.group - g.blk * RB));
+                    const int y = g.hk * a.blocks + g.blk;
+                    // given cuts: a segment for each piece of the range
+                    for (int x = x0; x < x1 && ok;) {
+                        int to = a.pinned ? min(x + a.piece_tiles, x1) : x1;
+                        if (to >= q.tiles) to = cost;
+                        g.tile0 = q.lo / kTile + x;
+                        g.nc = min(to, q.tiles) - x;
+                        g.fresh = a.k != nullptr && to == cost;
+                        g.out = -1;
+                        if (a.pinned) {
+                            if (q.tiles > a.piece_tiles)
+                                g.out = (r * a.max_pieces + x / a.piece_tiles) * (a.c.h_kv * a.blocks) + y;
+                        } else if (x0 > 0 || x1 < cost) {
+                            // the first CTA whose end lies past the start, the first whose end counts as the unit's
+                            const long long lo = su + kLeast, hi = su + q.tiles - kLeast + 1;
+                            Part p;
+                            p.r = r;
+                            p.y = y;
+                            p.owner = int((lo * ctas + total - 1) / total) - 1;
+                            p.count = int((hi * ctas + total - 1) / total) - p.owner;
+                            g.out = 2 * cta + (x0 > 0 ? 0 : 1);
+                            if (lane == 0) a.parts[g.out] = p;
+                        }
+                        run(g);
+                        x = to;
+                    }
+                }
+            }
+            at += w;
+            ++r;
+            q = next;
+            if (r >= a.B) break;
         }
-        if (!ok) {
-            // wait, again bounded, for the copies in flight into this CTA's shared memory
-            gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-            for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
-                (void)gdn::mbar_wait_bounded(&full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
+        if (ok) {
+            Segment g = {};
+            push(g);
         }
-        if (fresh && rq.n > 0) (void)gdn::mbar_wait_bounded(&fv_full, 0, a.wait_ns);
+        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+        // every copy has landed before the CTA leaves (on the usual path these waits are over)
+        for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
+            (void)gdn::mbar_wait_bounded(&s.full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
+        if (fresh_done) (void)gdn::mbar_wait_bounded(&s.fv_full, (fresh_done - 1) & 1, a.wait_ns);
     } else if (warp == kMmaWarp) {
         // ---- products: the warp runs the loop, one elected lane issues
-        if (nt > 0) {
-            constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
-            constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kAMnMajor | tc::kBMnMajor;
-            const uint64_t dq = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_q), 16);
-            // weights: rows are positions; RB = 64 has two tiles of 128 columns
-            const uint64_t dp = tc::smem_desc8<C::kPRow>(gdn::smem_u32(s_p), kTile * C::kPRow);
-            // V has 128 rows of M at d >= 128; at d = 64 rows 64.. read the next slot and are not used
-            constexpr uint32_t lbo = C::kRow == 64 ? C::kSlot : 16;
-            const uint64_t dk0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), 16);
-            const uint64_t dv0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), lbo);
-            const uint64_t dfk = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_fk), 16);
-            const bool leader = elect_one();
-            if (fresh) {
-                for (int j0 = 0; j0 < rq.n; j0 += 4) {
-                    const int j = j0 + (lane >> 3);
-                    uint4 w[D / 64];
-                    load_row<D>(a.k + (int64_t(rq.t0) + j) * a.k_stride + int64_t(hk) * D, lane & 7, j < rq.n, w);
-                    const float down = split_row<D>(w, lane & 7, s_fk, 32, j, 16 + j);
-                    if ((lane & 7) == 0) fresh_k[j] = down;
+        constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
+        constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kAMnMajor | tc::kBMnMajor;
+        const uint64_t dq = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_q), 16);
+        // weights: rows are positions; RB = 64 has two tiles of 128 columns
+        const uint64_t dp = tc::smem_desc8<C::kPRow>(gdn::smem_u32(s_p), kTile * C::kPRow);
+        // V has 128 rows of M at d >= 128; at d = 64 rows 64.. read the next slot and are not used
+        constexpr uint32_t lbo = C::kRow == 64 ? C::kSlot : 16;
+        const uint64_t dk0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), 16);
+        const uint64_t dv0 = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_ring), lbo);
+        const uint64_t dfk = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_fk), 16);
+        const bool leader = elect_one();
+        bool ok = true;
+        int ring = 0, gs = 0, gp = 0;  // ring positions, score tiles and weight tiles before this segment
+        for (int k = 0; ok; ++k) {
+            ok = gdn::mbar_wait_bounded(&s.seg_full[k % kQueue], (k / kQueue) & 1, a.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const Segment &g = s.seg[k % kQueue];
+            const int nc = g.nc, n = g.n, fresh = g.fresh, nt = nc + fresh;
+            if (g.cols == 0) break;
+            const uint16_t *kn = a.k + int64_t(g.t0) * a.k_stride + int64_t(g.hk) * D;
+            uint4 w[D / 64];
+            if (fresh) load_row<D>(kn + int64_t(lane >> 3) * a.k_stride, lane & 7, (lane >> 3) < n, w);
+            ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
+            for (int i = 0; i <= nt; ++i) {
+                if (fresh && i == min(1, nc)) {
+                    // the new keys, while the softmax is at the segment's first tile; their place
+                    // is free once the segment before is done
+                    if (ok && k > 0)
+                        ok = gdn::mbar_wait_bounded(&s.seg_empty[(k - 1) % kQueue], ((k - 1) / kQueue) & 1, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    for (int j0 = 0; j0 < n; j0 += 4) {
+                        const int j = j0 + (lane >> 3);
+                        if (j0) load_row<D>(kn + int64_t(j) * a.k_stride, lane & 7, j < n, w);
+                        const float down = split_row<D>(w, lane & 7, s_fk, 32, j, 16 + j);
+                        if ((lane & 7) == 0) s.fresh_k[j] = down;
+                    }
+                    gdn::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.fk_ready);
                 }
-                gdn::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive(&fk_ready);
-            }
-            bool ok = gdn::mbar_wait_bounded(&q_ready, 0, a.wait_ns);
-            for (int i = 0; i <= nt && ok; ++i) {
                 if (i < nt) {
                     const bool cached = i < nc;
-                    const int pos = k_pos(i), slot = pos % C::kSlots;
-                    if (cached) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                    if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&s_free[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
+                    const int pos = ring + k_pos(i), slot = pos % C::kSlots, x = gs + i;
+                    if (ok && cached) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                    if (ok && x >= 2) ok = gdn::mbar_wait_bounded(&s.s_free[x & 1], ((x >> 1) - 1) & 1, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::fence_after();
@@ -489,391 +507,440 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         const uint64_t dk = cached ? tc::desc_at(dk0, slot * C::kSlot) : dfk;
                         const uint32_t atom = cached ? kTile * C::kRow : 32 * C::kRow;
 #pragma unroll
-                        for (int s = 0; s < D / 32; ++s) {
-                            const uint32_t x = s * 32 / C::kRow, in = s * 32 % C::kRow;
-                            tc::mma_e4m3(tm + (i & 1) * C::kNs, tc::desc_at(dk, x * atom + in),
-                                         tc::desc_at(dq, x * C::kNs * C::kRow + in), id_s, s > 0);
+                        for (int e = 0; e < D / 32; ++e) {
+                            const uint32_t t = e * 32 / C::kRow, in = e * 32 % C::kRow;
+                            tc::mma_e4m3(tm + (x & 1) * C::kNs, tc::desc_at(dk, t * atom + in),
+                                         tc::desc_at(dq, t * C::kNs * C::kRow + in), id_s, e > 0);
                         }
-                        tc::commit(&s_full[i & 1]);
-                        if (cached) tc::commit(&empty[slot]);
+                        tc::commit(&s.s_full[x & 1]);
+                        if (cached) tc::commit(&s.empty[slot]);
                     }
                     __syncwarp();
                 }
                 if (i > 0 && i <= nc) {
-                    const int j = i - 1, pos = v_pos(j, nc), slot = pos % C::kSlots;
-                    ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                    if (ok) ok = gdn::mbar_wait_bounded(&p_full[j & 1], (j >> 1) & 1, a.wait_ns);
+                    const int j = i - 1, pos = ring + v_pos(j, nc), slot = pos % C::kSlots, x = gp + j;
+                    if (ok) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                    if (ok) ok = gdn::mbar_wait_bounded(&s.p_full[x & 1], (x >> 1) & 1, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc::fence_after();
                     if (leader) {
-                        const uint64_t dv = tc::desc_at(dv0, slot * C::kSlot), dpj = tc::desc_at(dp, (j & 1) * C::kP);
+                        const uint64_t dv = tc::desc_at(dv0, slot * C::kSlot), dpx = tc::desc_at(dp, (x & 1) * C::kP);
 #pragma unroll
-                        for (int x = 0; x < C::kAtoms; ++x)
+                        for (int t = 0; t < C::kAtoms; ++t)
 #pragma unroll
-                            for (int s = 0; s < kTile / 32; ++s)
-                                tc::mma_e4m3(tm_o + x * C::kNp,
-                                             tc::desc_at(dv, x * kTile * C::kRow + s * 32 * C::kRow),
-                                             tc::desc_at(dpj, s * 32 * C::kPRow), id_p, j > 0 || s > 0);
-                        tc::commit(&pv_done[j & 1]);
-                        tc::commit(&empty[slot]);
+                            for (int e = 0; e < kTile / 32; ++e)
+                                tc::mma_e4m3(tm_o + t * C::kNp, tc::desc_at(dv, t * kTile * C::kRow + e * 32 * C::kRow),
+                                             tc::desc_at(dpx, e * 32 * C::kPRow), id_p, j > 0 || e > 0);
+                        tc::commit(&s.pv_done[x & 1]);
+                        tc::commit(&s.empty[slot]);
                     }
                     __syncwarp();
                 }
             }
-            if (!ok) {
-                gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-                if (leader) tc::commit(&drain);  // products in flight read shared and write tensor memory
-                (void)gdn::mbar_wait_bounded(&drain, 0, a.wait_ns);
-            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ring += 2 * nc;
+            gs += nt;
+            gp += nc;
+            if (lane == 0) arrive(&s.seg_empty[k % kQueue]);
+        }
+        if (!ok) {
+            gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+            if (leader) tc::commit(&s.drain);  // products in flight read shared and write tensor memory
+            (void)gdn::mbar_wait_bounded(&s.drain, 0, a.wait_ns);
         }
         __syncwarp();
     } else {
-        // ---- softmax warps.  First the operands that come as bf16.
-        {
-            // eight threads a column; the columns fill whole warps, one pass takes them all
-            static_assert(RB <= C::kSoft / 8, "a thread has one column");
-            const int c = tid >> 3, sub = tid & 7;
-            if (c < RB) {
-                const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
-                uint4 w[D / 64];
-                load_row<D>(a.q + (int64_t(rq.t0) + row) * a.q_stride + int64_t(h) * D, sub, c < cols, w);
-                const float down = split_row<D>(w, sub, s_q, C::kNs, c, RB + c);
+        // ---- softmax.  This thread's position in a tile and its columns col0 .. col0 + N - 1;
+        // eight threads bring a column's queries (columns fill whole warps).
+        constexpr int N = C::kCols;
+        static_assert(RB <= C::kSoft / 8, "a thread has one column");
+        const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N, cq = tid >> 3, sub = tid & 7;
+        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+        bool ok = gdn::mbar_wait_bounded(&s.seg_full[0], 0, a.wait_ns);
+        if (group_or(grp, !ok)) ok = false;
+        Segment g = s.seg[0];
+        if (!ok) g.cols = 0;
+        uint4 wq[D / 64];
+        auto load_q = [&] {
+            const int x = g.blk * RB + cq;
+            if (cq < RB)
+                load_row<D>(a.q + (int64_t(g.t0) + x / a.group) * a.q_stride + int64_t(g.hk * a.group + x % a.group) * D,
+                            sub, cq < g.cols, wq);
+        };
+        load_q();
+        int gs = 0, gp = 0, ring = 0, fresh_seen = 0;  // score and weight tiles, ring positions, fresh tiles so far
+        for (int k = 0; g.cols > 0; ++k) {
+            if (cq < RB) {
+                const int x = g.blk * RB + cq;
+                const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq);
                 if (sub == 0) {
-                    col_nm[c] = -kUnset;
-                    col_coef[c] = a.c.sm_scale * 1.4426950408889634f * down;
-                    col_row[c] = uint8_t(row);
-                    col_head[c] = uint8_t(x % a.group);
+                    s.col_nm[cq] = -kUnset;
+                    s.col_coef[cq] = a.c.sm_scale * 1.4426950408889634f * down;
+                    s.col_row[cq] = uint8_t(x / a.group);
+                    s.col_head[cq] = uint8_t(x % a.group);
                 }
             }
             gdn::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(&q_ready);
-            soft_sync<C::kSoft>();
-        }
-        // this thread's position in a tile and its columns col0 .. col0 + N - 1
-        constexpr int N = C::kCols;
-        const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N;
-        // a row sees positions from lo0 + row * lo1 on (rq.lo is row 0's, and not negative)
-        const int lo0 = a.c.window ? rq.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
-        const int lo_last = lo0 + lo1 * col_row[cols - 1];
-        bool ok = true;
-        f2 l[N / 2];
-        float z[N];
-#pragma unroll
-        for (int c = 0; c < N / 2; ++c) l[c] = 0;
-        float vref = kv8::pow2i(kv8::kMinScaleExp), vinv = kBase / vref;
-        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+            if (lane == 0) arrive(&s.q_ready);
+            ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
 
-        for (int i = 0; i < nt; ++i) {
-            const bool is_fresh = i >= nc;
-            const int t = (tile0 + i) * kTile + pos_in;
-            if (ok)
-                ok = is_fresh ? gdn::mbar_wait_bounded(&fk_ready, 0, a.wait_ns)
-                              : gdn::mbar_wait_bounded(&sc_full[i % kScales], (i / kScales) & 1, a.wait_ns);
-            const float2 sc = is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < rq.n ? fresh_k[pos_in & 15] : 0.f, 0.f)
-                                       : sc_ring[i % kScales][pos_in >> shift];
-            // whole: every row sees every position of the tile
-            const bool whole = !is_fresh && (tile0 + i + 1) * kTile <= rq.len && (tile0 + i) * kTile >= lo_last;
-            if (ok) ok = gdn::mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, a.wait_ns);
-            tc::fence_after();
+            const int nc = g.nc, nt = nc + g.fresh;
+            // a row sees positions from lo0 + row * lo1 on (g.lo is row 0's, and not negative)
+            const int lo0 = a.c.window ? g.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
+            const int lo_last = lo0 + lo1 * s.col_row[g.cols - 1];
+            f2 l[N / 2];
+            float z[N];
+#pragma unroll
+            for (int c = 0; c < N / 2; ++c) l[c] = 0;
+            float vref = pow2i(kMinScaleExp), vinv = kBase / vref;
 
-            // z - m of every column (m = 0 where the reference is to move)
-            auto load_z = [&](bool plain) {
-                uint32_t hi[N], lo[N];
-                const uint32_t at = tm + lane_base + (i & 1) * C::kNs + col0;
-                if constexpr (N == 16) {
-                    tc::ld16_async(at, hi);
-                    tc::ld16_async(at + RB, lo);
-                } else {
-                    tc::ld8_async(at, hi);
-                    tc::ld8_async(at + RB, lo);
-                }
-                tc::ld_wait();
-                tc::ld_fence_regs(hi);
-                tc::ld_fence_regs(lo);
-                f2 s[N / 2];
-#pragma unroll
-                for (int c = 0; c < N / 2; ++c)
-                    s[c] = fma2(pair(lo[2 * c], lo[2 * c + 1]), pair(1.f / 32.f, 1.f / 32.f),
-                                pair(hi[2 * c], hi[2 * c + 1]));
-                if (is_fresh) {  // the other part of the position
-#pragma unroll
-                    for (int c = 0; c < N / 2; ++c) {
-                        const float2 x = both(s[c]);
-                        const f2 other = pair(__shfl_xor_sync(0xffffffffu, x.x, 16), __shfl_xor_sync(0xffffffffu, x.y, 16));
-                        s[c] = pos_in & 16 ? fma2(s[c], pair(1.f / 32.f, 1.f / 32.f), other)
-                                           : fma2(other, pair(1.f / 32.f, 1.f / 32.f), s[c]);
+            for (int i = 0; i < nt; ++i) {
+                const bool is_fresh = i >= nc;
+                const int x = gs + i, y = gp + i, t = (g.tile0 + i) * kTile + pos_in;
+                if (ok)
+                    ok = is_fresh ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
+                                  : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
+                const float2 sc =
+                    is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < g.n ? s.fresh_k[pos_in & 15] : 0.f, 0.f)
+                             : s.scales[y % C::kScales][pos_in >> shift];
+                // whole: every row sees every position of the tile
+                const bool whole = !is_fresh && (g.tile0 + i + 1) * kTile <= g.len && (g.tile0 + i) * kTile >= lo_last;
+                if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
+                tc::fence_after();
+
+                // z - m of every column (m = 0 where the reference is to move)
+                auto load_z = [&](bool plain) {
+                    uint32_t hi[N], lo[N];
+                    const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
+                    if constexpr (N == 16) {
+                        tc::ld16_async(at, hi);
+                        tc::ld16_async(at + RB, lo);
+                    } else {
+                        tc::ld8_async(at, hi);
+                        tc::ld8_async(at + RB, lo);
                     }
-                }
-                const f2 sx = pair(sc.x, sc.x);
+                    tc::ld_wait();
+                    tc::ld_fence_regs(hi);
+                    tc::ld_fence_regs(lo);
+                    f2 v[N / 2];
+                    const f2 part = pair(1.f / 32.f, 1.f / 32.f);
 #pragma unroll
-                for (int c = 0; c < N; c += 4) {
-                    const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(col_coef + col0 + c);
-                    ulonglong2 nm = make_ulonglong2(0, 0);
-                    if (!plain) nm = *reinterpret_cast<const ulonglong2 *>(col_nm + col0 + c);
-                    const float2 x = both(fma2(s[c / 2], mul2(sx, k.x), nm.x)),
-                                 y = both(fma2(s[c / 2 + 1], mul2(sx, k.y), nm.y));
-                    z[c] = x.x;
-                    z[c + 1] = x.y;
-                    z[c + 2] = y.x;
-                    z[c + 3] = y.y;
-                }
-                if (is_fresh) {
-                    const int j = pos_in & 15, w = a.c.window;
+                    for (int c = 0; c < N / 2; ++c)
+                        v[c] = fma2(pair(lo[2 * c], lo[2 * c + 1]), part, pair(hi[2 * c], hi[2 * c + 1]));
+                    if (is_fresh) {  // the other part of the position
 #pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        const int row = col_row[col0 + c];
-                        const bool see = pos_in < 32 && j < rq.n && j <= row && (!w || j > row - w);
-                        z[c] = see ? z[c] : -INFINITY;
+                        for (int c = 0; c < N / 2; ++c) {
+                            const float2 b = both(v[c]);
+                            const f2 other =
+                                pair(__shfl_xor_sync(0xffffffffu, b.x, 16), __shfl_xor_sync(0xffffffffu, b.y, 16));
+                            v[c] = pos_in & 16 ? fma2(v[c], part, other) : fma2(other, part, v[c]);
+                        }
                     }
-                } else if (!whole) {
+                    const f2 sx = pair(sc.x, sc.x);
 #pragma unroll
-                    for (int c = 0; c < N; ++c) z[c] = t < rq.len && t >= lo0 + lo1 * col_row[col0 + c] ? z[c] : -INFINITY;
-                }
-            };
-            load_z(false);
-            float over = -INFINITY;
+                    for (int c = 0; c < N; c += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s.col_coef + col0 + c);
+                        ulonglong2 nm = make_ulonglong2(0, 0);
+                        if (!plain) nm = *reinterpret_cast<const ulonglong2 *>(s.col_nm + col0 + c);
+                        const float2 b0 = both(fma2(v[c / 2], mul2(sx, f.x), nm.x)),
+                                     b1 = both(fma2(v[c / 2 + 1], mul2(sx, f.y), nm.y));
+                        z[c] = b0.x;
+                        z[c + 1] = b0.y;
+                        z[c + 2] = b1.x;
+                        z[c + 3] = b1.y;
+                    }
+                    if (is_fresh) {
+                        const int j = pos_in & 15, w = a.c.window;
 #pragma unroll
-            for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
-            if (group_or(grp, over > kSlack || sc.y > vref || !ok)) {
-                // ---- the reference moves (or a wait ran out)
-                if (group_or(grp, !ok)) {
-                    ok = false;
-                    break;
-                }
-                load_z(true);
+                        for (int c = 0; c < N; ++c) {
+                            const int row = s.col_row[col0 + c];
+                            const bool see = pos_in < 32 && j < g.n && j <= row && (!w || j > row - w);
+                            z[c] = see ? z[c] : -INFINITY;
+                        }
+                    } else if (!whole) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    const float x = warp_max(z[c]);
-                    if (lane == 0) col_max[warp & 3][col0 + c] = x;
-                }
-                const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
-                if (lane == 0) v_max[grp][warp & 3] = __uint_as_float(vm);
-                group_sync(grp);
-                if (pos_in < N) {
-                    const int c = col0 + pos_in;
-                    const float was = -col_nm[c];
-                    const float now =
-                        fmaxf(fmaxf(fmaxf(col_max[0][c], col_max[1][c]), fmaxf(col_max[2][c], col_max[3][c])), was);
-                    col_fac[c] = ex2(was - now);
-                    col_nm[c] = -now;
-                }
-                const float vnow = fmaxf(fmaxf(fmaxf(v_max[grp][0], v_max[grp][1]), fmaxf(v_max[grp][2], v_max[grp][3])), vref);
-                const float vfac = vref / vnow;
-                vref = vnow;
-                vinv = kBase / vnow;
-                group_sync(grp);
+                        for (int c = 0; c < N; ++c)
+                            z[c] = t < g.len && t >= lo0 + lo1 * s.col_row[col0 + c] ? z[c] : -INFINITY;
+                    }
+                };
+                load_z(false);
+                float over = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < N; c += 2) {
-                    l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(col_fac + col0 + c));
-                    z[c] += col_nm[col0 + c];
-                    z[c + 1] += col_nm[col0 + c + 1];
-                }
-                if (i > 0) {
-                    ok = gdn::mbar_wait_bounded(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, a.wait_ns);
+                for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
+                if (group_or(grp, over > kSlack || sc.y > vref || !ok)) {
+                    // ---- the reference moves (or a wait ran out)
                     if (group_or(grp, !ok)) {
                         ok = false;
                         break;
                     }
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int x = 0; x < C::kAtoms * 4 * N; x += 8) {  // this group's columns of every part
-                        const int at = x / N * RB + col0 + x % N;
-                        uint32_t w[8];
-                        tc::ld8_async(tm_o + lane_base + at, w);
-                        tc::ld_wait();
-                        tc::ld_fence_regs(w);
+                    load_z(true);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            w[c] = __float_as_uint(__uint_as_float(w[c]) * (col_fac[at % RB + c] * vfac));
-                        tc::st8(tm_o + lane_base + at, w);
+                    for (int c = 0; c < N; ++c) {
+                        const float top = warp_max(z[c]);
+                        if (lane == 0) s.col_max[warp & 3][col0 + c] = top;
                     }
-                    tc::st_wait();
-                }
-            }
-            // scores are read: their buffer is free
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&s_free[i & 1]);
-
-            if (is_fresh) {
-                if (pos_in < 16) {
+                    const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
+                    if (lane == 0) s.v_max[grp][warp & 3] = __uint_as_float(vm);
+                    group_sync(grp);
+                    if (pos_in < N) {
+                        const int c = col0 + pos_in;
+                        const float was = -s.col_nm[c];
+                        const float now = fmaxf(
+                            fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]), fmaxf(s.col_max[2][c], s.col_max[3][c])), was);
+                        s.col_fac[c] = ex2(was - now);
+                        s.col_nm[c] = -now;
+                    }
+                    const float vnow = fmaxf(
+                        fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]), fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
+                    const float vfac = vref / vnow;
+                    vref = vnow;
+                    vinv = kBase / vnow;
+                    group_sync(grp);
 #pragma unroll
                     for (int c = 0; c < N; c += 2) {
-                        const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
-                        l[c / 2] = add2(l[c / 2], p);
-                        *reinterpret_cast<f2 *>(fresh_p + pos_in * RB + col0 + c) = p;
+                        l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(s.col_fac + col0 + c));
+                        z[c] += s.col_nm[col0 + c];
+                        z[c + 1] += s.col_nm[col0 + c + 1];
+                    }
+                    if (i > 0) {
+                        ok = gdn::mbar_wait_bounded(&s.pv_done[(y - 1) & 1], ((y - 1) >> 1) & 1, a.wait_ns);
+                        if (group_or(grp, !ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int e = 0; e < C::kAtoms * 4 * N; e += 8) {  // this group's columns of every part
+                            const int at = e / N * RB + col0 + e % N;
+                            uint32_t w[8];
+                            tc::ld8_async(tm_o + lane_base + at, w);
+                            tc::ld_wait();
+                            tc::ld_fence_regs(w);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                w[c] = __float_as_uint(__uint_as_float(w[c]) * (s.col_fac[at % RB + c] * vfac));
+                            tc::st8(tm_o + lane_base + at, w);
+                        }
+                        tc::st_wait();
                     }
                 }
-                break;  // the last tile
-            }
-            const float xw = sc.y * vinv;
-            const f2 xw2 = pair(xw, xw), xw32 = pair(32.f * xw, 32.f * xw);
-            if (ok && i >= 2) ok = gdn::mbar_wait_bounded(&pv_done[i & 1], ((i >> 1) - 1) & 1, a.wait_ns);
-            uint8_t *pb = s_p + (i & 1) * C::kP;
-            // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
-            constexpr int W = N < 16 ? 8 : 16;
+                // scores are read: their buffer is free
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&s.s_free[x & 1]);
+
+                if (is_fresh) {
+                    if (pos_in < 16) {
 #pragma unroll
-            for (int c0 = 0; c0 < N; c0 += W) {
-                uint16_t e[4][W / 2];
-#pragma unroll
-                for (int c = 0; c < W / 2; ++c) {
-                    const f2 p = pair(ex2(z[c0 + 2 * c]), ex2(z[c0 + 2 * c + 1]));
-                    l[c0 / 2 + c] = add2(l[c0 / 2 + c], p);
-                    const float2 x = both(mul2(p, xw2));
-                    e[0][c] = uint16_t(kv8::e4m3x2(x.x, x.y));
-                    const float2 r = minus32(both(mul2(p, xw32)), kv8::f16x2_of(e[0][c]));  // exact
-                    uint32_t rest = f16x2(r.x, r.y);
-                    e[1][c] = e4m3x2_of(rest);
-                    rest = rest32(rest, kv8::f16x2_of(e[1][c]));
-                    e[2][c] = e4m3x2_of(rest);
-                    e[3][c] = e4m3x2_of(rest32(rest, kv8::f16x2_of(e[2][c])));
+                        for (int c = 0; c < N; c += 2) {
+                            const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
+                            l[c / 2] = add2(l[c / 2], p);
+                            *reinterpret_cast<f2 *>(fresh_p + pos_in * RB + col0 + c) = p;
+                        }
+                    }
+                    break;  // the last tile
                 }
+                const float xw = sc.y * vinv;
+                const f2 xw2 = pair(xw, xw), xw32 = pair(32.f * xw, 32.f * xw);
+                if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
+                uint8_t *pb = s_p + (y & 1) * C::kP;
+                // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
+                constexpr int W = N < 16 ? 8 : 16;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int b = k * RB + col0 + c0;  // byte of the row
-                    uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
-                                   tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
-                    if constexpr (W == 16)
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(join16(e[k][0], e[k][1]), join16(e[k][2], e[k][3]),
-                                                                     join16(e[k][4], e[k][5]), join16(e[k][6], e[k][7]));
-                    else
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(join16(e[k][0], e[k][1]), join16(e[k][2], e[k][3]));
+                for (int c0 = 0; c0 < N; c0 += W) {
+                    uint16_t e[4][W / 2];
+#pragma unroll
+                    for (int c = 0; c < W / 2; ++c) {
+                        const f2 p = pair(ex2(z[c0 + 2 * c]), ex2(z[c0 + 2 * c + 1]));
+                        l[c0 / 2 + c] = add2(l[c0 / 2 + c], p);
+                        const float2 v = both(mul2(p, xw2));
+                        e[0][c] = uint16_t(e4m3x2(v.x, v.y));
+                        const float2 r = minus32(both(mul2(p, xw32)), f16x2_of(e[0][c]));  // exact
+                        uint32_t rest = f16x2(r.x, r.y);
+                        e[1][c] = e4m3x2_of(rest);
+                        rest = rest32(rest, f16x2_of(e[1][c]));
+                        e[2][c] = e4m3x2_of(rest);
+                        e[3][c] = e4m3x2_of(rest32(rest, f16x2_of(e[2][c])));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = j * RB + col0 + c0;  // byte of the row
+                        uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
+                                       tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
+                        const uint32_t w0 = join16(e[j][0], e[j][1]), w1 = join16(e[j][2], e[j][3]);
+                        if constexpr (W == 16)
+                            *reinterpret_cast<uint4 *>(dst) =
+                                make_uint4(w0, w1, join16(e[j][4], e[j][5]), join16(e[j][6], e[j][7]));
+                        else
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+                    }
                 }
-            }
-            if (!whole && grp == 0) {
-                // What no row sees may hold anything, NaN codes too, and 0 * NaN is
-                // NaN: its values become zero.  Positions only some rows see keep
-                // their values but for NaN, which the epilogue gives to those rows.
-                const int pos = v_pos(i, nc), slot = pos % C::kSlots;
-                if (ok) ok = gdn::mbar_wait_bounded(&full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                const bool none = t < rq.lo || t >= rq.len, some = !none && t < lo_last;
-                if (ok && (none || some)) {
+                if (!whole && grp == 0) {
+                    // What no row sees may hold anything, NaN codes too, and 0 * NaN is
+                    // NaN: its values become zero.  Positions only some rows see keep
+                    // their values but for NaN, which the epilogue gives to those rows.
+                    const int pos = ring + v_pos(i, nc), slot = pos % C::kSlots;
+                    if (ok) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                    const bool none = t < g.lo || t >= g.len, some = !none && t < lo_last;
+                    if (ok && (none || some)) {
 #pragma unroll
-                    for (int x = 0; x < C::kAtoms; ++x)
-#pragma unroll
-                        for (int k = 0; k < C::kRow / 16; ++k) {
-                            uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot + x * kTile * C::kRow +
-                                                                 tc::swz8_off<C::kRow>(pos_in, k));
+                        for (int e = 0; e < C::kAtoms * C::kRow / 16; ++e) {
+                            uint4 *p = reinterpret_cast<uint4 *>(
+                                s_ring + slot * C::kSlot + e / (C::kRow / 16) * kTile * C::kRow +
+                                tc::swz8_off<C::kRow>(pos_in, e % (C::kRow / 16)));
                             uint4 w = make_uint4(0, 0, 0, 0);
                             if (some) {
                                 w = *p;
                                 uint32_t *u = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
-                                for (int b = 0; b < 4; ++b)
-                                    u[b] &= ~__vcmpeq4(u[b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                for (int b = 0; b < 4; ++b) u[b] &= ~__vcmpeq4(u[b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                             }
                             *p = w;
                         }
+                    }
                 }
+                gdn::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&s.p_full[y & 1]);
             }
-            gdn::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(&p_full[i & 1]);
-        }
-        // ---- the piece's end
-        if (ok && nc > 0) ok = gdn::mbar_wait_bounded(&pv_done[(nc - 1) & 1], ((nc - 1) >> 1) & 1, a.wait_ns);
-        if (ok && fresh && rq.n > 0) ok = gdn::mbar_wait_bounded(&fv_full, 0, a.wait_ns);
-        const bool bad = *reinterpret_cast<volatile int *>(&bad_page) != 0;  // set before the last tile's scales
-        const bool skip = group_or(grp, !ok || bad);
-        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-        if (bad && pos_in == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
-        tc::fence_after();
-        // sums over the 128 positions
-        float sums[N];
+            // ---- the segment's end
+            if (ok && nc > 0) {
+                const int y = gp + nc - 1;
+                ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], (y >> 1) & 1, a.wait_ns);
+            }
+            if (ok && g.fresh) ok = gdn::mbar_wait_bounded(&s.fv_full, fresh_seen & 1, a.wait_ns);
+            if (group_or(grp, !ok)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            const bool bad = *reinterpret_cast<volatile int *>(&s.bad[k % kQueue]) != 0;
+            if (bad && pos_in == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+            // the next segment's queries, on their way while this one is written
+            ok = gdn::mbar_wait_bounded(&s.seg_full[(k + 1) % kQueue], ((k + 1) / kQueue) & 1, a.wait_ns);
+            if (group_or(grp, !ok)) {
+                ok = false;
+                break;
+            }
+            const Segment h = g;
+            g = s.seg[(k + 1) % kQueue];
+            load_q();
+            // sums over the 128 positions
+            float sums[N];
 #pragma unroll
-        for (int c = 0; c < N / 2; ++c) {
-            sums[2 * c] = both(l[c]).x;
-            sums[2 * c + 1] = both(l[c]).y;
-        }
-        warp_sums<N>(sums, lane);
-        if ((lane & (32 / N - 1)) == 0) col_max[warp & 3][col0 + lane / (32 / N)] = sums[0];
-        group_sync(grp);
-        const bool direct = rq.pieces == 1;
-        const int64_t unit = (int64_t(r) * a.max_pieces + piece) * gridDim.y + blockIdx.y;
-        if (pos_in < N) {
-            const int c = col0 + pos_in;
-            const float sum = (col_max[0][c] + col_max[1][c]) + (col_max[2][c] + col_max[3][c]);
-            if (!direct) {
-                a.ws_ml[unit * RB + c] = make_float2(-col_nm[c], skip ? -1.f : sum);
-            } else if (a.lse && c < cols && !skip) {
-                a.lse[(int64_t(rq.t0) + col_row[c]) * a.c.h_q + hk * a.group + col_head[c]] =
-                    sum == 0.f ? -INFINITY : (log2f(sum) - col_nm[c]) * 0.6931471805599453f;
+            for (int c = 0; c < N / 2; ++c) {
+                sums[2 * c] = both(l[c]).x;
+                sums[2 * c + 1] = both(l[c]).y;
             }
-            col_l[c] = sum == 0.f ? 0.f : 1.f / sum;
-        }
-        group_sync(grp);
-        if (!skip) {
-            const float back = vref / kBase;
-            const int edge = min(min(lo_last, rq.len), (tile0 + nc) * kTile);
+            warp_sums<N>(sums, lane);
+            if ((lane & (32 / N - 1)) == 0) s.col_max[warp & 3][col0 + lane / (32 / N)] = sums[0];
+            group_sync(grp);
+            if (pos_in < N) {
+                const int c = col0 + pos_in;
+                const float sum = (s.col_max[0][c] + s.col_max[1][c]) + (s.col_max[2][c] + s.col_max[3][c]);
+                if (h.out >= 0) {
+                    a.ws_ml[int64_t(h.out) * RB + c] = make_float2(-s.col_nm[c], bad ? -1.f : sum);
+                } else if (a.lse && c < h.cols && !bad) {
+                    a.lse[(int64_t(h.t0) + s.col_row[c]) * a.c.h_q + h.hk * a.group + s.col_head[c]] =
+                        sum == 0.f ? -INFINITY : (log2f(sum) - s.col_nm[c]) * 0.6931471805599453f;
+                }
+                s.col_l[c] = sum == 0.f ? 0.f : 1.f / sum;
+            }
+            group_sync(grp);
+            if (!bad) {
+                const float back = vref / kBase;
+                const int edge = min(min(lo_last, h.len), (h.tile0 + nc) * kTile);
 #pragma unroll 1
-            for (int x = 0; x < C::kAtoms; ++x) {
-                const int e = x * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
-                const bool mine = e < D;
+                for (int at = 0; at < C::kAtoms; ++at) {
+                    const int e = at * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
 #pragma unroll 1
-                for (int c0 = col0; c0 < min(cols, col0 + N); c0 += 8) {
-                    uint32_t w0[8], w1[8], w2[8], w3[8];
-                    float o[8];
-                    if (nc > 0) {
-                        tc::ld8_async(tm_o + lane_base + x * C::kNp + c0, w0);
-                        tc::ld8_async(tm_o + lane_base + x * C::kNp + RB + c0, w1);
-                        tc::ld8_async(tm_o + lane_base + x * C::kNp + 2 * RB + c0, w2);
-                        tc::ld8_async(tm_o + lane_base + x * C::kNp + 3 * RB + c0, w3);
-                        tc::ld_wait();
-                        tc::ld_fence_regs(w0);
-                        tc::ld_fence_regs(w1);
-                        tc::ld_fence_regs(w2);
-                        tc::ld_fence_regs(w3);
+                    for (int c0 = col0; c0 < min(int(h.cols), col0 + N); c0 += 8) {
+                        uint32_t w0[8], w1[8], w2[8], w3[8];
+                        float o[8];
+                        if (nc > 0) {
+                            const uint32_t from = tm_o + lane_base + at * C::kNp + c0;
+                            tc::ld8_async(from, w0);
+                            tc::ld8_async(from + RB, w1);
+                            tc::ld8_async(from + 2 * RB, w2);
+                            tc::ld8_async(from + 3 * RB, w3);
+                            tc::ld_wait();
+                            tc::ld_fence_regs(w0);
+                            tc::ld_fence_regs(w1);
+                            tc::ld_fence_regs(w2);
+                            tc::ld_fence_regs(w3);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const float x = fmaf(__uint_as_float(w3[c]), 1.f / 32.f, __uint_as_float(w2[c]));
+                                o[c] = back * fmaf(fmaf(x, 1.f / 32.f, __uint_as_float(w1[c])), 1.f / 32.f,
+                                                   __uint_as_float(w0[c]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) o[c] = 0.f;
+                        }
+                        if (e >= D) continue;
+                        if (h.fresh) {
+                            int row[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) row[c] = s.col_row[c0 + c];
+                            const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
+                            for (int j = 0; j < h.n; ++j) {
+                                const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
+                                const float4 p0 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0),
+                                             p1 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0 + 4);
+                                const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    o[c] = uint32_t(row[c] - j) < uint32_t(w) ? fmaf(p[c], v, o[c]) : o[c];
+                            }
+                        }
+                        // NaN of positions that only some rows see
+                        for (int t = max(h.lo, h.tile0 * kTile); t < edge; ++t) {
+                            const int page = a.table[int64_t(h.r) * a.table_stride + (t >> shift)];
+                            const uint8_t code =
+                                a.c.kv[int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                                       (int64_t(a.c.h_kv + h.hk) * T + (t & (T - 1))) * D + e];
+                            if ((code & 0x7f) == 0x7f) {
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (c0 + c < h.cols && t >= lo0 + lo1 * s.col_row[c0 + c])
+                                        o[c] = __uint_as_float(0x7fc00000u);
+                            }
+                        }
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const float s = fmaf(__uint_as_float(w3[c]), 1.f / 32.f, __uint_as_float(w2[c]));
-                            o[c] = back * fmaf(fmaf(s, 1.f / 32.f, __uint_as_float(w1[c])), 1.f / 32.f,
-                                               __uint_as_float(w0[c]));
+                            if (c0 + c >= h.cols) break;
+                            if (h.out < 0)
+                                a.o[(int64_t(h.t0) + s.col_row[c0 + c]) * a.o_stride +
+                                    int64_t(h.hk * a.group + s.col_head[c0 + c]) * D + e] =
+                                    gdn::f32_to_bf16(o[c] * s.col_l[c0 + c]);
+                            else
+                                a.ws_o[(int64_t(h.out) * RB + c0 + c) * D + e] = o[c];
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) o[c] = 0.f;
-                    }
-                    if (!mine) continue;
-                    if (fresh) {
-                        int row[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) row[c] = col_row[c0 + c];
-                        const int wdw = a.c.window ? a.c.window : GDN_MAX_ROWS;
-                        for (int j = 0; j < rq.n; ++j) {
-                            const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
-                            const float4 p0 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0),
-                                         p1 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0 + 4);
-                            const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                o[c] = uint32_t(row[c] - j) < uint32_t(wdw) ? fmaf(p[c], v, o[c]) : o[c];
-                        }
-                    }
-                    // NaN of positions that only some rows see
-                    for (int t = max(rq.lo, tile0 * kTile); t < edge; ++t) {
-                        const int page = a.table[int64_t(r) * a.table_stride + (t >> shift)];
-                        const uint8_t code = a.c.kv[int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
-                                                    (int64_t(a.c.h_kv + hk) * T + (t & (T - 1))) * D + e];
-                        if ((code & 0x7f) == 0x7f) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c0 + c < cols && t >= lo0 + lo1 * col_row[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c0 + c >= cols) break;
-                        if (direct)
-                            a.o[(int64_t(rq.t0) + col_row[c0 + c]) * a.o_stride +
-                                int64_t(hk * a.group + col_head[c0 + c]) * D + e] = gdn::f32_to_bf16(o[c] * col_l[c0 + c]);
-                        else
-                            a.ws_o[(unit * RB + c0 + c) * D + e] = o[c];
                     }
                 }
             }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                arrive(&s.seg_empty[k % kQueue]);
+                arrive(&s.epi_done);
+            }
+            gs += nt;
+            gp += nc;
+            ring += 2 * nc;
+            fresh_seen += h.fresh;
+            // the other groups are done with the columns' numbers too
+            ok = gdn::mbar_wait_bounded(&s.epi_done, k & 1, a.wait_ns);
+            if (group_or(grp, !ok)) {
+                ok = false;
+                break;
+            }
         }
+        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
         tc::fence_before();
     }
     __syncthreads();
@@ -883,11 +950,12 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     }
 }
 
-// Joins a request's pieces: o = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
-// Groups of d/4 threads; a CTA takes `per_cta` columns of a (request, kv head,
-// block).  With few pieces a group joins a column by itself; with many the
+// Joins a unit's pieces: o = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  Groups of
+// d/4 threads.  With few pieces a group joins a column by itself; with many the
 // groups share one column's pieces, so that their loads are in flight together.
 // Which of the two, and so the order of the sums, goes by the pieces alone.
+// Free cuts: a CTA for each part, the parts of a unit sharing its columns.  Given
+// cuts: a CTA for each `per_cta` columns of a unit.
 constexpr int kJoin = 512;
 
 template <int D>
@@ -895,38 +963,74 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
                                                          const int per_cta) {
     gdn::pdl_enter();
     constexpr int W = D / 4, G = kJoin / W;
-    const int hk = blockIdx.y / a.blocks, blk = blockIdx.y % a.blocks, r = blockIdx.z, tid = threadIdx.x;
+    const int tid = threadIdx.x;
+    // the partial sums of a call in which a wait ran out are not to be trusted
+    if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
+    int r, y, begin, end, by;
+    Pieces pieces;
+    if (a.pinned) {
+        r = blockIdx.z;
+        y = blockIdx.y;
+        pieces.base = pieces.first = int64_t(r) * a.max_pieces * gridDim.y + y;
+        pieces.step = gridDim.y;
+        begin = blockIdx.x * per_cta;
+        end = begin + per_cta;
+        by = 1;
+    } else {
+        const Part p = a.parts[2 * blockIdx.y + blockIdx.x];
+        if (p.count <= 1) return;
+        r = p.r;
+        y = p.y;
+        pieces.count = p.count;
+        pieces.first = 2 * p.owner + 1;
+        pieces.base = 2 * p.owner;
+        pieces.step = 2;
+        begin = int(blockIdx.y) - p.owner;
+        end = RB;
+        by = p.count;
+    }
     const Request rq = request_of(a, r);
-    if (rq.bad || rq.pieces <= 1) return;
-    const int begin = blockIdx.x * per_cta, end = min(min(RB, rq.n * a.group - blk * RB), begin + per_cta);
-    const int64_t unit0 = int64_t(r) * a.max_pieces * gridDim.y + blockIdx.y;
-    __shared__ float s_l[G];
+    if (rq.bad) return;
+    if (a.pinned) {
+        pieces.count = (rq.tiles + a.piece_tiles - 1) / a.piece_tiles;
+        if (pieces.count <= 1) return;
+    }
+    const int hk = y / a.blocks, blk = y % a.blocks;
+    end = min(end, min(RB, rq.n * a.group - blk * RB));
+    __shared__ float s_l[G], s_m[kJoin / 32];
     __shared__ float4 s_o[G][W];
-    const int g = tid / W, e = tid % W;
-    const bool few = rq.pieces <= 8;
-    const int step = few ? G : 1, ps = few ? 1 : G, p0 = few ? 0 : g;
-    for (int c = begin + (few ? g : 0); c < end; c += step) {
-        const float2 *ml0 = a.ws_ml + unit0 * RB + c;
-        const int64_t ml_step = int64_t(gridDim.y) * RB;
+    const int g = tid / W, e = tid % W, count = pieces.count;
+    const bool few = count <= 8;
+    const int step = few ? G * by : by, ps = few ? 1 : G, p0 = few ? 0 : g;
+    for (int c = begin + (few ? g * by : 0); c < end; c += step) {
+        const float2 *ml = a.ws_ml + c;
         float m = -INFINITY;
         bool skip = false;
-#pragma unroll 8
-        for (int s = 0; s < rq.pieces; ++s) {
-            const float2 ml = ml0[s * ml_step];
-            m = fmaxf(m, ml.x);
-            skip |= ml.y < 0.f;
+        for (int s = few ? 0 : tid; s < count; s += few ? 1 : kJoin) {
+            const float2 x = ml[pieces.at(s) * RB];
+            m = fmaxf(m, x.x);
+            skip |= x.y < 0.f;  // a piece was refused
         }
-        if (skip) return;  // a piece was refused: so for every thread of the request
+        if (!few) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            __syncthreads();  // the last column's sums are read
+            if ((tid & 31) == 0) s_m[tid >> 5] = m;
+            skip = __syncthreads_or(skip);
+#pragma unroll
+            for (int k = 0; k < kJoin / 32; ++k) m = fmaxf(m, s_m[k]);
+        }
+        if (skip) return;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f;
 #pragma unroll 4
-        for (int s = p0; s < rq.pieces; s += ps) {
-            const float2 ml = ml0[s * ml_step];
-            const float4 o =
-                __ldcs(reinterpret_cast<const float4 *>(a.ws_o + ((unit0 + int64_t(s) * gridDim.y) * RB + c) * D) + e);
-            const float f = ex2(ml.x - m);
-            if (ml.y != 0.f) {  // else the row sees nothing of the piece
-                l = fmaf(f, ml.y, l);
+        for (int s = p0; s < count; s += ps) {
+            const int64_t at = pieces.at(s) * RB;
+            const float2 x = ml[at];
+            const float4 o = __ldcs(reinterpret_cast<const float4 *>(a.ws_o + (at + c) * D) + e);
+            const float f = ex2(x.x - m);
+            if (x.y != 0.f) {  // else the row sees nothing of the piece
+                l = fmaf(f, x.y, l);
                 acc.x = fmaf(f, o.x, acc.x);
                 acc.y = fmaf(f, o.y, acc.y);
                 acc.z = fmaf(f, o.z, acc.z);
@@ -934,7 +1038,6 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
             }
         }
         if (!few) {
-            __syncthreads();  // the last column's sums are read
             s_o[g][e] = acc;
             if (e == 0) s_l[g] = l;
             __syncthreads();
@@ -991,11 +1094,12 @@ bool encode_pages(CUtensorMap *m, const kv8_cache *c, int layer) {
 }
 
 struct Plan {
-    int rb, blocks, piece_tiles, max_pieces;
+    int rb, blocks, pinned, piece_tiles, max_pieces, ctas;
+    int64_t parts;  // of the workspace
 };
 
 Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, int32_t split_tokens) {
-    Plan p;
+    Plan p{};
     const int64_t cols = int64_t(max_rows) * (c->h_q / c->h_kv);
     const int most = c->d == 256 ? 32 : 64;
     p.rb = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || most == 32 ? 32 : 64;
@@ -1003,37 +1107,41 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
     // positions a request's rows can see, and the tiles they may lie in
     int64_t seen = max_len;
     if (c->window && c->window < seen) seen = int64_t(c->window) + kTile;
-    const int64_t tiles = (seen + kTile - 1) / kTile;
+    int64_t tiles = (seen + kTile - 1) / kTile;
+    if (tiles < 1) tiles = 1;
     const int64_t units = int64_t(B) * c->h_kv * p.blocks;
     const int64_t slots = 152 * (c->d == 256 || p.rb == 64 ? 1 : 2);
-    int64_t t;
-    if (split_tokens > 0)
-        t = (int64_t(split_tokens) + kTile - 1) / kTile;
-    else
-        t = (tiles * units + slots - 1) / slots;  // one wave
-    if (split_tokens <= 0 && t > 32) t = 32;
-    if (t > tiles) t = tiles;
-    if (t < 1) t = 1;
-    p.piece_tiles = int(t);
-    p.max_pieces = int(tiles > 0 ? (tiles + t - 1) / t : 1);
+    int64_t ctas;
+    if (split_tokens > 0 || tiles <= kWhole) {
+        // given cuts, or none in units so short that joining costs more than it gives
+        const int64_t t = split_tokens > 0 ? (int64_t(split_tokens) + kTile - 1) / kTile : tiles;
+        p.pinned = 1;
+        p.piece_tiles = int(t < tiles ? t : tiles);
+        p.max_pieces = int((tiles + p.piece_tiles - 1) / p.piece_tiles);
+        ctas = units * p.max_pieces;
+        p.parts = p.max_pieces > 1 ? ctas : 0;
+    } else {
+        p.piece_tiles = p.max_pieces = 1;
+        ctas = (units * (tiles + 1) + 3) / 4;
+    }
+    p.ctas = int(ctas < slots ? ctas : slots);
+    if (!p.pinned) p.parts = p.ctas > 1 ? 2 * int64_t(p.ctas) : 0;
     return p;
 }
 
 template <int D, int RB>
-int launch(const AttendArgs &a, dim3 grid, cudaStream_t st) {
+int launch(const AttendArgs &a, int ctas, cudaStream_t st) {
     using C = Cfg<D, RB>;
     static const cudaError_t set = cudaFuncSetAttribute(kv8_attend_kernel<D, RB>,
                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (set != cudaSuccess) return GDN_ERR_CUDA;
-    return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, grid, dim3(C::kThreads), C::kSmem, st, a);
+    return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, dim3(unsigned(ctas)), dim3(C::kThreads), C::kSmem, st, a);
 }
 
 }  // namespace
 
-static size_t ws_bytes(const kv8_cache *c, int32_t B, const Plan &p) {
-    if (p.max_pieces <= 1) return 0;
-    const size_t cols = size_t(B) * p.max_pieces * c->h_kv * p.blocks * p.rb;
-    return cols * (size_t(c->d) * 4 + 8);
+static size_t ws_bytes(const kv8_cache *c, const Plan &p) {
+    return size_t(p.parts) * p.rb * (size_t(c->d) * 4 + 8) + (p.pinned ? 0 : size_t(p.parts) * sizeof(Part));
 }
 
 extern "C" size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t max_len, int32_t max_rows,
@@ -1041,7 +1149,7 @@ extern "C" size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, 
     if (gdn_host::kv8_check(cache) != GDN_OK || B <= 0 || max_len < 0 || max_len > gdn_host::kKv8MaxLen ||
         max_rows <= 0 || max_rows > GDN_MAX_ROWS || split_tokens < 0)
         return 0;
-    return ws_bytes(cache, B, plan_of(cache, B, max_len, max_rows, split_tokens));
+    return ws_bytes(cache, plan_of(cache, B, max_len, max_rows, split_tokens));
 }
 
 extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
@@ -1065,7 +1173,8 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
                   !gdn_host::kv8_rows_ok(v_new, v_stride, cache->h_kv, cache->d)))
         return GDN_ERR_ARG;
     const Plan p = plan_of(cache, B, max_len, max_rows, split_tokens);
-    const size_t need = ws_bytes(cache, B, p);
+    const size_t need = ws_bytes(cache, p);
+    if (p.parts > (int64_t(1) << 30)) return GDN_ERR_ARG;
     if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (need && !gdn_host::aligned16(workspace)) return GDN_ERR_ARG;
     if (int64_t(cache->h_kv) * p.blocks > 65535) return GDN_ERR_ARG;
@@ -1081,6 +1190,7 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.max_rows = max_rows;
     a.group = cache->h_q / cache->h_kv;
     a.blocks = p.blocks;
+    a.pinned = p.pinned;
     a.piece_tiles = p.piece_tiles;
     a.max_pieces = p.max_pieces;
     a.page_shift = 31 - __builtin_clz(unsigned(cache->page_tokens));
@@ -1096,36 +1206,41 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.o_stride = o_stride;
     a.o = o;
     a.lse = lse;
-    a.ws_o = static_cast<float *>(workspace);
-    a.ws_ml = need ? reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
-                                                need / (size_t(cache->d) * 4 + 8) * (size_t(cache->d) * 4))
-                   : nullptr;
+    if (p.parts) {
+        const size_t columns = size_t(p.parts) * p.rb;
+        a.ws_o = static_cast<float *>(workspace);
+        a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + columns * cache->d);
+        if (!p.pinned) a.parts = reinterpret_cast<Part *>(a.ws_ml + columns);
+    }
     a.status = dev_status;
     a.wait_ns = gdn::kWaitLimitNs;
-    const dim3 grid(unsigned(p.max_pieces), unsigned(cache->h_kv * p.blocks), unsigned(B));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc = GDN_ERR_SHAPE;
     const int key = cache->d * 100 + p.rb;
     switch (key) {
-        case 6408: rc = launch<64, 8>(a, grid, st); break;
-        case 6416: rc = launch<64, 16>(a, grid, st); break;
-        case 6432: rc = launch<64, 32>(a, grid, st); break;
-        case 6464: rc = launch<64, 64>(a, grid, st); break;
-        case 12808: rc = launch<128, 8>(a, grid, st); break;
-        case 12816: rc = launch<128, 16>(a, grid, st); break;
-        case 12832: rc = launch<128, 32>(a, grid, st); break;
-        case 12864: rc = launch<128, 64>(a, grid, st); break;
-        case 25608: rc = launch<256, 8>(a, grid, st); break;
-        case 25616: rc = launch<256, 16>(a, grid, st); break;
-        case 25632: rc = launch<256, 32>(a, grid, st); break;
+        case 6408: rc = launch<64, 8>(a, p.ctas, st); break;
+        case 6416: rc = launch<64, 16>(a, p.ctas, st); break;
+        case 6432: rc = launch<64, 32>(a, p.ctas, st); break;
+        case 6464: rc = launch<64, 64>(a, p.ctas, st); break;
+        case 12808: rc = launch<128, 8>(a, p.ctas, st); break;
+        case 12816: rc = launch<128, 16>(a, p.ctas, st); break;
+        case 12832: rc = launch<128, 32>(a, p.ctas, st); break;
+        case 12864: rc = launch<128, 64>(a, p.ctas, st); break;
+        case 25608: rc = launch<256, 8>(a, p.ctas, st); break;
+        case 25616: rc = launch<256, 16>(a, p.ctas, st); break;
+        case 25632: rc = launch<256, 32>(a, p.ctas, st); break;
         default: break;
     }
-    if (rc != GDN_OK || p.max_pieces <= 1) return rc;
-    // as many columns a CTA as still leave four CTAs for each SM
-    const int64_t columns = int64_t(B) * grid.y * p.rb;
-    const int per = int(columns / (4 * 152) < 1 ? 1 : columns / (4 * 152) > p.rb ? p.rb : columns / (4 * 152));
-    const dim3 jgrid{unsigned((p.rb + per - 1) / per), grid.y, unsigned(B)};
-    if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
-    if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
-    return gdn_host::launch_pdl(kv8_join_kernel<256>, jgrid, dim3(kJoin), 0, st, a, p.rb, per);
+    if (rc != GDN_OK || !p.parts) return rc;
+    dim3 grid(2, unsigned(p.ctas));
+    int per = 1;
+    if (p.pinned) {
+        // as many columns a CTA as still leave four CTAs for each SM
+        const int64_t units = int64_t(B) * cache->h_kv * p.blocks, each = units * p.rb / (4 * 152);
+        per = int(each < 1 ? 1 : each > p.rb ? p.rb : each);
+        grid = dim3(unsigned((p.rb + per - 1) / per), unsigned(cache->h_kv * p.blocks), unsigned(B));
+    }
+    if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, grid, dim3(kJoin), 0, st, a, p.rb, per);
+    if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, grid, dim3(kJoin), 0, st, a, p.rb, per);
+    return gdn_host::launch_pdl(kv8_join_kernel<256>, grid, dim3(kJoin), 0, st, a, p.rb, per);
 }

@@ -1,0 +1,189 @@
+// Arithmetic of the attention over the 8-bit cache: pairs of fp32 and fp16
+// values, and rows split into e4m3 parts (sm_103a).
+#pragma once
+
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace kv8 {
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Barrier of a group's four softmax warps with an OR over a predicate.
+__device__ __forceinline__ bool group_or(int group, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, "
+        "q;\n}\n"
+        : "=r"(r)
+        : "r"(uint32_t(p)), "r"(group + 1)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// Pairs of fp32 values: one instruction an operation.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pair(uint32_t a, uint32_t b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// c - 32 h of two fp32 values c and two fp16 values h.
+__device__ __forceinline__ float2 minus32(float2 c, uint32_t h) {
+    float2 r;
+    asm("{\n .reg .b16 a, b, k;\n mov.b32 {a, b}, %2;\n mov.b16 k, 0xd000;\n fma.rn.f32.f16 %0, a, k, %3;\n"
+        " fma.rn.f32.f16 %1, b, k, %4;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(h), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) {
+    uint32_t r;
+    asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
+    return r;
+}
+
+// fp16 pair arithmetic of the splits.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint16_t e4m3x2_of(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+// (h - back) * 32 of two fp16 values: exact, `back` being h to 4 bits.
+__device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t back) {
+    uint32_t t, r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(h), "r"(0x50005000u));              // 32, 32
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(back), "r"(0xd000d000u), "r"(t));  // -32, -32
+    return r;
+}
+
+// A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
+// into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a
+// row that is not finite.
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, uint4 (&w)[D / 64]) {
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+        w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * (D / 8) + e * 8) : make_uint4(0, 0, 0, 0);
+}
+template <int D>
+__device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl) {
+    constexpr int E = D / 8, kRow = D < 128 ? D : 128;
+    float m = 0.f, x[E];
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
+            x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const bool f = fabsf(x[e]) < INFINITY;
+        finite &= f;
+        x[e] = f ? x[e] : 0.f;
+        m = fmaxf(m, fabsf(x[e]));
+    }
+    uint32_t top = __float_as_uint(m);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (threadIdx.x & 24)) & 0xffu;
+    const int k = max(-110, min(110, 7 - (int(top >> 23) - 127)));  // largest in [128, 256)
+    const float up = pow2i(k), up32 = up * 32.f, down = pow2i(-k);
+#pragma unroll
+    for (int b = 0; b < E / 8; ++b) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t hh[2], ll[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x0 = x[b * 8 + g * 4 + 2 * i], x1 = x[b * 8 + g * 4 + 2 * i + 1];
+                hh[i] = e4m3x2(x0 * up, x1 * up);
+                const float2 back = f32x2_of(uint16_t(hh[i]));
+                ll[i] = e4m3x2(fmaf(back.x, -32.f, x0 * up32), fmaf(back.y, -32.f, x1 * up32));
+            }
+            h[g] = hh[0] | (hh[1] << 16);
+            l[g] = ll[0] | (ll[1] << 16);
+        }
+        const int e0 = sub * E + b * 8, atom = e0 / kRow, in = e0 % kRow;
+        uint8_t *t = tile + atom * rows * kRow + (in & 8);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
+    }
+    return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
+}
+
+// Sums of N values over a warp's lanes: value k's sum lands in v[0] of the
+// lanes whose top log2(N) bits are k.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
+    constexpr int kSteps = N == 16 ? 4 : 3;
+    static_assert(N == 16 || N == 8, "columns a thread");
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int off = 16 >> s, half = N >> (s + 1);
+        const bool up = lane & off;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+#pragma unroll
+    for (int off = 16 >> kSteps; off; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+}
+
+}  // namespace kv8
