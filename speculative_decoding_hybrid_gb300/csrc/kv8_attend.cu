@@ -19,7 +19,7 @@
 // that is once, at a segment's first tile.  One vote a tile decides.
 //
 // Work is measured in tiles of 128 positions: a unit (request, kv head, block of
-// RB columns) costs its tiles plus one, and the units laid end to end are cut
+// RB columns) costs its tiles plus kUnit, and the units laid end to end are cut
 // into equal ranges, one for each of the persistent CTAs.  A CTA runs the units
 // and parts of units of its range as segments.  Its warps:
 //   copy     finds the segments, queues them, and moves pages (tiled TMA, K and V
@@ -49,6 +49,7 @@ constexpr float kBase = 4.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
+constexpr int kUnit = 4;        // tiles that a unit's queries, new rows and outputs cost as much as
 constexpr int kWhole = 8;       // units of so few tiles are not cut
 
 // A part of a unit cut by the ranges: which unit, and the CTAs owner .. owner +
@@ -81,11 +82,14 @@ struct Request {
     int t0, n, len, lo, tiles;  // lo: first position any row sees; tiles from lo / 128 on
     bool bad;
 };
-__device__ __forceinline__ Request request_of(const AttendArgs &a, int r) {
+__device__ __forceinline__ int3 rows_of(const AttendArgs &a, int r) {
+    return make_int3(a.cu_rows[r], a.cu_rows[r + 1], a.cache_len[r]);
+}
+__device__ __forceinline__ Request request_of(const AttendArgs &a, int3 x) {
     Request q;
-    q.t0 = a.cu_rows[r];
-    q.n = a.cu_rows[r + 1] - q.t0;
-    q.len = a.cache_len[r];
+    q.t0 = x.x;
+    q.n = x.y - x.x;
+    q.len = x.z;
     q.bad = q.t0 < 0 || q.n < 0 || q.n > a.max_rows || int64_t(q.t0) + q.n > a.row_capacity || q.len < 0 ||
             q.len > a.max_len || int64_t(q.len) > int64_t(a.table_pages) * a.c.page_tokens;
     const int w = a.c.window;
@@ -123,7 +127,7 @@ struct Cfg {
     // groups of four softmax warps, each with its share of the columns: a warp
     // waits on its own chain of loads, exponentials and conversions most of the
     // time, so an SM wants at least eight of them
-    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : RB / 16;
+    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : 2;
     static constexpr int kCols = RB / kGroups;           // columns a thread
     static constexpr int kSoft = 128 * kGroups;          // softmax threads
     static constexpr int kThreads = kSoft + 64;
@@ -160,7 +164,9 @@ struct Shared {
     int bad[kQueue];
     long long start_at;
     int start_r;
+    int3 start_rows;
     uint32_t tmem;
+    int col_out[RB];                    // element of o, from the request's first row on
     uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
 };
 
@@ -171,17 +177,22 @@ __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n -
 
 __device__ __forceinline__ long long weight_of(const AttendArgs &a, const Request &q, int rb) {
     if (q.bad || q.n == 0) return 0;
-    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + 1);
+    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + kUnit);
+}
+
+// a / b and a * b / c for values that are usually small.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return a < (1ll << 32) ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
 // Where a range's end at x falls in a unit of `tiles` tiles: 0 its start, tiles
-// + 1 its end.  Free cuts leave no part of fewer than kLeast tiles.
+// + kUnit its end.  Free cuts leave no part of fewer than kLeast tiles.
 __device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles) {
     if (x <= 0) return 0;
-    if (x > tiles) return tiles + 1;
-    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + 1 : int(x);
-    const long long y = (x + a.piece_tiles - 1) / a.piece_tiles * a.piece_tiles;
-    return y >= tiles ? tiles + 1 : int(y);
+    if (x > tiles) return tiles + kUnit;
+    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + kUnit : int(x);
+    const int y = (int(x) + a.piece_tiles - 1) / a.piece_tiles * a.piece_tiles;
+    return y >= tiles ? tiles + kUnit : y;
 }
 
 template <int D, int RB>
@@ -203,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         const int chunk = (a.B + C::kThreads - 1) / C::kThreads, r0 = tid * chunk, r1 = min(a.B, r0 + chunk);
         long long mine = 0;
         for (int r = r0; r < r1; ++r) {
-            const Request q = request_of(a, r);
+            const Request q = request_of(a, rows_of(a, r));
             mine += weight_of(a, q, RB);
             if (q.bad && blockIdx.x == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
         }
@@ -223,20 +234,22 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             total += s.scan[w];
         }
         // free cuts: at least four tiles a range, so that none is empty inside a unit
-        const long long most = a.pinned ? total : total / 4;
+        const long long most = a.pinned ? quotient(total, kUnit) : total / 4;
         ctas = int(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
         const int cta = blockIdx.x;
         if (tid == 0 && a.parts) a.parts[2 * cta].count = a.parts[2 * cta + 1].count = 0;
         if (cta >= ctas || total == 0) return;
-        begin = total * cta / ctas;
-        end = total * (cta + 1) / ctas;
+        begin = quotient(total * cta, ctas);
+        end = quotient(total * (cta + 1), ctas);
         incl += before;
         if (incl - mine <= begin && begin < incl) {
             long long at = incl - mine;
             for (int r = r0; r < r1; ++r) {
-                const long long w = weight_of(a, request_of(a, r), RB);
+                const int3 x = rows_of(a, r);
+                const long long w = weight_of(a, request_of(a, x), RB);
                 if (at + w > begin) {
                     s.start_r = r;
+                    s.start_rows = x;
                     s.start_at = at;
                     break;
                 }
@@ -390,13 +403,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         };
         int r = s.start_r;
         long long at = s.start_at;
-        Request q = request_of(a, r);
+        Request q = request_of(a, s.start_rows);
         while (at < end && ok) {
-            const Request next = request_of(a, min(r + 1, a.B - 1));
+            const int3 next = rows_of(a, min(r + 1, a.B - 1));  // looked at when its turn comes
             const long long w = weight_of(a, q, RB);
             if (w > 0) {
-                const int cost = q.tiles + 1, nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
-                for (int u = begin > at ? int((begin - at) / cost) : 0; u < units && at + (long long)u * cost < end && ok;
+                const int cost = q.tiles + kUnit, nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
+                for (int u = begin > at ? int(quotient(begin - at, cost)) : 0; u < units && at + (long long)u * cost < end && ok;
                      ++u) {
                     const long long su = at + (long long)u * cost;
                     const int x0 = cut_at(a, begin - su, q.tiles), x1 = cut_at(a, end - su, q.tiles);
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     // given cuts: a segment for each piece of the range
                     for (int x = x0; x < x1 && ok;) {
                         int to = a.pinned ? min(x + a.piece_tiles, x1) : x1;
-                        if (to >= q.tiles) to = cost;
+                        if (to >= q.tiles) to = cost;  // with the new rows and the end
                         g.tile0 = q.lo / kTile + x;
                         g.nc = min(to, q.tiles) - x;
                         g.fresh = a.k != nullptr && to == cost;
@@ -439,8 +452,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             }
             at += w;
             ++r;
-            q = next;
             if (r >= a.B) break;
+            q = request_of(a, next);
         }
         if (ok) {
             Segment g = {};
@@ -553,33 +566,40 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         __syncwarp();
     } else {
         // ---- softmax.  This thread's position in a tile and its columns col0 .. col0 + N - 1;
-        // eight threads bring a column's queries (columns fill whole warps).
-        constexpr int N = C::kCols;
-        static_assert(RB <= C::kSoft / 8, "a thread has one column");
+        // eight threads bring a column's queries (columns fill whole warps), kQs columns each.
+        constexpr int N = C::kCols, kQs = (RB * 8 + C::kSoft - 1) / C::kSoft;
         const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N, cq = tid >> 3, sub = tid & 7;
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
         bool ok = gdn::mbar_wait_bounded(&s.seg_full[0], 0, a.wait_ns);
         if (group_or(grp, !ok)) ok = false;
         Segment g = s.seg[0];
         if (!ok) g.cols = 0;
-        uint4 wq[D / 64];
+        uint4 wq[kQs][D / 64];
         auto load_q = [&] {
-            const int x = g.blk * RB + cq;
-            if (cq < RB)
-                load_row<D>(a.q + (int64_t(g.t0) + x / a.group) * a.q_stride + int64_t(g.hk * a.group + x % a.group) * D,
-                            sub, cq < g.cols, wq);
+#pragma unroll
+            for (int i = 0; i < kQs; ++i) {
+                const int c = cq + i * (C::kSoft / 8), x = g.blk * RB + c, row = x / a.group;
+                if (c < RB)
+                    load_row<D>(a.q + (int64_t(g.t0) + row) * a.q_stride +
+                                    int64_t(g.hk * a.group + x - row * a.group) * D,
+                                sub, c < g.cols, wq[i]);
+            }
         };
         load_q();
         int gs = 0, gp = 0, ring = 0, fresh_seen = 0;  // score and weight tiles, ring positions, fresh tiles so far
         for (int k = 0; g.cols > 0; ++k) {
-            if (cq < RB) {
-                const int x = g.blk * RB + cq;
-                const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq);
+#pragma unroll
+            for (int i = 0; i < kQs; ++i) {
+                const int c = cq + i * (C::kSoft / 8);
+                if (c >= RB) break;
+                const float down = split_row<D>(wq[i], sub, s_q, C::kNs, c, RB + c);
                 if (sub == 0) {
-                    s.col_nm[cq] = -kUnset;
-                    s.col_coef[cq] = a.c.sm_scale * 1.4426950408889634f * down;
-                    s.col_row[cq] = uint8_t(x / a.group);
-                    s.col_head[cq] = uint8_t(x % a.group);
+                    const int x = g.blk * RB + c, row = x / a.group, head = x - row * a.group;
+                    s.col_nm[c] = -kUnset;
+                    s.col_coef[c] = a.c.sm_scale * 1.4426950408889634f * down;
+                    s.col_row[c] = uint8_t(row);
+                    s.col_head[c] = uint8_t(head);
+                    s.col_out[c] = row * int(a.o_stride) + (g.hk * a.group + head) * D;
                 }
             }
             gdn::fence_proxy_async_smem();
@@ -615,7 +635,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 auto load_z = [&](bool plain) {
                     uint32_t hi[N], lo[N];
                     const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
-                    if constexpr (N == 16) {
+                    if constexpr (N == 32) {
+                        tc::ld32_async(at, hi);
+                        tc::ld32_async(at + RB, lo);
+                    } else if constexpr (N == 16) {
                         tc::ld16_async(at, hi);
                         tc::ld16_async(at + RB, lo);
                     } else {
@@ -852,6 +875,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             group_sync(grp);
             if (!bad) {
                 const float back = vref / kBase;
+                uint16_t *o_base = a.o + int64_t(h.t0) * a.o_stride;
+                float *ws_base = a.ws_o + int64_t(h.out) * RB * D;
                 const int edge = min(min(lo_last, h.len), (h.tile0 + nc) * kTile);
 #pragma unroll 1
                 for (int at = 0; at < C::kAtoms; ++at) {
@@ -859,7 +884,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 #pragma unroll 1
                     for (int c0 = col0; c0 < min(int(h.cols), col0 + N); c0 += 8) {
                         uint32_t w0[8], w1[8], w2[8], w3[8];
-                        float o[8];
+                        f2 acc[4] = {0, 0, 0, 0};
                         if (nc > 0) {
                             const uint32_t from = tm_o + lane_base + at * C::kNp + c0;
                             tc::ld8_async(from, w0);
@@ -871,31 +896,45 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             tc::ld_fence_regs(w1);
                             tc::ld_fence_regs(w2);
                             tc::ld_fence_regs(w3);
+                            const f2 part = pair(1.f / 32.f, 1.f / 32.f), b2 = pair(back, back);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float x = fmaf(__uint_as_float(w3[c]), 1.f / 32.f, __uint_as_float(w2[c]));
-                                o[c] = back * fmaf(fmaf(x, 1.f / 32.f, __uint_as_float(w1[c])), 1.f / 32.f,
-                                                   __uint_as_float(w0[c]));
+                            for (int c = 0; c < 4; ++c) {
+                                f2 x = fma2(pair(w3[2 * c], w3[2 * c + 1]), part, pair(w2[2 * c], w2[2 * c + 1]));
+                                x = fma2(x, part, pair(w1[2 * c], w1[2 * c + 1]));
+                                acc[c] = mul2(b2, fma2(x, part, pair(w0[2 * c], w0[2 * c + 1])));
                             }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) o[c] = 0.f;
                         }
                         if (e >= D) continue;
-                        if (h.fresh) {
-                            int row[8];
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) row[c] = s.col_row[c0 + c];
-                            const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
+                        uint32_t odd = 0;  // new rows whose value here is not finite
+                        if (h.fresh)
                             for (int j = 0; j < h.n; ++j) {
-                                const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
-                                const float4 p0 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0),
-                                             p1 = *reinterpret_cast<const float4 *>(fresh_p + j * RB + c0 + 4);
-                                const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    o[c] = uint32_t(row[c] - j) < uint32_t(w) ? fmaf(p[c], v, o[c]) : o[c];
+                                const uint32_t b = uint32_t(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]) << 16;
+                                const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+                                if (!finite) odd |= 1u << j;
+                                const f2 v = pair(finite ? b : 0u, finite ? b : 0u);
+                                const ulonglong2 p0 = *reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0),
+                                                 p1 = *reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0 + 4);
+                                acc[0] = fma2(p0.x, v, acc[0]);
+                                acc[1] = fma2(p0.y, v, acc[1]);
+                                acc[2] = fma2(p1.x, v, acc[2]);
+                                acc[3] = fma2(p1.y, v, acc[3]);
                             }
+                        float o[8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            o[2 * c] = both(acc[c]).x;
+                            o[2 * c + 1] = both(acc[c]).y;
+                        }
+                        if (odd) {  // such a value reaches the rows that see it, and no others
+                            const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
+                            for (int j = 0; j < h.n; ++j)
+                                if (odd >> j & 1) {
+                                    const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c)
+                                        if (uint32_t(s.col_row[c0 + c] - j) < uint32_t(w))
+                                            o[c] = fmaf(fresh_p[j * RB + c0 + c], v, o[c]);
+                                }
                         }
                         // NaN of positions that only some rows see
                         for (int t = max(h.lo, h.tile0 * kTile); t < edge; ++t) {
@@ -914,11 +953,9 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         for (int c = 0; c < 8; ++c) {
                             if (c0 + c >= h.cols) break;
                             if (h.out < 0)
-                                a.o[(int64_t(h.t0) + s.col_row[c0 + c]) * a.o_stride +
-                                    int64_t(h.hk * a.group + s.col_head[c0 + c]) * D + e] =
-                                    gdn::f32_to_bf16(o[c] * s.col_l[c0 + c]);
+                                o_base[s.col_out[c0 + c] + e] = gdn::f32_to_bf16(o[c] * s.col_l[c0 + c]);
                             else
-                                a.ws_o[(int64_t(h.out) * RB + c0 + c) * D + e] = o[c];
+                                ws_base[(c0 + c) * D + e] = o[c];
                         }
                     }
                 }
@@ -989,7 +1026,7 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
         end = RB;
         by = p.count;
     }
-    const Request rq = request_of(a, r);
+    const Request rq = request_of(a, rows_of(a, r));
     if (rq.bad) return;
     if (a.pinned) {
         pieces.count = (rq.tiles + a.piece_tiles - 1) / a.piece_tiles;
@@ -1122,7 +1159,7 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
         p.parts = p.max_pieces > 1 ? ctas : 0;
     } else {
         p.piece_tiles = p.max_pieces = 1;
-        ctas = (units * (tiles + 1) + 3) / 4;
+        ctas = (units * (tiles + kUnit) + 3) / 4;
     }
     p.ctas = int(ctas < slots ? ctas : slots);
     if (!p.pinned) p.parts = p.ctas > 1 ? 2 * int64_t(p.ctas) : 0;
@@ -1169,6 +1206,7 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     if (!gdn_host::kv8_rows_ok(q, q_stride, cache->h_q, cache->d) ||
         !gdn_host::kv8_rows_ok(o, o_stride, cache->h_q, cache->d))
         return GDN_ERR_ARG;
+    if (o_stride > (1 << 26)) return GDN_ERR_ARG;  // a request's outputs are indexed with 32 bits
     if (k_new && (!gdn_host::kv8_rows_ok(k_new, k_stride, cache->h_kv, cache->d) ||
                   !gdn_host::kv8_rows_ok(v_new, v_stride, cache->h_kv, cache->d)))
         return GDN_ERR_ARG;

@@ -108,7 +108,7 @@ __device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t back) {
 
 // A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
 // into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a
-// row that is not finite.
+// row that is not finite (whatever its parts then are: a row's products are its own).
 template <int D>
 __device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, uint4 (&w)[D / 64]) {
 #pragma unroll
@@ -118,60 +118,60 @@ __device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, 
 template <int D>
 __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl) {
     constexpr int E = D / 8, kRow = D < 128 ? D : 128;
-    float m = 0.f, x[E];
-    bool finite = true;
+    // magnitudes order like their bits; infinities and NaN come out on top
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < E / 8; ++e) {
+        m = __vmaxu2(m, __vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu));
+        m = __vmaxu2(m, __vmaxu2(w[e].z & 0x7fff7fffu, w[e].w & 0x7fff7fffu));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t top = max(m >> 16, m & 0xffffu);
+    const int k = max(-110, min(110, 7 - (int(top >> 7) - 127)));  // largest in [128, 256)
+    const f2 up = pair(pow2i(k), pow2i(k)), up32 = pair(32.f * pow2i(k), 32.f * pow2i(k));
+    uint32_t h[E / 4], l[E / 4];
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
         const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+        uint16_t hh[4], ll[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[e * 8 + 2 * i] = __uint_as_float(u[i] << 16);
-            x[e * 8 + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            const f2 x = pair(u[i] << 16, u[i] & 0xffff0000u);
+            const float2 a = both(mul2(x, up));
+            hh[i] = uint16_t(e4m3x2(a.x, a.y));
+            const float2 r = minus32(both(mul2(x, up32)), f16x2_of(hh[i]));
+            ll[i] = uint16_t(e4m3x2(r.x, r.y));
+        }
+        h[2 * e] = join16(hh[0], hh[1]);
+        h[2 * e + 1] = join16(hh[2], hh[3]);
+        l[2 * e] = join16(ll[0], ll[1]);
+        l[2 * e + 1] = join16(ll[2], ll[3]);
+    }
+    if constexpr (E == 8) {
+        uint8_t *t = tile + ((sub * 8) & 8);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, sub >> 1)) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rl, sub >> 1)) = make_uint2(l[0], l[1]);
+    } else {
+#pragma unroll
+        for (int b = 0; b < E / 16; ++b) {
+            const int e0 = sub * E + b * 16, in = e0 % kRow;
+            uint8_t *t = tile + e0 / kRow * rows * kRow;
+            *reinterpret_cast<uint4 *>(t + tc::swz8_off<kRow>(rh, in >> 4)) =
+                make_uint4(h[4 * b], h[4 * b + 1], h[4 * b + 2], h[4 * b + 3]);
+            *reinterpret_cast<uint4 *>(t + tc::swz8_off<kRow>(rl, in >> 4)) =
+                make_uint4(l[4 * b], l[4 * b + 1], l[4 * b + 2], l[4 * b + 3]);
         }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const bool f = fabsf(x[e]) < INFINITY;
-        finite &= f;
-        x[e] = f ? x[e] : 0.f;
-        m = fmaxf(m, fabsf(x[e]));
-    }
-    uint32_t top = __float_as_uint(m);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t all = (__ballot_sync(0xffffffffu, finite) >> (threadIdx.x & 24)) & 0xffu;
-    const int k = max(-110, min(110, 7 - (int(top >> 23) - 127)));  // largest in [128, 256)
-    const float up = pow2i(k), up32 = up * 32.f, down = pow2i(-k);
-#pragma unroll
-    for (int b = 0; b < E / 8; ++b) {
-        uint32_t h[2], l[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t hh[2], ll[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x0 = x[b * 8 + g * 4 + 2 * i], x1 = x[b * 8 + g * 4 + 2 * i + 1];
-                hh[i] = e4m3x2(x0 * up, x1 * up);
-                const float2 back = f32x2_of(uint16_t(hh[i]));
-                ll[i] = e4m3x2(fmaf(back.x, -32.f, x0 * up32), fmaf(back.y, -32.f, x1 * up32));
-            }
-            h[g] = hh[0] | (hh[1] << 16);
-            l[g] = ll[0] | (ll[1] << 16);
-        }
-        const int e0 = sub * E + b * 8, atom = e0 / kRow, in = e0 % kRow;
-        uint8_t *t = tile + atom * rows * kRow + (in & 8);
-        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, in >> 4)) = make_uint2(h[0], h[1]);
-        *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rl, in >> 4)) = make_uint2(l[0], l[1]);
-    }
-    return all != 0xffu ? __uint_as_float(0x7fc00000u) : down;
+    return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-k);
 }
 
 // Sums of N values over a warp's lanes: value k's sum lands in v[0] of the
 // lanes whose top log2(N) bits are k.
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
-    constexpr int kSteps = N == 16 ? 4 : 3;
-    static_assert(N == 16 || N == 8, "columns a thread");
+    constexpr int kSteps = N == 32 ? 5 : N == 16 ? 4 : 3;
+    static_assert(N == 32 || N == 16 || N == 8, "columns a thread");
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const int off = 16 >> s, half = N >> (s + 1);
