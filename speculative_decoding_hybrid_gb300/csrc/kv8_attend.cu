@@ -19,7 +19,7 @@
 // that is once, at a segment's first tile.  One vote a tile decides.
 //
 // Work is measured in tiles of 128 positions: a unit (request, kv head, block of
-// RB columns) costs its tiles plus kUnit, and the units laid end to end are cut
+// RB columns) costs its tiles plus a few for its ends, and the units laid end to end are cut
 // into equal ranges, one for each of the persistent CTAs.  A CTA runs the units
 // and parts of units of its range as segments.  Its warps:
 //   copy     finds the segments, queues them, and moves pages (tiled TMA, K and V
@@ -49,7 +49,12 @@ constexpr float kBase = 4.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
-constexpr int kUnit = 4;        // tiles that a unit's queries, new rows and outputs cost as much as
+
+// Tiles that a unit's queries, new rows and outputs cost as much as (measured:
+// cycles a segment over cycles a tile, 4.3, 2.5, 5.5 and 8.6 with the most used
+// head size of each).
+__host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : rb == 16 ? 3 : 4; }
+
 constexpr int kWhole = 8;       // units of so few tiles are not cut
 
 // A part of a unit cut by the ranges: which unit, and the CTAs owner .. owner +
@@ -150,8 +155,20 @@ struct Cfg {
 template <int D, int RB>
 struct Shared {
     using C = Cfg<D, RB>;
-    uint64_t full[C::kSlots], empty[C::kSlots], sc_full[C::kScales], s_full[2], s_free[2], p_full[2], pv_done[2];
-    uint64_t seg_full[kQueue], seg_empty[kQueue], q_ready, epi_done, fk_ready, fv_full, drain;
+    union {  // barriers that one thread or the tensor cores arrive at
+        uint64_t ones[C::kSlots * 2 + C::kScales + 4 + kQueue + 3];
+        struct {
+            uint64_t full[C::kSlots], empty[C::kSlots], sc_full[C::kScales], s_full[2], pv_done[2], seg_full[kQueue],
+                fk_ready, fv_full, drain;
+        };
+    };
+    union {  // barriers of the softmax warps
+        uint64_t warps[6];
+        struct {
+            uint64_t s_free[2], p_full[2], q_ready, epi_done;
+        };
+    };
+    uint64_t seg_empty[kQueue];  // of the softmax warps and the product warp
     float2 scales[C::kScales][8];
     alignas(16) float col_nm[RB], col_coef[RB], col_fac[RB];  // -m, score factor, rescaling
     float col_l[RB];
@@ -177,22 +194,22 @@ __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n -
 
 __device__ __forceinline__ long long weight_of(const AttendArgs &a, const Request &q, int rb) {
     if (q.bad || q.n == 0) return 0;
-    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + kUnit);
+    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + unit_cost(rb));
 }
 
-// a / b and a * b / c for values that are usually small.
-__device__ __forceinline__ long long quotient(long long a, int b) {
-    return a < (1ll << 32) ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+// a / b for values that usually fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
 // Where a range's end at x falls in a unit of `tiles` tiles: 0 its start, tiles
-// + kUnit its end.  Free cuts leave no part of fewer than kLeast tiles.
-__device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles) {
+// + extra its end.  Free cuts leave no part of fewer than kLeast tiles.
+__device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles, int extra) {
     if (x <= 0) return 0;
-    if (x > tiles) return tiles + kUnit;
-    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + kUnit : int(x);
+    if (x > tiles) return tiles + extra;
+    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + extra : int(x);
     const int y = (int(x) + a.piece_tiles - 1) / a.piece_tiles * a.piece_tiles;
-    return y >= tiles ? tiles + kUnit : y;
+    return y >= tiles ? tiles + extra : y;
 }
 
 template <int D, int RB>
@@ -203,9 +220,19 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     __shared__ Shared<D, RB> s;
     static_assert(sizeof(Shared<D, RB>) <= C::kStatic, "static shared memory");
 
-    gdn::pdl_enter();
+    gdn::pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
+    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1, kUnit = unit_cost(RB);
+    // barriers and tensor memory while the launch before may still be running
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&s.tmem, C::kTmem);
+    } else if (warp == kCopyWarp) {
+        constexpr int kOnes = C::kSlots * 2 + C::kScales + 4 + kQueue + 3, kWarps = C::kSoft / 32;
+        for (int i = lane; i < kOnes; i += 32) gdn::mbar_init(s.ones + i, 1);
+        if (lane < 6) gdn::mbar_init(s.warps + lane, kWarps);
+        if (lane < kQueue) gdn::mbar_init(s.seg_empty + lane, kWarps + 1);
+    }
+    gdn::pdl_wait();
 
     // ---- this CTA's range of the units laid end to end
     long long total, begin, end;
@@ -238,7 +265,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         ctas = int(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
         const int cta = blockIdx.x;
         if (tid == 0 && a.parts) a.parts[2 * cta].count = a.parts[2 * cta + 1].count = 0;
-        if (cta >= ctas || total == 0) return;
+        if (cta >= ctas || total == 0) {
+            if (warp == kMmaWarp) tc::tmem_dealloc(s.tmem, C::kTmem);
+            return;
+        }
         begin = quotient(total * cta, ctas);
         end = quotient(total * (cta + 1), ctas);
         incl += before;
@@ -263,29 +293,6 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     uint8_t *s_fk = sm, *s_fv = s_fk + C::kFresh, *s_q = s_fv + C::kFresh;
     uint8_t *s_p = s_q + ((C::kQ + 1023) & ~1023), *s_ring = s_p + 2 * C::kP;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
-            gdn::mbar_init(&s.full[i], 1);
-            gdn::mbar_init(&s.empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            gdn::mbar_init(&s.s_full[i], 1);
-            gdn::mbar_init(&s.s_free[i], C::kSoft / 32);
-            gdn::mbar_init(&s.p_full[i], C::kSoft / 32);
-            gdn::mbar_init(&s.pv_done[i], 1);
-        }
-        for (int i = 0; i < C::kScales; ++i) gdn::mbar_init(&s.sc_full[i], 1);
-        for (int i = 0; i < kQueue; ++i) {
-            gdn::mbar_init(&s.seg_full[i], 1);
-            gdn::mbar_init(&s.seg_empty[i], C::kSoft / 32 + 1);
-        }
-        gdn::mbar_init(&s.q_ready, C::kSoft / 32);
-        gdn::mbar_init(&s.epi_done, C::kSoft / 32);
-        gdn::mbar_init(&s.fk_ready, 1);
-        gdn::mbar_init(&s.fv_full, 1);
-        gdn::mbar_init(&s.drain, 1);
-    }
-    if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, C::kTmem);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -412,7 +419,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 for (int u = begin > at ? int(quotient(begin - at, cost)) : 0; u < units && at + (long long)u * cost < end && ok;
                      ++u) {
                     const long long su = at + (long long)u * cost;
-                    const int x0 = cut_at(a, begin - su, q.tiles), x1 = cut_at(a, end - su, q.tiles);
+                    const int x0 = cut_at(a, begin - su, q.tiles, kUnit),
+                              x1 = cut_at(a, end - su, q.tiles, kUnit);
                     Segment g;
                     g.r = r;
                     g.t0 = q.t0;
@@ -440,8 +448,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             Part p;
                             p.r = r;
                             p.y = y;
-                            p.owner = int((lo * ctas + total - 1) / total) - 1;
-                            p.count = int((hi * ctas + total - 1) / total) - p.owner;
+                            p.owner = int(quotient(lo * ctas + total - 1, total)) - 1;
+                            p.count = int(quotient(hi * ctas + total - 1, total)) - p.owner;
                             g.out = 2 * cta + (x0 > 0 ? 0 : 1);
                             if (lane == 0) a.parts[g.out] = p;
                         }
@@ -487,8 +495,15 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int nc = g.nc, n = g.n, fresh = g.fresh, nt = nc + fresh;
             if (g.cols == 0) break;
             const uint16_t *kn = a.k + int64_t(g.t0) * a.k_stride + int64_t(g.hk) * D;
-            uint4 w[D / 64];
-            if (fresh) load_row<D>(kn + int64_t(lane >> 3) * a.k_stride, lane & 7, (lane >> 3) < n, w);
+            uint4 w[4][D / 64];  // the new keys, four rows a pass
+            if (fresh) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * j < n) {
+                        const int row = 4 * j + (lane >> 3);
+                        load_row<D>(kn + int64_t(row) * a.k_stride, lane & 7, row < n, w[j]);
+                    }
+            }
             ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
             for (int i = 0; i <= nt; ++i) {
                 if (fresh && i == min(1, nc)) {
@@ -498,12 +513,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         ok = gdn::mbar_wait_bounded(&s.seg_empty[(k - 1) % kQueue], ((k - 1) / kQueue) & 1, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    for (int j0 = 0; j0 < n; j0 += 4) {
-                        const int j = j0 + (lane >> 3);
-                        if (j0) load_row<D>(kn + int64_t(j) * a.k_stride, lane & 7, j < n, w);
-                        const float down = split_row<D>(w, lane & 7, s_fk, 32, j, 16 + j);
-                        if ((lane & 7) == 0) s.fresh_k[j] = down;
-                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (4 * j < n) {
+                            const int row = 4 * j + (lane >> 3);
+                            const float down = split_row<D>(w[j], lane & 7, s_fk, 32, row, 16 + row);
+                            if ((lane & 7) == 0) s.fresh_k[row] = down;
+                        }
                     gdn::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive(&s.fk_ready);
@@ -689,11 +705,15 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             z[c] = t < g.len && t >= lo0 + lo1 * s.col_row[col0 + c] ? z[c] : -INFINITY;
                     }
                 };
-                load_z(false);
-                float over = -INFINITY;
+                bool move = i == 0;  // a segment's first tile sets the reference
+                if (!move) {
+                    load_z(false);
+                    float over = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
-                if (group_or(grp, over > kSlack || sc.y > vref || !ok)) {
+                    for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
+                    move = group_or(grp, over > kSlack || sc.y > vref || !ok);
+                }
+                if (__builtin_expect(move, 0)) {
                     // ---- the reference moves (or a wait ran out)
                     if (group_or(grp, !ok)) {
                         ok = false;
@@ -878,85 +898,96 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 uint16_t *o_base = a.o + int64_t(h.t0) * a.o_stride;
                 float *ws_base = a.ws_o + int64_t(h.out) * RB * D;
                 const int edge = min(min(lo_last, h.len), (h.tile0 + nc) * kTile);
+                constexpr int W = N < 16 ? N : 16;  // columns at a time
 #pragma unroll 1
-                for (int at = 0; at < C::kAtoms; ++at) {
+                for (int x = 0; x < C::kAtoms * (N / W); ++x) {
+                    const int at = x / (N / W), c0 = col0 + x % (N / W) * W;
                     const int e = at * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
-#pragma unroll 1
-                    for (int c0 = col0; c0 < min(int(h.cols), col0 + N); c0 += 8) {
-                        uint32_t w0[8], w1[8], w2[8], w3[8];
-                        f2 acc[4] = {0, 0, 0, 0};
-                        if (nc > 0) {
+                    if (c0 >= h.cols) continue;
+                    f2 acc[W / 2];
+#pragma unroll
+                    for (int c = 0; c < W / 2; ++c) acc[c] = 0;
+                    if (nc > 0) {
+                        const f2 part = pair(1.f / 32.f, 1.f / 32.f);
+#pragma unroll
+                        for (int j = 3; j >= 0; j -= 2) {  // from the last part on
+                            uint32_t u[W], v[W];
                             const uint32_t from = tm_o + lane_base + at * C::kNp + c0;
-                            tc::ld8_async(from, w0);
-                            tc::ld8_async(from + RB, w1);
-                            tc::ld8_async(from + 2 * RB, w2);
-                            tc::ld8_async(from + 3 * RB, w3);
+                            if constexpr (W == 16) {
+                                tc::ld16_async(from + j * RB, u);
+                                tc::ld16_async(from + (j - 1) * RB, v);
+                            } else {
+                                tc::ld8_async(from + j * RB, u);
+                                tc::ld8_async(from + (j - 1) * RB, v);
+                            }
                             tc::ld_wait();
-                            tc::ld_fence_regs(w0);
-                            tc::ld_fence_regs(w1);
-                            tc::ld_fence_regs(w2);
-                            tc::ld_fence_regs(w3);
-                            const f2 part = pair(1.f / 32.f, 1.f / 32.f), b2 = pair(back, back);
+                            tc::ld_fence_regs(u);
+                            tc::ld_fence_regs(v);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                f2 x = fma2(pair(w3[2 * c], w3[2 * c + 1]), part, pair(w2[2 * c], w2[2 * c + 1]));
-                                x = fma2(x, part, pair(w1[2 * c], w1[2 * c + 1]));
-                                acc[c] = mul2(b2, fma2(x, part, pair(w0[2 * c], w0[2 * c + 1])));
+                            for (int c = 0; c < W / 2; ++c) {
+                                acc[c] = fma2(acc[c], part, pair(u[2 * c], u[2 * c + 1]));
+                                acc[c] = fma2(acc[c], part, pair(v[2 * c], v[2 * c + 1]));
                             }
                         }
-                        if (e >= D) continue;
-                        uint32_t odd = 0;  // new rows whose value here is not finite
-                        if (h.fresh)
-                            for (int j = 0; j < h.n; ++j) {
-                                const uint32_t b = uint32_t(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]) << 16;
-                                const bool finite = (b & 0x7f800000u) != 0x7f800000u;
-                                if (!finite) odd |= 1u << j;
-                                const f2 v = pair(finite ? b : 0u, finite ? b : 0u);
-                                const ulonglong2 p0 = *reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0),
-                                                 p1 = *reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0 + 4);
-                                acc[0] = fma2(p0.x, v, acc[0]);
-                                acc[1] = fma2(p0.y, v, acc[1]);
-                                acc[2] = fma2(p1.x, v, acc[2]);
-                                acc[3] = fma2(p1.y, v, acc[3]);
-                            }
-                        float o[8];
+                        const f2 b2 = pair(back, back);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            o[2 * c] = both(acc[c]).x;
-                            o[2 * c + 1] = both(acc[c]).y;
-                        }
-                        if (odd) {  // such a value reaches the rows that see it, and no others
-                            const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
-                            for (int j = 0; j < h.n; ++j)
-                                if (odd >> j & 1) {
-                                    const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
+                        for (int c = 0; c < W / 2; ++c) acc[c] = mul2(acc[c], b2);
+                    }
+                    if (e >= D) continue;
+                    uint32_t odd = 0;  // new rows whose value here is not finite
+                    if (h.fresh)
+#pragma unroll 2
+                        for (int j = 0; j < h.n; ++j) {
+                            const uint32_t b = uint32_t(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]) << 16;
+                            const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+                            if (!finite) odd |= 1u << j;
+                            const f2 v = pair(finite ? b : 0u, finite ? b : 0u);
+                            const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0);
 #pragma unroll
-                                    for (int c = 0; c < 8; ++c)
-                                        if (uint32_t(s.col_row[c0 + c] - j) < uint32_t(w))
-                                            o[c] = fmaf(fresh_p[j * RB + c0 + c], v, o[c]);
-                                }
-                        }
-                        // NaN of positions that only some rows see
-                        for (int t = max(h.lo, h.tile0 * kTile); t < edge; ++t) {
-                            const int page = a.table[int64_t(h.r) * a.table_stride + (t >> shift)];
-                            const uint8_t code =
-                                a.c.kv[int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
-                                       (int64_t(a.c.h_kv + h.hk) * T + (t & (T - 1))) * D + e];
-                            if ((code & 0x7f) == 0x7f) {
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    if (c0 + c < h.cols && t >= lo0 + lo1 * s.col_row[c0 + c])
-                                        o[c] = __uint_as_float(0x7fc00000u);
+                            for (int c = 0; c < W / 4; ++c) {
+                                const ulonglong2 w = p[c];
+                                acc[2 * c] = fma2(w.x, v, acc[2 * c]);
+                                acc[2 * c + 1] = fma2(w.y, v, acc[2 * c + 1]);
                             }
                         }
+                    float o[W];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (c0 + c >= h.cols) break;
-                            if (h.out < 0)
+                    for (int c = 0; c < W / 2; ++c) {
+                        o[2 * c] = both(acc[c]).x;
+                        o[2 * c + 1] = both(acc[c]).y;
+                    }
+                    if (odd) {  // such a value reaches the rows that see it, and no others
+                        const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
+                        for (int j = 0; j < h.n; ++j)
+                            if (odd >> j & 1) {
+                                const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
+#pragma unroll
+                                for (int c = 0; c < W; ++c)
+                                    if (uint32_t(s.col_row[c0 + c] - j) < uint32_t(w))
+                                        o[c] = fmaf(fresh_p[j * RB + c0 + c], v, o[c]);
+                            }
+                    }
+                    // NaN of positions that only some rows see
+                    for (int t = max(h.lo, h.tile0 * kTile); t < edge; ++t) {
+                        const int page = a.table[int64_t(h.r) * a.table_stride + (t >> shift)];
+                        const uint8_t code =
+                            a.c.kv[int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                                   (int64_t(a.c.h_kv + h.hk) * T + (t & (T - 1))) * D + e];
+                        if ((code & 0x7f) == 0x7f) {
+#pragma unroll
+                            for (int c = 0; c < W; ++c)
+                                if (t >= lo0 + lo1 * s.col_row[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
+                        }
+                    }
+                    if (h.out < 0) {
+#pragma unroll
+                        for (int c = 0; c < W; ++c)
+                            if (c0 + c < h.cols)
                                 o_base[s.col_out[c0 + c] + e] = gdn::f32_to_bf16(o[c] * s.col_l[c0 + c]);
-                            else
-                                ws_base[(c0 + c) * D + e] = o[c];
-                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < W; ++c)
+                            if (c0 + c < h.cols) ws_base[(c0 + c) * D + e] = o[c];
                     }
                 }
             }
@@ -1159,7 +1190,7 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
         p.parts = p.max_pieces > 1 ? ctas : 0;
     } else {
         p.piece_tiles = p.max_pieces = 1;
-        ctas = (units * (tiles + kUnit) + 3) / 4;
+        ctas = (units * (tiles + unit_cost(p.rb)) + 3) / 4;
     }
     p.ctas = int(ctas < slots ? ctas : slots);
     if (!p.pinned) p.parts = p.ctas > 1 ? 2 * int64_t(p.ctas) : 0;
