@@ -152,8 +152,8 @@ class Kv8Cache:
         k_p, k_s = self._rows(k_new, self.h_kv, "k_new")
         v_p, v_s = self._rows(v_new, self.h_kv, "v_new")
         acc_p = None if accept_len is None else self._ints(accept_len, B, "accept_len")
-        st = gs.lib.kv8_append(self._c, layer, B, min(k_new.shape[0], v_new.shape[0]), cu_p, len_p, table_p, table_s,
-                               k_p, k_s, v_p, v_s, acc_p, max_rows, self._status,
+        st = gs.lib.kv8_append(self._c, layer, B, min(k_new.shape[0], v_new.shape[0]), cu_p, len_p, table_p, table_n,
+                               table_s, k_p, k_s, v_p, v_s, acc_p, max_rows, self._status,
                                _raw_stream(self._index) if stream is None else gs._stream(stream))
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_append", st)
