@@ -1,14 +1,15 @@
 // Commit of rows into the paged 8-bit key/value cache, and page copies
 // (sm_103a).
 //
-// kv8_append: one CTA per (page touched, kv head and K or V, request).  A
-// thread holds its pieces of 16 new elements (32 bytes of bf16) in registers
-// between the two things done with them: the page's largest magnitude, which
-// fixes the scale 2^e with amax <= 448 * 2^e, and the rounding to codes.  A
-// power of two makes x / scale exact, so codes do not depend on the order of
-// appends, and a scale that grows moves earlier codes exactly unless they
-// fall into e4m3's subnormals.
-#include "kv8.cuh"
+// kv8_append: one CTA per (page touched, kv head and K or V).  A thread holds
+// its pieces of 16 new elements (32 bytes of bf16) in registers between the two
+// things done with them: the page's largest magnitude, which fixes the scale 2^e
+// with amax <= 448 * 2^e, and the rounding to codes.  A power of two makes x /
+// scale exact, so codes do not depend on the order of appends, and a scale that
+// grows moves earlier codes exactly unless they fall into e4m3's subnormals.
+// HBM-bound on prompts (2 bytes read and 1 written a value): the new rows are
+// asked for before the page they go to is known.
+#include "kv8_math.cuh"
 
 namespace {
 
@@ -24,112 +25,118 @@ struct AppendArgs {
     uint32_t *status;
 };
 
-__device__ __forceinline__ float amax_finite(uint32_t w, float m) {
-    const float a = __uint_as_float((w << 16) & 0x7fffffffu), b = __uint_as_float(w & 0x7fff0000u);
-    m = a < INFINITY && a > m ? a : m;  // false for NaN and infinity
-    return b < INFINITY && b > m ? b : m;
+// Largest magnitudes of pairs of bf16: magnitudes order like their bits.
+__device__ __forceinline__ uint32_t max_of(const uint4 &w, uint32_t m) {
+    m = __vmaxu2(m, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+    return __vmaxu2(m, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+// The same without infinities and NaN.
+__device__ __forceinline__ uint32_t max_finite_of(const uint4 &w, uint32_t m) {
+    const uint32_t u[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, u[i] & __vcmpltu2(u[i], 0x7f807f80u));
+    return m;
 }
 
 // 16 bf16 values -> 16 codes.
 __device__ __forceinline__ uint4 encode16(const uint4 &a, const uint4 &b, float inv) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const kv8::f2 inv2 = kv8::pair(inv, inv);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = kv8::e4m3x2(__uint_as_float(w[2 * i] << 16) * inv,
-                                        __uint_as_float(w[2 * i] & 0xffff0000u) * inv);
-        const uint32_t hi = kv8::e4m3x2(__uint_as_float(w[2 * i + 1] << 16) * inv,
-                                        __uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv);
-        o[i] = lo | (hi << 16);
+        const float2 lo = kv8::both(kv8::mul2(kv8::pair(w[2 * i] << 16, w[2 * i] & 0xffff0000u), inv2)),
+                     hi = kv8::both(kv8::mul2(kv8::pair(w[2 * i + 1] << 16, w[2 * i + 1] & 0xffff0000u), inv2));
+        o[i] = kv8::join16(uint16_t(kv8::e4m3x2(lo.x, lo.y)), uint16_t(kv8::e4m3x2(hi.x, hi.y)));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+struct Rows {
+    int t0, rows, len, n;   // n: the rows to append
+    uint32_t bad;
+};
+__device__ __forceinline__ Rows rows_of(const AppendArgs &a, int r) {
+    Rows q;
+    q.t0 = a.cu_rows[r];
+    q.rows = a.cu_rows[r + 1] - q.t0;
+    q.len = a.cache_len[r];
+    const int j = a.accept_len ? a.accept_len[r] : 0;
+    q.bad = 0;
+    if (q.t0 < 0 || q.rows < 0 || q.rows > a.max_rows || int64_t(q.t0) + q.rows > a.row_capacity || q.len < 0 ||
+        int64_t(q.len) + q.rows > int64_t(a.table_pages) * a.c.page_tokens)
+        q.bad = GDN_DEV_ROWS_BAD;
+    else if (a.accept_len && j >= q.rows)
+        q.bad = GDN_DEV_ACCEPT_BAD;
+    q.n = q.bad ? 0 : !a.accept_len ? q.rows : j < 0 ? 0 : j + 1;
+    return q;
+}
+
+// One page of request rows `q`, its table's page len / T + step: all threads of a CTA.
 // PIECES: the most 16-element pieces of a page a thread may hold.
 template <int PIECES>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
-    gdn::pdl_enter();
-    const int r = blockIdx.z, h = blockIdx.y >> 1, is_v = blockIdx.y & 1;
-    const int T = a.c.page_tokens, d = a.c.d;
-    const int t0 = a.cu_rows[r], rows = a.cu_rows[r + 1] - t0, len = a.cache_len[r];
-    if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
-    const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
-    if (t0 < 0 || rows < 0 || rows > a.max_rows || int64_t(t0) + rows > a.row_capacity || len < 0 ||
-        int64_t(len) + rows > int64_t(a.table_pages) * T) {
-        if (first_cta) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
-        return;
-    }
-    int n = rows;
-    if (a.accept_len) {
-        const int j = a.accept_len[r];
-        if (j >= rows) {
-            if (first_cta) gdn::set_status(a.status, GDN_DEV_ACCEPT_BAD);
-            return;
-        }
-        n = j < 0 ? 0 : j + 1;
-    }
-    const int pj = len / T + blockIdx.x;           // page of the request's table
-    const int p0 = pj * T;                         // its first position
-    const int from = max(len, p0), to = min(len + n, p0 + T);
+__device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Rows &q, int step, int hv) {
+    const int is_v = hv >= a.c.h_kv, h = hv - is_v * a.c.h_kv, T = a.c.page_tokens, d = a.c.d;
+    const int page_shift = 31 - __clz(T), per_shift = 31 - __clz(d) - 4;  // 2^per_shift pieces a token
+    const int t0 = q.t0, len = q.len;
+    const int pj = (len >> page_shift) + step;                 // page of the request's table
+    const int p0 = pj << page_shift;                      // its first position
+    const int from = max(len, p0), to = min(len + q.n, p0 + T);
     if (from >= to) return;
-    const int page = a.table[int64_t(r) * a.table_stride + pj];
-    if (page < 0 || page >= a.c.num_pages) {
-        if (threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
-        return;
-    }
     const uint16_t *x = is_v ? a.v : a.k;
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
-    uint8_t *codes = a.c.kv + int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
-                     (int64_t(is_v) * a.c.h_kv + h) * T * d;
-    float *scale = a.c.scale + int64_t(page) * a.c.scale_page_stride + int64_t(a.layer) * a.c.scale_layer_stride +
-                   2 * h + is_v;
-    const int per = d / 16;                        // pieces a token
     const int held = from - p0;                    // tokens the page already holds
-    const int total = (to - from) * per;
+    const int total = (to - from) << per_shift;
     const uint16_t *src = x + (int64_t(t0) + (from - len)) * stride + int64_t(h) * d;
 
     uint4 w[PIECES][2];
-    float m = 0.f;
+    uint32_t m = 0;
+    const int page = a.table[int64_t(r) * a.table_stride + pj];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
         const int i = threadIdx.x + u * kThreads;
         w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
         if (i < total) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(src + int64_t(i / per) * stride + (i % per) * 16);
+            const uint4 *p = reinterpret_cast<const uint4 *>(src + int64_t(i >> per_shift) * stride + (i & ((1 << per_shift) - 1)) * 16);
             w[u][0] = __ldcs(p);
             w[u][1] = __ldcs(p + 1);
         }
     }
-#pragma unroll
-    for (int u = 0; u < PIECES; ++u)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            m = amax_finite(w[u][k].x, m);
-            m = amax_finite(w[u][k].y, m);
-            m = amax_finite(w[u][k].z, m);
-            m = amax_finite(w[u][k].w, m);
-        }
-    // magnitudes order like their bit patterns
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    __shared__ uint32_t red[kThreads / 32];
+    if (page < 0 || page >= a.c.num_pages) {
+        if (threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        return;
+    }
+    uint8_t *codes = a.c.kv + int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                     (int64_t(is_v) * a.c.h_kv + h) * T * d;
+    float *scale = a.c.scale + int64_t(page) * a.c.scale_page_stride + int64_t(a.layer) * a.c.scale_layer_stride +
+                   2 * h + is_v;
     const float was = held ? *scale : 0.f;
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) m = max_of(w[u][1], max_of(w[u][0], m));
+    if (max(m >> 16, m & 0xffffu) >= 0x7f80u) {
+        m = 0;
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) m = max_finite_of(w[u][1], max_finite_of(w[u][0], m));
+    }
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+    __shared__ uint32_t red[kThreads / 32];
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wm;
     __syncthreads();
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) top = max(top, red[i]);
-    const int e = kv8::scale_exp(__uint_as_float(top));
+    const int e = kv8::scale_exp(__uint_as_float(top << 16));
     const float fit = kv8::pow2i(e);
     const float now = fmaxf(was, fit);
     const float inv = 1.f / now;                   // exact: a power of two
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
         const int i = threadIdx.x + u * kThreads;
-        if (i < total) *reinterpret_cast<uint4 *>(codes + int64_t(held) * d + int64_t(i) * 16) = encode16(w[u][0], w[u][1], inv);
+        if (i < total) *reinterpret_cast<uint4 *>(codes + (held * d + i * 16)) = encode16(w[u][0], w[u][1], inv);
     }
     if (held && now > was) {
         const float f = was * inv;
-        for (int i = threadIdx.x; i < held * per; i += kThreads) {
+        for (int i = threadIdx.x; i < held << per_shift; i += kThreads) {
             uint4 *p = reinterpret_cast<uint4 *>(codes + int64_t(i) * 16);
             const uint4 old = *p;
             uint32_t o[4] = {old.x, old.y, old.z, old.w};
@@ -143,6 +150,56 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a
     }
     // every thread has read *scale before the barrier above
     if (threadIdx.x == 0) *scale = now;
+}
+
+// RAGGED: the CTAs count the pages touched over all requests, each finding its
+// request by a scan of the lengths; otherwise the pages one request may touch.
+template <int PIECES, bool RAGGED>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
+    gdn::pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const bool reports = blockIdx.x == 0 && threadIdx.x < 32;
+    // the heads of a page side by side: their parts of the rows are neighbours in memory
+    const int heads = 2 * a.c.h_kv, first = blockIdx.x / heads, hv = blockIdx.x - first * heads;
+    const int T = a.c.page_tokens, page_shift = 31 - __clz(T);
+    if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
+    if constexpr (!RAGGED) {
+        const Rows q = rows_of(a, blockIdx.z);
+        if (q.bad && blockIdx.x == 0 && threadIdx.x == 0) gdn::set_status(a.status, q.bad);
+        append_page<PIECES>(a, blockIdx.z, q, first, hv);
+    } else {
+        // every warp scans, 32 requests at a time; requests whose rows overlap may make
+        // more pages than there are CTAs
+        int at = first, total = 0;
+        do {
+            int r = -1, step = 0;
+            total = 0;
+            for (int r0 = 0; r0 < a.B; r0 += 32) {
+                int pages = 0;
+                if (r0 + lane < a.B) {
+                    const Rows x = rows_of(a, r0 + lane);
+                    if (x.bad && reports) gdn::set_status(a.status, x.bad);
+                    if (x.n > 0) pages = ((x.len & (T - 1)) + x.n + T - 1) >> page_shift;
+                }
+                int incl = pages;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, total + incl > at);
+                if (r < 0 && past) {
+                    const int w = __ffs(past) - 1;
+                    r = r0 + w;
+                    step = at - total - __shfl_sync(0xffffffffu, incl - pages, w);
+                }
+                total += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (r >= 0) append_page<PIECES>(a, r, rows_of(a, r), step, hv);
+            at += gridDim.x / heads;
+            __syncthreads();
+        } while (at < total);
+    }
 }
 
 struct CopyArgs {
@@ -191,9 +248,9 @@ __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(const CopyArgs a) {
 
 extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
                           const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
-                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new,
-                          int64_t v_stride, const int32_t *accept_len, int32_t max_rows, uint32_t *dev_status,
-                          void *stream) {
+                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *k_new, int64_t k_stride,
+                          const gdn_bf16 *v_new, int64_t v_stride, const int32_t *accept_len, int32_t max_rows,
+                          uint32_t *dev_status, void *stream) {
     const int bad = gdn_host::kv8_check(cache);
     if (bad != GDN_OK) return bad;
     if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_pages < 0 ||
@@ -224,15 +281,27 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.v_stride = v_stride;
     a.status = dev_status;
     const int T = cache->page_tokens;
-    // n rows starting anywhere touch at most (T - 1 + n - 1) / T + 1 pages
-    const dim3 grid(unsigned((max_rows + T - 2) / T + 1), unsigned(2 * cache->h_kv), unsigned(B));
+    // n rows starting anywhere touch at most (T - 1 + n - 1) / T + 1 pages, and all
+    // requests together at most row_capacity / T + 2 B.  The scan costs a decode's
+    // commit more than the few CTAs without rows it saves, and a ragged prompt's less.
+    const int64_t each = (max_rows + T - 2) / T + 1, all = row_capacity / T + int64_t(2) * B;
+    const bool ragged = all < each * B / 2;
+    const int64_t ctas = (ragged ? all : each) * 2 * cache->h_kv;
+    if (ctas > 0x7fffffff) return GDN_ERR_ARG;
+    const dim3 grid(unsigned(ctas), 1, unsigned(ragged ? 1 : B));
     const int most = max_rows < T ? max_rows : T;
     const int pieces = (most * cache->d / 16 + kThreads - 1) / kThreads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1>, grid, dim3(kThreads), 0, st, a);
-    if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2>, grid, dim3(kThreads), 0, st, a);
-    if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4>, grid, dim3(kThreads), 0, st, a);
-    return gdn_host::launch_pdl(kv8_append_kernel<8>, grid, dim3(kThreads), 0, st, a);
+    if (ragged) {
+        if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1, true>, grid, dim3(kThreads), 0, st, a);
+        if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2, true>, grid, dim3(kThreads), 0, st, a);
+        if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4, true>, grid, dim3(kThreads), 0, st, a);
+        return gdn_host::launch_pdl(kv8_append_kernel<8, true>, grid, dim3(kThreads), 0, st, a);
+    }
+    if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1, false>, grid, dim3(kThreads), 0, st, a);
+    if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2, false>, grid, dim3(kThreads), 0, st, a);
+    if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4, false>, grid, dim3(kThreads), 0, st, a);
+    return gdn_host::launch_pdl(kv8_append_kernel<8, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 extern "C" int kv8_copy_pages(const kv8_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,

@@ -201,3 +201,36 @@ def test_copy_of_a_layer_inside_a_wider_pool(cuda_dev):
     c = Kv8Cache(kv, s, 2, torch.zeros(1, dtype=torch.int32, device=cuda_dev))
     c.copy_pages(*(torch.tensor([x], dtype=torch.int32, device=cuda_dev) for x in (2, 7)))
     assert torch.equal(wide, want) and torch.equal(sc, want_s)
+
+
+@pytest.mark.parametrize("B", [3, 40])
+def test_ragged_prompts_of_many_requests(cuda_dev, B):
+    """Rows from none to hundreds, the pages counted over all requests."""
+    g = np.random.RandomState(B)
+    rows = [int(x) for x in g.choice([0, 1, 2, 17, 60, 333], B)]
+    rows[-1] = 700
+    lens = [int(x) for x in g.randint(0, 50, B)]
+    cache = ku.Cache(lens, 2, 2, 64, 16, room=[a + n for a, n in zip(lens, rows)], seed=10)
+    accept = [n - 1 if i % 3 else max(-1, n - 5) for i, n in enumerate(rows)]
+    same(append(cache, rows, cuda_dev, accept=accept), cache)
+
+
+def test_rows_named_twice(cuda_dev):
+    """Requests whose rows overlap (the table goes back) take more pages than the rows would: all are written,
+    the request that goes back is refused."""
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    n = 400
+    cache = ku.Cache([0, 0, 0, 5], 1, 1, 64, 16, room=[n, 1, n, 5 + n], seed=11)
+    g = np.random.RandomState(12)
+    t, f = ku.bf16(g.standard_normal((n, 2, 64)))
+    t = t.to(cuda_dev)
+    c = ku.gpu_cache(cache, cuda_dev)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)
+    k, v = t[:, :1], t[:, 1:]
+    cu = i32([0, n, 0, n, n])                                # request 1 has -n rows, 2 request 0's, 3 none
+    c.append(0, torch.from_numpy(cache.table).to(cuda_dev), i32(cache.lens), cu, k, v, max_rows=n)
+    assert int(c.status.item()) == gs.DEV_ROWS_BAD
+    c.status.zero_()
+    for r in (0, 2):
+        ku.append_request(cache, r, 0, f[:, :1], f[:, 1:])
+    same(c, cache)
