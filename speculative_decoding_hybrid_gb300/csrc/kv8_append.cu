@@ -155,7 +155,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
 // RAGGED: the CTAs count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
 template <int PIECES, bool RAGGED>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, PIECES <= 2 ? 8 : 1) kv8_append_kernel(const AppendArgs a) {
     gdn::pdl_enter();
     const int lane = threadIdx.x & 31;
     const bool reports = blockIdx.x == 0 && threadIdx.x < 32;

@@ -57,10 +57,11 @@ __host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb =
 
 constexpr int kWhole = 8;       // units of so few tiles are not cut
 
-// A part of a unit cut by the ranges: which unit, and the CTAs owner .. owner +
-// count - 1 that have its parts (count 0: none).
-struct Part {
-    int r, y, owner, count;
+// A part of a unit cut by the ranges: the unit (first row, kv head, block and its
+// columns in use) and the CTAs owner .. owner + count - 1 that have its parts
+// (count 0: none).
+struct alignas(16) Part {
+    int owner, count, t0, cols, hk, blk, pad[2];
 };
 
 struct AttendArgs {
@@ -104,13 +105,6 @@ __device__ __forceinline__ Request request_of(const AttendArgs &a, int3 x) {
     q.tiles = q.lo < q.len ? (q.len + kTile - 1) / kTile - first : 0;
     return q;
 }
-
-// The pieces of one unit in the workspace, in order.
-struct Pieces {
-    int count;
-    int64_t first, base, step;
-    __device__ __forceinline__ int64_t at(int s) const { return s == 0 ? first : base + s * step; }
-};
 
 struct Segment {
     int r, t0, len, lo, tile0, nc, out;  // cached tiles tile0 .. + nc; out: part of the workspace, -1: direct
@@ -445,9 +439,11 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         } else if (x0 > 0 || x1 < cost) {
                             // the first CTA whose end lies past the start, the first whose end counts as the unit's
                             const long long lo = su + kLeast, hi = su + q.tiles - kLeast + 1;
-                            Part p;
-                            p.r = r;
-                            p.y = y;
+                            Part p = {};
+                            p.t0 = q.t0;
+                            p.cols = g.cols;
+                            p.hk = g.hk;
+                            p.blk = g.blk;
                             p.owner = int(quotient(lo * ctas + total - 1, total)) - 1;
                             p.count = int(quotient(hi * ctas + total - 1, total)) - p.owner;
                             g.out = 2 * cta + (x0 > 0 ? 0 : 1);
@@ -1018,13 +1014,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     }
 }
 
-// Joins a unit's pieces: o = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.  Groups of
-// d/4 threads.  With few pieces a group joins a column by itself; with many the
-// groups share one column's pieces, so that their loads are in flight together.
-// Which of the two, and so the order of the sums, goes by the pieces alone.
-// Free cuts: a CTA for each part, the parts of a unit sharing its columns.  Given
-// cuts: a CTA for each `per_cta` columns of a unit.
-constexpr int kJoin = 512;
+// Joins a unit's pieces: o = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s, in one pass
+// with a running M.  Groups of d/4 threads.  With few pieces a group joins a column
+// by itself; with many the groups share one column's pieces, so that their loads are
+// in flight together.  Which of the two, and so the order of the sums, goes by the
+// pieces alone.  Free cuts: a CTA for each part, the parts of a unit sharing its
+// columns.  Given cuts: a CTA for each `per_cta` columns of a unit.
+constexpr int kJoin = 512, kFew = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__ AttendArgs a, const int RB,
@@ -1032,101 +1028,79 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
     gdn::pdl_enter();
     constexpr int W = D / 4, G = kJoin / W;
     const int tid = threadIdx.x;
+    int t0, hk, blk, begin, end, by, count;
+    int64_t first, base, step;  // pieces in the workspace: the first, then base + s * step
     // the partial sums of a call in which a wait ran out are not to be trusted
-    if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
-    int r, y, begin, end, by;
-    Pieces pieces;
+    const uint32_t status = a.status ? *reinterpret_cast<volatile uint32_t *>(a.status) : 0;
     if (a.pinned) {
-        r = blockIdx.z;
-        y = blockIdx.y;
-        pieces.base = pieces.first = int64_t(r) * a.max_pieces * gridDim.y + y;
-        pieces.step = gridDim.y;
+        const Request rq = request_of(a, rows_of(a, blockIdx.z));
+        hk = blockIdx.y / a.blocks;
+        blk = blockIdx.y - hk * a.blocks;
+        count = rq.bad ? 0 : (rq.tiles + a.piece_tiles - 1) / a.piece_tiles;
+        t0 = rq.t0;
+        first = base = int64_t(blockIdx.z) * a.max_pieces * gridDim.y + blockIdx.y;
+        step = gridDim.y;
         begin = blockIdx.x * per_cta;
-        end = begin + per_cta;
+        end = min(begin + per_cta, min(RB, rq.n * a.group - blk * RB));
         by = 1;
     } else {
         const Part p = a.parts[2 * blockIdx.y + blockIdx.x];
-        if (p.count <= 1) return;
-        r = p.r;
-        y = p.y;
-        pieces.count = p.count;
-        pieces.first = 2 * p.owner + 1;
-        pieces.base = 2 * p.owner;
-        pieces.step = 2;
+        hk = p.hk;
+        blk = p.blk;
+        count = p.count;
+        t0 = p.t0;
+        first = 2 * p.owner + 1;
+        base = 2 * p.owner;
+        step = 2;
         begin = int(blockIdx.y) - p.owner;
-        end = RB;
-        by = p.count;
+        end = p.cols;
+        by = count;
     }
-    const Request rq = request_of(a, rows_of(a, r));
-    if (rq.bad) return;
-    if (a.pinned) {
-        pieces.count = (rq.tiles + a.piece_tiles - 1) / a.piece_tiles;
-        if (pieces.count <= 1) return;
-    }
-    const int hk = y / a.blocks, blk = y % a.blocks;
-    end = min(end, min(RB, rq.n * a.group - blk * RB));
-    __shared__ float s_l[G], s_m[kJoin / 32];
+    if (count <= 1 || (status & GDN_DEV_TIMEOUT)) return;
+    __shared__ float2 s_ml[G];
     __shared__ float4 s_o[G][W];
-    const int g = tid / W, e = tid % W, count = pieces.count;
-    const bool few = count <= 8;
-    const int step = few ? G * by : by, ps = few ? 1 : G, p0 = few ? 0 : g;
-    for (int c = begin + (few ? g * by : 0); c < end; c += step) {
-        const float2 *ml = a.ws_ml + c;
-        float m = -INFINITY;
+    const int g = tid / W, e = tid % W;
+    const bool few = count <= kFew;
+    for (int c = begin + (few ? g * by : 0); c < end; c += few ? G * by : by) {
+        float m = kUnset, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         bool skip = false;
-        for (int s = few ? 0 : tid; s < count; s += few ? 1 : kJoin) {
-            const float2 x = ml[pieces.at(s) * RB];
-            m = fmaxf(m, x.x);
-            skip |= x.y < 0.f;  // a piece was refused
+        auto add = [&](float2 x, const float4 &o) {
+            if (x.y == 0.f) return;  // the row sees nothing of the piece
+            const float now = fmaxf(m, x.x), f = ex2(m - now), w = ex2(x.x - now);
+            m = now;
+            l = fmaf(l, f, x.y * w);
+            acc.x = fmaf(acc.x, f, o.x * w);
+            acc.y = fmaf(acc.y, f, o.y * w);
+            acc.z = fmaf(acc.z, f, o.z * w);
+            acc.w = fmaf(acc.w, f, o.w * w);
+        };
+#pragma unroll 4
+        for (int s = few ? 0 : g; s < count; s += few ? 1 : G) {
+            const int64_t at = (s == 0 ? first : base + s * step) * RB + c;
+            const float2 x = a.ws_ml[at];
+            const float4 o = __ldcs(reinterpret_cast<const float4 *>(a.ws_o + at * D) + e);
+            skip |= x.y < 0.f;  // the piece was refused
+            add(x, o);
         }
         if (!few) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             __syncthreads();  // the last column's sums are read
-            if ((tid & 31) == 0) s_m[tid >> 5] = m;
+            s_o[g][e] = acc;
+            if (e == 0) s_ml[g] = make_float2(m, l);
             skip = __syncthreads_or(skip);
-#pragma unroll
-            for (int k = 0; k < kJoin / 32; ++k) m = fmaxf(m, s_m[k]);
+            if (skip) return;
+            if (g > 0) continue;
+            for (int k = 1; k < G; ++k) add(s_ml[k], s_o[k][e]);
         }
         if (skip) return;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int s = p0; s < count; s += ps) {
-            const int64_t at = pieces.at(s) * RB;
-            const float2 x = ml[at];
-            const float4 o = __ldcs(reinterpret_cast<const float4 *>(a.ws_o + (at + c) * D) + e);
-            const float f = ex2(x.x - m);
-            if (x.y != 0.f) {  // else the row sees nothing of the piece
-                l = fmaf(f, x.y, l);
-                acc.x = fmaf(f, o.x, acc.x);
-                acc.y = fmaf(f, o.y, acc.y);
-                acc.z = fmaf(f, o.z, acc.z);
-                acc.w = fmaf(f, o.w, acc.w);
-            }
-        }
-        if (!few) {
-            s_o[g][e] = acc;
-            if (e == 0) s_l[g] = l;
-            __syncthreads();
-            if (g > 0) continue;
-            for (int k = 1; k < G; ++k) {
-                const float4 o = s_o[k][e];
-                acc.x += o.x;
-                acc.y += o.y;
-                acc.z += o.z;
-                acc.w += o.w;
-                l += s_l[k];
-            }
-        }
-        const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x % a.group;
+        const int x = blk * RB + c, row = x / a.group, h = hk * a.group + x - row * a.group;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint2 w;
         w.x = gdn::f32_to_bf16(acc.x * inv) | (uint32_t(gdn::f32_to_bf16(acc.y * inv)) << 16);
         w.y = gdn::f32_to_bf16(acc.z * inv) | (uint32_t(gdn::f32_to_bf16(acc.w * inv)) << 16);
-        *reinterpret_cast<uint2 *>(a.o + (int64_t(rq.t0) + row) * a.o_stride + int64_t(h) * D + e * 4) = w;
+        *reinterpret_cast<uint2 *>(a.o + (int64_t(t0) + row) * a.o_stride + int64_t(h) * D + e * 4) = w;
         if (e == 0 && a.lse)
-            a.lse[(int64_t(rq.t0) + row) * a.c.h_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            a.lse[(int64_t(t0) + row) * a.c.h_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 
