@@ -588,16 +588,23 @@ typedef struct kv8_cache {
  *   A row that sees nothing gets o = 0 and lse = -inf.  Query head h reads
  *   kv head h / (h_q/h_kv).  q [row][h_q][d], k_new and v_new [row][h_kv][d],
  *   o [row][h_q][d]: rows q_stride, k_stride, v_stride, o_stride elements
- *   apart (multiples of 8), bases 16-byte aligned; lse rows are h_q apart.
- *   split_tokens: cached positions per independently summed piece.  0 picks
- *   it from B, max_len, max_rows and the head layout; a given value (rounded
- *   up to 128) makes a request's bits independent of what else is in the
- *   batch.  Bytes of cache past cache_len, whatever they hold, reach no
- *   output.  Requests past max_len, max_rows or row_capacity set
- *   GDN_DEV_ROWS_BAD, page ids out of range GDN_DEV_PAGE_OOR; either skips
- *   the request (its o and lse are not written).
- *   workspace: kv8_attend_workspace_bytes(...) device bytes (16-byte aligned,
- *   no initialisation), 0 when no request can need more than one piece.
+ *   apart (multiples of 8; o_stride at most 2^26), bases 16-byte aligned; lse
+ *   rows are h_q apart.  Neither o nor lse may overlap an input.
+ *   split_tokens: 0 cuts the batch's work into equal ranges wherever they
+ *   fall; n > 0 sums every n cached positions (rounded up to a multiple of
+ *   128) by themselves, which makes a request's bits independent of what else
+ *   is in the batch.  Sums and softmax statistics are fp32; a weight enters its
+ *   product with v with 14 bits, and with 2^-27 of the largest weight seen.
+ *   A non-finite q or k that a row sees makes the row's outputs NaN; what a
+ *   row does not see, NaN and infinities included, and bytes of cache past
+ *   cache_len, whatever they hold, do not reach it.
+ *   Requests past max_len, max_rows or row_capacity set GDN_DEV_ROWS_BAD, page
+ *   ids out of range (of pages some row sees) GDN_DEV_PAGE_OOR; either skips
+ *   the request (its o and lse are not written).  A bounded wait that runs out
+ *   sets GDN_DEV_TIMEOUT: outputs of that call are not to be trusted.
+ *   B <= 65535.  workspace: kv8_attend_workspace_bytes(...) device bytes
+ *   (16-byte aligned, no initialisation, one call at a time), 0 when no work
+ *   is cut.  Any stride >= 0 of the table: requests may share a row of it.
  */
 size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t max_len, int32_t max_rows,
                                   int32_t split_tokens);
@@ -695,6 +702,18 @@ int gdn_selftest_prefill_timeout(const gdn_dims *dims, int32_t nseq, int32_t row
                                  const int32_t *src_slot, const int32_t *dst_slot, gdn_bf16 *o,
                                  void *workspace, size_t workspace_bytes,
                                  uint32_t *dev_status, uint64_t limit_ns, void *stream);
+
+/* Failure-detection self-test of kv8_attend (cache only, no lse) with every
+ * wait bounded by limit_ns (1 .. 1e9): the copy of a segment's last keys is
+ * announced and withheld, so the waits for it run out: GDN_DEV_TIMEOUT is set
+ * and the request's outputs are not written.  (Test-only.) */
+int kv8_selftest_attend_timeout(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+                                const int32_t *cu_rows, const int32_t *cache_len,
+                                const int32_t *table, int32_t table_pages, int64_t table_stride,
+                                const gdn_bf16 *q, int64_t q_stride, gdn_bf16 *o, int64_t o_stride,
+                                int32_t max_len, int32_t max_rows, int32_t split_tokens,
+                                void *workspace, size_t workspace_bytes,
+                                uint32_t *dev_status, uint64_t limit_ns, void *stream);
 
 /* Failure-detection self-test: a kernel waits on an mbarrier that is never
  * completed, gives up after limit_ns (1 .. 1e9) of device time and sets

@@ -37,7 +37,7 @@ EXPORTS = ["gdn_decode_step", "gdn_verify", "mtp_accept_workspace_bytes", "mtp_g
            "gdn_pool_share", "gdn_pool_release", "plan_transaction", "gdn_pool_apply", "gdn_pool_abort",
            "gdn_decode_transaction", "gdn_decode_transaction_at", "gdn_status_string",
            "gdn_selftest_prefill_timeout", "kv8_attend_workspace_bytes", "kv8_attend", "kv8_append",
-           "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free", "kv8_pages_compact"]
+           "kv8_selftest_attend_timeout", "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free", "kv8_pages_compact"]
 
 
 class GdnError(RuntimeError):
@@ -151,6 +151,8 @@ def _load():
         "kv8_attend_workspace_bytes": [CP, I32, I32, I32, I32],
         "kv8_attend": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, P, I64, P, I64, P, I32, I32, I32, P, SZ, P,
                        P],
+        "kv8_selftest_attend_timeout": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, I32, I32, I32, P, SZ, P,
+                                        ctypes.c_uint64, P],
         "kv8_append": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, P, I32, P, P],
         "kv8_copy_pages": [CP, I32, P, P, P, P],
         "kv8_pages_reserve": [PP, P, I32, P, I32, I32, I32, P, P, P],
@@ -383,6 +385,15 @@ def kv8_attend(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, 
         ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
         table_stride, _ptr(q), q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse), max_len, max_rows,
         split_tokens, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
+
+
+def kv8_selftest_attend_timeout(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages,
+                                table_stride, q, q_stride, o, o_stride, max_len, max_rows, split_tokens, workspace,
+                                workspace_bytes, dev_status, limit_ns: int, stream=None):
+    return _check("kv8_selftest_attend_timeout", lib.kv8_selftest_attend_timeout(
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
+        table_stride, _ptr(q), q_stride, _ptr(o), o_stride, max_len, max_rows, split_tokens, _ptr(workspace),
+        workspace_bytes, _ptr(dev_status), int(limit_ns), _stream(stream)))
 
 
 def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, k_new,

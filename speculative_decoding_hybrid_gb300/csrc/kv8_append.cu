@@ -97,7 +97,8 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
         const int i = threadIdx.x + u * kThreads;
         w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
         if (i < total) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(src + int64_t(i >> per_shift) * stride + (i & ((1 << per_shift) - 1)) * 16);
+            const int in = (i & ((1 << per_shift) - 1)) * 16;
+            const uint4 *p = reinterpret_cast<const uint4 *>(src + int64_t(i >> per_shift) * stride + in);
             w[u][0] = __ldcs(p);
             w[u][1] = __ldcs(p + 1);
         }

@@ -81,6 +81,7 @@ struct AttendArgs {
     Part *parts;       // [CTA][2]: of a unit begun before the range, of one that goes on after it
     uint32_t *status;
     uint64_t wait_ns;
+    int32_t withhold;  // self-test: a segment's last keys are announced and never copied
 };
 
 // What a request asks for; the same test in both kernels.
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 if (lane == 0) gdn::mbar_arrive_expect_tx(&s.full[slot], uint32_t(__popc(have)) * uint32_t(T * D));
                 __syncwarp();
                 issued = pos + 1;
+                if (a.withhold && pos == ring + k_pos(nc - 1)) return;
                 if (lane < per && page >= 0) {
 #pragma unroll
                     for (int x = 0; x < C::kAtoms; ++x)
@@ -395,8 +397,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (lane == 0) gdn::mbar_arrive_expect_tx(&s.fv_full, uint32_t(g.n) * (2 * D));
                     __syncwarp();
                     if (lane < g.n)
-                        gdn::bulk_g2s(s_fv + lane * 2 * D, a.v + (int64_t(g.t0) + lane) * a.v_stride + int64_t(g.hk) * D,
-                                      2 * D, &s.fv_full);
+                        gdn::bulk_g2s(s_fv + lane * 2 * D,
+                                      a.v + (int64_t(g.t0) + lane) * a.v_stride + int64_t(g.hk) * D, 2 * D, &s.fv_full);
                     ++fresh_done;
                 }
             }
@@ -410,8 +412,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const long long w = weight_of(a, q, RB);
             if (w > 0) {
                 const int cost = q.tiles + kUnit, nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
-                for (int u = begin > at ? int(quotient(begin - at, cost)) : 0; u < units && at + (long long)u * cost < end && ok;
-                     ++u) {
+                int u = begin > at ? int(quotient(begin - at, cost)) : 0;
+                for (; u < units && at + (long long)u * cost < end && ok; ++u) {
                     const long long su = at + (long long)u * cost;
                     const int x0 = cut_at(a, begin - su, q.tiles, kUnit),
                               x1 = cut_at(a, end - su, q.tiles, kUnit);
@@ -727,8 +729,9 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (pos_in < N) {
                         const int c = col0 + pos_in;
                         const float was = -s.col_nm[c];
-                        const float now = fmaxf(
-                            fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]), fmaxf(s.col_max[2][c], s.col_max[3][c])), was);
+                        const float top = fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]),
+                                                fmaxf(s.col_max[2][c], s.col_max[3][c]));
+                        const float now = fmaxf(top, was);
                         s.col_fac[c] = ex2(was - now);
                         s.col_nm[c] = -now;
                     }
@@ -1194,12 +1197,12 @@ extern "C" size_t kv8_attend_workspace_bytes(const kv8_cache *cache, int32_t B, 
     return ws_bytes(cache, plan_of(cache, B, max_len, max_rows, split_tokens));
 }
 
-extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
-                          const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
-                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k_new,
-                          int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride, gdn_bf16 *o, int64_t o_stride,
-                          float *lse, int32_t max_len, int32_t max_rows, int32_t split_tokens, void *workspace,
-                          size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+static int attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity, const int32_t *cu_rows,
+                  const int32_t *cache_len, const int32_t *table, int32_t table_pages, int64_t table_stride,
+                  const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k_new, int64_t k_stride,
+                  const gdn_bf16 *v_new, int64_t v_stride, gdn_bf16 *o, int64_t o_stride, float *lse,
+                  int32_t max_len, int32_t max_rows, int32_t split_tokens, void *workspace, size_t workspace_bytes,
+                  uint32_t *dev_status, uint64_t wait_ns, int32_t withhold, void *stream) {
     const int bad = gdn_host::kv8_check(cache);
     if (bad != GDN_OK) return bad;
     if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_pages < 0 ||
@@ -1256,7 +1259,8 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
         if (!p.pinned) a.parts = reinterpret_cast<Part *>(a.ws_ml + columns);
     }
     a.status = dev_status;
-    a.wait_ns = gdn::kWaitLimitNs;
+    a.wait_ns = wait_ns;
+    a.withhold = withhold;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc = GDN_ERR_SHAPE;
     const int key = cache->d * 100 + p.rb;
@@ -1286,4 +1290,29 @@ extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int3
     if (cache->d == 64) return gdn_host::launch_pdl(kv8_join_kernel<64>, grid, dim3(kJoin), 0, st, a, p.rb, per);
     if (cache->d == 128) return gdn_host::launch_pdl(kv8_join_kernel<128>, grid, dim3(kJoin), 0, st, a, p.rb, per);
     return gdn_host::launch_pdl(kv8_join_kernel<256>, grid, dim3(kJoin), 0, st, a, p.rb, per);
+}
+
+extern "C" int kv8_attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+                          const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
+                          int32_t table_pages, int64_t table_stride, const gdn_bf16 *q, int64_t q_stride,
+                          const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
+                          gdn_bf16 *o, int64_t o_stride, float *lse, int32_t max_len, int32_t max_rows,
+                          int32_t split_tokens, void *workspace, size_t workspace_bytes, uint32_t *dev_status,
+                          void *stream) {
+    return attend(cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, q, q_stride,
+                  k_new, k_stride, v_new, v_stride, o, o_stride, lse, max_len, max_rows, split_tokens, workspace,
+                  workspace_bytes, dev_status, gdn::kWaitLimitNs, 0, stream);
+}
+
+extern "C" int kv8_selftest_attend_timeout(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+                                           const int32_t *cu_rows, const int32_t *cache_len, const int32_t *table,
+                                           int32_t table_pages, int64_t table_stride, const gdn_bf16 *q,
+                                           int64_t q_stride, gdn_bf16 *o, int64_t o_stride, int32_t max_len,
+                                           int32_t max_rows, int32_t split_tokens, void *workspace,
+                                           size_t workspace_bytes, uint32_t *dev_status, uint64_t limit_ns,
+                                           void *stream) {
+    if (limit_ns == 0 || limit_ns > gdn::kWaitLimitNs) return GDN_ERR_ARG;
+    return attend(cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, q, q_stride,
+                  nullptr, 0, nullptr, 0, o, o_stride, nullptr, max_len, max_rows, split_tokens, workspace,
+                  workspace_bytes, dev_status, limit_ns, 1, stream);
 }

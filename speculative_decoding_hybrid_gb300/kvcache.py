@@ -245,7 +245,8 @@ class PagedKv(Kv8Cache):
             self.length[r] += int(n)
 
     def upload(self, requests: Sequence[int], stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-        """-> (table [B, pages], cache_len [B]) on the device, row i for requests[i]."""
+        """-> (table [B, pages], cache_len [B]) on the device, row i for requests[i].  They are the same
+        tensors every time: work that reads one upload's goes to the stream of the next, or is waited for first."""
         B, cap = len(requests), self.tables.shape[1]
         if self._staged is not None:
             self._staged.synchronize()  # the last upload has left the staging rows
@@ -253,7 +254,7 @@ class PagedKv(Kv8Cache):
         stage = self._stage[:B].numpy()
         stage[:, :cap] = self.tables[idx]
         stage[:, cap] = self.length[idx]
-        s = torch.cuda.current_stream() if stream is None else stream
+        s = torch.cuda.current_stream() if stream is None else _stream_object(stream)
         with torch.cuda.stream(s):
             both = self._stage[:B].to(self.dev_table.device, non_blocking=True)
             self.dev_table[:B].copy_(both[:, :cap])

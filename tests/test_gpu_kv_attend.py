@@ -377,3 +377,61 @@ def test_host_refusals(cuda_dev):
                            qt.stride(0), kt.data_ptr(), kt.stride(0), vt.data_ptr(), vt.stride(0), o.data_ptr(), 512,
                            None, 100000, 2, 128, None, 0, c.status.data_ptr(), None)
     assert st == gs.GDN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("split", [0, 256])
+def test_a_wait_that_runs_out_writes_nothing(cuda_dev, d, split):
+    """A copy that never comes: every wait gives up in time, the status says so, outputs stay as they were, and
+    the next call is whole again."""
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    cache = ku.Cache([1500, 40, 700], 4, 2, d, 32, seed=22)
+    c, o, _, _, _, (table, length, cu), (qt, _, _) = run(cache, [2, 1, 3], cuda_dev, split=split, fresh=False)
+    need = gs.kv8_attend_workspace_bytes(c.c, 3, 1500, 3, split)
+    ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=cuda_dev)
+    out = torch.full_like(o, 5.0)
+    gs.kv8_selftest_attend_timeout(c.c, 0, 3, 6, cu, length, table, table.shape[1], table.stride(0), qt, qt.stride(0),
+                                   out, out.stride(0), 1500, 3, split, ws, need, c.status, 2_000_000)
+    assert int(c.status.item()) == gs.DEV_TIMEOUT and (out == 5.0).all()
+    c.status.zero_()
+    again, _ = c.attend(0, table, length, cu, qt, None, None, max_len=1500, max_rows=3, split_tokens=split)
+    assert int(c.status.item()) == 0 and torch.equal(again, o)
+
+
+def test_requests_may_share_a_table_row(cuda_dev):
+    """One prefix read by several requests through a table of stride 0."""
+    cache = ku.Cache([500], 8, 2, 128, 64, seed=23)
+    c, _, _, _, _, (table, length, _), _ = run(cache, [4], cuda_dev)
+    g = torch.Generator(device=cuda_dev).manual_seed(3)
+    q = torch.randn((12, 8, 128), generator=g, device=cuda_dev).to(torch.bfloat16)
+    cu = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device=cuda_dev)
+    lens = torch.tensor([500, 128, 300], dtype=torch.int32, device=cuda_dev)
+    a, _ = c.attend(0, table.expand(3, -1), lens, cu, q, None, None, max_len=500, max_rows=4, split_tokens=256)
+    b, _ = c.attend(0, table.repeat(3, 1), lens, cu, q, None, None, max_len=500, max_rows=4, split_tokens=256)
+    assert torch.equal(a, b) and int(c.status.item()) == 0
+
+
+def test_values_that_are_not_finite_reach_only_who_sees_them(cuda_dev):
+    """A NaN and an infinity among the new rows' values and a NaN code in the cache inside some rows' window."""
+    cache = ku.Cache([300], 4, 2, 128, 32, seed=24)
+    t0 = 300 - 99 + 1                                   # window 100: row 0 sees 201.., row 1 from 202, row 2 from 203
+    cache.kv[cache.table[0, t0 // 32], 0, 1, 1, t0 % 32, 17] = 127
+
+    def edit(t, q, k, v):
+        t[2, (4 + 2) * 128 + 5] = float("nan")          # row 2, kv head 0, element 5
+        t[3, (4 + 2) * 128 + 128 + 9] = float("inf")    # row 3, kv head 1, element 9
+    for split in (0, 128):
+        _, o, lse, (q, k, v), _, _, _ = run(cache, [4], cuda_dev, window=100, edit=edit, split=split)
+        x = cache.dense(0, 0)
+        x[1, 1, t0, 17] = 0.0
+        ro, rl, ra, rw = ku.attend_request(x, q, k, v, 100, ku.default_scale(128))
+        ob, lb = ku.attend_bounds(ro, rl, ra, rw, 128)
+        got = o.double().cpu().numpy()
+        odd = np.zeros(got.shape, bool)
+        odd[0:2, 2:4, 17] = True                        # rows 0 and 1 see position t0 = 202
+        odd[2:4, 0:2, 5] = True
+        assert np.isnan(got[odd]).all()
+        assert (got[3, 2:4, 9] == np.inf).all()
+        odd[3, 2:4, 9] = True
+        assert np.max(np.abs(got - ro)[~odd] / ob[~odd]) <= 1.0
+        assert np.max(np.abs(lse.double().cpu().numpy() - rl) / lb) <= 1.0

@@ -161,7 +161,8 @@ def test_random_life_against_a_model(gs, seed):
             np.add.at(counts, tables[q, :n[q]], 1)
             got = [mem[tables[q, t // T], t % T] for t in range(length[q])]
             assert got == want[q]
-        assert np.array_equal(counts, pool.refcount) and sorted(pool.free_list()) == np.flatnonzero(counts == 0).tolist()
+        assert np.array_equal(counts, pool.refcount)
+        assert sorted(pool.free_list()) == np.flatnonzero(counts == 0).tolist()
 
 
 def test_oracle_rounds_like_its_definition():
