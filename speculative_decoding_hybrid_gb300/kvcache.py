@@ -24,6 +24,7 @@ from . import binding as gs
 
 PAGE_TOKENS = (16, 32, 64, 128)
 HEAD_SIZES = (64, 128, 256)
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 # The current stream's handle without building a Stream object (a few microseconds a call).
@@ -67,29 +68,16 @@ class Kv8Cache:
         self._status = status.data_ptr()
         self._workspace = {}  # (B, max_len, max_rows, split_tokens) -> bytes
 
-    def _rows(self, x: torch.Tensor, heads: int, name: str):
-        """-> (address, row stride) of packed rows of heads."""
-        shape, stride = x.shape, x.stride()
-        if (x.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != self.d
-                or stride[1] != self.d or stride[2] != 1 or x.get_device() != self._index):
-            raise ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads, on the cache's device"
-                             % (name, heads, self.d))
-        return x.data_ptr(), stride[0]
+    # The checks stand in the calls themselves: on small transactions a call's time is
+    # its host side, and a Python function a tensor cost 2.4 of 16 us.
 
-    def _ints(self, x: torch.Tensor, n: int, name: str):
-        """-> address of a contiguous int32 list of at least n."""
-        if (x.dtype is not torch.int32 or x.dim() != 1 or x.numel() < n or not x.is_contiguous()
-                or x.get_device() != self._index):
-            raise ValueError("%s must be a contiguous int32 list of at least %d, on the cache's device" % (name, n))
-        return x.data_ptr()
+    def _bad_rows(self, name: str, heads: int):
+        return ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads on the cache's device, a row for each "
+                          "of the call's" % (name, heads, self.d))
 
-    def _table(self, table: torch.Tensor, B: int):
-        """-> (address, entries a row, row stride) of the page table."""
-        shape, stride = table.shape, table.stride()
-        if (table.dtype is not torch.int32 or len(shape) != 2 or shape[0] < B or (stride[1] != 1 and shape[1] > 1)
-                or table.get_device() != self._index):
-            raise ValueError("table must be int32 [requests, pages] with contiguous rows, on the cache's device")
-        return table.data_ptr(), shape[1], stride[0]
+    def _bad_lists(self, names: str):
+        return ValueError("table must be int32 [requests, pages] with contiguous rows, and %s contiguous int32 lists "
+                          "that fit it, on the cache's device" % names)
 
     def attend(self, layer: int, table: torch.Tensor, cache_len: torch.Tensor, cu_rows: torch.Tensor,
                q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor], max_len: int,
@@ -99,16 +87,42 @@ class Kv8Cache:
         """-> (o bf16 [rows, h_q, d], lse fp32 [rows, h_q] or None); ``kv8_attend`` in the header.
 
         max_len and max_rows are host bounds on cache_len and on a request's rows."""
-        B, R = cache_len.shape[0], q.shape[0]
-        len_p, cu_p = self._ints(cache_len, B, "cache_len"), self._ints(cu_rows, B + 1, "cu_rows")
-        table_p, table_n, table_s = self._table(table, B)
-        q_p, q_s = self._rows(q, self.h_q, "q")
-        k_p = k_s = v_p = v_s = 0
+        h_q, h_kv, d, device = self.h_q, self.h_kv, self.d, self._index
+        B = cache_len.numel()
+        tables, pages = table.shape
+        table_s, one = table.stride()
+        if (table.dtype is not _I32 or cache_len.dtype is not _I32 or cu_rows.dtype is not _I32 or tables < B
+                or (one != 1 and pages > 1) or cu_rows.numel() <= B or not cache_len.is_contiguous()
+                or not cu_rows.is_contiguous() or table.get_device() != device or cache_len.get_device() != device
+                or cu_rows.get_device() != device):
+            raise self._bad_lists("cache_len and cu_rows")
+        R, a, b = q.shape
+        q_s, c, one = q.stride()
+        if q.dtype is not _BF16 or a != h_q or b != d or c != d or one != 1 or q.get_device() != device:
+            raise self._bad_rows("q", h_q)
+        k_p = v_p = None
+        k_s = v_s = 0
         if k_new is not None or v_new is not None:
-            if k_new is None or v_new is None or k_new.shape[0] < R or v_new.shape[0] < R:
-                raise ValueError("k_new and v_new come together and need a row for each of q's")
-            k_p, k_s = self._rows(k_new, self.h_kv, "k_new")
-            v_p, v_s = self._rows(v_new, self.h_kv, "v_new")
+            if k_new is None or v_new is None:
+                raise ValueError("k_new and v_new come together")
+            n, a, b = k_new.shape
+            k_s, c, one = k_new.stride()
+            if (k_new.dtype is not _BF16 or n < R or a != h_kv or b != d or c != d or one != 1
+                    or k_new.get_device() != device):
+                raise self._bad_rows("k_new", h_kv)
+            n, a, b = v_new.shape
+            v_s, c, one = v_new.stride()
+            if (v_new.dtype is not _BF16 or n < R or a != h_kv or b != d or c != d or one != 1
+                    or v_new.get_device() != device):
+                raise self._bad_rows("v_new", h_kv)
+            k_p, v_p = k_new.data_ptr(), v_new.data_ptr()
+        o_s = h_q * d
+        if out is not None:
+            n, a, b = out.shape
+            o_s, c, one = out.stride()
+            if (out.dtype is not _BF16 or n < R or a != h_q or b != d or c != d or one != 1
+                    or out.get_device() != device):
+                raise self._bad_rows("out", h_q)
         key = (B, max_len, max_rows, split_tokens)
         need = self._workspace.get(key)
         if need is None:
@@ -117,26 +131,21 @@ class Kv8Cache:
             need = self._workspace[key] = gs.lib.kv8_attend_workspace_bytes(self._c, *key)
         if stream is not None:
             # what the call allocates belongs to the stream it runs on
-            stream = _stream_object(stream)
             before = torch.cuda.current_stream(self._device)
-            torch.cuda.set_stream(stream)
+            torch.cuda.set_stream(_stream_object(stream))
         try:
-            raw = _raw_stream(self._index)
+            raw = _raw_stream(device)
             if out is None:
-                out = torch.empty((R, self.h_q, self.d), dtype=torch.bfloat16, device=self._device)
-                o_p, o_s = out.data_ptr(), self.h_q * self.d
-            elif out.shape[0] < R:
-                raise ValueError("out needs a row for each of q's")
-            else:
-                o_p, o_s = self._rows(out, self.h_q, "out")
-            lse = torch.empty((R, self.h_q), dtype=torch.float32, device=self._device) if want_lse else None
+                out = torch.empty((R, h_q, d), dtype=_BF16, device=self._device)
+            lse = torch.empty((R, h_q), dtype=torch.float32, device=self._device) if want_lse else None
             ws = torch.empty((need,), dtype=torch.uint8, device=self._device) if need else None
         finally:
             if stream is not None:
                 torch.cuda.set_stream(before)
-        st = gs.lib.kv8_attend(self._c, layer, B, R, cu_p, len_p, table_p, table_n, table_s, q_p, q_s, k_p or None, k_s,
-                               v_p or None, v_s, o_p, o_s, lse.data_ptr() if want_lse else None, max_len, max_rows,
-                               split_tokens, ws.data_ptr() if need else None, need, self._status, raw)
+        st = gs.lib.kv8_attend(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(), pages,
+                               table_s, q.data_ptr(), q_s, k_p, k_s, v_p, v_s, out.data_ptr(), o_s,
+                               lse.data_ptr() if want_lse else None, max_len, max_rows, split_tokens,
+                               ws.data_ptr() if need else None, need, self._status, raw)
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_attend", st)
         return out, lse
@@ -146,24 +155,43 @@ class Kv8Cache:
                max_rows: int = gs.MAX_ROWS, stream=None):
         """Commits the first accept_len[r] + 1 rows of each request (all rows without accept_len);
         ``kv8_append`` in the header."""
-        B = cache_len.shape[0]
-        len_p, cu_p = self._ints(cache_len, B, "cache_len"), self._ints(cu_rows, B + 1, "cu_rows")
-        table_p, table_n, table_s = self._table(table, B)
-        k_p, k_s = self._rows(k_new, self.h_kv, "k_new")
-        v_p, v_s = self._rows(v_new, self.h_kv, "v_new")
-        acc_p = None if accept_len is None else self._ints(accept_len, B, "accept_len")
-        st = gs.lib.kv8_append(self._c, layer, B, min(k_new.shape[0], v_new.shape[0]), cu_p, len_p, table_p, table_n,
-                               table_s, k_p, k_s, v_p, v_s, acc_p, max_rows, self._status,
-                               _raw_stream(self._index) if stream is None else gs._stream(stream))
+        h_kv, d, device = self.h_kv, self.d, self._index
+        B = cache_len.numel()
+        tables, pages = table.shape
+        table_s, one = table.stride()
+        if (table.dtype is not _I32 or cache_len.dtype is not _I32 or cu_rows.dtype is not _I32 or tables < B
+                or (one != 1 and pages > 1) or cu_rows.numel() <= B or not cache_len.is_contiguous()
+                or not cu_rows.is_contiguous() or table.get_device() != device or cache_len.get_device() != device
+                or cu_rows.get_device() != device):
+            raise self._bad_lists("cache_len and cu_rows")
+        acc_p = None
+        if accept_len is not None:
+            if (accept_len.dtype is not _I32 or accept_len.numel() < B or not accept_len.is_contiguous()
+                    or accept_len.get_device() != device):
+                raise self._bad_lists("accept_len")
+            acc_p = accept_len.data_ptr()
+        R, a, b = k_new.shape
+        k_s, c, one = k_new.stride()
+        if k_new.dtype is not _BF16 or a != h_kv or b != d or c != d or one != 1 or k_new.get_device() != device:
+            raise self._bad_rows("k_new", h_kv)
+        n, a, b = v_new.shape
+        v_s, c, one = v_new.stride()
+        if (v_new.dtype is not _BF16 or n != R or a != h_kv or b != d or c != d or one != 1
+                or v_new.get_device() != device):
+            raise self._bad_rows("v_new", h_kv)
+        st = gs.lib.kv8_append(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(), pages,
+                               table_s, k_new.data_ptr(), k_s, v_new.data_ptr(), v_s, acc_p, max_rows, self._status,
+                               _raw_stream(device) if stream is None else gs._stream(stream))
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_append", st)
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Page dst[i] <- page src[i], every layer; ``kv8_copy_pages`` in the header."""
-        n = src.shape[0]
-        if dst.shape != src.shape:
-            raise ValueError("src and dst must be lists of one length")
-        st = gs.lib.kv8_copy_pages(self._c, n, self._ints(src, n, "src"), self._ints(dst, n, "dst"), self._status,
+        n = src.numel()
+        if (src.dtype is not _I32 or dst.dtype is not _I32 or dst.numel() != n or not src.is_contiguous()
+                or not dst.is_contiguous() or src.get_device() != self._index or dst.get_device() != self._index):
+            raise ValueError("src and dst must be contiguous int32 lists of one length on the cache's device")
+        st = gs.lib.kv8_copy_pages(self._c, n, src.data_ptr(), dst.data_ptr(), self._status,
                                    _raw_stream(self._index) if stream is None else gs._stream(stream))
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_copy_pages", st)
