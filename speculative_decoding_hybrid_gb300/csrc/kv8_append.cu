@@ -13,7 +13,8 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a page copy, and of an append of whole pages
+constexpr int kRowThreads = 64;  // of an append of at most 256 pieces a page: a few rows, small pages
 
 struct AppendArgs {
     kv8_cache c;
@@ -74,7 +75,7 @@ __device__ __forceinline__ Rows rows_of(const AppendArgs &a, int r) {
 
 // One page of request rows `q`, its table's page len / T + step: all threads of a CTA.
 // PIECES: the most 16-element pieces of a page a thread may hold.
-template <int PIECES>
+template <int THREADS, int PIECES>
 __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Rows &q, int step, int hv) {
     const int is_v = hv >= a.c.h_kv, h = hv - is_v * a.c.h_kv, T = a.c.page_tokens, d = a.c.d;
     const int page_shift = 31 - __clz(T), per_shift = 31 - __clz(d) - 4;  // 2^per_shift pieces a token
@@ -94,7 +95,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
     const int page = a.table[int64_t(r) * a.table_stride + pj];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
-        const int i = threadIdx.x + u * kThreads;
+        const int i = threadIdx.x + u * THREADS;
         w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
         if (i < total) {
             const int in = (i & ((1 << per_shift) - 1)) * 16;
@@ -120,24 +121,25 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
         for (int u = 0; u < PIECES; ++u) m = max_finite_of(w[u][1], max_finite_of(w[u][0], m));
     }
     const uint32_t wm = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
-    __shared__ uint32_t red[kThreads / 32];
+    __shared__ uint32_t red[THREADS / 32];
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wm;
     __syncthreads();
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) top = max(top, red[i]);
+    for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
     const int e = kv8::scale_exp(__uint_as_float(top << 16));
     const float fit = kv8::pow2i(e);
     const float now = fmaxf(was, fit);
     const float inv = 1.f / now;                   // exact: a power of two
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
-        const int i = threadIdx.x + u * kThreads;
+        const int i = threadIdx.x + u * THREADS;
         if (i < total) *reinterpret_cast<uint4 *>(codes + (held * d + i * 16)) = encode16(w[u][0], w[u][1], inv);
     }
     if (held && now > was) {
         const float f = was * inv;
-        for (int i = threadIdx.x; i < held << per_shift; i += kThreads) {
+#pragma unroll(THREADS == kRowThreads ? 4 : 1)
+        for (int i = threadIdx.x; i < held << per_shift; i += THREADS) {
             uint4 *p = reinterpret_cast<uint4 *>(codes + int64_t(i) * 16);
             const uint4 old = *p;
             uint32_t o[4] = {old.x, old.y, old.z, old.w};
@@ -155,8 +157,8 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
 
 // RAGGED: the CTAs count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
-template <int PIECES, bool RAGGED>
-__global__ void __launch_bounds__(kThreads, PIECES <= 2 ? 8 : 1) kv8_append_kernel(const AppendArgs a) {
+template <int THREADS, int PIECES, bool RAGGED>
+__global__ void __launch_bounds__(THREADS, PIECES <= 2 ? 2048 / THREADS : 4096 / (THREADS * PIECES)) kv8_append_kernel(const AppendArgs a) {
     gdn::pdl_enter();
     const int lane = threadIdx.x & 31;
     const bool reports = blockIdx.x == 0 && threadIdx.x < 32;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, PIECES <= 2 ? 8 : 1) kv8_append_kern
     if constexpr (!RAGGED) {
         const Rows q = rows_of(a, blockIdx.z);
         if (q.bad && blockIdx.x == 0 && threadIdx.x == 0) gdn::set_status(a.status, q.bad);
-        append_page<PIECES>(a, blockIdx.z, q, first, hv);
+        append_page<THREADS, PIECES>(a, blockIdx.z, q, first, hv);
     } else {
         // every warp scans, 32 requests at a time; requests whose rows overlap may make
         // more pages than there are CTAs
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, PIECES <= 2 ? 8 : 1) kv8_append_kern
                 }
                 total += __shfl_sync(0xffffffffu, incl, 31);
             }
-            if (r >= 0) append_page<PIECES>(a, r, rows_of(a, r), step, hv);
+            if (r >= 0) append_page<THREADS, PIECES>(a, r, rows_of(a, r), step, hv);
             at += gridDim.x / heads;
             __syncthreads();
         } while (at < total);
@@ -291,18 +293,27 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     if (ctas > 0x7fffffff) return GDN_ERR_ARG;
     const dim3 grid(unsigned(ctas), 1, unsigned(ragged ? 1 : B));
     const int most = max_rows < T ? max_rows : T;
-    const int pieces = (most * cache->d / 16 + kThreads - 1) / kThreads;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto launch = [&](auto kernel, int threads) {
+        return gdn_host::launch_pdl(kernel, grid, dim3(unsigned(threads)), 0, static_cast<cudaStream_t>(stream), a);
+    };
+    // Small CTAs where a page has few new pieces: a large batch's commit is then all in
+    // flight at once (256 requests x 4 rows 6.4 us with 256 threads, 3.6 with 64), and a
+    // prompt into pages of 16 tokens keeps its threads busy (278 against 99 us).  Four
+    // pieces a thread are the best of 2, 4 and 8 while a CTA stays within 256 threads
+    // (99, 91 and 92 us at 512 pieces a page).
+    const int all_pieces = most * cache->d / 16;
     if (ragged) {
-        if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1, true>, grid, dim3(kThreads), 0, st, a);
-        if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2, true>, grid, dim3(kThreads), 0, st, a);
-        if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4, true>, grid, dim3(kThreads), 0, st, a);
-        return gdn_host::launch_pdl(kv8_append_kernel<8, true>, grid, dim3(kThreads), 0, st, a);
+        if (all_pieces <= 2 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 2, true>, kRowThreads);
+        if (all_pieces <= 4 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 4, true>, kRowThreads);
+        if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, true>, 128);
+        if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, true>, kThreads);
+        return launch(kv8_append_kernel<kThreads, 8, true>, kThreads);
     }
-    if (pieces <= 1) return gdn_host::launch_pdl(kv8_append_kernel<1, false>, grid, dim3(kThreads), 0, st, a);
-    if (pieces <= 2) return gdn_host::launch_pdl(kv8_append_kernel<2, false>, grid, dim3(kThreads), 0, st, a);
-    if (pieces <= 4) return gdn_host::launch_pdl(kv8_append_kernel<4, false>, grid, dim3(kThreads), 0, st, a);
-    return gdn_host::launch_pdl(kv8_append_kernel<8, false>, grid, dim3(kThreads), 0, st, a);
+    if (all_pieces <= 2 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 2, false>, kRowThreads);
+    if (all_pieces <= 4 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 4, false>, kRowThreads);
+    if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, false>, 128);
+    if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, false>, kThreads);
+    return launch(kv8_append_kernel<kThreads, 8, false>, kThreads);
 }
 
 extern "C" int kv8_copy_pages(const kv8_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,
