@@ -158,7 +158,8 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
 // RAGGED: the CTAs count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
 template <int THREADS, int PIECES, bool RAGGED>
-__global__ void __launch_bounds__(THREADS, PIECES <= 2 ? 2048 / THREADS : 4096 / (THREADS * PIECES)) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(THREADS, PIECES <= 2 ? 2048 / THREADS : 4096 / (THREADS * PIECES))
+    kv8_append_kernel(const AppendArgs a) {
     gdn::pdl_enter();
     const int lane = threadIdx.x & 31;
     const bool reports = blockIdx.x == 0 && threadIdx.x < 32;

@@ -42,6 +42,7 @@ namespace {
 using namespace kv8;
 
 constexpr int kTile = 128;      // positions a tile
+constexpr int kSms = 152;
 // Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
 // is 2^-25, so 2^-27 of a weight at the reference.  More slack moves the
 // reference less often and costs that many bits at the low end.
@@ -50,12 +51,26 @@ constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 
-// Tiles that a unit's queries, new rows and outputs cost as much as (measured:
-// cycles a segment over cycles a tile, 4.3, 2.5, 5.5 and 8.6 with the most used
-// head size of each).
-__host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : rb == 16 ? 3 : 4; }
+// Tiles that a unit's queries, new rows and outputs cost as much as.  Cycles a
+// segment over cycles a tile are 4.3, 2.5, 5.5 and 8.6 for RB = 8 .. 64; of these and
+// two tiles more or less, these were the fastest (4 rows x 256 requests 146, 141 and
+// 142 us at 4, 6 and 8).
+__host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : 4; }
 
-constexpr int kWhole = 8;       // units of so few tiles are not cut
+// Units of at most 2 * kLeast tiles are not cut, nor, where they fill half of the CTAs
+// and each can have its own, of kWhole: the join costs more (24 windowed requests x 12
+// heads, 9 tiles: 22.5 us cut, 16.1 whole; two heads of one request, d = 256, are the
+// other way round: 6 tiles 15 us cut, 17 whole, 16 tiles 18 and 28).
+constexpr int kWhole = 16;
+
+// Ranges that a total weight is cut into where CTAs do not run out: of four tiles or
+// more, or, up to one CTA an SM, of two (two heads of one request of 16 tiles: 17.8 us
+// with four, 15.7 with two; 32 units of 16 tiles: 16.7 on 176 CTAs, 18.2 on 304).  No
+// fewer than kLeast, or one could lie empty inside a unit.
+__host__ __device__ constexpr long long ranges_of(long long total) {
+    const long long two = total / kLeast, four = total / 4;
+    return four > kSms ? four : two < kSms ? two : kSms;
+}
 
 // A part of a unit cut by the ranges: the unit (first row, kv head, block and its
 // columns in use) and the CTAs owner .. owner + count - 1 that have its parts
@@ -69,7 +84,7 @@ struct AttendArgs {
     kv8_cache c;
     int32_t layer, B, row_capacity, table_pages, max_len, max_rows;
     int32_t group, blocks, page_shift;  // page_tokens = 1 << page_shift
-    int32_t pinned, piece_tiles, max_pieces;
+    int32_t pinned, piece_tiles, max_pieces;  // given cuts, at multiples of piece_tiles
     int64_t table_stride;
     const int32_t *cu_rows, *cache_len, *table;
     const uint16_t *q, *k, *v;
@@ -124,10 +139,12 @@ struct Cfg {
     static constexpr int kQ = kNs * D;
     static constexpr int kP = kTile * (RB == 8 ? 64 : kNp);
     static constexpr int kSlot = kTile * D;
-    // groups of four softmax warps, each with its share of the columns: a warp
-    // waits on its own chain of loads, exponentials and conversions most of the
-    // time, so an SM wants at least eight of them
-    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : 2;
+    // Groups of four softmax warps, each with its share of the columns: a warp waits
+    // on its own chain of loads, exponentials and conversions most of the time, so an
+    // SM wants eight of them (4 rows x 256 requests 362 us with four, 279 with eight),
+    // and sixteen where 64 columns leave the products time (16 rows x 32 requests 134
+    // us with eight, 128 with sixteen, whose 96 registers spill a little).
+    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : RB == 32 ? 2 : 4;
     static constexpr int kCols = RB / kGroups;           // columns a thread
     static constexpr int kSoft = 128 * kGroups;          // softmax threads
     static constexpr int kThreads = kSoft + 64;
@@ -187,9 +204,13 @@ struct Shared {
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
+// What a unit of `tiles` tiles weighs in the ranges: with given cuts its pieces.
+__device__ __forceinline__ int cost_of(const AttendArgs &a, int tiles, int rb) {
+    return a.pinned ? max(1, (tiles + a.piece_tiles - 1) / a.piece_tiles) : tiles + unit_cost(rb);
+}
 __device__ __forceinline__ long long weight_of(const AttendArgs &a, const Request &q, int rb) {
     if (q.bad || q.n == 0) return 0;
-    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * (q.tiles + unit_cost(rb));
+    return (long long)(a.c.h_kv) * ((q.n * a.group + rb - 1) / rb) * cost_of(a, q.tiles, rb);
 }
 
 // a / b for values that usually fit 32 bits.
@@ -197,14 +218,14 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
-// Where a range's end at x falls in a unit of `tiles` tiles: 0 its start, tiles
-// + extra its end.  Free cuts leave no part of fewer than kLeast tiles.
-__device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles, int extra) {
+// The tile at which a range's end, x into a unit of `tiles` tiles, cuts it: 0 its
+// start, tiles + 1 its end.  Free cuts leave no part of fewer than kLeast tiles.
+__device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tiles) {
     if (x <= 0) return 0;
-    if (x > tiles) return tiles + extra;
-    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + extra : int(x);
-    const int y = (int(x) + a.piece_tiles - 1) / a.piece_tiles * a.piece_tiles;
-    return y >= tiles ? tiles + extra : y;
+    if (x > tiles) return tiles + 1;
+    if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + 1 : int(x);
+    const long long y = x * a.piece_tiles;
+    return y >= tiles ? tiles + 1 : int(y);
 }
 
 template <int D, int RB>
@@ -217,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 
     gdn::pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1, kUnit = unit_cost(RB);
+    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1;
     // barriers and tensor memory while the launch before may still be running
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&s.tmem, C::kTmem);
@@ -255,8 +276,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             if (w < warp) before += s.scan[w];
             total += s.scan[w];
         }
-        // free cuts: at least four tiles a range, so that none is empty inside a unit
-        const long long most = a.pinned ? quotient(total, kUnit) : total / 4;
+        const long long most = a.pinned ? total : ranges_of(total);
         ctas = int(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
         const int cta = blockIdx.x;
         if (tid == 0 && a.parts) a.parts[2 * cta].count = a.parts[2 * cta + 1].count = 0;
@@ -411,12 +431,12 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int3 next = rows_of(a, min(r + 1, a.B - 1));  // looked at when its turn comes
             const long long w = weight_of(a, q, RB);
             if (w > 0) {
-                const int cost = q.tiles + kUnit, nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
+                const int cost = cost_of(a, q.tiles, RB), whole = q.tiles + 1;
+                const int nb = (q.n * a.group + RB - 1) / RB, units = a.c.h_kv * nb;
                 int u = begin > at ? int(quotient(begin - at, cost)) : 0;
                 for (; u < units && at + (long long)u * cost < end && ok; ++u) {
                     const long long su = at + (long long)u * cost;
-                    const int x0 = cut_at(a, begin - su, q.tiles, kUnit),
-                              x1 = cut_at(a, end - su, q.tiles, kUnit);
+                    const int x0 = cut_at(a, begin - su, q.tiles), x1 = cut_at(a, end - su, q.tiles);
                     Segment g;
                     g.r = r;
                     g.t0 = q.t0;
@@ -430,15 +450,15 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     // given cuts: a segment for each piece of the range
                     for (int x = x0; x < x1 && ok;) {
                         int to = a.pinned ? min(x + a.piece_tiles, x1) : x1;
-                        if (to >= q.tiles) to = cost;  // with the new rows and the end
+                        if (to >= q.tiles) to = whole;  // with the new rows and the end
                         g.tile0 = q.lo / kTile + x;
                         g.nc = min(to, q.tiles) - x;
-                        g.fresh = a.k != nullptr && to == cost;
+                        g.fresh = a.k != nullptr && to == whole;
                         g.out = -1;
                         if (a.pinned) {
                             if (q.tiles > a.piece_tiles)
                                 g.out = (r * a.max_pieces + x / a.piece_tiles) * (a.c.h_kv * a.blocks) + y;
-                        } else if (x0 > 0 || x1 < cost) {
+                        } else if (x0 > 0 || x1 < whole) {
                             // the first CTA whose end lies past the start, the first whose end counts as the unit's
                             const long long lo = su + kLeast, hi = su + q.tiles - kLeast + 1;
                             Part p = {};
@@ -580,40 +600,34 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         __syncwarp();
     } else {
         // ---- softmax.  This thread's position in a tile and its columns col0 .. col0 + N - 1;
-        // eight threads bring a column's queries (columns fill whole warps), kQs columns each.
-        constexpr int N = C::kCols, kQs = (RB * 8 + C::kSoft - 1) / C::kSoft;
+        // eight threads bring a column's queries (columns fill whole warps).
+        constexpr int N = C::kCols;
+        static_assert(RB * 8 <= C::kSoft, "a thread has one column's queries");
         const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N, cq = tid >> 3, sub = tid & 7;
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
         bool ok = gdn::mbar_wait_bounded(&s.seg_full[0], 0, a.wait_ns);
         if (group_or(grp, !ok)) ok = false;
         Segment g = s.seg[0];
         if (!ok) g.cols = 0;
-        uint4 wq[kQs][D / 64];
+        uint4 wq[D / 64];
         auto load_q = [&] {
-#pragma unroll
-            for (int i = 0; i < kQs; ++i) {
-                const int c = cq + i * (C::kSoft / 8), x = g.blk * RB + c, row = x / a.group;
-                if (c < RB)
-                    load_row<D>(a.q + (int64_t(g.t0) + row) * a.q_stride +
-                                    int64_t(g.hk * a.group + x - row * a.group) * D,
-                                sub, c < g.cols, wq[i]);
-            }
+            const int x = g.blk * RB + cq, row = x / a.group;
+            if (cq < RB)
+                load_row<D>(a.q + (int64_t(g.t0) + row) * a.q_stride + int64_t(g.hk * a.group + x - row * a.group) * D,
+                            sub, cq < g.cols, wq);
         };
         load_q();
         int gs = 0, gp = 0, ring = 0, fresh_seen = 0;  // score and weight tiles, ring positions, fresh tiles so far
         for (int k = 0; g.cols > 0; ++k) {
-#pragma unroll
-            for (int i = 0; i < kQs; ++i) {
-                const int c = cq + i * (C::kSoft / 8);
-                if (c >= RB) break;
-                const float down = split_row<D>(wq[i], sub, s_q, C::kNs, c, RB + c);
+            if (cq < RB) {
+                const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq);
                 if (sub == 0) {
-                    const int x = g.blk * RB + c, row = x / a.group, head = x - row * a.group;
-                    s.col_nm[c] = -kUnset;
-                    s.col_coef[c] = a.c.sm_scale * 1.4426950408889634f * down;
-                    s.col_row[c] = uint8_t(row);
-                    s.col_head[c] = uint8_t(head);
-                    s.col_out[c] = row * int(a.o_stride) + (g.hk * a.group + head) * D;
+                    const int x = g.blk * RB + cq, row = x / a.group, head = x - row * a.group;
+                    s.col_nm[cq] = -kUnset;
+                    s.col_coef[cq] = a.c.sm_scale * 1.4426950408889634f * down;
+                    s.col_row[cq] = uint8_t(row);
+                    s.col_head[cq] = uint8_t(head);
+                    s.col_out[cq] = row * int(a.o_stride) + (g.hk * a.group + head) * D;
                 }
             }
             gdn::fence_proxy_async_smem();
@@ -649,10 +663,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 auto load_z = [&](bool plain) {
                     uint32_t hi[N], lo[N];
                     const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
-                    if constexpr (N == 32) {
-                        tc::ld32_async(at, hi);
-                        tc::ld32_async(at + RB, lo);
-                    } else if constexpr (N == 16) {
+                    if constexpr (N == 16) {
                         tc::ld16_async(at, hi);
                         tc::ld16_async(at + RB, lo);
                     } else {
@@ -706,9 +717,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 bool move = i == 0;  // a segment's first tile sets the reference
                 if (!move) {
                     load_z(false);
-                    float over = -INFINITY;
+                    float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-                    for (int c = 0; c < N; ++c) over = fmaxf(over, z[c]);
+                    for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
+                    const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     move = group_or(grp, over > kSlack || sc.y > vref || !ok);
                 }
                 if (__builtin_expect(move, 0)) {
@@ -789,36 +801,31 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 const f2 xw2 = pair(xw, xw), xw32 = pair(32.f * xw, 32.f * xw);
                 if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
                 uint8_t *pb = s_p + (y & 1) * C::kP;
-                // sixteen columns (eight if there are no more) at a time: 16 bytes of each part
-                constexpr int W = N < 16 ? 8 : 16;
+                uint16_t e[4][N / 2];
 #pragma unroll
-                for (int c0 = 0; c0 < N; c0 += W) {
-                    uint16_t e[4][W / 2];
+                for (int c = 0; c < N / 2; ++c) {
+                    const f2 p = pair(ex2(z[2 * c]), ex2(z[2 * c + 1]));
+                    l[c] = add2(l[c], p);
+                    const float2 v = both(mul2(p, xw2));
+                    e[0][c] = uint16_t(e4m3x2(v.x, v.y));
+                    const float2 r = minus32(both(mul2(p, xw32)), f16x2_of(e[0][c]));  // exact
+                    uint32_t rest = f16x2(r.x, r.y);
+                    e[1][c] = e4m3x2_of(rest);
+                    rest = rest32(rest, f16x2_of(e[1][c]));
+                    e[2][c] = e4m3x2_of(rest);
+                    e[3][c] = e4m3x2_of(rest32(rest, f16x2_of(e[2][c])));
+                }
 #pragma unroll
-                    for (int c = 0; c < W / 2; ++c) {
-                        const f2 p = pair(ex2(z[c0 + 2 * c]), ex2(z[c0 + 2 * c + 1]));
-                        l[c0 / 2 + c] = add2(l[c0 / 2 + c], p);
-                        const float2 v = both(mul2(p, xw2));
-                        e[0][c] = uint16_t(e4m3x2(v.x, v.y));
-                        const float2 r = minus32(both(mul2(p, xw32)), f16x2_of(e[0][c]));  // exact
-                        uint32_t rest = f16x2(r.x, r.y);
-                        e[1][c] = e4m3x2_of(rest);
-                        rest = rest32(rest, f16x2_of(e[1][c]));
-                        e[2][c] = e4m3x2_of(rest);
-                        e[3][c] = e4m3x2_of(rest32(rest, f16x2_of(e[2][c])));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int b = j * RB + col0 + c0;  // byte of the row
-                        uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
-                                       tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
-                        const uint32_t w0 = join16(e[j][0], e[j][1]), w1 = join16(e[j][2], e[j][3]);
-                        if constexpr (W == 16)
-                            *reinterpret_cast<uint4 *>(dst) =
-                                make_uint4(w0, w1, join16(e[j][4], e[j][5]), join16(e[j][6], e[j][7]));
-                        else
-                            *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int b = j * RB + col0;  // byte of the row
+                    uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
+                                   tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
+                    const uint32_t w0 = join16(e[j][0], e[j][1]), w1 = join16(e[j][2], e[j][3]);
+                    if constexpr (N == 16)
+                        *reinterpret_cast<uint4 *>(dst) =
+                            make_uint4(w0, w1, join16(e[j][4], e[j][5]), join16(e[j][6], e[j][7]));
+                    else
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
                 }
                 if (!whole && grp == 0) {
                     // What no row sees may hold anything, NaN codes too, and 0 * NaN is
@@ -897,22 +904,19 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 uint16_t *o_base = a.o + int64_t(h.t0) * a.o_stride;
                 float *ws_base = a.ws_o + int64_t(h.out) * RB * D;
                 const int edge = min(min(lo_last, h.len), (h.tile0 + nc) * kTile);
-                constexpr int W = N < 16 ? N : 16;  // columns at a time
 #pragma unroll 1
-                for (int x = 0; x < C::kAtoms * (N / W); ++x) {
-                    const int at = x / (N / W), c0 = col0 + x % (N / W) * W;
+                for (int at = 0; at < C::kAtoms && col0 < h.cols; ++at) {
                     const int e = at * C::kRow + pos_in;  // this thread's element (d = 64: lanes past 63 hold none)
-                    if (c0 >= h.cols) continue;
-                    f2 acc[W / 2];
+                    f2 acc[N / 2];
 #pragma unroll
-                    for (int c = 0; c < W / 2; ++c) acc[c] = 0;
+                    for (int c = 0; c < N / 2; ++c) acc[c] = 0;
                     if (nc > 0) {
                         const f2 part = pair(1.f / 32.f, 1.f / 32.f);
 #pragma unroll
                         for (int j = 3; j >= 0; j -= 2) {  // from the last part on
-                            uint32_t u[W], v[W];
-                            const uint32_t from = tm_o + lane_base + at * C::kNp + c0;
-                            if constexpr (W == 16) {
+                            uint32_t u[N], v[N];
+                            const uint32_t from = tm_o + lane_base + at * C::kNp + col0;
+                            if constexpr (N == 16) {
                                 tc::ld16_async(from + j * RB, u);
                                 tc::ld16_async(from + (j - 1) * RB, v);
                             } else {
@@ -923,14 +927,14 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             tc::ld_fence_regs(u);
                             tc::ld_fence_regs(v);
 #pragma unroll
-                            for (int c = 0; c < W / 2; ++c) {
+                            for (int c = 0; c < N / 2; ++c) {
                                 acc[c] = fma2(acc[c], part, pair(u[2 * c], u[2 * c + 1]));
                                 acc[c] = fma2(acc[c], part, pair(v[2 * c], v[2 * c + 1]));
                             }
                         }
                         const f2 b2 = pair(back, back);
 #pragma unroll
-                        for (int c = 0; c < W / 2; ++c) acc[c] = mul2(acc[c], b2);
+                        for (int c = 0; c < N / 2; ++c) acc[c] = mul2(acc[c], b2);
                     }
                     if (e >= D) continue;
                     uint32_t odd = 0;  // new rows whose value here is not finite
@@ -941,17 +945,17 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             const bool finite = (b & 0x7f800000u) != 0x7f800000u;
                             if (!finite) odd |= 1u << j;
                             const f2 v = pair(finite ? b : 0u, finite ? b : 0u);
-                            const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + c0);
+                            const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(fresh_p + j * RB + col0);
 #pragma unroll
-                            for (int c = 0; c < W / 4; ++c) {
+                            for (int c = 0; c < N / 4; ++c) {
                                 const ulonglong2 w = p[c];
                                 acc[2 * c] = fma2(w.x, v, acc[2 * c]);
                                 acc[2 * c + 1] = fma2(w.y, v, acc[2 * c + 1]);
                             }
                         }
-                    float o[W];
+                    float o[N];
 #pragma unroll
-                    for (int c = 0; c < W / 2; ++c) {
+                    for (int c = 0; c < N / 2; ++c) {
                         o[2 * c] = both(acc[c]).x;
                         o[2 * c + 1] = both(acc[c]).y;
                     }
@@ -961,9 +965,9 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             if (odd >> j & 1) {
                                 const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
 #pragma unroll
-                                for (int c = 0; c < W; ++c)
-                                    if (uint32_t(s.col_row[c0 + c] - j) < uint32_t(w))
-                                        o[c] = fmaf(fresh_p[j * RB + c0 + c], v, o[c]);
+                                for (int c = 0; c < N; ++c)
+                                    if (uint32_t(s.col_row[col0 + c] - j) < uint32_t(w))
+                                        o[c] = fmaf(fresh_p[j * RB + col0 + c], v, o[c]);
                             }
                     }
                     // NaN of positions that only some rows see
@@ -974,19 +978,19 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                                    (int64_t(a.c.h_kv + h.hk) * T + (t & (T - 1))) * D + e];
                         if ((code & 0x7f) == 0x7f) {
 #pragma unroll
-                            for (int c = 0; c < W; ++c)
-                                if (t >= lo0 + lo1 * s.col_row[c0 + c]) o[c] = __uint_as_float(0x7fc00000u);
+                            for (int c = 0; c < N; ++c)
+                                if (t >= lo0 + lo1 * s.col_row[col0 + c]) o[c] = __uint_as_float(0x7fc00000u);
                         }
                     }
                     if (h.out < 0) {
 #pragma unroll
-                        for (int c = 0; c < W; ++c)
-                            if (c0 + c < h.cols)
-                                o_base[s.col_out[c0 + c] + e] = gdn::f32_to_bf16(o[c] * s.col_l[c0 + c]);
+                        for (int c = 0; c < N; ++c)
+                            if (col0 + c < h.cols)
+                                o_base[s.col_out[col0 + c] + e] = gdn::f32_to_bf16(o[c] * s.col_l[col0 + c]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < W; ++c)
-                            if (c0 + c < h.cols) ws_base[(c0 + c) * D + e] = o[c];
+                        for (int c = 0; c < N; ++c)
+                            if (col0 + c < h.cols) ws_base[(col0 + c) * D + e] = o[c];
                     }
                 }
             }
@@ -1155,10 +1159,10 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
     int64_t tiles = (seen + kTile - 1) / kTile;
     if (tiles < 1) tiles = 1;
     const int64_t units = int64_t(B) * c->h_kv * p.blocks;
-    const int64_t slots = 152 * (c->d == 256 || p.rb == 64 ? 1 : 2);
+    const int64_t slots = kSms * (c->d == 256 || p.rb == 64 ? 1 : 2);
     int64_t ctas;
-    if (split_tokens > 0 || tiles <= kWhole) {
-        // given cuts, or none in units so short that joining costs more than it gives
+    const bool whole = tiles <= 2 * kLeast || (tiles <= kWhole && units <= slots && 2 * units >= slots);
+    if (split_tokens > 0 || whole) {
         const int64_t t = split_tokens > 0 ? (int64_t(split_tokens) + kTile - 1) / kTile : tiles;
         p.pinned = 1;
         p.piece_tiles = int(t < tiles ? t : tiles);
@@ -1167,7 +1171,7 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
         p.parts = p.max_pieces > 1 ? ctas : 0;
     } else {
         p.piece_tiles = p.max_pieces = 1;
-        ctas = (units * (tiles + unit_cost(p.rb)) + 3) / 4;
+        ctas = ranges_of(units * (tiles + unit_cost(p.rb)));
     }
     p.ctas = int(ctas < slots ? ctas : slots);
     if (!p.pinned) p.parts = p.ctas > 1 ? 2 * int64_t(p.ctas) : 0;

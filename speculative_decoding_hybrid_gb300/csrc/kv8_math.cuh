@@ -170,8 +170,8 @@ __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, ui
 // lanes whose top log2(N) bits are k.
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
-    constexpr int kSteps = N == 32 ? 5 : N == 16 ? 4 : 3;
-    static_assert(N == 32 || N == 16 || N == 8, "columns a thread");
+    constexpr int kSteps = N == 16 ? 4 : 3;
+    static_assert(N == 16 || N == 8, "columns a thread");
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const int off = 16 >> s, half = N >> (s + 1);
