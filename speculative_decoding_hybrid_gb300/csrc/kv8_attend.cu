@@ -311,8 +311,6 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    float *fresh_p = reinterpret_cast<float *>(s_fk);  // [16][RB], once the fresh keys' product is done
-    static_assert(RB * 16 * 4 <= C::kFresh, "weights of the fresh rows");
     const uint32_t tm = s.tmem, tm_o = tm + 2 * C::kNs;
 
     if (warp == kCopyWarp) {
@@ -505,6 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         const bool leader = elect_one();
         bool ok = true;
         int ring = 0, gs = 0, gp = 0;  // ring positions, score tiles and weight tiles before this segment
+        int last_fresh = -1;           // the last tile of new keys
         for (int k = 0; ok; ++k) {
             ok = gdn::mbar_wait_bounded(&s.seg_full[k % kQueue], (k / kQueue) & 1, a.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -513,35 +512,35 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int nc = g.nc, n = g.n, fresh = g.fresh, nt = nc + fresh;
             if (g.cols == 0) break;
             const uint16_t *kn = a.k + int64_t(g.t0) * a.k_stride + int64_t(g.hk) * D;
-            uint4 w[4][D / 64];  // the new keys, four rows a pass
             if (fresh) {
+                // the new keys, while the softmax ends the segment before: their place is free
+                // once the scores of the last ones are read
+                uint4 w[4][D / 64];  // four rows a pass
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (4 * j < n) {
                         const int row = 4 * j + (lane >> 3);
                         load_row<D>(kn + int64_t(row) * a.k_stride, lane & 7, row < n, w[j]);
                     }
+                // (a tile two or more back is waited for before the one that took its buffer)
+                const int x = last_fresh;
+                if (x >= 0 && x >= gs - 2) ok = gdn::mbar_wait_bounded(&s.s_free[x & 1], (x >> 1) & 1, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (4 * j < n) {
+                        const int row = 4 * j + (lane >> 3);
+                        const float down = split_row<D>(w[j], lane & 7, s_fk, 32, row, 16 + row);
+                        if ((lane & 7) == 0) s.fresh_k[row] = down;
+                    }
+                gdn::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&s.fk_ready);
+                last_fresh = gs + nc;
             }
             ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
             for (int i = 0; i <= nt; ++i) {
-                if (fresh && i == min(1, nc)) {
-                    // the new keys, while the softmax is at the segment's first tile; their place
-                    // is free once the segment before is done
-                    if (ok && k > 0)
-                        ok = gdn::mbar_wait_bounded(&s.seg_empty[(k - 1) % kQueue], ((k - 1) / kQueue) & 1, a.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (4 * j < n) {
-                            const int row = 4 * j + (lane >> 3);
-                            const float down = split_row<D>(w[j], lane & 7, s_fk, 32, row, 16 + row);
-                            if ((lane & 7) == 0) s.fresh_k[row] = down;
-                        }
-                    gdn::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) arrive(&s.fk_ready);
-                }
                 if (i < nt) {
                     const bool cached = i < nc;
                     const int pos = ring + k_pos(i), slot = pos % C::kSlots, x = gs + i;
@@ -639,6 +638,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             // a row sees positions from lo0 + row * lo1 on (g.lo is row 0's, and not negative)
             const int lo0 = a.c.window ? g.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
             const int lo_last = lo0 + lo1 * s.col_row[g.cols - 1];
+            // [16][RB], the new rows' weights, where the next tile's would go
+            float *fresh_p = reinterpret_cast<float *>(s_p + ((gp + nc) & 1) * C::kP);
             f2 l[N / 2];
             float z[N];
 #pragma unroll
@@ -787,7 +788,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 if (lane == 0) arrive(&s.s_free[x & 1]);
 
                 if (is_fresh) {
-                    if (pos_in < 16) {
+                    if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
+                    if (pos_in < 16 && ok) {
 #pragma unroll
                         for (int c = 0; c < N; c += 2) {
                             const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
