@@ -135,7 +135,7 @@ struct Cfg {
     static constexpr int kNs = 2 * RB;                   // score columns
     static constexpr int kNp = 4 * RB;                   // weight columns
     static constexpr int kPRow = RB == 8 ? 64 : RB == 64 ? 128 : kNp;  // bytes of a weight tile's row (64 or 128)
-    static constexpr int kFresh = 32 * D > 64 * RB ? 32 * D : 64 * RB;  // bytes of the fresh keys, and of the values
+    static constexpr int kFresh = 32 * D;  // bytes of the fresh keys, and of the values
     static constexpr int kQ = kNs * D;
     static constexpr int kP = kTile * (RB == 8 ? 64 : kNp);
     static constexpr int kSlot = kTile * D;
@@ -515,25 +515,21 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             if (fresh) {
                 // the new keys, while the softmax ends the segment before: their place is free
                 // once the scores of the last ones are read
-                uint4 w[4][D / 64];  // four rows a pass
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * j < n) {
-                        const int row = 4 * j + (lane >> 3);
-                        load_row<D>(kn + int64_t(row) * a.k_stride, lane & 7, row < n, w[j]);
-                    }
                 // (a tile two or more back is waited for before the one that took its buffer)
                 const int x = last_fresh;
                 if (x >= 0 && x >= gs - 2) ok = gdn::mbar_wait_bounded(&s.s_free[x & 1], (x >> 1) & 1, a.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                uint4 w[D / 64], next[D / 64];  // four rows a pass
+                load_row<D>(kn + int64_t(lane >> 3) * a.k_stride, lane & 7, (lane >> 3) < n, w);
+#pragma unroll 1
+                for (int row = lane >> 3; row - (lane >> 3) < n; row += 4) {
+                    load_row<D>(kn + int64_t(row + 4) * a.k_stride, lane & 7, row + 4 < n, next);
+                    const float down = split_row<D>(w, lane & 7, s_fk, 32, row, 16 + row);
+                    if ((lane & 7) == 0) s.fresh_k[row] = down;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (4 * j < n) {
-                        const int row = 4 * j + (lane >> 3);
-                        const float down = split_row<D>(w[j], lane & 7, s_fk, 32, row, 16 + row);
-                        if ((lane & 7) == 0) s.fresh_k[row] = down;
-                    }
+                    for (int e = 0; e < D / 64; ++e) w[e] = next[e];
+                }
                 gdn::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(&s.fk_ready);
@@ -716,13 +712,16 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     }
                 };
                 bool move = i == 0;  // a segment's first tile sets the reference
-                if (!move) {
-                    load_z(false);
+#pragma unroll 1
+                for (;;) {
+                    load_z(move);
+                    if (move) break;
                     float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
                     for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
                     const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     move = group_or(grp, over > kSlack || sc.y > vref || !ok);
+                    if (!move) break;
                 }
                 if (__builtin_expect(move, 0)) {
                     // ---- the reference moves (or a wait ran out)
@@ -730,7 +729,6 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         ok = false;
                         break;
                     }
-                    load_z(true);
 #pragma unroll
                     for (int c = 0; c < N; ++c) {
                         const float top = warp_max(z[c]);
@@ -837,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (ok) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
                     const bool none = t < g.lo || t >= g.len, some = !none && t < lo_last;
                     if (ok && (none || some)) {
-#pragma unroll
+#pragma unroll 2
                         for (int e = 0; e < C::kAtoms * C::kRow / 16; ++e) {
                             uint4 *p = reinterpret_cast<uint4 *>(
                                 s_ring + slot * C::kSlot + e / (C::kRow / 16) * kTile * C::kRow +
@@ -941,7 +939,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (e >= D) continue;
                     uint32_t odd = 0;  // new rows whose value here is not finite
                     if (h.fresh)
-#pragma unroll 2
+#pragma unroll 1
                         for (int j = 0; j < h.n; ++j) {
                             const uint32_t b = uint32_t(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]) << 16;
                             const bool finite = (b & 0x7f800000u) != 0x7f800000u;
@@ -963,6 +961,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     }
                     if (odd) {  // such a value reaches the rows that see it, and no others
                         const int w = a.c.window ? a.c.window : GDN_MAX_ROWS;
+#pragma unroll 1
                         for (int j = 0; j < h.n; ++j)
                             if (odd >> j & 1) {
                                 const float v = gdn::bf16_to_f32(reinterpret_cast<const uint16_t *>(s_fv)[j * D + e]);
@@ -973,6 +972,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             }
                     }
                     // NaN of positions that only some rows see
+#pragma unroll 1
                     for (int t = max(h.lo, h.tile0 * kTile); t < edge; ++t) {
                         const int page = a.table[int64_t(h.r) * a.table_stride + (t >> shift)];
                         const uint8_t code =
