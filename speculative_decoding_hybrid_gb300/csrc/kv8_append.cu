@@ -1,7 +1,7 @@
 // Commit of rows into the paged 8-bit key/value cache, and page copies
 // (sm_103a).
 //
-// kv8_append: one CTA per (page touched, kv head and K or V).  A thread holds
+// kv8_append: a CTA, or a warp of one, per (page touched, kv head and K or V).  A thread holds
 // its pieces of 16 new elements (32 bytes of bf16) in registers between the two
 // things done with them: the page's largest magnitude, which fixes the scale 2^e
 // with amax <= 448 * 2^e, and the rounding to codes.  A power of two makes x /
@@ -15,10 +15,12 @@ namespace {
 
 constexpr int kThreads = 256;  // of a page copy, and of an append of whole pages
 constexpr int kRowThreads = 64;  // of an append of at most 256 pieces a page: a few rows, small pages
+constexpr int kPack = 4;         // units of one warp in a CTA
 
 struct AppendArgs {
     kv8_cache c;
     int32_t layer, B, row_capacity, table_pages, max_rows;
+    int32_t pages;  // that there are units for: of every request, or (ragged) of all together
     int64_t table_stride;
     const int32_t *cu_rows, *cache_len, *table, *accept_len;
     const uint16_t *k, *v;
@@ -73,10 +75,11 @@ __device__ __forceinline__ Rows rows_of(const AppendArgs &a, int r) {
     return q;
 }
 
-// One page of request rows `q`, its table's page len / T + step: all threads of a CTA.
-// PIECES: the most 16-element pieces of a page a thread may hold.
+// One page of request rows `q`, its table's page len / T + step: a unit's THREADS threads,
+// a CTA's or a warp's.  PIECES: the most 16-element pieces of a page a thread may hold.
 template <int THREADS, int PIECES>
 __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Rows &q, int step, int hv) {
+    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
     const int is_v = hv >= a.c.h_kv, h = hv - is_v * a.c.h_kv, T = a.c.page_tokens, d = a.c.d;
     const int page_shift = 31 - __clz(T), per_shift = 31 - __clz(d) - 4;  // 2^per_shift pieces a token
     const int t0 = q.t0, len = q.len;
@@ -95,7 +98,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
     const int page = a.table[int64_t(r) * a.table_stride + pj];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
-        const int i = threadIdx.x + u * THREADS;
+        const int i = tid + u * THREADS;
         w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
         if (i < total) {
             const int in = (i & ((1 << per_shift) - 1)) * 16;
@@ -105,7 +108,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
         }
     }
     if (page < 0 || page >= a.c.num_pages) {
-        if (threadIdx.x == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+        if (tid == 0) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
         return;
     }
     uint8_t *codes = a.c.kv + int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
@@ -120,26 +123,27 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) m = max_finite_of(w[u][1], max_finite_of(w[u][0], m));
     }
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
-    __shared__ uint32_t red[THREADS / 32];
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wm;
-    __syncthreads();
-    uint32_t top = 0;
+    uint32_t top = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
+    if constexpr (THREADS > 32) {
+        __shared__ uint32_t red[THREADS / 32];
+        if ((tid & 31) == 0) red[tid >> 5] = top;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
+        for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
+    }
     const int e = kv8::scale_exp(__uint_as_float(top << 16));
     const float fit = kv8::pow2i(e);
     const float now = fmaxf(was, fit);
     const float inv = 1.f / now;                   // exact: a power of two
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
-        const int i = threadIdx.x + u * THREADS;
+        const int i = tid + u * THREADS;
         if (i < total) *reinterpret_cast<uint4 *>(codes + (held * d + i * 16)) = encode16(w[u][0], w[u][1], inv);
     }
     if (held && now > was) {
         const float f = was * inv;
-#pragma unroll(THREADS == kRowThreads ? 4 : 1)
-        for (int i = threadIdx.x; i < held << per_shift; i += THREADS) {
+#pragma unroll(THREADS <= kRowThreads ? 4 : 1)
+        for (int i = tid; i < held << per_shift; i += THREADS) {
             uint4 *p = reinterpret_cast<uint4 *>(codes + int64_t(i) * 16);
             const uint4 old = *p;
             uint32_t o[4] = {old.x, old.y, old.z, old.w};
@@ -151,20 +155,24 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
             *p = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
-    // every thread has read *scale before the barrier above
-    if (threadIdx.x == 0) *scale = now;
+    // every thread has read *scale before the reduction above
+    if (tid == 0) *scale = now;
 }
 
-// RAGGED: the CTAs count the pages touched over all requests, each finding its
+constexpr int cta_of(int threads) { return threads == 32 ? 32 * kPack : threads; }
+
+// RAGGED: the units count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
 template <int THREADS, int PIECES, bool RAGGED>
-__global__ void __launch_bounds__(THREADS, PIECES <= 2 ? 2048 / THREADS : 4096 / (THREADS * PIECES))
+__global__ void __launch_bounds__(cta_of(THREADS), (PIECES <= 2 ? 2048 : 4096 / PIECES) / cta_of(THREADS))
     kv8_append_kernel(const AppendArgs a) {
     gdn::pdl_enter();
     const int lane = threadIdx.x & 31;
     const bool reports = blockIdx.x == 0 && threadIdx.x < 32;
+    const int unit = THREADS == 32 ? blockIdx.x * kPack + (threadIdx.x >> 5) : blockIdx.x;
     // the heads of a page side by side: their parts of the rows are neighbours in memory
-    const int heads = 2 * a.c.h_kv, first = blockIdx.x / heads, hv = blockIdx.x - first * heads;
+    const int heads = 2 * a.c.h_kv, first = unit / heads, hv = unit - first * heads;
+    if (first >= a.pages) return;
     const int T = a.c.page_tokens, page_shift = 31 - __clz(T);
     if (a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT)) return;
     if constexpr (!RAGGED) {
@@ -200,8 +208,8 @@ __global__ void __launch_bounds__(THREADS, PIECES <= 2 ? 2048 / THREADS : 4096 /
                 total += __shfl_sync(0xffffffffu, incl, 31);
             }
             if (r >= 0) append_page<THREADS, PIECES>(a, r, rows_of(a, r), step, hv);
-            at += gridDim.x / heads;
-            __syncthreads();
+            at += a.pages;
+            if (THREADS > 32) __syncthreads();
         } while (at < total);
     }
 }
@@ -290,28 +298,32 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     // commit more than the few CTAs without rows it saves, and a ragged prompt's less.
     const int64_t each = (max_rows + T - 2) / T + 1, all = row_capacity / T + int64_t(2) * B;
     const bool ragged = all < each * B / 2;
-    const int64_t ctas = (ragged ? all : each) * 2 * cache->h_kv;
-    if (ctas > 0x7fffffff) return GDN_ERR_ARG;
-    const dim3 grid(unsigned(ctas), 1, unsigned(ragged ? 1 : B));
+    const int64_t pages = ragged ? all : each, units = pages * 2 * cache->h_kv;
+    if (units > 0x7fffffff - kPack) return GDN_ERR_ARG;
+    a.pages = int(pages);
     const int most = max_rows < T ? max_rows : T;
     const auto launch = [&](auto kernel, int threads) {
-        return gdn_host::launch_pdl(kernel, grid, dim3(unsigned(threads)), 0, static_cast<cudaStream_t>(stream), a);
+        const int64_t ctas = threads == 32 ? (units + kPack - 1) / kPack : units;
+        return gdn_host::launch_pdl(kernel, dim3(unsigned(ctas), 1, unsigned(ragged ? 1 : B)),
+                                    dim3(unsigned(cta_of(threads))), 0, static_cast<cudaStream_t>(stream), a);
     };
-    // Small CTAs where a page has few new pieces: a large batch's commit is then all in
+    // Few threads where a page has few new pieces: a large batch's commit is then all in
     // flight at once (256 requests x 4 rows 6.4 us with 256 threads, 3.6 with 64), and a
     // prompt into pages of 16 tokens keeps its threads busy (278 against 99 us).  Four
     // pieces a thread are the best of 2, 4 and 8 while a CTA stays within 256 threads
     // (99, 91 and 92 us at 512 pieces a page).
     const int all_pieces = most * cache->d / 16;
     if (ragged) {
-        if (all_pieces <= 2 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 2, true>, kRowThreads);
-        if (all_pieces <= 4 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 4, true>, kRowThreads);
+        if (all_pieces <= 64) return launch(kv8_append_kernel<32, 2, true>, 32);
+        if (all_pieces <= 128) return launch(kv8_append_kernel<32, 4, true>, 32);
+        if (all_pieces <= 256) return launch(kv8_append_kernel<kRowThreads, 4, true>, kRowThreads);
         if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, true>, 128);
         if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, true>, kThreads);
         return launch(kv8_append_kernel<kThreads, 8, true>, kThreads);
     }
-    if (all_pieces <= 2 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 2, false>, kRowThreads);
-    if (all_pieces <= 4 * kRowThreads) return launch(kv8_append_kernel<kRowThreads, 4, false>, kRowThreads);
+    if (all_pieces <= 64) return launch(kv8_append_kernel<32, 2, false>, 32);
+    if (all_pieces <= 128) return launch(kv8_append_kernel<32, 4, false>, 32);
+    if (all_pieces <= 256) return launch(kv8_append_kernel<kRowThreads, 4, false>, kRowThreads);
     if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, false>, 128);
     if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, false>, kThreads);
     return launch(kv8_append_kernel<kThreads, 8, false>, kThreads);
