@@ -13,9 +13,8 @@
 
 namespace {
 
-constexpr int kThreads = 256;  // of a page copy, and of an append of whole pages
-constexpr int kRowThreads = 64;  // of an append of at most 256 pieces a page: a few rows, small pages
-constexpr int kPack = 4;         // units of one warp in a CTA
+constexpr int kThreads = 256;  // of a page copy
+constexpr int kPack = 4;       // units of one warp in a CTA
 
 struct AppendArgs {
     kv8_cache c;
@@ -142,7 +141,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
     }
     if (held && now > was) {
         const float f = was * inv;
-#pragma unroll(THREADS <= kRowThreads ? 4 : 1)
+#pragma unroll(THREADS <= 64 ? 4 : 1)
         for (int i = tid; i < held << per_shift; i += THREADS) {
             uint4 *p = reinterpret_cast<uint4 *>(codes + int64_t(i) * 16);
             const uint4 old = *p;
@@ -160,11 +159,15 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
 }
 
 constexpr int cta_of(int threads) { return threads == 32 ? 32 * kPack : threads; }
+// Registers for a thread's pieces (8 words each) against threads in flight: 8 pieces at
+// 512, 768 and 896 threads an SM 55, 50 and 52 us (a prompt of 8 requests, 1000..20000
+// tokens, 8 heads of 128, pages of 32), 4 pieces at 1024, 1280 and 1536 (pages of 16) 54, 54 and 60.
+constexpr int threads_an_sm(int pieces) { return pieces == 2 ? 2048 : pieces == 4 ? 1024 : 768; }
 
 // RAGGED: the units count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
 template <int THREADS, int PIECES, bool RAGGED>
-__global__ void __launch_bounds__(cta_of(THREADS), (PIECES <= 2 ? 2048 : 4096 / PIECES) / cta_of(THREADS))
+__global__ void __launch_bounds__(cta_of(THREADS), threads_an_sm(PIECES) / cta_of(THREADS))
     kv8_append_kernel(const AppendArgs a) {
     gdn::pdl_enter();
     const int lane = threadIdx.x & 31;
@@ -307,26 +310,26 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
         return gdn_host::launch_pdl(kernel, dim3(unsigned(ctas), 1, unsigned(ragged ? 1 : B)),
                                     dim3(unsigned(cta_of(threads))), 0, static_cast<cudaStream_t>(stream), a);
     };
-    // Few threads where a page has few new pieces: a large batch's commit is then all in
-    // flight at once (256 requests x 4 rows 6.4 us with 256 threads, 3.6 with 64), and a
-    // prompt into pages of 16 tokens keeps its threads busy (278 against 99 us).  Four
-    // pieces a thread are the best of 2, 4 and 8 while a CTA stays within 256 threads
-    // (99, 91 and 92 us at 512 pieces a page).
+    // As few threads a page as hold its new pieces, eight each: units of one warp reduce
+    // without a barrier (2 rows x 512 requests 17.3 us with 64 threads a page, 9.2 with
+    // 32; the prompt below into pages of 16 tokens 97 and 54), and eight pieces keep more
+    // of a prompt in flight than four by twice the threads (60 and 50 us in pages of 32,
+    // 56 and 50 in pages of 128).  Two pieces, or four, where no page has more.
     const int all_pieces = most * cache->d / 16;
     if (ragged) {
         if (all_pieces <= 64) return launch(kv8_append_kernel<32, 2, true>, 32);
         if (all_pieces <= 128) return launch(kv8_append_kernel<32, 4, true>, 32);
-        if (all_pieces <= 256) return launch(kv8_append_kernel<kRowThreads, 4, true>, kRowThreads);
-        if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, true>, 128);
-        if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, true>, kThreads);
-        return launch(kv8_append_kernel<kThreads, 8, true>, kThreads);
+        if (all_pieces <= 256) return launch(kv8_append_kernel<32, 8, true>, 32);
+        if (all_pieces <= 512) return launch(kv8_append_kernel<64, 8, true>, 64);
+        if (all_pieces <= 1024) return launch(kv8_append_kernel<128, 8, true>, 128);
+        return launch(kv8_append_kernel<256, 8, true>, 256);
     }
     if (all_pieces <= 64) return launch(kv8_append_kernel<32, 2, false>, 32);
     if (all_pieces <= 128) return launch(kv8_append_kernel<32, 4, false>, 32);
-    if (all_pieces <= 256) return launch(kv8_append_kernel<kRowThreads, 4, false>, kRowThreads);
-    if (all_pieces <= 512) return launch(kv8_append_kernel<128, 4, false>, 128);
-    if (all_pieces <= 1024) return launch(kv8_append_kernel<kThreads, 4, false>, kThreads);
-    return launch(kv8_append_kernel<kThreads, 8, false>, kThreads);
+    if (all_pieces <= 256) return launch(kv8_append_kernel<32, 8, false>, 32);
+    if (all_pieces <= 512) return launch(kv8_append_kernel<64, 8, false>, 64);
+    if (all_pieces <= 1024) return launch(kv8_append_kernel<128, 8, false>, 128);
+    return launch(kv8_append_kernel<256, 8, false>, 256);
 }
 
 extern "C" int kv8_copy_pages(const kv8_cache *cache, int32_t n, const int32_t *src, const int32_t *dst,
