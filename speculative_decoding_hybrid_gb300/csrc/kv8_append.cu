@@ -1,14 +1,17 @@
 // Commit of rows into the paged 8-bit key/value cache, and page copies
 // (sm_103a).
 //
-// kv8_append: a CTA, or a warp of one, per (page touched, kv head and K or V).  A thread holds
-// its pieces of 16 new elements (32 bytes of bf16) in registers between the two
-// things done with them: the page's largest magnitude, which fixes the scale 2^e
-// with amax <= 448 * 2^e, and the rounding to codes.  A power of two makes x /
-// scale exact, so codes do not depend on the order of appends, and a scale that
-// grows moves earlier codes exactly unless they fall into e4m3's subnormals.
-// HBM-bound on prompts (2 bytes read and 1 written a value): the new rows are
-// asked for before the page they go to is known.
+// kv8_append: a unit, a CTA or a warp of one, per (page touched, kv head and K or
+// V).  A thread holds its pieces of 16 new elements (32 bytes of bf16) in registers
+// between the two things done with them: the page's largest magnitude, which fixes
+// the scale 2^e with amax <= 448 * 2^e, and the rounding to codes, so the rows are
+// read once.  A power of two makes x / scale exact: a code is x rounded once, to
+// e4m3's 4 bits, codes do not depend on the order of appends, and a scale that grows
+// moves earlier codes exactly unless they fall into e4m3's subnormals.
+// HBM-bound on prompts (2 bytes read and 1 written a value): the new rows are asked
+// for before the page they go to is known.  8 prompts of 512..32768 tokens, 8 heads of
+// 128, pages of 64: 88 us, 6.45 TB/s, 95 % of a copy's rate.  A decode's commit is
+// a launch and one chain of loads: 4 rows x 256 requests, 2 heads of 256: 3.4 us.
 #include "kv8_math.cuh"
 
 namespace {
@@ -226,7 +229,8 @@ struct CopyArgs {
 
 constexpr int kPiece = 16384;
 
-// One CTA per (16 KB piece of a page of a layer, layer, pair).
+// One CTA per (16 KB piece of a page of a layer, layer, pair): all of its loads before
+// its first store.  A copy, bound by HBM: 1.97 GB moved in 280 us, 7.02 TB/s.
 __global__ void __launch_bounds__(kThreads) kv8_copy_kernel(const CopyArgs a) {
     gdn::pdl_enter();
     const int64_t id = blockIdx.x;
@@ -297,10 +301,13 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     a.status = dev_status;
     const int T = cache->page_tokens;
     // n rows starting anywhere touch at most (T - 1 + n - 1) / T + 1 pages, and all
-    // requests together at most row_capacity / T + 2 B.  The scan costs a decode's
-    // commit more than the few CTAs without rows it saves, and a ragged prompt's less.
+    // requests together at most row_capacity / T + 2 B.  Counting those saves units
+    // without a page (8 requests of 512..32768 tokens 114 us without, 88 with; of
+    // 1000..20000 into pages of 16, heads of 64, 46 and 37) and costs each unit a scan,
+    // of 32 requests at a time (95 requests of 1..98 tokens 9.4 us without, 11.2 with; 256
+    // of 4 rows 3.6 and 7.6).
     const int64_t each = (max_rows + T - 2) / T + 1, all = row_capacity / T + int64_t(2) * B;
-    const bool ragged = all < each * B / 2;
+    const bool ragged = all * (2 + B / 16) < each * B * 2;
     const int64_t pages = ragged ? all : each, units = pages * 2 * cache->h_kv;
     if (units > 0x7fffffff - kPack) return GDN_ERR_ARG;
     a.pages = int(pages);
