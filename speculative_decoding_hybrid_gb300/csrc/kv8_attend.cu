@@ -33,6 +33,20 @@
 // fp32 in the epilogue.  A unit inside one range is written directly; the parts
 // of a cut one leave (m, l, O) in the workspace for kv8_join_kernel.  With a
 // given split the cuts are at its multiples instead, whatever the ranges.
+//
+// Roundings: q and the new keys are split exactly; a weight keeps 14 bits or more in
+// its parts, which the products add in fp32; scores, statistics and outputs are
+// fp32, and an output is rounded once, to bf16.
+//
+// What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
+// of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 135
+// us, 5.82 TB/s, 86 %) and long requests (256k tokens: 269 MB in 53 us, 5.06 TB/s, 75
+// %, of which about 5 us are the join and 4 the start; 16 requests of a mixed batch 258
+// MB in 52.6 us, 72 %); the softmax's instructions from 64 columns on (16 rows x 32
+// requests, 4 heads of 128: 129 us, 4.8 times what HBM would need); the chain from a
+// segment's queries to its outputs, about 4 us, where requests are short, and then
+// also the fetching of its instructions: loops there are rolled wherever that costs
+// nothing.
 #include <cuda.h>
 
 #include "kv8_math.cuh"
@@ -45,16 +59,17 @@ constexpr int kTile = 128;      // positions a tile
 constexpr int kSms = 152;
 // Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
 // is 2^-25, so 2^-27 of a weight at the reference.  More slack moves the
-// reference less often and costs that many bits at the low end.
+// reference less often (4 rows x 256 requests 152 us with 3, 136 with 6) and costs
+// that many bits at the low end.
 constexpr float kBase = 4.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 
-// Tiles that a unit's queries, new rows and outputs cost as much as.  Cycles a
-// segment over cycles a tile are 4.3, 2.5, 5.5 and 8.6 for RB = 8 .. 64; of these and
-// two tiles more or less, these were the fastest (4 rows x 256 requests 146, 141 and
-// 142 us at 4, 6 and 8).
+// Tiles that a unit's queries, new rows and outputs cost as much as.  A fit of a CTA's
+// cycles to its tiles and segments gives 3 to 7; of those and two tiles more or less,
+// these were the fastest (4 rows x 256 requests 140, 136 and 139 us at 4, 6 and 8,
+// 16 rows x 32 requests 129, 129 and 136 at 6, 8 and 10).
 __host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : 4; }
 
 // Units of at most 2 * kLeast tiles are not cut, nor, where they fill half of the CTAs
@@ -148,7 +163,8 @@ struct Cfg {
     static constexpr int kCols = RB / kGroups;           // columns a thread
     static constexpr int kSoft = 128 * kGroups;          // softmax threads
     static constexpr int kThreads = kSoft + 64;
-    // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule it out
+    // CTAs an SM: two, unless 512 tensor-memory columns or two sets of 32 KB slots rule
+    // it out (three at d = 64 change nothing: 152 requests of 1 row 45.5 and 45.7 us)
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
     static constexpr int kFixed = 2 * kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024;
     static constexpr int kStatic = RB == 64 ? 4096 : D == 64 ? 2560 : 2048;  // bound on sizeof(Shared)
@@ -183,7 +199,7 @@ struct Shared {
     uint64_t seg_empty[kQueue];  // of the softmax warps and the product warp
     float2 scales[C::kScales][8];
     alignas(16) float col_nm[RB], col_coef[RB], col_fac[RB];  // -m, score factor, rescaling
-    float col_l[RB];
+    float col_l[RB];  // what a moving reference adds to z; at the end 1 / l
     union {
         float col_max[4][RB];
         long long scan[C::kThreads / 32];
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int nc = g.nc, nt = nc + g.fresh;
             // a row sees positions from lo0 + row * lo1 on (g.lo is row 0's, and not negative)
             const int lo0 = a.c.window ? g.len + (a.k ? 1 : 0) - a.c.window : 0, lo1 = a.c.window && a.k ? 1 : 0;
-            const int lo_last = lo0 + lo1 * s.col_row[g.cols - 1];
+            const int lo_last = lo0 + lo1 * s.col_row[g.cols - 1], lo_request = lo0 + lo1 * (g.n - 1);
             // [16][RB], the new rows' weights, where the next tile's would go
             float *fresh_p = reinterpret_cast<float *>(s_p + ((gp + nc) & 1) * C::kP);
             f2 l[N / 2];
@@ -656,8 +672,12 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
                 tc::fence_after();
 
-                // z - m of every column (m = 0 where the reference is to move)
-                auto load_z = [&](bool plain) {
+                // While some row of the request may not have seen a position (a segment's first
+                // tile, and those that its window begins in or past) every column's reference
+                // follows its largest score, which z holds as it is; from then on z is against
+                // the reference.  Both go by the request alone.
+                const bool first = i == 0 || lo_request >= (is_fresh ? g.len : (g.tile0 + i) * kTile);
+                {
                     uint32_t hi[N], lo[N];
                     const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
                     if constexpr (N == 16) {
@@ -689,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     for (int c = 0; c < N; c += 4) {
                         const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s.col_coef + col0 + c);
                         ulonglong2 nm = make_ulonglong2(0, 0);
-                        if (!plain) nm = *reinterpret_cast<const ulonglong2 *>(s.col_nm + col0 + c);
+                        if (!first) nm = *reinterpret_cast<const ulonglong2 *>(s.col_nm + col0 + c);
                         const float2 b0 = both(fma2(v[c / 2], mul2(sx, f.x), nm.x)),
                                      b1 = both(fma2(v[c / 2 + 1], mul2(sx, f.y), nm.y));
                         z[c] = b0.x;
@@ -710,18 +730,14 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         for (int c = 0; c < N; ++c)
                             z[c] = t < g.len && t >= lo0 + lo1 * s.col_row[col0 + c] ? z[c] : -INFINITY;
                     }
-                };
-                bool move = i == 0;  // a segment's first tile sets the reference
-#pragma unroll 1
-                for (;;) {
-                    load_z(move);
-                    if (move) break;
+                }
+                bool move = first;
+                if (!first) {
                     float top[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
                     for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
                     const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     move = group_or(grp, over > kSlack || sc.y > vref || !ok);
-                    if (!move) break;
                 }
                 if (__builtin_expect(move, 0)) {
                     // ---- the reference moves (or a wait ran out)
@@ -742,9 +758,11 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         const float was = -s.col_nm[c];
                         const float top = fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]),
                                                 fmaxf(s.col_max[2][c], s.col_max[3][c]));
-                        const float now = fmaxf(top, was);
-                        s.col_fac[c] = ex2(was - now);
+                        // columns within the slack stay, or a column's bits would go by its neighbours
+                        const float now = first ? fmaxf(top, was) : top > kSlack ? was + top : was;
                         s.col_nm[c] = -now;
+                        s.col_fac[c] = ex2(was - now);
+                        s.col_l[c] = first ? -now : was - now;
                     }
                     const float vnow = fmaxf(
                         fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]), fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
@@ -755,8 +773,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 #pragma unroll
                     for (int c = 0; c < N; c += 2) {
                         l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(s.col_fac + col0 + c));
-                        z[c] += s.col_nm[col0 + c];
-                        z[c + 1] += s.col_nm[col0 + c + 1];
+                        z[c] += s.col_l[col0 + c];
+                        z[c + 1] += s.col_l[col0 + c + 1];
                     }
                     if (i > 0) {
                         ok = gdn::mbar_wait_bounded(&s.pv_done[(y - 1) & 1], ((y - 1) >> 1) & 1, a.wait_ns);
@@ -1027,7 +1045,8 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 // with a running M.  Groups of d/4 threads.  With few pieces a group joins a column
 // by itself; with many the groups share one column's pieces, so that their loads are
 // in flight together.  Which of the two, and so the order of the sums, goes by the
-// pieces alone.  Free cuts: a CTA for each part, the parts of a unit sharing its
+// pieces alone.  It is latency: 2 to 5 us behind the attention, whose end hides part
+// of its launch.  Free cuts: a CTA for each part, the parts of a unit sharing its
 // columns.  Given cuts: a CTA for each `per_cta` columns of a unit.
 constexpr int kJoin = 512, kFew = 8;
 
@@ -1153,6 +1172,9 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
     Plan p{};
     const int64_t cols = int64_t(max_rows) * (c->h_q / c->h_kv);
     const int most = c->d == 256 ? 32 : 64;
+    // the narrowest block that holds a request's columns: the work a tile costs goes by its
+    // width (1 row x 256 requests, 4 columns: 63 us in 8, 80 in 16, 104 in 32), and a wider
+    // one reads the cache less often (16 rows, 128 columns: 135 us by 32, 129 by 64)
     p.rb = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || most == 32 ? 32 : 64;
     p.blocks = int((cols + p.rb - 1) / p.rb);
     // positions a request's rows can see, and the tiles they may lie in

@@ -258,6 +258,30 @@ def test_pinned_pieces_make_bits_independent_of_the_batch(cuda_dev):
     assert torch.equal(again, o)
 
 
+@pytest.mark.parametrize("d,h_kv,group,rows", [(64, 2, 8, 2), (128, 1, 8, 2), (256, 1, 8, 2), (256, 2, 8, 1),
+                                               (64, 1, 4, 4), (128, 2, 16, 4)])
+@pytest.mark.parametrize("window", [0, 222])  # 222: row 0 alone sees one position of a tile
+def test_pinned_pieces_make_bits_independent_of_max_rows(cuda_dev, d, h_kv, group, rows, window):
+    """Scores that grow along the cache move a column's reference again and again, at other tiles than its
+    neighbours': how many columns a block has (it goes by max_rows) must not show."""
+    lens = [1500, 700]
+    cache = ku.Cache(lens, h_kv * group, h_kv, d, 64, seed=23)
+    c, o, lse, _, cu, (table, length, cu_t), (qt, kt, vt) = run(cache, [rows, rows], cuda_dev, window=window,
+                                                             split=1024)
+    for r, n in enumerate(lens):  # keys eight times larger every four pages
+        for j in range(-(-n // 64)):
+            c.scale[table[r, j].long(), :, :, 0] = 2.0 ** (3 * (j // 4) - 9)
+    want = None
+    for most in (rows, 4, 8, 16):
+        o, lse = c.attend(0, table, length, cu_t, qt, kt, vt, max_len=1500, max_rows=max(rows, most),
+                          split_tokens=1024, want_lse=True)
+        assert torch.isfinite(lse).all()
+        if want is None:
+            want = o, lse
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), most
+    assert int(c.status.item()) == 0
+
+
 def test_another_stream_and_repeats(cuda_dev):
     cache = ku.Cache([2000, 50], 8, 2, 128, 64, seed=17)
     c, o, lse, _, _, args, (qt, kt, vt) = run(cache, [4, 4], cuda_dev)
