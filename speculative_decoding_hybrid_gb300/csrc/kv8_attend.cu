@@ -156,10 +156,12 @@ struct Cfg {
     static constexpr int kSlot = kTile * D;
     // Groups of four softmax warps, each with its share of the columns: a warp waits
     // on its own chain of loads, exponentials and conversions most of the time, so an
-    // SM wants eight of them (4 rows x 256 requests 362 us with four, 279 with eight),
-    // and sixteen where 64 columns leave the products time (16 rows x 32 requests 134
-    // us with eight, 128 with sixteen, whose 96 registers spill a little).
-    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 256 ? 2 : 1) : RB == 32 ? 2 : 4;
+    // SM wants eight of them or more (171 requests of 2 rows, 12 columns of 256: 43 us
+    // with four, 37 with eight; 64 of 4 rows, 16 columns of 128, two CTAs an SM: 34.7
+    // us with eight, 32.2 with sixteen; at d = 64 it is 47.5 and 49), and sixteen where
+    // 64 columns leave the products time (16 rows x 32 requests 134 us with eight, 129
+    // with sixteen, whose 96 registers spill a little).
+    static constexpr int kGroups = RB <= 8 ? 1 : RB == 16 ? (D == 64 ? 1 : 2) : RB == 32 ? 2 : 4;
     static constexpr int kCols = RB / kGroups;           // columns a thread
     static constexpr int kSoft = 128 * kGroups;          // softmax threads
     static constexpr int kThreads = kSoft + 64;
