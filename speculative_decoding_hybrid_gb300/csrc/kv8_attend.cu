@@ -1173,19 +1173,25 @@ struct Plan {
 Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, int32_t split_tokens) {
     Plan p{};
     const int64_t cols = int64_t(max_rows) * (c->h_q / c->h_kv);
-    const int most = c->d == 256 ? 32 : 64;
-    // the narrowest block that holds a request's columns: the work a tile costs goes by its
-    // width (1 row x 256 requests, 4 columns: 63 us in 8, 80 in 16, 104 in 32), and a wider
-    // one reads the cache less often (16 rows, 128 columns: 135 us by 32, 129 by 64)
-    p.rb = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || most == 32 ? 32 : 64;
-    p.blocks = int((cols + p.rb - 1) / p.rb);
     // positions a request's rows can see, and the tiles they may lie in
     int64_t seen = max_len;
     if (c->window && c->window < seen) seen = int64_t(c->window) + kTile;
     int64_t tiles = (seen + kTile - 1) / kTile;
     if (tiles < 1) tiles = 1;
-    const int64_t units = int64_t(B) * c->h_kv * p.blocks;
-    const int64_t slots = kSms * (c->d == 256 || p.rb == 64 ? 1 : 2);
+    const auto slots_of = [&](int rb) { return int64_t(kSms) * (c->d == 256 || rb == 64 ? 1 : 2); };
+    const auto units_of = [&](int rb) { return int64_t(B) * c->h_kv * ((cols + rb - 1) / rb); };
+    // the narrowest block that holds a request's columns: the work a tile costs goes by its
+    // width (1 row x 256 requests, 4 columns: 63 us in 8, 80 in 16, 104 in 32), and a wider
+    // one reads the cache less often (16 rows, 128 columns: 135 us by 32, 129 by 64) ...
+    const int widest = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || c->d == 256 ? 32 : 64;
+    // ... or narrower ones, where every one of them can have its CTA and there are few tiles
+    // an SM: then they share tiles that are in L2, and a unit's ends are shorter (32 columns of
+    // 256, one request of 2 heads: 422 tokens 15.0 us in 32, 11.7 in 8, 8000 tokens 17.5 and
+    // 15.9; 512 units of 1 tile 42 in 32, 52 in 16)
+    p.rb = 8;
+    while (p.rb < widest && (units_of(p.rb) > slots_of(p.rb) || units_of(p.rb) * tiles > 4 * kSms)) p.rb *= 2;
+    p.blocks = int((cols + p.rb - 1) / p.rb);
+    const int64_t units = units_of(p.rb), slots = slots_of(p.rb);
     int64_t ctas;
     const bool whole = tiles <= 2 * kLeast || (tiles <= kWhole && units <= slots && 2 * units >= slots);
     if (split_tokens > 0 || whole) {
@@ -1313,7 +1319,7 @@ static int attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_
     int per = 1;
     if (p.pinned) {
         // as many columns a CTA as still leave four CTAs for each SM
-        const int64_t units = int64_t(B) * cache->h_kv * p.blocks, each = units * p.rb / (4 * 152);
+        const int64_t units = int64_t(B) * cache->h_kv * p.blocks, each = units * p.rb / (4 * kSms);
         per = int(each < 1 ? 1 : each > p.rb ? p.rb : each);
         grid = dim3(unsigned((p.rb + per - 1) / per), unsigned(cache->h_kv * p.blocks), unsigned(B));
     }
