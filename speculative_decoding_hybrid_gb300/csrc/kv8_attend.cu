@@ -3,13 +3,14 @@
 // With R = rows * (h_q / h_kv) query vectors on one kv head a position costs
 // 2 d bytes and 4 d R flops: from R of about 8 on only the tensor cores keep
 // up with the memory.  Keys and values go to them as they lie in the cache,
-// without a conversion: the products are e4m3 x e4m3 with the cache's side
-// exact by construction and the other side split into exact or nearly exact
-// e4m3 parts, side by side in the N extent, which the few rows leave free:
+// without a conversion: the products are 8-bit with the cache's side exact by
+// construction and the other side split into exact 8-bit parts, side by side in
+// the N extent, which the few rows leave free:
 //   scores   S^T[128 positions][2 RB] = K [q_hi | q_lo]     q = (q_hi + q_lo/32) 2^-k  (bf16's 8 bits, exactly)
-//   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 32^-j
-// A part is its predecessor's remainder times 32, so three carry 14 bits of a
-// weight; the fourth keeps that precision for weights 2^-12 times smaller.
+//   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 8^-j  (fp16's 11 bits, exactly)
+// q in e4m3.  A weight is rounded to fp16, whose upper byte is an e5m2 number, 3 bits
+// of it; a part is the upper byte of its predecessor's remainder times 8, so the four hold
+// all 11 bits, of subnormals too, and cost neither conversions to 8 bits nor back.
 // A position is a tensor-memory lane, so its page's scales are two numbers of
 // the thread that owns the lane: K's multiplies the score, V's the weight.
 //
@@ -34,8 +35,8 @@
 // of a cut one leave (m, l, O) in the workspace for kv8_join_kernel.  With a
 // given split the cuts are at its multiples instead, whatever the ranges.
 //
-// Roundings: q and the new keys are split exactly; a weight keeps 14 bits or more in
-// its parts, which the products add in fp32; scores, statistics and outputs are
+// Roundings: q and the new keys are split exactly; a weight is rounded to fp16, 2^-12
+// of it at most, an eighth of what an output's rounding to bf16 takes; scores, statistics and outputs are
 // fp32, and an output is rounded once, to bf16.
 //
 // What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
@@ -57,11 +58,10 @@ using namespace kv8;
 
 constexpr int kTile = 128;      // positions a tile
 constexpr int kSms = 152;
-// Weights are scaled by 2^2 and at most 2^(2 + 6) < 448; the last part's rounding
-// is 2^-25, so 2^-27 of a weight at the reference.  More slack moves the
-// reference less often (4 rows x 256 requests 152 us with 3, 136 with 6) and costs
-// that many bits at the low end.
-constexpr float kBase = 4.f, kSlack = 6.f;
+// Weights are scaled by 2^8 and at most 2^(8 + 6), well inside fp16, whose normal
+// numbers go down to 2^-14: 2^-22 of a weight at the reference.  More slack moves the
+// reference less often (4 rows x 256 requests 152 us with 3, 136 with 6).
+constexpr float kBase = 256.f, kSlack = 6.f;
 constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
     } else if (warp == kMmaWarp) {
         // ---- products: the warp runs the loop, one elected lane issues
         constexpr uint32_t id_s = tc::idesc_e4m3(128, C::kNs);
-        constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kAMnMajor | tc::kBMnMajor;
+        constexpr uint32_t id_p = tc::idesc_e4m3(128, C::kNp) | tc::kBE5m2 | tc::kAMnMajor | tc::kBMnMajor;
         const uint64_t dq = tc::smem_desc8<C::kRow>(gdn::smem_u32(s_q), 16);
         // weights: rows are positions; RB = 64 has two tiles of 128 columns
         const uint64_t dp = tc::smem_desc8<C::kPRow>(gdn::smem_u32(s_p), kTile * C::kPRow);
@@ -818,32 +818,29 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     break;  // the last tile
                 }
                 const float xw = sc.y * vinv;
-                const f2 xw2 = pair(xw, xw), xw32 = pair(32.f * xw, 32.f * xw);
+                const f2 xw2 = pair(xw, xw);
                 if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
                 uint8_t *pb = s_p + (y & 1) * C::kP;
-                uint16_t e[4][N / 2];
+                uint32_t e[4][N / 2];  // the parts, in the upper bytes
 #pragma unroll
                 for (int c = 0; c < N / 2; ++c) {
                     const f2 p = pair(ex2(z[2 * c]), ex2(z[2 * c + 1]));
                     l[c] = add2(l[c], p);
                     const float2 v = both(mul2(p, xw2));
-                    e[0][c] = uint16_t(e4m3x2(v.x, v.y));
-                    const float2 r = minus32(both(mul2(p, xw32)), f16x2_of(e[0][c]));  // exact
-                    uint32_t rest = f16x2(r.x, r.y);
-                    e[1][c] = e4m3x2_of(rest);
-                    rest = rest32(rest, f16x2_of(e[1][c]));
-                    e[2][c] = e4m3x2_of(rest);
-                    e[3][c] = e4m3x2_of(rest32(rest, f16x2_of(e[2][c])));
+                    e[0][c] = f16x2(v.x, v.y);
+                    e[1][c] = rest8(e[0][c]);
+                    e[2][c] = rest8(e[1][c]);
+                    e[3][c] = rest8(e[2][c]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int b = j * RB + col0;  // byte of the row
                     uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
                                    tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
-                    const uint32_t w0 = join16(e[j][0], e[j][1]), w1 = join16(e[j][2], e[j][3]);
+                    const uint32_t w0 = upper4(e[j][0], e[j][1]), w1 = upper4(e[j][2], e[j][3]);
                     if constexpr (N == 16)
                         *reinterpret_cast<uint4 *>(dst) =
-                            make_uint4(w0, w1, join16(e[j][4], e[j][5]), join16(e[j][6], e[j][7]));
+                            make_uint4(w0, w1, upper4(e[j][4], e[j][5]), upper4(e[j][6], e[j][7]));
                     else
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
                 }
@@ -931,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 #pragma unroll
                     for (int c = 0; c < N / 2; ++c) acc[c] = 0;
                     if (nc > 0) {
-                        const f2 part = pair(1.f / 32.f, 1.f / 32.f);
+                        const f2 part = pair(1.f / 8.f, 1.f / 8.f);
 #pragma unroll
                         for (int j = 3; j >= 0; j -= 2) {  // from the last part on
                             uint32_t u[N], v[N];

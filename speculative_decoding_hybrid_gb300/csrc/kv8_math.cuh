@@ -87,24 +87,21 @@ __device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) {
     return r;
 }
 
-// fp16 pair arithmetic of the splits.
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint16_t e4m3x2_of(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+// An fp16 value's upper byte is an e5m2 code, the value cut to 3 bits.  What that
+// leaves of two values, times 8: exact.
+__device__ __forceinline__ uint32_t rest8(uint32_t h) {
+    uint32_t d, r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(h & 0xff00ff00u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x48004800u));  // 8, 8
     return r;
 }
-// (h - back) * 32 of two fp16 values: exact, `back` being h to 4 bits.
-__device__ __forceinline__ uint32_t rest32(uint32_t h, uint32_t back) {
-    uint32_t t, r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(t) : "r"(h), "r"(0x50005000u));              // 32, 32
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(back), "r"(0xd000d000u), "r"(t));  // -32, -32
-    return r;
-}
+// The upper bytes of four fp16 values.
+__device__ __forceinline__ uint32_t upper4(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 
 // A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
 // into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a

@@ -130,9 +130,10 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// ---- kind::f8f6f4: e4m3 x e4m3, fp32 accumulation, K = 32 a step -----------
+// ---- kind::f8f6f4: e4m3 x e4m3 or e5m2, fp32 accumulation, K = 32 a step ----
 
-// Instruction descriptor; A or B MN-major with the bits above.
+// Instruction descriptor; A or B MN-major with the bits above, B in e5m2 with kBE5m2.
+constexpr uint32_t kBE5m2 = 1u << 10;
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4)                       // D format: f32 (A, B formats 0: e4m3)
            | (uint32_t(N >> 3) << 17)      // N / 8

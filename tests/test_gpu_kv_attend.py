@@ -282,6 +282,26 @@ def test_pinned_pieces_make_bits_independent_of_max_rows(cuda_dev, d, h_kv, grou
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("d,group,rows,window,page", [
+    (64, 2, 8, 0, 16), (64, 4, 8, 70, 32), (64, 4, 16, 0, 64), (128, 4, 4, 40, 64), (128, 8, 4, 0, 16),
+    (128, 4, 16, 130, 128), (128, 6, 16, 0, 64), (256, 4, 4, 0, 64), (256, 8, 4, 33, 32), (256, 3, 16, 0, 128)])
+def test_many_requests_have_wide_blocks(cuda_dev, d, group, rows, window, page):
+    """More requests than CTAs: a block has as many of a request's 16 to 96 columns as it can."""
+    g = np.random.RandomState(d + group + rows)
+    lens = [int(x) for x in g.randint(0, 300, 160)]
+    n = [int(x) for x in g.randint(0, rows + 1, 160)]
+    n[7], n[80], lens[80], lens[81] = rows, rows, 0, 256
+    check("wide blocks", ku.Cache(lens, group, 1, d, page, seed=31), n, cuda_dev, window=window)
+
+
+@pytest.mark.parametrize("d,group,rows,lens", [(64, 8, 2, [20000, 100]), (128, 8, 4, [12001, 9000, 30]),
+                                               (128, 4, 16, [12000, 127, 9000, 0]), (256, 8, 4, [20010, 3])])
+@pytest.mark.parametrize("split", [0, 5000])
+def test_long_requests_have_wide_blocks(cuda_dev, d, group, rows, lens, split):
+    n = [rows] + [max(1, rows - 1 - i) for i in range(len(lens) - 1)]
+    check("wide blocks, long", ku.Cache(lens, 2 * group, 2, d, 64, seed=32), n, cuda_dev, split=split)
+
+
 def test_another_stream_and_repeats(cuda_dev):
     cache = ku.Cache([2000, 50], 8, 2, 128, 64, seed=17)
     c, o, lse, _, _, args, (qt, kt, vt) = run(cache, [4, 4], cuda_dev)
