@@ -594,7 +594,7 @@ typedef struct kv8_cache {
  *   fall; n > 0 sums every n cached positions (rounded up to a multiple of
  *   128) by themselves, which makes a request's bits independent of what else
  *   is in the batch.  Sums and softmax statistics are fp32; a weight enters its
- *   product with v rounded to fp16's 11 bits, and to 2^-33 of the largest.
+ *   product with v rounded to fp16's 11 bits, and to 2^-32 of the largest.
  *   A non-finite q or k that a row sees makes the row's outputs NaN; what a
  *   row does not see, NaN and infinities included, and bytes of cache past
  *   cache_len, whatever they hold, do not reach it.

@@ -19,10 +19,10 @@
 // page's V scale the reference one) is m moved and the sums rescaled; usually
 // that is once, at a segment's first tile.  One vote a tile decides.
 //
-// Work is measured in tiles of 128 positions: a unit (request, kv head, block of
-// RB columns) costs its tiles plus a few for its ends, and the units laid end to end are cut
-// into equal ranges, one for each of the persistent CTAs.  A CTA runs the units
-// and parts of units of its range as segments.  Its warps:
+// Work is measured in tiles of 128 positions: a unit (request, kv head, block of RB
+// columns) costs its tiles plus a few for its ends, and the units laid end to end
+// are cut into equal ranges, one for each of the persistent CTAs.  A CTA runs the
+// units and parts of units of its range as segments.  Its warps:
 //   copy     finds the segments, queues them, and moves pages (tiled TMA, K and V
 //            tiles through one ring) and their scales, into the next segment while
 //            the last one is still being summed
@@ -36,18 +36,18 @@
 // given split the cuts are at its multiples instead, whatever the ranges.
 //
 // Roundings: q and the new keys are split exactly; a weight is rounded to fp16, 2^-12
-// of it at most, an eighth of what an output's rounding to bf16 takes; scores, statistics and outputs are
-// fp32, and an output is rounded once, to bf16.
+// of it at most, an eighth of what an output's rounding to bf16 takes; scores,
+// statistics and outputs are fp32, and an output is rounded once, to bf16.
 //
 // What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
 // of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 135
-// us, 5.82 TB/s, 86 %) and long requests (256k tokens: 269 MB in 53 us, 5.06 TB/s, 75
-// %, of which about 5 us are the join and 4 the start; 16 requests of a mixed batch 258
-// MB in 52.6 us, 72 %); the softmax's instructions from 64 columns on (16 rows x 32
-// requests, 4 heads of 128: 129 us, 4.8 times what HBM would need); the chain from a
-// segment's queries to its outputs, about 4 us, where requests are short, and then
-// also the fetching of its instructions: loops there are rolled wherever that costs
-// nothing.
+// us, 5.8 TB/s, 86 %) and long requests (256k tokens: 269 MB in 53 us, 5.0 TB/s, 74
+// %, of which about 5 us are the join and 4 the start; 16 requests of a mixed batch
+// 258 MB in 53 us, 72 %); the softmax's instructions from 64 columns on (16 rows x 32
+// requests, 4 heads of 128: 119 us, five times what HBM would need); the chain from
+// a segment's queries to its outputs, about 4 us, where requests are short, and
+// then also the fetching of its instructions: loops there are rolled wherever that
+// costs nothing.
 #include <cuda.h>
 
 #include "kv8_math.cuh"
@@ -58,10 +58,10 @@ using namespace kv8;
 
 constexpr int kTile = 128;      // positions a tile
 constexpr int kSms = 152;
-// Weights are scaled by 2^8 and at most 2^(8 + 6), well inside fp16, whose normal
-// numbers go down to 2^-14: 2^-22 of a weight at the reference.  More slack moves the
-// reference less often (4 rows x 256 requests 152 us with 3, 136 with 6).
-constexpr float kBase = 256.f, kSlack = 6.f;
+// Weights are scaled by 2^7 and at most 2^(7 + 8), inside fp16, whose normal numbers
+// go down to 2^-14: 2^-21 of a weight at the reference.  More slack moves the reference
+// less often (16 rows x 32 requests 145 us with 3, 121 with 6, 119.5 with 8 and with 10).
+constexpr float kBase = 128.f, kSlack = 8.f;
 constexpr float kUnset = -1e30f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
@@ -69,7 +69,7 @@ constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 // Tiles that a unit's queries, new rows and outputs cost as much as.  A fit of a CTA's
 // cycles to its tiles and segments gives 3 to 7; of those and two tiles more or less,
 // these were the fastest (4 rows x 256 requests 140, 136 and 139 us at 4, 6 and 8,
-// 16 rows x 32 requests 129, 129 and 136 at 6, 8 and 10).
+// 16 rows x 32 requests 129, 129 and 136 at 6, 8 and 10, before its weights were fp16).
 __host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : 4; }
 
 // Units of at most 2 * kLeast tiles are not cut, nor, where they fill half of the CTAs
@@ -1179,7 +1179,7 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
     const auto units_of = [&](int rb) { return int64_t(B) * c->h_kv * ((cols + rb - 1) / rb); };
     // the narrowest block that holds a request's columns: the work a tile costs goes by its
     // width (1 row x 256 requests, 4 columns: 63 us in 8, 80 in 16, 104 in 32), and a wider
-    // one reads the cache less often (16 rows, 128 columns: 135 us by 32, 129 by 64) ...
+    // one reads the cache less often (16 rows, 128 columns: 131 us by 32, 121 by 64) ...
     const int widest = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 || c->d == 256 ? 32 : 64;
     // ... or narrower ones, where every one of them can have its CTA and there are few tiles
     // an SM: then they share tiles that are in L2, and a unit's ends are shorter (32 columns of
