@@ -72,10 +72,11 @@ constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 // 16 rows x 32 requests 129, 129 and 136 at 6, 8 and 10, before its weights were fp16).
 __host__ __device__ constexpr int unit_cost(int rb) { return rb == 64 ? 8 : rb == 32 ? 6 : 4; }
 
-// Units of at most 2 * kLeast tiles are not cut, nor, where they fill half of the CTAs
-// and each can have its own, of kWhole: the join costs more (24 windowed requests x 12
-// heads, 9 tiles: 22.5 us cut, 16.1 whole; two heads of one request, d = 256, are the
-// other way round: 6 tiles 15 us cut, 17 whole, 16 tiles 18 and 28).
+// Units of at most 2 * kLeast tiles are not cut, nor, where each can have its own CTA,
+// of kWhole if they fill half of the CTAs, of half that if a quarter: the join costs
+// more (24 windowed requests x 12 heads, 9 tiles: 22.5 us cut, 16.1 whole; 64 requests
+// x 2 heads, 8 tiles: 19.6 and 16.5; but 8 heads of one request, 8 tiles: 10.7 and
+// 12.3, and 32 units of 16 tiles 16.5 and 22).
 constexpr int kWhole = 16;
 
 // Ranges that a total weight is cut into where CTAs do not run out: of four tiles or
@@ -1190,7 +1191,8 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
     p.blocks = int((cols + p.rb - 1) / p.rb);
     const int64_t units = units_of(p.rb), slots = slots_of(p.rb);
     int64_t ctas;
-    const bool whole = tiles <= 2 * kLeast || (tiles <= kWhole && units <= slots && 2 * units >= slots);
+    const bool whole = tiles <= 2 * kLeast ||
+                       (tiles <= kWhole && units <= slots && tiles * slots <= 2 * kWhole * units);
     if (split_tokens > 0 || whole) {
         const int64_t t = split_tokens > 0 ? (int64_t(split_tokens) + kTile - 1) / kTile : tiles;
         p.pinned = 1;
