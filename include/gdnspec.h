@@ -595,6 +595,11 @@ typedef struct kv8_cache {
  *   128) by themselves, which makes a request's bits independent of what else
  *   is in the batch.  Sums and softmax statistics are fp32; a weight enters its
  *   product with v rounded to fp16's 11 bits, and to 2^-32 of the largest.
+ *   q and the new keys enter with all their bits, of any finite magnitude, but
+ *   for elements below 2^-14 of their row's largest in a row where no more
+ *   than one in 32 of the elements (zeros aside) is below 2^-12 of it: those
+ *   are rounded to 2^-22 of the largest.  Rows with more such elements are
+ *   computed in fp32, some 50 times slower.
  *   A non-finite q or k that a row sees makes the row's outputs NaN; what a
  *   row does not see, NaN and infinities included, and bytes of cache past
  *   cache_len, whatever they hold, do not reach it.

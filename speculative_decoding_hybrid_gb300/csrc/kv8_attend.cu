@@ -6,9 +6,11 @@
 // without a conversion: the products are 8-bit with the cache's side exact by
 // construction and the other side split into exact 8-bit parts, side by side in
 // the N extent, which the few rows leave free:
-//   scores   S^T[128 positions][2 RB] = K [q_hi | q_lo]     q = (q_hi + q_lo/32) 2^-k  (bf16's 8 bits, exactly)
+//   scores   S^T[128 positions][2 RB] = K [q_hi | q_lo]     q = (q_hi + q_lo/32) 2^-k  (bf16's 8 bits)
 //   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 8^-j  (fp16's 11 bits, exactly)
-// q in e4m3.  A weight is rounded to fp16, whose upper byte is an e5m2 number, 3 bits
+// q in e4m3, exact but for elements below 2^-14 of their row's largest; the scores of a
+// row where that might show are summed by the softmax's threads instead (wide_scores).
+// A weight is rounded to fp16, whose upper byte is an e5m2 number, 3 bits
 // of it; a part is the upper byte of its predecessor's remainder times 8, so the four hold
 // all 11 bits, of subnormals too, and cost neither conversions to 8 bits nor back.
 // A position is a tensor-memory lane, so its page's scales are two numbers of
@@ -35,9 +37,11 @@
 // of a cut one leave (m, l, O) in the workspace for kv8_join_kernel.  With a
 // given split the cuts are at its multiples instead, whatever the ranges.
 //
-// Roundings: q and the new keys are split exactly; a weight is rounded to fp16, 2^-12
-// of it at most, an eighth of what an output's rounding to bf16 takes; scores,
-// statistics and outputs are fp32, and an output is rounded once, to bf16.
+// Roundings: q and the new keys are split exactly, but for an element below 2^-14 of its
+// row's largest, which is rounded to 2^-22 of that, where at most one element in 32 is
+// so small; a weight is rounded to fp16, 2^-12 of it at most, an eighth of what an
+// output's rounding to bf16 takes; scores, statistics and outputs are fp32, and an
+// output is rounded once, to bf16.
 //
 // What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
 // of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 135
@@ -63,6 +67,7 @@ constexpr int kSms = 152;
 // less often (16 rows x 32 requests 145 us with 3, 121 with 6, 119.5 with 8 and with 10).
 constexpr float kBase = 128.f, kSlack = 8.f;
 constexpr float kUnset = -1e30f;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 
@@ -170,7 +175,7 @@ struct Cfg {
     // it out (three at d = 64 change nothing: 152 requests of 1 row 45.5 and 45.7 us)
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
     static constexpr int kFixed = 2 * kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024;
-    static constexpr int kStatic = RB == 64 ? 4096 : D == 64 ? 2560 : 2048;  // bound on sizeof(Shared)
+    static constexpr int kStatic = RB == 64 ? 4096 : D == 64 || RB == 32 ? 2560 : 2048;  // bound on sizeof(Shared)
     static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kStatic - kFixed;
     static constexpr int kSlots = kRoom / kSlot > 10 ? 10 : kRoom / kSlot;
     static constexpr int kSmem = kFixed + kSlots * kSlot;
@@ -207,13 +212,15 @@ struct Shared {
         float col_max[4][RB];
         long long scan[C::kThreads / 32];
     };
-    float v_max[C::kGroups][4], fresh_k[16];
+    float v_max[C::kGroups][4];
+    float fresh_k[16], col_down[RB];  // what a new key's and a column's parts are times; negative: a wide row's unit
     Segment seg[kQueue];
     int bad[kQueue];
     long long start_at;
     int start_r;
     int3 start_rows;
     uint32_t tmem;
+    int fresh_wide;                     // whether any new key is wide
     int col_out[RB];                    // element of o, from the request's first row on
     uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
 };
@@ -245,6 +252,55 @@ __device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tile
     if (!a.pinned) return x < kLeast ? 0 : x > tiles - kLeast ? tiles + 1 : int(x);
     const long long y = x * a.piece_tiles;
     return y >= tiles ? tiles + 1 : int(y);
+}
+
+// The scores of wide columns and wide new keys, from the queries and keys in global
+// memory, into this warp's lanes of the score tile (the low parts' columns zero).  t: the
+// lane's cached position, -1 in a tile of new keys.  Rare: small for the loop's sake, and
+// slow, with all of a unit's columns wide a tile takes some 50 times as long.  (With the
+// keys' codes in registers it is 20 times, but then the ordinary tiles suffer: 16 requests
+// 75 us for 53.)
+template <int D, int RB>
+__device__ __noinline__ void wide_scores(const AttendArgs &a, const Shared<D, RB> &s, const Segment &g, int t,
+                                            int pos_in, int col0, uint32_t at) {
+    const int T = a.c.page_tokens, j = pos_in & 15;
+    const bool is_fresh = t < 0;
+    bool have = is_fresh ? pos_in < 32 && j < g.n : t >= g.lo && t < g.len;
+    const uint8_t *codes = a.c.kv;
+    const uint16_t *key = a.k;
+    float down = 1.f;
+    if (is_fresh) {
+        key += (int64_t(g.t0) + j) * a.k_stride + int64_t(g.hk) * D;
+        if (have) down = s.fresh_k[j];
+        have = have && down == down;
+    } else if (have) {
+        const int page = a.table[int64_t(g.r) * a.table_stride + (t >> a.page_shift)];
+        have = page >= 0 && page < a.c.num_pages;
+        if (have)
+            codes += int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                     (int64_t(g.hk) * T + (t & (T - 1))) * D;
+    }
+#pragma unroll 1
+    for (int c = 0; c < Cfg<D, RB>::kCols && col0 + c < g.cols; ++c) {
+        const float f = s.col_down[col0 + c];
+        const bool mine = have && f == f && (f < 0.f || (is_fresh && down < 0.f));
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        uint32_t hi = tc::ld1(at + c), lo = tc::ld1(at + RB + c);
+        if (mine) {
+            const uint16_t *q = a.q + (int64_t(g.t0) + s.col_row[col0 + c]) * a.q_stride +
+                                int64_t(g.hk * a.group + s.col_head[col0 + c]) * D;
+            const float up = 1.f / fabsf(f);
+            if (!is_fresh)
+                hi = __float_as_uint(dot_codes<D>(codes, q, up));
+            else  // the low parts of the keys lie 16 lanes on
+                hi = pos_in & 16 ? 0u : __float_as_uint(dot_rows<D>(key, 1.f / fabsf(down), q, up));
+            lo = 0;
+        }
+        __syncwarp();
+        tc::st1(at + c, hi);
+        tc::st1(at + RB + c, lo);
+    }
+    tc::st_wait();
 }
 
 template <int D, int RB>
@@ -531,6 +587,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int nc = g.nc, n = g.n, fresh = g.fresh, nt = nc + fresh;
             if (g.cols == 0) break;
             const uint16_t *kn = a.k + int64_t(g.t0) * a.k_stride + int64_t(g.hk) * D;
+            bool maybe = false;  // some new key may be wide, and fk_ready is still to come
             if (fresh) {
                 // the new keys, while the softmax ends the segment before: their place is free
                 // once the scores of the last ones are read
@@ -544,14 +601,20 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 #pragma unroll 1
                 for (int row = lane >> 3; row - (lane >> 3) < n; row += 4) {
                     load_row<D>(kn + int64_t(row + 4) * a.k_stride, lane & 7, row + 4 < n, next);
-                    const float down = split_row<D>(w, lane & 7, s_fk, 32, row, 16 + row);
+                    bool here;
+                    const float down = split_row<D>(w, lane & 7, s_fk, 32, row, 16 + row, here);
+                    maybe |= here;
                     if ((lane & 7) == 0) s.fresh_k[row] = down;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) w[e] = next[e];
                 }
                 gdn::fence_proxy_async_smem();
+                maybe = __any_sync(0xffffffffu, maybe);
                 __syncwarp();
-                if (lane == 0) arrive(&s.fk_ready);
+                if (lane == 0 && !maybe) {
+                    s.fresh_wide = 0;
+                    arrive(&s.fk_ready);
+                }
                 last_fresh = gs + nc;
             }
             ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
@@ -577,6 +640,25 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                         if (cached) tc::commit(&s.empty[slot]);
                     }
                     __syncwarp();
+                    if (maybe) {
+                        // the first scores are on their way: time to look at the new keys again
+                        bool wide = false;
+#pragma unroll 1
+                        for (int row = lane >> 3; row - (lane >> 3) < n; row += 4) {
+                            uint4 w[D / 64];
+                            load_row<D>(kn + int64_t(row) * a.k_stride, lane & 7, row < n, w);
+                            const float unit = wide_row<D>(w);
+                            if ((lane & 7) == 0 && unit > 0.f) s.fresh_k[row] = -unit;
+                            wide |= unit > 0.f;
+                        }
+                        wide = __any_sync(0xffffffffu, wide);
+                        __syncwarp();
+                        if (lane == 0) {
+                            s.fresh_wide = wide;
+                            arrive(&s.fk_ready);
+                        }
+                        maybe = false;
+                    }
                 }
                 if (i > 0 && i <= nc) {
                     const int j = i - 1, pos = ring + v_pos(j, nc), slot = pos % C::kSlots, x = gp + j;
@@ -614,10 +696,11 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         __syncwarp();
     } else {
         // ---- softmax.  This thread's position in a tile and its columns col0 .. col0 + N - 1;
-        // eight threads bring a column's queries (columns fill whole warps).
+        // eight threads bring a column's queries, of their own group's (columns fill whole warps).
         constexpr int N = C::kCols;
-        static_assert(RB * 8 <= C::kSoft, "a thread has one column's queries");
-        const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N, cq = tid >> 3, sub = tid & 7;
+        static_assert(N == 8 || N == 16, "a thread has one column's queries");
+        const int grp = warp >> 2, pos_in = tid & 127, col0 = grp * N, cq = col0 + (pos_in >> 3), sub = tid & 7;
+        const bool brings = pos_in < 8 * N;
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
         bool ok = gdn::mbar_wait_bounded(&s.seg_full[0], 0, a.wait_ns);
         if (group_or(grp, !ok)) ok = false;
@@ -626,19 +709,21 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         uint4 wq[D / 64];
         auto load_q = [&] {
             const int x = g.blk * RB + cq, row = x / a.group;
-            if (cq < RB)
+            if (brings)
                 load_row<D>(a.q + (int64_t(g.t0) + row) * a.q_stride + int64_t(g.hk * a.group + x - row * a.group) * D,
                             sub, cq < g.cols, wq);
         };
         load_q();
         int gs = 0, gp = 0, ring = 0, fresh_seen = 0;  // score and weight tiles, ring positions, fresh tiles so far
         for (int k = 0; g.cols > 0; ++k) {
-            if (cq < RB) {
-                const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq);
+            bool maybe = false, wide = false;
+            if (brings) {
+                const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq, maybe);
                 if (sub == 0) {
                     const int x = g.blk * RB + cq, row = x / a.group, head = x - row * a.group;
                     s.col_nm[cq] = -kUnset;
-                    s.col_coef[cq] = a.c.sm_scale * 1.4426950408889634f * down;
+                    s.col_coef[cq] = a.c.sm_scale * kLog2e * down;
+                    s.col_down[cq] = down;
                     s.col_row[cq] = uint8_t(row);
                     s.col_head[cq] = uint8_t(head);
                     s.col_out[cq] = row * int(a.o_stride) + (g.hk * a.group + head) * D;
@@ -647,7 +732,17 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             gdn::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&s.q_ready);
+            // while the first products run: is a column of this group wide?
+            if (brings && __any_sync(0xffffffffu, maybe)) {
+                const float unit = wide_row<D>(wq);
+                wide = unit > 0.f;
+                if (sub == 0 && wide) {
+                    s.col_coef[cq] = a.c.sm_scale * kLog2e * unit;
+                    s.col_down[cq] = -unit;
+                }
+            }
             ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
+            wide = group_or(grp, wide);
 
             const int nc = g.nc, nt = nc + g.fresh;
             // a row sees positions from lo0 + row * lo1 on (g.lo is row 0's, and not negative)
@@ -661,217 +756,239 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             for (int c = 0; c < N / 2; ++c) l[c] = 0;
             float vref = pow2i(kMinScaleExp), vinv = kBase / vref;
 
-            for (int i = 0; i < nt; ++i) {
+            // Tile by tile; where a column or a new key is wide the loop is left before the tile, its scores
+            // are put right and it goes on.  (In the loop that code, taken or not, called or not, made 16 rows
+            // x 32 requests 133 to 136 us, in a second form of the loop 128 to 131; beside it 121.5.)
+            for (int i = 0, stop = wide ? 0 : nt, fixed = -1;;) {
+                for (; i < stop; ++i) {
+                    const bool is_fresh = i >= nc;
+                    const int x = gs + i, y = gp + i, t = (g.tile0 + i) * kTile + pos_in;
+                    if (ok)
+                        ok = is_fresh ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
+                                      : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
+                    if (is_fresh && fixed != i && __any_sync(0xffffffffu, ok && s.fresh_wide)) break;
+                    const float2 sc =
+                        is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < g.n ? fabsf(s.fresh_k[pos_in & 15]) : 0.f, 0.f)
+                                 : s.scales[y % C::kScales][pos_in >> shift];
+                    // whole: every row sees every position of the tile
+                    const bool whole = !is_fresh && (g.tile0 + i + 1) * kTile <= g.len && (g.tile0 + i) * kTile >= lo_last;
+                    if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
+                    tc::fence_after();
+
+                    // While some row of the request may not have seen a position (a segment's first
+                    // tile, and those that its window begins in or past) every column's reference
+                    // follows its largest score, which z holds as it is; from then on z is against
+                    // the reference.  Both go by the request alone.
+                    const bool first = i == 0 || lo_request >= (is_fresh ? g.len : (g.tile0 + i) * kTile);
+                    {
+                        uint32_t hi[N], lo[N];
+                        const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
+                        if constexpr (N == 16) {
+                            tc::ld16_async(at, hi);
+                            tc::ld16_async(at + RB, lo);
+                        } else {
+                            tc::ld8_async(at, hi);
+                            tc::ld8_async(at + RB, lo);
+                        }
+                        tc::ld_wait();
+                        tc::ld_fence_regs(hi);
+                        tc::ld_fence_regs(lo);
+                        f2 v[N / 2];
+                        const f2 part = pair(1.f / 32.f, 1.f / 32.f);
+#pragma unroll
+                        for (int c = 0; c < N / 2; ++c)
+                            v[c] = fma2(pair(lo[2 * c], lo[2 * c + 1]), part, pair(hi[2 * c], hi[2 * c + 1]));
+                        if (is_fresh) {  // the other part of the position
+#pragma unroll
+                            for (int c = 0; c < N / 2; ++c) {
+                                const float2 b = both(v[c]);
+                                const f2 other =
+                                    pair(__shfl_xor_sync(0xffffffffu, b.x, 16), __shfl_xor_sync(0xffffffffu, b.y, 16));
+                                v[c] = pos_in & 16 ? fma2(v[c], part, other) : fma2(other, part, v[c]);
+                            }
+                        }
+                        const f2 sx = pair(sc.x, sc.x);
+#pragma unroll
+                        for (int c = 0; c < N; c += 4) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s.col_coef + col0 + c);
+                            ulonglong2 nm = make_ulonglong2(0, 0);
+                            if (!first) nm = *reinterpret_cast<const ulonglong2 *>(s.col_nm + col0 + c);
+                            const float2 b0 = both(fma2(v[c / 2], mul2(sx, f.x), nm.x)),
+                                         b1 = both(fma2(v[c / 2 + 1], mul2(sx, f.y), nm.y));
+                            z[c] = b0.x;
+                            z[c + 1] = b0.y;
+                            z[c + 2] = b1.x;
+                            z[c + 3] = b1.y;
+                        }
+                        if (is_fresh) {
+                            const int j = pos_in & 15, w = a.c.window;
+#pragma unroll
+                            for (int c = 0; c < N; ++c) {
+                                const int row = s.col_row[col0 + c];
+                                const bool see = pos_in < 32 && j < g.n && j <= row && (!w || j > row - w);
+                                z[c] = see ? z[c] : -INFINITY;
+                            }
+                        } else if (!whole) {
+#pragma unroll
+                            for (int c = 0; c < N; ++c)
+                                z[c] = t < g.len && t >= lo0 + lo1 * s.col_row[col0 + c] ? z[c] : -INFINITY;
+                        }
+                    }
+                    bool move = first;
+                    if (!first) {
+                        float top[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+                        for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
+                        const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        move = group_or(grp, over > kSlack || sc.y > vref || !ok);
+                    }
+                    if (__builtin_expect(move, 0)) {
+                        // ---- the reference moves (or a wait ran out)
+                        if (group_or(grp, !ok)) {
+                            ok = false;
+                            i = nt;
+                            break;
+                        }
+#pragma unroll
+                        for (int c = 0; c < N; ++c) {
+                            const float top = warp_max(z[c]);
+                            if (lane == 0) s.col_max[warp & 3][col0 + c] = top;
+                        }
+                        const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
+                        if (lane == 0) s.v_max[grp][warp & 3] = __uint_as_float(vm);
+                        group_sync(grp);
+                        if (pos_in < N) {
+                            const int c = col0 + pos_in;
+                            const float was = -s.col_nm[c];
+                            const float top = fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]),
+                                                    fmaxf(s.col_max[2][c], s.col_max[3][c]));
+                            // columns within the slack stay, or a column's bits would go by its neighbours
+                            const float now = first ? fmaxf(top, was) : top > kSlack ? was + top : was;
+                            s.col_nm[c] = -now;
+                            s.col_fac[c] = ex2(was - now);
+                            s.col_l[c] = first ? -now : was - now;
+                        }
+                        const float vnow = fmaxf(
+                            fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]), fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
+                        const float vfac = vref / vnow;
+                        vref = vnow;
+                        vinv = kBase / vnow;
+                        group_sync(grp);
+#pragma unroll
+                        for (int c = 0; c < N; c += 2) {
+                            l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(s.col_fac + col0 + c));
+                            z[c] += s.col_l[col0 + c];
+                            z[c + 1] += s.col_l[col0 + c + 1];
+                        }
+                        if (i > 0) {
+                            ok = gdn::mbar_wait_bounded(&s.pv_done[(y - 1) & 1], ((y - 1) >> 1) & 1, a.wait_ns);
+                            if (group_or(grp, !ok)) {
+                                ok = false;
+                                i = nt;
+                                break;
+                            }
+                            tc::fence_after();
+#pragma unroll 1
+                            for (int e = 0; e < C::kAtoms * 4 * N; e += 8) {  // this group's columns of every part
+                                const int at = e / N * RB + col0 + e % N;
+                                uint32_t w[8];
+                                tc::ld8_async(tm_o + lane_base + at, w);
+                                tc::ld_wait();
+                                tc::ld_fence_regs(w);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    w[c] = __float_as_uint(__uint_as_float(w[c]) * (s.col_fac[at % RB + c] * vfac));
+                                tc::st8(tm_o + lane_base + at, w);
+                            }
+                            tc::st_wait();
+                        }
+                    }
+                    // scores are read: their buffer is free
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.s_free[x & 1]);
+
+                    if (is_fresh) {
+                        if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
+                        if (pos_in < 16 && ok) {
+#pragma unroll
+                            for (int c = 0; c < N; c += 2) {
+                                const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
+                                l[c / 2] = add2(l[c / 2], p);
+                                *reinterpret_cast<f2 *>(fresh_p + pos_in * RB + col0 + c) = p;
+                            }
+                        }
+                        i = nt;  // the last tile
+                        break;
+                    }
+                    const float xw = sc.y * vinv;
+                    const f2 xw2 = pair(xw, xw);
+                    if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
+                    uint8_t *pb = s_p + (y & 1) * C::kP;
+                    uint32_t e[4][N / 2];  // the parts, in the upper bytes
+#pragma unroll
+                    for (int c = 0; c < N / 2; ++c) {
+                        const f2 p = pair(ex2(z[2 * c]), ex2(z[2 * c + 1]));
+                        l[c] = add2(l[c], p);
+                        const float2 v = both(mul2(p, xw2));
+                        e[0][c] = f16x2(v.x, v.y);
+                        e[1][c] = rest8(e[0][c]);
+                        e[2][c] = rest8(e[1][c]);
+                        e[3][c] = rest8(e[2][c]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = j * RB + col0;  // byte of the row
+                        uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
+                                       tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
+                        const uint32_t w0 = upper4(e[j][0], e[j][1]), w1 = upper4(e[j][2], e[j][3]);
+                        if constexpr (N == 16)
+                            *reinterpret_cast<uint4 *>(dst) =
+                                make_uint4(w0, w1, upper4(e[j][4], e[j][5]), upper4(e[j][6], e[j][7]));
+                        else
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+                    }
+                    if (!whole && grp == 0) {
+                        // What no row sees may hold anything, NaN codes too, and 0 * NaN is
+                        // NaN: its values become zero.  Positions only some rows see keep
+                        // their values but for NaN, which the epilogue gives to those rows.
+                        const int pos = ring + v_pos(i, nc), slot = pos % C::kSlots;
+                        if (ok) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
+                        const bool none = t < g.lo || t >= g.len, some = !none && t < lo_last;
+                        if (ok && (none || some)) {
+#pragma unroll 2
+                            for (int e = 0; e < C::kAtoms * C::kRow / 16; ++e) {
+                                uint4 *p = reinterpret_cast<uint4 *>(
+                                    s_ring + slot * C::kSlot + e / (C::kRow / 16) * kTile * C::kRow +
+                                    tc::swz8_off<C::kRow>(pos_in, e % (C::kRow / 16)));
+                                uint4 w = make_uint4(0, 0, 0, 0);
+                                if (some) {
+                                    w = *p;
+                                    uint32_t *u = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                                    for (int b = 0; b < 4; ++b) u[b] &= ~__vcmpeq4(u[b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                }
+                                *p = w;
+                            }
+                        }
+                    }
+                    gdn::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.p_full[y & 1]);
+                }
+                if (i >= nt) break;
                 const bool is_fresh = i >= nc;
-                const int x = gs + i, y = gp + i, t = (g.tile0 + i) * kTile + pos_in;
+                const int x = gs + i, y = gp + i;
                 if (ok)
                     ok = is_fresh ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
                                   : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
-                const float2 sc =
-                    is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < g.n ? s.fresh_k[pos_in & 15] : 0.f, 0.f)
-                             : s.scales[y % C::kScales][pos_in >> shift];
-                // whole: every row sees every position of the tile
-                const bool whole = !is_fresh && (g.tile0 + i + 1) * kTile <= g.len && (g.tile0 + i) * kTile >= lo_last;
                 if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
+                __syncwarp();
                 tc::fence_after();
-
-                // While some row of the request may not have seen a position (a segment's first
-                // tile, and those that its window begins in or past) every column's reference
-                // follows its largest score, which z holds as it is; from then on z is against
-                // the reference.  Both go by the request alone.
-                const bool first = i == 0 || lo_request >= (is_fresh ? g.len : (g.tile0 + i) * kTile);
-                {
-                    uint32_t hi[N], lo[N];
-                    const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
-                    if constexpr (N == 16) {
-                        tc::ld16_async(at, hi);
-                        tc::ld16_async(at + RB, lo);
-                    } else {
-                        tc::ld8_async(at, hi);
-                        tc::ld8_async(at + RB, lo);
-                    }
-                    tc::ld_wait();
-                    tc::ld_fence_regs(hi);
-                    tc::ld_fence_regs(lo);
-                    f2 v[N / 2];
-                    const f2 part = pair(1.f / 32.f, 1.f / 32.f);
-#pragma unroll
-                    for (int c = 0; c < N / 2; ++c)
-                        v[c] = fma2(pair(lo[2 * c], lo[2 * c + 1]), part, pair(hi[2 * c], hi[2 * c + 1]));
-                    if (is_fresh) {  // the other part of the position
-#pragma unroll
-                        for (int c = 0; c < N / 2; ++c) {
-                            const float2 b = both(v[c]);
-                            const f2 other =
-                                pair(__shfl_xor_sync(0xffffffffu, b.x, 16), __shfl_xor_sync(0xffffffffu, b.y, 16));
-                            v[c] = pos_in & 16 ? fma2(v[c], part, other) : fma2(other, part, v[c]);
-                        }
-                    }
-                    const f2 sx = pair(sc.x, sc.x);
-#pragma unroll
-                    for (int c = 0; c < N; c += 4) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(s.col_coef + col0 + c);
-                        ulonglong2 nm = make_ulonglong2(0, 0);
-                        if (!first) nm = *reinterpret_cast<const ulonglong2 *>(s.col_nm + col0 + c);
-                        const float2 b0 = both(fma2(v[c / 2], mul2(sx, f.x), nm.x)),
-                                     b1 = both(fma2(v[c / 2 + 1], mul2(sx, f.y), nm.y));
-                        z[c] = b0.x;
-                        z[c + 1] = b0.y;
-                        z[c + 2] = b1.x;
-                        z[c + 3] = b1.y;
-                    }
-                    if (is_fresh) {
-                        const int j = pos_in & 15, w = a.c.window;
-#pragma unroll
-                        for (int c = 0; c < N; ++c) {
-                            const int row = s.col_row[col0 + c];
-                            const bool see = pos_in < 32 && j < g.n && j <= row && (!w || j > row - w);
-                            z[c] = see ? z[c] : -INFINITY;
-                        }
-                    } else if (!whole) {
-#pragma unroll
-                        for (int c = 0; c < N; ++c)
-                            z[c] = t < g.len && t >= lo0 + lo1 * s.col_row[col0 + c] ? z[c] : -INFINITY;
-                    }
-                }
-                bool move = first;
-                if (!first) {
-                    float top[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-                    for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
-                    const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    move = group_or(grp, over > kSlack || sc.y > vref || !ok);
-                }
-                if (__builtin_expect(move, 0)) {
-                    // ---- the reference moves (or a wait ran out)
-                    if (group_or(grp, !ok)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        const float top = warp_max(z[c]);
-                        if (lane == 0) s.col_max[warp & 3][col0 + c] = top;
-                    }
-                    const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
-                    if (lane == 0) s.v_max[grp][warp & 3] = __uint_as_float(vm);
-                    group_sync(grp);
-                    if (pos_in < N) {
-                        const int c = col0 + pos_in;
-                        const float was = -s.col_nm[c];
-                        const float top = fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]),
-                                                fmaxf(s.col_max[2][c], s.col_max[3][c]));
-                        // columns within the slack stay, or a column's bits would go by its neighbours
-                        const float now = first ? fmaxf(top, was) : top > kSlack ? was + top : was;
-                        s.col_nm[c] = -now;
-                        s.col_fac[c] = ex2(was - now);
-                        s.col_l[c] = first ? -now : was - now;
-                    }
-                    const float vnow = fmaxf(
-                        fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]), fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
-                    const float vfac = vref / vnow;
-                    vref = vnow;
-                    vinv = kBase / vnow;
-                    group_sync(grp);
-#pragma unroll
-                    for (int c = 0; c < N; c += 2) {
-                        l[c / 2] = mul2(l[c / 2], *reinterpret_cast<const f2 *>(s.col_fac + col0 + c));
-                        z[c] += s.col_l[col0 + c];
-                        z[c + 1] += s.col_l[col0 + c + 1];
-                    }
-                    if (i > 0) {
-                        ok = gdn::mbar_wait_bounded(&s.pv_done[(y - 1) & 1], ((y - 1) >> 1) & 1, a.wait_ns);
-                        if (group_or(grp, !ok)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after();
-#pragma unroll 1
-                        for (int e = 0; e < C::kAtoms * 4 * N; e += 8) {  // this group's columns of every part
-                            const int at = e / N * RB + col0 + e % N;
-                            uint32_t w[8];
-                            tc::ld8_async(tm_o + lane_base + at, w);
-                            tc::ld_wait();
-                            tc::ld_fence_regs(w);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                w[c] = __float_as_uint(__uint_as_float(w[c]) * (s.col_fac[at % RB + c] * vfac));
-                            tc::st8(tm_o + lane_base + at, w);
-                        }
-                        tc::st_wait();
-                    }
-                }
-                // scores are read: their buffer is free
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(&s.s_free[x & 1]);
-
-                if (is_fresh) {
-                    if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
-                    if (pos_in < 16 && ok) {
-#pragma unroll
-                        for (int c = 0; c < N; c += 2) {
-                            const f2 p = pair(ex2(z[c]), ex2(z[c + 1]));
-                            l[c / 2] = add2(l[c / 2], p);
-                            *reinterpret_cast<f2 *>(fresh_p + pos_in * RB + col0 + c) = p;
-                        }
-                    }
-                    break;  // the last tile
-                }
-                const float xw = sc.y * vinv;
-                const f2 xw2 = pair(xw, xw);
-                if (ok && y >= 2) ok = gdn::mbar_wait_bounded(&s.pv_done[y & 1], ((y >> 1) - 1) & 1, a.wait_ns);
-                uint8_t *pb = s_p + (y & 1) * C::kP;
-                uint32_t e[4][N / 2];  // the parts, in the upper bytes
-#pragma unroll
-                for (int c = 0; c < N / 2; ++c) {
-                    const f2 p = pair(ex2(z[2 * c]), ex2(z[2 * c + 1]));
-                    l[c] = add2(l[c], p);
-                    const float2 v = both(mul2(p, xw2));
-                    e[0][c] = f16x2(v.x, v.y);
-                    e[1][c] = rest8(e[0][c]);
-                    e[2][c] = rest8(e[1][c]);
-                    e[3][c] = rest8(e[2][c]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int b = j * RB + col0;  // byte of the row
-                    uint8_t *dst = pb + (b / C::kPRow) * kTile * C::kPRow +
-                                   tc::swz8_off<C::kPRow>(pos_in, (b % C::kPRow) >> 4) + (b & 8);
-                    const uint32_t w0 = upper4(e[j][0], e[j][1]), w1 = upper4(e[j][2], e[j][3]);
-                    if constexpr (N == 16)
-                        *reinterpret_cast<uint4 *>(dst) =
-                            make_uint4(w0, w1, upper4(e[j][4], e[j][5]), upper4(e[j][6], e[j][7]));
-                    else
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
-                }
-                if (!whole && grp == 0) {
-                    // What no row sees may hold anything, NaN codes too, and 0 * NaN is
-                    // NaN: its values become zero.  Positions only some rows see keep
-                    // their values but for NaN, which the epilogue gives to those rows.
-                    const int pos = ring + v_pos(i, nc), slot = pos % C::kSlots;
-                    if (ok) ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                    const bool none = t < g.lo || t >= g.len, some = !none && t < lo_last;
-                    if (ok && (none || some)) {
-#pragma unroll 2
-                        for (int e = 0; e < C::kAtoms * C::kRow / 16; ++e) {
-                            uint4 *p = reinterpret_cast<uint4 *>(
-                                s_ring + slot * C::kSlot + e / (C::kRow / 16) * kTile * C::kRow +
-                                tc::swz8_off<C::kRow>(pos_in, e % (C::kRow / 16)));
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (some) {
-                                w = *p;
-                                uint32_t *u = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-                                for (int b = 0; b < 4; ++b) u[b] &= ~__vcmpeq4(u[b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            }
-                            *p = w;
-                        }
-                    }
-                }
-                gdn::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive(&s.p_full[y & 1]);
+                wide_scores<D, RB>(a, s, s.seg[k % kQueue], is_fresh ? -1 : (g.tile0 + i) * kTile + pos_in, pos_in, col0,
+                                   tm + lane_base + (x & 1) * C::kNs + col0);
+                fixed = i;
+                stop = wide ? i + 1 : nt;
             }
             // ---- the segment's end
             if (ok && nc > 0) {

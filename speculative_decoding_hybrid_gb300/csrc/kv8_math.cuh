@@ -103,31 +103,46 @@ __device__ __forceinline__ uint32_t rest8(uint32_t h) {
 // The upper bytes of four fp16 values.
 __device__ __forceinline__ uint32_t upper4(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 
-// A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
-// into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a
-// row that is not finite (whatever its parts then are: a row's products are its own).
 template <int D>
 __device__ __forceinline__ void load_row(const uint16_t *p, int sub, bool have, uint4 (&w)[D / 64]) {
 #pragma unroll
     for (int e = 0; e < D / 64; ++e)
         w[e] = have ? *reinterpret_cast<const uint4 *>(p + sub * (D / 8) + e * 8) : make_uint4(0, 0, 0, 0);
 }
+// The largest magnitude of a row, as bf16's bits: magnitudes order like them, with
+// infinities and NaN on top.
 template <int D>
-__device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl) {
-    constexpr int E = D / 8, kRow = D < 128 ? D : 128;
-    // magnitudes order like their bits; infinities and NaN come out on top
+__device__ __forceinline__ uint32_t row_top(const uint4 (&w)[D / 64]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < E / 8; ++e) {
+    for (int e = 0; e < D / 64; ++e) {
         m = __vmaxu2(m, __vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu));
         m = __vmaxu2(m, __vmaxu2(w[e].z & 0x7fff7fffu, w[e].w & 0x7fff7fffu));
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t top = max(m >> 16, m & 0xffffu);
-    const int k = max(-110, min(110, 7 - (int(top >> 7) - 127)));  // largest in [128, 256)
+    return max(m >> 16, m & 0xffffu);
+}
+// The power of two that brings such a magnitude to 2^7 .. 2^8; rows are scaled by at
+// most 2^kMaxUp (32 times that is still finite), and by 2^-120 at least.
+constexpr int kMaxUp = 110;
+__device__ __forceinline__ int fit_of(uint32_t top) { return 7 - (int(top >> 7) - 127); }
+
+// A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
+// into rows rh and rl of an operand tile of `rows` rows.  -> 2^-k, or NaN for a row
+// that is not finite (whatever its parts then are: a row's products are its own).
+// The low part ends at 2^-14: an element from 2^-7 on, 2^-14 of the largest at most,
+// keeps all its 8 bits; a smaller one is off by up to 2^-15, 2^-22 of the largest.
+// `maybe`: this thread has an element that small, zeros among them, or the row is past
+// 2^103 or below 2^-103: wide_row has to say whether that will do.
+template <int D>
+__device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl,
+                                           bool &maybe) {
+    constexpr int E = D / 8, kRow = D < 128 ? D : 128;
+    const uint32_t top = row_top<D>(w);
+    const int fit = fit_of(top), k = min(kMaxUp, fit);
     const f2 up = pair(pow2i(k), pow2i(k)), up32 = pair(32.f * pow2i(k), 32.f * pow2i(k));
-    uint32_t h[E / 4], l[E / 4];
+    uint32_t h[E / 4], l[E / 4], large = ~0u;  // every byte's top bit: hi's code is 5 (5 * 2^-9) or more
 #pragma unroll
     for (int e = 0; e < E / 8; ++e) {
         const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
@@ -144,7 +159,9 @@ __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, ui
         h[2 * e + 1] = join16(hh[2], hh[3]);
         l[2 * e] = join16(ll[0], ll[1]);
         l[2 * e + 1] = join16(ll[2], ll[3]);
+        large &= ((h[2 * e] & 0x7f7f7f7fu) + 0x7b7b7b7bu) & ((h[2 * e + 1] & 0x7f7f7f7fu) + 0x7b7b7b7bu);
     }
+    maybe = top > 0 && top < 0x7f80u && ((~large & 0x80808080u) || fit < -96 || fit > kMaxUp);
     if constexpr (E == 8) {
         uint8_t *t = tile + ((sub * 8) & 8);
         *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, sub >> 1)) = make_uint2(h[0], h[1]);
@@ -161,6 +178,72 @@ __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, ui
         }
     }
     return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-k);
+}
+
+// Whether a row's parts will do, and if not (a wide row) a power of two that its elements
+// are to be divided by, so that their products with the other side's stay inside fp32;
+// 0 if they do.  What a small element loses is nothing beside the larger ones, but the
+// other side may be zero wherever those are.  So a row is wide that has such an element
+// and more than one in 32 below 2^-5 (of 2^7 for the largest), zeros aside, or whose
+// factors would leave fp32.  A normal distribution has one in 2,000 below 2^-5: an
+// ordinary row never is wide.
+template <int D>
+__device__ __forceinline__ float wide_row(const uint4 (&w)[D / 64]) {
+    const uint32_t top = row_top<D>(w);
+    const int fit = fit_of(top), k = min(kMaxUp, fit);
+    // |x| < 2^(-5 - k) by halves, the top bits set so that nothing is borrowed
+    const uint32_t lim = (uint32_t(122 - k) << 7) - 1u, lim2 = lim | (lim << 16) | 0x80008000u;
+    uint32_t n = 0, small = 0;  // 128 for each that is not zero, and for those below
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = u[i] & 0x7fff7fffu, some = (m + 0x7fff7fffu) & 0x80008000u;
+            n = __dp4a(some, 0x01010101u, n);
+            small = __dp4a((lim2 - m) & some, 0x01010101u, small);
+        }
+    }
+    n = n << 9 | small >> 7;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    const bool wide = top > 0 && top < 0x7f80u && ((n & 0xffffu) * 32 > n >> 16 || fit < -96 || fit > kMaxUp);
+    return !wide ? 0.f : k < -60 ? 0x1p30f : k > 60 ? 0x1p-30f : 1.f;
+}
+
+// Sums of products in fp32: of a key as the cache holds it and a query times up, of a
+// new key times down and a query times up.
+__device__ __forceinline__ void add4(float (&acc)[4], float2 a, float2 b, uint32_t y0, uint32_t y1, float up) {
+    acc[0] = fmaf(a.x, __uint_as_float(y0 << 16) * up, acc[0]);
+    acc[1] = fmaf(a.y, __uint_as_float(y0 & 0xffff0000u) * up, acc[1]);
+    acc[2] = fmaf(b.x, __uint_as_float(y1 << 16) * up, acc[2]);
+    acc[3] = fmaf(b.y, __uint_as_float(y1 & 0xffff0000u) * up, acc[3]);
+}
+template <int D>
+__device__ __forceinline__ float dot_codes(const uint8_t *k, const uint16_t *q, float up) {
+    float acc[4] = {};
+#pragma unroll 2
+    for (int e = 0; e < D; e += 8) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(k + e);
+        const uint4 y = *reinterpret_cast<const uint4 *>(q + e);
+        add4(acc, f32x2_of(uint16_t(x.x)), f32x2_of(uint16_t(x.x >> 16)), y.x, y.y, up);
+        add4(acc, f32x2_of(uint16_t(x.y)), f32x2_of(uint16_t(x.y >> 16)), y.z, y.w, up);
+    }
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+template <int D>
+__device__ __forceinline__ float dot_rows(const uint16_t *k, float down, const uint16_t *q, float up) {
+    float acc[4] = {};
+#pragma unroll 1
+    for (int e = 0; e < D; e += 8) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(k + e), y = *reinterpret_cast<const uint4 *>(q + e);
+        const auto two = [down](uint32_t w) {
+            return make_float2(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+        };
+        add4(acc, two(x.x), two(x.y), y.x, y.y, up);
+        add4(acc, two(x.z), two(x.w), y.z, y.w, up);
+    }
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 // Sums of N values over a warp's lanes: value k's sum lands in v[0] of the

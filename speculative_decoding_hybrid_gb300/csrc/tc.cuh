@@ -212,6 +212,18 @@ __device__ __forceinline__ void ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr)
                  : "memory");
 }
+// 32 lanes x 32 bits of one column, loaded (waited for) and stored.
+__device__ __forceinline__ uint32_t ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(taddr)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ void st1(uint32_t taddr, uint32_t x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
+}
 __device__ __forceinline__ void ld_fence_regs(uint32_t (&r)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[i]));

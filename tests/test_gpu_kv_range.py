@@ -1,0 +1,159 @@
+"""Attention over the paged 8-bit cache where magnitudes lie far apart: queries
+and new keys with large channels that the other side is zero in, and rows near
+the ends of bf16's range; against the fp64 form."""
+import numpy as np
+import pytest
+import torch
+
+import kv_util as ku
+from gpu_util import build_lib, noted
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_lib()
+
+
+def rows_of(cache, n, seed):
+    """fp64 q [R, h_q, d], k and v [R, h_kv, d], N(0, 1)."""
+    g = np.random.RandomState(seed)
+    R = sum(n)
+    return tuple(g.standard_normal((R, h, cache.d)) for h in (cache.h_q, cache.h_kv, cache.h_kv))
+
+
+def check(name, cache, n, q, k, v, dev, window=0, sm_scale=None, split=0):
+    """One call against the fp64 form.  The error budget is kv_util's, with a weight's rounding as the header
+    states it: to fp16's 11 bits, 2^-11 of it at most, and to 2^-32 of the largest weight times V scale that the
+    row sees (each position's, times its code)."""
+    (qt, q), (kt, k), (vt, v) = ku.bf16(q), ku.bf16(k), ku.bf16(v)
+    c = ku.gpu_cache(cache, dev, window, sm_scale)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    o, lse = c.attend(0, torch.from_numpy(cache.table).to(dev), torch.tensor(cache.lens, dtype=torch.int32, device=dev),
+                      torch.from_numpy(cu).to(dev), qt.to(dev), kt.to(dev), vt.to(dev), max_len=max(cache.lens),
+                      max_rows=max(n), split_tokens=split, want_lse=True)
+    assert int(c.status.item()) == 0
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    sc = ku.default_scale(cache.d) if sm_scale is None else float(np.float32(sm_scale))
+    worst = [0.0, 0.0]
+    for r in range(len(n)):
+        a, b = cu[r], cu[r + 1]
+        if a == b:
+            continue
+        ro, rl, ra, rw = ku.attend_request(cache.dense(r, 0), q[a:b], k[a:b], v[a:b], window, sc)
+        ob, lb = ku.attend_bounds(ro, rl, ra, rw, cache.d)
+        ob = ob + 2.0 ** -12 * ra + floor(cache, r, q[a:b], k[a:b], window, sc)
+        assert np.isfinite(o[a:b]).all() and np.isfinite(lse[a:b]).all()
+        worst[0] = max(worst[0], noted("kv range %s: o" % name, np.max(np.abs(o[a:b] - ro) / ob)))
+        worst[1] = max(worst[1], noted("kv range %s: lse" % name, np.max(np.abs(lse[a:b] - rl) / lb)))
+    assert worst[0] <= 1.0 and worst[1] <= 1.0, worst
+
+
+def floor(cache, r, q, k, window, sm_scale):
+    """2^-32 max_t(p_t s_t) sum_t |code_t|, over the cached positions a row sees: [n, h_q, d]."""
+    L, T, hk = cache.lens[r], cache.T, cache.h_kv
+    n, h_q, d = q.shape
+    if L == 0:
+        return 0.0
+    x = cache.dense(r, 0)                                                    # [2, h, L, d]
+    ids = cache.table[r, :-(-L // T)]
+    sv = np.repeat(cache.scale[ids, 0, :, 1].astype(np.float64).T, T, 1)[:, :L]  # [h, L]
+    keys = np.concatenate([x[0], k.transpose(1, 0, 2)], 1)
+    z = np.einsum("nhgd,htd->nhgt", q.reshape(n, hk, h_q // hk, d), keys) * sm_scale
+    t, at = np.arange(L + n)[None], (L + np.arange(n))[:, None]
+    see = (t <= at) & (t > at - window if window else True)
+    z = np.where(see[:, None, None, :], z, -np.inf)
+    p = np.exp(z - z.max(-1, keepdims=True))
+    p = (p / p.sum(-1, keepdims=True))[..., :L]
+    codes = np.abs(x[1]) / np.where(sv > 0, sv, 1.0)[..., None]
+    top = (p * sv[None, :, None, :]).max(-1)                                 # [n, h, g]
+    total = np.einsum("nt,htd->nhd", see[:, :L].astype(float), codes)
+    return 2.0 ** -32 * (top[..., None] * total[:, :, None, :]).reshape(n, h_q, d)
+
+
+LAYOUTS = [(64, 8, 1, 2), (64, 16, 2, 8), (128, 2, 1, 4), (128, 16, 2, 2), (128, 8, 1, 3), (128, 8, 1, 16),
+           (256, 8, 1, 1), (256, 16, 2, 4)]
+
+
+@pytest.mark.parametrize("r", [8, 12, 14, 15, 17, 20, 30, 60, 100])
+@pytest.mark.parametrize("d,h_q,h_kv,rows", LAYOUTS)
+def test_large_query_channel_under_zero_keys(cuda_dev, d, h_q, h_kv, rows, r):
+    """One channel of the queries 2^r times the others; the keys, cached and new, are zero in it."""
+    cache = ku.Cache([300, 40, 0], h_q, h_kv, d, 32, seed=r)
+    n = [rows, max(1, rows - 1), rows]
+    q, k, v = rows_of(cache, n, 100 + r)
+    for h in range(h_kv):
+        c = (37 * h + 5 * r) % d
+        cache.kv[:, :, 0, h, :, c] = 0
+        k[:, h, c] = 0
+        q[:, h * h_q // h_kv:(h + 1) * h_q // h_kv, c] = 1.5 * 2.0 ** r
+    check("large query channel", cache, n, q, k, v, cuda_dev)
+    check("large query channel", cache, n, q, k, v, cuda_dev, window=50, split=128)
+
+
+@pytest.mark.parametrize("r", [13, 16, 24])
+@pytest.mark.parametrize("d,h_q,h_kv,rows", LAYOUTS)
+def test_many_large_query_channels_under_zero_keys(cuda_dev, d, h_q, h_kv, rows, r):
+    """All but an eighth of the channels, anywhere, 2^r times the rest, and only some rows' queries so."""
+    cache = ku.Cache([260, 700], h_q, h_kv, d, 64, seed=r)
+    n = [rows, rows]
+    q, k, v = rows_of(cache, n, 200 + r)
+    big = np.random.RandomState(r).permutation(d)[d // 8:]
+    cache.kv[..., big] = np.where(np.arange(2)[None, None, :, None, None, None] == 0, 0, cache.kv[..., big])
+    k[:, :, big] = 0
+    q[::2, ::2][..., big] *= 2.0 ** r
+    check("many large query channels", cache, n, q, k, v, cuda_dev)
+
+
+@pytest.mark.parametrize("r", [8, 12, 14, 17, 20, 60, 100])
+@pytest.mark.parametrize("d,h_q,h_kv,rows", LAYOUTS)
+def test_large_key_channel_under_zero_queries(cuda_dev, d, h_q, h_kv, rows, r):
+    """One channel of some new keys 2^r times the others; the queries are zero in it."""
+    cache = ku.Cache([130, 0], h_q, h_kv, d, 32, seed=r)
+    n = [rows, rows]
+    q, k, v = rows_of(cache, n, 300 + r)
+    c = (11 * r) % d
+    q[..., c] = 0
+    k[::2, :, c] = -1.25 * 2.0 ** r
+    check("large key channel", cache, n, q, k, v, cuda_dev, sm_scale=0.25)
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,rows", [(64, 4, 2, 4), (128, 8, 1, 2), (128, 8, 1, 16), (256, 8, 1, 4)])
+def test_large_channels_on_both_sides(cuda_dev, d, h_q, h_kv, rows):
+    """Queries large in one channel and new keys in another, each zero in the other's."""
+    cache = ku.Cache([70], h_q, h_kv, d, 32, seed=d)
+    q, k, v = rows_of(cache, [rows], 400)
+    cache.kv[:, :, 0, :, :, 7] = 0
+    q[..., 9], k[..., 7] = 0, 0
+    q[..., 7] = 2.0 ** 25
+    k[..., 9] = 2.0 ** 22
+    check("large channels on both sides", cache, [rows], q, k, v, cuda_dev)
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,rows", [(64, 4, 2, 4), (128, 8, 1, 2), (128, 8, 1, 16), (256, 8, 1, 4)])
+def test_ends_of_the_range(cuda_dev, d, h_q, h_kv, rows):
+    """Queries and new keys of 1e37 and of 1e-35, the other side as far the other way; zero rows among them."""
+    none = ku.Cache([0], h_q, h_kv, d, 32, seed=1)
+    q, k, v = rows_of(none, [rows], 500)
+    q[0, 0] = 0
+    for e in (123, 110, 100, -100, -110, -118):
+        check("ends of the range, new keys", none, [rows], q * 2.0 ** e, k * 2.0 ** -(e - 4), v, cuda_dev, sm_scale=0.01)
+    for e, s in ((122, -94), (100, -80), (-118, 112), (-105, 100)):
+        cache = ku.Cache([200], h_q, h_kv, d, 32, seed=2)
+        cache.scale[..., 0] = 2.0 ** s                       # keys of about 448 * 2^s at most
+        check("ends of the range, cache", cache, [rows], q * 2.0 ** e, k * 2.0 ** (s + 3), v, cuda_dev,
+              sm_scale=2.0 ** (-e - s - 9))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_finite_rows_of_the_largest_values_stay_finite(cuda_dev, d):
+    """A query of 3e38 in a channel that every key is zero in, over keys of 1e6 elsewhere."""
+    cache = ku.Cache([150], 2, 1, d, 32, seed=3)
+    cache.kv[:, :, 0, :, :, 3] = 0
+    cache.scale[..., 0] = 2.0 ** 13
+    q, k, v = rows_of(cache, [2], 600)
+    k *= 2.0 ** 13
+    k[..., 3] = 0
+    q[..., 3] = 3e38
+    check("largest values", cache, [2], q, k, v, cuda_dev, sm_scale=2.0 ** -24)
