@@ -593,8 +593,10 @@ typedef struct kv8_cache {
  *   split_tokens: 0 cuts the batch's work into equal ranges wherever they
  *   fall; n > 0 sums every n cached positions (rounded up to a multiple of
  *   128) by themselves, which makes a request's bits independent of what else
- *   is in the batch.  Sums and softmax statistics are fp32; a weight enters its
- *   product with v rounded to fp16's 11 bits, and to 2^-32 of the largest.
+ *   is in the batch.  Sums and softmax statistics are fp32; a weight, times its
+ *   page's V scale, enters the product with v rounded to fp16's 11 bits, and to
+ *   2^-32 of the largest such product that the row sees (if the V scales of the
+ *   request's pages lie within 2^48 of each other; zeros aside).
  *   q and the new keys enter with all their bits, of any finite magnitude, but
  *   for elements below 2^-14 of their row's largest in a row where no more
  *   than one in 32 of the elements (zeros aside) is below 2^-12 of it: those

@@ -19,6 +19,11 @@ __device__ __forceinline__ int scale_exp(float amax) {
 // 2^e for a normal exponent.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
+// The exponent of a power of two (of another positive number, its largest power of two's; -127 for zero).
+__device__ __forceinline__ float exponent_of(float x) {
+    return __uint_as_float(0x4b000000u | (__float_as_uint(x) >> 23)) - 8388735.f;  // 2^23 + 127
+}
+
 // Two fp32 -> two e4m3 codes (nearest even, +-448 beyond), lo in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;

@@ -16,10 +16,12 @@
 // A position is a tensor-memory lane, so its page's scales are two numbers of
 // the thread that owns the lane: K's multiplies the score, V's the weight.
 //
-// The softmax keeps a reference m per column, not the running maximum: a
-// column's weights are 2^(z - m), and only when some z passes m + kSlack (or a
-// page's V scale the reference one) is m moved and the sums rescaled; usually
-// that is once, at a segment's first tile.  One vote a tile decides.
+// The softmax keeps a reference m per column, not the running maximum: a column's
+// weights are 2^(z - m), and what enters the product is a weight times its page's V
+// scale, against the largest such scale: 2^(z + e - m).  Only when some z + e passes m
+// + kSlack (or a page's V scale the largest so far) is m moved and the sums rescaled;
+// usually that is once, at a segment's first tile.  One vote a tile decides.  So a page
+// whose large values get next to no weight takes no bits from the others' weights.
 //
 // Work is measured in tiles of 128 positions: a unit (request, kv head, block of RB
 // columns) costs its tiles plus a few for its ends, and the units laid end to end
@@ -62,11 +64,14 @@ using namespace kv8;
 
 constexpr int kTile = 128;      // positions a tile
 constexpr int kSms = 152;
-// Weights are scaled by 2^7 and at most 2^(7 + 8), inside fp16, whose normal numbers
-// go down to 2^-14: 2^-21 of a weight at the reference.  More slack moves the reference
+// Weights (times V scale) are scaled by 2^7 and at most 2^(7 + 8), inside fp16, whose normal
+// numbers go down to 2^-14: 2^-21 of a weight at the reference.  More slack moves the reference
 // less often (16 rows x 32 requests 145 us with 3, 121 with 6, 119.5 with 8 and with 10).
 constexpr float kBase = 128.f, kSlack = 8.f;
 constexpr float kUnset = -1e30f;
+// How far apart (in powers of two) V scales may lie for a reference to follow them: weights
+// before their V scale are then at most 2^(kSlack + 2 kLift), and sums of 2^20 of them finite.
+constexpr float kLift = 48.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
@@ -754,8 +759,15 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             float z[N];
 #pragma unroll
             for (int c = 0; c < N / 2; ++c) l[c] = 0;
-            float vref = pow2i(kMinScaleExp), vinv = kBase / vref;
+            float vref = pow2i(kMinScaleExp), vinv = kBase / vref;  // the largest V scale so far
+            float eref = kMinScaleExp, sunk = 0.f;  // its exponent; how far references have followed it down
 
+            // what goes with tile i's scores is there: its pages' scales, or the new keys'
+            const auto tile_known = [&](int i) {
+                const int y = gp + i;
+                return i >= nc ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
+                               : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
+            };
             // Tile by tile; where a column or a new key is wide the loop is left before the tile, its scores
             // are put right and it goes on.  (In the loop that code, taken or not, called or not, made 16 rows
             // x 32 requests 133 to 136 us, in a second form of the loop 128 to 131; beside it 121.5.)
@@ -763,23 +775,22 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 for (; i < stop; ++i) {
                     const bool is_fresh = i >= nc;
                     const int x = gs + i, y = gp + i, t = (g.tile0 + i) * kTile + pos_in;
-                    if (ok)
-                        ok = is_fresh ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
-                                      : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
+                    if (ok) ok = tile_known(i);
                     if (is_fresh && fixed != i && __any_sync(0xffffffffu, ok && s.fresh_wide)) break;
                     const float2 sc =
-                        is_fresh ? make_float2(pos_in < 32 && (pos_in & 15) < g.n ? fabsf(s.fresh_k[pos_in & 15]) : 0.f, 0.f)
-                                 : s.scales[y % C::kScales][pos_in >> shift];
+                        is_fresh
+                            ? make_float2(fabsf(pos_in < 32 && (pos_in & 15) < g.n ? s.fresh_k[pos_in & 15] : 0.f), 0.f)
+                            : s.scales[y % C::kScales][pos_in >> shift];
                     // whole: every row sees every position of the tile
-                    const bool whole = !is_fresh && (g.tile0 + i + 1) * kTile <= g.len && (g.tile0 + i) * kTile >= lo_last;
-                    if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
-                    tc::fence_after();
-
+                    const int tile = g.tile0 + i;
+                    const bool whole = !is_fresh && (tile + 1) * kTile <= g.len && tile * kTile >= lo_last;
                     // While some row of the request may not have seen a position (a segment's first
                     // tile, and those that its window begins in or past) every column's reference
-                    // follows its largest score, which z holds as it is; from then on z is against
-                    // the reference.  Both go by the request alone.
+                    // follows its largest weight, and z holds the scores as they are; from then on z is
+                    // against the reference.  Both go by the request alone.
                     const bool first = i == 0 || lo_request >= (is_fresh ? g.len : (g.tile0 + i) * kTile);
+                    if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
+                    tc::fence_after();
                     {
                         uint32_t hi[N], lo[N];
                         const uint32_t at = tm + lane_base + (x & 1) * C::kNs + col0;
@@ -849,13 +860,21 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             i = nt;
                             break;
                         }
-#pragma unroll
-                        for (int c = 0; c < N; ++c) {
-                            const float top = warp_max(z[c]);
-                            if (lane == 0) s.col_max[warp & 3][col0 + c] = top;
-                        }
                         const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
                         if (lane == 0) s.v_max[grp][warp & 3] = __uint_as_float(vm);
+                        group_sync(grp);
+                        const float vnow = fmaxf(fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]),
+                                                       fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
+                        // a reference is to a weight times its V scale (in powers of two, against the largest: 0
+                        // or less, so a vote by the weight alone misses none), and follows the largest scale down
+                        const float enow = vnow > vref ? exponent_of(vnow) : eref;
+                        const float lift = is_fresh ? 0.f : fmaxf(exponent_of(sc.y) - enow, -kLift);
+                        const float drop = i > 0 ? fminf(enow - eref, kLift - sunk) : 0.f;
+#pragma unroll
+                        for (int c = 0; c < N; ++c) {
+                            const float top = warp_max(z[c] + lift);
+                            if (lane == 0) s.col_max[warp & 3][col0 + c] = top;
+                        }
                         group_sync(grp);
                         if (pos_in < N) {
                             const int c = col0 + pos_in;
@@ -863,16 +882,18 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                             const float top = fmaxf(fmaxf(s.col_max[0][c], s.col_max[1][c]),
                                                     fmaxf(s.col_max[2][c], s.col_max[3][c]));
                             // columns within the slack stay, or a column's bits would go by its neighbours
-                            const float now = first ? fmaxf(top, was) : top > kSlack ? was + top : was;
+                            const float now = first                  ? fmaxf(top, was - drop)
+                                              : top + drop > kSlack ? was + top
+                                                                    : was - drop;
                             s.col_nm[c] = -now;
                             s.col_fac[c] = ex2(was - now);
                             s.col_l[c] = first ? -now : was - now;
                         }
-                        const float vnow = fmaxf(
-                            fmaxf(fmaxf(s.v_max[grp][0], s.v_max[grp][1]), fmaxf(s.v_max[grp][2], s.v_max[grp][3])), vref);
                         const float vfac = vref / vnow;
                         vref = vnow;
                         vinv = kBase / vnow;
+                        eref = enow;
+                        sunk += drop;
                         group_sync(grp);
 #pragma unroll
                         for (int c = 0; c < N; c += 2) {
@@ -977,16 +998,13 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     if (lane == 0) arrive(&s.p_full[y & 1]);
                 }
                 if (i >= nt) break;
-                const bool is_fresh = i >= nc;
-                const int x = gs + i, y = gp + i;
-                if (ok)
-                    ok = is_fresh ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
-                                  : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
+                const int x = gs + i;
+                if (ok) ok = tile_known(i);
                 if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
                 __syncwarp();
                 tc::fence_after();
-                wide_scores<D, RB>(a, s, s.seg[k % kQueue], is_fresh ? -1 : (g.tile0 + i) * kTile + pos_in, pos_in, col0,
-                                   tm + lane_base + (x & 1) * C::kNs + col0);
+                wide_scores<D, RB>(a, s, s.seg[k % kQueue], i >= nc ? -1 : (g.tile0 + i) * kTile + pos_in, pos_in,
+                                   col0, tm + lane_base + (x & 1) * C::kNs + col0);
                 fixed = i;
                 stop = wide ? i + 1 : nt;
             }

@@ -1,6 +1,7 @@
 """Attention over the paged 8-bit cache where magnitudes lie far apart: queries
-and new keys with large channels that the other side is zero in, and rows near
-the ends of bf16's range; against the fp64 form."""
+and new keys with large channels that the other side is zero in, rows near the
+ends of bf16's range, and pages with far larger V scales and next to no weight;
+against the fp64 form."""
 import numpy as np
 import pytest
 import torch
@@ -138,7 +139,8 @@ def test_ends_of_the_range(cuda_dev, d, h_q, h_kv, rows):
     q, k, v = rows_of(none, [rows], 500)
     q[0, 0] = 0
     for e in (123, 110, 100, -100, -110, -118):
-        check("ends of the range, new keys", none, [rows], q * 2.0 ** e, k * 2.0 ** -(e - 4), v, cuda_dev, sm_scale=0.01)
+        check("ends of the range, new keys", none, [rows], q * 2.0 ** e, k * 2.0 ** -(e - 4), v, cuda_dev,
+              sm_scale=0.01)
     for e, s in ((122, -94), (100, -80), (-118, 112), (-105, 100)):
         cache = ku.Cache([200], h_q, h_kv, d, 32, seed=2)
         cache.scale[..., 0] = 2.0 ** s                       # keys of about 448 * 2^s at most
@@ -157,3 +159,83 @@ def test_finite_rows_of_the_largest_values_stay_finite(cuda_dev, d):
     k[..., 3] = 0
     q[..., 3] = 3e38
     check("largest values", cache, [2], q, k, v, cuda_dev, sm_scale=2.0 ** -24)
+
+
+def scaled_page(cache, j, e, score_down, channel=0):
+    """Request 0's page j: values 2^e larger, keys that score `score_down` below the others' (queries hold
+    1 in `channel`, in which all other keys are zero)."""
+    p = cache.table[0, j]
+    cache.kv[:, :, 0, :, :, channel] = 0
+    cache.kv[p, :, 0] = 0
+    cache.kv[p, :, 0, :, :, channel] = ku.encode(-1.0)
+    cache.scale[p, :, :, 0] = score_down
+    cache.scale[p, :, :, 1] *= 2.0 ** e
+
+
+@pytest.mark.parametrize("e", [10, 20, 24, 28, 34, 40])
+@pytest.mark.parametrize("d,h_q,h_kv,rows", [(64, 8, 1, 1), (128, 8, 1, 2), (128, 16, 2, 8), (256, 8, 1, 4)])
+def test_large_values_without_weight(cuda_dev, d, h_q, h_kv, rows, e):
+    """A page whose values are 2^e larger takes next to no weight: the others make the output, wherever it lies."""
+    for j in (0, 5, 18):
+        cache = ku.Cache([600], h_q, h_kv, d, 32, seed=e)
+        scaled_page(cache, j, e, 64.0)
+        q, k, v = rows_of(cache, [rows], 700 + e)
+        q[..., 0], k[..., 0] = 1.0, 0.0
+        for split in (0, 128):
+            check("large values without weight", cache, [rows], q, k, v, cuda_dev, sm_scale=1.0, split=split)
+
+
+@pytest.mark.parametrize("e", [16, 32])
+def test_large_values_of_any_weight(cuda_dev, e):
+    """The same with a weight that makes up for the size, or leaves a part of it."""
+    for down in (0.5 * e, 0.6931471805599453 * e, 1.2 * e):
+        cache = ku.Cache([600], 8, 1, 128, 32, seed=e)
+        scaled_page(cache, 7, e, float(np.float32(down)))
+        q, k, v = rows_of(cache, [2], 800 + e)
+        q[..., 0], k[..., 0] = 1.0, 0.0
+        check("large values of any weight", cache, [2], q, k, v, cuda_dev, sm_scale=1.0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e", [24, 40])
+def test_large_values_that_other_rows_see(cuda_dev, d, e):
+    """Row 0 alone sees the last position of a page whose values are 2^e larger; the rows after it see none."""
+    T, L, window = 32, 400, 113                         # row 0 sees positions from 288 = 9 * 32 on
+    cache = ku.Cache([L], 8, 1, d, T, seed=e)
+    cache.scale[cache.table[0, 8], :, :, 1] *= 2.0 ** e  # positions 256 .. 287
+    q, k, v = rows_of(cache, [4], 900)
+    for w in (window, window + 1, window + 2):
+        for split in (0, 128):
+            check("large values that others see", cache, [4], q, k, v, cuda_dev, window=w, split=split)
+
+
+def test_values_that_rise_by_pages(cuda_dev):
+    """V scales that rise page by page, 2^40 in all, under scores that fall as fast, rise, or stay."""
+    for fall in (-1.5, 0.0, 0.6931471805599453, 1.0, 2.0):
+        for sign in (1, -1):
+            cache = ku.Cache([640], 8, 1, 128, 32, seed=40)
+            cache.kv[:, :, 0, :, :, 0] = 0
+            for j, p in enumerate(cache.table[0]):
+                x = sign * 2.0 * j
+                cache.kv[p, :, 0] = 0
+                cache.kv[p, :, 0, :, :, 0] = ku.encode(-1.0 if fall * x > 0 else 1.0)
+                cache.scale[p, :, :, 0] = max(2.0 ** -20, abs(fall * x))
+                cache.scale[p, :, :, 1] *= 2.0 ** x
+            q, k, v = rows_of(cache, [3], 41)
+            q[..., 0], k[..., 0] = 1.0, 0.0
+            check("values that rise by pages", cache, [3], q, k, v, cuda_dev, sm_scale=1.0)
+            check("values that rise by pages", cache, [3], q, k, v, cuda_dev, sm_scale=1.0, split=256)
+
+
+def test_pages_of_zeros_before_the_others(cuda_dev):
+    """A first tile of values zero (the smallest scale there is) that scores highest, then ordinary pages."""
+    cache = ku.Cache([700], 8, 1, 128, 32, seed=42)
+    cache.kv[:, :, 0, :, :, 0] = 0
+    for p in cache.table[0, :4]:
+        cache.kv[p] = 0
+        cache.kv[p, :, 0, :, :, 0] = ku.encode(20.0)
+        cache.scale[p, :, :, 0], cache.scale[p, :, :, 1] = 1.0, 2.0 ** -100
+    q, k, v = rows_of(cache, [2], 43)
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    check("pages of zeros first", cache, [2], q, k, v, cuda_dev, sm_scale=1.0)
+    check("pages of zeros first", cache, [2], q, k, v, cuda_dev, sm_scale=1.0, split=256)
