@@ -594,7 +594,8 @@ typedef struct kv8_cache {
  *   fall; n > 0 sums every n cached positions (rounded up to a multiple of
  *   128) by themselves, which makes a request's bits independent of what else
  *   is in the batch.  Sums and softmax statistics are fp32; a weight, times its
- *   page's V scale, enters the product with v rounded to fp16's 11 bits, and to
+ *   page's V scale, enters the product with v rounded to fp16's 11 bits (by
+ *   2^-11 of it at most; their sum, and lse, are of the unrounded ones), and to
  *   2^-32 of the largest such product that the row sees (if the V scales of the
  *   request's pages lie within 2^48 of each other; zeros aside).
  *   q and the new keys enter with all their bits, of any finite magnitude, but

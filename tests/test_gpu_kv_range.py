@@ -1,7 +1,7 @@
 """Attention over the paged 8-bit cache where magnitudes lie far apart: queries
 and new keys with large channels that the other side is zero in, rows near the
-ends of bf16's range, and pages with far larger V scales and next to no weight;
-against the fp64 form."""
+ends of bf16's range, pages with far larger V scales and next to no weight, and
+weights whose rounding shows most; against the fp64 form."""
 import numpy as np
 import pytest
 import torch
@@ -239,3 +239,24 @@ def test_pages_of_zeros_before_the_others(cuda_dev):
     q[..., 0], k[..., 0] = 1.0, 0.0
     check("pages of zeros first", cache, [2], q, k, v, cuda_dev, sm_scale=1.0)
     check("pages of zeros first", cache, [2], q, k, v, cuda_dev, sm_scale=1.0, split=256)
+
+
+def test_a_late_position_that_takes_all(cuda_dev):
+    """One late position outweighs all others by less than moves a reference, so that its weight is rounded where
+    it is no power of two: by up to 2^-11, which the unrounded sum does not share."""
+    L = 300
+    cache = ku.Cache([L], 8, 1, 128, 32, seed=44)
+    cache.kv[:, :, 0] = 0
+    cache.scale[..., 0] = 1.0
+    cache.kv[cache.table[0, 8], :, 0, :, 10, 0] = ku.encode(1.0)          # position 266, in the third tile
+    cache.kv[cache.table[0, 0], :, 0, :, 0, 1] = ku.encode(1.0)           # and position 0, the reference
+    q, k, v = rows_of(cache, [16], 45)
+    q[:], k[:] = 0, 0
+    q[..., 1] = 60.0
+    q[..., 0] = 60.0 + 4.9 + 0.62 * np.arange(128).reshape(16, 8) / 128   # bf16 steps of 0.5 round these
+    q[..., 2:] = 0
+    check("a late position takes all", cache, [16], q, k, v, cuda_dev, sm_scale=1.0)
+    q[..., 0] = 4.9 + 0.62 * np.arange(128).reshape(16, 8) / 128
+    q[..., 1] = 0
+    cache.scale[:] = 1.0
+    check("a late position takes all", cache, [16], q, k, v, cuda_dev, sm_scale=1.0)
