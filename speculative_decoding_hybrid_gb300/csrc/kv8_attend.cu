@@ -59,6 +59,8 @@
 // costs nothing.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "kv8_math.cuh"
 
 namespace {
@@ -1274,17 +1276,19 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// Kept once it is found; a failure is not.
 EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<EncodeTiledFn>(nullptr);
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
+    static std::atomic<EncodeTiledFn> fn{nullptr};
+    EncodeTiledFn f = fn.load(std::memory_order_acquire);
+    if (f) return f;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<EncodeTiledFn>(p);
+    fn.store(f, std::memory_order_release);
+    return f;
 }
 
 // A layer's pages as [page][2 h_kv page_tokens rows][d] bytes; boxes of one
@@ -1350,9 +1354,10 @@ Plan plan_of(const kv8_cache *c, int32_t B, int32_t max_len, int32_t max_rows, i
 template <int D, int RB>
 int launch(const AttendArgs &a, int ctas, cudaStream_t st) {
     using C = Cfg<D, RB>;
-    static const cudaError_t set = cudaFuncSetAttribute(kv8_attend_kernel<D, RB>,
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (set != cudaSuccess) return GDN_ERR_CUDA;
+    // for every launch: the limit is the current device's
+    if (cudaFuncSetAttribute(kv8_attend_kernel<D, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+        cudaSuccess)
+        return GDN_ERR_CUDA;
     return gdn_host::launch_pdl(kv8_attend_kernel<D, RB>, dim3(unsigned(ctas)), dim3(C::kThreads), C::kSmem, st, a);
 }
 
