@@ -282,7 +282,7 @@ class PagedKv(Kv8Cache):
         stage = self._stage[:B].numpy()
         stage[:, :cap] = self.tables[idx]
         stage[:, cap] = self.length[idx]
-        s = torch.cuda.current_stream() if stream is None else _stream_object(stream)
+        s = torch.cuda.current_stream(self._device) if stream is None else _stream_object(stream)
         with torch.cuda.stream(s):
             both = self._stage[:B].to(self.dev_table.device, non_blocking=True)
             self.dev_table[:B].copy_(both[:, :cap])
