@@ -579,7 +579,7 @@ typedef struct kv8_cache {
  * kv8_attend -- one layer's attention for a transaction's packed rows.
  *   Request r has cache_len[r] committed positions (0 .. max_len) and n =
  *   cu_rows[r+1]-cu_rows[r] rows (0 .. max_rows <= GDN_MAX_ROWS; 0 rows: no
- *   work).  Row i sits at position cache_len[r] + i and sees the committed
+ *   work; with row_capacity 0 the rows' pointers may be NULL, as in kv8_append).  Row i sits at position cache_len[r] + i and sees the committed
  *   positions and the new rows j <= i, all inside the window; k_new and v_new
  *   are used as given (bf16), the cache as stored.  With k_new = v_new = NULL
  *   every row sees the committed positions only (the last `window` of them).

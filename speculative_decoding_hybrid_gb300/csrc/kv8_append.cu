@@ -278,7 +278,9 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
         return GDN_ERR_ARG;
     if (int64_t(table_pages) * cache->page_tokens > gdn_host::kKv8MaxLen) return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0) return GDN_OK;
-    if (!cu_rows || !cache_len || !table || !k_new || !v_new) return GDN_ERR_NULL;
+    // (an empty tensor's address is null: with no rows, or no pages, nothing of theirs is read)
+    if (!cu_rows || !cache_len || (!table && table_pages > 0) || (row_capacity > 0 && (!k_new || !v_new)))
+        return GDN_ERR_NULL;
     if (!gdn_host::kv8_rows_ok(k_new, k_stride, cache->h_kv, cache->d) ||
         !gdn_host::kv8_rows_ok(v_new, v_stride, cache->h_kv, cache->d))
         return GDN_ERR_ARG;

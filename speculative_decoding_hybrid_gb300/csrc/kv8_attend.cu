@@ -1388,7 +1388,9 @@ static int attend(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_
         max_len < 0 || max_len > gdn_host::kKv8MaxLen || max_rows < 0 || max_rows > GDN_MAX_ROWS || split_tokens < 0)
         return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0) return GDN_OK;
-    if (!cu_rows || !cache_len || (!table && table_pages > 0) || !q || !o || !k_new != !v_new) return GDN_ERR_NULL;
+    // (an empty tensor's address is null: with no rows nothing of theirs is read)
+    if (!cu_rows || !cache_len || (!table && table_pages > 0) || (row_capacity > 0 && (!q || !o)) || !k_new != !v_new)
+        return GDN_ERR_NULL;
     if (!gdn_host::kv8_rows_ok(q, q_stride, cache->h_q, cache->d) ||
         !gdn_host::kv8_rows_ok(o, o_stride, cache->h_q, cache->d))
         return GDN_ERR_ARG;

@@ -1,0 +1,43 @@
+"""The paged 8-bit cache's calls at their smallest: no rows at all, one row or one head of any stride."""
+import numpy as np
+import pytest
+import torch
+
+import kv_util as ku
+from gpu_util import build_lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_lib()
+
+
+def ints(dev, *x):
+    return torch.tensor(x, dtype=torch.int32, device=dev)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("split", [0, 128])
+def test_no_rows_in_the_whole_batch(cuda_dev, d, split):
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    cache = ku.Cache([2000, 3, 0], 8, 2, d, 64, seed=d)
+    c = ku.gpu_cache(cache, cuda_dev)
+    table, lens = torch.from_numpy(cache.table).to(cuda_dev), ints(cuda_dev, *cache.lens)
+    q = torch.empty((0, 8, d), dtype=torch.bfloat16, device=cuda_dev)
+    k = torch.empty((0, 2, d), dtype=torch.bfloat16, device=cuda_dev)
+    kv, scale = c.kv.clone(), c.scale.clone()
+    cu = ints(cuda_dev, 0, 0, 0, 0)
+    for new in ((k, k), (None, None)):
+        o, lse = c.attend(0, table, lens, cu, q, *new, max_len=2000, split_tokens=split, want_lse=True)
+        assert o.shape == (0, 8, d) and lse.shape == (0, 8)
+    c.append(0, table, lens, cu, k, k)
+    c.append(0, table[:, :0], ints(cuda_dev, 0, 0, 0), cu, k, k)
+    assert int(c.status.item()) == 0 and torch.equal(c.kv, kv) and torch.equal(c.scale, scale)
+    # rows that are not there are still found out
+    c.attend(0, table, lens, ints(cuda_dev, 0, 0, 2, 2), q, k, k, max_len=2000, split_tokens=split)
+    assert int(c.status.item()) == gs.DEV_ROWS_BAD
+    c.status.zero_()
+    c.append(0, table, lens, ints(cuda_dev, 0, 0, 2, 2), k, k)
+    assert int(c.status.item()) == gs.DEV_ROWS_BAD and torch.equal(c.kv, kv)

@@ -92,3 +92,20 @@ def test_a_first_failure_does_not_stay(fake, what):
         assert attend(c) == gs.GDN_ERR_CUDA and fake.fake_launches() == 0
         assert attend(c) == gs.GDN_OK and fake.fake_launches() == 1
     """ % what)
+
+
+def test_nothing_to_do_needs_no_rows(fake):
+    """No rows in the whole batch (empty tensors have a null address): launched, for the device's checks of the
+    lengths, and never a null pointer where there are rows."""
+    run(fake, """
+        c = cache()
+        none = dict(cap=0, q=None, k=None, v=None, o=None)
+        assert attend(c, **none) == gs.GDN_OK
+        for name in ("q", "k", "v", "o"):
+            assert attend(c, **{name: None}) == gs.GDN_ERR_NULL, name
+        assert append(c, cap=0, k=None, v=None) == gs.GDN_OK
+        assert append(c, cap=0, k=None, v=None, table=None, pages=0) == gs.GDN_OK
+        assert append(c, table=None, pages=0) == gs.GDN_OK
+        for kw in (dict(k=None), dict(v=None), dict(table=None)):
+            assert append(c, **kw) == gs.GDN_ERR_NULL, kw
+    """)
