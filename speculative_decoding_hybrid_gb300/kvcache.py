@@ -98,8 +98,11 @@ class Kv8Cache:
             raise self._bad_lists("cache_len and cu_rows")
         R, a, b = q.shape
         q_s, c, one = q.stride()
-        if q.dtype is not _BF16 or a != h_q or b != d or c != d or one != 1 or q.get_device() != device:
+        if (q.dtype is not _BF16 or a != h_q or b != d or (c != d and h_q > 1) or one != 1
+                or q.get_device() != device):
             raise self._bad_rows("q", h_q)
+        if R <= 1:
+            q_s = h_q * d  # a single row's stride, as a single head's, says nothing
         k_p = v_p = None
         k_s = v_s = 0
         if k_new is not None or v_new is not None:
@@ -107,22 +110,28 @@ class Kv8Cache:
                 raise ValueError("k_new and v_new come together")
             n, a, b = k_new.shape
             k_s, c, one = k_new.stride()
-            if (k_new.dtype is not _BF16 or n < R or a != h_kv or b != d or c != d or one != 1
+            if (k_new.dtype is not _BF16 or n < R or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
                     or k_new.get_device() != device):
                 raise self._bad_rows("k_new", h_kv)
+            if n <= 1:
+                k_s = h_kv * d
             n, a, b = v_new.shape
             v_s, c, one = v_new.stride()
-            if (v_new.dtype is not _BF16 or n < R or a != h_kv or b != d or c != d or one != 1
+            if (v_new.dtype is not _BF16 or n < R or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
                     or v_new.get_device() != device):
                 raise self._bad_rows("v_new", h_kv)
+            if n <= 1:
+                v_s = h_kv * d
             k_p, v_p = k_new.data_ptr(), v_new.data_ptr()
         o_s = h_q * d
         if out is not None:
             n, a, b = out.shape
             o_s, c, one = out.stride()
-            if (out.dtype is not _BF16 or n < R or a != h_q or b != d or c != d or one != 1
+            if (out.dtype is not _BF16 or n < R or a != h_q or b != d or (c != d and h_q > 1) or one != 1
                     or out.get_device() != device):
                 raise self._bad_rows("out", h_q)
+            if n <= 1:
+                o_s = h_q * d
         key = (B, max_len, max_rows, split_tokens)
         need = self._workspace.get(key)
         if need is None:
@@ -172,13 +181,16 @@ class Kv8Cache:
             acc_p = accept_len.data_ptr()
         R, a, b = k_new.shape
         k_s, c, one = k_new.stride()
-        if k_new.dtype is not _BF16 or a != h_kv or b != d or c != d or one != 1 or k_new.get_device() != device:
+        if (k_new.dtype is not _BF16 or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
+                or k_new.get_device() != device):
             raise self._bad_rows("k_new", h_kv)
         n, a, b = v_new.shape
         v_s, c, one = v_new.stride()
-        if (v_new.dtype is not _BF16 or n != R or a != h_kv or b != d or c != d or one != 1
+        if (v_new.dtype is not _BF16 or n != R or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
                 or v_new.get_device() != device):
             raise self._bad_rows("v_new", h_kv)
+        if R <= 1:
+            k_s = v_s = h_kv * d
         st = gs.lib.kv8_append(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(), pages,
                                table_s, k_new.data_ptr(), k_s, v_new.data_ptr(), v_s, acc_p, max_rows, self._status,
                                _raw_stream(device) if stream is None else gs._stream(stream))

@@ -41,3 +41,33 @@ def test_no_rows_in_the_whole_batch(cuda_dev, d, split):
     c.status.zero_()
     c.append(0, table, lens, ints(cuda_dev, 0, 0, 2, 2), k, k)
     assert int(c.status.item()) == gs.DEV_ROWS_BAD and torch.equal(c.kv, kv)
+
+
+@pytest.mark.parametrize("h_q,h_kv,rows", [(8, 2, 1), (4, 1, 3), (1, 1, 2), (4, 1, 1)])
+def test_strides_of_single_rows_and_heads_say_nothing(cuda_dev, h_q, h_kv, rows):
+    """One row, or one head: whatever stride its dimension has, as transposes and expansions leave it."""
+    d = 128
+    cache = ku.Cache([70], h_q, h_kv, d, 32, room=[90], seed=rows)
+    c = ku.gpu_cache(cache, cuda_dev)
+    table, lens, cu = torch.from_numpy(cache.table).to(cuda_dev), ints(cuda_dev, 70), ints(cuda_dev, 0, rows)
+    g = torch.Generator(device=cuda_dev).manual_seed(rows)
+    plain = [torch.randn((rows, h, d), generator=g, device=cuda_dev).to(torch.bfloat16) for h in (h_q, h_kv, h_kv)]
+
+    def odd(x):
+        stride = [x.stride(0) if rows > 1 else 8, d if x.shape[1] > 1 else 1, 1]
+        y = torch.empty_strided(x.shape, stride, dtype=x.dtype, device=x.device)
+        return y.copy_(x)
+
+    strange = [odd(x) for x in plain]
+    assert any(x.stride() != y.stride() for x, y in zip(plain, strange))
+    want = c.attend(0, table, lens, cu, *plain, max_len=70, max_rows=rows, want_lse=True)
+    got = c.attend(0, table, lens, cu, *strange, max_len=70, max_rows=rows, want_lse=True, out=odd(plain[0]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    before = c.kv.clone(), c.scale.clone()
+    c.append(0, table, lens, cu, plain[1], plain[2])
+    after = c.kv.clone(), c.scale.clone()
+    c.kv.copy_(before[0])
+    c.scale.copy_(before[1])
+    c.append(0, table, lens, cu, strange[1], strange[2])
+    assert int(c.status.item()) == 0 and torch.equal(c.kv, after[0]) and torch.equal(c.scale, after[1])
+    assert not torch.equal(c.kv, before[0])
