@@ -495,12 +495,21 @@ def _i32(n=0):
     return ctypes.c_int32(n)
 
 
+def _table_row(fn: str, table: np.ndarray, n_pages: int = 0) -> int:
+    """Address of a page table's row.  What C would read as something else, or past the row's end, stops here."""
+    if not isinstance(table, np.ndarray) or table.dtype != np.int32 or table.ndim != 1 or not table.flags.c_contiguous:
+        raise ValueError("%s: a page table is a contiguous int32 row" % fn)
+    if n_pages > len(table):
+        raise GdnError(fn, GDN_ERR_ARG)
+    return table.ctypes.data
+
+
 def kv8_pages_reserve(pool: Pool, table: np.ndarray, n_pages: int, length: int, n_new: int, page_tokens: int):
     """-> (n_pages, (src, dst) to copy before the append, or None).  table: int32 row, changed in place."""
     have, src, dst, n = _i32(n_pages), _i32(-1), _i32(-1), _i32()
     _check("kv8_pages_reserve", lib.kv8_pages_reserve(
-        ctypes.byref(pool.c), table.ctypes.data, len(table), ctypes.byref(have), length, n_new, page_tokens,
-        ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)))
+        ctypes.byref(pool.c), _table_row("kv8_pages_reserve", table), len(table), ctypes.byref(have), length, n_new,
+        page_tokens, ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)))
     return have.value, ((src.value, dst.value) if n.value else None)
 
 
@@ -509,19 +518,23 @@ def kv8_pages_fork(pool: Pool, src_table: np.ndarray, src_pages: int, length: in
     """-> (pages of dst, (src, dst) to copy, or None).  dst_table: an empty table's int32 row, changed in place."""
     have, src, dst, n = _i32(), _i32(-1), _i32(-1), _i32()
     _check("kv8_pages_fork", lib.kv8_pages_fork(
-        ctypes.byref(pool.c), src_table.ctypes.data, src_pages, length, page_tokens, dst_table.ctypes.data,
-        len(dst_table), ctypes.byref(have), ctypes.byref(src), ctypes.byref(dst), ctypes.byref(n)))
+        ctypes.byref(pool.c), _table_row("kv8_pages_fork", src_table, src_pages), src_pages, length, page_tokens,
+        _table_row("kv8_pages_fork", dst_table), len(dst_table), ctypes.byref(have), ctypes.byref(src),
+        ctypes.byref(dst), ctypes.byref(n)))
     return have.value, ((src.value, dst.value) if n.value else None)
 
 
 def kv8_pages_free(pool: Pool, table: np.ndarray, n_pages: int):
     have = _i32(n_pages)
-    _check("kv8_pages_free", lib.kv8_pages_free(ctypes.byref(pool.c), table.ctypes.data, ctypes.byref(have)))
+    _check("kv8_pages_free", lib.kv8_pages_free(
+        ctypes.byref(pool.c), _table_row("kv8_pages_free", table, n_pages), ctypes.byref(have)))
 
 
 def kv8_pages_compact(pool: Pool, tables: np.ndarray, n_pages: np.ndarray):
     """-> (move_src, move_dst) int32 arrays.  tables: C-contiguous int32 [n][cap], renamed in place."""
-    assert tables.dtype == np.int32 and tables.flags.c_contiguous and n_pages.dtype == np.int32
+    if (tables.dtype != np.int32 or tables.ndim != 2 or not tables.flags.c_contiguous or n_pages.dtype != np.int32
+            or n_pages.shape != tables.shape[:1] or not n_pages.flags.c_contiguous):
+        raise ValueError("kv8_pages_compact: tables are contiguous int32 [requests, pages], n_pages int32 [requests]")
     src, dst, n = np.empty(pool.c.num_slots, np.int32), np.empty(pool.c.num_slots, np.int32), _i32()
     _check("kv8_pages_compact", lib.kv8_pages_compact(
         ctypes.byref(pool.c), tables.shape[0], tables.ctypes.data, tables.shape[1], n_pages.ctypes.data,
