@@ -37,7 +37,8 @@ EXPORTS = ["gdn_decode_step", "gdn_verify", "mtp_accept_workspace_bytes", "mtp_g
            "gdn_pool_share", "gdn_pool_release", "plan_transaction", "gdn_pool_apply", "gdn_pool_abort",
            "gdn_decode_transaction", "gdn_decode_transaction_at", "gdn_status_string",
            "gdn_selftest_prefill_timeout", "kv8_attend_workspace_bytes", "kv8_attend", "kv8_append",
-           "kv8_selftest_attend_timeout", "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free", "kv8_pages_compact"]
+           "kv8_selftest_attend_timeout", "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free",
+           "kv8_pages_compact"]
 
 
 class GdnError(RuntimeError):
@@ -383,8 +384,8 @@ def kv8_attend(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, 
                workspace_bytes, dev_status, stream=None):
     return _check("kv8_attend", lib.kv8_attend(
         ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
-        table_stride, _ptr(q), q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse), max_len, max_rows,
-        split_tokens, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
+        table_stride, _ptr(q), q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse),
+        max_len, max_rows, split_tokens, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
 
 
 def kv8_selftest_attend_timeout(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages,
@@ -400,7 +401,8 @@ def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, 
                k_stride, v_new, v_stride, accept_len, max_rows, dev_status, stream=None):
     return _check("kv8_append", lib.kv8_append(
         ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
-        table_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(accept_len), max_rows, _ptr(dev_status), _stream(stream)))
+        table_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(accept_len), max_rows, _ptr(dev_status),
+        _stream(stream)))
 
 
 def kv8_copy_pages(c: kv8_cache, n, src, dst, dev_status, stream=None):

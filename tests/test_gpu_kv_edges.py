@@ -71,3 +71,38 @@ def test_strides_of_single_rows_and_heads_say_nothing(cuda_dev, h_q, h_kv, rows)
     c.append(0, table, lens, cu, strange[1], strange[2])
     assert int(c.status.item()) == 0 and torch.equal(c.kv, after[0]) and torch.equal(c.scale, after[1])
     assert not torch.equal(c.kv, before[0])
+
+
+def test_entry_points_by_their_own_names(cuda_dev):
+    """The binding's kv8_attend, kv8_append and kv8_copy_pages do what the handle's calls do, on any stream, and
+    raise on the status codes."""
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    cache = ku.Cache([300, 40], 8, 2, 128, 32, room=[310, 50], seed=7)
+    c, e = ku.gpu_cache(cache, cuda_dev), ku.gpu_cache(cache, cuda_dev)
+    table, lens = torch.from_numpy(cache.table).to(cuda_dev), ints(cuda_dev, 300, 40)
+    cu, acc = ints(cuda_dev, 0, 4, 7), ints(cuda_dev, 2, 0)
+    g = torch.Generator(device=cuda_dev).manual_seed(7)
+    q, k, v = (torch.randn((7, h, 128), generator=g, device=cuda_dev).to(torch.bfloat16) for h in (8, 2, 2))
+    want, want_lse = c.attend(0, table, lens, cu, q, k, v, max_len=300, max_rows=4, split_tokens=128, want_lse=True)
+    need = gs.kv8_attend_workspace_bytes(e.c, 2, 300, 4, 128)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o, lse = torch.zeros_like(q), torch.zeros((7, 8), device=cuda_dev)
+        ws = torch.empty((need,), dtype=torch.uint8, device=cuda_dev)
+        args = (e.c, 0, 2, 7, cu, lens, table, table.shape[1], table.stride(0), q, q.stride(0), k, k.stride(0), v,
+                v.stride(0), o, o.stride(0), lse, 300, 4, 128, ws)
+        gs.kv8_attend(*args, need, e.status)
+        gs.kv8_append(e.c, 0, 2, 7, cu, lens, table, table.shape[1], table.stride(0), k, k.stride(0), v, v.stride(0),
+                      acc, 4, e.status)
+        moves = ints(cuda_dev, int(cache.table[0, 9])), ints(cuda_dev, int(cache.table[0, 0]))
+        gs.kv8_copy_pages(e.c, 1, *moves, e.status, stream=side)
+    side.synchronize()
+    c.append(0, table, lens, cu, k, v, accept_len=acc, max_rows=4)
+    c.copy_pages(*moves)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert torch.equal(c.kv, e.kv) and torch.equal(c.scale, e.scale) and int(e.status.item()) == 0
+    with pytest.raises(gs.GdnError):
+        gs.kv8_attend(*args, need - 16, e.status)
+    with pytest.raises(gs.GdnError):
+        gs.kv8_copy_pages(e.c, -1, *moves, e.status)
