@@ -132,6 +132,8 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < THREADS / 32; ++i) top = max(top, red[i]);
+    } else {
+        __syncwarp();
     }
     const int e = kv8::scale_exp(__uint_as_float(top << 16));
     const float fit = kv8::pow2i(e);
@@ -157,7 +159,7 @@ __device__ __forceinline__ void append_page(const AppendArgs &a, int r, const Ro
             *p = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
-    // every thread has read *scale before the reduction above
+    // every thread has read *scale before the barrier above
     if (tid == 0) *scale = now;
 }
 
