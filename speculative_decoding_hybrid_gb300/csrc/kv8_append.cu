@@ -167,7 +167,9 @@ constexpr int cta_of(int threads) { return threads == 32 ? 32 * kPack : threads;
 // Registers for a thread's pieces (8 words each) against threads in flight: 8 pieces at
 // 512, 768 and 896 threads an SM 55, 50 and 52 us (a prompt of 8 requests, 1000..20000
 // tokens, 8 heads of 128, pages of 32), 4 pieces at 1024, 1280 and 1536 (pages of 16) 54, 54 and 60.
-constexpr int threads_an_sm(int pieces) { return pieces == 2 ? 2048 : pieces == 4 ? 1024 : 768; }
+// Two pieces at 1024, 1536 and 2048: 256 requests of 1..4 rows, 8 heads of 64, pages of 16
+// 4.6, 4.7 and 5.7 us, 8 of 1000..20000 45, 41 and 50, 512 of 1..2 in pages of 32 6.7, 7.2 and 9.0.
+constexpr int threads_an_sm(int pieces) { return pieces <= 4 ? 1024 : 768; }
 
 // RAGGED: the units count the pages touched over all requests, each finding its
 // request by a scan of the lengths; otherwise the pages one request may touch.
