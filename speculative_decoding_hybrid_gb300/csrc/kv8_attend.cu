@@ -1187,7 +1187,10 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 // in flight together.  Which of the two, and so the order of the sums, goes by the
 // pieces alone.  It is latency: 2 to 5 us behind the attention, whose end hides part
 // of its launch.  Free cuts: a CTA for each part, the parts of a unit sharing its
-// columns.  Given cuts: a CTA for each `per_cta` columns of a unit.
+// columns.  Given cuts: a CTA for each `per_cta` columns of a unit.  Few are kFew: with 4,
+// 8 and 16 one request of 2 heads of 256, 4 rows, 3000 tokens takes 14.6, 14.5 and 16.1 us,
+// 4 of 8 heads of 128, 2000..8000 tokens 22.9, 20.1 and 20.7, but one of 16 rows, 4 heads of
+// 128, 4000 tokens 25.4, 25.2 and 21.6.
 constexpr int kJoin = 512, kFew = 8;
 
 template <int D>
