@@ -598,11 +598,13 @@ typedef struct kv8_cache {
  *   2^-11 of it at most; their sum, and lse, are of the unrounded ones), and to
  *   2^-32 of the largest such product that the row sees (if the V scales of the
  *   request's pages lie within 2^48 of each other; zeros aside).
- *   q and the new keys enter with all their bits, of any finite magnitude, but
- *   for elements below 2^-14 of their row's largest in a row where no more
- *   than one in 32 of the elements (zeros aside) is below 2^-12 of it: those
- *   are rounded to 2^-22 of the largest.  Rows with more such elements are
- *   computed in fp32, some 50 times slower.
+ *   q and the new keys enter as they are, of any finite magnitude, but for
+ *   elements below 2^-14 of their row's largest, whose rounding moves a score
+ *   (sm_scale q.k, in powers of two) by 2^-14 at most for q and as much for a
+ *   new key.  Where it might be more (by the row's losses and the largest that
+ *   the other side can be) scores are summed from the elements, in fp32 and
+ *   some 50 times slower.  The sums of weights times v are fp32 too, before the
+ *   division: |v| up to 2^100.
  *   A non-finite q or k that a row sees makes the row's outputs NaN; what a
  *   row does not see, NaN and infinities included, and bytes of cache past
  *   cache_len, whatever they hold, do not reach it.

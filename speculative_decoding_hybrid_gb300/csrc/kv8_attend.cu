@@ -8,11 +8,11 @@
 // the N extent, which the few rows leave free:
 //   scores   S^T[128 positions][2 RB] = K [q_hi | q_lo]     q = (q_hi + q_lo/32) 2^-k  (bf16's 8 bits)
 //   outputs  O^T[d][4 RB] += V^T [p_0 | p_1 | p_2 | p_3]    p = sum p_j 8^-j  (fp16's 11 bits, exactly)
-// q in e4m3, exact but for elements below 2^-14 of their row's largest; the scores of a
-// row where that might show are summed by the softmax's threads instead (wide_scores).
-// A weight is rounded to fp16, whose upper byte is an e5m2 number, 3 bits
-// of it; a part is the upper byte of its predecessor's remainder times 8, so the four hold
-// all 11 bits, of subnormals too, and cost neither conversions to 8 bits nor back.
+// q in e4m3, exactly but for elements below 2^-14 of their row's largest; where what those
+// lose may show, scores are summed by the softmax's threads instead (exact_scores).
+// A weight is rounded to fp16, whose upper byte is an e5m2 number, 3 bits of it; a part is
+// the upper byte of its predecessor's remainder times 8, so the four hold all 11 bits, of
+// subnormals too, and cost neither conversions to 8 bits nor back.
 // A position is a tensor-memory lane, so its page's scales are two numbers of
 // the thread that owns the lane: K's multiplies the score, V's the weight.
 //
@@ -39,14 +39,14 @@
 // of a cut one leave (m, l, O) in the workspace for kv8_join_kernel.  With a
 // given split the cuts are at its multiples instead, whatever the ranges.
 //
-// Roundings: q and the new keys are split exactly, but for an element below 2^-14 of its
-// row's largest, which is rounded to 2^-22 of that, where at most one element in 32 is
-// so small.  A weight is rounded to fp16, 2^-11 of it at most, an eighth of what an
-// output's rounding to bf16 takes: the four 8-bit parts would hold one bit more, and four
-// e4m3 parts 14 bits, but the conversions made 16 rows x 32 requests 128 us for 121.
-// The sum of the weights is of the unrounded ones (the log-sum-exp is to be right), so a
-// row that one position makes up keeps that position's rounding.  Scores, statistics and
-// outputs are fp32, and an output is rounded once, to bf16.
+// Roundings: what the splits of q and of a new key leave out is 2^-14 of a score (in
+// powers of two) at most each, an eighth of a weight's rounding.  A weight is rounded to
+// fp16, 2^-11 of it at most, an eighth of what an output's rounding to bf16 takes: the four
+// 8-bit parts would hold one bit more, and four e4m3 parts 14 bits, but the conversions
+// made 16 rows x 32 requests 128 us for 121.  The sum of the weights is of the unrounded
+// ones (the log-sum-exp is to be right), so a row that one position makes up keeps that
+// position's rounding.  Scores, statistics and outputs are fp32, and an output is rounded
+// once, to bf16.
 //
 // What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
 // of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 135
@@ -78,6 +78,12 @@ constexpr float kUnset = -1e30f;
 // before their V scale are then at most 2^(kSlack + 2 kLift), and sums of 2^20 of them finite.
 constexpr float kLift = 48.f;
 constexpr float kLog2e = 1.4426950408889634f;
+// What a score (in powers of two) may be off by for the parts of a query or of a new key;
+// where it might be more it is summed from the elements (exact_scores).  One element of a
+// normal distribution in 8,000 loses bits, 2^-22 of its row's largest at most: with scores
+// of hundreds that is still less, and ordinary requests are never summed that way.
+constexpr float kScoreLoss = 0x1p-14f;
+constexpr float kUnit = 0x1p30f;  // what rows past 2^67 are divided by there
 constexpr int kQueue = 4;       // segments queued
 constexpr int kLeast = 2;       // tiles a part of a cut unit has at least
 
@@ -185,7 +191,8 @@ struct Cfg {
     // it out (three at d = 64 change nothing: 152 requests of 1 row 45.5 and 45.7 us)
     static constexpr int kCtas = D == 256 || RB == 64 ? 1 : 2;
     static constexpr int kFixed = 2 * kFresh + kQ + 2 * kP + (D == 64 ? kSlot : 0) + 1024;
-    static constexpr int kStatic = RB == 64 ? 4096 : D == 64 || RB == 32 ? 2560 : 2048;  // bound on sizeof(Shared)
+    static constexpr int kStatic =  // bound on sizeof(Shared)
+        RB == 64 ? 5120 : RB == 32 ? 3072 : RB == 16 || D == 64 ? 2560 : 2048;
     static constexpr int kRoom = (kCtas == 1 ? 227 * 1024 : 113 * 1024) - kStatic - kFixed;
     static constexpr int kSlots = kRoom / kSlot > 10 ? 10 : kRoom / kSlot;
     static constexpr int kSmem = kFixed + kSlots * kSlot;
@@ -223,14 +230,16 @@ struct Shared {
         long long scan[C::kThreads / 32];
     };
     float v_max[C::kGroups][4];
-    float fresh_k[16], col_down[RB];  // what a new key's and a column's parts are times; negative: a wide row's unit
+    // what a new key's and a column's parts are times (negative: always summed from the elements, over kUnit);
+    // a new key's loss; the K scale past which a column's loss shows, and the least of a group's (by segments in turn)
+    float fresh_k[16], fresh_loss[16], col_down[RB], col_limit[RB], k_limit[2][C::kGroups];
     Segment seg[kQueue];
     int bad[kQueue];
     long long start_at;
     int start_r;
     int3 start_rows;
     uint32_t tmem;
-    int fresh_wide;                     // whether any new key is wide
+    int fresh_lossy;                    // whether any new key's loss may show
     int col_out[RB];                    // element of o, from the request's first row on
     uint8_t col_row[RB], col_head[RB];  // of the request's rows, of the kv head's queries
 };
@@ -264,46 +273,59 @@ __device__ __forceinline__ int cut_at(const AttendArgs &a, long long x, int tile
     return y >= tiles ? tiles + 1 : int(y);
 }
 
-// The scores of wide columns and wide new keys, from the queries and keys in global
-// memory, into this warp's lanes of the score tile (the low parts' columns zero).  t: the
-// lane's cached position, -1 in a tile of new keys.  Rare: small for the loop's sake, and
-// slow, with all of a unit's columns wide a tile takes some 50 times as long.  (With the
-// keys' codes in registers it is 20 times, but then the ordinary tiles suffer: 16 requests
-// 75 us for 53.)
+// Of a group's columns those in whose score with this lane's key (a cached one of K scale
+// k, or new key j) more than kScoreLoss may be missing.  Every element of a key is below
+// 448 times its page's scale, or 256 times what its parts are times; of a query likewise.
 template <int D, int RB>
-__device__ __noinline__ void wide_scores(const AttendArgs &a, const Shared<D, RB> &s, const Segment &g, int t,
-                                            int pos_in, int col0, uint32_t at) {
-    const int T = a.c.page_tokens, j = pos_in & 15;
+__device__ __noinline__ uint32_t lossy_columns(const Shared<D, RB> &s, int j, float k, int col0, int cols) {
+    float loss = 0.f;
+    bool all = false;
+    if (j >= 0) {
+        k = s.fresh_k[j];
+        if (k != k) return 0;  // not finite: the parts' scores say so
+        all = k < 0.f;
+        k = fabsf(k);
+        if (s.fresh_lossy) loss = s.fresh_loss[j];
+    }
+    uint32_t mask = 0;
+#pragma unroll 1
+    for (int c = 0; c < Cfg<D, RB>::kCols && col0 + c < cols; ++c) {
+        const float f = s.col_down[col0 + c], coef = 256.f * fabsf(s.col_coef[col0 + c]);
+        if (f < 0.f || (f == f && (all || k > s.col_limit[col0 + c] || loss * coef > kScoreLoss))) mask |= 1u << c;
+    }
+    return mask;
+}
+// Such scores, summed in fp32 from the queries and keys in global memory, into this warp's
+// lanes of the score tile (the low parts' columns zero).  t: the lane's cached position, -1
+// in a tile of new keys; mask: its columns.  Rare: small for the loop's sake, and slow, with
+// all of a unit's columns a tile takes some 50 times as long.  (With the keys' codes in
+// registers it is 20 times, but then the ordinary tiles suffer: 16 requests 75 us for 53.)
+template <int D, int RB>
+__device__ __noinline__ void exact_scores(const AttendArgs &a, const Shared<D, RB> &s, const Segment &g, int t,
+                                          uint32_t mask, int pos_in, int col0, uint32_t at) {
+    const int T = a.c.page_tokens;
     const bool is_fresh = t < 0;
-    bool have = is_fresh ? pos_in < 32 && j < g.n : t >= g.lo && t < g.len;
     const uint8_t *codes = a.c.kv;
-    const uint16_t *key = a.k;
-    float down = 1.f;
-    if (is_fresh) {
-        key += (int64_t(g.t0) + j) * a.k_stride + int64_t(g.hk) * D;
-        if (have) down = s.fresh_k[j];
-        have = have && down == down;
-    } else if (have) {
+    const uint16_t *key = a.k + (int64_t(g.t0) + (pos_in & 15)) * a.k_stride + int64_t(g.hk) * D;
+    if (!is_fresh && mask) {
         const int page = a.table[int64_t(g.r) * a.table_stride + (t >> a.page_shift)];
-        have = page >= 0 && page < a.c.num_pages;
-        if (have)
-            codes += int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
-                     (int64_t(g.hk) * T + (t & (T - 1))) * D;
+        if (page < 0 || page >= a.c.num_pages) mask = 0;
+        codes += int64_t(page) * a.c.page_stride + int64_t(a.layer) * a.c.layer_stride +
+                 (int64_t(g.hk) * T + (t & (T - 1))) * D;
     }
 #pragma unroll 1
-    for (int c = 0; c < Cfg<D, RB>::kCols && col0 + c < g.cols; ++c) {
-        const float f = s.col_down[col0 + c];
-        const bool mine = have && f == f && (f < 0.f || (is_fresh && down < 0.f));
+    for (int c = 0; c < Cfg<D, RB>::kCols; ++c) {
+        const bool mine = mask >> c & 1;
         if (!__any_sync(0xffffffffu, mine)) continue;
         uint32_t hi = tc::ld1(at + c), lo = tc::ld1(at + RB + c);
         if (mine) {
             const uint16_t *q = a.q + (int64_t(g.t0) + s.col_row[col0 + c]) * a.q_stride +
                                 int64_t(g.hk * a.group + s.col_head[col0 + c]) * D;
-            const float up = 1.f / fabsf(f);
+            const float up = 1.f / fabsf(s.col_down[col0 + c]);
             if (!is_fresh)
                 hi = __float_as_uint(dot_codes<D>(codes, q, up));
             else  // the low parts of the keys lie 16 lanes on
-                hi = pos_in & 16 ? 0u : __float_as_uint(dot_rows<D>(key, 1.f / fabsf(down), q, up));
+                hi = pos_in & 16 ? 0u : __float_as_uint(dot_rows<D>(key, 1.f / fabsf(s.fresh_k[pos_in & 15]), q, up));
             lo = 0;
         }
         __syncwarp();
@@ -331,6 +353,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         constexpr int kOnes = C::kSlots * 2 + C::kScales + 4 + kQueue + 3, kWarps = C::kSoft / 32;
         for (int i = lane; i < kOnes; i += 32) gdn::mbar_init(s.ones + i, 1);
         if (lane < 6) gdn::mbar_init(s.warps + lane, kWarps);
+        if (lane < C::kGroups) s.k_limit[0][lane] = INFINITY;
         if (lane < kQueue) gdn::mbar_init(s.seg_empty + lane, kWarps + 1);
     }
     gdn::pdl_wait();
@@ -597,7 +620,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             const int nc = g.nc, n = g.n, fresh = g.fresh, nt = nc + fresh;
             if (g.cols == 0) break;
             const uint16_t *kn = a.k + int64_t(g.t0) * a.k_stride + int64_t(g.hk) * D;
-            bool maybe = false;  // some new key may be wide, and fk_ready is still to come
+            bool maybe = false;  // some new key may have a loss, and fk_ready is still to come
             if (fresh) {
                 // the new keys, while the softmax ends the segment before: their place is free
                 // once the scores of the last ones are read
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 maybe = __any_sync(0xffffffffu, maybe);
                 __syncwarp();
                 if (lane == 0 && !maybe) {
-                    s.fresh_wide = 0;
+                    s.fresh_lossy = 0;
                     arrive(&s.fk_ready);
                 }
                 last_fresh = gs + nc;
@@ -652,19 +675,25 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     __syncwarp();
                     if (maybe) {
                         // the first scores are on their way: time to look at the new keys again
-                        bool wide = false;
+                        float coef = 0.f;  // the columns' largest score factor
+                        for (int c = lane; c < g.cols; c += 32) coef = fmaxf(coef, fabsf(s.col_coef[c]));
+                        coef = 256.f * warp_max(coef);
+                        bool lossy = false;
 #pragma unroll 1
                         for (int row = lane >> 3; row - (lane >> 3) < n; row += 4) {
                             uint4 w[D / 64];
                             load_row<D>(kn + int64_t(row) * a.k_stride, lane & 7, row < n, w);
-                            const float unit = wide_row<D>(w);
-                            if ((lane & 7) == 0 && unit > 0.f) s.fresh_k[row] = -unit;
-                            wide |= unit > 0.f;
+                            const float loss = row_loss<D>(w);
+                            if ((lane & 7) == 0 && row < n) {
+                                s.fresh_loss[row] = loss;
+                                if (loss < 0.f) s.fresh_k[row] = -kUnit;
+                            }
+                            lossy |= loss < 0.f || loss * coef > kScoreLoss;
                         }
-                        wide = __any_sync(0xffffffffu, wide);
+                        lossy = __any_sync(0xffffffffu, lossy);
                         __syncwarp();
                         if (lane == 0) {
-                            s.fresh_wide = wide;
+                            s.fresh_lossy = lossy;
                             arrive(&s.fk_ready);
                         }
                         maybe = false;
@@ -726,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
         load_q();
         int gs = 0, gp = 0, ring = 0, fresh_seen = 0;  // score and weight tiles, ring positions, fresh tiles so far
         for (int k = 0; g.cols > 0; ++k) {
-            bool maybe = false, wide = false;
+            bool maybe = false;
             if (brings) {
                 const float down = split_row<D>(wq, sub, s_q, C::kNs, cq, RB + cq, maybe);
                 if (sub == 0) {
@@ -734,6 +763,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     s.col_nm[cq] = -kUnset;
                     s.col_coef[cq] = a.c.sm_scale * kLog2e * down;
                     s.col_down[cq] = down;
+                    s.col_limit[cq] = INFINITY;
                     s.col_row[cq] = uint8_t(row);
                     s.col_head[cq] = uint8_t(head);
                     s.col_out[cq] = row * int(a.o_stride) + (g.hk * a.group + head) * D;
@@ -742,17 +772,24 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
             gdn::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&s.q_ready);
-            // while the first products run: is a column of this group wide?
+            // while the first products run: does a column have a loss, and past which K scale does it show?
             if (brings && __any_sync(0xffffffffu, maybe)) {
-                const float unit = wide_row<D>(wq);
-                wide = unit > 0.f;
-                if (sub == 0 && wide) {
-                    s.col_coef[cq] = a.c.sm_scale * kLog2e * unit;
-                    s.col_down[cq] = -unit;
+                const float loss = row_loss<D>(wq), factor = fabsf(a.c.sm_scale * kLog2e);
+                if (sub == 0 && loss != 0.f) {
+                    // (not negative, so it orders like its bits)
+                    const float limit = loss < 0.f ? 0.f : kScoreLoss / (448.f * (loss * factor));
+                    s.col_limit[cq] = limit;
+                    atomicMin(reinterpret_cast<uint32_t *>(&s.k_limit[k & 1][grp]), __float_as_uint(limit));
+                    if (loss < 0.f) {
+                        s.col_down[cq] = -kUnit;
+                        s.col_coef[cq] = a.c.sm_scale * kLog2e * kUnit;
+                    }
                 }
             }
             ok = gdn::mbar_wait_bounded(&s.q_ready, k & 1, a.wait_ns);
-            wide = group_or(grp, wide);
+            group_sync(grp);
+            float k_limit = s.k_limit[k & 1][grp];
+            if (pos_in == 0) s.k_limit[(k + 1) & 1][grp] = INFINITY;
 
             const int nc = g.nc, nt = nc + g.fresh;
             // a row sees positions from lo0 + row * lo1 on (g.lo is row 0's, and not negative)
@@ -773,19 +810,21 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 return i >= nc ? gdn::mbar_wait_bounded(&s.fk_ready, fresh_seen & 1, a.wait_ns)
                                : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
             };
-            // Tile by tile; where a column or a new key is wide the loop is left before the tile, its scores
-            // are put right and it goes on.  (In the loop that code, taken or not, called or not, made 16 rows
-            // x 32 requests 133 to 136 us, in a second form of the loop 128 to 131; beside it 121.5.)
-            for (int i = 0, stop = wide ? 0 : nt, fixed = -1;;) {
+            // Tile by tile.  From the first tile on where a loss might show, which a vote finds, the loop is left
+            // before each, its scores are put right and it goes on.  (In the loop that code, taken or not, called or
+            // not, made 16 rows x 32 requests 133 to 136 us, in a second form of the loop 128 to 131, so 121.5 to 123.)
+            for (int i = 0, stop = nt, fixed = -1;;) {
                 for (; i < stop; ++i) {
                     const bool is_fresh = i >= nc;
                     const int x = gs + i, y = gp + i, t = (g.tile0 + i) * kTile + pos_in;
                     if (ok) ok = tile_known(i);
-                    if (is_fresh && fixed != i && __any_sync(0xffffffffu, ok && s.fresh_wide)) break;
+                    if (is_fresh && fixed != i && __any_sync(0xffffffffu, ok && s.fresh_lossy)) break;
                     const float2 sc =
                         is_fresh
                             ? make_float2(fabsf(pos_in < 32 && (pos_in & 15) < g.n ? s.fresh_k[pos_in & 15] : 0.f), 0.f)
                             : s.scales[y % C::kScales][pos_in >> shift];
+                    // (the elements of a new key are below 256 times its factor, of a cached one 448 times its scale)
+                    const bool look = sc.x > k_limit;
                     // whole: every row sees every position of the tile
                     const int tile = g.tile0 + i;
                     const bool whole = !is_fresh && (tile + 1) * kTile <= g.len && tile * kTile >= lo_last;
@@ -856,13 +895,16 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
 #pragma unroll
                         for (int c = 4; c < N; ++c) top[c & 3] = fmaxf(top[c & 3], z[c]);
                         const float over = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        move = group_or(grp, over > kSlack || sc.y > vref || !ok);
+                        move = group_or(grp, over > kSlack || sc.y > vref || look || !ok);
                     }
                     if (__builtin_expect(move, 0)) {
-                        // ---- the reference moves (or a wait ran out)
-                        if (group_or(grp, !ok)) {
-                            ok = false;
-                            i = nt;
+                        // ---- the reference moves (or the scores are to be put right, or a wait ran out)
+                        if (group_or(grp, look || !ok)) {
+                            k_limit = INFINITY;  // the tiles from here on are looked at one by one
+                            if (group_or(grp, !ok)) {
+                                ok = false;
+                                i = nt;
+                            }
                             break;
                         }
                         const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(sc.y));
@@ -1008,10 +1050,16 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                 if (ok) ok = gdn::mbar_wait_bounded(&s.s_full[x & 1], (x >> 1) & 1, a.wait_ns);
                 __syncwarp();
                 tc::fence_after();
-                wide_scores<D, RB>(a, s, s.seg[k % kQueue], i >= nc ? -1 : (g.tile0 + i) * kTile + pos_in, pos_in,
-                                   col0, tm + lane_base + (x & 1) * C::kNs + col0);
+                const int t = i >= nc ? -1 : (g.tile0 + i) * kTile + pos_in;
+                uint32_t mask = 0;
+                if (t >= 0 ? t >= g.lo && t < g.len : pos_in < 32 && (pos_in & 15) < g.n)
+                    mask = lossy_columns<D, RB>(s, t >= 0 ? -1 : pos_in & 15,
+                                                s.scales[(gp + i) % C::kScales][pos_in >> shift].x, col0, g.cols);
+                if (__any_sync(0xffffffffu, mask))
+                    exact_scores<D, RB>(a, s, s.seg[k % kQueue], t, mask, pos_in, col0,
+                                        tm + lane_base + (x & 1) * C::kNs + col0);
                 fixed = i;
-                stop = wide ? i + 1 : nt;
+                stop = i + 1;
             }
             // ---- the segment's end
             if (ok && nc > 0) {

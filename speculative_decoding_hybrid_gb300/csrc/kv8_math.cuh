@@ -124,8 +124,9 @@ __device__ __forceinline__ uint32_t row_top(const uint4 (&w)[D / 64]) {
     return max(m >> 16, m & 0xffffu);
 }
 // The power of two that brings such a magnitude to 2^7 .. 2^8; rows are scaled by at
-// most 2^kMaxUp (32 times that is still finite), and by 2^-120 at least.
-constexpr int kMaxUp = 110;
+// most 2^kMaxUp (32 times that, and 2^14 times, are still finite), and by 2^-120 at least;
+// past 2^kMinFit scores are not left to the parts.
+constexpr int kMaxUp = 110, kMinFit = -60;
 __device__ __forceinline__ int fit_of(uint32_t top) { return 7 - (int(top >> 7) - 127); }
 
 // A warp splits four rows of bf16, eight threads (sub) a row: x = (hi + lo/32) 2^-k
@@ -134,7 +135,7 @@ __device__ __forceinline__ int fit_of(uint32_t top) { return 7 - (int(top >> 7) 
 // The low part ends at 2^-14: an element from 2^-7 on, 2^-14 of the largest at most,
 // keeps all its 8 bits; a smaller one is off by up to 2^-15, 2^-22 of the largest.
 // `maybe`: this thread has an element that small, zeros among them, or the row is past
-// 2^103 or below 2^-103: wide_row has to say whether that will do.
+// 2^67: row_loss has to say what that means.
 template <int D>
 __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, uint8_t *tile, int rows, int rh, int rl,
                                            bool &maybe) {
@@ -161,7 +162,7 @@ __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, ui
         l[2 * e + 1] = join16(ll[2], ll[3]);
         large &= ((h[2 * e] & 0x7f7f7f7fu) + 0x7b7b7b7bu) & ((h[2 * e + 1] & 0x7f7f7f7fu) + 0x7b7b7b7bu);
     }
-    maybe = top > 0 && top < 0x7f80u && ((~large & 0x80808080u) || fit < -96 || fit > kMaxUp);
+    maybe = top > 0 && top < 0x7f80u && ((~large & 0x80808080u) || fit < kMinFit);
     if constexpr (E == 8) {
         uint8_t *t = tile + ((sub * 8) & 8);
         *reinterpret_cast<uint2 *>(t + tc::swz8_off<kRow>(rh, sub >> 1)) = make_uint2(h[0], h[1]);
@@ -180,35 +181,32 @@ __device__ __forceinline__ float split_row(const uint4 (&w)[D / 64], int sub, ui
     return top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2i(-k);
 }
 
-// Whether a row's parts will do, and if not (a wide row) a power of two that its elements
-// are to be divided by, so that their products with the other side's stay inside fp32;
-// 0 if they do.  What a small element loses is nothing beside the larger ones, but the
-// other side may be zero wherever those are.  So a row is wide that has such an element
-// and more than one in 32 below 2^-5 (of 2^7 for the largest), zeros aside, or whose
-// factors would leave fp32.  A normal distribution has one in 2,000 below 2^-5: an
-// ordinary row never is wide.
+// What a row's parts leave of it: the sum of its elements' losses, which times the other
+// side's largest magnitude bounds what a product loses; -1 for a row past 2^67, whose
+// factors might leave fp32 whatever its parts hold.
 template <int D>
-__device__ __forceinline__ float wide_row(const uint4 (&w)[D / 64]) {
+__device__ __forceinline__ float row_loss(const uint4 (&w)[D / 64]) {
     const uint32_t top = row_top<D>(w);
     const int fit = fit_of(top), k = min(kMaxUp, fit);
-    // |x| < 2^(-5 - k) by halves, the top bits set so that nothing is borrowed
-    const uint32_t lim = (uint32_t(122 - k) << 7) - 1u, lim2 = lim | (lim << 16) | 0x80008000u;
-    uint32_t n = 0, small = 0;  // 128 for each that is not zero, and for those below
+    // in units of 2^-14, the low part's last bit; an element from 2^-7 on is a whole number of them, and all
+    // are below 2^22, where adding 1.5 * 2^23 rounds
+    const f2 unit = pair(pow2i(k + 14), pow2i(k + 14)), whole = pair(12582912.f, 12582912.f),
+             back = pair(-12582912.f, -12582912.f), minus = pair(-1.f, -1.f);
+    float loss = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) {
         const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t m = u[i] & 0x7fff7fffu, some = (m + 0x7fff7fffu) & 0x80008000u;
-            n = __dp4a(some, 0x01010101u, n);
-            small = __dp4a((lim2 - m) & some, 0x01010101u, small);
+            const f2 y = mul2(pair(u[i] << 16, u[i] & 0xffff0000u), unit);
+            const float2 d = both(fma2(add2(add2(y, whole), back), minus, y));
+            loss += fabsf(d.x) + fabsf(d.y);
         }
     }
-    n = n << 9 | small >> 7;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    const bool wide = top > 0 && top < 0x7f80u && ((n & 0xffffu) * 32 > n >> 16 || fit < -96 || fit > kMaxUp);
-    return !wide ? 0.f : k < -60 ? 0x1p30f : k > 60 ? 0x1p-30f : 1.f;
+    for (int o = 1; o < 8; o <<= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    if (top == 0 || top >= 0x7f80u) return 0.f;
+    return fit < kMinFit ? -1.f : loss * pow2i(-k) * 0x1p-14f;
 }
 
 // Sums of products in fp32: of a key as the cache holds it and a query times up, of a

@@ -2,6 +2,8 @@
 and new keys with large channels that the other side is zero in, rows near the
 ends of bf16's range, pages with far larger V scales and next to no weight, and
 weights whose rounding shows most; against the fp64 form."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -24,10 +26,10 @@ def rows_of(cache, n, seed):
     return tuple(g.standard_normal((R, h, cache.d)) for h in (cache.h_q, cache.h_kv, cache.h_kv))
 
 
-def check(name, cache, n, q, k, v, dev, window=0, sm_scale=None, split=0):
+def check(name, cache, n, q, k, v, dev, window=0, sm_scale=None, split=0, loss=0.0):
     """One call against the fp64 form.  The error budget is kv_util's, with a weight's rounding as the header
     states it: to fp16's 11 bits, 2^-11 of it at most, and to 2^-32 of the largest weight times V scale that the
-    row sees (each position's, times its code)."""
+    row sees (each position's, times its code).  loss: what scores may be off by besides, in powers of two."""
     (qt, q), (kt, k), (vt, v) = ku.bf16(q), ku.bf16(k), ku.bf16(v)
     c = ku.gpu_cache(cache, dev, window, sm_scale)
     cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
@@ -44,7 +46,8 @@ def check(name, cache, n, q, k, v, dev, window=0, sm_scale=None, split=0):
             continue
         ro, rl, ra, rw = ku.attend_request(cache.dense(r, 0), q[a:b], k[a:b], v[a:b], window, sc)
         ob, lb = ku.attend_bounds(ro, rl, ra, rw, cache.d)
-        ob = ob + 2.0 ** -12 * ra + floor(cache, r, q[a:b], k[a:b], window, sc)
+        ob = ob + (2.0 ** -12 + 2 * math.log(2) * loss) * ra + floor(cache, r, q[a:b], k[a:b], window, sc)
+        lb = lb + math.log(2) * loss
         assert np.isfinite(o[a:b]).all() and np.isfinite(lse[a:b]).all()
         worst[0] = max(worst[0], noted("kv range %s: o" % name, np.max(np.abs(o[a:b] - ro) / ob)))
         worst[1] = max(worst[1], noted("kv range %s: lse" % name, np.max(np.abs(lse[a:b] - rl) / lb)))
@@ -260,3 +263,34 @@ def test_a_late_position_that_takes_all(cuda_dev):
     q[..., 1] = 0
     cache.scale[:] = 1.0
     check("a late position takes all", cache, [16], q, k, v, cuda_dev, sm_scale=1.0)
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_any_shape_and_range(cuda_dev, seed):
+    """Drawn sizes, masks and cuts with drawn channels, all but a few of them or one, 2^5 to 2^60 above the others
+    on one side and zero on the other, and V scales 2^40 apart.  Scores may be off by the 2^-14 that the header
+    gives each of the two sides, and sum to nearly nothing."""
+    g = np.random.RandomState(1000 + seed)
+    pick = lambda *x: x[g.randint(len(x))]
+    d, h, group, page = pick(64, 128, 256), pick(1, 2, 4), pick(1, 2, 3, 4, 8, 16), pick(16, 32, 64, 128)
+    B, most = pick(1, 2, 3, 8, 40), pick(1, 2, 3, 4, 7, 16)
+    hi = pick(3, 50, 130, 400, 1500) if B <= 8 else pick(3, 50, 200)
+    lens, rows = [int(x) for x in g.randint(0, hi + 1, B)], [int(x) for x in g.randint(0, most + 1, B)]
+    rows[0] = most
+    cache = ku.Cache(lens, h * group, h, d, page, seed=seed, fill=pick("normal", "garbage"))
+    q, k, v = rows_of(cache, rows, seed)
+    if seed % 4 != 3:
+        big = g.permutation(d)[:pick(1, d // 2, d - 4, d - 1)]
+        keys = cache.kv[:, :, 0]
+        keys[..., big] = np.where((keys[..., big] & 127) == 127, keys[..., big], 0)
+        k[..., big] = 0
+        q[..., big] *= np.where(g.rand(*q.shape[:2]) < 0.7, 2.0 ** float(g.randint(5, 60)), 1.0)[..., None]
+    if seed % 4 >= 2:
+        c = int(g.randint(d))
+        q[..., c] = 0
+        k[..., c] *= np.where(g.rand(*k.shape[:2]) < 0.5, 2.0 ** float(g.randint(5, 60)), 1.0)
+    if seed % 2:
+        some = np.isfinite(cache.scale[..., 1])
+        cache.scale[..., 1] *= np.where(some, 2.0 ** g.randint(-20, 21, some.shape), 1.0)
+    check("any shape and range", cache, rows, q, k, v, cuda_dev, window=pick(0, 0, 5, 60, 129, 300),
+          split=pick(0, 0, 128, 512), loss=2.0 ** -13)
