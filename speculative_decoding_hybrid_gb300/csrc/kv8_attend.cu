@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                     __syncwarp();
                     if (maybe) {
                         // the first scores are on their way: time to look at the new keys again
-                        float coef = 0.f;  // the columns' largest score factor
+                        float coef = 0.f;  // the columns' largest score factor (a kUnit one counts for itself)
                         for (int c = lane; c < g.cols; c += 32) coef = fmaxf(coef, fabsf(s.col_coef[c]));
                         coef = 256.f * warp_max(coef);
                         bool lossy = false;
@@ -811,8 +811,9 @@ __global__ void __launch_bounds__(Cfg<D, RB>::kThreads, Cfg<D, RB>::kCtas)
                                : gdn::mbar_wait_bounded(&s.sc_full[y % C::kScales], (y / C::kScales) & 1, a.wait_ns);
             };
             // Tile by tile.  From the first tile on where a loss might show, which a vote finds, the loop is left
-            // before each, its scores are put right and it goes on.  (In the loop that code, taken or not, called or
-            // not, made 16 rows x 32 requests 133 to 136 us, in a second form of the loop 128 to 131, so 121.5 to 123.)
+            // before each, its scores are put right and it goes on.  (In the loop that code, taken or not, called
+            // or not, made 16 rows x 32 requests 133 to 136 us, in a second form of the loop 128 to 131, beside it
+            // 121.5 to 123.)
             for (int i = 0, stop = nt, fixed = -1;;) {
                 for (; i < stop; ++i) {
                     const bool is_fresh = i >= nc;

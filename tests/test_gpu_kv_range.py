@@ -294,3 +294,36 @@ def test_any_shape_and_range(cuda_dev, seed):
         cache.scale[..., 1] *= np.where(some, 2.0 ** g.randint(-20, 21, some.shape), 1.0)
     check("any shape and range", cache, rows, q, k, v, cuda_dev, window=pick(0, 0, 5, 60, 129, 300),
           split=pick(0, 0, 128, 512), loss=2.0 ** -13)
+
+
+@pytest.mark.parametrize("d,h_kv,group", [(64, 2, 8), (128, 1, 8), (256, 2, 4)])
+def test_bits_of_such_rows_do_not_go_by_their_neighbours(cuda_dev, d, h_kv, group):
+    """With given cuts a request's bits are its own, whether a row beside it, in its block or not, is summed from
+    its elements, and however wide the blocks are."""
+    h_q, lens, n = h_kv * group, [900, 300, 40], [4, 2, 3]
+    cache = ku.Cache(lens, h_q, h_kv, d, 32, seed=d)
+    cache.kv[:, :, 0, :, :, 5] = 0
+    q, k, v = rows_of(cache, n, d)
+    k[..., 5] = 0
+    q[1, 1, 5], q[4, 0, 5], q[6, h_q - 1, 5] = 2.0 ** 20, 2.0 ** 30, 2.0 ** 90
+    qt, kt, vt = (ku.bf16(x)[0].to(cuda_dev) for x in (q, k, v))
+    c = ku.gpu_cache(cache, cuda_dev)
+    table = torch.from_numpy(cache.table).to(cuda_dev)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)
+    run = lambda r, a, b, most: c.attend(0, table[r], ints(*[lens[i] for i in range(3)][r]),
+                                         ints(*np.concatenate([[0], np.cumsum(n[r])]).tolist()), qt[a:b], kt[a:b],
+                                         vt[a:b], max_len=900, max_rows=most, split_tokens=256, want_lse=True)
+    o, lse = run(slice(0, 3), 0, 9, 4)
+    for most in (8, 16):
+        o1, l1 = run(slice(0, 3), 0, 9, most)
+        assert torch.equal(o1, o) and torch.equal(l1, lse)
+    for r, (a, b) in enumerate(((0, 4), (4, 6), (6, 9))):
+        o1, l1 = run(slice(r, r + 1), a, b, n[r])
+        assert torch.equal(o1, o[a:b]) and torch.equal(l1, lse[a:b])
+    # the other rows' bits are those they have without such a row
+    q[1, 1, 5] = q[4, 0, 5] = q[6, h_q - 1, 5] = 0
+    qt = ku.bf16(q)[0].to(cuda_dev)
+    o1, l1 = run(slice(0, 3), 0, 9, 4)
+    same = torch.ones((9, h_q), dtype=torch.bool, device=cuda_dev)
+    same[1, 1] = same[4, 0] = same[6, h_q - 1] = False
+    assert torch.equal(o1[same], o[same]) and torch.equal(l1[same], lse[same])
