@@ -49,14 +49,14 @@
 // once, to bf16.
 //
 // What bounds it (bytes over time, and of the 6.78 TB/s of a copy): HBM and the ends
-// of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 135
-// us, 5.8 TB/s, 86 %) and long requests (256k tokens: 269 MB in 53 us, 5.0 TB/s, 74
+// of segments in large batches (4 rows x 256 requests, 2 heads of 256: 786 MB in 137
+// us, 5.7 TB/s, 84 %) and long requests (256k tokens: 269 MB in 53.5 us, 5.0 TB/s, 74
 // %, of which about 5 us are the join and 4 the start; 16 requests of a mixed batch
-// 258 MB in 53 us, 72 %); the softmax's instructions from 64 columns on (16 rows x 32
-// requests, 4 heads of 128: 119 us, five times what HBM would need); the chain from
-// a segment's queries to its outputs, about 4 us, where requests are short, and
-// then also the fetching of its instructions: loops there are rolled wherever that
-// costs nothing.
+// 258 MB in 54.5 us, 70 %); from 64 columns on the softmax's chains, about 500
+// instructions a warp and tile at 60 % of the issue slots (16 rows x 32 requests, 4
+// heads of 128: 123 us, five times what HBM would need); the chain from a segment's
+// queries to its outputs, about 4 us, where requests are short, and then also the
+// fetching of its instructions: loops there are rolled wherever that costs nothing.
 #include <cuda.h>
 
 #include <atomic>
