@@ -309,9 +309,9 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
     // n rows starting anywhere touch at most (T - 1 + n - 1) / T + 1 pages, and all
     // requests together at most row_capacity / T + 2 B.  Counting those saves units
     // without a page (8 requests of 512..32768 tokens 114 us without, 88 with; of
-    // 1000..20000 into pages of 16, heads of 64, 46 and 37) and costs each unit a scan,
-    // of 32 requests at a time (95 requests of 1..98 tokens 9.4 us without, 11.2 with; 256
-    // of 4 rows 3.6 and 7.6).
+    // 1000..20000 into pages of 16, heads of 64, 60 and 45) and costs each unit a scan,
+    // of 32 requests at a time (95 requests of 1..98 tokens 7.2 us without, 8.5 with; 256
+    // of 4 rows 3.0 and 6.8).
     const int64_t each = (max_rows + T - 2) / T + 1, all = row_capacity / T + int64_t(2) * B;
     const bool ragged = all * (2 + B / 16) < each * B * 2;
     const int64_t pages = ragged ? all : each, units = pages * 2 * cache->h_kv;
@@ -324,10 +324,11 @@ extern "C" int kv8_append(const kv8_cache *cache, int32_t layer, int32_t B, int3
                                     dim3(unsigned(cta_of(threads))), 0, static_cast<cudaStream_t>(stream), a);
     };
     // As few threads a page as hold its new pieces, eight each: units of one warp reduce
-    // without a barrier (2 rows x 512 requests 17.3 us with 64 threads a page, 9.2 with
-    // 32; the prompt below into pages of 16 tokens 97 and 54), and eight pieces keep more
-    // of a prompt in flight than four by twice the threads (60 and 50 us in pages of 32,
-    // 56 and 50 in pages of 128).  Two pieces, or four, where no page has more.
+    // without a barrier (2 rows x 512 requests 17.2 us with 64 threads a page, 6.8 with
+    // 32; the prompts above into pages of 16 tokens 86 and 45), and eight pieces keep more
+    // of a prompt in flight than four by twice the threads (8 requests of 1000..20000, 8
+    // heads of 128: 66.4 and 64.3 us in pages of 128, but 64.1 and 66.8 in pages of 32).
+    // Two pieces, or four, where no page has more.
     const int all_pieces = most * cache->d / 16;
     if (ragged) {
         if (all_pieces <= 64) return launch(kv8_append_kernel<32, 2, true>, 32);
