@@ -695,6 +695,103 @@ int kv8_pages_free(gdn_pool *pool, int32_t *table, int32_t *n_pages);
 int kv8_pages_compact(gdn_pool *pool, int32_t n_tables, int32_t *tables, int32_t table_stride,
                       const int32_t *n_pages, int32_t *move_src, int32_t *move_dst, int32_t *n_moves);
 
+/* ------------------------------------------------------------------------
+ * The attention layers' prompt side: what a prefill transaction does for the
+ * softmax-attention layers beside gdn_chunked_prefill ([ENGINE] Correctness
+ * fix: long prefills in the packed batch; H200 RC4 evidence: paged Engine).
+ * Per layer: rope_rows turns the queries and new keys to their positions,
+ * attn_prompts (whole prompts) or kv8_chunk (new rows behind a cache) computes
+ * the rows' outputs, kv8_append commits the new keys and values.
+ * Packed rows: request r owns rows cu_rows[r] .. cu_rows[r+1]-1, any number
+ * of them (0: no work).  Rows that belong to no request are not written.
+ * ------------------------------------------------------------------------ */
+typedef struct rope_spec {
+    int32_t h_q, h_kv, d;         /* heads of q and of k (either may be 0), channels a head: a multiple of 8 up to 512 */
+    int32_t rot;                  /* the first rot channels turn (even); the others pass unchanged */
+    int32_t interleaved;          /* 0: pairs (j, j + rot/2); 1: pairs (2j, 2j + 1) */
+    float magnitude;              /* on cosine and sine (1 without a long-context correction) */
+} rope_spec;
+
+/*
+ * rope_rows -- rotary positions.  Row i of request r is at position p =
+ *   cache_len[r] + i (cache_len NULL: i).  With theta = 2 pi p turns[j] / 2^64,
+ *   pair j of every head becomes
+ *     (a, b) -> magnitude * (a cos theta - b sin theta, a sin theta + b cos theta)
+ *   in fp32, rounded once to bf16.  turns: device uint64 [rot/2], frequency j
+ *   over 2 pi as a 64-bit fraction: the angle is right to 2^-33 of a turn at
+ *   every position (frequencies are the caller's: any base, any scaling).
+ *   q [row][h_q][d], k [row][h_kv][d], rows *_stride elements apart (multiples
+ *   of 8), bases 16-byte aligned.  q_out == q (k_out == k) with equal strides
+ *   turns in place; otherwise an output overlaps no input.  A head count of 0
+ *   leaves its pointers unused.
+ *   Requests with bad rows, or positions past 2^31 - 1, set GDN_DEV_ROWS_BAD
+ *   and are skipped.  B <= 65535; h_q + h_kv <= 65535.
+ */
+int rope_rows(const rope_spec *spec, int32_t B, int32_t row_capacity, const int32_t *cu_rows,
+              const int32_t *cache_len, const uint64_t *turns,
+              const gdn_bf16 *q, int64_t q_stride, gdn_bf16 *q_out, int64_t q_out_stride,
+              const gdn_bf16 *k, int64_t k_stride, gdn_bf16 *k_out, int64_t k_out_stride,
+              uint32_t *dev_status, void *stream);
+
+typedef struct attn_dims {
+    int32_t h_q, h_kv, d;         /* d in {64, 128, 256}; h_q a multiple of h_kv, h_q/h_kv <= 64 */
+    int32_t window;               /* a row at position p sees positions > p - window; 0 = all */
+    float sm_scale;               /* multiplies q.k */
+} attn_dims;
+
+/*
+ * attn_prompts -- causal attention of whole prompts.  Row i of a request sees
+ *   the request's rows j <= i inside the window:
+ *     o[row][h]   = sum_j softmax_j(sm_scale q.k_j) v_j          (bf16)
+ *     lse[row][h] = log sum_j exp(sm_scale q.k_j)                (fp32, may be NULL)
+ *   Query head h reads kv head h / (h_q/h_kv).  q [row][h_q][d], k and v
+ *   [row][h_kv][d], o [row][h_q][d]: rows *_stride elements apart (multiples of
+ *   8), bases 16-byte aligned; lse rows are h_q apart.  Neither o nor lse may
+ *   overlap an input.  Requests have at most max_rows rows.
+ *   Scores, sums and softmax statistics are fp32; a weight enters the product
+ *   with v rounded to bf16 (by 2^-8 of it at most; lse is of the unrounded
+ *   ones).  |v| up to 2^100.  A score that is NaN or +inf makes its row's
+ *   outputs NaN; one of -inf has no weight, and a row with no other gets o = 0
+ *   and lse = -inf.  A v that is not finite makes the outputs of its channel
+ *   infinite or NaN in the rows that see it.  What a row does not see does not
+ *   reach it, whatever it holds.
+ *   Bad rows set GDN_DEV_ROWS_BAD: the request is skipped (its o and lse are
+ *   not written).  A bounded wait that runs out sets GDN_DEV_TIMEOUT: outputs
+ *   of that call are not to be trusted.  B <= 65535.  workspace:
+ *   attn_prompts_workspace_bytes(...) device bytes (16-byte aligned, no
+ *   initialisation, one call at a time), 0 when no work is cut.
+ */
+size_t attn_prompts_workspace_bytes(const attn_dims *dims, int32_t B, int32_t row_capacity, int32_t max_rows);
+int attn_prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const int32_t *cu_rows,
+                 const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, int64_t k_stride,
+                 const gdn_bf16 *v, int64_t v_stride, gdn_bf16 *o, int64_t o_stride, float *lse,
+                 int32_t max_rows, void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/*
+ * kv8_chunk -- kv8_attend for any number of rows: one layer's attention of
+ *   each request's new rows over its cache_len[r] committed positions (0 ..
+ *   max_len, as stored) and the new rows j <= i (as given), inside the window.
+ *   Arguments as of kv8_attend, numerics as of attn_prompts; k_new and v_new
+ *   are wanted, max_rows has no limit of its own, and total_len is a host bound
+ *   on the sum of cache_len (it sizes the workspace: kv8_chunk_workspace_bytes
+ *   device bytes, 4 h_kv d of them for each committed position and row; 0 for
+ *   arguments that kv8_chunk refuses).  Bytes of cache past cache_len do not
+ *   reach an output, whatever they hold.  Requests past max_len, max_rows,
+ *   row_capacity or, with those before them, total_len set GDN_DEV_ROWS_BAD,
+ *   page ids out of range (of pages some row sees) GDN_DEV_PAGE_OOR; either
+ *   skips the request.  total_len + row_capacity < 2^30.
+ */
+size_t kv8_chunk_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t row_capacity, int32_t max_len,
+                                 int32_t max_rows, int64_t total_len);
+int kv8_chunk(const kv8_cache *cache, int32_t layer, int32_t B, int32_t row_capacity,
+              const int32_t *cu_rows, const int32_t *cache_len,
+              const int32_t *table, int32_t table_pages, int64_t table_stride,
+              const gdn_bf16 *q, int64_t q_stride,
+              const gdn_bf16 *k_new, int64_t k_stride, const gdn_bf16 *v_new, int64_t v_stride,
+              gdn_bf16 *o, int64_t o_stride, float *lse,
+              int32_t max_len, int32_t max_rows, int64_t total_len,
+              void *workspace, size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
 const char *gdn_status_string(int status);
 
 /* Failure-detection self-test of the chunked prefill: gdn_chunked_prefill
@@ -724,6 +821,16 @@ int kv8_selftest_attend_timeout(const kv8_cache *cache, int32_t layer, int32_t B
                                 int32_t max_len, int32_t max_rows, int32_t split_tokens,
                                 void *workspace, size_t workspace_bytes,
                                 uint32_t *dev_status, uint64_t limit_ns, void *stream);
+
+/* Failure-detection self-test of attn_prompts (no lse) with every wait bounded
+ * by limit_ns (1 .. 1e9): the copy of a unit's last values is withheld, so the
+ * waits for it run out: GDN_DEV_TIMEOUT is set and no output is written.
+ * (Test-only.) */
+int attn_selftest_prompts_timeout(const attn_dims *dims, int32_t B, int32_t row_capacity, const int32_t *cu_rows,
+                                  const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, int64_t k_stride,
+                                  const gdn_bf16 *v, int64_t v_stride, gdn_bf16 *o, int64_t o_stride,
+                                  int32_t max_rows, void *workspace, size_t workspace_bytes,
+                                  uint32_t *dev_status, uint64_t limit_ns, void *stream);
 
 /* Failure-detection self-test: a kernel waits on an mbarrier that is never
  * completed, gives up after limit_ns (1 .. 1e9) of device time and sets

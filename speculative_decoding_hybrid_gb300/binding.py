@@ -38,7 +38,8 @@ EXPORTS = ["gdn_decode_step", "gdn_verify", "mtp_accept_workspace_bytes", "mtp_g
            "gdn_decode_transaction", "gdn_decode_transaction_at", "gdn_status_string",
            "gdn_selftest_prefill_timeout", "kv8_attend_workspace_bytes", "kv8_attend", "kv8_append",
            "kv8_selftest_attend_timeout", "kv8_copy_pages", "kv8_pages_reserve", "kv8_pages_fork", "kv8_pages_free",
-           "kv8_pages_compact"]
+           "kv8_pages_compact", "rope_rows", "attn_prompts_workspace_bytes", "attn_prompts",
+           "attn_selftest_prompts_timeout", "kv8_chunk_workspace_bytes", "kv8_chunk"]
 
 
 class GdnError(RuntimeError):
@@ -116,6 +117,15 @@ class kv8_cache(ctypes.Structure):
                  ("scale_page_stride", ctypes.c_int64), ("scale_layer_stride", ctypes.c_int64)])
 
 
+class rope_spec(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("h_q", "h_kv", "d", "rot", "interleaved")] +
+                [("magnitude", ctypes.c_float)])
+
+
+class attn_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("h_q", "h_kv", "d", "window")] + [("sm_scale", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libgdnspec.so is not built (expected at %s); run "
@@ -124,6 +134,7 @@ def _load():
     P, I32, I64, U32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
     DP = ctypes.POINTER(gdn_dims)
     CP, PP = ctypes.POINTER(kv8_cache), ctypes.POINTER(gdn_pool)
+    RP, AP = ctypes.POINTER(rope_spec), ctypes.POINTER(attn_dims)
     sig = {
         "gdn_decode_step": [DP, I32, P, P, P, P, P, P, I64, I32, P, P, P, P, P],
         "gdn_verify": [DP, I32, I32, P, P, P, P, P, P, P, I64, I32, P, P, P, U32, P, P, P],
@@ -160,6 +171,14 @@ def _load():
         "kv8_pages_fork": [PP, P, I32, I32, I32, P, I32, P, P, P, P],
         "kv8_pages_free": [PP, P, P],
         "kv8_pages_compact": [PP, I32, P, I32, P, P, P, P],
+        "rope_rows": [RP, I32, I32, P, P, P, P, I64, P, I64, P, I64, P, I64, P, P],
+        "attn_prompts_workspace_bytes": [AP, I32, I32, I32],
+        "attn_prompts": [AP, I32, I32, P, P, I64, P, I64, P, I64, P, I64, P, I32, P, SZ, P, P],
+        "attn_selftest_prompts_timeout": [AP, I32, I32, P, P, I64, P, I64, P, I64, P, I64, I32, P, SZ, P,
+                                          ctypes.c_uint64, P],
+        "kv8_chunk_workspace_bytes": [CP, I32, I32, I32, I32, I64],
+        "kv8_chunk": [CP, I32, I32, I32, P, P, P, I32, I64, P, I64, P, I64, P, I64, P, I64, P, I32, I32, I64, P, SZ, P,
+                      P],
         "gdn_selftest_wait_timeout": [P, ctypes.c_uint64, P],
         "gdn_selftest_prefill_timeout": [DP, I32, I32, P, P, P, P, P, P, P, I64, I32, P, P, P, P, SZ, P,
                                          ctypes.c_uint64, P],
@@ -178,6 +197,8 @@ def _load():
     L.mtp_accept_workspace_bytes.restype = SZ
     L.gdn_prefill_workspace_bytes.restype = SZ
     L.kv8_attend_workspace_bytes.restype = SZ
+    L.attn_prompts_workspace_bytes.restype = SZ
+    L.kv8_chunk_workspace_bytes.restype = SZ
     L.gdn_status_string.restype = ctypes.c_char_p
     return L
 
@@ -408,6 +429,46 @@ def kv8_append(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, 
 def kv8_copy_pages(c: kv8_cache, n, src, dst, dev_status, stream=None):
     return _check("kv8_copy_pages", lib.kv8_copy_pages(ctypes.byref(c), n, _ptr(src), _ptr(dst), _ptr(dev_status),
                                                        _stream(stream)))
+
+
+def rope_rows(spec: rope_spec, B, row_capacity, cu_rows, cache_len, turns, q, q_stride, q_out, q_out_stride, k,
+              k_stride, k_out, k_out_stride, dev_status, stream=None):
+    return _check("rope_rows", lib.rope_rows(
+        ctypes.byref(spec), B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(turns), _ptr(q), q_stride,
+        _ptr(q_out), q_out_stride, _ptr(k), k_stride, _ptr(k_out), k_out_stride, _ptr(dev_status), _stream(stream)))
+
+
+def attn_prompts_workspace_bytes(dims: attn_dims, B, row_capacity, max_rows) -> int:
+    return int(lib.attn_prompts_workspace_bytes(ctypes.byref(dims), B, row_capacity, max_rows))
+
+
+def attn_prompts(dims: attn_dims, B, row_capacity, cu_rows, q, q_stride, k, k_stride, v, v_stride, o, o_stride, lse,
+                 max_rows, workspace, workspace_bytes, dev_status, stream=None):
+    return _check("attn_prompts", lib.attn_prompts(
+        ctypes.byref(dims), B, row_capacity, _ptr(cu_rows), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+        _ptr(o), o_stride, _ptr(lse), max_rows, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
+
+
+def attn_selftest_prompts_timeout(dims: attn_dims, B, row_capacity, cu_rows, q, q_stride, k, k_stride, v, v_stride, o,
+                                  o_stride, max_rows, workspace, workspace_bytes, dev_status, limit_ns: int,
+                                  stream=None):
+    return _check("attn_selftest_prompts_timeout", lib.attn_selftest_prompts_timeout(
+        ctypes.byref(dims), B, row_capacity, _ptr(cu_rows), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+        _ptr(o), o_stride, max_rows, _ptr(workspace), workspace_bytes, _ptr(dev_status), int(limit_ns),
+        _stream(stream)))
+
+
+def kv8_chunk_workspace_bytes(c: kv8_cache, B, row_capacity, max_len, max_rows, total_len) -> int:
+    return int(lib.kv8_chunk_workspace_bytes(ctypes.byref(c), B, row_capacity, max_len, max_rows, total_len))
+
+
+def kv8_chunk(c: kv8_cache, layer, B, row_capacity, cu_rows, cache_len, table, table_pages, table_stride, q, q_stride,
+              k_new, k_stride, v_new, v_stride, o, o_stride, lse, max_len, max_rows, total_len, workspace,
+              workspace_bytes, dev_status, stream=None):
+    return _check("kv8_chunk", lib.kv8_chunk(
+        ctypes.byref(c), layer, B, row_capacity, _ptr(cu_rows), _ptr(cache_len), _ptr(table), table_pages,
+        table_stride, _ptr(q), q_stride, _ptr(k_new), k_stride, _ptr(v_new), v_stride, _ptr(o), o_stride, _ptr(lse),
+        max_len, max_rows, total_len, _ptr(workspace), workspace_bytes, _ptr(dev_status), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -57,11 +57,8 @@
 // heads of 128: 123 us, five times what HBM would need); the chain from a segment's
 // queries to its outputs, about 4 us, where requests are short, and then also the
 // fetching of its instructions: loops there are rolled wherever that costs nothing.
-#include <cuda.h>
-
-#include <atomic>
-
 #include "kv8_math.cuh"
+#include "tmap.cuh"
 
 namespace {
 
@@ -1324,29 +1321,10 @@ __global__ void __launch_bounds__(kJoin) kv8_join_kernel(const __grid_constant__
     }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Kept once it is found; a failure is not.
-EncodeTiledFn encode_tiled() {
-    static std::atomic<EncodeTiledFn> fn{nullptr};
-    EncodeTiledFn f = fn.load(std::memory_order_acquire);
-    if (f) return f;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    f = reinterpret_cast<EncodeTiledFn>(p);
-    fn.store(f, std::memory_order_release);
-    return f;
-}
-
 // A layer's pages as [page][2 h_kv page_tokens rows][d] bytes; boxes of one
 // page and head, rows of at most 128 bytes, swizzled to that width.
 bool encode_pages(CUtensorMap *m, const kv8_cache *c, int layer) {
-    const EncodeTiledFn fn = encode_tiled();
+    const gdn_host::EncodeTiledFn fn = gdn_host::encode_tiled();
     if (!fn) return false;
     const cuuint64_t dims[3] = {cuuint64_t(c->d), cuuint64_t(2) * c->h_kv * c->page_tokens, cuuint64_t(c->num_pages)};
     const cuuint64_t strides[2] = {cuuint64_t(c->d), cuuint64_t(c->page_stride)};

@@ -159,6 +159,58 @@ class Kv8Cache:
             raise gs.GdnError("kv8_attend", st)
         return out, lse
 
+    def attend_chunk(self, layer: int, table: torch.Tensor, cache_len: torch.Tensor, cu_rows: torch.Tensor,
+                     q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, max_len: int, max_rows: int,
+                     total_len: Optional[int] = None, want_lse: bool = False, out: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+        """attend for any number of new rows a request (chunks of prompts, next turns); ``kv8_chunk`` in the header.
+
+        max_len and max_rows are host bounds on cache_len and on a request's rows, total_len on the sum of cache_len
+        (it sizes the call's workspace; None: the requests times max_len)."""
+        h_q, h_kv, d, device = self.h_q, self.h_kv, self.d, self._index
+        B = cache_len.numel()
+        tables, pages = table.shape
+        table_s, one = table.stride()
+        if (table.dtype is not _I32 or cache_len.dtype is not _I32 or cu_rows.dtype is not _I32 or tables < B
+                or (one != 1 and pages > 1) or cu_rows.numel() <= B or not cache_len.is_contiguous()
+                or not cu_rows.is_contiguous() or table.get_device() != device or cache_len.get_device() != device
+                or cu_rows.get_device() != device):
+            raise self._bad_lists("cache_len and cu_rows")
+        R = q.shape[0]
+        strides = []
+        for name, x, h in (("q", q, h_q), ("k_new", k_new, h_kv), ("v_new", v_new, h_kv), ("out", out, h_q)):
+            if x is None and name == "out":
+                strides.append(h * d)
+                continue
+            n, a, b = x.shape
+            s, c, one = x.stride()
+            if (x.dtype is not _BF16 or n < R or a != h or b != d or (c != d and h > 1) or one != 1
+                    or x.get_device() != device):
+                raise self._bad_rows(name, h)
+            strides.append(h * d if n <= 1 else s)  # a single row's stride says nothing
+        total = B * max_len if total_len is None else total_len
+        need = gs.lib.kv8_chunk_workspace_bytes(self._c, B, R, max_len, max_rows, total)
+        if stream is not None:
+            # what the call allocates belongs to the stream it runs on
+            before = torch.cuda.current_stream(self._device)
+            torch.cuda.set_stream(_stream_object(stream))
+        try:
+            raw = _raw_stream(device)
+            if out is None:
+                out = torch.empty((R, h_q, d), dtype=_BF16, device=self._device)
+            lse = torch.empty((R, h_q), dtype=torch.float32, device=self._device) if want_lse else None
+            ws = torch.empty((need,), dtype=torch.uint8, device=self._device) if need else None
+        finally:
+            if stream is not None:
+                torch.cuda.set_stream(before)
+        st = gs.lib.kv8_chunk(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(), pages,
+                              table_s, q.data_ptr(), strides[0], k_new.data_ptr(), strides[1], v_new.data_ptr(),
+                              strides[2], out.data_ptr(), strides[3], lse.data_ptr() if want_lse else None, max_len,
+                              max_rows, total, ws.data_ptr() if need else None, need, self._status, raw)
+        if st != gs.GDN_OK:
+            raise gs.GdnError("kv8_chunk", st)
+        return out, lse
+
     def append(self, layer: int, table: torch.Tensor, cache_len: torch.Tensor, cu_rows: torch.Tensor,
                k_new: torch.Tensor, v_new: torch.Tensor, accept_len: Optional[torch.Tensor] = None,
                max_rows: int = gs.MAX_ROWS, stream=None):

@@ -1,0 +1,193 @@
+"""The attention layers' prompt side: rotary positions and attention over whole prompts.
+
+What a prefill transaction does in a hybrid's softmax-attention layers, beside
+``gdn_chunked_prefill`` in its GatedDeltaNet layers: ``Rope.rotate`` turns the
+queries and new keys, ``attend_prompts`` computes the outputs of prompts without
+earlier tokens (``Kv8Cache.attend_chunk`` those of rows behind a cache), and
+``Kv8Cache.append`` commits the keys and values.
+
+All device work is asynchronous on the caller's stream; errors only the device
+can see set bits in ``status`` (see ``include/gdnspec.h``).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import numpy as np
+import torch
+
+from . import binding as gs
+from .kvcache import _BF16, _I32, _raw_stream, _stream_object
+
+SCALINGS = ("none", "linear", "base", "parts")
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, trained: int = 0,
+                     slow: float = 1.0, fast: float = 32.0) -> Tuple[np.ndarray, float]:
+    """-> (fp64 [rot/2] angular frequencies, the factor on cosine and sine).
+
+    f_j = base^(-2j/rot), and for contexts `factor` times as long as the trained one:
+    linear: every frequency over factor;
+    base:   base * factor^(rot/(rot-2)), which leaves the fastest and divides the slowest by factor;
+    parts:  frequencies that turn at least `fast` times in `trained` positions stay, those that turn at most `slow`
+            times are divided by factor, in between a straight line; cosine and sine times 1 + 0.1 ln(factor)."""
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot is a positive even number of channels")
+    if scaling not in SCALINGS:
+        raise ValueError("scaling is one of %r" % (SCALINGS,))
+    if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("base is above 1 and factor at least 1")
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError("a scaled base wants rot of 4 or more")
+        base = base * factor ** (rot / (rot - 2.0))
+    f = base ** (-2.0 * np.arange(rot // 2, dtype=np.float64) / rot)
+    magnitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if trained <= 0 or not slow < fast:
+            raise ValueError("scaling by parts wants the trained length and slow < fast")
+        keep = np.clip((trained * f / (2.0 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        magnitude = 1.0 + 0.1 * math.log(factor)
+    return f, magnitude
+
+
+class Rope:
+    """Rotary positions of d-channel heads: the first `rot` channels (default all) turn, in pairs (j, j + rot/2) or,
+    interleaved, (2j, 2j + 1).  The frequencies are rope_frequencies(...) or given (`frequencies`, `magnitude`)."""
+
+    def __init__(self, d: int, rot: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, trained: int = 0, device="cuda",
+                 frequencies=None, magnitude: float = 1.0):
+        rot = d if rot is None else rot
+        if d <= 0 or d % 8 or d > 512 or rot <= 0 or rot % 2 or rot > d:
+            raise ValueError("d is a multiple of 8 up to 512, rot an even number up to d")
+        if frequencies is None:
+            f, magnitude = rope_frequencies(rot, base, scaling, factor, trained)
+        else:
+            f = np.asarray(frequencies, dtype=np.float64)
+            if f.shape != (rot // 2,) or not np.isfinite(f).all():
+                raise ValueError("frequencies are rot/2 finite numbers")
+        self.d, self.rot, self.interleaved, self.frequencies, self.magnitude = d, rot, bool(interleaved), f, magnitude
+        turns = np.array([int(round(math.ldexp(x, 64))) % (1 << 64) for x in (f / (2.0 * math.pi)).tolist()],
+                         dtype=np.uint64)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self._device = self.turns.device
+        self._index = self.turns.get_device()
+        self._spec = {}  # (h_q, h_kv) -> rope_spec
+
+    def _bad(self, name: str):
+        return ValueError("%s must be bf16 [rows, heads, %d] with contiguous heads on the table's device, a row for "
+                          "each of the call's" % (name, self.d))
+
+    def rotate(self, q: torch.Tensor, k: Optional[torch.Tensor], cu_rows: torch.Tensor,
+               cache_len: Optional[torch.Tensor], status: torch.Tensor, in_place: bool = False,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+        """-> (q, k) turned to positions cache_len[r] + i (``rope_rows`` in the header): new tensors, q_out and k_out,
+        or in place.  k may be None."""
+        d, device = self.d, self._index
+        B = cu_rows.numel() - 1
+        if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != device
+                or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != device):
+            raise ValueError("cu_rows must be a contiguous int32 list and status one int32, on the table's device")
+        if cache_len is not None and (cache_len.dtype is not _I32 or cache_len.numel() < B
+                                      or not cache_len.is_contiguous() or cache_len.get_device() != device):
+            raise ValueError("cache_len must be a contiguous int32 list of the requests, on the table's device")
+        if in_place and (q_out is not None or k_out is not None):
+            raise ValueError("in place there is no other output")
+        if k is None and k_out is not None:
+            raise ValueError("k_out without k")
+        rows = q.shape[0]
+        if stream is not None:
+            # what the call allocates belongs to the stream it runs on
+            before = torch.cuda.current_stream(self._device)
+            torch.cuda.set_stream(_stream_object(stream))
+        try:
+            raw = _raw_stream(device)
+            args, outs, heads = [], [], []
+            for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+                if x is None:
+                    args += [None, 0, None, 0]
+                    outs.append(None)
+                    heads.append(0)
+                    continue
+                n, h, c = x.shape
+                if in_place:
+                    y = x
+                elif y is None:
+                    y = torch.empty((n, h, d), dtype=_BF16, device=self._device)
+                for label, t in ((name, x), (name + "_out", y)):
+                    if (t.dtype is not _BF16 or t.shape != (rows, h, d) or t.stride(2) != 1
+                            or (t.stride(1) != d and h > 1) or t.get_device() != device):
+                        raise self._bad(label)
+                one = rows <= 1  # a single row's stride says nothing
+                args += [x.data_ptr(), h * d if one else x.stride(0), y.data_ptr(), h * d if one else y.stride(0)]
+                outs.append(y)
+                heads.append(h)
+        finally:
+            if stream is not None:
+                torch.cuda.set_stream(before)
+        spec = self._spec.get(tuple(heads))
+        if spec is None:
+            spec = self._spec[tuple(heads)] = gs.rope_spec(heads[0], heads[1], d, self.rot, int(self.interleaved),
+                                                           self.magnitude)
+        st = gs.lib.rope_rows(ctypes.byref(spec), B, rows, cu_rows.data_ptr(),
+                              None if cache_len is None else cache_len.data_ptr(), self.turns.data_ptr(), *args,
+                              status.data_ptr(), raw)
+        if st != gs.GDN_OK:
+            raise gs.GdnError("rope_rows", st)
+        return outs[0], outs[1]
+
+
+def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
+                   status: torch.Tensor, window: int = 0, sm_scale: Optional[float] = None, want_lse: bool = False,
+                   out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """-> (o bf16 [rows, h_q, d], lse fp32 [rows, h_q] or None); ``attn_prompts`` in the header.
+
+    q [rows, h_q, d], k and v [rows, h_kv, d]: packed prompts; max_rows is a host bound on a prompt's rows."""
+    R, h_q, d = q.shape
+    h_kv = k.shape[1]
+    device, index = q.device, q.get_device()
+    B = cu_rows.numel() - 1
+    if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != index
+            or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != index):
+        raise ValueError("cu_rows must be a contiguous int32 list and status one int32, on the rows' device")
+    strides = []
+    for name, x, h in (("q", q, h_q), ("k", k, h_kv), ("v", v, h_kv), ("out", out, h_q)):
+        if x is None:
+            strides.append(h * d)
+            continue
+        n, a, b = x.shape
+        s, c, one = x.stride()
+        if (x.dtype is not _BF16 or n < R or a != h or b != d or (c != d and h > 1) or one != 1
+                or x.get_device() != index):
+            raise ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads on q's device, a row for each of "
+                             "the call's" % (name, h, d))
+        strides.append(h * d if n <= 1 else s)  # a single row's stride says nothing
+    dims = gs.attn_dims(h_q, h_kv, d, window, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
+    need = gs.attn_prompts_workspace_bytes(dims, B, R, max_rows)
+    if stream is not None:
+        # what the call allocates belongs to the stream it runs on
+        before = torch.cuda.current_stream(device)
+        torch.cuda.set_stream(_stream_object(stream))
+    try:
+        raw = _raw_stream(index)
+        if out is None:
+            out = torch.empty((R, h_q, d), dtype=_BF16, device=device)
+        lse = torch.empty((R, h_q), dtype=torch.float32, device=device) if want_lse else None
+        ws = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    finally:
+        if stream is not None:
+            torch.cuda.set_stream(before)
+    st = gs.lib.attn_prompts(ctypes.byref(dims), B, R, cu_rows.data_ptr(), q.data_ptr(), strides[0], k.data_ptr(),
+                             strides[1], v.data_ptr(), strides[2], out.data_ptr(), strides[3],
+                             lse.data_ptr() if want_lse else None, max_rows, ws.data_ptr() if need else None, need,
+                             status.data_ptr(), raw)
+    if st != gs.GDN_OK:
+        raise gs.GdnError("attn_prompts", st)
+    return out, lse
