@@ -24,6 +24,7 @@ constexpr int kSms = 152;
 constexpr float kSlack = 8.f;
 constexpr int kLeast = 4;    // tiles a part of a cut unit has at least
 constexpr int kMostParts = 64;
+constexpr double kEnds = 5.0;
 constexpr int kAhead = 4;    // tiles of values that the ring can hold: 8 slots, every other one of values
 
 struct Info {                // a unit's parts, for the join: parts 0: nothing to join
@@ -62,8 +63,14 @@ struct Cfg {
     static constexpr int kRoom = 227 * 1024 - 3072 - kStages * kQTile;
     static constexpr int kSlots = kRoom / kSlot > 8 ? 8 : kRoom / kSlot;
     static constexpr int kSmem = kStages * kQTile + kSlots * kSlot + 1024;
-    static constexpr int kSoft = 128 * kStages;  // softmax threads
-    static constexpr int kThreads = kSoft + 128;
+    static constexpr int kSoftWarps = 4 * kStages;
+    static constexpr int kGuards = kStages == 2 ? 1 : 5;  // warps that look through values
+    static constexpr int kThreads = 32 * (kSoftWarps + 3 + kGuards);
+    // Registers a thread: of the 168 that 384 threads may have, the softmax's rows take more, the other warps fewer.
+    static constexpr int kLaunchRegs = 168, kSoftRegs = kStages == 2 ? 208 : 232, kOtherRegs = kStages == 2 ? 88 : 136;
+    static_assert(kThreads == 384 && 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <=
+                                         kThreads * kLaunchRegs,
+                  "more registers than a launch has: the wait for them would not end");
     static_assert(kSlots >= 2 * kPieces + 1 && kSlots <= 2 * kAhead * kPieces, "does not fit an SM");
 };
 
@@ -71,29 +78,63 @@ struct Unit {
     int t0, n, len, r, tok0, parts;
     int64_t kv0;  // its first position's row of the keys
 };
+// What a unit's part sums: tiles tile0 .. of the request's positions, `tiles` of them, of which query tile st uses the
+// first ns[st].  Some row of the unit sees positions begin .. end-1, every row sees full .. all-1; tiles before `left` and
+// from `right` on are masked: they hold positions that not every row sees.
+struct Span {
+    int tile0, tiles, ns[2], left, right, begin, end, full, all;
+};
+struct Work {
+    Unit u;
+    Span sp;
+    int hk, part, x;  // x: the unit's number; -1: no more work
+};
+
+constexpr int kQueue = 2;    // units announced: one in work and the next
+constexpr int kGroups = 8;   // groups of loads that are freed together, in turn (no more fit the ring)
+constexpr int kChunks = 128; // parts of the list of requests whose sums a CTA keeps
 
 template <int D>
 struct Shared {
     using C = Cfg<D>;
-    uint64_t full[C::kSlots], empty[C::kSlots], s_full[2], o_done[2], q_full, drain;  // one arrival
-    uint64_t p_ready[2];  // of four warps
-    uint64_t v_sent[kAhead];        // masked tiles in turn: the copy of the values is under way ...
-    uint64_t v_ok[kAhead], pages;   // ... and looked through (of the two guards)
+    uint64_t full[C::kSlots], freed[kGroups], s_full[2], o_done[2], q_full, q_free, drain;  // one arrival
+    uint64_t p_ready[2];                      // of four warps
+    uint64_t v_sent[kAhead];                  // masked tiles in turn: the copy of the values is under way ...
+    uint64_t v_ok[kAhead];                    // ... and looked through
+    uint64_t w_full[kQueue], w_free[kQueue];  // a unit is announced; everybody is done with it
+    uint64_t pages[kQueue];                   // its pages' numbers are looked through
+    uint64_t near, got;                       // a unit's last tiles are being copied; the next one's number is here
+    alignas(16) uint4 next;
+    Work work[kQueue];
+    int fix[kQueue], bad[kQueue];
+    int holds[C::kSlots];                     // the group of loads that a slot's is in
     prompt::Scan<C::kThreads> scan;
-    Unit u;
+    int blocks[kChunks], kv[kChunks];         // before each part of the list of requests
     uint32_t tmem;
-    int found, fix, bad;
+};
+
+// The ring's slots of a tile's pieces, tile after tile.
+template <int D>
+struct Slots {
+    using C = Cfg<D>;
+    int slot[C::kPieces], phase[C::kPieces];
+    __device__ __forceinline__ Slots() {
+#pragma unroll
+        for (int y = 0; y < C::kPieces; ++y) slot[y] = y, phase[y] = 0;
+    }
+    __device__ __forceinline__ void next() {
+#pragma unroll
+        for (int y = 0; y < C::kPieces; ++y) {
+            slot[y] += C::kPieces;
+            if (slot[y] >= C::kSlots) slot[y] -= C::kSlots, phase[y] ^= 1;
+        }
+    }
 };
 
 // Ring positions of the loads of n tiles, in the order the products use them: K0 K1 V0 K2 V1 ... V(n-1).
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
-// What a unit's part sums: tiles tile0 .. of the request's positions, `tiles` of them, of which query tile st uses the
-// first ns[st].
-struct Span {
-    int tile0, tiles, ns[2];
-};
 __device__ __forceinline__ int unit_tiles(const Args &a, const Unit &u, int stages, int &tile0) {
     const int lo = a.window ? max(0, u.len + u.tok0 + 1 - a.window) : 0;
     const int last = min(u.tok0 + stages * a.per_tile, u.n) - 1;
@@ -112,31 +153,181 @@ __device__ __forceinline__ Span span_of(const Args &a, const Unit &u, int stages
         const int first = u.tok0 + st * a.per_tile, last = min(first + a.per_tile, u.n) - 1;
         s.ns[st] = st < stages && first < u.n ? min(max((u.len + last) / kTile + 1 - s.tile0, 0), s.tiles) : 0;
     }
+    const int last = min(u.tok0 + stages * a.per_tile, u.n) - 1;
+    s.all = u.len + u.tok0 + 1;
+    s.end = u.len + last + 1;
+    s.begin = a.window ? max(0, u.len + u.tok0 + 1 - a.window) : 0;
+    s.full = a.window ? max(0, u.len + last + 1 - a.window) : 0;
+    s.right = s.all / kTile;
+    s.left = (s.full + kTile - 1) / kTile;
     return s;
 }
-// Whether some row of the unit does not see all of a tile's positions.
-__device__ __forceinline__ bool masked(const Args &a, const Unit &u, int stages, int tile) {
-    const int last = min(u.tok0 + stages * a.per_tile, u.n) - 1;
-    return tile * kTile + kTile - 1 > u.len + u.tok0 || (a.window && tile * kTile <= u.len + last - a.window);
+__device__ __forceinline__ bool masked(const Span &s, int tile) { return tile >= s.right || tile < s.left; }
+// Steps of 16 positions of a tile that some row sees.
+__device__ __forceinline__ int2 steps_of(const Span &s, int tile) {
+    return make_int2(max(s.begin - tile * kTile, 0) / 16, (min(s.end - tile * kTile, kTile) + 15) / 16);
 }
 
 // Adds to a row's 32 sums the values that are not finite at positions of masked tiles that it sees: they were taken out
 // of the tiles, where a zero weight would not have kept them from the other rows.
-template <int D>
-__device__ __noinline__ void add_special(const Args &a, const Unit &u, const Span &s, int stages, int hk, int pos,
-                                         int ch, float *o) {
+__device__ __noinline__ void add_special(const Args &a, const Unit &u, const Span &s, int hk, int pos, int ch,
+                                         float *o) {
     for (int j = 0; j < s.tiles; ++j) {
         const int tile = s.tile0 + j;
-        if (!masked(a, u, stages, tile)) continue;
+        if (!masked(s, tile)) continue;
         const int from = max(tile * kTile, a.window ? pos - a.window + 1 : 0), to = min(tile * kTile + kTile - 1, pos);
         for (int t = from; t <= to; ++t) {
-            const uint16_t *v = a.v + (u.kv0 + t) * a.v_row + int64_t(hk) * a.v_head + ch;
-            for (int c = 0; c < 32; ++c) {
-                const float x = gdn::bf16_to_f32(v[c]);
-                if (!(fabsf(x) < INFINITY)) o[c] += x;
+            const uint4 *v = reinterpret_cast<const uint4 *>(a.v + (u.kv0 + t) * a.v_row + int64_t(hk) * a.v_head + ch);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4 y = v[e];
+                const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+                const uint32_t most = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                               __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+                if (max(most >> 16, most & 0xffffu) < 0x7f80u) continue;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if ((x[c] & 0x7f80u) == 0x7f80u) o[8 * e + 2 * c] += __uint_as_float(x[c] << 16);
+                    if ((x[c] & 0x7f800000u) == 0x7f800000u) o[8 * e + 2 * c + 1] += __uint_as_float(x[c] & 0xffff0000u);
+                }
             }
         }
     }
+}
+
+// The next launch-grid block that has not started, taken over by this CTA; the answer lands in *to.
+__device__ __forceinline__ void ask_next(uint4 *to, uint64_t *bar) {
+    gdn::mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            gdn::smem_u32(to)),
+        "r"(gdn::smem_u32(bar))
+        : "memory");
+}
+// Its block numbers; false: there is none left.
+__device__ __forceinline__ bool next_of(const uint4 *from, int &x, int &y) {
+    uint32_t got, bx, by;
+    asm volatile(
+        "{\n .reg .b128 r;\n .reg .pred p;\n .reg .b32 z, w;\n ld.shared.b128 r, [%3];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " mov.u32 %2, 0;\n @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, w}, r;\n}\n"
+        : "=&r"(got), "=&r"(bx), "=&r"(by)
+        : "r"(gdn::smem_u32(from))
+        : "memory");
+    x = int(bx);
+    y = int(by);
+    return got != 0;
+}
+
+// The unit of block (x, part), found by a warp: the later rows of a request, which see most, come first.
+template <int D>
+__device__ __forceinline__ bool find_unit(const Args &a, const Shared<D> &s, int x, int part, int total, Work &w) {
+    constexpr int kStages = Cfg<D>::kStages;
+    const int lane = threadIdx.x & 31, per_unit = kStages * a.per_tile;
+    const int rank = x / a.h_kv;
+    if (rank >= total) return false;
+    int i = 0;  // the last part of the list that begins at or before the rank
+#pragma unroll
+    for (int e = 0; e < kChunks / 32; ++e) i += __popc(__ballot_sync(0xffffffffu, s.blocks[e * 32 + lane] <= rank));
+    --i;
+    const int chunk = (a.rq.B + kChunks - 1) / kChunks, r1 = min(a.rq.B, (i + 1) * chunk);
+    int blocks = s.blocks[i];
+    int64_t kv = s.kv[i];
+    Unit &u = w.u;
+    for (int r0 = i * chunk; r0 < r1; r0 += 32) {
+        prompt::Request q{};
+        if (r0 + lane < r1) q = prompt::request_of(a.rq, r0 + lane);
+        const int nb = (q.n + per_unit - 1) / per_unit, rows = int(prompt::kv_rows_of(q));
+        int nb_in = nb, rows_in = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, nb_in, o), z = __shfl_up_sync(0xffffffffu, rows_in, o);
+            if (lane >= o) nb_in += y, rows_in += z;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, rank < blocks + nb_in);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            const int before = blocks + __shfl_sync(0xffffffffu, nb_in - nb, l);
+            const int count = __shfl_sync(0xffffffffu, nb, l);
+            kv += __shfl_sync(0xffffffffu, rows_in - rows, l);
+            u.t0 = __shfl_sync(0xffffffffu, q.t0, l);
+            u.n = __shfl_sync(0xffffffffu, q.n, l);
+            u.len = __shfl_sync(0xffffffffu, q.len, l);
+            u.r = r0 + l;
+            u.tok0 = (count - 1 - (rank - before)) * per_unit;
+            u.kv0 = a.rq.kv_capacity ? kv : int64_t(u.t0);
+            if (a.rq.kv_capacity && kv + u.len + u.n > a.rq.kv_capacity) return false;
+            int tile0;
+            const int tiles = unit_tiles(a, u, kStages, tile0);
+            u.parts = min(a.splits, max(1, tiles / kLeast));
+            if (part >= u.parts) return false;
+            w.sp = span_of(a, u, kStages, part);
+            w.hk = x - rank * a.h_kv;
+            w.part = part;
+            w.x = x;
+            return true;
+        }
+        blocks += __shfl_sync(0xffffffffu, nb_in, 31);
+        kv += __shfl_sync(0xffffffffu, rows_in, 31);
+    }
+    return false;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The loads before a ld_wait are done: no use of them comes earlier.
+template <int N>
+__device__ __forceinline__ void arrived(uint32_t (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
+}
+// Positions past hi and up to lo of a tile are not seen: their scores become -inf where they lie (a loop of little code;
+// for few tiles).
+__device__ __forceinline__ void hide(uint32_t t_s, int hi, int lo) {
+#pragma unroll 1
+    for (int i = 0; i < kTile; i += 32) {
+        const int h = hi - i, b = lo - i;
+        const uint32_t up = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+        const uint32_t see = b < 0 ? up : b >= 31 ? 0u : up & ~((2u << b) - 1u);
+        if (__all_sync(0xffffffffu, see == ~0u)) continue;
+        uint32_t x[32];
+        tc::ld32_async(t_s + i, x);
+        tc::ld_wait();
+        arrived(x);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = see & (1u << c) ? x[c] : 0xff800000u;
+        tc::st32_async(t_s + i, x);
+    }
+    tc::st_wait();
+}
+__device__ __forceinline__ float top_of(const uint32_t (&x)[kTile]) {
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < kTile / 2; ++i)
+        top[i & 3] = max3(top[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+    return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+}
+// Four lanes' pieces of four rows, transposed: v[i] becomes lane i's (of the four) piece of this lane's number.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
+    const int lane = threadIdx.x;
+#pragma unroll
+    for (int s = 1; s <= 2; s *= 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & s) continue;
+            const bool up = lane & s;
+            uint4 &lo = v[i], &hi = v[i | s];
+            uint4 t = up ? lo : hi;
+            t.x = __shfl_xor_sync(0xffffffffu, t.x, s);
+            t.y = __shfl_xor_sync(0xffffffffu, t.y, s);
+            t.z = __shfl_xor_sync(0xffffffffu, t.z, s);
+            t.w = __shfl_xor_sync(0xffffffffu, t.w, s);
+            lo = up ? t : lo;
+            hi = up ? hi : t;
+        }
 }
 
 template <int D>
@@ -148,454 +339,600 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     static_assert(sizeof(Shared<D>) <= 2048, "static shared memory");
     gdn::pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kCopyWarp = C::kSoft / 32, kMmaWarp = kCopyWarp + 1, kGuard = kCopyWarp + 2;
+    constexpr int kCopyWarp = C::kSoftWarps, kMmaWarp = kCopyWarp + 1, kFindWarp = kCopyWarp + 2,
+                  kGuardWarp = kCopyWarp + 3;
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&s.tmem, 512);
     } else if (warp == kCopyWarp && lane == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
-            gdn::mbar_init(s.full + i, 1);
-            gdn::mbar_init(s.empty + i, 1);
-        }
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.mq) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.mk) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.mv) : "memory");
+        for (int i = 0; i < C::kSlots; ++i) gdn::mbar_init(s.full + i, 1);
+        for (int i = 0; i < kGroups; ++i) gdn::mbar_init(s.freed + i, 1);
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s.s_full + i, 1);
             gdn::mbar_init(s.o_done + i, 1);
             gdn::mbar_init(s.p_ready + i, 4);
         }
         gdn::mbar_init(&s.q_full, 1);
+        gdn::mbar_init(&s.q_free, 1);
         gdn::mbar_init(&s.drain, 1);
+        gdn::mbar_init(&s.got, 1);
+        gdn::mbar_init(&s.near, 1);
         for (int i = 0; i < kAhead; ++i) {
             gdn::mbar_init(s.v_sent + i, 1);
-            gdn::mbar_init(s.v_ok + i, 2);
+            gdn::mbar_init(s.v_ok + i, C::kGuards);
         }
-        gdn::mbar_init(&s.pages, 2);
-        s.found = s.fix = s.bad = 0;
+        for (int i = 0; i < kQueue; ++i) {
+            gdn::mbar_init(s.w_full + i, 1);
+            gdn::mbar_init(s.w_free + i, C::kSoftWarps + 2 + C::kGuards);
+            gdn::mbar_init(s.pages + i, C::kGuards);
+        }
     }
     gdn::pdl_wait();
-    __syncthreads();
+    // what a CTA left undone that timed out, no other tries again
+    const bool late = a.status && (*reinterpret_cast<volatile uint32_t *>(a.status) & GDN_DEV_TIMEOUT);
 
-    // ---- this CTA's unit: the later rows of a request, which see most, come first
-    const int hk = blockIdx.x % a.h_kv, rank = blockIdx.x / a.h_kv, part = blockIdx.y;
+    // ---- the requests: sums over parts of their list
     const int per_unit = kStages * a.per_tile;
+    long long total;
     {
-        const int chunk = (a.rq.B + C::kThreads - 1) / C::kThreads, r0 = tid * chunk, r1 = min(a.rq.B, r0 + chunk);
-        long long blocks = 0, kv = 0, all, kv_all;
+        const int chunk = (a.rq.B + kChunks - 1) / kChunks, r0 = min(a.rq.B, tid * chunk), r1 = min(a.rq.B, r0 + chunk);
+        long long blocks = 0, kv = 0, kv_all;
         for (int r = r0; r < r1; ++r) {
             const prompt::Request q = prompt::request_of(a.rq, r);
-            if (q.bad && blockIdx.x == 0 && part == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
+            if (q.bad && blockIdx.x == 0 && blockIdx.y == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
             blocks += (q.n + per_unit - 1) / per_unit;
             kv += prompt::kv_rows_of(q);
         }
-        const long long mine = blocks;
-        prompt::scan2<C::kThreads>(s.scan, blocks, kv, all, kv_all);
-        if (blocks <= rank && rank < blocks + mine) {
-            for (int r = r0; r < r1; ++r) {
-                const prompt::Request q = prompt::request_of(a.rq, r);
-                const int nb = (q.n + per_unit - 1) / per_unit;
-                if (rank < blocks + nb) {
-                    Unit u;
-                    u.t0 = q.t0;
-                    u.n = q.n;
-                    u.len = q.len;
-                    u.r = r;
-                    u.tok0 = (nb - 1 - int(rank - blocks)) * per_unit;
-                    u.kv0 = a.rq.kv_capacity ? kv : int64_t(q.t0);
-                    int tile0;
-                    const int tiles = unit_tiles(a, u, kStages, tile0);
-                    u.parts = min(a.splits, max(1, tiles / kLeast));
-                    s.u = u;
-                    s.found = !a.rq.kv_capacity || kv + q.len + q.n <= a.rq.kv_capacity;
-                    break;
-                }
-                blocks += nb;
-                kv += prompt::kv_rows_of(q);
-            }
+        prompt::scan2<C::kThreads>(s.scan, blocks, kv, total, kv_all);
+        if (tid < kChunks) {
+            s.blocks[tid] = int(blocks);
+            // (past the workspace's rows a request is refused, however far)
+            s.kv[tid] = int(min(kv, (long long)gdn_host::kKv8MaxLen));
         }
     }
     tc::fence_before();
-    __syncthreads();
+    const bool stop = __syncthreads_or(late);
     tc::fence_after();
     const uint32_t tm = s.tmem;
-    const Unit u = s.u;
-    if (!s.found || part >= u.parts) {
-        if (tid == 0 && a.info && part == 0) a.info[blockIdx.x].parts = 0;
-        __syncthreads();
-        if (warp == kMmaWarp) tc::tmem_dealloc(tm, 512);
-        return;
-    }
-    const Span sp = span_of(a, u, kStages, part);
-    const int nt = sp.tiles;
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *s_q = sm, *s_ring = sm + kStages * C::kQTile;
+    bool ok = !stop;
+    // A warp's wait: one lane's.
+    auto wait = [&](uint64_t *bar, int phase) {
+        if (lane == 0) ok = gdn::mbar_wait_bounded(bar, phase & 1, a.wait_ns);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        return ok;
+    };
+    // Whether there is a unit k, once that is known, and that this warp is done with it.
+    auto take = [&](int k) {
+        return ok && wait(&s.w_full[k % kQueue], k / kQueue) && s.work[k % kQueue].x >= 0;
+    };
+    auto done = [&](int k) {
+        __syncwarp();
+        if (lane == 0) arrive(&s.w_free[k % kQueue]);
+    };
 
     if (warp < kCopyWarp) {
         // ---- softmax: a thread a row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         const int st = warp >> 2;
         const int row = (warp & 3) * 32 + lane, tok = row / a.group, head = row - tok * a.group;
-        const int at = u.tok0 + st * a.per_tile + tok;
-        const bool valid = tok < a.per_tile && at < u.n;
-        const int pos = u.len + at;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
         const uint32_t t_o = tm + 256 + (kStages == 2 ? st * D : 0) + lanes;
-        const int n = sp.ns[st];
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const int slot = kStages == 2 ? st : j & 1;
-            ok = gdn::mbar_wait_bounded(&s.s_full[slot], (kStages == 2 ? j : j >> 1) & 1, a.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc::fence_after();
-            const uint32_t t_s = tm + slot * kTile + lanes;
-            uint32_t x[kTile];
+        const f2 c2 = pair(a.scale_log2, a.scale_log2);
+        int g = 0, units = 0;  // tiles so far, and units with any
+        for (int k = 0; take(k); ++k) {
+            const Work &w = s.work[k % kQueue];
+            const int n = w.sp.ns[st];
+            // (rows of nobody: weights of 0)
+            const auto position = [&] { return w.u.tok0 + st * a.per_tile + tok; };
+            const auto valid = [&] { return tok < a.per_tile && position() < w.u.n; };
+            float m = valid() ? -INFINITY : INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j, ++g) {
+                const int slot = kStages == 2 ? st : g & 1, turn = kStages == 2 ? g : g >> 1;
+                if (!wait(&s.s_full[slot], turn)) break;
+                tc::fence_after();
+                const uint32_t t_s = tm + slot * kTile + lanes;
+                if (masked(w.sp, w.sp.tile0 + j)) {
+                    const int hi = w.u.len + position() - (w.sp.tile0 + j) * kTile;
+                    hide(t_s, hi, a.window ? hi - a.window : -1);
+                }
+                uint32_t x[kTile];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tc::ld32_async(t_s + 32 * i, x + 32 * i);
-            tc::ld_wait();
+                for (int i = 0; i < 4; ++i) tc::ld32_async(t_s + 32 * i, x + 32 * i);
+                tc::ld_wait();
+                arrived(x);
+                const float z = top_of(x) * a.scale_log2;
+                if (__any_sync(0xffffffffu, z > m + kSlack)) {
+                    const float now = fmaxf(m, z), f = ex2(m - (now == -INFINITY ? 0.f : now));
+                    if (j > 0) {
+                        // (with two query tiles the scores are behind the products before)
+                        if (kStages == 1 && !wait(&s.o_done[(g - 1) & 1], (g - 1) >> 1)) break;
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc::ld16_async(t_o + c, o);
+                            tc::ld_wait();
+                            arrived(o);
 #pragma unroll
-            for (int i = 0; i < kTile; ++i) asm volatile("" : "+r"(x[i]));
-            if (masked(a, u, kStages, sp.tile0 + j)) {
-                const int hi = pos - (sp.tile0 + j) * kTile, lo = a.window ? hi - a.window : -1;
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc::st16_async(t_o + c, o);
+                        }
+                    }
+                    l *= f;
+                    m = now;
+                }
+                const float ref = m == -INFINITY ? 0.f : -m;
+                const f2 r2 = pair(ref, ref);
+                f2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int h = hi - 32 * i, b = lo - 32 * i;
-                    const uint32_t up = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
-                    const uint32_t see = b < 0 ? up : b >= 31 ? 0u : up & ~((2u << b) - 1u);
+                    uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!(see >> c & 1)) x[32 * i + c] = 0xff800000u;
-                }
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < kTile; i += 2)
-                top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-            float z = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-            if (!valid) z = -INFINITY;
-            if (__any_sync(0xffffffffu, z > m + kSlack)) {
-                const float now = fmaxf(m, z), f = ex2(m - (now == -INFINITY ? 0.f : now));
-                if (j > 0) {
-                    ok = gdn::mbar_wait_bounded(&s.o_done[st], (j - 1) & 1, a.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::ld32_async(t_o + c, o);
-                        tc::ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            asm volatile("" : "+r"(o[i]));
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        }
-                        tc::st32_async(t_o + c, o);
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 e = both(fma2(pair(x[32 * i + 2 * c], x[32 * i + 2 * c + 1]), c2, r2));
+                        const float e0 = ex2(e.x), e1 = ex2(e.y);
+                        sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[c]) : "f"(e1), "f"(e0));
                     }
+                    tc::st16_async(t_s + 16 * i, p);
                 }
-                l *= f;
-                m = now;
+                const float2 t = both(add2(sum[0], sum[1]));
+                l += t.x + t.y;
+                tc::st_wait();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&s.p_ready[slot]);
             }
-            const float ref = m == -INFINITY ? 0.f : m;
-            const f2 c2 = pair(a.scale_log2, a.scale_log2), r2 = pair(-ref, -ref);
-            f2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t p[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float2 e = both(fma2(pair(x[64 * i + 2 * c], x[64 * i + 2 * c + 1]), c2, r2));
-                    const float e0 = ex2(e.x), e1 = ex2(e.y);
-                    sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[c]) : "f"(e1), "f"(e0));
-                }
-                tc::st32_async(t_s + 32 * i, p);
+            if (!ok) break;
+            if (!wait(&s.pages[k % kQueue], k / kQueue)) break;
+            if (n > 0) {
+                if (!wait(&s.o_done[kStages == 2 ? st : (g - 1) & 1], kStages == 2 ? units : (g - 1) >> 1)) break;
+                ++units;
             }
-            const float2 t = both(add2(sum[0], sum[1]));
-            l += t.x + t.y;
-            tc::st_wait();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&s.p_ready[slot]);
-        }
-        if (ok) {
-            ok = gdn::mbar_wait_bounded(&s.pages, 0, a.wait_ns);
-            // (with two tiles of scores ahead, the products of the last tile but one may be running too)
-            if (ok && kStages == 1 && n > 1) ok = gdn::mbar_wait_bounded(&s.o_done[st], n & 1, a.wait_ns);
-            if (ok && n > 0) ok = gdn::mbar_wait_bounded(&s.o_done[st], (n - 1) & 1, a.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        if (ok) {
             tc::fence_after();
-            const bool fix = *reinterpret_cast<volatile int *>(&s.fix);
-            const bool write = valid && !*reinterpret_cast<volatile int *>(&s.bad);
-            const bool whole = u.parts == 1;
-            const int64_t wrow = ((int64_t(blockIdx.x) * a.splits + part) * kStages + st) * kTile + row;
+            const bool fix = *reinterpret_cast<volatile int *>(&s.fix[k % kQueue]);
+            const bool bad = *reinterpret_cast<volatile int *>(&s.bad[k % kQueue]);
+            const int at = position();
+            const bool write = valid() && !bad, whole = w.u.parts == 1;
+            const int64_t wrow = ((int64_t(w.x) * a.splits + w.part) * kStages + st) * kTile + row;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int h = hk * a.group + head;
-            uint16_t *o_row = a.o + (int64_t(u.t0) + at) * a.o_stride + int64_t(h) * D;
+            const int h = w.hk * a.group + head;
+            // where this lane's piece of each of four lanes' rows goes
+            uint16_t *to[4];
+            {
+                const unsigned long long o_row = reinterpret_cast<unsigned long long>(
+                    write ? a.o + (int64_t(w.u.t0) + at) * a.o_stride + int64_t(h) * D : nullptr);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const unsigned long long x = __shfl_sync(0xffffffffu, o_row, (lane & ~3) + i);
+                    to[i] = x ? reinterpret_cast<uint16_t *>(x) + (lane & 3) * 8 : nullptr;
+                }
+            }
+            const bool keep = n > 0 && l != 0.f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t x[32];
-                float o[32];
                 if (n > 0) {
                     tc::ld32_async(t_o + c, x);
                     tc::ld_wait();
                 }
+                arrived(x);
+                if (!keep) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    asm volatile("" : "+r"(x[i]));
-                    o[i] = n > 0 && l != 0.f ? __uint_as_float(x[i]) : 0.f;
+                    for (int i = 0; i < 32; ++i) x[i] = 0;
                 }
-                if (fix && write && n > 0) add_special<D>(a, u, sp, kStages, hk, pos, c, o);
-                if (write && whole) {
+                if (fix && write && n > 0) {
+                    float o[32];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 w;
-                        uint32_t *ww = reinterpret_cast<uint32_t *>(&w);
+                    for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
+                    add_special(a, w.u, w.sp, w.hk, w.u.len + at, c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(o[i]);
+                }
+                // A store of 16 bytes from each of 32 rows is 32 accesses; four lanes trade pieces, so that they
+                // write 64 bytes of a row together.
+                if (whole) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t y[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                                : "=r"(ww[e])
-                                : "f"(o[i + 2 * e + 1] * inv), "f"(o[i + 2 * e] * inv));
-                        *reinterpret_cast<uint4 *>(o_row + c + i) = w;
+                                : "=r"(y[e])
+                                : "f"(__uint_as_float(x[8 * i + 2 * e + 1]) * inv),
+                                  "f"(__uint_as_float(x[8 * i + 2 * e]) * inv));
+                        v[i] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                } else if (write) {
+                    transpose4(v);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4 *>(a.ws_o + wrow * D + c + i) =
-                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        if (to[i]) *reinterpret_cast<uint4 *>(to[i] + c) = v[i];
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = make_uint4(x[16 * y + 4 * i], x[16 * y + 4 * i + 1], x[16 * y + 4 * i + 2],
+                                              x[16 * y + 4 * i + 3]);
+                        transpose4(v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (to[i])
+                                *reinterpret_cast<uint4 *>(a.ws_o + (wrow - (lane & 3) + i) * D + (lane & 3) * 4 + c +
+                                                           16 * y) = v[i];
+                    }
                 }
             }
             if (write && whole) {
                 if (a.lse)
-                    a.lse[(int64_t(u.t0) + at) * a.h_q + h] =
+                    a.lse[(int64_t(w.u.t0) + at) * a.h_q + h] =
                         l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else if (write) {
                 a.ws_ml[wrow] = make_float2(m, l);
             }
+            if (tid == 0 && w.part == 0 && a.info) {
+                Info f = {};
+                f.t0 = w.u.t0;
+                f.tok0 = w.u.tok0;
+                f.n = w.u.n;
+                f.hk = w.hk;
+                f.parts = whole || bad ? 0 : w.u.parts;
+                a.info[w.x] = f;
+            }
+            tc::fence_before();
+            done(k);
         }
-        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-        tc::fence_before();
-    } else if (warp == kCopyWarp) {
-        // ---- copies
-        const bool leader = elect_one();
-        bool ok = true;
-        int issued = 0;
-        if (leader) {
-            int tiles = 0;
-            for (int st = 0; st < kStages; ++st) tiles += sp.ns[st] > 0;
-            gdn::mbar_arrive_expect_tx(&s.q_full, uint32_t(tiles * a.per_tile * a.group) * (D * 2));
-            for (int st = 0; st < kStages; ++st)
-                if (sp.ns[st] > 0)
-                    for (int c = 0; c < D; c += 64)
-                        gdn::tma_load_3d(s_q + st * C::kQTile + c * kTile * 2, &a.mq, c, hk * a.group,
-                                         u.t0 + u.tok0 + st * a.per_tile, &s.q_full);
-        }
-        auto load = [&](const CUtensorMap &map, int tile, int at) {
-            for (int x = 0; x < C::kPieces; ++x) {
-                const int pos = at * C::kPieces + x, slot = pos % C::kSlots;
-                if (pos >= C::kSlots)
-                    ok = ok && gdn::mbar_wait_bounded(&s.empty[slot], (pos / C::kSlots - 1) & 1, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                if (leader) {
+        if (!ok && !stop) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (warp == kCopyWarp) {
+            // ---- copies: one lane
+            const bool one = elect_one();
+            // ring: tiles' places before this unit; group: of loads that the products free together, a tile's keys and the
+            // values of the one before, or each by itself where they fill the ring
+            int ring = 0, issued = 0, sent = 0, units = 0, group = 0;
+            auto load = [&](const CUtensorMap &map, const Work &w, int tile, int place) {
+                for (int x = 0; x < C::kPieces; ++x) {
+                    const int pos = place * C::kPieces + x, slot = pos % C::kSlots;
+                    if (pos >= C::kSlots)
+                        ok = ok && gdn::mbar_wait_bounded(&s.freed[s.holds[slot] % kGroups],
+                                                          s.holds[slot] / kGroups & 1, a.wait_ns);
+                    if (!ok) return;
+                    s.holds[slot] = group;
                     gdn::mbar_arrive_expect_tx(&s.full[slot], C::kSlot);
                     for (int c = 0; c < C::kPiece; c += 64)
-                        gdn::tma_load_3d(s_ring + slot * C::kSlot + c * kTile * 2, &map, x * C::kPiece + c, hk,
-                                         int(u.kv0) + tile * kTile, &s.full[slot]);
+                        gdn::tma_load_3d(s_ring + slot * C::kSlot + c * kTile * 2, &map, x * C::kPiece + c, w.hk,
+                                         int(w.u.kv0) + tile * kTile, &s.full[slot]);
+                    issued = pos + 1;
                 }
-                issued = pos + 1;
-            }
-        };
-        int sent = 0;
-        for (int i = 0; i <= nt && ok; ++i) {
-            if (i < nt) load(a.mk, sp.tile0 + i, k_pos(i));
-            if (i == 0 || !ok || (a.withhold && i == nt)) continue;
-            load(a.mv, sp.tile0 + i - 1, v_pos(i - 1, nt));
-            if (ok && masked(a, u, kStages, sp.tile0 + i - 1)) {
-                if (leader) arrive(&s.v_sent[sent % kAhead]);
-                ++sent;
-            }
-        }
-        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-        // every copy has landed before the CTA leaves (on the usual path these waits are over)
-        (void)gdn::mbar_wait_bounded(&s.q_full, 0, a.wait_ns);
-        for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
-            (void)gdn::mbar_wait_bounded(&s.full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
-    } else if (warp == kMmaWarp) {
-        // ---- products: the warp runs the loop, one elected lane issues
-        const uint32_t id_s = tc::idesc_bf16(128, kTile) | (a.negate ? tc::kNegA : 0);
-        constexpr uint32_t id_p = tc::idesc_bf16(128, C::kPiece) | tc::kBMnMajor;
-        const uint64_t dq = tc::smem_desc(gdn::smem_u32(s_q)), dk = tc::smem_desc(gdn::smem_u32(s_ring));
-        const uint64_t dv = tc::smem_desc_mn(gdn::smem_u32(s_ring), kTile * 128);
-        const bool leader = elect_one();
-        bool ok = gdn::mbar_wait_bounded(&s.q_full, 0, a.wait_ns);
-        int guarded = 0;
-        auto wait_tile = [&](int at) {
-            for (int x = 0; x < C::kPieces; ++x) {
-                const int pos = at * C::kPieces + x;
-                ok = ok && gdn::mbar_wait_bounded(&s.full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            tc::fence_after();
-        };
-        auto free_tile = [&](int at) {
-            if (leader)
-                for (int x = 0; x < C::kPieces; ++x) tc::commit(&s.empty[(at * C::kPieces + x) % C::kSlots]);
-        };
-        auto scores = [&](int st, int slot, int j) {
-            if (!leader) return;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const int pos = k_pos(j) * C::kPieces + k * 16 / C::kPiece, in = k * 16 % C::kPiece;
-                tc::mma_bf16(tm + slot * kTile,
-                             tc::desc_at(dq, st * C::kQTile + (k / 4) * kTile * 128 + (k % 4) * 32),
-                             tc::desc_at(dk, (pos % C::kSlots) * C::kSlot + (in / 64) * kTile * 128 + (in % 64) * 2),
-                             id_s, k > 0);
-            }
-            tc::commit(&s.s_full[slot]);
-        };
-        auto outputs = [&](int st, int slot, int j) {
-            if (!leader) return;
-#pragma unroll
-            for (int x = 0; x < C::kPieces; ++x) {
-                const int pos = v_pos(j, nt) * C::kPieces + x;
-                const uint64_t d = tc::desc_at(dv, (pos % C::kSlots) * C::kSlot);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc::mma_bf16_ts(tm + 256 + (kStages == 2 ? st * D : 0) + x * C::kPiece, tm + slot * kTile + k * 8,
-                                    tc::desc_at(d, k * 2048), id_p, j > 0 || k > 0);
-            }
-            tc::commit(&s.o_done[st]);
-        };
-        auto wait_weights = [&](int slot, int phase) {
-            ok = ok && gdn::mbar_wait_bounded(&s.p_ready[slot], phase & 1, a.wait_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            tc::fence_after();
-        };
-        auto wait_values = [&](int j) {
-            wait_tile(v_pos(j, nt));
-            if (masked(a, u, kStages, sp.tile0 + j)) {
-                ok = ok && gdn::mbar_wait_bounded(&s.v_ok[guarded % kAhead], guarded / kAhead & 1, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                ++guarded;
-            }
-        };
-        wait_tile(k_pos(0));
-        if constexpr (kStages == 2) {
-            if (ok) {
-                for (int st = 0; st < 2; ++st)
-                    if (sp.ns[st] > 0) scores(st, st, 0);
-                free_tile(k_pos(0));
-            }
-            for (int j = 0; j < nt && ok; ++j) {
-                if (j + 1 < nt) wait_tile(k_pos(j + 1));
-                if (ok) wait_values(j);
-                for (int st = 0; st < 2 && ok; ++st) {
-                    if (j < sp.ns[st]) {
-                        wait_weights(st, j);
-                        if (!ok) break;
-                        outputs(st, st, j);
+            };
+            for (int k = 0; one; ++k) {
+                ok = ok && gdn::mbar_wait_bounded(&s.w_full[k % kQueue], k / kQueue & 1, a.wait_ns);
+                if (!ok || s.work[k % kQueue].x < 0) break;
+                const Work w = s.work[k % kQueue];
+                const int nt = w.sp.tiles;
+                load(a.mk, w, w.sp.tile0, ring);
+                ++group;
+                if (ok && k > 0) ok = gdn::mbar_wait_bounded(&s.q_free, (k - 1) & 1, a.wait_ns);
+                if (!ok) break;
+                int tiles = 0;
+                for (int st = 0; st < kStages; ++st) tiles += w.sp.ns[st] > 0;
+                gdn::mbar_arrive_expect_tx(&s.q_full, uint32_t(tiles * a.per_tile * a.group) * (D * 2));
+                for (int st = 0; st < kStages; ++st)
+                    if (w.sp.ns[st] > 0)
+                        for (int c = 0; c < D; c += 64)
+                            gdn::tma_load_3d(s_q + st * C::kQTile + c * kTile * 2, &a.mq, c, w.hk * a.group,
+                                             w.u.t0 + w.u.tok0 + st * a.per_tile, &s.q_full);
+                units = k + 1;
+                for (int i = 1; i <= nt && ok; ++i) {
+                    if (i == max(1, nt - 3)) arrive(&s.near);
+                    if (i < nt) {
+                        load(a.mk, w, w.sp.tile0 + i, ring + k_pos(i));
+                        if (kStages == 1) ++group;
                     }
-                    if (st == 1) free_tile(v_pos(j, nt));
-                    if (j + 1 < sp.ns[st]) scores(st, st, j + 1);
+                    if (!ok || (a.withhold && i == nt)) continue;
+                    load(a.mv, w, w.sp.tile0 + i - 1, ring + v_pos(i - 1, nt));
+                    ++group;
+                    if (ok && masked(w.sp, w.sp.tile0 + i - 1)) {
+                        arrive(&s.v_sent[sent % kAhead]);
+                        ++sent;
+                    }
                 }
-                if (ok && j + 1 < nt) free_tile(k_pos(j + 1));
+                if (!ok) break;
+                ring += 2 * nt;
+                arrive(&s.w_free[k % kQueue]);
+            }
+            // every copy has landed before the CTA leaves (on the usual path these waits are over)
+            if (units) (void)gdn::mbar_wait_bounded(&s.q_full, (units - 1) & 1, a.wait_ns);
+            for (int pos = max(0, issued - C::kSlots); pos < issued; ++pos)
+                (void)gdn::mbar_wait_bounded(&s.full[pos % C::kSlots], (pos / C::kSlots) & 1, a.wait_ns);
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            // ---- products: one lane waits and issues
+            if (elect_one()) {
+                const uint32_t id_s = tc::idesc_bf16(128, kTile) | (a.negate ? tc::kNegA : 0);
+                constexpr uint32_t id_p = tc::idesc_bf16(128, C::kPiece) | tc::kBMnMajor;
+                const uint64_t dq = tc::smem_desc(gdn::smem_u32(s_q)), dk = tc::smem_desc(gdn::smem_u32(s_ring));
+                const uint64_t dv = tc::smem_desc_mn(gdn::smem_u32(s_ring), kTile * 128);
+                int guarded = 0, groups = 0;
+                int g0 = 0, g1 = 0;  // tiles of each query tile before this unit
+                Slots<D> at;         // of the ring's next tile
+                // A tile's pieces have landed.
+                auto landed = [&](const Slots<D> &x) {
+#pragma unroll
+                    for (int y = 0; y < C::kPieces; ++y) ok = ok && gdn::mbar_wait_bounded(&s.full[x.slot[y]], x.phase[y], a.wait_ns);
+                    return ok;
+                };
+                auto scores = [&](int st, int slot, const Slots<D> &x) {
+#pragma unroll
+                    for (int y = 0; y < C::kPieces; ++y) {
+                        const uint64_t d = tc::desc_at(dk, x.slot[y] * C::kSlot), q = tc::desc_at(dq, st * C::kQTile);
+#pragma unroll
+                        for (int i = 0; i < C::kPiece / 16; ++i) {
+                            const int e = y * C::kPiece / 16 + i;
+                            tc::mma_bf16(tm + slot * kTile, tc::desc_at(q, (e / 4) * kTile * 128 + (e % 4) * 32),
+                                         tc::desc_at(d, (i / 4) * kTile * 128 + (i % 4) * 32), id_s, e > 0);
+                        }
+                    }
+                    tc::commit(&s.s_full[slot]);
+                };
+                // (the softmax warps give a unit's first weights after they have read the last unit's sums)
+                auto outputs = [&](int st, int slot, const Slots<D> &x, bool more) {
+#pragma unroll
+                    for (int y = 0; y < C::kPieces; ++y) {
+                        const uint64_t d = tc::desc_at(dv, x.slot[y] * C::kSlot);
+                        const uint32_t to = tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece;
+#pragma unroll
+                        for (int i = 0; i < kTile / 16; ++i)
+                            tc::mma_bf16_ts(to, tm + slot * kTile + i * 8, tc::desc_at(d, i * 2048), id_p,
+                                            more || i > 0);
+                    }
+                };
+                // The same over the positions that some row sees.
+                auto outputs_cut = [&](int st, int slot, const Slots<D> &x, bool more, int2 e) {
+#pragma unroll 1
+                    for (int i = e.x; i < e.y; ++i)
+#pragma unroll
+                        for (int y = 0; y < C::kPieces; ++y)
+                            tc::mma_bf16_ts(tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece,
+                                            tm + slot * kTile + i * 8,
+                                            tc::desc_at(dv, x.slot[y] * C::kSlot + i * 2048), id_p, more || i > e.x);
+                };
+                auto free_group = [&] {
+                    tc::commit(&s.freed[groups % kGroups]);
+                    ++groups;
+                };
+                auto weights_of = [&](int slot, int turn) {
+                    ok = ok && gdn::mbar_wait_bounded(&s.p_ready[slot], turn & 1, a.wait_ns);
+                    tc::fence_after();
+                    return ok;
+                };
+                for (int k = 0;; ++k) {
+                    ok = ok && gdn::mbar_wait_bounded(&s.w_full[k % kQueue], k / kQueue & 1, a.wait_ns);
+                    if (!ok || s.work[k % kQueue].x < 0) break;
+                    const Span sp = s.work[k % kQueue].sp;
+                    const int nt = sp.tiles, n0 = sp.ns[0], n1 = sp.ns[1];
+                    ok = gdn::mbar_wait_bounded(&s.q_full, k & 1, a.wait_ns);
+                    if (!ok) break;
+                    if constexpr (kStages == 2) {
+                        // a tile's outputs, and the next one's scores where its weights lay
+                        Slots<D> kt = at;
+                        at.next();
+                        if (!landed(kt)) break;
+                        tc::fence_after();
+                        if (n0 > 0) scores(0, 0, kt);
+                        if (n1 > 0) scores(1, 1, kt);
+                        free_group();
+                        if (nt == 1) tc::commit(&s.q_free);
+                        const int whole = min(min(n0, n1) - 1, sp.right - sp.tile0);
+#pragma unroll 1
+                        for (int j = 0; j < nt; ++j) {
+                            kt = at;
+                            if (j + 1 < nt) at.next();
+                            const Slots<D> vt = at;
+                            at.next();
+                            if (j > 0 && j < whole && sp.tile0 + j >= sp.left) {
+                                // both query tiles, every position
+                                if (!landed(kt) || !landed(vt) || !weights_of(0, g0 + j)) break;
+                                outputs(0, 0, vt, true);
+                                scores(0, 0, kt);
+                                if (!weights_of(1, g1 + j)) break;
+                                outputs(1, 1, vt, true);
+                                scores(1, 1, kt);
+                            } else {
+                                const bool cut = masked(sp, sp.tile0 + j);
+                                const int2 e = cut ? steps_of(sp, sp.tile0 + j) : make_int2(0, kTile / 16);
+                                if (j + 1 < nt) landed(kt);
+                                if (!landed(vt)) break;
+                                if (cut) {
+                                    ok = gdn::mbar_wait_bounded(&s.v_ok[guarded % kAhead], guarded / kAhead & 1, a.wait_ns);
+                                    ++guarded;
+                                }
+#pragma unroll 1
+                                for (int st = 0; st < 2; ++st) {
+                                    const int n = st ? n1 : n0;
+                                    if (j < n) {
+                                        if (!weights_of(st, (st ? g1 : g0) + j)) break;
+                                        outputs_cut(st, st, vt, j > 0, e);
+                                        if (j + 1 == n) tc::commit(&s.o_done[st]);
+                                    }
+                                    if (j + 1 < n) scores(st, st, kt);
+                                }
+                                if (!ok) break;
+                            }
+                            free_group();
+                            if (j + 2 == nt) tc::commit(&s.q_free);
+                        }
+                        g0 += n0;
+                        g1 += n1;
+                    } else {
+                        // a tile's outputs, and the scores of the next but one where its weights lay
+#pragma unroll 1
+                        for (int j = -2; j < nt; ++j) {
+                            const int y = g0 + j;
+                            if (j >= 0) {
+                                const Slots<D> vt = at;
+                                at.next();
+                                const bool cut = masked(sp, sp.tile0 + j);
+                                if (!landed(vt)) break;
+                                if (cut) {
+                                    ok = gdn::mbar_wait_bounded(&s.v_ok[guarded % kAhead], guarded / kAhead & 1,
+                                                                a.wait_ns);
+                                    ++guarded;
+                                }
+                                if (!weights_of(y & 1, y >> 1)) break;
+                                if (cut)
+                                    outputs_cut(0, y & 1, vt, j > 0, steps_of(sp, sp.tile0 + j));
+                                else
+                                    outputs(0, y & 1, vt, j > 0);
+                                tc::commit(&s.o_done[y & 1]);
+                                free_group();
+                            }
+                            if (j + 2 < nt) {
+                                const Slots<D> kt = at;
+                                at.next();
+                                if (!landed(kt)) break;
+                                scores(0, y & 1, kt);
+                                free_group();
+                                if (j + 3 == nt) tc::commit(&s.q_free);
+                            }
+                        }
+                        g0 += nt;
+                    }
+                    if (!ok) break;
+                    arrive(&s.w_free[k % kQueue]);
+                }
+                if (!ok && !stop) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+                // no product reads shared memory after the CTA has left
+                tc::commit(&s.drain);
+                (void)gdn::mbar_wait_bounded(&s.drain, 0, a.wait_ns);
+            }
+            __syncwarp();
+        } else if (warp == kFindWarp) {
+            // ---- units: this block's own, then those of blocks that have not started
+            int x = blockIdx.x, part = blockIdx.y, asked = 0, k = 0;
+            bool more = ok;
+            while (more) {
+                Work w;
+                const bool found = find_unit<D>(a, s, x, part, int(total), w);
+                if (!found && part == 0 && a.info && lane == 0) a.info[x].parts = 0;
+                if (found) {
+                    if (k >= kQueue)
+                        ok = gdn::mbar_wait_bounded(&s.w_free[k % kQueue], (k / kQueue - 1) & 1, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && lane == 0) {
+                        s.fix[k % kQueue] = s.bad[k % kQueue] = 0;
+                        s.work[k % kQueue] = w;
+                        arrive(&s.w_full[k % kQueue]);
+                    }
+                    // the next one is taken over when this one ends, not before: others may be free earlier
+                    ok = ok && gdn::mbar_wait_bounded(&s.near, k & 1, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++k;
+                }
+                if (!ok) break;
+                if (lane == 0) ask_next(&s.next, &s.got);
+                const bool here = gdn::mbar_wait_bounded(&s.got, asked & 1, a.wait_ns);
+                ok = __all_sync(0xffffffffu, here);
+                ++asked;
+                if (!ok) break;
+                more = next_of(&s.next, x, part);
+                // the answer is read before the next one is written
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            if (ok) {
+                if (k >= kQueue) ok = gdn::mbar_wait_bounded(&s.w_free[k % kQueue], (k / kQueue - 1) & 1, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && lane == 0) {
+                    s.work[k % kQueue].x = -1;
+                    arrive(&s.w_full[k % kQueue]);
+                }
             }
         } else {
-            if (ok) {
-                scores(0, 0, 0);
-                free_tile(k_pos(0));
-            }
-            if (nt > 1 && ok) {
-                wait_tile(k_pos(1));
-                if (ok) {
-                    scores(0, 1, 1);
-                    free_tile(k_pos(1));
-                }
-            }
-            for (int j = 0; j < nt && ok; ++j) {
-                wait_values(j);
-                if (ok) wait_weights(j & 1, j >> 1);
-                if (!ok) break;
-                outputs(0, j & 1, j);
-                free_tile(v_pos(j, nt));
-                if (j + 2 < nt) {
-                    wait_tile(k_pos(j + 2));
-                    if (!ok) break;
-                    scores(0, j & 1, j + 2);
-                    free_tile(k_pos(j + 2));
-                }
-            }
-        }
-        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
-        // no product reads shared memory after the CTA has left
-        if (leader) tc::commit(&s.drain);
-        __syncwarp();
-        (void)gdn::mbar_wait_bounded(&s.drain, 0, a.wait_ns);
-    } else {
-        // ---- guards: a zero weight times what is not finite is not zero, so such values go out of masked tiles
-        const int me = tid - kGuard * 32;
-        bool ok = true;
-        if (a.table) {
-            const int T = 1 << a.page_shift;
-            const int first = (a.window ? max(0, u.len + 1 - a.window) : 0) >> a.page_shift;
-            const int last = u.len > 0 ? (u.len + T - 1) >> a.page_shift : 0;
-            bool bad = false;
-            for (int i = first + me; i < last; i += 64) {
-                const int p = a.table[int64_t(u.r) * a.table_stride + i];
-                bad |= p < 0 || p >= a.num_pages;
-            }
-            if (bad) *reinterpret_cast<volatile int *>(&s.bad) = 1;
-        }
-        __syncwarp();
-        if (lane == 0) arrive(&s.pages);
-        int seen = 0;
-        for (int j = 0; j < nt && ok; ++j) {
-            if (!masked(a, u, kStages, sp.tile0 + j)) continue;
-            // (a copy under way: its barrier is in that copy's phase, not in an earlier one of the same parity)
-            ok = gdn::mbar_wait_bounded(&s.v_sent[seen % kAhead], seen / kAhead & 1, a.wait_ns);
-            bool any = false;
-            for (int x = 0; x < C::kPieces && ok; ++x) {
-                const int pos = v_pos(j, nt) * C::kPieces + x, slot = pos % C::kSlots;
-                ok = gdn::mbar_wait_bounded(&s.full[slot], (pos / C::kSlots) & 1, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot);
-#pragma unroll 4
-                for (int i = me; i < C::kSlot / 16; i += 64) {
-                    uint4 w = p[i];
-                    const uint32_t t = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-                    if (max(t >> 16, t & 0xffffu) >= 0x7f80u) {
-                        w.x &= __vcmpltu2(w.x & 0x7fff7fffu, 0x7f807f80u);
-                        w.y &= __vcmpltu2(w.y & 0x7fff7fffu, 0x7f807f80u);
-                        w.z &= __vcmpltu2(w.z & 0x7fff7fffu, 0x7f807f80u);
-                        w.w &= __vcmpltu2(w.w & 0x7fff7fffu, 0x7f807f80u);
-                        p[i] = w;
-                        any = true;
+            // ---- guards: a zero weight times what is not finite is not zero, so such values go out of masked tiles
+            const int me = tid - kGuardWarp * 32;
+            int ring = 0, seen = 0;
+            for (int k = 0; take(k); ++k) {
+                const Work w = s.work[k % kQueue];
+                const int nt = w.sp.tiles;
+                if (a.table) {
+                    const int T = 1 << a.page_shift;
+                    const int first = (a.window ? max(0, w.u.len + 1 - a.window) : 0) >> a.page_shift;
+                    const int last = w.u.len > 0 ? (w.u.len + T - 1) >> a.page_shift : 0;
+                    bool bad = false;
+                    for (int i = first + me; i < last; i += 32 * C::kGuards) {
+                        const int p = a.table[int64_t(w.u.r) * a.table_stride + i];
+                        bad |= p < 0 || p >= a.num_pages;
                     }
+                    if (bad) *reinterpret_cast<volatile int *>(&s.bad[k % kQueue]) = 1;
                 }
+                __syncwarp();
+                if (lane == 0) arrive(&s.pages[k % kQueue]);
+                for (int j = 0; j < nt && ok; ++j) {
+                    if (!masked(w.sp, w.sp.tile0 + j)) continue;
+                    // (a copy under way: its barrier is in that copy's phase, not in an earlier one of the same parity)
+                    if (!wait(&s.v_sent[seen % kAhead], seen / kAhead)) break;
+                    bool any = false;
+                    for (int y = 0; y < C::kPieces && ok; ++y) {
+                        const int pos = (ring + v_pos(j, nt)) * C::kPieces + y, slot = pos % C::kSlots;
+                        if (!wait(&s.full[slot], pos / C::kSlots)) break;
+                        uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot);
+                        // rows of a block of 64 channels: those before `full` and from `all` on, a lane a row
+                        const int base = (w.sp.tile0 + j) * kTile;
+                        const int2 e = steps_of(w.sp, w.sp.tile0 + j);
+                        const int r0 = 16 * e.x, r1 = min(max(w.sp.full - base, r0), 16 * e.y);
+                        const int r2 = min(max(w.sp.all - base, r1), 16 * e.y), r3 = 16 * e.y;
+                        const int rows = r1 - r0 + r3 - r2;
+#pragma unroll 1
+                        for (int i = me; i < rows * (C::kPiece / 64); i += 32 * C::kGuards) {
+                            const int blk = i >= rows, in = i - blk * rows;
+                            const int row = in < r1 - r0 ? r0 + in : r2 - (r1 - r0) + in;
+                            uint4 *at = p + (blk * kTile + row) * 8, v[8];
+                            uint32_t t = 0;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                v[c] = at[(c + lane) & 7];  // (lanes on different banks)
+                                t = __vmaxu2(t, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                                         __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+                            }
+                            if (max(t >> 16, t & 0xffffu) < 0x7f80u) continue;
+                            any = true;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint4 x = at[c];
+                                x.x &= __vcmpltu2(x.x & 0x7fff7fffu, 0x7f807f80u);
+                                x.y &= __vcmpltu2(x.y & 0x7fff7fffu, 0x7f807f80u);
+                                x.z &= __vcmpltu2(x.z & 0x7fff7fffu, 0x7f807f80u);
+                                x.w &= __vcmpltu2(x.w & 0x7fff7fffu, 0x7f807f80u);
+                                at[c] = x;
+                            }
+                        }
+                    }
+                    if (any) *reinterpret_cast<volatile int *>(&s.fix[k % kQueue]) = 1;
+                    gdn::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0) arrive(&s.v_ok[seen % kAhead]);
+                    ++seen;
+                }
+                if (!ok) break;
+                ring += 2 * nt;
+                done(k);
             }
-            if (any) *reinterpret_cast<volatile int *>(&s.fix) = 1;
-            gdn::fence_proxy_async_smem();
-            __syncwarp();
-            if (ok && lane == 0) arrive(&s.v_ok[seen % kAhead]);
-            ++seen;
         }
-        if (!ok) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
+        if (!ok && !stop) gdn::set_status(a.status, GDN_DEV_TIMEOUT);
     }
+    tc::fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
-    }
-    if (tid == 0 && part == 0 && a.info) {
-        Info f = {};
-        f.t0 = u.t0;
-        f.tok0 = u.tok0;
-        f.n = u.n;
-        f.hk = hk;
-        f.parts = u.parts > 1 && !s.bad ? u.parts : 0;
-        a.info[blockIdx.x] = f;
     }
 }
 
@@ -660,11 +997,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 
 // ---- the workspace's keys and values: cached positions as bf16 (exactly: 4 bits times a power of two), then the new rows
 
-constexpr int kGatherRows = 32, kGatherThreads = 256;
+constexpr int kGatherRows = 128, kGatherThreads = 256;  // rows of a CTA at most
 
 struct GatherArgs {
     kv8_cache c;
-    int32_t layer, page_shift;
+    int32_t layer, page_shift, rows;  // rows of a CTA, a power of two
     prompt::Requests rq;
     const int32_t *table;
     int64_t table_stride;
@@ -684,52 +1021,62 @@ __device__ __forceinline__ uint32_t bf16x2_scaled(uint16_t codes, float f) {
 __global__ void __launch_bounds__(kGatherThreads) kv8_gather_kernel(const __grid_constant__ GatherArgs a) {
     gdn::pdl_enter();
     __shared__ prompt::Scan<kGatherThreads> scan;
-    __shared__ int page[kGatherRows], pos[kGatherRows];  // page >= 0: a cached position; -1: new row pos; -2: nothing
+    // of each row: its request and position; then a page (-1: a new row, -2: nothing, -3: zeros) and the place in it or
+    // the row
+    __shared__ int who[kGatherRows], place[kGatherRows];
     const int tid = threadIdx.x;
-    const int64_t w0 = int64_t(blockIdx.x) * kGatherRows;
-    if (tid < kGatherRows) page[tid] = -2;
+    const int64_t w0 = int64_t(blockIdx.x) * a.rows;
+    for (int i = tid; i < a.rows; i += kGatherThreads) who[i] = -2;
     {
-        const int chunk = (a.rq.B + kGatherThreads - 1) / kGatherThreads, r0 = tid * chunk, r1 = min(a.rq.B, r0 + chunk);
-        long long rows = 0, kv = 0, all, kv_all;
+        const int chunk = (a.rq.B + kGatherThreads - 1) / kGatherThreads, r0 = min(a.rq.B, tid * chunk),
+                  r1 = min(a.rq.B, r0 + chunk);
+        long long none = 0, kv = 0, none_all, kv_all;
         for (int r = r0; r < r1; ++r) kv += prompt::kv_rows_of(prompt::request_of(a.rq, r));
         const long long mine = kv;
-        prompt::scan2<kGatherThreads>(scan, rows, kv, all, kv_all);
-        if (kv < w0 + kGatherRows && kv + mine > w0)
+        prompt::scan2<kGatherThreads>(scan, none, kv, none_all, kv_all);
+        // what the last tile reads behind the last request is in masked places, but had better not be NaN there
+        if (tid < a.rows && w0 + tid >= kv_all && w0 + tid < min(kv_all + kTile, (long long)a.rq.kv_capacity))
+            who[tid] = -3;
+        if (kv < w0 + a.rows && kv + mine > w0)
             for (int r = r0; r < r1; ++r) {
-                const prompt::Request q = prompt::request_of(a.rq, r);
-                const long long n = prompt::kv_rows_of(q);
-                const bool fits = kv + n <= a.rq.kv_capacity;
-                const int lo = a.c.window ? max(0, q.len + 1 - a.c.window) : 0;
-                if (!fits && n && kv < w0 + kGatherRows && kv + n > w0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
-                for (long long w = max((long long)w0, kv); fits && w < min((long long)w0 + kGatherRows, kv + n); ++w) {
-                    const int t = int(w - kv);
-                    int p = -1, at = q.t0 + t - q.len;
-                    if (t < q.len) {
-                        at = t;
-                        p = -2;
-                        if (t >= lo) {
-                            p = a.table[int64_t(r) * a.table_stride + (t >> a.page_shift)];
-                            if (p < 0 || p >= a.c.num_pages) {
-                                gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
-                                p = -2;
-                            }
-                        }
+                const long long n = prompt::kv_rows_of(prompt::request_of(a.rq, r));
+                const long long from = max((long long)w0, kv), to = min((long long)w0 + a.rows, kv + n);
+                if (from < to && kv + n > a.rq.kv_capacity)
+                    gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
+                else
+                    for (long long w = from; w < to; ++w) {
+                        who[w - w0] = r;
+                        place[w - w0] = int(w - kv);
                     }
-                    page[w - w0] = p;
-                    pos[w - w0] = at;
-                }
                 kv += n;
             }
     }
     __syncthreads();
+    if (tid < a.rows && who[tid] >= 0) {
+        const int r = who[tid], t = place[tid];
+        const prompt::Request q = prompt::request_of(a.rq, r);
+        if (t >= q.len) {
+            who[tid] = -1;
+            place[tid] = q.t0 + t - q.len;
+        } else if (a.c.window && t <= q.len - a.c.window) {
+            // nobody sees it; but a tile reads it, this request's first or the last one of the request before
+            who[tid] = t / kTile == (q.len + 1 - a.c.window) / kTile || t < kTile ? -3 : -2;
+        } else {
+            const int p = a.table[int64_t(r) * a.table_stride + (t >> a.page_shift)];
+            const bool bad = p < 0 || p >= a.c.num_pages;
+            if (bad) gdn::set_status(a.status, GDN_DEV_PAGE_OOR);
+            who[tid] = bad ? -3 : p;
+        }
+    }
+    __syncthreads();
     const int d = a.c.d, h_kv = a.c.h_kv, T = a.c.page_tokens;
     const int per = d / 16, shift = 31 - __clz(per);  // pieces of 16 channels a row
-    const int items = 2 * h_kv * kGatherRows * per;
+    const int row_shift = 31 - __clz(a.rows), items = 2 * h_kv * a.rows * per;
 #pragma unroll 4
     for (int i = tid; i < items; i += kGatherThreads) {
-        const int ch = (i & (per - 1)) * 16, w = (i >> shift) % kGatherRows, hv = (i >> shift) / kGatherRows;
+        const int ch = (i & (per - 1)) * 16, w = (i >> shift) & (a.rows - 1), hv = i >> (shift + row_shift);
         const int is_v = hv >= h_kv, h = hv - is_v * h_kv;
-        const int p = page[w], at = pos[w];
+        const int p = who[w], at = place[w];
         if (p == -2) continue;
         uint4 lo, hi;
         if (p >= 0) {
@@ -742,6 +1089,8 @@ __global__ void __launch_bounds__(kGatherThreads) kv8_gather_kernel(const __grid
                             bf16x2_scaled(uint16_t(x.y), f), bf16x2_scaled(uint16_t(x.y >> 16), f));
             hi = make_uint4(bf16x2_scaled(uint16_t(x.z), f), bf16x2_scaled(uint16_t(x.z >> 16), f),
                             bf16x2_scaled(uint16_t(x.w), f), bf16x2_scaled(uint16_t(x.w >> 16), f));
+        } else if (p == -3) {
+            lo = hi = make_uint4(0, 0, 0, 0);
         } else {
             const uint4 *x = reinterpret_cast<const uint4 *>((is_v ? a.v + at * a.v_stride : a.k + at * a.k_stride) +
                                                              int64_t(h) * d + ch);
@@ -785,10 +1134,22 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     int64_t seen = int64_t(max_len) + max_rows;
     if (window && window + per_unit < seen) seen = window + per_unit + kTile;
     const int64_t tiles = (seen + kTile - 1) / kTile;
-    // work is cut where it leaves SMs idle: every unit into as many parts as make one CTA an SM
-    int64_t s = p.units >= kSms || p.units == 0 ? 1 : kSms / p.units;
-    if (s > tiles / kLeast) s = tiles / kLeast;
-    p.splits = int(s < 1 ? 1 : s > kMostParts ? kMostParts : s);
+    // Work is cut where SMs would idle.  With `s` parts a unit the longest takes tiles / s, and all of them take the SMs'
+    // share of the whole, in full waves where all are about as long; a part's ends cost as much as kEnds tiles, and the
+    // join of the parts as much again.
+    const double avg = window ? double(tiles) : (double(max_len) + 0.5 * max_rows) / kTile + 1.0;
+    int64_t s = 1;
+    double best = 0.0;
+    for (int64_t i = 1; p.units && i <= kMostParts && (i == 1 || i <= tiles / kLeast); ++i) {
+        const double share = double(p.units) * i / kSms, waves = avg > 0.75 * tiles ? ceil(share) : share;
+        const double all = waves * (avg / i + kEnds), longest = double(tiles) / i + kEnds;
+        const double cost = ((all > longest ? all : longest) + (i > 1 ? kEnds : 0.0)) * (i > 1 ? 1.1 : 1.0);
+        if (i == 1 || cost < best) {
+            best = cost;
+            s = i;
+        }
+    }
+    p.splits = int(s);
     return p;
 }
 size_t part_bytes(const Plan &p, int d) {
@@ -799,6 +1160,10 @@ size_t kv_bytes(const kv8_cache *c, int64_t rows) { return size_t(rows) * c->h_k
 template <int D>
 int launch(const Args &a, const Plan &p, cudaStream_t st) {
     using C = Cfg<D>;
+    // what its warps take from one another is shared out of this many registers
+    cudaFuncAttributes have;
+    if (cudaFuncGetAttributes(&have, prompt_attend_kernel<D>) != cudaSuccess || have.numRegs != C::kLaunchRegs)
+        return GDN_ERR_CUDA;
     // for every launch: the limit is the current device's
     if (cudaFuncSetAttribute(prompt_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
         cudaSuccess)
@@ -973,7 +1338,8 @@ extern "C" int kv8_chunk(const kv8_cache *cache, int32_t layer, int32_t B, int32
     g.out = dense;
     g.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int rc = gdn_host::launch_pdl(kv8_gather_kernel, dim3(unsigned((rows + kGatherRows - 1) / kGatherRows)),
+    g.rows = rows >= 6 * kSms * kGatherRows ? kGatherRows : rows >= 6 * kSms * 32 ? 32 : 8;
+    const int rc = gdn_host::launch_pdl(kv8_gather_kernel, dim3(unsigned((rows + g.rows - 1) / g.rows)),
                                         dim3(kGatherThreads), 0, st, g);
     if (rc != GDN_OK) return rc;
     a.rq = g.rq;
