@@ -67,7 +67,7 @@ struct Cfg {
     static constexpr int kGuards = kStages == 2 ? 1 : 5;  // warps that look through values
     static constexpr int kThreads = 32 * (kSoftWarps + 3 + kGuards);
     // Registers a thread: of the 168 that 384 threads may have, the softmax's rows take more, the other warps fewer.
-    static constexpr int kLaunchRegs = 168, kSoftRegs = kStages == 2 ? 208 : 232, kOtherRegs = kStages == 2 ? 88 : 136;
+    static constexpr int kLaunchRegs = 168, kSoftRegs = kStages == 2 ? 200 : 232, kOtherRegs = kStages == 2 ? 104 : 136;
     static_assert(kThreads == 384 && 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <=
                                          kThreads * kLaunchRegs,
                   "more registers than a launch has: the wait for them would not end");
@@ -98,7 +98,7 @@ template <int D>
 struct Shared {
     using C = Cfg<D>;
     uint64_t full[C::kSlots], freed[kGroups], s_full[2], o_done[2], q_full, q_free, drain;  // one arrival
-    uint64_t p_ready[2];                      // of four warps
+    uint64_t p_ready[4];                      // halves of a tile's weights, of four warps
     uint64_t v_sent[kAhead];                  // masked tiles in turn: the copy of the values is under way ...
     uint64_t v_ok[kAhead];                    // ... and looked through
     uint64_t w_full[kQueue], w_free[kQueue];  // a unit is announced; everybody is done with it
@@ -303,12 +303,31 @@ __device__ __forceinline__ void hide(uint32_t t_s, int hi, int lo) {
     }
     tc::st_wait();
 }
-__device__ __forceinline__ float top_of(const uint32_t (&x)[kTile]) {
+constexpr int kHalf = kTile / 2;
+__device__ __forceinline__ void load_half(uint32_t t_s, uint32_t (&x)[kHalf]) {
+#pragma unroll
+    for (int i = 0; i < kHalf; i += 32) tc::ld32_async(t_s + i, x + i);
+}
+__device__ __forceinline__ float top_of(const uint32_t (&x)[kHalf]) {
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < kTile / 2; ++i)
+    for (int i = 0; i < kHalf / 2; ++i)
         top[i & 3] = max3(top[i & 3], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
     return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+}
+// The weights 2^(c x + r) as bf16 pairs; returns their sum before that rounding.
+__device__ __forceinline__ float weights(const uint32_t (&x)[kHalf], f2 c2, float r, uint32_t (&p)[kHalf / 2]) {
+    const f2 r2 = pair(r, r);
+    f2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < kHalf / 2; ++c) {
+        const float2 e = both(fma2(pair(x[2 * c], x[2 * c + 1]), c2, r2));
+        const float e0 = ex2(e.x), e1 = ex2(e.y);
+        sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[c]) : "f"(e1), "f"(e0));
+    }
+    const float2 t = both(add2(sum[0], sum[1]));
+    return t.x + t.y;
 }
 // Four lanes' pieces of four rows, transposed: v[i] becomes lane i's (of the four) piece of this lane's number.
 __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
@@ -352,8 +371,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s.s_full + i, 1);
             gdn::mbar_init(s.o_done + i, 1);
-            gdn::mbar_init(s.p_ready + i, 4);
         }
+        for (int i = 0; i < 4; ++i) gdn::mbar_init(s.p_ready + i, 4);
         gdn::mbar_init(&s.q_full, 1);
         gdn::mbar_init(&s.q_free, 1);
         gdn::mbar_init(&s.drain, 1);
@@ -439,14 +458,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     const int hi = w.u.len + position() - (w.sp.tile0 + j) * kTile;
                     hide(t_s, hi, a.window ? hi - a.window : -1);
                 }
-                uint32_t x[kTile];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tc::ld32_async(t_s + 32 * i, x + 32 * i);
+                uint32_t x[2][kHalf];
+                load_half(t_s, x[0]);
+                load_half(t_s + kHalf, x[1]);
                 tc::ld_wait();
-                arrived(x);
-                const float z = top_of(x) * a.scale_log2;
+                arrived(x[0]);
+                arrived(x[1]);
+                const float z = fmaxf(top_of(x[0]), top_of(x[1])) * a.scale_log2;
                 if (__any_sync(0xffffffffu, z > m + kSlack)) {
-                    const float now = fmaxf(m, z), f = ex2(m - (now == -INFINITY ? 0.f : now));
+                    const float now = fmaxf(m, z), f = m == now ? 1.f : ex2(m - now);  // (-inf less -inf is no number)
                     if (j > 0) {
                         // (with two query tiles the scores are behind the products before)
                         if (kStages == 1 && !wait(&s.o_done[(g - 1) & 1], (g - 1) >> 1)) break;
@@ -465,27 +485,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     l *= f;
                     m = now;
                 }
-                const float ref = m == -INFINITY ? 0.f : -m;
-                const f2 r2 = pair(ref, ref);
-                f2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+                // The products with the first half's weights run beside the second half's exponentials.
+                const float r = m == -INFINITY ? 0.f : -m;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float2 e = both(fma2(pair(x[32 * i + 2 * c], x[32 * i + 2 * c + 1]), c2, r2));
-                        const float e0 = ex2(e.x), e1 = ex2(e.y);
-                        sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[c]) : "f"(e1), "f"(e0));
-                    }
-                    tc::st16_async(t_s + 16 * i, p);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[kHalf / 2];
+                    l += weights(x[half], c2, r, p);
+                    tc::st32_async(t_s + half * (kHalf / 2), p);
+                    tc::st_wait();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.p_ready[2 * slot + half]);
                 }
-                const float2 t = both(add2(sum[0], sum[1]));
-                l += t.x + t.y;
-                tc::st_wait();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(&s.p_ready[slot]);
             }
             if (!ok) break;
             if (!wait(&s.pages[k % kQueue], k / kQueue)) break;
@@ -683,16 +694,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     tc::commit(&s.s_full[slot]);
                 };
                 // (the softmax warps give a unit's first weights after they have read the last unit's sums)
-                auto outputs = [&](int st, int slot, const Slots<D> &x, bool more) {
+                auto outputs = [&](int st, int slot, const Slots<D> &x, bool more, int turn) {
 #pragma unroll
-                    for (int y = 0; y < C::kPieces; ++y) {
-                        const uint64_t d = tc::desc_at(dv, x.slot[y] * C::kSlot);
-                        const uint32_t to = tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece;
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && gdn::mbar_wait_bounded(&s.p_ready[2 * slot + half], turn & 1, a.wait_ns);
+                        if (!ok) return false;
+                        tc::fence_after();
 #pragma unroll
-                        for (int i = 0; i < kTile / 16; ++i)
-                            tc::mma_bf16_ts(to, tm + slot * kTile + i * 8, tc::desc_at(d, i * 2048), id_p,
-                                            more || i > 0);
+                        for (int y = 0; y < C::kPieces; ++y) {
+                            const uint64_t d = tc::desc_at(dv, x.slot[y] * C::kSlot);
+                            const uint32_t to = tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece;
+#pragma unroll
+                            for (int i = half * kHalf / 16; i < (half + 1) * kHalf / 16; ++i)
+                                tc::mma_bf16_ts(to, tm + slot * kTile + i * 8, tc::desc_at(d, i * 2048), id_p,
+                                                more || i > 0);
+                        }
                     }
+                    return true;
                 };
                 // The same over the positions that some row sees.
                 auto outputs_cut = [&](int st, int slot, const Slots<D> &x, bool more, int2 e) {
@@ -709,7 +727,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     ++groups;
                 };
                 auto weights_of = [&](int slot, int turn) {
-                    ok = ok && gdn::mbar_wait_bounded(&s.p_ready[slot], turn & 1, a.wait_ns);
+                    for (int half = 0; half < 2; ++half)
+                        ok = ok && gdn::mbar_wait_bounded(&s.p_ready[2 * slot + half], turn & 1, a.wait_ns);
                     tc::fence_after();
                     return ok;
                 };
@@ -739,11 +758,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                             at.next();
                             if (j > 0 && j < whole && sp.tile0 + j >= sp.left) {
                                 // both query tiles, every position
-                                if (!landed(kt) || !landed(vt) || !weights_of(0, g0 + j)) break;
-                                outputs(0, 0, vt, true);
+                                if (!landed(kt) || !landed(vt)) break;
+                                if (!outputs(0, 0, vt, true, g0 + j)) break;
                                 scores(0, 0, kt);
-                                if (!weights_of(1, g1 + j)) break;
-                                outputs(1, 1, vt, true);
+                                if (!outputs(1, 1, vt, true, g1 + j)) break;
                                 scores(1, 1, kt);
                             } else {
                                 const bool cut = masked(sp, sp.tile0 + j);
@@ -786,11 +804,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                                                                 a.wait_ns);
                                     ++guarded;
                                 }
-                                if (!weights_of(y & 1, y >> 1)) break;
-                                if (cut)
+                                if (!cut) {
+                                    if (!outputs(0, y & 1, vt, j > 0, y >> 1)) break;
+                                } else {
+                                    if (!weights_of(y & 1, y >> 1)) break;
                                     outputs_cut(0, y & 1, vt, j > 0, steps_of(sp, sp.tile0 + j));
-                                else
-                                    outputs(0, y & 1, vt, j > 0);
+                                }
                                 tc::commit(&s.o_done[y & 1]);
                                 free_group();
                             }
