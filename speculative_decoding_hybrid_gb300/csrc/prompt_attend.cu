@@ -110,6 +110,7 @@ struct Shared {
     int holds[C::kSlots];                     // the group of loads that a slot's is in
     prompt::Scan<C::kThreads> scan;
     int blocks[kChunks], kv[kChunks];         // before each part of the list of requests
+    uint8_t order[kChunks];                   // where a part is one request: the one with the longest rows first
     uint32_t tmem;
 };
 
@@ -230,8 +231,10 @@ __device__ __forceinline__ bool find_unit(const Args &a, const Shared<D> &s, int
 #pragma unroll
     for (int e = 0; e < kChunks / 32; ++e) i += __popc(__ballot_sync(0xffffffffu, s.blocks[e * 32 + lane] <= rank));
     --i;
-    const int chunk = (a.rq.B + kChunks - 1) / kChunks, r1 = min(a.rq.B, (i + 1) * chunk);
+    const int chunk = (a.rq.B + kChunks - 1) / kChunks;
     int blocks = s.blocks[i];
+    if (chunk == 1) i = s.order[i];
+    const int r1 = min(a.rq.B, (i + 1) * chunk);
     int64_t kv = s.kv[i];
     Unit &u = w.u;
     for (int r0 = i * chunk; r0 < r1; r0 += 32) {
@@ -284,29 +287,22 @@ __device__ __forceinline__ void arrived(uint32_t (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(x[i]));
 }
-// Positions past hi and up to lo of a tile are not seen: their scores become -inf where they lie (a loop of little code;
-// for few tiles).
-__device__ __forceinline__ void hide(uint32_t t_s, int hi, int lo) {
-#pragma unroll 1
-    for (int i = 0; i < kTile; i += 32) {
-        const int h = hi - i, b = lo - i;
-        const uint32_t up = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
-        const uint32_t see = b < 0 ? up : b >= 31 ? 0u : up & ~((2u << b) - 1u);
-        if (__all_sync(0xffffffffu, see == ~0u)) continue;
-        uint32_t x[32];
-        tc::ld32_async(t_s + i, x);
-        tc::ld_wait();
-        arrived(x);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = see & (1u << c) ? x[c] : 0xff800000u;
-        tc::st32_async(t_s + i, x);
-    }
-    tc::st_wait();
-}
 constexpr int kHalf = kTile / 2;
 __device__ __forceinline__ void load_half(uint32_t t_s, uint32_t (&x)[kHalf]) {
 #pragma unroll
     for (int i = 0; i < kHalf; i += 32) tc::ld32_async(t_s + i, x + i);
+}
+// Positions past hi and up to lo (from the half's first) are not seen.
+__device__ __forceinline__ void hide(uint32_t (&x)[kHalf], int hi, int lo) {
+#pragma unroll
+    for (int i = 0; i < kHalf / 32; ++i) {
+        const int h = hi - 32 * i, b = lo - 32 * i;
+        const uint32_t up = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+        const uint32_t see = b < 0 ? up : b >= 31 ? 0u : up & ~((2u << b) - 1u);
+        if (__all_sync(0xffffffffu, see == ~0u)) continue;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[32 * i + c] = see & (1u << c) ? x[32 * i + c] : 0xff800000u;
+    }
 }
 __device__ __forceinline__ float top_of(const uint32_t (&x)[kHalf]) {
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -398,11 +394,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     {
         const int chunk = (a.rq.B + kChunks - 1) / kChunks, r0 = min(a.rq.B, tid * chunk), r1 = min(a.rq.B, r0 + chunk);
         long long blocks = 0, kv = 0, kv_all;
+        prompt::Request q{};
         for (int r = r0; r < r1; ++r) {
-            const prompt::Request q = prompt::request_of(a.rq, r);
+            q = prompt::request_of(a.rq, r);
             if (q.bad && blockIdx.x == 0 && blockIdx.y == 0) gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
             blocks += (q.n + per_unit - 1) / per_unit;
             kv += prompt::kv_rows_of(q);
+        }
+        if (chunk == 1 && a.rq.B > 1) {
+            // long units started last would run alone (8 prompts of 512..12,000 rows: 1,070 us in the order given)
+            if (tid < kChunks) s.kv[tid] = q.n ? q.len + q.n : 0;
+            __syncthreads();
+            if (tid < a.rq.B) {
+                const int mine = s.kv[tid];
+                int at = 0;
+                for (int r = 0; r < a.rq.B; ++r) at += s.kv[r] > mine || (s.kv[r] == mine && r < tid);
+                s.order[at] = uint8_t(tid);
+                s.blocks[at] = int(blocks);
+            }
+            __syncthreads();
+            blocks = tid < a.rq.B ? s.blocks[tid] : 0;
+            __syncthreads();
+        } else if (tid < kChunks) {
+            s.order[tid] = uint8_t(tid);
         }
         prompt::scan2<C::kThreads>(s.scan, blocks, kv, total, kv_all);
         if (tid < kChunks) {
@@ -454,16 +468,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 if (!wait(&s.s_full[slot], turn)) break;
                 tc::fence_after();
                 const uint32_t t_s = tm + slot * kTile + lanes;
-                if (masked(w.sp, w.sp.tile0 + j)) {
-                    const int hi = w.u.len + position() - (w.sp.tile0 + j) * kTile;
-                    hide(t_s, hi, a.window ? hi - a.window : -1);
-                }
                 uint32_t x[2][kHalf];
                 load_half(t_s, x[0]);
                 load_half(t_s + kHalf, x[1]);
                 tc::ld_wait();
                 arrived(x[0]);
                 arrived(x[1]);
+                if (masked(w.sp, w.sp.tile0 + j)) {
+                    const int hi = w.u.len + position() - (w.sp.tile0 + j) * kTile, lo = a.window ? hi - a.window : -1;
+                    hide(x[0], hi, lo);
+                    hide(x[1], hi - kHalf, lo - kHalf);
+                }
                 const float z = fmaxf(top_of(x[0]), top_of(x[1])) * a.scale_log2;
                 if (__any_sync(0xffffffffu, z > m + kSlack)) {
                     const float now = fmaxf(m, z), f = m == now ? 1.f : ex2(m - now);  // (-inf less -inf is no number)
@@ -524,14 +539,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 }
             }
             const bool keep = n > 0 && l != 0.f;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t x[32];
-                if (n > 0) {
-                    tc::ld32_async(t_o + c, x);
-                    tc::ld_wait();
-                }
-                arrived(x);
+            const auto put = [&](int c, uint32_t (&x)[32]) {
                 if (!keep) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = 0;
@@ -579,6 +587,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                                                            16 * y) = v[i];
                     }
                 }
+            };
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t x[32];
+                if (n > 0) {
+                    tc::ld32_async(t_o + c, x);
+                    tc::ld_wait();
+                }
+                arrived(x);
+                put(c, x);
             }
             if (write && whole) {
                 if (a.lse)
@@ -1142,8 +1160,8 @@ struct Plan {
     int64_t units;
     int per_tile, splits, rows;
 };
-Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capacity, int32_t max_len,
-             int32_t max_rows) {
+Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capacity, int32_t max_len, int32_t max_rows,
+             int64_t total_len) {
     Plan p{};
     p.per_tile = kTile / (h_q / h_kv);
     p.rows = (d == 256 ? 1 : 2) * kTile;
@@ -1153,16 +1171,19 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     int64_t seen = int64_t(max_len) + max_rows;
     if (window && window + per_unit < seen) seen = window + per_unit + kTile;
     const int64_t tiles = (seen + kTile - 1) / kTile;
-    // Work is cut where SMs would idle.  With `s` parts a unit the longest takes tiles / s, and all of them take the SMs'
-    // share of the whole, in full waves where all are about as long; a part's ends cost as much as kEnds tiles, and the
-    // join of the parts as much again.
-    const double avg = window ? double(tiles) : (double(max_len) + 0.5 * max_rows) / kTile + 1.0;
+    // Work is cut where SMs would idle.  With i parts a unit they share the whole, and the last ones run on alone for
+    // most of the longest part; units about as long as one another run in full waves.  A part's ends cost as much as
+    // kEnds tiles, and the join as much again.
+    const double rows = double(row_capacity) / B;
+    const double mean = ((total_len < int64_t(B) * max_len ? double(total_len) / B : double(max_len)) + 0.5 * rows) / kTile + 1.0;
+    const double avg = mean < tiles ? mean : double(tiles);
     int64_t s = 1;
     double best = 0.0;
     for (int64_t i = 1; p.units && i <= kMostParts && (i == 1 || i <= tiles / kLeast); ++i) {
-        const double share = double(p.units) * i / kSms, waves = avg > 0.75 * tiles ? ceil(share) : share;
-        const double all = waves * (avg / i + kEnds), longest = double(tiles) / i + kEnds;
-        const double cost = ((all > longest ? all : longest) + (i > 1 ? kEnds : 0.0)) * (i > 1 ? 1.1 : 1.0);
+        const double share = double(p.units) * i / kSms, part = avg / i + kEnds, longest = double(tiles) / i + kEnds;
+        double cost = avg > 0.75 * tiles ? ceil(share) * part : share * part + 0.7 * longest;
+        if (cost < longest) cost = longest;
+        if (i > 1) cost = 1.05 * (cost + kEnds);
         if (i == 1 || cost < best) {
             best = cost;
             s = i;
@@ -1226,7 +1247,7 @@ constexpr int64_t kMostUnits = (int64_t(1) << 31) - 1;
 extern "C" size_t attn_prompts_workspace_bytes(const attn_dims *dims, int32_t B, int32_t row_capacity,
                                                int32_t max_rows) {
     if (check_dims(dims) != GDN_OK || B <= 0 || B > 65535 || row_capacity < 0 || max_rows <= 0) return 0;
-    return part_bytes(plan_of(dims->h_q, dims->h_kv, dims->d, dims->window, B, row_capacity, 0, max_rows), dims->d);
+    return part_bytes(plan_of(dims->h_q, dims->h_kv, dims->d, dims->window, B, row_capacity, 0, max_rows, 0), dims->d);
 }
 
 static int prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const int32_t *cu_rows, const gdn_bf16 *q,
@@ -1243,7 +1264,7 @@ static int prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const
         !gdn_host::kv8_rows_ok(v, v_stride, dims->h_kv, dims->d) ||
         !gdn_host::kv8_rows_ok(o, o_stride, dims->h_q, dims->d))
         return GDN_ERR_ARG;
-    const Plan p = plan_of(dims->h_q, dims->h_kv, dims->d, dims->window, B, row_capacity, 0, max_rows);
+    const Plan p = plan_of(dims->h_q, dims->h_kv, dims->d, dims->window, B, row_capacity, 0, max_rows, 0);
     const size_t need = part_bytes(p, dims->d);
     if (p.units > kMostUnits) return GDN_ERR_ARG;
     if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
@@ -1305,7 +1326,8 @@ extern "C" size_t kv8_chunk_workspace_bytes(const kv8_cache *cache, int32_t B, i
     const int64_t rows = kv_rows(B, row_capacity, max_len, total_len);
     if (rows >= gdn_host::kKv8MaxLen) return 0;
     return kv_bytes(cache, rows) +
-           part_bytes(plan_of(cache->h_q, cache->h_kv, cache->d, cache->window, B, row_capacity, max_len, max_rows),
+           part_bytes(plan_of(cache->h_q, cache->h_kv, cache->d, cache->window, B, row_capacity, max_len, max_rows,
+                              total_len),
                       cache->d);
 }
 
@@ -1329,7 +1351,8 @@ extern "C" int kv8_chunk(const kv8_cache *cache, int32_t layer, int32_t B, int32
         !gdn_host::kv8_rows_ok(o, o_stride, cache->h_q, cache->d))
         return GDN_ERR_ARG;
     const int64_t rows = kv_rows(B, row_capacity, max_len, total_len);
-    const Plan p = plan_of(cache->h_q, cache->h_kv, cache->d, cache->window, B, row_capacity, max_len, max_rows);
+    const Plan p = plan_of(cache->h_q, cache->h_kv, cache->d, cache->window, B, row_capacity, max_len, max_rows,
+                           total_len);
     // (row numbers of the workspace are the copy engine's 32-bit coordinates)
     if (rows >= gdn_host::kKv8MaxLen || p.units > kMostUnits) return GDN_ERR_ARG;
     const size_t need = kv_bytes(cache, rows) + part_bytes(p, cache->d);
