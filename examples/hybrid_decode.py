@@ -2,7 +2,8 @@
 
     python examples/hybrid_decode.py [--requests 4] [--prompt 300] [--steps 12] [--layers 3] [--attention 2]
 
-Requests share a system prompt: its keys and values are committed once and the other requests fork its pages.
+Requests share a system prompt: its rows are turned to their positions, attended to in chunks and committed once, and
+the other requests fork its pages.
 Every step is one transaction of K-draft verification: the planner grants drafts, the GatedDeltaNet layers verify
 into checkpoints, the attention layers read the paged 8-bit cache and the transaction's own rows, the drafts are
 accepted greedily, and the commit moves both kinds of state by the accepted rows.  Halfway one request leaves and
@@ -20,6 +21,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import gdnsynth as sy  # noqa: E402
 from speculative_decoding_hybrid_gb300 import binding as gs  # noqa: E402
 from speculative_decoding_hybrid_gb300.kvcache import PagedKv  # noqa: E402
+from speculative_decoding_hybrid_gb300.prefill import Rope, attend_prompts  # noqa: E402
 from speculative_decoding_hybrid_gb300.step import DecodeLoop, LayerRows, VerifyStep  # noqa: E402
 
 VOCAB = 512
@@ -42,6 +44,7 @@ class HybridDecode:
         # one status word for both kinds of layer: a timed-out wait in either stops the commits of both
         self.kv = PagedKv(attention_layers, pages, requests, max_tokens, h_q, h_kv, d, page_tokens, device=self.dev,
                           status=self.vs.status)
+        self.rope = Rope(d, d // 2, base=1e6, device=self.dev)
         self.drafted = self.accepted = 0
 
     def normal(self, *shape, scale=1.0):
@@ -54,19 +57,38 @@ class HybridDecode:
         q, k, v = qkv.split([kv.h_q * kv.d, kv.h_kv * kv.d, kv.h_kv * kv.d], 1)
         return q.unflatten(1, (kv.h_q, kv.d)), k.unflatten(1, (kv.h_kv, kv.d)), v.unflatten(1, (kv.h_kv, kv.d))
 
-    def prompt(self, request, tokens):
-        """A prompt's keys and values into every attention layer (the outputs of its rows come from a prefill kernel
-        of the caller's, or 16 rows at a time from attend)."""
-        self.kv.reserve([request], [tokens])
-        table, length = self.kv.upload([request])
-        cu = torch.tensor([0, tokens], dtype=torch.int32, device=self.dev)
-        rows = []
-        for layer in range(self.kv.kv.shape[1]):
-            _, k, v = self.attention_rows(tokens)
-            self.kv.append(layer, table, length, cu, k, v, max_rows=tokens)
-            rows.append((k, v))
-        self.kv.advance([request], [tokens])
-        return rows
+    def rotate(self, q, k, cu, length):
+        """Queries and keys turned to their positions, in place in the projection's rows."""
+        return self.rope.rotate(q, k, cu, length, self.kv.status, in_place=True)
+
+    def prefill(self, request, tokens, chunk=256):
+        """A prompt through every attention layer, `chunk` rows a transaction: the first ones attend to their own rows,
+        later ones to the cache and their own.  -> per chunk a list of the layers' (q, k, v, o)."""
+        kv, seen = self.kv, []
+        for at in range(0, tokens, chunk):
+            n, held = min(chunk, tokens - at), int(self.kv.length[request])
+            kv.reserve([request], [n])
+            table, length = kv.upload([request])
+            cu = torch.tensor([0, n], dtype=torch.int32, device=self.dev)
+            rows = []
+            for layer in range(kv.kv.shape[1]):
+                q, k, v = self.attention_rows(n)
+                self.rotate(q, k, cu, length)
+                if held == 0:
+                    o, _ = attend_prompts(q, k, v, cu, n, kv.status)
+                else:
+                    o, _ = kv.attend_chunk(layer, table, length, cu, q, k, v, max_len=held, max_rows=n, total_len=held)
+                kv.append(layer, table, length, cu, k, v, max_rows=n)
+                rows.append((q, k, v, o))
+            kv.advance([request], [n])
+            seen.append(rows)
+        return seen
+
+    def prompt(self, request, tokens, chunk=256):
+        """prefill; -> per attention layer the keys and values that were committed."""
+        seen = self.prefill(request, tokens, chunk)
+        return [tuple(torch.cat([rows[layer][i] for rows in seen]) for i in (1, 2))
+                for layer in range(self.kv.kv.shape[1])]
 
     def step(self, drafts):
         """One transaction; -> per attention layer (q, k, v, o), and the accept lengths."""
@@ -85,6 +107,7 @@ class HybridDecode:
         seen = []
         for layer in range(kv.kv.shape[1]):
             q, k, v = self.attention_rows(rows)
+            self.rotate(q, k, loop.cu_rows, length)
             o, _ = kv.attend(layer, table, length, loop.cu_rows, q, k, v, max_len=kv.max_len, max_rows=max(n))
             seen.append((q, k, v, o))
         logits = self.normal(vs.cap, VOCAB, scale=2.0)

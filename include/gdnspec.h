@@ -757,7 +757,8 @@ typedef struct attn_dims {
  *   reach it, whatever it holds.
  *   Bad rows set GDN_DEV_ROWS_BAD: the request is skipped (its o and lse are
  *   not written).  A bounded wait that runs out sets GDN_DEV_TIMEOUT: outputs
- *   of that call are not to be trusted.  B <= 65535.  workspace:
+ *   of that call are not to be trusted, and while *dev_status holds it calls
+ *   write nothing.  B <= 65535; max_rows <= 2^25.  workspace:
  *   attn_prompts_workspace_bytes(...) device bytes (16-byte aligned, no
  *   initialisation, one call at a time), 0 when no work is cut.
  */
@@ -779,7 +780,8 @@ int attn_prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const i
  *   reach an output, whatever they hold.  Requests past max_len, max_rows,
  *   row_capacity or, with those before them, total_len set GDN_DEV_ROWS_BAD,
  *   page ids out of range (of pages some row sees) GDN_DEV_PAGE_OOR; either
- *   skips the request.  total_len + row_capacity < 2^30.
+ *   skips the request.  max_len + max_rows <= 2^25, total_len + row_capacity
+ *   < 2^30.
  */
 size_t kv8_chunk_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t row_capacity, int32_t max_len,
                                  int32_t max_rows, int64_t total_len);

@@ -64,6 +64,8 @@ struct Cfg {
     static constexpr int kSlots = kRoom / kSlot > 8 ? 8 : kRoom / kSlot;
     static constexpr int kSmem = kStages * kQTile + kSlots * kSlot + 1024;
     static constexpr int kSoftWarps = 4 * kStages;
+    // Whether the weights have tensor memory of their own: then the next scores need not wait for the products with them.
+    static constexpr bool kApart = D == 64;
     static constexpr int kGuards = kStages == 2 ? 1 : 5;  // warps that look through values
     static constexpr int kThreads = 32 * (kSoftWarps + 3 + kGuards);
     // Registers a thread: of the 168 that 384 threads may have, the softmax's rows take more, the other warps fewer.
@@ -98,7 +100,7 @@ template <int D>
 struct Shared {
     using C = Cfg<D>;
     uint64_t full[C::kSlots], freed[kGroups], s_full[2], o_done[2], q_full, q_free, drain;  // one arrival
-    uint64_t p_ready[4];                      // halves of a tile's weights, of four warps
+    uint64_t p_ready[4], s_read[2];           // halves of a tile's weights; its scores are read; of four warps
     uint64_t v_sent[kAhead];                  // masked tiles in turn: the copy of the values is under way ...
     uint64_t v_ok[kAhead];                    // ... and looked through
     uint64_t w_full[kQueue], w_free[kQueue];  // a unit is announced; everybody is done with it
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s.s_full + i, 1);
             gdn::mbar_init(s.o_done + i, 1);
+            gdn::mbar_init(s.s_read + i, 4);
         }
         for (int i = 0; i < 4; ++i) gdn::mbar_init(s.p_ready + i, 4);
         gdn::mbar_init(&s.q_full, 1);
@@ -467,23 +470,33 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 const int slot = kStages == 2 ? st : g & 1, turn = kStages == 2 ? g : g >> 1;
                 if (!wait(&s.s_full[slot], turn)) break;
                 tc::fence_after();
-                const uint32_t t_s = tm + slot * kTile + lanes;
+                const uint32_t t_s = tm + slot * kTile + lanes, t_p = C::kApart ? tm + 384 + st * kHalf + lanes : t_s;
                 uint32_t x[2][kHalf];
                 load_half(t_s, x[0]);
                 load_half(t_s + kHalf, x[1]);
                 tc::ld_wait();
                 arrived(x[0]);
                 arrived(x[1]);
+                if constexpr (C::kApart) {
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s.s_read[slot]);
+                }
                 if (masked(w.sp, w.sp.tile0 + j)) {
                     const int hi = w.u.len + position() - (w.sp.tile0 + j) * kTile, lo = a.window ? hi - a.window : -1;
                     hide(x[0], hi, lo);
                     hide(x[1], hi - kHalf, lo - kHalf);
                 }
                 const float z = fmaxf(top_of(x[0]), top_of(x[1])) * a.scale_log2;
+                if constexpr (C::kApart) {
+                    // the last tile's products are done with the sums and the weights
+                    if (j > 0 && !wait(&s.o_done[st], g - 1)) break;
+                    tc::fence_after();
+                }
                 if (__any_sync(0xffffffffu, z > m + kSlack)) {
                     const float now = fmaxf(m, z), f = m == now ? 1.f : ex2(m - now);  // (-inf less -inf is no number)
                     if (j > 0) {
-                        // (with two query tiles the scores are behind the products before)
+                        // (with two query tiles and no room the scores are behind the products before)
                         if (kStages == 1 && !wait(&s.o_done[(g - 1) & 1], (g - 1) >> 1)) break;
                         tc::fence_after();
 #pragma unroll 1
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 for (int half = 0; half < 2; ++half) {
                     uint32_t p[kHalf / 2];
                     l += weights(x[half], c2, r, p);
-                    tc::st32_async(t_s + half * (kHalf / 2), p);
+                    tc::st32_async(t_p + half * (kHalf / 2), p);
                     tc::st_wait();
                     tc::fence_before();
                     __syncwarp();
@@ -516,7 +529,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             if (!ok) break;
             if (!wait(&s.pages[k % kQueue], k / kQueue)) break;
             if (n > 0) {
-                if (!wait(&s.o_done[kStages == 2 ? st : (g - 1) & 1], kStages == 2 ? units : (g - 1) >> 1)) break;
+                if (!wait(&s.o_done[kStages == 2 ? st : (g - 1) & 1],
+                          C::kApart ? g - 1 : kStages == 2 ? units : (g - 1) >> 1))
+                    break;
                 ++units;
             }
             tc::fence_after();
@@ -711,6 +726,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     }
                     tc::commit(&s.s_full[slot]);
                 };
+                const auto t_p = [&](int slot) { return C::kApart ? tm + 384 + slot * kHalf : tm + slot * kTile; };
                 // (the softmax warps give a unit's first weights after they have read the last unit's sums)
                 auto outputs = [&](int st, int slot, const Slots<D> &x, bool more, int turn) {
 #pragma unroll
@@ -724,8 +740,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                             const uint32_t to = tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece;
 #pragma unroll
                             for (int i = half * kHalf / 16; i < (half + 1) * kHalf / 16; ++i)
-                                tc::mma_bf16_ts(to, tm + slot * kTile + i * 8, tc::desc_at(d, i * 2048), id_p,
-                                                more || i > 0);
+                                tc::mma_bf16_ts(to, t_p(slot) + i * 8, tc::desc_at(d, i * 2048), id_p, more || i > 0);
                         }
                     }
                     return true;
@@ -737,8 +752,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
 #pragma unroll
                         for (int y = 0; y < C::kPieces; ++y)
                             tc::mma_bf16_ts(tm + 256 + (kStages == 2 ? st * D : 0) + y * C::kPiece,
-                                            tm + slot * kTile + i * 8,
-                                            tc::desc_at(dv, x.slot[y] * C::kSlot + i * 2048), id_p, more || i > e.x);
+                                            t_p(slot) + i * 8, tc::desc_at(dv, x.slot[y] * C::kSlot + i * 2048), id_p,
+                                            more || i > e.x);
                 };
                 auto free_group = [&] {
                     tc::commit(&s.freed[groups % kGroups]);
@@ -747,6 +762,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 auto weights_of = [&](int slot, int turn) {
                     for (int half = 0; half < 2; ++half)
                         ok = ok && gdn::mbar_wait_bounded(&s.p_ready[2 * slot + half], turn & 1, a.wait_ns);
+                    tc::fence_after();
+                    return ok;
+                };
+                // (each tile's reading is waited for once: by the next tile's scores, or the next unit's first)
+                auto read = [&](int st, int turn) {
+                    ok = ok && gdn::mbar_wait_bounded(&s.s_read[st], turn & 1, a.wait_ns);
                     tc::fence_after();
                     return ok;
                 };
@@ -762,6 +783,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                         Slots<D> kt = at;
                         at.next();
                         if (!landed(kt)) break;
+                        if (C::kApart && ((n0 > 0 && g0 > 0 && !read(0, g0 - 1)) || (n1 > 0 && g1 > 0 && !read(1, g1 - 1))))
+                            break;
                         tc::fence_after();
                         if (n0 > 0) scores(0, 0, kt);
                         if (n1 > 0) scores(1, 1, kt);
@@ -777,14 +800,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                             if (j > 0 && j < whole && sp.tile0 + j >= sp.left) {
                                 // both query tiles, every position
                                 if (!landed(kt) || !landed(vt)) break;
-                                if (!outputs(0, 0, vt, true, g0 + j)) break;
-                                scores(0, 0, kt);
-                                if (!outputs(1, 1, vt, true, g1 + j)) break;
-                                scores(1, 1, kt);
+                                if constexpr (C::kApart) {
+                                    if (!read(0, g0 + j)) break;
+                                    scores(0, 0, kt);
+                                    if (!read(1, g1 + j)) break;
+                                    scores(1, 1, kt);
+                                    if (!outputs(0, 0, vt, true, g0 + j)) break;
+                                    tc::commit(&s.o_done[0]);
+                                    if (!outputs(1, 1, vt, true, g1 + j)) break;
+                                    tc::commit(&s.o_done[1]);
+                                } else {
+                                    if (!outputs(0, 0, vt, true, g0 + j)) break;
+                                    scores(0, 0, kt);
+                                    if (!outputs(1, 1, vt, true, g1 + j)) break;
+                                    scores(1, 1, kt);
+                                }
                             } else {
                                 const bool cut = masked(sp, sp.tile0 + j);
                                 const int2 e = cut ? steps_of(sp, sp.tile0 + j) : make_int2(0, kTile / 16);
                                 if (j + 1 < nt) landed(kt);
+                                if constexpr (C::kApart) {
+#pragma unroll 1
+                                    for (int st = 0; st < 2 && ok; ++st)
+                                        if (j + 1 < (st ? n1 : n0) && read(st, (st ? g1 : g0) + j)) scores(st, st, kt);
+                                }
                                 if (!landed(vt)) break;
                                 if (cut) {
                                     ok = gdn::mbar_wait_bounded(&s.v_ok[guarded % kAhead], guarded / kAhead & 1, a.wait_ns);
@@ -796,9 +835,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                                     if (j < n) {
                                         if (!weights_of(st, (st ? g1 : g0) + j)) break;
                                         outputs_cut(st, st, vt, j > 0, e);
-                                        if (j + 1 == n) tc::commit(&s.o_done[st]);
+                                        if (C::kApart || j + 1 == n) tc::commit(&s.o_done[st]);
                                     }
-                                    if (j + 1 < n) scores(st, st, kt);
+                                    if (!C::kApart && j + 1 < n) scores(st, st, kt);
                                 }
                                 if (!ok) break;
                             }
@@ -1200,10 +1239,14 @@ size_t kv_bytes(const kv8_cache *c, int64_t rows) { return size_t(rows) * c->h_k
 template <int D>
 int launch(const Args &a, const Plan &p, cudaStream_t st) {
     using C = Cfg<D>;
-    // what its warps take from one another is shared out of this many registers
-    cudaFuncAttributes have;
-    if (cudaFuncGetAttributes(&have, prompt_attend_kernel<D>) != cudaSuccess || have.numRegs != C::kLaunchRegs)
-        return GDN_ERR_CUDA;
+    // What its warps take from one another is shared out of this many registers (looked at once: it is the code's).
+    static std::atomic<bool> looked{false};
+    if (!looked.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes have;
+        if (cudaFuncGetAttributes(&have, prompt_attend_kernel<D>) != cudaSuccess || have.numRegs != C::kLaunchRegs)
+            return GDN_ERR_CUDA;
+        looked.store(true, std::memory_order_relaxed);
+    }
     // for every launch: the limit is the current device's
     if (cudaFuncSetAttribute(prompt_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
         cudaSuccess)
@@ -1241,12 +1284,16 @@ int check_dims(const attn_dims *c) {
     return GDN_OK;
 }
 constexpr int64_t kMostUnits = (int64_t(1) << 31) - 1;
+// A unit's longest waits are for all of its tiles, about 2 us each: half a second of the bound's one.
+constexpr int64_t kMostPositions = int64_t(1) << 25;
 
 }  // namespace
 
 extern "C" size_t attn_prompts_workspace_bytes(const attn_dims *dims, int32_t B, int32_t row_capacity,
                                                int32_t max_rows) {
-    if (check_dims(dims) != GDN_OK || B <= 0 || B > 65535 || row_capacity < 0 || max_rows <= 0) return 0;
+    if (check_dims(dims) != GDN_OK || B <= 0 || B > 65535 || row_capacity < 0 || max_rows <= 0 ||
+        max_rows > kMostPositions)
+        return 0;
     return part_bytes(plan_of(dims->h_q, dims->h_kv, dims->d, dims->window, B, row_capacity, 0, max_rows, 0), dims->d);
 }
 
@@ -1256,7 +1303,7 @@ static int prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const
                    size_t workspace_bytes, uint32_t *dev_status, uint64_t wait_ns, int32_t withhold, void *stream) {
     const int bad = check_dims(dims);
     if (bad != GDN_OK) return bad;
-    if (B < 0 || B > 65535 || row_capacity < 0 || max_rows < 0) return GDN_ERR_ARG;
+    if (B < 0 || B > 65535 || row_capacity < 0 || max_rows < 0 || max_rows > kMostPositions) return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0 || row_capacity == 0) return GDN_OK;
     if (!cu_rows || !q || !k || !v || !o) return GDN_ERR_NULL;
     if (!gdn_host::kv8_rows_ok(q, q_stride, dims->h_q, dims->d) ||
@@ -1321,7 +1368,7 @@ static int64_t kv_rows(int32_t B, int32_t row_capacity, int32_t max_len, int64_t
 extern "C" size_t kv8_chunk_workspace_bytes(const kv8_cache *cache, int32_t B, int32_t row_capacity, int32_t max_len,
                                             int32_t max_rows, int64_t total_len) {
     if (gdn_host::kv8_check(cache) != GDN_OK || B <= 0 || B > 65535 || row_capacity < 0 || max_len < 0 ||
-        max_len > gdn_host::kKv8MaxLen || max_rows <= 0 || total_len < 0)
+        max_rows <= 0 || int64_t(max_len) + max_rows > kMostPositions || total_len < 0)
         return 0;
     const int64_t rows = kv_rows(B, row_capacity, max_len, total_len);
     if (rows >= gdn_host::kKv8MaxLen) return 0;
@@ -1340,8 +1387,8 @@ extern "C" int kv8_chunk(const kv8_cache *cache, int32_t layer, int32_t B, int32
     const int bad = gdn_host::kv8_check(cache);
     if (bad != GDN_OK) return bad;
     if (layer < 0 || layer >= cache->num_layers || B < 0 || B > 65535 || row_capacity < 0 || table_pages < 0 ||
-        table_stride < 0 || max_len < 0 || max_len > gdn_host::kKv8MaxLen || max_rows < 0 ||
-        max_rows > gdn_host::kKv8MaxLen || total_len < 0)
+        table_stride < 0 || max_len < 0 || max_rows < 0 || int64_t(max_len) + max_rows > kMostPositions ||
+        total_len < 0)
         return GDN_ERR_ARG;
     if (B == 0 || max_rows == 0 || row_capacity == 0) return GDN_OK;
     if (!cu_rows || !cache_len || (!table && table_pages > 0) || !q || !k_new || !v_new || !o) return GDN_ERR_NULL;

@@ -66,7 +66,7 @@ class Kv8Cache:
         self._device = kv.device
         self._index = kv.get_device()
         self._status = status.data_ptr()
-        self._workspace = {}  # (B, max_len, max_rows, split_tokens) -> bytes
+        self._workspace = {}  # (B, max_len, max_rows, split_tokens), or a chunk's sizes -> bytes
 
     # The checks stand in the calls themselves: on small transactions a call's time is
     # its host side, and a Python function a tensor cost 2.4 of 16 us.
@@ -176,20 +176,43 @@ class Kv8Cache:
                 or not cu_rows.is_contiguous() or table.get_device() != device or cache_len.get_device() != device
                 or cu_rows.get_device() != device):
             raise self._bad_lists("cache_len and cu_rows")
-        R = q.shape[0]
-        strides = []
-        for name, x, h in (("q", q, h_q), ("k_new", k_new, h_kv), ("v_new", v_new, h_kv), ("out", out, h_q)):
-            if x is None and name == "out":
-                strides.append(h * d)
-                continue
-            n, a, b = x.shape
-            s, c, one = x.stride()
-            if (x.dtype is not _BF16 or n < R or a != h or b != d or (c != d and h > 1) or one != 1
-                    or x.get_device() != device):
-                raise self._bad_rows(name, h)
-            strides.append(h * d if n <= 1 else s)  # a single row's stride says nothing
+        R, a, b = q.shape
+        q_s, c, one = q.stride()
+        if (q.dtype is not _BF16 or a != h_q or b != d or (c != d and h_q > 1) or one != 1
+                or q.get_device() != device):
+            raise self._bad_rows("q", h_q)
+        if R <= 1:
+            q_s = h_q * d  # a single row's stride says nothing
+        n, a, b = k_new.shape
+        k_s, c, one = k_new.stride()
+        if (k_new.dtype is not _BF16 or n < R or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
+                or k_new.get_device() != device):
+            raise self._bad_rows("k_new", h_kv)
+        if n <= 1:
+            k_s = h_kv * d
+        n, a, b = v_new.shape
+        v_s, c, one = v_new.stride()
+        if (v_new.dtype is not _BF16 or n < R or a != h_kv or b != d or (c != d and h_kv > 1) or one != 1
+                or v_new.get_device() != device):
+            raise self._bad_rows("v_new", h_kv)
+        if n <= 1:
+            v_s = h_kv * d
+        o_s = h_q * d
+        if out is not None:
+            n, a, b = out.shape
+            o_s, c, one = out.stride()
+            if (out.dtype is not _BF16 or n < R or a != h_q or b != d or (c != d and h_q > 1) or one != 1
+                    or out.get_device() != device):
+                raise self._bad_rows("out", h_q)
+            if n <= 1:
+                o_s = h_q * d
         total = B * max_len if total_len is None else total_len
-        need = gs.lib.kv8_chunk_workspace_bytes(self._c, B, R, max_len, max_rows, total)
+        key = (B, R, max_len, max_rows, total)
+        need = self._workspace.get(key)
+        if need is None:
+            if len(self._workspace) > 4096:
+                self._workspace.clear()
+            need = self._workspace[key] = gs.lib.kv8_chunk_workspace_bytes(self._c, *key)
         if stream is not None:
             # what the call allocates belongs to the stream it runs on
             before = torch.cuda.current_stream(self._device)
@@ -197,16 +220,16 @@ class Kv8Cache:
         try:
             raw = _raw_stream(device)
             if out is None:
-                out = torch.empty((R, h_q, d), dtype=_BF16, device=self._device)
-            lse = torch.empty((R, h_q), dtype=torch.float32, device=self._device) if want_lse else None
-            ws = torch.empty((need,), dtype=torch.uint8, device=self._device) if need else None
+                out = q.new_empty((R, h_q, d))
+            lse = q.new_empty((R, h_q), dtype=torch.float32) if want_lse else None
+            ws = q.new_empty((need,), dtype=torch.uint8) if need else None
         finally:
             if stream is not None:
                 torch.cuda.set_stream(before)
         st = gs.lib.kv8_chunk(self._c, layer, B, R, cu_rows.data_ptr(), cache_len.data_ptr(), table.data_ptr(), pages,
-                              table_s, q.data_ptr(), strides[0], k_new.data_ptr(), strides[1], v_new.data_ptr(),
-                              strides[2], out.data_ptr(), strides[3], lse.data_ptr() if want_lse else None, max_len,
-                              max_rows, total, ws.data_ptr() if need else None, need, self._status, raw)
+                              table_s, q.data_ptr(), q_s, k_new.data_ptr(), k_s, v_new.data_ptr(), v_s,
+                              out.data_ptr(), o_s, lse.data_ptr() if want_lse else None, max_len, max_rows, total,
+                              ws.data_ptr() if need else None, need, self._status, raw)
         if st != gs.GDN_OK:
             raise gs.GdnError("kv8_chunk", st)
         return out, lse

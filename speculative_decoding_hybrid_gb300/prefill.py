@@ -78,6 +78,7 @@ class Rope:
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self._device = self.turns.device
         self._index = self.turns.get_device()
+        self._turns = self.turns.data_ptr()
         self._spec = {}  # (h_q, h_kv) -> rope_spec
 
     def _bad(self, name: str):
@@ -90,58 +91,83 @@ class Rope:
                ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
         """-> (q, k) turned to positions cache_len[r] + i (``rope_rows`` in the header): new tensors, q_out and k_out,
         or in place.  k may be None."""
-        d, device = self.d, self._index
+        # (the checks stand in the call: on few rows its time is its host side)
+        d, index = self.d, self._index
         B = cu_rows.numel() - 1
-        if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != device
-                or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != device):
+        if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != index
+                or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != index):
             raise ValueError("cu_rows must be a contiguous int32 list and status one int32, on the table's device")
-        if cache_len is not None and (cache_len.dtype is not _I32 or cache_len.numel() < B
-                                      or not cache_len.is_contiguous() or cache_len.get_device() != device):
-            raise ValueError("cache_len must be a contiguous int32 list of the requests, on the table's device")
-        if in_place and (q_out is not None or k_out is not None):
-            raise ValueError("in place there is no other output")
-        if k is None and k_out is not None:
+        len_p = None
+        if cache_len is not None:
+            if (cache_len.dtype is not _I32 or cache_len.numel() < B or not cache_len.is_contiguous()
+                    or cache_len.get_device() != index):
+                raise ValueError("cache_len must be a contiguous int32 list of the requests, on the table's device")
+            len_p = cache_len.data_ptr()
+        if in_place:
+            if q_out is not None or k_out is not None:
+                raise ValueError("in place there is no other output")
+            q_out, k_out = q, k
+        R, h_q, c = q.shape
+        q_s, x, one = q.stride()
+        if q.dtype is not _BF16 or c != d or one != 1 or (x != d and h_q > 1) or q.get_device() != index:
+            raise self._bad("q")
+        h_kv = k_s = 0
+        if k is not None:
+            n, h_kv, c = k.shape
+            k_s, x, one = k.stride()
+            if (k.dtype is not _BF16 or n != R or c != d or one != 1 or (x != d and h_kv > 1)
+                    or k.get_device() != index):
+                raise self._bad("k")
+        elif k_out is not None:
             raise ValueError("k_out without k")
-        rows = q.shape[0]
         if stream is not None:
             # what the call allocates belongs to the stream it runs on
             before = torch.cuda.current_stream(self._device)
             torch.cuda.set_stream(_stream_object(stream))
         try:
-            raw = _raw_stream(device)
-            args, outs, heads = [], [], []
-            for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-                if x is None:
-                    args += [None, 0, None, 0]
-                    outs.append(None)
-                    heads.append(0)
-                    continue
-                n, h, c = x.shape
-                if in_place:
-                    y = x
-                elif y is None:
-                    y = torch.empty((n, h, d), dtype=_BF16, device=self._device)
-                for label, t in ((name, x), (name + "_out", y)):
-                    if (t.dtype is not _BF16 or t.shape != (rows, h, d) or t.stride(2) != 1
-                            or (t.stride(1) != d and h > 1) or t.get_device() != device):
-                        raise self._bad(label)
-                one = rows <= 1  # a single row's stride says nothing
-                args += [x.data_ptr(), h * d if one else x.stride(0), y.data_ptr(), h * d if one else y.stride(0)]
-                outs.append(y)
-                heads.append(h)
+            raw = _raw_stream(index)
+            if q_out is None:
+                q_out, qo_s = q.new_empty((R, h_q, d)), h_q * d
+            else:
+                n, h, c = q_out.shape
+                qo_s, x, one = q_out.stride()
+                if (q_out.dtype is not _BF16 or n != R or h != h_q or c != d or one != 1 or (x != d and h > 1)
+                        or q_out.get_device() != index):
+                    raise self._bad("q_out")
+            ko_s = 0
+            if k_out is not None:
+                n, h, c = k_out.shape
+                ko_s, x, one = k_out.stride()
+                if (k_out.dtype is not _BF16 or n != R or h != h_kv or c != d or one != 1 or (x != d and h > 1)
+                        or k_out.get_device() != index):
+                    raise self._bad("k_out")
+            elif k is not None:
+                k_out, ko_s = k.new_empty((R, h_kv, d)), h_kv * d
         finally:
             if stream is not None:
                 torch.cuda.set_stream(before)
-        spec = self._spec.get(tuple(heads))
+        if R <= 1:
+            q_s = qo_s = h_q * d  # a single row's stride says nothing
+            k_s = ko_s = h_kv * d
+        spec = self._spec.get((h_q, h_kv))
         if spec is None:
-            spec = self._spec[tuple(heads)] = gs.rope_spec(heads[0], heads[1], d, self.rot, int(self.interleaved),
-                                                           self.magnitude)
-        st = gs.lib.rope_rows(ctypes.byref(spec), B, rows, cu_rows.data_ptr(),
-                              None if cache_len is None else cache_len.data_ptr(), self.turns.data_ptr(), *args,
+            spec = self._spec[h_q, h_kv] = ctypes.byref(gs.rope_spec(h_q, h_kv, d, self.rot, int(self.interleaved),
+                                                                     self.magnitude))
+        st = gs.lib.rope_rows(spec, B, R, cu_rows.data_ptr(), len_p, self._turns, q.data_ptr(), q_s, q_out.data_ptr(),
+                              qo_s, k.data_ptr() if h_kv else None, k_s, k_out.data_ptr() if h_kv else None, ko_s,
                               status.data_ptr(), raw)
         if st != gs.GDN_OK:
             raise gs.GdnError("rope_rows", st)
-        return outs[0], outs[1]
+        return q_out, k_out
+
+
+# A call's head layout and the workspace that its sizes want, by the arguments that fix them.
+_workspace = {}
+
+
+def _bad_rows(name: str, heads: int, d: int):
+    return ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads on q's device, a row for each of the "
+                      "call's" % (name, heads, d))
 
 
 def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
@@ -151,43 +177,63 @@ def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: t
 
     q [rows, h_q, d], k and v [rows, h_kv, d]: packed prompts; max_rows is a host bound on a prompt's rows."""
     R, h_q, d = q.shape
-    h_kv = k.shape[1]
-    device, index = q.device, q.get_device()
+    q_s, x, one = q.stride()
+    index = q.get_device()
     B = cu_rows.numel() - 1
     if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != index
             or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != index):
         raise ValueError("cu_rows must be a contiguous int32 list and status one int32, on the rows' device")
-    strides = []
-    for name, x, h in (("q", q, h_q), ("k", k, h_kv), ("v", v, h_kv), ("out", out, h_q)):
-        if x is None:
-            strides.append(h * d)
-            continue
-        n, a, b = x.shape
-        s, c, one = x.stride()
-        if (x.dtype is not _BF16 or n < R or a != h or b != d or (c != d and h > 1) or one != 1
-                or x.get_device() != index):
-            raise ValueError("%s must be bf16 [rows, %d, %d] with contiguous heads on q's device, a row for each of "
-                             "the call's" % (name, h, d))
-        strides.append(h * d if n <= 1 else s)  # a single row's stride says nothing
-    dims = gs.attn_dims(h_q, h_kv, d, window, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
-    need = gs.attn_prompts_workspace_bytes(dims, B, R, max_rows)
+    if q.dtype is not _BF16 or one != 1 or (x != d and h_q > 1):
+        raise _bad_rows("q", h_q, d)
+    n, h_kv, c = k.shape
+    k_s, x, one = k.stride()
+    if k.dtype is not _BF16 or n < R or c != d or one != 1 or (x != d and h_kv > 1) or k.get_device() != index:
+        raise _bad_rows("k", h_kv, d)
+    k1 = n <= 1
+    n, h, c = v.shape
+    v_s, x, one = v.stride()
+    if (v.dtype is not _BF16 or n < R or h != h_kv or c != d or one != 1 or (x != d and h > 1)
+            or v.get_device() != index):
+        raise _bad_rows("v", h_kv, d)
+    if n <= 1:
+        v_s = h_kv * d  # a single row's stride says nothing
+    if k1:
+        k_s = h_kv * d
+    if R <= 1:
+        q_s = h_q * d
+    o_s = h_q * d
+    if out is not None:
+        n, h, c = out.shape
+        o_s, x, one = out.stride()
+        if (out.dtype is not _BF16 or n < R or h != h_q or c != d or one != 1 or (x != d and h > 1)
+                or out.get_device() != index):
+            raise _bad_rows("out", h_q, d)
+        if n <= 1:
+            o_s = h_q * d
+    key = (h_q, h_kv, d, window, sm_scale, B, R, max_rows)
+    plan = _workspace.get(key)
+    if plan is None:
+        if len(_workspace) > 4096:
+            _workspace.clear()
+        dims = gs.attn_dims(h_q, h_kv, d, window, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
+        plan = _workspace[key] = ctypes.byref(dims), gs.attn_prompts_workspace_bytes(dims, B, R, max_rows)
+    dims, need = plan
     if stream is not None:
         # what the call allocates belongs to the stream it runs on
-        before = torch.cuda.current_stream(device)
+        before = torch.cuda.current_stream(q.device)
         torch.cuda.set_stream(_stream_object(stream))
     try:
         raw = _raw_stream(index)
         if out is None:
-            out = torch.empty((R, h_q, d), dtype=_BF16, device=device)
-        lse = torch.empty((R, h_q), dtype=torch.float32, device=device) if want_lse else None
-        ws = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+            out = q.new_empty((R, h_q, d))
+        lse = q.new_empty((R, h_q), dtype=torch.float32) if want_lse else None
+        ws = q.new_empty((need,), dtype=torch.uint8) if need else None
     finally:
         if stream is not None:
             torch.cuda.set_stream(before)
-    st = gs.lib.attn_prompts(ctypes.byref(dims), B, R, cu_rows.data_ptr(), q.data_ptr(), strides[0], k.data_ptr(),
-                             strides[1], v.data_ptr(), strides[2], out.data_ptr(), strides[3],
-                             lse.data_ptr() if want_lse else None, max_rows, ws.data_ptr() if need else None, need,
-                             status.data_ptr(), raw)
+    st = gs.lib.attn_prompts(dims, B, R, cu_rows.data_ptr(), q.data_ptr(), q_s, k.data_ptr(), k_s, v.data_ptr(), v_s,
+                             out.data_ptr(), o_s, lse.data_ptr() if want_lse else None, max_rows,
+                             ws.data_ptr() if need else None, need, status.data_ptr(), raw)
     if st != gs.GDN_OK:
         raise gs.GdnError("attn_prompts", st)
     return out, lse

@@ -1,5 +1,8 @@
 """Attention of many new rows over the paged 8-bit cache against the fp64 form: head layouts, pages, ragged rows and
 lengths, windows, work cut into parts, what lies past a request's end, refusals, streams and graphs."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,11 +12,13 @@ import prompt_util as pu
 from gpu_util import build_lib, noted
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
     build_lib()
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
 
 
 def run(cache, rows, dev, window=0, layer=0, seed=0, sm_scale=None, pad=0, edit=None, total=True, table=None,
@@ -258,3 +263,43 @@ def test_arguments_are_checked(cuda_dev):
         with pytest.raises(gs.GdnError) as e:
             c.attend_chunk(**{**good, **bad})
         assert e.value.status == gs.GDN_ERR_ARG
+
+
+@pytest.mark.parametrize("d,page_tokens,h_q,h_kv", [(128, 32, 8, 2), (256, 64, 16, 2), (64, 16, 6, 6)])
+def test_prompts_in_chunks_then_transactions(cuda_dev, d, page_tokens, h_q, h_kv):
+    """Rotation, attention of the first rows and of later chunks, commits and verification together, against the fp64
+    forms on a cache that is followed chunk by chunk."""
+    import hybrid_decode as hd
+    from test_gpu_kv_paged import Follow
+    from test_gpu_rope import turned
+    h = hd.HybridDecode(2, 1, 2, 900, h_q=h_q, h_kv=h_kv, d=d, page_tokens=page_tokens, seed=d)
+    raw = []
+    h.rotate = lambda q, k, cu, length, f=h.rotate: (raw.append((q.clone(), k.clone(), int(length[0]))), f(q, k, cu, length))
+    f = Follow(h.kv, 2)
+    sc = ku.default_scale(d)
+    for r, tokens, chunk in ((0, 700, 300), (1, 90, 37)):
+        at = 0
+        for rows in h.prefill(r, tokens, chunk):
+            n = rows[0][0].shape[0]
+            for layer, (q, k, v, o) in enumerate(rows):
+                q0, k0, first = raw.pop(0)
+                assert first == at
+                for x0, x in ((q0, q), (k0, k)):
+                    x0, got = x0.double().cpu().numpy(), x.double().cpu().numpy()
+                    ref = turned(x0, np.arange(at, at + n, dtype=np.float64), h.rope.frequencies, 1.0, d // 2, False)
+                    half = d // 4
+                    hyp = np.hypot(x0[..., :half], x0[..., half:2 * half])
+                    bound = 2.0 ** -8 * np.abs(ref) + 1e-30
+                    bound[..., :2 * half] += 2.0 ** -19.9 * np.concatenate([hyp, hyp], -1)
+                    assert (np.abs(got - ref) <= bound).all()
+                q, k, v = (x.double().cpu().numpy() for x in (q, k, v))
+                ref = pu.attend(q, k, v, 0, sc, f.c[r].dense(0, layer) if at else None)
+                ob, _ = pu.bounds(*ref, d)
+                assert noted("prompts in chunks d=%d" % d, np.max(np.abs(o.double().cpu().numpy() - ref[0]) / ob)) <= 1.0
+            f.append(r, [(k, v) for _, k, v, _ in rows])
+            at += n
+        f.check(h.kv, r)
+    seen, accept = h.step([3, 2])
+    f.attend("transactions after prompts d=%d: o" % d, 0, seen, 0, 4, [x[3] for x in seen])
+    f.attend("transactions after prompts d=%d: o" % d, 1, seen, 4, 7, [x[3] for x in seen])
+    assert int(h.vs.status.item()) == 0
