@@ -220,9 +220,9 @@ class Kv8Cache:
         try:
             raw = _raw_stream(device)
             if out is None:
-                out = q.new_empty((R, h_q, d))
-            lse = q.new_empty((R, h_q), dtype=torch.float32) if want_lse else None
-            ws = q.new_empty((need,), dtype=torch.uint8) if need else None
+                out = torch.empty((R, h_q, d), dtype=_BF16, device=self._device)
+            lse = torch.empty((R, h_q), dtype=torch.float32, device=self._device) if want_lse else None
+            ws = torch.empty((need,), dtype=torch.uint8, device=self._device) if need else None
         finally:
             if stream is not None:
                 torch.cuda.set_stream(before)

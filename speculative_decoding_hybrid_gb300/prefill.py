@@ -127,7 +127,7 @@ class Rope:
         try:
             raw = _raw_stream(index)
             if q_out is None:
-                q_out, qo_s = q.new_empty((R, h_q, d)), h_q * d
+                q_out, qo_s = torch.empty((R, h_q, d), dtype=_BF16, device=self._device), h_q * d
             else:
                 n, h, c = q_out.shape
                 qo_s, x, one = q_out.stride()
@@ -142,7 +142,7 @@ class Rope:
                         or k_out.get_device() != index):
                     raise self._bad("k_out")
             elif k is not None:
-                k_out, ko_s = k.new_empty((R, h_kv, d)), h_kv * d
+                k_out, ko_s = torch.empty((R, h_kv, d), dtype=_BF16, device=self._device), h_kv * d
         finally:
             if stream is not None:
                 torch.cuda.set_stream(before)
@@ -218,16 +218,17 @@ def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: t
         dims = gs.attn_dims(h_q, h_kv, d, window, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
         plan = _workspace[key] = ctypes.byref(dims), gs.attn_prompts_workspace_bytes(dims, B, R, max_rows)
     dims, need = plan
+    device = q.device
     if stream is not None:
         # what the call allocates belongs to the stream it runs on
-        before = torch.cuda.current_stream(q.device)
+        before = torch.cuda.current_stream(device)
         torch.cuda.set_stream(_stream_object(stream))
     try:
         raw = _raw_stream(index)
         if out is None:
-            out = q.new_empty((R, h_q, d))
-        lse = q.new_empty((R, h_q), dtype=torch.float32) if want_lse else None
-        ws = q.new_empty((need,), dtype=torch.uint8) if need else None
+            out = torch.empty((R, h_q, d), dtype=_BF16, device=device)
+        lse = torch.empty((R, h_q), dtype=torch.float32, device=device) if want_lse else None
+        ws = torch.empty((need,), dtype=torch.uint8, device=device) if need else None
     finally:
         if stream is not None:
             torch.cuda.set_stream(before)
