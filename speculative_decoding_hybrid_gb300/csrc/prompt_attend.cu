@@ -575,11 +575,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     for (int i = 0; i < 4; ++i) {
                         uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                                : "=r"(y[e])
-                                : "f"(__uint_as_float(x[8 * i + 2 * e + 1]) * inv),
-                                  "f"(__uint_as_float(x[8 * i + 2 * e]) * inv));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = both(mul2(pair(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]), pair(inv, inv)));
+                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[e]) : "f"(f.y), "f"(f.x));
+                        }
                         v[i] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                     transpose4(v);
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             if (write && whole) {
                 if (a.lse)
                     a.lse[(int64_t(w.u.t0) + at) * a.h_q + h] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                        l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;  // (l is 1 or more)
             } else if (write) {
                 a.ws_ml[wrow] = make_float2(m, l);
             }
@@ -1073,7 +1072,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 
 // ---- the workspace's keys and values: cached positions as bf16 (exactly: 4 bits times a power of two), then the new rows
 
-constexpr int kGatherRows = 128, kGatherThreads = 256;  // rows of a CTA at most
+constexpr int kGatherRows = 32, kGatherThreads = 256;  // rows of a CTA at most
 
 struct GatherArgs {
     kv8_cache c;
@@ -1427,7 +1426,9 @@ extern "C" int kv8_chunk(const kv8_cache *cache, int32_t layer, int32_t B, int32
     g.out = dense;
     g.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    g.rows = rows >= 6 * kSms * kGatherRows ? kGatherRows : rows >= 6 * kSms * 32 ? 32 : 8;
+    // Rows of a CTA: as many as leave six CTAs for an SM (14,600 positions, 4 heads of 64: 9.9 us with 8, 8.8 with 16,
+    // 9.1 with 32, 12.9 with 64; 262,656 positions, 2 heads of 256: 143 with 16, 134 with 32, 142 with 128).
+    g.rows = rows >= 6 * kSms * 32 ? 32 : rows >= 6 * kSms * 8 ? 16 : 8;
     const int rc = gdn_host::launch_pdl(kv8_gather_kernel, dim3(unsigned((rows + g.rows - 1) / g.rows)),
                                         dim3(kGatherThreads), 0, st, g);
     if (rc != GDN_OK) return rc;
