@@ -69,7 +69,7 @@ struct Cfg {
     static constexpr int kGuards = kStages == 2 ? 1 : 5;  // warps that look through values
     static constexpr int kThreads = 32 * (kSoftWarps + 3 + kGuards);
     // Registers a thread: of the 168 that 384 threads may have, the softmax's rows take more, the other warps fewer.
-    static constexpr int kLaunchRegs = 168, kSoftRegs = kStages == 2 ? 200 : 232, kOtherRegs = kStages == 2 ? 104 : 136;
+    static constexpr int kLaunchRegs = 168, kSoftRegs = kStages == 2 ? 192 : 232, kOtherRegs = kStages == 2 ? 120 : 136;
     static_assert(kThreads == 384 && 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <=
                                          kThreads * kLaunchRegs,
                   "more registers than a launch has: the wait for them would not end");
