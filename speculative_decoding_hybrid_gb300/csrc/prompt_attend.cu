@@ -24,7 +24,7 @@ constexpr int kSms = 152;
 constexpr float kSlack = 8.f;
 constexpr int kLeast = 4;    // tiles a part of a cut unit has at least
 constexpr int kMostParts = 64;
-constexpr double kEnds = 5.0;
+constexpr double kEnds = 5.0, kPartEnds = 10.0;
 constexpr int kAhead = 4;    // tiles of values that the ring can hold: 8 slots, every other one of values
 
 struct Info {                // a unit's parts, for the join: parts 0: nothing to join
@@ -35,7 +35,7 @@ struct Args {
     CUtensorMap mq, mk, mv;
     prompt::Requests rq;
     int32_t h_q, h_kv, group, per_tile;  // per_tile: positions a query tile
-    int32_t window, splits, negate;
+    int32_t window, splits, part_tiles, negate;  // a unit's parts at most, and the tiles that one may have
     float scale_log2;
     int64_t o_stride;
     uint16_t *o;
@@ -264,7 +264,7 @@ __device__ __forceinline__ bool find_unit(const Args &a, const Shared<D> &s, int
             if (a.rq.kv_capacity && kv + u.len + u.n > a.rq.kv_capacity) return false;
             int tile0;
             const int tiles = unit_tiles(a, u, kStages, tile0);
-            u.parts = min(a.splits, max(1, tiles / kLeast));
+            u.parts = min(a.splits, (tiles + a.part_tiles - 1) / a.part_tiles);
             if (part >= u.parts) return false;
             w.sp = span_of(a, u, kStages, part);
             w.hk = x - rank * a.h_kv;
@@ -1196,7 +1196,7 @@ bool encode_rows(CUtensorMap *m, const uint16_t *p, int d, int heads, int64_t ro
 
 struct Plan {
     int64_t units;
-    int per_tile, splits, rows;
+    int per_tile, splits, part_tiles, rows;
 };
 Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capacity, int32_t max_len, int32_t max_rows,
              int64_t total_len) {
@@ -1209,17 +1209,28 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     int64_t seen = int64_t(max_len) + max_rows;
     if (window && window + per_unit < seen) seen = window + per_unit + kTile;
     const int64_t tiles = (seen + kTile - 1) / kTile;
-    // Work is cut where SMs would idle.  With i parts a unit they share the whole, and the last ones run on alone for
-    // most of the longest part; units about as long as one another run in full waves.  A part's ends cost as much as
-    // kEnds tiles, and the join as much again.
+    // Work is cut where SMs would idle, into parts of up to tiles / i tiles.  All units share the SMs; units about as long
+    // as one another run in full waves; the longest, which start first, matter where they are not small beside an SM's
+    // share.  A unit's ends cost as much as kEnds tiles, those of a part, whose sums are written and read again, kPartEnds.
+    // (8 requests of 60..2,048 rows behind 512..32,768 positions, 32/8 heads of 128: 1,270 us whole, 1,175 with 3 parts
+    // for every unit; 8 prompts of 512..12,000 rows, 32/4 heads: 1,050 whole, 1,490 with 7.)
     const double rows = double(row_capacity) / B;
-    const double mean = ((total_len < int64_t(B) * max_len ? double(total_len) / B : double(max_len)) + 0.5 * rows) / kTile + 1.0;
-    const double avg = mean < tiles ? mean : double(tiles);
+    double avg = ((total_len < int64_t(B) * max_len ? double(total_len) / B : double(max_len)) + 0.5 * rows) / kTile + 1.0;
+    if (max_len == 0) avg = sqrt(avg * (0.5 * tiles + 1.0));  // of prompts: long ones have more units too
+    if (avg > tiles) avg = double(tiles);
     int64_t s = 1;
     double best = 0.0;
     for (int64_t i = 1; p.units && i <= kMostParts && (i == 1 || i <= tiles / kLeast); ++i) {
-        const double share = double(p.units) * i / kSms, part = avg / i + kEnds, longest = double(tiles) / i + kEnds;
-        double cost = avg > 0.75 * tiles ? ceil(share) * part : share * part + 0.7 * longest;
+        const double ends = i > 1 ? kPartEnds : kEnds, longest = double(tiles) / i + ends;
+        const double parts = avg * i > tiles ? avg * i / tiles : 1.0;
+        double cost;
+        if (avg > 0.75 * tiles) {
+            cost = ceil(double(p.units) * i / kSms) * (avg / i + ends);
+        } else {
+            cost = p.units * (avg + (parts > 1.0 ? ends : kEnds) * parts) / kSms;
+            if (i == 1 && longest < 0.25 * cost) break;
+            cost += 0.7 * longest;
+        }
         if (cost < longest) cost = longest;
         if (i > 1) cost = 1.05 * (cost + kEnds);
         if (i == 1 || cost < best) {
@@ -1227,6 +1238,7 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
             s = i;
         }
     }
+    p.part_tiles = int((tiles + s - 1) / s);
     p.splits = int(s);
     return p;
 }
@@ -1260,6 +1272,7 @@ int launch(const Args &a, const Plan &p, cudaStream_t st) {
 int run(Args &a, const Plan &p, int d, float sm_scale, uint8_t *parts, cudaStream_t st) {
     a.per_tile = p.per_tile;
     a.splits = p.splits;
+    a.part_tiles = p.part_tiles;
     a.negate = sm_scale < 0.f;
     const float c = fabsf(sm_scale) * 1.4426950408889634f;
     a.scale_log2 = c < 1e-37f ? 1e-37f : c;  // a masked score times zero would be no number
