@@ -25,7 +25,7 @@ constexpr float kSlack = 8.f;
 constexpr int kLeast = 4;    // tiles a part of a cut unit has at least
 constexpr int kMostParts = 64;
 constexpr double kEnds = 5.0, kPartEnds = 10.0;
-constexpr int kAhead = 4;    // tiles of values that the ring can hold: 8 slots, every other one of values
+constexpr int kAhead = 8;    // tiles of values that the ring holds at most: its slots
 
 struct Info {                // a unit's parts, for the join: parts 0: nothing to join
     int t0, tok0, n, hk, parts, pad[3];
@@ -73,7 +73,7 @@ struct Cfg {
     static_assert(kThreads == 384 && 32 * kSoftWarps * kSoftRegs + (kThreads - 32 * kSoftWarps) * kOtherRegs <=
                                          kThreads * kLaunchRegs,
                   "more registers than a launch has: the wait for them would not end");
-    static_assert(kSlots >= 2 * kPieces + 1 && kSlots <= 2 * kAhead * kPieces, "does not fit an SM");
+    static_assert(kSlots >= 2 * kPieces + 1 && kSlots <= kAhead, "does not fit an SM");
 };
 
 struct Unit {
@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             s.order[tid] = uint8_t(tid);
         }
         prompt::scan2<C::kThreads>(s.scan, blocks, kv, total, kv_all);
+        if (a.rq.kv_capacity && kv_all > a.rq.kv_capacity && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+            gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
         if (tid < kChunks) {
             s.blocks[tid] = int(blocks);
             // (past the workspace's rows a request is refused, however far)
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *s_q = sm, *s_ring = sm + kStages * C::kQTile;
     bool ok = !stop;
-    // A warp's wait: one lane's.
+    // A warp's wait: one lane's.  (Before shared memory is read that it is for: a __syncwarp.  Tensor memory has its fence.)
     auto wait = [&](uint64_t *bar, int phase) {
         if (lane == 0) ok = gdn::mbar_wait_bounded(bar, phase & 1, a.wait_ns);
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -443,7 +445,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     };
     // Whether there is a unit k, once that is known, and that this warp is done with it.
     auto take = [&](int k) {
-        return ok && wait(&s.w_full[k % kQueue], k / kQueue) && s.work[k % kQueue].x >= 0;
+        if (!ok || !wait(&s.w_full[k % kQueue], k / kQueue)) return false;
+        __syncwarp();
+        return s.work[k % kQueue].x >= 0;
     };
     auto done = [&](int k) {
         __syncwarp();
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 ++units;
             }
             tc::fence_after();
+            __syncwarp();
             const bool fix = *reinterpret_cast<volatile int *>(&s.fix[k % kQueue]);
             const bool bad = *reinterpret_cast<volatile int *>(&s.bad[k % kQueue]);
             const int at = position();
@@ -958,6 +963,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     for (int y = 0; y < C::kPieces && ok; ++y) {
                         const int pos = (ring + v_pos(j, nt)) * C::kPieces + y, slot = pos % C::kSlots;
                         if (!wait(&s.full[slot], pos / C::kSlots)) break;
+                        __syncwarp();
                         uint4 *p = reinterpret_cast<uint4 *>(s_ring + slot * C::kSlot);
                         // rows of a block of 64 channels: those before `full` and from `all` on, a lane a row
                         const int base = (w.sp.tile0 + j) * kTile;
@@ -1116,9 +1122,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv8_gather_kernel(const __grid
             for (int r = r0; r < r1; ++r) {
                 const long long n = prompt::kv_rows_of(prompt::request_of(a.rq, r));
                 const long long from = max((long long)w0, kv), to = min((long long)w0 + a.rows, kv + n);
-                if (from < to && kv + n > a.rq.kv_capacity)
-                    gdn::set_status(a.status, GDN_DEV_ROWS_BAD);
-                else
+                if (kv + n <= a.rq.kv_capacity)  // (the attention refuses those that do not fit)
                     for (long long w = from; w < to; ++w) {
                         who[w - w0] = r;
                         place[w - w0] = int(w - kv);

@@ -194,6 +194,31 @@ def test_more_than_total_len(cuda_dev):
     assert (o[40:] == 7.0).all()
 
 
+def test_a_request_that_starts_past_total_len(cuda_dev):
+    """The first request fills what the bound leaves to the row: the one behind it is refused, and said to be."""
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    cache = ku.Cache([100, 100], 2, 1, 64, 32, seed=4)
+    t, f = pu.rows_of(60, 2, 1, 64, 0)
+    q, k, v = pu.split(t.to(cuda_dev), 2, 1, 64)
+    c = ku.gpu_cache(cache, cuda_dev)
+    out = torch.full((60, 2, 64), 7.0, dtype=torch.bfloat16, device=cuda_dev)
+    o, lse = c.attend_chunk(0, torch.from_numpy(cache.table).to(cuda_dev), pu.dev32(cache.lens, cuda_dev),
+                            pu.dev32([0, 40, 60], cuda_dev), q, k, v, max_len=100, max_rows=40, total_len=80,
+                            want_lse=True, out=out)
+    assert int(c.status.item()) == gs.DEV_ROWS_BAD       # 80 + 60 rows of room: 140 for the first, none for the second
+    compare("within", cache, o, lse, f, [0, 40, 60], 0, 0, ku.default_scale(64), [0])
+    assert (o[40:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", [(64, 1, 1), (64, 2, 1), (128, 2, 1), (256, 4, 1)])
+def test_many_requests_of_masked_tiles(cuda_dev, d, h_q, h_kv):
+    """More requests than a list's parts and than CTAs, whose units are masked tiles throughout."""
+    rows = [256 if i % 3 else 90 + i % 40 for i in range(330)] if d == 64 else [70 + i % 60 for i in range(330)]
+    lens = [100 + i % 7 for i in range(330)]
+    cache = ku.Cache(lens, h_q, h_kv, d, 128, seed=d)
+    check("many d=%d" % d, cache, rows, cuda_dev)
+
+
 def test_workspace_of_every_request_at_its_longest(cuda_dev):
     cache = ku.Cache([100, 3, 50], 4, 2, 128, 32, seed=4)
     check("no total", cache, [20, 30, 40], cuda_dev, total=False)

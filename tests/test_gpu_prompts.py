@@ -74,6 +74,11 @@ def test_many_units_are_not_cut(cuda_dev, d):
     check("units d=%d" % d, [700] * 5, 16, 8, d, cuda_dev, seed=d)
 
 
+@pytest.mark.parametrize("B", [2, 33, 128, 129, 700])
+def test_many_prompts(cuda_dev, B):
+    check("many prompts", [(37 * i) % 61 for i in range(B)], 4, 2, 64, cuda_dev, seed=B)
+
+
 @pytest.mark.parametrize("window", [1, 2, 64, 100, 127, 128, 129, 1000])
 @pytest.mark.parametrize("d", [64, 256])
 def test_windows(cuda_dev, window, d):
