@@ -95,6 +95,9 @@ struct Cfg {
     static constexpr int kSlots = kRoom / kSlot > 8 ? 8 : kRoom / kSlot;
     static constexpr int kSmem = kStages * kQTile + kSlots * kSlot + 1024;
     static constexpr int kSoftWarps = 4 * kStages;
+    // Columns of outputs at a time: wider loads are fewer (37 tokens, 16/2 heads of 256: 9.6 us with 32, 9.3 with 64), but
+    // beside two query tiles' registers they spill (16 prompts 468 -> 545).
+    static constexpr int kOut = D == 256 ? 64 : 32;
     // Whether the weights have tensor memory of their own: then the next scores need not wait for the products with them.
     static constexpr bool kApart = D == 64;
     static constexpr int kGuards = kStages == 2 ? 1 : 5;  // warps that look through values
@@ -202,29 +205,40 @@ __device__ __forceinline__ int2 steps_of(const Span &s, int tile) {
     return make_int2(max(s.begin - tile * kTile, 0) / 16, (min(s.end - tile * kTile, kTile) + 15) / 16);
 }
 
-// Adds to a row's 32 sums the values that are not finite at positions of masked tiles that it sees: they were taken out
-// of the tiles, where a zero weight would not have kept them from the other rows.
-__device__ __noinline__ void add_special(const Args &a, const Unit &u, const Span &s, int hk, int pos, int ch,
-                                         float *o) {
-    for (int j = 0; j < s.tiles; ++j) {
-        const int tile = s.tile0 + j;
-        if (!masked(s, tile)) continue;
-        const int from = max(tile * kTile, a.window ? pos - a.window + 1 : 0), to = min(tile * kTile + kTile - 1, pos);
-        for (int t = from; t <= to; ++t) {
-            const uint4 *v = reinterpret_cast<const uint4 *>(a.v + (u.kv0 + t) * a.v_row + int64_t(hk) * a.v_head + ch);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 y = v[e];
-                const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+// Adds to a row, as it was written, the values that are not finite at positions of masked tiles that it sees: they were
+// taken out of the tiles, where a zero weight would not have kept them from the other rows.
+template <int D>
+__device__ __noinline__ void add_special(const Args &a, const Work &w, int pos, uint16_t *row, float *part_row) {
+    for (int ch = 0; ch < D; ch += 8) {
+        float add[8] = {};
+        bool any = false;
+        for (int j = 0; j < w.sp.tiles; ++j) {
+            const int tile = w.sp.tile0 + j;
+            if (!masked(w.sp, tile)) continue;
+            const int from = max(tile * kTile, a.window ? pos - a.window + 1 : 0),
+                      to = min(tile * kTile + kTile - 1, pos);
+            const uint16_t *v = a.v + (w.u.kv0 + from) * a.v_row + int64_t(w.hk) * a.v_head + ch;
+            for (int t = from; t <= to; ++t, v += a.v_row) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(v);
                 const uint32_t most = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
                                                __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
                 if (max(most >> 16, most & 0xffffu) < 0x7f80u) continue;
+                const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+                any = true;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if ((x[c] & 0x7f80u) == 0x7f80u) o[8 * e + 2 * c] += __uint_as_float(x[c] << 16);
-                    if ((x[c] & 0x7f800000u) == 0x7f800000u) o[8 * e + 2 * c + 1] += __uint_as_float(x[c] & 0xffff0000u);
+                    if ((x[c] & 0x7f80u) == 0x7f80u) add[2 * c] += __uint_as_float(x[c] << 16);
+                    if ((x[c] & 0x7f800000u) == 0x7f800000u) add[2 * c + 1] += __uint_as_float(x[c] & 0xffff0000u);
                 }
             }
+        }
+        if (!any) continue;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            if (part_row)
+                part_row[ch + c] += add[c];
+            else
+                row[ch + c] = gdn::f32_to_bf16(gdn::bf16_to_f32(row[ch + c]) + add[c]);
         }
     }
 }
@@ -378,6 +392,28 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
         }
 }
 
+// Writes four lanes' pieces of four rows, `c` bytes into the rows.
+__device__ __forceinline__ void put(const unsigned long long (&to)[4], uint4 (&v)[4], int c) {
+    transpose4(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (to[i])
+            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(to[i] + c), "r"(v[i].x), "r"(v[i].y),
+                         "r"(v[i].z), "r"(v[i].w)
+                         : "memory");
+}
+__device__ __forceinline__ void rounded(const uint32_t (&x)[32], float inv, uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = both(mul2(pair(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]), pair(inv, inv)));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[e]) : "f"(f.y), "f"(f.x));
+        }
+        v[i] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+}
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(const __grid_constant__ Args a) {
     using C = Cfg<D>;
@@ -578,75 +614,56 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             const int64_t wrow = ((int64_t(w.x) * a.splits + w.part) * kStages + st) * kTile + row;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int h = w.hk * a.group + head;
-            // where this lane's piece of each of four lanes' rows goes
-            uint16_t *to[4];
+            uint16_t *const row_o = a.o + (int64_t(w.u.t0) + at) * a.o_stride + int64_t(h) * D;
+            float *const row_p = whole ? nullptr : a.ws_o + wrow * D;
+            // A store of 16 bytes from each of 32 rows is 32 accesses; four lanes trade pieces, so that they write 64 bytes
+            // of a row together.  Where this lane's piece of each of four lanes' rows goes (0: nowhere):
+            unsigned long long to[4];
             {
-                const unsigned long long o_row = reinterpret_cast<unsigned long long>(
-                    write ? a.o + (int64_t(w.u.t0) + at) * a.o_stride + int64_t(h) * D : nullptr);
+                const unsigned long long x = !write  ? 0
+                                             : whole ? reinterpret_cast<unsigned long long>(row_o)
+                                                     : reinterpret_cast<unsigned long long>(row_p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const unsigned long long x = __shfl_sync(0xffffffffu, o_row, (lane & ~3) + i);
-                    to[i] = x ? reinterpret_cast<uint16_t *>(x) + (lane & 3) * 8 : nullptr;
+                    to[i] = __shfl_sync(0xffffffffu, x, (lane & ~3) + i);
+                    if (to[i]) to[i] += (lane & 3) * 16;
                 }
             }
             const bool keep = n > 0 && l != 0.f;
-            const auto put = [&](int c, uint32_t (&x)[32]) {
-                if (!keep) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = 0;
-                }
-                if (fix && write && n > 0) {
-                    float o[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
-                    add_special(a, w.u, w.sp, w.hk, w.u.len + at, c, o);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(o[i]);
-                }
-                // A store of 16 bytes from each of 32 rows is 32 accesses; four lanes trade pieces, so that they
-                // write 64 bytes of a row together.
-                if (whole) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = both(mul2(pair(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]), pair(inv, inv)));
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[e]) : "f"(f.y), "f"(f.x));
-                        }
-                        v[i] = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                    transpose4(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (to[i]) *reinterpret_cast<uint4 *>(to[i] + c) = v[i];
-                } else {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = make_uint4(x[16 * y + 4 * i], x[16 * y + 4 * i + 1], x[16 * y + 4 * i + 2],
-                                              x[16 * y + 4 * i + 3]);
-                        transpose4(v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (to[i])
-                                *reinterpret_cast<uint4 *>(a.ws_o + (wrow - (lane & 3) + i) * D + (lane & 3) * 4 + c +
-                                                           16 * y) = v[i];
-                    }
-                }
-            };
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t x[32];
+            for (int c = 0; c < D; c += C::kOut) {
+                uint32_t x[C::kOut / 32][32];
                 if (n > 0) {
-                    tc::ld32_async(t_o + c, x);
+#pragma unroll
+                    for (int e = 0; e < C::kOut / 32; ++e) tc::ld32_async(t_o + c + 32 * e, x[e]);
                     tc::ld_wait();
                 }
-                arrived(x);
-                put(c, x);
+#pragma unroll
+                for (int e = 0; e < C::kOut / 32; ++e) {
+                    arrived(x[e]);
+                    if (!keep) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[e][i] = 0;
+                    }
+                    uint4 v[4];
+                    if (whole) {
+                        rounded(x[e], inv, v);
+                        put(to, v, 2 * (c + 32 * e));
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 16) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = make_uint4(x[e][y + 4 * i], x[e][y + 4 * i + 1], x[e][y + 4 * i + 2],
+                                                  x[e][y + 4 * i + 3]);
+                            put(to, v, 4 * (c + 32 * e + y));
+                        }
+                    }
+                }
+            }
+            if (fix) {
+                __syncwarp();
+                if (write && n > 0) add_special<D>(a, w, w.u.len + at, row_o, row_p);
             }
             if (write && whole) {
                 if (a.lse)
