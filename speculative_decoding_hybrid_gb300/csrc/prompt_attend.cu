@@ -145,7 +145,7 @@ struct Shared {
     int fix[kQueue], bad[kQueue];
     int holds[C::kSlots];                     // the group of loads that a slot's is in
     prompt::Scan<C::kThreads> scan;
-    int blocks[kChunks], kv[kChunks];         // before each part of the list of requests
+    alignas(16) int blocks[kChunks], kv[kChunks];  // before each part of the list of requests
     uint8_t order[kChunks];                   // where a part is one request: the one with the longest rows first
     uint32_t tmem;
 };
@@ -473,12 +473,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
         }
         if (chunk == 1 && a.rq.B > 1) {
             // long units started last would run alone (8 prompts of 512..12,000 rows: 1,070 us in the order given)
-            if (tid < kChunks) s.kv[tid] = q.n ? q.len + q.n : 0;
+            if (tid < kChunks) s.kv[tid] = tid >= a.rq.B ? -1 : q.n ? q.len + q.n : 0;
             __syncthreads();
             if (tid < a.rq.B) {
                 const int mine = s.kv[tid];
                 int at = 0;
-                for (int r = 0; r < a.rq.B; ++r) at += s.kv[r] > mine || (s.kv[r] == mine && r < tid);
+                for (int r = 0; r < a.rq.B; r += 4) {
+                    const int4 x = *reinterpret_cast<const int4 *>(s.kv + r);
+                    at += (x.x > mine || (x.x == mine && r < tid)) + (x.y > mine || (x.y == mine && r + 1 < tid)) +
+                          (x.z > mine || (x.z == mine && r + 2 < tid)) + (x.w > mine || (x.w == mine && r + 3 < tid));
+                }
                 s.order[at] = uint8_t(tid);
                 s.blocks[at] = int(blocks);
             }
