@@ -182,7 +182,7 @@ __device__ __forceinline__ Span span_of(const Args &a, const Unit &u, int stages
     Span s;
     int tile0;
     const int all = unit_tiles(a, u, stages, tile0);
-    const int from = int(int64_t(all) * part / u.parts), to = int(int64_t(all) * (part + 1) / u.parts);
+    const int from = all * part / u.parts, to = all * (part + 1) / u.parts;  // (2^18 tiles, 64 parts)
     s.tile0 = tile0 + from;
     s.tiles = to - from;
 #pragma unroll
@@ -633,19 +633,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     if (to[i]) to[i] += (lane & 3) * 16;
                 }
             }
-            const bool keep = n > 0 && l != 0.f;
+            // (without a tile there are no rows, or, of a part, sums that the join leaves out)
 #pragma unroll 1
-            for (int c = 0; c < D; c += C::kOut) {
+            for (int c = 0; n > 0 && c < D; c += C::kOut) {
                 uint32_t x[C::kOut / 32][32];
-                if (n > 0) {
 #pragma unroll
-                    for (int e = 0; e < C::kOut / 32; ++e) tc::ld32_async(t_o + c + 32 * e, x[e]);
-                    tc::ld_wait();
-                }
+                for (int e = 0; e < C::kOut / 32; ++e) tc::ld32_async(t_o + c + 32 * e, x[e]);
+                tc::ld_wait();
 #pragma unroll
                 for (int e = 0; e < C::kOut / 32; ++e) {
                     arrived(x[e]);
-                    if (!keep) {
+                    if (l == 0.f) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[e][i] = 0;
                     }
