@@ -55,7 +55,7 @@ constexpr int kSms = 152;
 constexpr float kSlack = 8.f;
 constexpr int kLeast = 4;    // tiles a part of a cut unit has at least
 constexpr int kMostParts = 64;
-constexpr double kEnds = 5.0, kPartEnds = 10.0;
+constexpr double kEnds = 5.0, kPartEnds = 10.0, kJoinCost = 4.0;  // tiles that they cost as much as
 constexpr int kAhead = 8;    // tiles of values that the ring holds at most: its slots
 
 struct Info {                // a unit's parts, for the join: parts 0: nothing to join
@@ -1267,7 +1267,9 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     // as one another run in full waves; the longest, which start first, matter where they are not small beside an SM's
     // share.  A unit's ends cost as much as kEnds tiles, those of a part, whose sums are written and read again, kPartEnds.
     // (8 requests of 60..2,048 rows behind 512..32,768 positions, 32/8 heads of 128: 1,270 us whole, 1,175 with 3 parts
-    // for every unit; 8 prompts of 512..12,000 rows, 32/4 heads: 1,050 whole, 1,490 with 7.)
+    // for every unit, 1,153 with 3 for the long ones; 8 prompts of 512..12,000 rows, 32/4 heads: 1,050 whole, 1,490 with
+    // 7; one of 2,000 rows, 4/1 heads of 128: 33.6 whole, 23.2 with 4; two of 1,500 and 3,000, 8/1 heads of 256: 48.4
+    // whole, 62.1 with 2.)
     const double rows = double(row_capacity) / B;
     double avg = ((total_len < int64_t(B) * max_len ? double(total_len) / B : double(max_len)) + 0.5 * rows) / kTile + 1.0;
     if (max_len == 0) avg = sqrt(avg * (0.5 * tiles + 1.0));  // of prompts: long ones have more units too
@@ -1275,7 +1277,7 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     int64_t s = 1;
     double best = 0.0;
     for (int64_t i = 1; p.units && i <= kMostParts && (i == 1 || i <= tiles / kLeast); ++i) {
-        const double ends = i > 1 ? kPartEnds : kEnds, longest = double(tiles) / i + ends;
+        const double ends = i > 1 ? kPartEnds : kEnds, longest = double(tiles) / i + kEnds;
         const double parts = avg * i > tiles ? avg * i / tiles : 1.0;
         double cost;
         if (avg > 0.75 * tiles) {
@@ -1283,10 +1285,10 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
         } else {
             cost = p.units * (avg + (parts > 1.0 ? ends : kEnds) * parts) / kSms;
             if (i == 1 && longest < 0.25 * cost) break;
-            cost += 0.7 * longest;
+            cost += 0.3 * longest;
         }
         if (cost < longest) cost = longest;
-        if (i > 1) cost = 1.05 * (cost + kEnds);
+        if (i > 1) cost = 1.05 * (cost + kJoinCost);
         if (i == 1 || cost < best) {
             best = cost;
             s = i;
