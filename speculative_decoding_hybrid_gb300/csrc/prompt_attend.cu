@@ -66,6 +66,7 @@ struct Args {
     CUtensorMap mq, mk, mv;
     prompt::Requests rq;
     int32_t h_q, h_kv, group, per_tile;  // per_tile: positions a query tile
+    int32_t join_rows;       // rows of a CTA of the join
     int32_t window, splits, part_tiles, negate;  // a unit's parts at most, and the tiles that one may have
     float scale_log2;
     int64_t o_stride;
@@ -91,7 +92,7 @@ struct Cfg {
     static constexpr int kPieces = D / kPiece;
     static constexpr int kSlot = kTile * kPiece * 2;
     static constexpr int kQTile = kTile * D * 2;
-    static constexpr int kRoom = 227 * 1024 - 3072 - kStages * kQTile;
+    static constexpr int kRoom = (227 - 3) * 1024 - kStages * kQTile;
     static constexpr int kSlots = kRoom / kSlot > 8 ? 8 : kRoom / kSlot;
     static constexpr int kSmem = kStages * kQTile + kSlots * kSlot + 1024;
     static constexpr int kSoftWarps = 4 * kStages;
@@ -1067,18 +1068,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     }
 }
 
-// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.
-constexpr int kJoinRows = 16;
+// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  It is latency, and the bytes of the
+// parts (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a time, 11 with eight in flight and CTAs of 8 rows).
+constexpr int kFew = 8;
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ Args a) {
     gdn::pdl_enter();
-    constexpr int kRows = Cfg<D>::kStages * kTile, W = D / 32;
+    constexpr int kRows = Cfg<D>::kStages * kTile, W = D / 32, V = W < 4 ? W : 4;  // channels of a lane, and of a load
     const Info f = a.info[blockIdx.x];
     const uint32_t status = a.status ? *reinterpret_cast<volatile uint32_t *>(a.status) : 0;
     if (f.parts == 0 || (status & GDN_DEV_TIMEOUT)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = warp; i < kJoinRows; i += 8) {
-        const int row = blockIdx.y * kJoinRows + i, st = row / kTile, in = row % kTile;
+    for (int i = warp; i < a.join_rows; i += 8) {
+        const int row = blockIdx.y * a.join_rows + i, st = row / kTile, in = row % kTile;
         const int tok = in / a.group, head = in - tok * a.group, at = f.tok0 + st * a.per_tile + tok;
         if (tok >= a.per_tile || at >= f.n) continue;
         const int64_t base = int64_t(blockIdx.x) * a.splits * kRows + row;
@@ -1100,27 +1102,48 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        // kFew parts' sums are in flight together (of a part without weight they say nothing)
         float acc[W] = {};
-#pragma unroll 4
-        for (int p = 0; p < f.parts; ++p) {
-            const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
-            const float lp = __shfl_sync(0xffffffffu, p < 32 ? x[0].y : x[1].y, p & 31);
-            if (lp == 0.f) continue;
-            const float *o = a.ws_o + (base + int64_t(p) * kRows) * D + lane * 2;
+        const float *from = a.ws_o + base * D + lane * V;
+#pragma unroll 1
+        for (int p0 = 0; p0 < f.parts; p0 += kFew) {
+            float y[kFew][W];
 #pragma unroll
-            for (int e = 0; e < W / 2; ++e) {
-                const float2 y = *reinterpret_cast<const float2 *>(o + e * 64);
-                acc[2 * e] = fmaf(y.x, wp, acc[2 * e]);
-                acc[2 * e + 1] = fmaf(y.y, wp, acc[2 * e + 1]);
+            for (int i = 0; i < kFew; ++i) {
+                if (p0 + i >= f.parts) break;
+                const float *o = from + int64_t(p0 + i) * kRows * D;
+#pragma unroll
+                for (int e = 0; e < W; e += V) {
+                    if constexpr (V == 4)
+                        *reinterpret_cast<float4 *>(&y[i][e]) = __ldcs(reinterpret_cast<const float4 *>(o + e * 32));
+                    else
+                        *reinterpret_cast<float2 *>(&y[i][e]) = __ldcs(reinterpret_cast<const float2 *>(o + e * 32));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                const int p = p0 + i;
+                const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
+                const float lp = __shfl_sync(0xffffffffu, p < 32 ? x[0].y : x[1].y, p & 31);
+                if (p >= f.parts || lp == 0.f) continue;
+#pragma unroll
+                for (int e = 0; e < W; ++e) acc[e] = fmaf(y[i][e], wp, acc[e]);
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int h = f.hk * a.group + head;
-        uint16_t *o = a.o + (int64_t(f.t0) + at) * a.o_stride + int64_t(h) * D + lane * 2;
+        uint16_t *o = a.o + (int64_t(f.t0) + at) * a.o_stride + int64_t(h) * D + lane * V;
 #pragma unroll
-        for (int e = 0; e < W / 2; ++e)
-            *reinterpret_cast<uint32_t *>(o + e * 64) =
-                gdn::f32_to_bf16(acc[2 * e] * inv) | uint32_t(gdn::f32_to_bf16(acc[2 * e + 1] * inv)) << 16;
+        for (int e = 0; e < W; e += V) {
+            uint32_t r[V / 2];
+#pragma unroll
+            for (int c = 0; c < V; c += 2)
+                r[c / 2] = gdn::f32_to_bf16(acc[e + c] * inv) | uint32_t(gdn::f32_to_bf16(acc[e + c + 1] * inv)) << 16;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2 *>(o + e * 32) = make_uint2(r[0], r[1]);
+            else
+                *reinterpret_cast<uint32_t *>(o + e * 32) = r[0];
+        }
         if (lane == 0 && a.lse)
             a.lse[(int64_t(f.t0) + at) * a.h_q + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
     }
@@ -1321,7 +1344,7 @@ int launch(const Args &a, const Plan &p, cudaStream_t st) {
     const int rc = gdn_host::launch_pdl(prompt_attend_kernel<D>, dim3(unsigned(p.units), unsigned(p.splits)),
                                         dim3(C::kThreads), C::kSmem, st, a);
     if (rc != GDN_OK || p.splits == 1) return rc;
-    return gdn_host::launch_pdl(prompt_join_kernel<D>, dim3(unsigned(p.units), unsigned(p.rows / kJoinRows)), dim3(256),
+    return gdn_host::launch_pdl(prompt_join_kernel<D>, dim3(unsigned(p.units), unsigned(p.rows / a.join_rows)), dim3(256),
                                 0, st, a);
 }
 
@@ -1329,6 +1352,9 @@ int run(Args &a, const Plan &p, int d, float sm_scale, uint8_t *parts, cudaStrea
     a.per_tile = p.per_tile;
     a.splits = p.splits;
     a.part_tiles = p.part_tiles;
+    // rows of a CTA of the join: few of few rows are latency; many start too many CTAs
+    // (8 chunks of 60 to 2,048 rows, the call: 1,169 us with 8, 1,155 with 32; 32 rows behind 32,000 tokens: 55.8 and 80)
+    a.join_rows = p.units * p.rows >= 2 * kSms * 32 ? 32 : 8;
     a.negate = sm_scale < 0.f;
     const float c = fabsf(sm_scale) * 1.4426950408889634f;
     a.scale_log2 = c < 1e-37f ? 1e-37f : c;  // a masked score times zero would be no number
