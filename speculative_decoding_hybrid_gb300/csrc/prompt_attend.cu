@@ -1069,7 +1069,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
 }
 
 // Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  It is latency, and the bytes of the
-// parts (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a time, 11 with eight in flight and CTAs of 8 rows).
+// parts (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a time, 11 with eight in flight and CTAs of 8
+// rows).
 constexpr int kFew = 8;
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ Args a) {

@@ -32,8 +32,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_object(stream):
     return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _stream_on(stream, device: int):
+    stream = _stream_object(stream)
+    if stream.device_index != device:
+        raise ValueError("the stream must be one of the rows' device")
+    return stream
 
 
 class Kv8Cache:
@@ -213,10 +223,15 @@ class Kv8Cache:
             if len(self._workspace) > 4096:
                 self._workspace.clear()
             need = self._workspace[key] = gs.lib.kv8_chunk_workspace_bytes(self._c, *key)
+        if _current_device() != device:
+            with torch.cuda.device(device):  # the library launches on the current one
+                return self.attend_chunk(layer, table, cache_len, cu_rows, q, k_new, v_new, max_len, max_rows,
+                                         total_len, want_lse, out, stream)
         if stream is not None:
             # what the call allocates belongs to the stream it runs on
+            stream = _stream_on(stream, device)
             before = torch.cuda.current_stream(self._device)
-            torch.cuda.set_stream(_stream_object(stream))
+            torch.cuda.set_stream(stream)
         try:
             raw = _raw_stream(device)
             if out is None:

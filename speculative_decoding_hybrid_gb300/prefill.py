@@ -19,7 +19,7 @@ import numpy as np
 import torch
 
 from . import binding as gs
-from .kvcache import _BF16, _I32, _raw_stream, _stream_object
+from .kvcache import _BF16, _I32, _current_device, _raw_stream, _stream_on
 
 SCALINGS = ("none", "linear", "base", "parts")
 
@@ -120,10 +120,14 @@ class Rope:
                 raise self._bad("k")
         elif k_out is not None:
             raise ValueError("k_out without k")
+        if _current_device() != index:
+            with torch.cuda.device(index):  # the library launches on the current one
+                return self.rotate(q, k, cu_rows, cache_len, status, False, q_out, k_out, stream)
         if stream is not None:
             # what the call allocates belongs to the stream it runs on
+            stream = _stream_on(stream, index)
             before = torch.cuda.current_stream(self._device)
-            torch.cuda.set_stream(_stream_object(stream))
+            torch.cuda.set_stream(stream)
         try:
             raw = _raw_stream(index)
             if q_out is None:
@@ -219,10 +223,14 @@ def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: t
         plan = _workspace[key] = ctypes.byref(dims), gs.attn_prompts_workspace_bytes(dims, B, R, max_rows)
     dims, need = plan
     device = q.device
+    if _current_device() != index:
+        with torch.cuda.device(index):  # the library launches on the current one
+            return attend_prompts(q, k, v, cu_rows, max_rows, status, window, sm_scale, want_lse, out, stream)
     if stream is not None:
         # what the call allocates belongs to the stream it runs on
+        stream = _stream_on(stream, index)
         before = torch.cuda.current_stream(device)
-        torch.cuda.set_stream(_stream_object(stream))
+        torch.cuda.set_stream(stream)
     try:
         raw = _raw_stream(index)
         if out is None:
