@@ -40,8 +40,8 @@
 // 12,000 tokens, 32/4 heads of 128, 1.06 ms, 1,380 TFLOP/s: a query tile's chain of scores ->
 // tensor-memory load (500 clocks beside products, 60 alone) -> maximum -> exponentials ->
 // products, 2,800 clocks a tile for 2,048 of products; short prompts (16 of 100 to 4,000
-// tokens, 32/8 heads: 0.47 ms, 1,150 TFLOP/s) the ends of units, 3 us each.  A single short
-// prompt is one chain: 37 tokens, 16/2 heads of 256, 9.8 us.
+// tokens, 32/8 heads: 0.46 ms, 1,165 TFLOP/s) the ends of units, 3 us each.  A single short
+// prompt is one chain: 37 tokens, 16/2 heads of 256, 9.4 us.
 #include "kv8_math.cuh"
 #include "prompt.cuh"
 #include "tmap.cuh"
@@ -1068,11 +1068,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     }
 }
 
-// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  It is latency, and the bytes of the
-// parts (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a time, 11 with eight in flight and CTAs of 8
-// rows).
+// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  Of few parts a lane takes every m and
+// l itself (8 chunks of 60 to 2,048 rows in up to 3 parts, 139 MB cold: 56 us -> 45); of many, a lane those of every 32nd
+// part, and kFew parts' sums are in flight together (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a
+// time, 11 with eight in flight and CTAs of 8 rows).  It is latency and CTAs to start: many of the parts' bounds are idle.
 constexpr int kFew = 8;
 template <int D>
+__device__ __forceinline__ void load_part(float (&y)[D / 32], const float *o) {
+    constexpr int W = D / 32, V = W < 4 ? W : 4;
+#pragma unroll
+    for (int e = 0; e < W; e += V) {
+        if constexpr (V == 4)
+            *reinterpret_cast<float4 *>(&y[e]) = __ldcs(reinterpret_cast<const float4 *>(o + e * 32));
+        else
+            *reinterpret_cast<float2 *>(&y[e]) = __ldcs(reinterpret_cast<const float2 *>(o + e * 32));
+    }
+}
+
+template <int D, bool MANY>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ Args a) {
     gdn::pdl_enter();
     constexpr int kRows = Cfg<D>::kStages * kTile, W = D / 32, V = W < 4 ? W : 4;  // channels of a lane, and of a load
@@ -1080,55 +1093,72 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
     const uint32_t status = a.status ? *reinterpret_cast<volatile uint32_t *>(a.status) : 0;
     if (f.parts == 0 || (status & GDN_DEV_TIMEOUT)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned over = 65536u / unsigned(a.group) + 1;  // x / group = x * over >> 16 for x < 128, group <= 64
     for (int i = warp; i < a.join_rows; i += 8) {
         const int row = blockIdx.y * a.join_rows + i, st = row / kTile, in = row % kTile;
-        const int tok = in / a.group, head = in - tok * a.group, at = f.tok0 + st * a.per_tile + tok;
+        const int tok = in * over >> 16, head = in - tok * a.group, at = f.tok0 + st * a.per_tile + tok;
         if (tok >= a.per_tile || at >= f.n) continue;
         const int64_t base = int64_t(blockIdx.x) * a.splits * kRows + row;
-        float2 x[kMostParts / 32];
-        float top = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kMostParts / 32; ++e) {
-            const int p = lane + 32 * e;
-            x[e] = p < f.parts ? a.ws_ml[base + int64_t(p) * kRows] : make_float2(-INFINITY, 0.f);
-            top = fmaxf(top, x[e].x);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float w[kMostParts / 32], l = 0.f;
-#pragma unroll
-        for (int e = 0; e < kMostParts / 32; ++e) {
-            w[e] = x[e].y == 0.f ? 0.f : ex2(x[e].x - top);
-            l += x[e].y == 0.f ? 0.f : x[e].y * w[e];
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        // kFew parts' sums are in flight together (of a part without weight they say nothing)
-        float acc[W] = {};
+        const float2 *ml = a.ws_ml + base;
         const float *from = a.ws_o + base * D + lane * V;
-#pragma unroll 1
-        for (int p0 = 0; p0 < f.parts; p0 += kFew) {
+        float acc[W] = {}, top = -INFINITY, l = 0.f;
+        // (of a part without weight its sums say nothing)
+        if constexpr (!MANY) {
+            float2 x[kFew];
             float y[kFew][W];
 #pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                if (p0 + i >= f.parts) break;
-                const float *o = from + int64_t(p0 + i) * kRows * D;
-#pragma unroll
-                for (int e = 0; e < W; e += V) {
-                    if constexpr (V == 4)
-                        *reinterpret_cast<float4 *>(&y[i][e]) = __ldcs(reinterpret_cast<const float4 *>(o + e * 32));
-                    else
-                        *reinterpret_cast<float2 *>(&y[i][e]) = __ldcs(reinterpret_cast<const float2 *>(o + e * 32));
-                }
+            for (int p = 0; p < kFew; ++p) {
+                if (p >= f.parts) break;
+                x[p] = ml[p * kRows];
+                load_part<D>(y[p], from + p * kRows * D);
             }
 #pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                const int p = p0 + i;
-                const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
-                const float lp = __shfl_sync(0xffffffffu, p < 32 ? x[0].y : x[1].y, p & 31);
-                if (p >= f.parts || lp == 0.f) continue;
+            for (int p = 0; p < kFew; ++p)
+                if (p < f.parts) top = fmaxf(top, x[p].x);
 #pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] = fmaf(y[i][e], wp, acc[e]);
+            for (int p = 0; p < kFew; ++p) {
+                if (p >= f.parts) break;
+                if (x[p].y == 0.f) continue;
+                const float w = ex2(x[p].x - top);
+                l = fmaf(x[p].y, w, l);
+#pragma unroll
+                for (int e = 0; e < W; ++e) acc[e] = fmaf(y[p][e], w, acc[e]);
+            }
+        } else {
+            float2 x[kMostParts / 32];
+#pragma unroll
+            for (int e = 0; e < kMostParts / 32; ++e) {
+                const int p = lane + 32 * e;
+                x[e] = p < f.parts ? ml[int64_t(p) * kRows] : make_float2(-INFINITY, 0.f);
+                top = fmaxf(top, x[e].x);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float w[kMostParts / 32];
+#pragma unroll
+            for (int e = 0; e < kMostParts / 32; ++e) {
+                w[e] = x[e].y == 0.f ? 0.f : ex2(x[e].x - top);
+                l += x[e].y == 0.f ? 0.f : x[e].y * w[e];
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll 1
+            for (int p0 = 0; p0 < f.parts; p0 += kFew) {
+                float y[kFew][W];
+#pragma unroll
+                for (int i = 0; i < kFew; ++i) {
+                    if (p0 + i >= f.parts) break;
+                    load_part<D>(y[i], from + int64_t(p0 + i) * kRows * D);
+                }
+#pragma unroll
+                for (int i = 0; i < kFew; ++i) {
+                    const int p = p0 + i;
+                    const float wp = __shfl_sync(0xffffffffu, p < 32 ? w[0] : w[1], p & 31);
+                    const float lp = __shfl_sync(0xffffffffu, p < 32 ? x[0].y : x[1].y, p & 31);
+                    if (p >= f.parts || lp == 0.f) continue;
+#pragma unroll
+                    for (int e = 0; e < W; ++e) acc[e] = fmaf(y[i][e], wp, acc[e]);
+                }
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1345,16 +1375,18 @@ int launch(const Args &a, const Plan &p, cudaStream_t st) {
     const int rc = gdn_host::launch_pdl(prompt_attend_kernel<D>, dim3(unsigned(p.units), unsigned(p.splits)),
                                         dim3(C::kThreads), C::kSmem, st, a);
     if (rc != GDN_OK || p.splits == 1) return rc;
-    return gdn_host::launch_pdl(prompt_join_kernel<D>, dim3(unsigned(p.units), unsigned(p.rows / a.join_rows)), dim3(256),
-                                0, st, a);
+    const dim3 grid(unsigned(p.units), unsigned(p.rows / a.join_rows));
+    return p.splits > kFew ? gdn_host::launch_pdl(prompt_join_kernel<D, true>, grid, dim3(256), 0, st, a)
+                           : gdn_host::launch_pdl(prompt_join_kernel<D, false>, grid, dim3(256), 0, st, a);
 }
 
 int run(Args &a, const Plan &p, int d, float sm_scale, uint8_t *parts, cudaStream_t st) {
     a.per_tile = p.per_tile;
     a.splits = p.splits;
     a.part_tiles = p.part_tiles;
-    // rows of a CTA of the join: few of few rows are latency; many start too many CTAs
-    // (8 chunks of 60 to 2,048 rows, the call: 1,169 us with 8, 1,155 with 32; 32 rows behind 32,000 tokens: 55.8 and 80)
+    // Rows of a CTA of the join: of few rows it is latency, of many CTAs to start (whole calls: 8 chunks of 60 to 2,048
+    // rows 1,174 us with 8, 1,144 with 32, 1,140 with 64; 3 of 100 to 300 74.2 with 32, 75.9 with 64; 32 rows behind
+    // 32,000 tokens 55.8 with 8, 80 with 32).
     a.join_rows = p.units * p.rows >= 2 * kSms * 32 ? 32 : 8;
     a.negate = sm_scale < 0.f;
     const float c = fabsf(sm_scale) * 1.4426950408889634f;
