@@ -40,7 +40,7 @@
 // 12,000 tokens, 32/4 heads of 128, 1.06 ms, 1,380 TFLOP/s: a query tile's chain of scores ->
 // tensor-memory load (500 clocks beside products, 60 alone) -> maximum -> exponentials ->
 // products, 2,800 clocks a tile for 2,048 of products; short prompts (16 of 100 to 4,000
-// tokens, 32/8 heads: 0.46 ms, 1,165 TFLOP/s) the ends of units, 3 us each.  A single short
+// tokens, 32/8 heads: 0.46 ms, 1,160 TFLOP/s) the ends of units, 3 us each.  A single short
 // prompt is one chain: 37 tokens, 16/2 heads of 256, 9.4 us.
 #include "kv8_math.cuh"
 #include "prompt.cuh"
@@ -1068,10 +1068,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
     }
 }
 
-// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  Of few parts a lane takes every m and
-// l itself (8 chunks of 60 to 2,048 rows in up to 3 parts, 139 MB cold: 56 us -> 45); of many, a lane those of every 32nd
+// Joins a unit's parts: o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p, a warp a row.  Of few parts a lane takes every m
+// and l itself (8 chunks of 60 to 2,048 rows in up to 3 parts, 139 MB cold: 56 us -> 45); of many, those of every 32nd
 // part, and kFew parts' sums are in flight together (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a
-// time, 11 with eight in flight and CTAs of 8 rows).  It is latency and CTAs to start: many of the parts' bounds are idle.
+// time, 11 with eight in flight and CTAs of 8 rows).  Latency bounds it, and CTAs to start, many for units that are not.
 constexpr int kFew = 8;
 template <int D>
 __device__ __forceinline__ void load_part(float (&y)[D / 32], const float *o) {
@@ -1320,10 +1320,9 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     // Work is cut where SMs would idle, into parts of up to tiles / i tiles.  All units share the SMs; units about as long
     // as one another run in full waves; the longest, which start first, matter where they are not small beside an SM's
     // share.  A unit's ends cost as much as kEnds tiles, those of a part, whose sums are written and read again, kPartEnds.
-    // (8 requests of 60..2,048 rows behind 512..32,768 positions, 32/8 heads of 128: 1,270 us whole, 1,175 with 3 parts
-    // for every unit, 1,153 with 3 for the long ones; 8 prompts of 512..12,000 rows, 32/4 heads: 1,050 whole, 1,490 with
-    // 7; one of 2,000 rows, 4/1 heads of 128: 33.6 whole, 23.2 with 4; two of 1,500 and 3,000, 8/1 heads of 256: 48.4
-    // whole, 62.1 with 2.)
+    // (8 requests of 60..2,048 rows behind 512..32,768 positions, 32/8 heads of 128: 1,270 us whole, 1,144 with 3 for
+    // the long ones; 8 prompts of 512..12,000 rows, 32/4 heads: 1,050 whole, 1,490 with 7; one of 2,000 rows, 4/1 heads
+    // of 128: 33.6 whole, 21.2 with 4; two of 1,500 and 3,000, 8/1 heads of 256: 48.4 whole, 62.1 with 2.)
     const double rows = double(row_capacity) / B;
     double avg = ((total_len < int64_t(B) * max_len ? double(total_len) / B : double(max_len)) + 0.5 * rows) / kTile + 1.0;
     if (max_len == 0) avg = sqrt(avg * (0.5 * tiles + 1.0));  // of prompts: long ones have more units too
