@@ -7,7 +7,9 @@
 //   S = Q K^T                 scores, fp32 in tensor memory, a row in a lane
 //   p = 2^(c S - m)           a thread a row: its maximum, exponentials and sum in registers
 //   O += P V                  P in bf16 from tensor memory
-// with m moved (and O rescaled) only when a score passes it by 2^8.  At d <= 128 a unit has
+// with m moved (and O rescaled) only when a score passes it by 2^8.  m is a rounded product, which
+// c x - m is not: from 2^20 on, where a row's largest weight would not be near 1 for it, the largest
+// score is taken off the scores before the scale instead.  At d <= 128 a unit has
 // two query tiles that share the keys, so one's softmax runs beside the other's products; at
 // d = 256, where one tile's O takes half of tensor memory, the softmax of a tile of positions
 // runs beside the products of its neighbours.  P lies where S lay, but for d = 64, which
@@ -53,6 +55,7 @@ using namespace kv8;
 constexpr int kTile = 128;   // positions a tile, and rows of a query tile
 constexpr int kSms = 152;
 constexpr float kSlack = 8.f;
+constexpr float kFar = 0x1p20f;  // below it c x is off by 2^-5 at most
 constexpr int kLeast = 4;    // tiles a part of a cut unit has at least
 constexpr int kMostParts = 64;
 constexpr double kEnds = 5.0, kPartEnds = 10.0, kJoinCost = 4.0;  // tiles that they cost as much as
@@ -541,7 +544,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             // (rows of nobody: weights of 0)
             const auto position = [&] { return w.u.tok0 + st * a.per_tile + tok; };
             const auto valid = [&] { return tok < a.per_tile && position() < w.u.n; };
-            float m = valid() ? -INFINITY : INFINITY, l = 0.f;
+            // Weights are 2^(c x - m), from kFar on 2^(c (x - base)): then m stays -inf, so that every tile is looked at.
+            float m = valid() ? -INFINITY : INFINITY, l = 0.f, base = 0.f;
             for (int j = 0; j < n; ++j, ++g) {
                 const int slot = kStages == 2 ? st : g & 1, turn = kStages == 2 ? g : g >> 1;
                 if (!wait(&s.s_full[slot], turn)) break;
@@ -563,15 +567,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                     hide(x[0], hi, lo);
                     hide(x[1], hi - kHalf, lo - kHalf);
                 }
-                const float z = fmaxf(top_of(x[0]), top_of(x[1])) * a.scale_log2;
+                const float top = fmaxf(top_of(x[0]), top_of(x[1])), z = top * a.scale_log2;
                 if constexpr (C::kApart) {
                     // the last tile's products are done with the sums and the weights
                     if (j > 0 && !wait(&s.o_done[st], g - 1)) break;
                     tc::fence_after();
                 }
                 if (__any_sync(0xffffffffu, z > m + kSlack)) {
-                    const float now = fmaxf(m, z), f = m == now ? 1.f : ex2(m - now);  // (-inf less -inf is no number)
-                    if (j > 0) {
+                    float f = 1.f;
+                    if (base == 0.f ? z > m : top > base) {
+                        const float last_m = base == 0.f ? m : 0.f, last_base = base;
+                        const bool far = fabsf(z) >= kFar && fabsf(top) < INFINITY;
+                        base = far ? top : 0.f;
+                        m = far ? -INFINITY : z;
+                        f = ex2(fmaf(a.scale_log2, last_base - base, last_m - (far ? 0.f : z)));
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                         // (with two query tiles and no room the scores are behind the products before)
                         if (kStages == 1 && !wait(&s.o_done[(g - 1) & 1], (g - 1) >> 1)) break;
                         tc::fence_after();
@@ -587,7 +598,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                         }
                     }
                     l *= f;
-                    m = now;
+                    if (__any_sync(0xffffffffu, base != 0.f)) {
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            x[i / kHalf][i % kHalf] = __float_as_uint(__uint_as_float(x[i / kHalf][i % kHalf]) - base);
+                    }
                 }
                 // The products with the first half's weights run beside the second half's exponentials.
                 const float r = m == -INFINITY ? 0.f : -m;
@@ -671,9 +686,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             if (write && whole) {
                 if (a.lse)
                     a.lse[(int64_t(w.u.t0) + at) * a.h_q + h] =
-                        l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;  // (l is 1 or more)
+                        l == 0.f ? -INFINITY
+                                 : fmaf(a.scale_log2, base, (base == 0.f ? m : 0.f) + __log2f(l)) * 0.6931471805599453f;
             } else if (write) {
-                a.ws_ml[wrow] = make_float2(m, l);
+                a.ws_ml[wrow] = base == 0.f ? make_float2(m, l) : make_float2(base, copysignf(l, -1.f));
             }
             if (tid == 0 && w.part == 0 && a.info) {
                 Info f = {};
@@ -1073,6 +1089,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
 // part, and kFew parts' sums are in flight together (32 rows of 16/2 heads of 256 in 38 parts: 39 us with a part at a
 // time, 11 with eight in flight and CTAs of 8 rows).  Latency bounds it, and CTAs to start, many for units that are not.
 constexpr int kFew = 8;
+// A part's reference, c x + y, of its (m, l) as written: a base has l's sign; and how far one is above another.
+__device__ __forceinline__ float2 reference_of(float2 ml) {
+    return signbit(ml.y) ? make_float2(ml.x, 0.f) : make_float2(0.f, ml.x);
+}
+__device__ __forceinline__ float above(float2 a, float2 b, float c) { return fmaf(c, a.x - b.x, a.y - b.y); }
 template <int D>
 __device__ __forceinline__ void load_part(float (&y)[D / 32], const float *o) {
     constexpr int W = D / 32, V = W < 4 ? W : 4;
@@ -1101,7 +1122,13 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
         const int64_t base = int64_t(blockIdx.x) * a.splits * kRows + row;
         const float2 *ml = a.ws_ml + base;
         const float *from = a.ws_o + base * D + lane * V;
-        float acc[W] = {}, top = -INFINITY, l = 0.f;
+        float acc[W] = {}, l = 0.f;
+        float2 top = make_float2(0.f, -INFINITY);
+        // (two references of -inf are a NaN apart, which is not above 0)
+        const auto raise = [&](float2 y) {
+            if (above(y, top, a.scale_log2) > 0.f) top = y;
+        };
+        bool based = false;  // whether some part has one; then x becomes how far it is below the top
         // (of a part without weight its sums say nothing)
         if constexpr (!MANY) {
             float2 x[kFew];
@@ -1114,13 +1141,23 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
             }
 #pragma unroll
             for (int p = 0; p < kFew; ++p)
-                if (p < f.parts) top = fmaxf(top, x[p].x);
+                if (p < f.parts) top.y = fmaxf(top.y, x[p].x), based |= signbit(x[p].y);
+            if (based) {
+                top.y = -INFINITY;
+#pragma unroll
+                for (int p = 0; p < kFew; ++p)
+                    if (p < f.parts) raise(reference_of(x[p]));
+#pragma unroll
+                for (int p = 0; p < kFew; ++p)
+                    if (p < f.parts) x[p].x = above(reference_of(x[p]), top, a.scale_log2);
+            }
+            const float from_top = based ? 0.f : top.y;
 #pragma unroll
             for (int p = 0; p < kFew; ++p) {
                 if (p >= f.parts) break;
                 if (x[p].y == 0.f) continue;
-                const float w = ex2(x[p].x - top);
-                l = fmaf(x[p].y, w, l);
+                const float w = ex2(x[p].x - from_top);
+                l = fmaf(fabsf(x[p].y), w, l);
 #pragma unroll
                 for (int e = 0; e < W; ++e) acc[e] = fmaf(y[p][e], w, acc[e]);
             }
@@ -1130,15 +1167,30 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
             for (int e = 0; e < kMostParts / 32; ++e) {
                 const int p = lane + 32 * e;
                 x[e] = p < f.parts ? ml[int64_t(p) * kRows] : make_float2(-INFINITY, 0.f);
-                top = fmaxf(top, x[e].x);
+                top.y = fmaxf(top.y, x[e].x);
+                based |= signbit(x[e].y);
             }
+            based = __any_sync(0xffffffffu, based);
+            if (based) {
+                top.y = -INFINITY;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int e = 0; e < kMostParts / 32; ++e) raise(reference_of(x[e]));
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    raise(make_float2(__shfl_xor_sync(0xffffffffu, top.x, o), __shfl_xor_sync(0xffffffffu, top.y, o)));
+#pragma unroll
+                for (int e = 0; e < kMostParts / 32; ++e)
+                    x[e].x = above(reference_of(x[e]), top, a.scale_log2);
+            } else {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
+            }
+            const float from_top = based ? 0.f : top.y;
             float w[kMostParts / 32];
 #pragma unroll
             for (int e = 0; e < kMostParts / 32; ++e) {
-                w[e] = x[e].y == 0.f ? 0.f : ex2(x[e].x - top);
-                l += x[e].y == 0.f ? 0.f : x[e].y * w[e];
+                w[e] = x[e].y == 0.f ? 0.f : ex2(x[e].x - from_top);
+                l += x[e].y == 0.f ? 0.f : fabsf(x[e].y) * w[e];
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -1176,7 +1228,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
                 *reinterpret_cast<uint32_t *>(o + e * 32) = r[0];
         }
         if (lane == 0 && a.lse)
-            a.lse[(int64_t(f.t0) + at) * a.h_q + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+            a.lse[(int64_t(f.t0) + at) * a.h_q + h] =
+                l == 0.f ? -INFINITY : fmaf(a.scale_log2, top.x, top.y + log2f(l)) * 0.6931471805599453f;
     }
 }
 
