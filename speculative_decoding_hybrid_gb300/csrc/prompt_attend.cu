@@ -681,7 +681,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
             }
             if (fix) {
                 __syncwarp();
-                if (write && n > 0) add_special<D>(a, w, w.u.len + at, row_o, row_p);
+                // (a row of nothing but -inf is zero, whatever the values)
+                if (write && n > 0 && l != 0.f) add_special<D>(a, w, w.u.len + at, row_o, row_p);
             }
             if (write && whole) {
                 if (a.lse)

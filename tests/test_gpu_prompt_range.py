@@ -1,5 +1,6 @@
 """Attention of prompts and chunks where scores and values are far from ordinary: finite scores up to 2^125 that are not
-powers of two, infinite ones, values up to 2^90, in whole units and in units cut into parts; against the fp64 form.
+powers of two, infinite ones, rows that see nothing but -inf, values up to 2^90, in whole units and in units cut into
+parts; against the fp64 form.
 
 Scores come of one channel of q and of k, so that the products of their 8-bit significands are exact in fp32 and a
 score's error is the scale's alone: the budget is prompt_util's without its term for scores.  Weights of positions whose
@@ -194,3 +195,17 @@ def test_large_values(cuda_dev, d):
         ob, lb = pu.bounds(ro, rl, ra, rw, d)
         assert noted("prompt range 2^90: o", np.max(np.abs(o - ro) / ob)) <= 1.0
         assert noted("prompt range 2^90: lse", np.max(np.abs(lse - rl) / lb)) <= 1.0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n", [200, 1500])
+def test_rows_of_nothing_but_minus_infinity_are_zero(cuda_dev, d, what, n):
+    """o = 0 and lse = -inf whatever the values hold there, in tiles that every row sees and in others."""
+    q, k, v = np.zeros((n, 1, d)), np.zeros((n, 1, d)), np.random.RandomState(d).standard_normal((n, 1, d))
+    q[:, 0, 3], k[:, 0, 3] = -1.0, np.inf
+    k[n - 1, 0, 3] = 1.0
+    v[[0, 50, 127, 128, 150, n - 2], 0, 5] = what
+    (o, lse), _ = prompts([n], q, k, v, cuda_dev, cut=n > 1000)
+    assert (o[:n - 1] == 0).all() and np.isneginf(lse[:n - 1]).all()
+    assert np.isfinite(lse[n - 1]).all() and np.isfinite(np.delete(o[n - 1, 0], 5)).all()
