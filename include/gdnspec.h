@@ -750,15 +750,15 @@ typedef struct attn_dims {
  *   overlap an input.  Requests have at most max_rows rows.
  *   Scores, sums and softmax statistics are fp32; a weight enters the product
  *   with v rounded to bf16 (by 2^-8 of it at most; lse is of the unrounded
- *   ones).  |sm_scale q.k| up to 2^125, |v| up to 2^90.  A score that is NaN or
- *   +inf makes its row's outputs NaN; one of -inf has no weight, and a row with
- *   no other gets o = 0 and lse = -inf, whatever v holds.  A v that is not
- *   finite makes the outputs of its channel infinite or NaN in the rows that
- *   see it at a score above -inf (at -inf it may).  What a row does not see
- *   does not reach it, whatever it holds.  How long requests are
- *   cut into parts, and so the order of their sums, goes by the call's bounds
- *   (B, row_capacity, max_rows; of kv8_chunk max_len and total_len too); with
- *   the same bounds a call gives the same bits.
+ *   ones).  |q.k| and |sm_scale q.k| up to 2^125, |v| up to 2^90.  A score that
+ *   is NaN or +inf makes its row's outputs NaN; one of -inf has no weight, and
+ *   a row with no other gets o = 0 and lse = -inf, whatever v holds.  A v that
+ *   is not finite makes the outputs of its channel infinite or NaN in the rows
+ *   that see it at a score above -inf (at -inf it may).  What a row does not
+ *   see does not reach it, whatever it holds.  How long requests are cut into
+ *   parts, and so the order of their sums, goes by the call's bounds (B,
+ *   row_capacity, max_rows; of kv8_chunk max_len and total_len too); with the
+ *   same bounds a call gives the same bits.
  *   Bad rows set GDN_DEV_ROWS_BAD: the request is skipped (its o and lse are
  *   not written).  A bounded wait that runs out sets GDN_DEV_TIMEOUT: outputs
  *   of that call are not to be trusted, and while *dev_status holds it calls

@@ -1443,7 +1443,7 @@ int run(Args &a, const Plan &p, int d, float sm_scale, uint8_t *parts, cudaStrea
     a.join_rows = p.units * p.rows >= 2 * kSms * 32 ? 32 : 8;
     a.negate = sm_scale < 0.f;
     const float c = fabsf(sm_scale) * 1.4426950408889634f;
-    a.scale_log2 = c < 1e-37f ? 1e-37f : c;  // a masked score times zero would be no number
+    a.scale_log2 = c == 0.f ? 0x1p-149f : c;  // a masked score times zero would be no number; times this, any score is 0
     if (p.splits > 1) {
         const size_t rows = size_t(p.units) * p.splits * p.rows;
         a.ws_o = reinterpret_cast<float *>(parts);

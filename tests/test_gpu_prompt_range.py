@@ -1,6 +1,6 @@
 """Attention of prompts and chunks where scores and values are far from ordinary: finite scores up to 2^125 that are not
-powers of two, infinite ones, rows that see nothing but -inf, values up to 2^90, in whole units and in units cut into
-parts; against the fp64 form.
+powers of two, infinite ones, rows that see nothing but -inf, values up to 2^90, scales of next to nothing, in whole
+units and in units cut into parts; against the fp64 form.
 
 Scores come of one channel of q and of k, so that the products of their 8-bit significands are exact in fp32 and a
 score's error is the scale's alone: the budget is prompt_util's without its term for scores.  Weights of positions whose
@@ -209,3 +209,13 @@ def test_rows_of_nothing_but_minus_infinity_are_zero(cuda_dev, d, what, n):
     (o, lse), _ = prompts([n], q, k, v, cuda_dev, cut=n > 1000)
     assert (o[:n - 1] == 0).all() and np.isneginf(lse[:n - 1]).all()
     assert np.isfinite(lse[n - 1]).all() and np.isfinite(np.delete(o[n - 1, 0], 5)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sm_scale", [0.0, 1e-42, -1e-42, 1e-39, -2e-38])
+def test_scales_of_next_to_nothing(cuda_dev, d, sm_scale):
+    """Large q.k under a scale of zero, or of a subnormal number: nearly every position weighs the same."""
+    for n, cut in ((150, False), (1500, True)):
+        q, k, v = _scores(n, 2, 1, d, "both", 122, 3)
+        got, (q, k, v) = prompts([n], q, k, v, cuda_dev, sm_scale=sm_scale, cut=cut)
+        check("small scale", got, pu.attend(q, k, v, 0, float(np.float32(sm_scale))))
