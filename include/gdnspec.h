@@ -762,7 +762,8 @@ typedef struct attn_dims {
  *   Bad rows set GDN_DEV_ROWS_BAD: the request is skipped (its o and lse are
  *   not written).  A bounded wait that runs out sets GDN_DEV_TIMEOUT: outputs
  *   of that call are not to be trusted, and while *dev_status holds it calls
- *   write nothing.  B <= 65535; max_rows <= 2^25.  workspace:
+ *   write nothing.  dev_status may be NULL: then the same is skipped and
+ *   nothing says so.  B <= 65535; max_rows <= 2^25.  workspace:
  *   attn_prompts_workspace_bytes(...) device bytes (16-byte aligned, no
  *   initialisation, one call at a time), 0 when no work is cut.
  */

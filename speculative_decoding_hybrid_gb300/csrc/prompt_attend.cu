@@ -1405,8 +1405,9 @@ Plan plan_of(int h_q, int h_kv, int d, int window, int32_t B, int32_t row_capaci
     p.splits = int(s);
     return p;
 }
+// (at the end a status word, for calls without one: by it the join knows that units' records were written)
 size_t part_bytes(const Plan &p, int d) {
-    return p.splits > 1 ? size_t(p.units) * (size_t(p.splits) * p.rows * (size_t(d) * 4 + 8) + sizeof(Info)) : 0;
+    return p.splits > 1 ? size_t(p.units) * (size_t(p.splits) * p.rows * (size_t(d) * 4 + 8) + sizeof(Info)) + 16 : 0;
 }
 size_t kv_bytes(const kv8_cache *c, int64_t rows) { return size_t(rows) * c->h_kv * c->d * 4; }
 
@@ -1449,6 +1450,10 @@ int run(Args &a, const Plan &p, int d, float sm_scale, uint8_t *parts, cudaStrea
         a.ws_o = reinterpret_cast<float *>(parts);
         a.ws_ml = reinterpret_cast<float2 *>(a.ws_o + rows * d);
         a.info = reinterpret_cast<Info *>(a.ws_ml + rows);
+        if (!a.status) {
+            a.status = reinterpret_cast<uint32_t *>(a.info + p.units);
+            if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st) != cudaSuccess) return GDN_ERR_CUDA;
+        }
     }
     if (d == 64) return launch<64>(a, p, st);
     if (d == 128) return launch<128>(a, p, st);

@@ -206,3 +206,48 @@ def test_a_wait_that_runs_out_before_the_join(cuda_dev, d, h_q):
                                      k, k.stride(0), v, v.stride(0), o, h_q * d, n, ws, need, status, 2_000_000)
     assert int(status.item()) == gs.DEV_TIMEOUT and (o == 7.0).all()
     prompt(t, h_q, 1, d, cuda_dev)
+
+
+@pytest.mark.parametrize("d,h_q", [(64, 4), (128, 4), (256, 2)])
+def test_without_a_status_word(cuda_dev, d, h_q):
+    """The same bits as with one, captured too; a wait that runs out writes nothing, whatever the workspace held."""
+    from speculative_decoding_hybrid_gb300 import binding as gs
+    n = 2000
+    need, parts = prompt_workspace(h_q, 1, d, n)
+    assert parts >= 2
+    t, _ = pu.rows_of(n, h_q, 1, d, 1)
+    ref, lref = prompt(t, h_q, 1, d, cuda_dev)
+    q, k, v = pu.split(t.to(cuda_dev), h_q, 1, d)
+    cu, dims = pu.dev32([0, n], cuda_dev), gs.attn_dims(h_q, 1, d, 0, pu.scale_of(d))
+    o, lse = torch.empty(n, h_q, d, dtype=torch.bfloat16, device=cuda_dev), torch.empty(n, h_q, device=cuda_dev)
+    ws = torch.full((need,), 127, dtype=torch.uint8, device=cuda_dev)
+    rows = (q, q.stride(0), k, k.stride(0), v, v.stride(0))
+
+    def call():
+        gs.attn_prompts(dims, 1, n, cu, *rows, o, h_q * d, lse, n, ws, need, None)
+    call()
+    assert torch.equal(o.cpu(), ref) and torch.equal(lse.cpu(), lref)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        call()
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        o.zero_()
+        g.replay()
+        assert torch.equal(o.cpu(), ref) and torch.equal(lse.cpu(), lref)
+    ws[:] = torch.arange(need, device=cuda_dev).to(torch.uint8)
+    o.fill_(7.0)
+    gs.attn_selftest_prompts_timeout(dims, 1, n, cu, *rows, o, h_q * d, n, ws, need, None, 2_000_000)
+    assert (o == 7.0).all()
+
+    cache = ku.Cache([5000], h_q, 1, d, 64, seed=4)
+    t = t[:20]
+    c, ref, lref = chunk(cache, t, cuda_dev)
+    need, parts = chunk_workspace(c, cache, 20)
+    assert parts >= 2
+    ws = torch.full((need,), 127, dtype=torch.uint8, device=cuda_dev)
+    table = torch.from_numpy(cache.table).to(cuda_dev)
+    gs.kv8_chunk(c.c, 0, 1, 20, pu.dev32([0, 20], cuda_dev), pu.dev32([5000], cuda_dev), table, table.shape[1],
+                 table.stride(0), *rows, o, h_q * d, lse, 5000, 20, 5000, ws, need, None)
+    assert torch.equal(o[:20].cpu(), ref) and torch.equal(lse[:20].cpu(), lref)
