@@ -178,6 +178,8 @@ class Kv8Cache:
         max_len and max_rows are host bounds on cache_len and on a request's rows, total_len on the sum of cache_len
         (it sizes the call's workspace; None: the requests times max_len)."""
         h_q, h_kv, d, device = self.h_q, self.h_kv, self.d, self._index
+        if device < 0:
+            raise ValueError("the cache must be on a GPU")
         B = cache_len.numel()
         tables, pages = table.shape
         table_s, one = table.stride()

@@ -93,6 +93,8 @@ class Rope:
         or in place.  k may be None."""
         # (the checks stand in the call: on few rows its time is its host side)
         d, index = self.d, self._index
+        if index < 0:
+            raise ValueError("the table must be on a GPU")
         B = cu_rows.numel() - 1
         if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != index
                 or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != index):
@@ -183,6 +185,8 @@ def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: t
     R, h_q, d = q.shape
     q_s, x, one = q.stride()
     index = q.get_device()
+    if index < 0:
+        raise ValueError("the rows must be on a GPU")
     B = cu_rows.numel() - 1
     if (cu_rows.dtype is not _I32 or B < 0 or not cu_rows.is_contiguous() or cu_rows.get_device() != index
             or status.dtype is not _I32 or status.numel() != 1 or status.get_device() != index):

@@ -19,3 +19,28 @@ def test_cut_work_has_room_for_a_status_word(gs):
         per = stages * (128 // h_q)
         units = min(-(-n // per), n // per + 1)
         assert need > 0 and (need - units * 32) % (units * stages * 128 * (d * 4 + 8)) == 16
+
+
+def calls(gs, device):
+    """Each call with all of its tensors on `device`."""
+    from speculative_decoding_hybrid_gb300.kvcache import PagedKv
+    from speculative_decoding_hybrid_gb300.prefill import Rope, attend_prompts
+    x = lambda h: torch.zeros((8, h, 64), dtype=torch.bfloat16, device=device)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device=device)
+    cu, status = i(0, 8), i(0)
+    yield "rotate", lambda **kw: Rope(64, device=device).rotate(x(4), x(2), cu, None, status, **kw)
+    yield "rotate in place", lambda **kw: Rope(64, device=device).rotate(x(4), None, cu, i(5), status, in_place=True, **kw)
+    yield "attend_prompts", lambda **kw: attend_prompts(x(4), x(2), x(2), cu, 8, status, **kw)
+    cache = PagedKv(1, 4, 1, 64, 4, 2, 64, page_tokens=16, device=device)
+    yield "attend_chunk", lambda **kw: cache.attend_chunk(0, i(0, 1).view(1, 2), i(10), cu, x(4), x(2), x(2), 10, 8, **kw)
+
+
+def test_tensors_that_are_all_on_the_cpu_are_refused(gs, monkeypatch):
+    """All of one device, which is none that the library launches on; whatever the current device is."""
+    from speculative_decoding_hybrid_gb300 import kvcache, prefill
+    for module in (kvcache, prefill):
+        monkeypatch.setattr(module, "_current_device", lambda: 0)
+    for name, call in calls(gs, "cpu"):
+        for kw in (dict(), dict(stream=0)):
+            with pytest.raises(ValueError, match="on a GPU"):
+                call(**kw)
