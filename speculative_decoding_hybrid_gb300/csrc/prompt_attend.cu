@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) prompt_attend_kernel(cons
                 if (a.lse)
                     a.lse[(int64_t(w.u.t0) + at) * a.h_q + h] =
                         l == 0.f ? -INFINITY
-                                 : fmaf(a.scale_log2, base, (base == 0.f ? m : 0.f) + __log2f(l)) * 0.6931471805599453f;
+                                 : fmaf(a.scale_log2, base, (base == 0.f ? m : 0.f) + log2f(l)) * 0.6931471805599453f;
             } else if (write) {
                 a.ws_ml[wrow] = base == 0.f ? make_float2(m, l) : make_float2(base, copysignf(l, -1.f));
             }

@@ -219,3 +219,18 @@ def test_scales_of_next_to_nothing(cuda_dev, d, sm_scale):
         q, k, v = _scores(n, 2, 1, d, "both", 122, 3)
         got, (q, k, v) = prompts([n], q, k, v, cuda_dev, sm_scale=sm_scale, cut=cut)
         check("small scale", got, pu.attend(q, k, v, 0, float(np.float32(sm_scale))))
+
+
+def test_the_log_of_a_sum_near_one(cuda_dev):
+    """Rows of two positions, scores 0 and -s: lse = log(1 + e^-s), to 2^-22.  (The smaller weight is off by 2^-22.5 of
+    itself, their sum by 2^-24 of itself, its logarithm to base 2 and the product with ln 2 by 2^-24 each: 2^-22.2.)"""
+    s = np.concatenate([np.arange(0, 256) / 256.0 * 2.0 ** e for e in range(5)])
+    s = ku.bf16(s)[1]
+    for d in (64, 128, 256):
+        n = len(s)
+        q, k, v = np.zeros((2 * n, 1, d)), np.zeros((2 * n, 1, d)), np.zeros((2 * n, 1, d))
+        q[..., 3] = -1.0
+        k[1::2, 0, 3] = s
+        (_, lse), _ = prompts([2] * n, q, k, v, cuda_dev, sm_scale=1.0)
+        assert (lse[::2] == 0).all()
+        assert noted("prompt range log: lse", np.max(np.abs(lse[1::2, 0] - np.log1p(np.exp(-s)))) * 2.0 ** 22) <= 1.0
