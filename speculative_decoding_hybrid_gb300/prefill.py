@@ -218,6 +218,8 @@ def attend_prompts(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: t
             raise _bad_rows("out", h_q, d)
         if n <= 1:
             o_s = h_q * d
+    if sm_scale is not None:
+        sm_scale = float(sm_scale)  # (a tensor would be a key by its identity, not by its value)
     key = (h_q, h_kv, d, window, sm_scale, B, R, max_rows)
     plan = _workspace.get(key)
     if plan is None:

@@ -234,3 +234,13 @@ def test_the_log_of_a_sum_near_one(cuda_dev):
         (_, lse), _ = prompts([2] * n, q, k, v, cuda_dev, sm_scale=1.0)
         assert (lse[::2] == 0).all()
         assert noted("prompt range log: lse", np.max(np.abs(lse[1::2, 0] - np.log1p(np.exp(-s)))) * 2.0 ** 22) <= 1.0
+
+
+def test_a_scale_in_a_tensor_is_read_at_every_call(cuda_dev):
+    q, k, v = (np.random.RandomState(1).standard_normal((40, h, 64)) for h in (2, 1, 1))
+    scale = torch.tensor(0.125)
+    for x in (0.125, 0.5, -0.25):
+        scale.fill_(x)
+        (o, lse), _ = prompts([40], q, k, v, cuda_dev, sm_scale=scale)
+        (ro, rl), _ = prompts([40], q, k, v, cuda_dev, sm_scale=x)
+        assert np.array_equal(o, ro) and np.array_equal(lse, rl)
