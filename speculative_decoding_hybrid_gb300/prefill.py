@@ -32,7 +32,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
     linear: every frequency over factor;
     base:   base * factor^(rot/(rot-2)), which leaves the fastest and divides the slowest by factor;
     parts:  frequencies that turn at least `fast` times in `trained` positions stay, those that turn at most `slow`
-            times are divided by factor, in between a straight line; cosine and sine times 1 + 0.1 ln(factor)."""
+            times are divided by factor, in between a straight line in the number of turns; cosine and sine times
+            1 + 0.1 ln(factor).  (A model trained with a line in the channel's number instead, with whole channels as
+            its ends, or without the factor on cosine and sine, wants its own frequencies and magnitude.)"""
     if rot <= 0 or rot % 2:
         raise ValueError("rot is a positive even number of channels")
     if scaling not in SCALINGS:
@@ -58,16 +60,17 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
 
 class Rope:
     """Rotary positions of d-channel heads: the first `rot` channels (default all) turn, in pairs (j, j + rot/2) or,
-    interleaved, (2j, 2j + 1).  The frequencies are rope_frequencies(...) or given (`frequencies`, `magnitude`)."""
+    interleaved, (2j, 2j + 1).  The frequencies are rope_frequencies(...) or given (`frequencies`, and with them
+    `magnitude`, on cosine and sine)."""
 
     def __init__(self, d: int, rot: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
                  scaling: str = "none", factor: float = 1.0, trained: int = 0, device="cuda",
-                 frequencies=None, magnitude: float = 1.0):
+                 frequencies=None, magnitude: float = 1.0, slow: float = 1.0, fast: float = 32.0):
         rot = d if rot is None else rot
         if d <= 0 or d % 8 or d > 512 or rot <= 0 or rot % 2 or rot > d:
             raise ValueError("d is a multiple of 8 up to 512, rot an even number up to d")
         if frequencies is None:
-            f, magnitude = rope_frequencies(rot, base, scaling, factor, trained)
+            f, magnitude = rope_frequencies(rot, base, scaling, factor, trained, slow, fast)
         else:
             f = np.asarray(frequencies, dtype=np.float64)
             if f.shape != (rot // 2,) or not np.isfinite(f).all():

@@ -1,4 +1,8 @@
-"""The prompt side on the host: room for a status word, tensors that are not on a GPU (no GPU: nothing is launched)."""
+"""The prompt side on the host: room for a status word, tensors that are not on a GPU, frequencies scaled by parts (no GPU:
+nothing is launched)."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -44,3 +48,22 @@ def test_tensors_that_are_all_on_the_cpu_are_refused(gs, monkeypatch):
         for kw in (dict(), dict(stream=0)):
             with pytest.raises(ValueError, match="on a GPU"):
                 call(**kw)
+
+
+def test_the_line_of_scaling_by_parts(gs):
+    """Between its ends a frequency's share goes by how often it turns in the trained length: at a quarter of the way
+    from `slow` to `fast` a quarter of it stays and three quarters are divided by the factor."""
+    from speculative_decoding_hybrid_gb300.prefill import Rope, rope_frequencies
+    for slow, fast, factor in ((1.0, 32.0, 8.0), (1.0, 4.0, 16.0), (2.5, 20.0, 3.0)):
+        for share in (0.0, 0.25, 0.5, 0.9, 1.0):
+            f = 1000.0 ** -0.5                                 # the second of two frequencies, of base 1000
+            turns = slow + share * (fast - slow)
+            trained = 2 * math.pi * turns / f
+            kw = dict(base=1000.0, scaling="parts", factor=factor, trained=trained, slow=slow, fast=fast)
+            g, m = rope_frequencies(4, **kw)
+            assert abs(g[1] - (share * f + (1 - share) * f / factor)) < 1e-12 * f
+            assert abs(m - (1 + 0.1 * math.log(factor))) < 1e-15
+            rope = Rope(8, 4, device="cpu", **kw)
+            assert np.array_equal(rope.frequencies, g) and rope.magnitude == m
+    with pytest.raises(ValueError):
+        Rope(8, 4, device="cpu", scaling="parts", factor=2.0, trained=100, slow=4.0, fast=4.0)
