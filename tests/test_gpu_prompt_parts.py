@@ -251,3 +251,27 @@ def test_without_a_status_word(cuda_dev, d, h_q):
     gs.kv8_chunk(c.c, 0, 1, 20, pu.dev32([0, 20], cuda_dev), pu.dev32([5000], cuda_dev), table, table.shape[1],
                  table.stride(0), *rows, o, h_q * d, lse, 5000, 20, 5000, ws, need, None)
     assert torch.equal(o[:20].cpu(), ref) and torch.equal(lse[:20].cpu(), lref)
+
+
+def test_two_calls_at_once(cuda_dev):
+    """Prompts, a cut prompt and a cut chunk on three streams together: the bits of each by itself."""
+    from speculative_decoding_hybrid_gb300.prefill import attend_prompts
+    cache = ku.Cache([5000], 4, 1, 128, 64, seed=4)
+    c = ku.gpu_cache(cache, cuda_dev)
+    table, status = torch.from_numpy(cache.table).to(cuda_dev), torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    rows, calls = [], []
+    for total, h_q, h_kv, d, seed in ((6000, 8, 4, 128, 1), (2000, 2, 1, 256, 2), (20, 4, 1, 128, 3)):
+        rows.append(pu.split(pu.rows_of(total, h_q, h_kv, d, seed)[0].to(cuda_dev), h_q, h_kv, d))
+    many, one, few, length = (pu.dev32(x, cuda_dev) for x in ([0, 2500, 2600, 6000], [0, 2000], [0, 20], [5000]))
+    calls = [lambda s=None: attend_prompts(*rows[0], many, 3400, status, want_lse=True, stream=s),
+             lambda s=None: attend_prompts(*rows[1], one, 2000, status, want_lse=True, stream=s),
+             lambda s=None: c.attend_chunk(0, table, length, few, *rows[2], 5000, 20, want_lse=True, stream=s)]
+    ref = [call() for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        got = [call(s) for call, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(ref, got):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert int(status.item()) == 0 and int(c.status.item()) == 0
