@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
         const auto raise = [&](float2 y) {
             if (above(y, top, a.scale_log2) > 0.f) top = y;
         };
-        bool based = false;  // whether some part has one; then x becomes how far it is below the top
+        bool based;  // whether some part has one; then x becomes how far it is below the top
         // (of a part without weight its sums say nothing)
         if constexpr (!MANY) {
             float2 x[kFew];
@@ -1140,10 +1140,12 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
                 x[p] = ml[p * kRows];
                 load_part<D>(y[p], from + p * kRows * D);
             }
+            uint32_t signs = 0;
 #pragma unroll
             for (int p = 0; p < kFew; ++p)
-                if (p < f.parts) top.y = fmaxf(top.y, x[p].x), based |= signbit(x[p].y);
-            if (based) {
+                if (p < f.parts) top.y = fmaxf(top.y, x[p].x), signs |= __float_as_uint(x[p].y);
+            based = signs >> 31;
+            if (__builtin_expect(based, 0)) {
                 top.y = -INFINITY;
 #pragma unroll
                 for (int p = 0; p < kFew; ++p)
@@ -1164,15 +1166,16 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
             }
         } else {
             float2 x[kMostParts / 32];
+            uint32_t signs = 0;
 #pragma unroll
             for (int e = 0; e < kMostParts / 32; ++e) {
                 const int p = lane + 32 * e;
                 x[e] = p < f.parts ? ml[int64_t(p) * kRows] : make_float2(-INFINITY, 0.f);
                 top.y = fmaxf(top.y, x[e].x);
-                based |= signbit(x[e].y);
+                signs |= __float_as_uint(x[e].y);
             }
-            based = __any_sync(0xffffffffu, based);
-            if (based) {
+            based = __any_sync(0xffffffffu, signs >> 31);
+            if (__builtin_expect(based, 0)) {
                 top.y = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < kMostParts / 32; ++e) raise(reference_of(x[e]));
