@@ -603,8 +603,9 @@ typedef struct kv8_cache {
  *   (sm_scale q.k, in powers of two) by 2^-14 at most for q and as much for a
  *   new key.  Where it might be more (by the row's losses and the largest that
  *   the other side can be) scores are summed from the elements, in fp32 and
- *   some 50 times slower.  The sums of weights times v are fp32 too, before the
- *   division: |v| up to 2^100.
+ *   some 50 times slower.  |sm_scale q.k| up to 2^23: beyond it the rounding of
+ *   a score to fp32 is more than the range of its weight allows for.  The sums
+ *   of weights times v are fp32 too, before the division: |v| up to 2^100.
  *   A non-finite q or k that a row sees makes the row's outputs NaN; what a
  *   row does not see, NaN and infinities included, and bytes of cache past
  *   cache_len, whatever they hold, do not reach it.
@@ -718,8 +719,9 @@ typedef struct rope_spec {
  *   pair j of every head becomes
  *     (a, b) -> magnitude * (a cos theta - b sin theta, a sin theta + b cos theta)
  *   in fp32, rounded once to bf16.  turns: device uint64 [rot/2], frequency j
- *   over 2 pi as a 64-bit fraction: the angle is right to 2^-33 of a turn at
- *   every position (frequencies are the caller's: any base, any scaling).
+ *   over 2 pi as a 64-bit fraction: the angle is right to 2^-26 of a turn and a
+ *   little (2^-31), fp32's 24 bits of half a turn, at every position
+ *   (frequencies are the caller's: any base, any scaling).
  *   q [row][h_q][d], k [row][h_kv][d], rows *_stride elements apart (multiples
  *   of 8), bases 16-byte aligned.  q_out == q (k_out == k) with equal strides
  *   turns in place; otherwise an output overlaps no input.  A head count of 0
@@ -777,8 +779,10 @@ int attn_prompts(const attn_dims *dims, int32_t B, int32_t row_capacity, const i
  * kv8_chunk -- kv8_attend for any number of rows: one layer's attention of
  *   each request's new rows over its cache_len[r] committed positions (0 ..
  *   max_len, as stored) and the new rows j <= i (as given), inside the window.
- *   Arguments as of kv8_attend, numerics as of attn_prompts; k_new and v_new
- *   are wanted, max_rows has no limit of its own, and total_len is a host bound
+ *   Arguments as of kv8_attend, numerics as of attn_prompts (a weight keeps 8
+ *   bits in the product with v: of up to GDN_MAX_ROWS rows kv8_attend, which
+ *   keeps 11, has the more exact outputs); k_new and v_new are wanted,
+ *   max_rows has no limit of its own, and total_len is a host bound
  *   on the sum of cache_len (it sizes the workspace: kv8_chunk_workspace_bytes
  *   device bytes, 4 h_kv d of them for each committed position and row; 0 for
  *   arguments that kv8_chunk refuses).  Bytes of cache past cache_len do not

@@ -34,16 +34,18 @@
 // behind 256K positions.  In the loop the conversion would cost more from about 1,300 query
 // vectors a kv head on: shared memory already moves 128 bytes a clock for the products.
 //
-// Roundings: p to bf16, as V's type wants, 2^-8 of it at most (its sum is of the unrounded
-// ones); outputs once, to bf16.  Everything else is fp32.
+// Roundings: p to bf16, as V's type wants (both sides of a product have one type), 2^-8 of it at
+// most; its sum is of the unrounded ones.  Outputs are 0.0018 to 0.0023 of their size from the
+// fp64 form for it, where their own rounding alone, once, to bf16, leaves 0.0016; p in two bf16
+// parts would hold 16 bits for half as many products again.  Everything else is fp32.
 //
-// What bounds it: one prompt of 20,011 tokens, 16/2 heads of 256, 1.94 ms, 1,690 TFLOP/s,
-// the power limit (a long loop of a library's products reaches 1,736); 8 prompts of 512 to
-// 12,000 tokens, 32/4 heads of 128, 1.06 ms, 1,380 TFLOP/s: a query tile's chain of scores ->
+// What bounds it: one prompt of 20,011 tokens, 16/2 heads of 256, 1.98 to 2.0 ms, 1,640 to 1,660
+// TFLOP/s, the power limit (a long loop of a library's products reaches 1,736); 8 prompts of 512
+// to 12,000 tokens, 32/4 heads of 128, 1.05 ms, 1,390 TFLOP/s: a query tile's chain of scores ->
 // tensor-memory load (500 clocks beside products, 60 alone) -> maximum -> exponentials ->
 // products, 2,800 clocks a tile for 2,048 of products; short prompts (16 of 100 to 4,000
-// tokens, 32/8 heads: 0.46 ms, 1,160 TFLOP/s) the ends of units, 3 us each.  A single short
-// prompt is one chain: 37 tokens, 16/2 heads of 256, 9.4 us.
+// tokens, 32/8 heads: 0.45 ms, 1,180 TFLOP/s) the ends of units, 3 us each.  A single short
+// prompt is one chain: 37 tokens, 16/2 heads of 256, 9.6 us.
 #include "kv8_math.cuh"
 #include "prompt.cuh"
 #include "tmap.cuh"

@@ -1,12 +1,15 @@
 // Rotary positions of packed rows (sm_103a).
 //
 // Channel pair j of a head turns by position * f_j.  Angles are held in turns, as 64-bit fixed
-// point: position * round(2^64 f_j / 2 pi) modulo 2^64 is the fraction of a turn, exact to 2^-33 of
-// one at every position (a product in fp32 is off by 0.06 rad at position 10^6), and costs one
-// integer multiplication.  A thread makes the cosines and sines of its channels once a row and
-// takes them through the row's heads, 16 bytes at a time (rot not a multiple of 16: 2 bytes).
+// point: position * round(2^64 f_j / 2 pi) modulo 2^64 is the fraction of a turn, off by 2^-34 of
+// one at the farthest position (a product in fp32 is off by 0.06 rad at position 10^6), and costs
+// one integer multiplication.  Its upper 32 bits as an fp32 number of half turns are off by 2^-32
+// and 2^-26 of a turn more, 10^-7 rad: a bf16 result wants 2^-9.  A thread makes the cosines and
+// sines of its channels once a row and takes them through the row's heads, 16 bytes at a time.
 // HBM-bound: 67,237 rows of 40 heads of 128 in 211 us, 6.53 TB/s, 96 % of a copy's rate; 1,024
-// rows 6.7 us, one row 3.3 us, a launch and a chain of loads.
+// rows 6.7 us, one row 3.4 us, a launch and a chain of loads.  Where rot is no multiple of 16 a
+// half's pieces do not begin at 16 bytes, and the row goes 2 bytes at a time: the same rows with
+// 120 of 128 channels turned 755 us, 1.8 TB/s (rot of 16, 32, 64, 96 and whole heads are wide).
 #include "kv8.cuh"
 #include "prompt.cuh"
 
